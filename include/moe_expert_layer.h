@@ -36,6 +36,11 @@
  *                   way along F before the down projection.  The output is bfloat16.  The MX format
  *                   is the one named for the reference MC2 matmul on the page
  *                   "MC2 通算融合架构总览", §1.
+ *   MOE_INT8        signed 8-bit codes with one float32 scale per token row (x_scale [T]) and one per
+ *                   expert and output channel (wg_scale / wu_scale [E, F], wd_scale [E, H]): a value
+ *                   is code * scale.  Products are exact int32 sums, scaled in float32; h is float32
+ *                   and quantised per row (the rule of moe_int8_quantize) before the down projection.
+ *                   The output is bfloat16.
  */
 #ifndef MOE_EXPERT_LAYER_H
 #define MOE_EXPERT_LAYER_H
@@ -58,7 +63,7 @@ typedef enum moe_status {
     MOE_ERR_HIP = 5                     /* a HIP runtime call failed (message in moe_last_error)  */
 } moe_status;
 
-enum moe_dtype_code { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP8_E4M3 = 2 };
+enum moe_dtype_code { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP8_E4M3 = 2, MOE_INT8 = 3 };
 
 /* moe_problem.flags.  By default the forward calls fold the permute step (a gather of token rows
  * into expert order, "NPU Training Operators - MC2", 执行路径 step 6) into the first grouped GEMM's
@@ -67,7 +72,8 @@ enum moe_dtype_code { MOE_F32 = 0, MOE_BF16 = 1, MOE_MXFP8_E4M3 = 2 };
  * on x_perm instead; the result is bitwise the same either way. */
 #define MOE_FLAG_SEPARATE_PERMUTE 1u
 
-/* moe_problem.flags, MX problems only: x is bfloat16 [T,H] and the library encodes it to OCP-MX
+/* moe_problem.flags, MX and int8 problems only (int8: x is bfloat16 and quantised once per token by
+ * the rule of moe_int8_quantize): x is bfloat16 [T,H] and the library encodes it to OCP-MX
  * (E4M3 codes, one E8M0 scale per 32 elements along H, the rule of moe_mx_quantize) on its way into
  * the gather of 执行路径 step 6 ("NPU Training Operators - MC2"; the MX matmul of
  * "MC2 通算融合架构总览", §1): once per token into the workspace when the first grouped GEMM gathers
@@ -105,7 +111,8 @@ typedef struct moe_problem {
  * Whole layer.
  * ------------------------------------------------------------------------------------------- */
 
-/* Host only.  Workspace bytes needed by moe_expert_forward / moe_expert_forward_mx for `p`. */
+/* Host only.  Workspace bytes needed by moe_expert_forward / moe_expert_forward_mx /
+ * moe_expert_forward_int8 for `p`. */
 moe_status moe_workspace_size(const moe_problem* p, size_t* bytes /* host */);
 
 /* out[T,H] = sum_j probs[t,j] * FFN_{expert_ids[t,j]}(x[t]),
@@ -143,6 +150,19 @@ moe_status moe_expert_forward_mx(const moe_problem* p, const uint8_t* x, const u
                                  const uint8_t* w_down, const uint8_t* wd_scale,
                                  const int32_t* expert_ids, const float* probs, void* out_bf16,
                                  void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The same layer on int8 weights (dtype must be MOE_INT8; H and F multiples of 128 and at most 130944;
+ * head_m_size 0; MOE_FLAG_SEPARATE_PERMUTE is ignored: rows are always gathered).  x int8 [T,H] with
+ * x_scale [T], or with MOE_FLAG_QUANTIZE_X bfloat16 [T,H] with x_scale NULL.  Weights are int8 codes in
+ * the layouts of moe_expert_forward, wg_scale / wu_scale [E,F] and wd_scale [E,H] float32; out is
+ * bfloat16 [T,H].  A token whose x or h row holds an infinity or NaN gets NaN outputs from that
+ * expert.  T * H must be below 2^32.  The int32 sums are exact, so the output does not depend on how
+ * the library cuts the products; deterministic.  Errors as for moe_expert_forward. */
+moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, const float* x_scale,
+                                   const int8_t* w_gate, const float* wg_scale, const int8_t* w_up,
+                                   const float* wu_scale, const int8_t* w_down, const float* wd_scale,
+                                   const int32_t* expert_ids, const float* probs, void* out_bf16,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
  * Backward of the layer.
@@ -229,7 +249,8 @@ moe_status moe_permute(const moe_problem* p, const void* x, const uint8_t* x_sca
 moe_status moe_unpermute(const moe_problem* p, const void* y_perm, const int32_t* pos,
                          const float* probs, void* out, hipStream_t stream);
 
-/* Host only.  Workspace bytes for moe_grouped_ffn / moe_grouped_ffn_mx with M rows in G groups. */
+/* Host only.  Workspace bytes for moe_grouped_ffn / moe_grouped_ffn_mx / moe_grouped_ffn_int8 with M
+ * rows in G groups. */
 moe_status moe_grouped_ffn_workspace_size(const moe_problem* p, int64_t M, int64_t G,
                                           size_t* bytes /* host */);
 
@@ -253,6 +274,32 @@ moe_status moe_grouped_ffn_mx(const moe_problem* p, const uint8_t* rows, const u
                               const uint8_t* wd_scale, void* y_rows, void* workspace,
                               size_t workspace_bytes, hipStream_t stream);
 
+/* The same for int8 rows (rows [M,H] codes, rows_scale [M]; dtype MOE_INT8, p->flags 0,
+ * p->head_m_size 0); y_rows is bfloat16 [M,H].  Rows that no group holds, and the rows of a skipped
+ * group, are left as they were. */
+moe_status moe_grouped_ffn_int8(const moe_problem* p, const int8_t* rows, const float* rows_scale,
+                                int64_t M, const int32_t* group_offsets, const int32_t* group_expert,
+                                int64_t G, const int8_t* w_gate, const float* wg_scale,
+                                const int8_t* w_up, const float* wu_scale, const int8_t* w_down,
+                                const float* wd_scale, void* y_rows, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* One grouped product on int8 operands with scales per token and channel:
+ *   out[r,n] = rows_scale[r] * w_scale[e,n] * sum_k rows[r,k] w[e,k,n],   e the expert of r's group
+ * rows int8 [M,K], rows_scale [M], w int8 [E,K,N], w_scale [E,N] float32; out [M,N] of out_dtype
+ * (MOE_BF16 or MOE_F32).  Groups as for moe_grouped_ffn (a group expert outside [0, E) skips the
+ * group and sets the status word); rows that no group holds are left as they were.  The sum is exact
+ * int32; one conversion to float32, two float32 products, one rounding to out_dtype.
+ * K and N multiples of 128, K <= 130944, N <= MOE_MAX_HIDDEN, E < 1024, M < 2^31.  All pointers
+ * aligned to 16 bytes. */
+moe_status moe_grouped_matmul_int8_workspace_size(int64_t M, int64_t G, int64_t K, int64_t N,
+                                                  size_t* bytes /* host */);
+moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows_scale, int64_t M,
+                                   const int32_t* group_offsets, const int32_t* group_expert,
+                                   int64_t G, const int8_t* w, const float* w_scale, int64_t E,
+                                   int64_t K, int64_t N, void* out, int32_t out_dtype,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Router in front of the layer: the gate's top-k.  logits [T, E] float32 (E <= 1024) ->
  * expert_ids [T, k] int32 and probs [T, k] float32 (1 <= k <= min(E, 64)), ready for
  * moe_expert_forward.  The gate is the first step of the step breakdown on the page "MC2 通算融合";
@@ -264,6 +311,57 @@ moe_status moe_grouped_ffn_mx(const moe_problem* p, const uint8_t* rows, const u
  * Errors: MOE_ERR_INVALID_ARGUMENT for bad sizes or null pointers (nothing enqueued). */
 moe_status moe_router_topk(const float* logits, int64_t T, int64_t E, int64_t k,
                            int32_t* expert_ids, float* probs, hipStream_t stream);
+
+/* The gate in its general form.  Per token with logits l[E]:
+ *   scores     s = softmax(l) over all E experts, or sigmoid(l)
+ *   selection  c = s + bias (bias NULL: c = s); c = -inf where l = -inf.  The bias takes part in the
+ *              selection alone.
+ *   groups     with groups > 1 the experts form `groups` runs of E / groups neighbours; a group's score
+ *              is the sum of its group_top largest c (-inf ones add nothing; a group of none else has
+ *              score -inf); the topk_groups groups with the largest scores stay, equal scores to
+ *              the lower group
+ *   top-k      the k largest c of the experts that stay, in descending order, equal c to the lower id
+ *              (so -inf ones are taken last, in ascending id)
+ *   weights    probs[t,j] = scale * s_j, divided by the sum of the k s_j with renormalize != 0; where
+ *              all k scores are zero (every selected logit -inf) the weights are 0
+ * Without a bias the logits themselves are compared; with one, and between groups, scores and sums are
+ * float64: the selection is that of real arithmetic up to float64 rounding.  A NaN logit counts as the
+ * largest and makes the weights NaN (with sigmoid scores: its own, and all of them with renormalize);
+ * with softmax a +inf logit does as well.  The ids are distinct and inside [0, E) in any case. */
+enum moe_score_code { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+typedef struct moe_gate {
+    int32_t score;        /* enum moe_score_code                                                 */
+    int32_t renormalize;  /* 0 or 1                                                              */
+    int32_t groups;       /* 1: no groups.  Must divide E                                        */
+    int32_t topk_groups;  /* 1 .. groups, and topk_groups * (E / groups) >= k                     */
+    int32_t group_top;    /* 1 or 2: how many of a group's c make its score                      */
+    float scale;          /* factor of the weights, finite                                       */
+} moe_gate;
+
+/* logits [T,E] of dtype MOE_F32 or MOE_BF16, bias [E] float32 or NULL -> expert_ids [T,k] int32 and
+ * probs [T,k] float32, ready for moe_expert_forward.  1 <= E <= 1024, 1 <= k <= min(E, 64).
+ * Errors: MOE_ERR_INVALID_ARGUMENT for bad sizes or null pointers, MOE_ERR_UNSUPPORTED for another
+ * dtype (nothing enqueued). */
+moe_status moe_router_gate(const moe_gate* gate, const void* logits, int32_t dtype, const float* bias,
+                           int64_t T, int64_t E, int64_t k, int32_t* expert_ids, float* probs,
+                           hipStream_t stream);
+
+/* Gradient of moe_router_gate: dprobs [T,k] float32 (as moe_expert_backward gives it) -> dlogits [T,E]
+ * of the logits' dtype, for the selection expert_ids [T,k] (ids carry no gradient, and neither does
+ * the bias).  Of `gate`, score, renormalize and scale are used.  Every element of dlogits is written
+ * (zero where no gradient arrives).  float32 arithmetic, no atomics.  An id that a token names twice
+ * gets both slots' gradients; a slot whose id is outside [0, E) is skipped, as if it were not there.
+ * Errors as for moe_router_gate. */
+moe_status moe_router_gate_backward(const moe_gate* gate, const void* logits, int32_t dtype, int64_t T,
+                                    int64_t E, int64_t k, const int32_t* expert_ids,
+                                    const float* dprobs, void* dlogits, hipStream_t stream);
+
+/* int8 row quantiser of the int8 layer: x [rows, cols] of dtype MOE_F32 or MOE_BF16 -> codes
+ * [rows, cols] int8 and scales [rows] float32, scale = max|x| / 127 of the row, code = 127 x / max|x|
+ * rounded to nearest, ties to even (of the real quotient: bit-exact); a row of zeros gets scale 0 and
+ * codes 0, a row that holds an infinity or NaN gets scale NaN and codes 0. */
+moe_status moe_int8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int8_t* codes,
+                             float* scales, hipStream_t stream);
 
 /* OCP-MX encoder used on h inside the MX layer, exposed on its own: v [rows, cols] float32
  * (cols a multiple of 32) -> codes [rows, cols] E4M3 bytes and scales [rows, cols/32] E8M0 bytes.

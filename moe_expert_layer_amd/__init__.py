@@ -15,16 +15,18 @@ import threading
 import torch
 
 __all__ = [
-    "MoeError", "library", "lib_path", "F32", "BF16", "MXFP8",
+    "MoeError", "library", "lib_path", "F32", "BF16", "MXFP8", "INT8",
     "workspace_size", "expert_forward", "expert_forward_mx", "expert_forward_train",
     "backward_workspace_size", "expert_backward", "route", "route_noalloc", "permute", "unpermute",
     "grouped_ffn_workspace_size", "grouped_ffn", "grouped_ffn_mx", "mx_quantize",
     "mx_fc1_epilogue_encode", "device_status", "chunk_counters",
     "intermediate_h", "quantized_x",
+    "router_topk", "router_gate", "router_gate_backward", "int8_quantize", "grouped_matmul_int8",
+    "grouped_ffn_int8", "expert_forward_int8",
     "timing_enable", "timing_collect", "timing_reset",
 ]
 
-F32, BF16, MXFP8 = 0, 1, 2
+F32, BF16, MXFP8, INT8 = 0, 1, 2, 3
 _HERE = os.path.dirname(os.path.abspath(__file__))
 lib_path = os.path.join(_HERE, "libmoe_expert_layer.so")
 _lock = threading.Lock()
@@ -39,6 +41,11 @@ class MoeProblem(ctypes.Structure):
                 ("E", ctypes.c_int64), ("k", ctypes.c_int64), ("dtype", ctypes.c_int32),
                 ("head_m_size", ctypes.c_int32), ("flags", ctypes.c_uint32),
                 ("reserved", ctypes.c_uint32)]
+
+
+class MoeGate(ctypes.Structure):
+    _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -69,6 +76,15 @@ _SIGS = {
     "moe_mx_quantize": [_P, _I64, _I64, _P, _P, _P],
     "moe_mx_fc1_epilogue_encode": [_P, _I64, _I64, ctypes.c_int32, _P, _P, _P],
     "moe_router_topk": [_P, _I64, _I64, _I64, _P, _P, _P],
+    "moe_router_gate": [ctypes.POINTER(MoeGate), _P, ctypes.c_int32, _P, _I64, _I64, _I64, _P, _P, _P],
+    "moe_router_gate_backward": [ctypes.POINTER(MoeGate), _P, ctypes.c_int32, _I64, _I64, _I64, _P, _P, _P, _P],
+    "moe_int8_quantize": [_P, ctypes.c_int32, _I64, _I64, _P, _P, _P],
+    "moe_grouped_matmul_int8_workspace_size": [_I64, _I64, _I64, _I64, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_grouped_matmul_int8": [_P, _P, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I64, _P, ctypes.c_int32,
+                                _P, ctypes.c_size_t, _P],
+    "moe_grouped_ffn_int8": [ctypes.POINTER(MoeProblem), _P, _P, _I64, _P, _P, _I64, _P, _P, _P,
+                             _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_expert_forward_int8": [ctypes.POINTER(MoeProblem)] + [_P] * 12 + [ctypes.c_size_t, _P],
     "moe_query_device_status": [_P, _P, ctypes.POINTER(ctypes.c_int32)],
     "moe_chunk_counters": [ctypes.POINTER(MoeProblem), _P, ctypes.c_size_t, _I64,
                            ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_I64)],
@@ -301,6 +317,49 @@ def expert_forward_mx(x, x_scale, w_gate, wg_scale, w_up, wu_scale, w_down, wd_s
     return out
 
 
+def expert_forward_int8(x, x_scale, w_gate, wg_scale, w_up, wu_scale, w_down, wd_scale, expert_ids, probs,
+                        out=None, workspace=None):
+    """The same layer on int8 weights with one float32 scale per expert and output channel (wg_scale,
+    wu_scale [E, F], wd_scale [E, H]); bfloat16 output.  x is int8 [T, H] with x_scale [T], or bfloat16
+    with x_scale None (quantised by the library, int8_quantize's rule)."""
+    T, H = x.shape
+    E, _, F = w_gate.shape
+    k = expert_ids.shape[1]
+    dev = x.device
+    quantize_x = x.dtype == torch.bfloat16
+    if quantize_x:
+        if x_scale is not None:
+            raise ValueError("a bfloat16 x is quantised by the library: pass x_scale=None")
+        _need(x, "x", torch.bfloat16, (T, H))
+    else:
+        _need(x, "x", torch.int8, (T, H))
+        _need(x_scale, "x_scale", torch.float32, (T,), dev)
+    _need_int8_weights(dev, E, H, F, w_gate, wg_scale, w_up, wu_scale, w_down, wd_scale)
+    _need(expert_ids, "expert_ids", torch.int32, (T, k), dev)
+    _need(probs, "probs", torch.float32, (T, k), dev)
+    prob = problem(T, H, F, E, k, INT8, 0, FLAG_QUANTIZE_X if quantize_x else 0)
+    ws = _workspace(workspace_size(prob), dev, workspace)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (T, H), dev)
+    with torch.cuda.device(dev):
+        _check(library().moe_expert_forward_int8(
+            ctypes.byref(prob), _ptr(x), _ptr(x_scale), _ptr(w_gate), _ptr(wg_scale), _ptr(w_up),
+            _ptr(wu_scale), _ptr(w_down), _ptr(wd_scale), _ptr(expert_ids), _ptr(probs), _ptr(out),
+            _ptr(ws), ws.numel(), _stream(x)))
+    return out
+
+
+def _need_int8_weights(dev, E, H, F, w_gate, wg_scale, w_up, wu_scale, w_down, wd_scale):
+    i8, f32 = torch.int8, torch.float32
+    _need(w_gate, "w_gate", i8, (E, H, F), dev)
+    _need(wg_scale, "wg_scale", f32, (E, F), dev)
+    _need(w_up, "w_up", i8, (E, H, F), dev)
+    _need(wu_scale, "wu_scale", f32, (E, F), dev)
+    _need(w_down, "w_down", i8, (E, F, H), dev)
+    _need(wd_scale, "wd_scale", f32, (E, H), dev)
+
+
 # ---------------------------------------------------------------------------------------------- sub-steps
 
 def route(expert_ids, E: int, workspace=None):
@@ -431,6 +490,123 @@ def grouped_ffn_mx(rows, rows_scale, group_offsets, group_expert, w_gate, wg_sca
         _ptr(group_expert), G, _ptr(w_gate), _ptr(wg_scale), _ptr(w_up), _ptr(wu_scale),
         _ptr(w_down), _ptr(wd_scale), _ptr(out), _ptr(ws), ws.numel(), _stream(rows)))
     return out
+
+
+def grouped_ffn_int8(rows, rows_scale, group_offsets, group_expert, w_gate, wg_scale, w_up, wu_scale,
+                     w_down, wd_scale, workspace=None, out=None):
+    """grouped_ffn on int8 rows [M, H] with rows_scale [M] and int8 weights (expert_forward_int8);
+    bfloat16 output.  Rows that no group holds are left as they were in a given `out`."""
+    M, H = rows.shape
+    E, _, F = w_gate.shape
+    G = group_expert.shape[0]
+    dev = rows.device
+    _need(rows, "rows", torch.int8, (M, H))
+    _need(rows_scale, "rows_scale", torch.float32, (M,), dev)
+    _need(group_offsets, "group_offsets", torch.int32, (G + 1,), dev)
+    _need(group_expert, "group_expert", torch.int32, (G,), dev)
+    _need_int8_weights(dev, E, H, F, w_gate, wg_scale, w_up, wu_scale, w_down, wd_scale)
+    prob = problem(0, H, F, E, 1, INT8)
+    ws = _workspace(grouped_ffn_workspace_size(prob, M, G), dev, workspace)
+    if out is None:
+        out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
+    _need(out, "out", torch.bfloat16, (M, H), dev)
+    with torch.cuda.device(dev):
+        _check(library().moe_grouped_ffn_int8(
+            ctypes.byref(prob), _ptr(rows), _ptr(rows_scale), M, _ptr(group_offsets), _ptr(group_expert), G,
+            _ptr(w_gate), _ptr(wg_scale), _ptr(w_up), _ptr(wu_scale), _ptr(w_down), _ptr(wd_scale),
+            _ptr(out), _ptr(ws), ws.numel(), _stream(rows)))
+    return out
+
+
+def grouped_matmul_int8(rows, rows_scale, group_offsets, group_expert, w, w_scale,
+                        out_dtype=torch.bfloat16, workspace=None, out=None):
+    """out[r] = rows_scale[r] * w_scale[e] * (rows[r] @ w[e]), e the expert of r's group: int8 rows
+    [M, K] and weights [E, K, N], float32 scales [M] and [E, N]; out bfloat16 or float32 [M, N].  Rows
+    that no group holds are left as they were in a given `out`."""
+    M, K = rows.shape
+    E, _, N = w.shape
+    G = group_expert.shape[0]
+    dev = rows.device
+    _need(rows, "rows", torch.int8, (M, K))
+    _need(rows_scale, "rows_scale", torch.float32, (M,), dev)
+    _need(group_offsets, "group_offsets", torch.int32, (G + 1,), dev)
+    _need(group_expert, "group_expert", torch.int32, (G,), dev)
+    _need(w, "w", torch.int8, (E, K, N), dev)
+    _need(w_scale, "w_scale", torch.float32, (E, N), dev)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _need(out, "out", out_dtype, (M, N), dev)
+    n = ctypes.c_size_t()
+    _check(library().moe_grouped_matmul_int8_workspace_size(M, G, K, N, ctypes.byref(n)))
+    ws = _workspace(n.value, dev, workspace)
+    with torch.cuda.device(dev):
+        _check(library().moe_grouped_matmul_int8(
+            _ptr(rows), _ptr(rows_scale), M, _ptr(group_offsets), _ptr(group_expert), G, _ptr(w),
+            _ptr(w_scale), E, K, N, _ptr(out), _dtype_code(out), _ptr(ws), ws.numel(), _stream(rows)))
+    return out
+
+
+def int8_quantize(x):
+    """One scale per row: float32 or bfloat16 [rows, cols] -> (codes int8 [rows, cols], scales float32
+    [rows]), scale = max|x| / 127, codes rounded to nearest even."""
+    _need(x, "x")
+    dt = _dtype_code(x)
+    rows, cols = x.shape
+    codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
+    scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    with torch.cuda.device(x.device):
+        _check(library().moe_int8_quantize(_ptr(x), dt, rows, cols, _ptr(codes), _ptr(scales), _stream(x)))
+    return codes, scales
+
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _gate(score, renormalize, groups, topk_groups, group_top, scale):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return MoeGate(_SCORES[score], 1 if renormalize else 0, int(groups), int(topk_groups), int(group_top),
+                   float(scale))
+
+
+def router_gate(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
+                group_top: int = 2, renormalize: bool = True, scale: float = 1.0):
+    """The gate in its general form: float32 or bfloat16 logits [T, E] -> (expert_ids int32 [T, k], probs
+    float32 [T, k]).  Scores are a softmax over the experts or sigmoids; `bias` (float32 [E]) is added
+    for the selection alone; with groups > 1 the experts come from the topk_groups best of that many
+    groups (a group's score: the sum of its group_top best experts); the weights are the chosen scores,
+    divided by their sum with renormalize, times scale."""
+    _need(logits, "logits")
+    dt = _dtype_code(logits)
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (E,), logits.device)
+    gate = _gate(score, renormalize, groups, topk_groups, group_top, scale)
+    ids = torch.empty((T, max(int(k), 0)), dtype=torch.int32, device=logits.device)
+    probs = torch.empty((T, max(int(k), 0)), dtype=torch.float32, device=logits.device)
+    with torch.cuda.device(logits.device):
+        _check(library().moe_router_gate(ctypes.byref(gate), _ptr(logits), dt, _ptr(bias), T, E, k,
+                                         _ptr(ids), _ptr(probs), _stream(logits)))
+    return ids, probs
+
+
+def router_gate_backward(logits, expert_ids, dprobs, score: str = "softmax", renormalize: bool = True,
+                         scale: float = 1.0):
+    """Gradient of router_gate for the selection expert_ids [T, k]: dprobs float32 [T, k] (as
+    expert_backward returns it) -> dlogits [T, E] in the logits' dtype."""
+    _need(logits, "logits")
+    dt = _dtype_code(logits)
+    T, E = logits.shape
+    k = expert_ids.shape[1]
+    _need(expert_ids, "expert_ids", torch.int32, (T, k), logits.device)
+    _need(dprobs, "dprobs", torch.float32, (T, k), logits.device)
+    gate = _gate(score, renormalize, 1, 1, 2, scale)
+    dlogits = torch.empty_like(logits)
+    with torch.cuda.device(logits.device):
+        _check(library().moe_router_gate_backward(ctypes.byref(gate), _ptr(logits), dt, T, E, k,
+                                                  _ptr(expert_ids), _ptr(dprobs), _ptr(dlogits),
+                                                  _stream(logits)))
+    return dlogits
 
 
 def router_topk(logits, k: int):

@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstring>
 #include <algorithm>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <string>
@@ -207,6 +208,59 @@ moe_status check_problem(const moe_problem* p, bool need_tokens, bool gemm = tru
     // rows of K elements, 32 weight rows of N), which this bound keeps below 2^31 bytes
     if (p->H > MOE_MAX_HIDDEN || p->F > MOE_MAX_HIDDEN)
         return fail(MOE_ERR_UNSUPPORTED, "H and F must be at most %d", MOE_MAX_HIDDEN);
+    return MOE_OK;
+}
+
+// Sizes of an int8 grouped product.
+moe_status check_int8_product(int64_t M, int64_t G, int64_t E, int64_t K, int64_t N)
+{
+    if (M < 0 || G <= 0 || E <= 0 || K <= 0 || N <= 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "bad int8 product sizes");
+    if (M > INT32_MAX || G > INT32_MAX || E >= kMaxExperts)
+        return fail(MOE_ERR_UNSUPPORTED, "int8 products need M and G below 2^31 and E below %d", kMaxExperts);
+    if (!int8_supported(K, N) || N > MOE_MAX_HIDDEN)
+        return fail(MOE_ERR_UNSUPPORTED, "int8 products need K and N multiples of 128, K <= %lld, N <= %d",
+                    (long long)kInt8MaxK, MOE_MAX_HIDDEN);
+    return MOE_OK;
+}
+
+// A problem of the int8 layer or grouped FFN.
+moe_status check_int8_problem(const moe_problem* p, bool need_tokens)
+{
+    if (p == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "problem is null");
+    if (p->dtype != MOE_INT8)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "the int8 calls need dtype MOE_INT8");
+    const uint32_t known = need_tokens ? MOE_FLAG_SEPARATE_PERMUTE | MOE_FLAG_QUANTIZE_X : 0u;
+    if ((p->flags & ~known) != 0 || p->reserved != 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "unknown flags, or reserved not 0");
+    if (p->H <= 0 || p->F <= 0 || p->E <= 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "H, F and E must be positive");
+    if (p->E >= kMaxExperts)
+        return fail(MOE_ERR_UNSUPPORTED, "E = %lld exceeds %d", (long long)p->E, kMaxExperts - 1);
+    if (!int8_supported(p->H, p->F) || !int8_supported(p->F, p->H))
+        return fail(MOE_ERR_UNSUPPORTED, "int8 needs H and F multiples of 128, at most %lld", (long long)kInt8MaxK);
+    if (p->head_m_size != 0)
+        return fail(MOE_ERR_UNSUPPORTED, "the int8 calls are unchunked (head_m_size must be 0)");
+    if (need_tokens) {
+        if (p->T < 0 || p->k <= 0)
+            return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0 and k >= 1");
+        if (p->k > p->E)
+            return fail(MOE_ERR_INVALID_ARGUMENT, "k = %lld exceeds E = %lld", (long long)p->k, (long long)p->E);
+        if (p->T > INT32_MAX || p->T * p->k > INT32_MAX)
+            return fail(MOE_ERR_UNSUPPORTED, "T * k exceeds int32 indexing");
+        if (p->T * p->H > UINT32_MAX)
+            return fail(MOE_ERR_UNSUPPORTED, "int8 needs T * H < 2^32");
+    }
+    return MOE_OK;
+}
+
+// The int8 kernels load and store 16 bytes at a time.
+moe_status check_aligned(std::initializer_list<const void*> pointers)
+{
+    for (const void* q : pointers)
+        if ((reinterpret_cast<uintptr_t>(q) & 15) != 0)
+            return fail(MOE_ERR_INVALID_ARGUMENT, "int8 operands must be aligned to 16 bytes");
     return MOE_OK;
 }
 
@@ -420,6 +474,98 @@ moe_status run_ffn(int dtype, const void* rows, const uint8_t* rows_scale, int64
     return MOE_OK;
 }
 
+// Workspace of the int8 calls.  Tile tables of both forms (build_tiles writes the first, the kernels
+// take the second: each group one run of balanced tiles), h as float32 or as partial sums, its codes
+// and scales, the partial sums of y, and for the layer the routing, the quantised x and the rows y.
+struct Int8Layout {
+    RouteLayout route;
+    Int8Plan fc1{}, fc2{};
+    size_t counts = 0, offsets = 0, perm = 0, pos = 0, tile_count = 0, tiles = 0, tiles_run = 0;
+    size_t h = 0, h_q = 0, h_scale = 0, y_part = 0, x_q = 0, x_q_scale = 0, y = 0, total = 0;
+    int64_t max_tiles = 0;
+};
+
+struct Take {
+    size_t off;
+    size_t operator()(int64_t bytes)
+    {
+        const size_t o = off;
+        off = align_up(off + static_cast<size_t>(bytes));
+        return o;
+    }
+};
+
+Int8Layout int8_layout(int64_t M, int64_t G, int64_t H, int64_t F, int64_t T, int64_t k, int64_t E, bool layer)
+{
+    Int8Layout L;
+    L.fc1 = int8_plan(M, G, H, F, true);
+    L.fc2 = int8_plan(M, G, F, H, false);
+    Take take{kAlign};                                        // the status word
+    if (layer) {
+        L.route = route_layout(T, k, E, 0);
+        take.off = L.route.total;
+        L.counts = take(4 * E);
+        L.offsets = take(4 * (E + 1));
+        L.perm = take(4 * M);
+        L.pos = take(4 * M);
+        L.x_q = take(T * H);
+        L.x_q_scale = take(4 * T);
+        L.y = take(2 * M * H);
+    }
+    L.max_tiles = max_mtiles(M, G, 0, L.fc1.row_tile);
+    L.tile_count = take(8 * 4);
+    L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
+    L.tiles_run = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
+    L.h = take(4 * M * F * (L.fc1.partial ? 2 * L.fc1.splits : 1));
+    L.h_q = take(M * F);
+    L.h_scale = take(4 * M);
+    if (L.fc2.partial)
+        L.y_part = take(4 * M * H * L.fc2.splits);
+    L.total = take.off;
+    return L;
+}
+
+struct Int8Weights {
+    const int8_t *gate, *up, *down;
+    const float *gate_scale, *up_scale, *down_scale;
+};
+
+// fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.
+moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, const int32_t* offsets,
+                        const int32_t* group_expert, int64_t G, int64_t E, int64_t H, int64_t F,
+                        const Int8Weights& w, void* y, void* ws, const Int8Layout& L, bool write_status,
+                        hipStream_t s, const int32_t* gather, int gather_k)
+{
+    int32_t* tcount = at<int32_t>(ws, L.tile_count);
+    MTile* tiles = at<MTile>(ws, L.tiles_run);
+    const int32_t* count = tcount + 4;
+    LAUNCH(s, "build_tiles",
+           launch_build_tiles(offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.fc1.row_tile,
+                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0, nullptr,
+                              at<int32_t>(ws, 0), write_status, s, tiles, tcount + 4));
+    int8_t* h_q = at<int8_t>(ws, L.h_q);
+    float* h_scale = at<float>(ws, L.h_scale);
+    LAUNCH(s, "fc1_i8",
+           launch_gemm_i8(L.fc1, rows, rows_scale, w.gate, w.gate_scale, w.up, w.up_scale, at<void>(ws, L.h),
+                          MOE_F32, M, H, F, tiles, count, gather, gather_k, s));
+    if (L.fc1.partial)
+        LAUNCH(s, "int8_swiglu",
+               launch_int8_swiglu_partial(at<int32_t>(ws, L.h), L.fc1.splits, rows_scale, gather, gather_k,
+                                          w.gate_scale, w.up_scale, offsets, group_expert, G, E, M, F, h_q,
+                                          h_scale, s));
+    else
+        LAUNCH(s, "int8_quantize", launch_int8_quantize(MOE_F32, at<void>(ws, L.h), M, F, h_q, h_scale, s));
+    LAUNCH(s, "fc2_i8",
+           launch_gemm_i8(L.fc2, h_q, h_scale, w.down, w.down_scale, nullptr, nullptr,
+                          L.fc2.partial ? at<void>(ws, L.y_part) : y, MOE_BF16, M, F, H, tiles, count, nullptr, 1,
+                          s));
+    if (L.fc2.partial)
+        LAUNCH(s, "int8_finish",
+               launch_int8_finish(at<int32_t>(ws, L.y_part), L.fc2.splits, h_scale, w.down_scale, offsets,
+                                  group_expert, G, E, M, H, y, MOE_BF16, s));
+    return MOE_OK;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -431,6 +577,12 @@ MOE_API moe_status moe_workspace_size(const moe_problem* p, size_t* bytes)
 {
     if (bytes == nullptr)
         return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
+    if (p != nullptr && p->dtype == MOE_INT8) {
+        if (moe_status st = check_int8_problem(p, true); st != MOE_OK)
+            return st;
+        *bytes = int8_layout(p->T * p->k, p->E, p->H, p->F, p->T, p->k, p->E, true).total;
+        return MOE_OK;
+    }
     if (moe_status st = check_problem(p, true); st != MOE_OK)
         return st;
     *bytes = forward_layout(p->dtype, p->T, p->H, p->F, p->E, p->k, p->head_m_size,
@@ -555,6 +707,58 @@ MOE_API moe_status moe_expert_forward_mx(const moe_problem* p, const uint8_t* x,
         return fail(MOE_ERR_INVALID_ARGUMENT, "null scale pointer");
     return forward_common(p, x, x_scale, w_gate, wg_scale, w_up, wu_scale, w_down, wd_scale,
                           expert_ids, probs, out_bf16, workspace, workspace_bytes, stream);
+}
+
+MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, const float* x_scale,
+                                           const int8_t* w_gate, const float* wg_scale,
+                                           const int8_t* w_up, const float* wu_scale,
+                                           const int8_t* w_down, const float* wd_scale,
+                                           const int32_t* expert_ids, const float* probs,
+                                           void* out_bf16, void* workspace, size_t workspace_bytes,
+                                           hipStream_t stream)
+{
+    if (moe_status st = check_int8_problem(p, true); st != MOE_OK)
+        return st;
+    const bool quantize_x = (p->flags & MOE_FLAG_QUANTIZE_X) != 0;
+    if (quantize_x && x_scale != nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "with MOE_FLAG_QUANTIZE_X, x is bfloat16 and x_scale must be null");
+    const int64_t T = p->T, k = p->k, M = T * k, H = p->H, F = p->F, E = p->E;
+    const Int8Layout L = int8_layout(M, E, H, F, T, k, E, true);
+    if (workspace == nullptr || workspace_bytes < L.total)
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes, got %zu", L.total,
+                    workspace == nullptr ? size_t{0} : workspace_bytes);
+    if (T > 0 && (x == nullptr || (!quantize_x && x_scale == nullptr) || w_gate == nullptr || w_up == nullptr ||
+                  w_down == nullptr || wg_scale == nullptr || wu_scale == nullptr || wd_scale == nullptr ||
+                  expert_ids == nullptr || probs == nullptr || out_bf16 == nullptr))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null data pointer");
+    if (moe_status st = check_aligned({x, w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale, out_bf16, workspace});
+        st != MOE_OK)
+        return st;
+    hipStream_t s = stream;
+    void* ws = workspace;
+    int32_t* perm = at<int32_t>(ws, L.perm);
+    int32_t* pos = at<int32_t>(ws, L.pos);
+    int32_t* offsets = at<int32_t>(ws, L.offsets);
+    if (moe_status st = run_route(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos, ws, L.route, s);
+        st != MOE_OK)
+        return st;
+    if (T == 0)
+        return MOE_OK;
+    const int8_t* rows = static_cast<const int8_t*>(x);
+    const float* rows_scale = x_scale;
+    if (quantize_x) {
+        LAUNCH(s, "int8_quantize",
+               launch_int8_quantize(MOE_BF16, x, T, H, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_q_scale), s));
+        rows = at<int8_t>(ws, L.x_q);
+        rows_scale = at<float>(ws, L.x_q_scale);
+    }
+    const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
+    if (moe_status st = run_ffn_int8(rows, rows_scale, M, offsets, nullptr, E, E, H, F, w, at<void>(ws, L.y), ws, L,
+                                     false, s, perm, static_cast<int>(k));
+        st != MOE_OK)
+        return st;
+    LAUNCH(s, "unpermute", launch_unpermute(1, at<void>(ws, L.y), pos, probs, out_bf16, T, k, M, H, s));
+    return MOE_OK;
 }
 
 // ------------------------------------------------------------------------------------- backward
@@ -825,6 +1029,14 @@ MOE_API moe_status moe_grouped_ffn_workspace_size(const moe_problem* p, int64_t 
 {
     if (bytes == nullptr || M < 0 || G <= 0 || M > INT32_MAX)
         return fail(MOE_ERR_INVALID_ARGUMENT, "bad grouped sizes");
+    if (p != nullptr && p->dtype == MOE_INT8) {
+        if (moe_status st = check_int8_problem(p, false); st != MOE_OK)
+            return st;
+        if (G > INT32_MAX)
+            return fail(MOE_ERR_INVALID_ARGUMENT, "bad grouped sizes");
+        *bytes = int8_layout(M, G, p->H, p->F, 0, 1, p->E, false).total;
+        return MOE_OK;
+    }
     if (moe_status st = check_problem(p, false); st != MOE_OK)
         return st;
     if (p->dtype == MOE_MXFP8_E4M3 && M * std::max(p->H, p->F) > UINT32_MAX)
@@ -884,6 +1096,125 @@ MOE_API moe_status moe_grouped_ffn_mx(const moe_problem* p, const uint8_t* rows,
                           stream);
 }
 
+MOE_API moe_status moe_grouped_ffn_int8(const moe_problem* p, const int8_t* rows, const float* rows_scale,
+                                        int64_t M, const int32_t* group_offsets,
+                                        const int32_t* group_expert, int64_t G, const int8_t* w_gate,
+                                        const float* wg_scale, const int8_t* w_up, const float* wu_scale,
+                                        const int8_t* w_down, const float* wd_scale, void* y_rows,
+                                        void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (p == nullptr || p->dtype != MOE_INT8)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "moe_grouped_ffn_int8 needs dtype MOE_INT8");
+    size_t need = 0;
+    if (moe_status st = moe_grouped_ffn_workspace_size(p, M, G, &need); st != MOE_OK)
+        return st;
+    if (workspace == nullptr || workspace_bytes < need)
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes", need);
+    if (group_offsets == nullptr || group_expert == nullptr ||
+        (M > 0 && (rows == nullptr || rows_scale == nullptr || w_gate == nullptr || w_up == nullptr ||
+                   w_down == nullptr || wg_scale == nullptr || wu_scale == nullptr || wd_scale == nullptr ||
+                   y_rows == nullptr)))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+    if (moe_status st = check_aligned({rows, w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale, y_rows, workspace});
+        st != MOE_OK)
+        return st;
+    const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
+    return run_ffn_int8(rows, rows_scale, M, group_offsets, group_expert, G, p->E, p->H, p->F, w, y_rows, workspace,
+                        int8_layout(M, G, p->H, p->F, 0, 1, p->E, false), true, stream, nullptr, 1);
+}
+
+namespace moe {
+namespace {
+
+struct MatmulLayout {
+    Int8Plan plan{};
+    size_t tile_count = 0, tiles = 0, tiles_run = 0, part = 0, total = 0;
+    int64_t max_tiles = 0;
+};
+
+MatmulLayout matmul_layout(int64_t M, int64_t G, int64_t K, int64_t N)
+{
+    MatmulLayout L;
+    L.plan = int8_plan(M, G, K, N, false);
+    L.max_tiles = max_mtiles(M, G, 0, L.plan.row_tile);
+    Take take{kAlign};
+    L.tile_count = take(8 * 4);
+    L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
+    L.tiles_run = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
+    if (L.plan.partial)
+        L.part = take(4 * M * N * L.plan.splits);
+    L.total = take.off;
+    return L;
+}
+
+}  // namespace
+}  // namespace moe
+
+MOE_API moe_status moe_grouped_matmul_int8_workspace_size(int64_t M, int64_t G, int64_t K, int64_t N,
+                                                          size_t* bytes)
+{
+    if (bytes == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
+    if (moe_status st = check_int8_product(M, G, 1, K, N); st != MOE_OK)
+        return st;
+    *bytes = matmul_layout(M, G, K, N).total;
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows_scale, int64_t M,
+                                           const int32_t* group_offsets, const int32_t* group_expert,
+                                           int64_t G, const int8_t* w, const float* w_scale, int64_t E,
+                                           int64_t K, int64_t N, void* out, int32_t out_dtype,
+                                           void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (moe_status st = check_int8_product(M, G, E, K, N); st != MOE_OK)
+        return st;
+    if (out_dtype != MOE_F32 && out_dtype != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "out_dtype must be MOE_F32 or MOE_BF16");
+    const MatmulLayout L = matmul_layout(M, G, K, N);
+    if (workspace == nullptr || workspace_bytes < L.total)
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes", L.total);
+    if (group_offsets == nullptr || group_expert == nullptr ||
+        (M > 0 && (rows == nullptr || rows_scale == nullptr || w == nullptr || w_scale == nullptr || out == nullptr)))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+    if (moe_status st = check_aligned({rows, w, w_scale, out, workspace}); st != MOE_OK)
+        return st;
+    hipStream_t s = stream;
+    void* ws = workspace;
+    int32_t* tcount = at<int32_t>(ws, L.tile_count);
+    MTile* tiles = at<MTile>(ws, L.tiles_run);
+    LAUNCH(s, "build_tiles",
+           launch_build_tiles(group_offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.plan.row_tile,
+                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0, nullptr,
+                              at<int32_t>(ws, 0), true, s, tiles, tcount + 4));
+    if (M == 0)
+        return MOE_OK;
+    LAUNCH(s, "matmul_i8",
+           launch_gemm_i8(L.plan, rows, rows_scale, w, w_scale, nullptr, nullptr,
+                          L.plan.partial ? at<void>(ws, L.part) : out, out_dtype, M, K, N, tiles, tcount + 4, nullptr,
+                          1, s));
+    if (L.plan.partial)
+        LAUNCH(s, "int8_finish",
+               launch_int8_finish(at<int32_t>(ws, L.part), L.plan.splits, rows_scale, w_scale, group_offsets,
+                                  group_expert, G, E, M, N, out, out_dtype, s));
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_int8_quantize(const void* x, int32_t dtype, int64_t rows, int64_t cols, int8_t* codes,
+                                     float* scales, hipStream_t stream)
+{
+    if (rows < 0 || cols <= 0 || rows > INT32_MAX || cols > (int64_t{1} << 40) / std::max<int64_t>(rows, 1))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "need 0 <= rows < 2^31, cols >= 1 and rows * cols <= 2^40");
+    if (dtype != MOE_F32 && dtype != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "x must be float32 or bfloat16");
+    if (rows == 0)
+        return MOE_OK;
+    if (x == nullptr || codes == nullptr || scales == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+    LAUNCH(stream, "int8_quantize", launch_int8_quantize(dtype, x, rows, cols, codes, scales, stream));
+    return MOE_OK;
+}
+
 MOE_API moe_status moe_mx_quantize(const float* v, int64_t rows, int64_t cols, uint8_t* codes,
                                    uint8_t* scales, hipStream_t stream)
 {
@@ -927,6 +1258,65 @@ MOE_API moe_status moe_router_topk(const float* logits, int64_t T, int64_t E, in
     if (logits == nullptr || expert_ids == nullptr || probs == nullptr)
         return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
     LAUNCH(stream, "router", launch_router(logits, T, E, k, expert_ids, probs, stream));
+    return MOE_OK;
+}
+
+namespace moe {
+namespace {
+
+moe_status check_gate(const moe_gate* gate, int32_t dtype, int64_t T, int64_t E, int64_t k)
+{
+    if (gate == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "gate is null");
+    if (T < 0 || E < 1 || E > 1024 || k < 1 || k > E || k > 64)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "need T >= 0, 1 <= E <= 1024, 1 <= k <= min(E, 64)");
+    if (T > (int64_t{1} << 40) / E)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "T * E too large");
+    if (dtype != MOE_F32 && dtype != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "logits must be float32 or bfloat16");
+    if ((gate->score != MOE_SCORE_SOFTMAX && gate->score != MOE_SCORE_SIGMOID) ||
+        (gate->renormalize != 0 && gate->renormalize != 1))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "unknown score, or renormalize not 0 or 1");
+    if (gate->groups < 1 || E % gate->groups != 0 || gate->topk_groups < 1 || gate->topk_groups > gate->groups ||
+        gate->topk_groups * (E / gate->groups) < k)
+        return fail(MOE_ERR_INVALID_ARGUMENT,
+                    "groups must divide E, with 1 <= topk_groups <= groups and k experts in topk_groups groups");
+    if (gate->group_top != 1 && gate->group_top != 2)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "group_top must be 1 or 2");
+    if (!(gate->scale - gate->scale == 0.0f))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "scale must be finite");
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+MOE_API moe_status moe_router_gate(const moe_gate* gate, const void* logits, int32_t dtype, const float* bias,
+                                   int64_t T, int64_t E, int64_t k, int32_t* expert_ids, float* probs,
+                                   hipStream_t stream)
+{
+    if (moe_status st = check_gate(gate, dtype, T, E, k); st != MOE_OK)
+        return st;
+    if (T == 0)
+        return MOE_OK;
+    if (logits == nullptr || expert_ids == nullptr || probs == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+    LAUNCH(stream, "gate", launch_gate(*gate, logits, dtype, bias, T, E, k, expert_ids, probs, stream));
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_router_gate_backward(const moe_gate* gate, const void* logits, int32_t dtype, int64_t T,
+                                            int64_t E, int64_t k, const int32_t* expert_ids, const float* dprobs,
+                                            void* dlogits, hipStream_t stream)
+{
+    if (moe_status st = check_gate(gate, dtype, T, E, k); st != MOE_OK)
+        return st;
+    if (T == 0)
+        return MOE_OK;
+    if (logits == nullptr || expert_ids == nullptr || dprobs == nullptr || dlogits == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+    LAUNCH(stream, "gate_backward",
+           launch_gate_backward(*gate, logits, dtype, T, E, k, expert_ids, dprobs, dlogits, stream));
     return MOE_OK;
 }
 

@@ -1,0 +1,344 @@
+// int8 rows: one float32 scale per row, codes -127 .. 127.
+//
+//   scale = max|x| / 127,   code = round_to_nearest_even(127 x / max|x|)
+//
+// The code is that of the real quotient: x and the maximum are brought to the maximum's binade by an
+// exact power of two, and for bfloat16 the product 127 x is exact, a quotient that is not a half lies
+// at least 2^-9 away from one, and one residual step makes the quotient right to less than an ulp (and
+// exact where it is a half), so the rounding cannot go to the wrong side.  For float32 values a
+// quotient within 2^-12 of a half is decided again in float64, where 127 x is exact.
+#include <algorithm>
+
+#include "common.h"
+#include "internal.h"
+#include "moe_expert_layer.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 8;
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// A row's constants: y = x * 2^-e lies in (-2, 2).
+struct RowCode {
+    float amax;      // maximum in [1, 2)
+    float inv;       // 1 / amax
+    int shift;       // -e
+    bool finite;     // false: the row holds an infinity or NaN
+    float scale;
+};
+
+__device__ __forceinline__ RowCode row_code(uint32_t amax_bits)
+{
+    RowCode c;
+    c.finite = amax_bits < kInfBits;
+    const float amax = __uint_as_float(amax_bits);
+    const int e = amax_bits == 0 || !c.finite ? 0 : floor_log2_pos(amax_bits);
+    c.shift = -e;
+    c.amax = amax_bits == 0 || !c.finite ? 1.0f : ldexpf(amax, -e);
+    c.inv = 1.0f / c.amax;
+    c.scale = c.finite ? amax / 127.0f : __uint_as_float(0x7fc00000u);
+    return c;
+}
+
+template <bool kExactProduct>
+__device__ __forceinline__ int code_of(float x, const RowCode& c)
+{
+    const float v = ldexpf(x, c.shift);
+    const float y = 127.0f * v;
+    const float q0 = y * c.inv;
+    const float q1 = fmaf(fmaf(-q0, c.amax, y), c.inv, q0);
+    float r = rintf(q1);
+    if constexpr (!kExactProduct) {
+        // |q1 - r| near a half: the float32 product may have moved the quotient over it
+        if (fabsf(fabsf(q1 - r) - 0.5f) < 0x1p-12f)
+            r = static_cast<float>(rint(127.0 * static_cast<double>(v) / static_cast<double>(c.amax)));
+    }
+    return static_cast<int>(r);
+}
+
+// The largest of the workgroup's values, on every thread.
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf)
+{
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1)
+        v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), off)));
+    if ((threadIdx.x & 63) == 0)
+        buf[threadIdx.x >> 6] = v;
+    __syncthreads();
+    uint32_t m = buf[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w)
+        m = max(m, buf[w]);
+    return m;
+}
+
+// The group that holds `row` (offsets clamped into [0, M] as in the tile table) and its expert, or
+// -1 where no group does or its expert is outside [0, E).  All threads call it.
+__device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets,
+                                          const int32_t* __restrict__ group_expert, int G, int E, int64_t M,
+                                          int64_t row, int* found)
+{
+    if (threadIdx.x == 0)
+        *found = INT32_MAX;
+    __syncthreads();
+    for (int g = threadIdx.x; g < G; g += kThreads) {
+        const int64_t rb = min(max(static_cast<int64_t>(offsets[g]), int64_t{0}), M);
+        const int64_t re = min(static_cast<int64_t>(offsets[g + 1]), M);
+        if (row >= rb && row < re)
+            atomicMin(found, g);
+    }
+    __syncthreads();
+    const int g = *found;
+    if (g == INT32_MAX)
+        return -1;
+    const int e = group_expert != nullptr ? group_expert[g] : g;
+    return e >= 0 && e < E ? e : -1;
+}
+
+// One workgroup per row.  The row's values come from Src::load (kV neighbouring ones at a time); the
+// first kPer vectors of a thread stay in registers between the maximum and the codes, later ones are
+// made again.
+template <class Src, int kV, int kPer, bool kExactProduct>
+__device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_t* __restrict__ codes,
+                                             float* __restrict__ scale, uint32_t* buf)
+{
+    float keep[kPer][kV];
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int64_t c = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kV;
+        if (c < cols) {
+            src.load(c, keep[i]);
+#pragma unroll
+            for (int v = 0; v < kV; ++v)
+                amax = max(amax, __float_as_uint(keep[i][v]) & 0x7fffffffu);
+        }
+    }
+    for (int64_t c = (static_cast<int64_t>(kPer) * kThreads + threadIdx.x) * kV; c < cols; c += kThreads * kV) {
+        float x[kV];
+        src.load(c, x);
+#pragma unroll
+        for (int v = 0; v < kV; ++v)
+            amax = max(amax, __float_as_uint(x[v]) & 0x7fffffffu);
+    }
+    const RowCode rc = row_code(block_max(amax, buf));
+    const auto store = [&](int64_t c, const float (&x)[kV]) {
+        if constexpr (kV == 1) {
+            codes[c] = static_cast<int8_t>(rc.finite ? code_of<kExactProduct>(x[0], rc) : 0);
+        } else {
+            uint32_t w[kV / 4];
+#pragma unroll
+            for (int q = 0; q < kV / 4; ++q) {
+                w[q] = 0;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const int code = rc.finite ? code_of<kExactProduct>(x[4 * q + b], rc) : 0;
+                    w[q] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * b);
+                }
+            }
+            *reinterpret_cast<u32x2_t*>(codes + c) = u32x2_t{w[0], w[1]};
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int64_t c = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kV;
+        if (c < cols)
+            store(c, keep[i]);
+    }
+    for (int64_t c = (static_cast<int64_t>(kPer) * kThreads + threadIdx.x) * kV; c < cols; c += kThreads * kV) {
+        float x[kV];
+        src.load(c, x);
+        store(c, x);
+    }
+    if (threadIdx.x == 0)
+        *scale = rc.scale;
+}
+
+template <int kV>
+struct Bf16Row {
+    const uint16_t* x;
+    __device__ __forceinline__ void load(int64_t c, float (&v)[kV]) const
+    {
+        if constexpr (kV == 1) {
+            v[0] = bf16_to_f32(x[c]);
+        } else {
+            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(x + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    }
+};
+
+template <int kV>
+struct F32Row {
+    const float* x;
+    __device__ __forceinline__ void load(int64_t c, float (&v)[kV]) const
+    {
+        if constexpr (kV == 1) {
+            v[0] = x[c];
+        } else {
+            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(x + c);
+            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(x + c + 4);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = lo[i];
+                v[4 + i] = hi[i];
+            }
+        }
+    }
+};
+
+template <class T, template <int> class Row, int kV, int kPer, bool kExactProduct>
+__global__ __launch_bounds__(kThreads) void int8_quantize_kernel(const T* __restrict__ x, int64_t rows,
+                                                                 int64_t cols, int8_t* __restrict__ codes,
+                                                                 float* __restrict__ scales)
+{
+    __shared__ uint32_t buf[2][kThreads / 64];
+    int slot = 0;                                        // two slots: a row's maxima are read while the next row's are written
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, slot ^= 1)
+        quantize_row<Row<kV>, kV, kPer, kExactProduct>(Row<kV>{x + r * cols}, cols, codes + r * cols, scales + r, buf[slot]);
+}
+
+// The SwiGLU of a row's gate and up sums, cut by cut of K.
+struct SwigluRow {
+    const int32_t* p;      // the row in the first cut: gate [F], up [F]
+    int64_t cut;           // elements from one cut to the next
+    int splits;
+    float a_scale;
+    const float* sg;
+    const float* su;
+    int64_t F;
+    __device__ __forceinline__ void load(int64_t c, float (&v)[kVec]) const
+    {
+#pragma unroll
+        for (int q = 0; q < kVec / 4; ++q) {
+            const int64_t cc = c + 4 * q;
+            i32x4_t g = *reinterpret_cast<const i32x4_t*>(p + cc);
+            i32x4_t u = *reinterpret_cast<const i32x4_t*>(p + F + cc);
+            for (int s = 1; s < splits; ++s) {
+                g += *reinterpret_cast<const i32x4_t*>(p + s * cut + cc);
+                u += *reinterpret_cast<const i32x4_t*>(p + s * cut + F + cc);
+            }
+            const f32x4_t wg = *reinterpret_cast<const f32x4_t*>(sg + cc);
+            const f32x4_t wu = *reinterpret_cast<const f32x4_t*>(su + cc);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[4 * q + i] = swiglu(static_cast<float>(g[i]) * a_scale * wg[i], static_cast<float>(u[i]) * a_scale * wu[i]);
+        }
+    }
+};
+
+__global__ __launch_bounds__(kThreads) void int8_swiglu_partial_kernel(
+    const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
+    const int32_t* __restrict__ gather, int gather_k, const float* __restrict__ sg, const float* __restrict__ su,
+    const int32_t* __restrict__ offsets, const int32_t* __restrict__ group_expert, int G, int E, int64_t M,
+    int64_t F, int8_t* __restrict__ codes, float* __restrict__ scales)
+{
+    __shared__ uint32_t buf[kThreads / 64];
+    __shared__ int found;
+    const int64_t r = blockIdx.x;
+    const int e = row_expert(offsets, group_expert, G, E, M, r, &found);
+    if (e < 0)
+        return;
+    SwigluRow src;
+    src.p = partial + r * 2 * F;
+    src.cut = M * 2 * F;
+    src.splits = splits;
+    src.a_scale = a_scale[gather != nullptr ? gather[r] / gather_k : r];
+    src.sg = sg + static_cast<int64_t>(e) * F;
+    src.su = su + static_cast<int64_t>(e) * F;
+    src.F = F;
+    quantize_row<SwigluRow, kVec, 8, false>(src, F, codes + r * F, scales + r, buf);
+}
+
+template <bool kBf16>
+__global__ __launch_bounds__(kThreads) void int8_finish_kernel(
+    const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
+    const float* __restrict__ w_scale, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ group_expert, int G, int E, int64_t M, int64_t N, void* __restrict__ out)
+{
+    __shared__ int found;
+    const int64_t r = blockIdx.x;
+    const int e = row_expert(offsets, group_expert, G, E, M, r, &found);
+    if (e < 0)
+        return;
+    const float as = a_scale[r];
+    const float* ws = w_scale + static_cast<int64_t>(e) * N;
+    for (int64_t c = 4 * (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x); c < N;
+         c += 4 * static_cast<int64_t>(gridDim.y) * kThreads) {
+        i32x4_t a = *reinterpret_cast<const i32x4_t*>(partial + r * N + c);
+        for (int s = 1; s < splits; ++s)
+            a += *reinterpret_cast<const i32x4_t*>(partial + (s * M + r) * N + c);
+        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(ws + c);
+        f32x4_t v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            v[i] = static_cast<float>(a[i]) * as * w[i];
+        if constexpr (kBf16)
+            *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + r * N + c) =
+                u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+        else
+            *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + r * N + c) = v;
+    }
+}
+
+template <class T, template <int> class Row, bool kExactProduct>
+hipError_t launch_quantize(const T* x, int64_t rows, int64_t cols, int8_t* codes, float* scales, hipStream_t s)
+{
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, int64_t{1} << 30));
+    const bool aligned = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
+    if (cols % kVec == 0 && aligned)
+        int8_quantize_kernel<T, Row, kVec, 4, kExactProduct><<<dim3(grid), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
+    else
+        int8_quantize_kernel<T, Row, 1, 16, kExactProduct><<<dim3(grid), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* codes,
+                                float* scales, hipStream_t s)
+{
+    if (rows <= 0)
+        return hipSuccess;
+    if (dtype == MOE_F32)
+        return launch_quantize<float, F32Row, false>(static_cast<const float*>(x), rows, cols, codes, scales, s);
+    return launch_quantize<uint16_t, Bf16Row, true>(static_cast<const uint16_t*>(x), rows, cols, codes, scales, s);
+}
+
+hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const float* a_scale,
+                                      const int32_t* gather, int gather_k, const float* sg, const float* su,
+                                      const int32_t* offsets, const int32_t* group_expert, int64_t G,
+                                      int64_t E, int64_t M, int64_t F, int8_t* codes, float* scales,
+                                      hipStream_t s)
+{
+    if (M <= 0)
+        return hipSuccess;
+    int8_swiglu_partial_kernel<<<dim3(static_cast<unsigned>(M)), dim3(kThreads), 0, s>>>(
+        partial, splits, a_scale, gather, gather_k, sg, su, offsets, group_expert, static_cast<int>(G),
+        static_cast<int>(E), M, F, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_finish(const int32_t* partial, int splits, const float* a_scale, const float* w_scale,
+                              const int32_t* offsets, const int32_t* group_expert, int64_t G, int64_t E,
+                              int64_t M, int64_t N, void* out, int out_dtype, hipStream_t s)
+{
+    if (M <= 0)
+        return hipSuccess;
+    const dim3 grid(static_cast<unsigned>(M), static_cast<unsigned>(std::min<int64_t>(ceil_div(N, 4 * kThreads), 16)));
+    if (out_dtype == MOE_F32)
+        int8_finish_kernel<false><<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, offsets, group_expert,
+                                                                  static_cast<int>(G), static_cast<int>(E), M, N, out);
+    else
+        int8_finish_kernel<true><<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, offsets, group_expert,
+                                                                 static_cast<int>(G), static_cast<int>(E), M, N, out);
+    return hipGetLastError();
+}
+
+}  // namespace moe

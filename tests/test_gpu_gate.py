@@ -1,0 +1,293 @@
+"""The gate (scores, bias, groups, renormalised weights) and its gradient against plain float64 forms.
+
+Tolerances.  U = 2^-24 is half a step of float32.  With bias or groups scores are float64 and one
+rounding to float32 remains: 2 U covers it.  Otherwise: l - max rounds to |l - max| U absolute, i.e.
+relative in the exponential; the exponential itself is within 2 ulp (4 U); a sum of at most 1024
+positive terms over 64 lanes adds at most 16 + 6 roundings; a quotient, the scale and the final value
+one each.  So (|l - max| + 32) U relative to the weight.  The gradient's q = w (d - sum d w) has the same
+relative errors on each product: (2 |l - max| + 96) U times w (|d| + sum |d| w).  bfloat16 outputs add
+2^-8 of the value."""
+import numpy as np
+import pytest
+import torch
+
+import int8_gate_reference as ref
+import moe_expert_layer_amd as mel
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    mel.library()
+
+
+def _logits(T, E, dtype, seed, grid=False):
+    rng = np.random.default_rng(seed)
+    l = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    if grid:
+        l[::2] = np.round(l[::2] * 2) / 2               # equal logits
+    t = torch.from_numpy(l).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    return t, t.float().numpy()
+
+
+def _spread(l):
+    f = np.where(np.isfinite(l), l, 0)
+    return np.abs(f - f.max(1, keepdims=True)).max(initial=0) + np.abs(f).max(initial=0)
+
+
+def _check(t, l, k, **kw):
+    bias = kw.get("bias")
+    dev = dict(kw)
+    if bias is not None:
+        dev["bias"] = torch.from_numpy(bias).cuda()
+    ids, probs = mel.router_gate(t.cuda(), k, **dev)
+    torch.cuda.synchronize()
+    rids, rw, _ = ref.gate(l, k, **kw)
+    assert np.array_equal(ids.cpu().numpy(), rids)
+    wide = bias is not None or kw.get("groups", 1) > 1
+    tol = (2 if wide else _spread(l) + 32) * U
+    got = probs.cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(got))
+    assert np.all(np.abs(got - rw) <= tol * np.abs(rw) + 2.0 ** -149), np.abs(got - rw).max()
+    return ids, probs
+
+
+CASES = [(1, 1, 1, 1, 1), (1, 256, 8, 8, 4), (7, 3, 3, 1, 1), (33, 65, 5, 5, 2), (100, 64, 64, 1, 1), (50, 96, 7, 8, 3),
+         (20, 200, 16, 4, 4), (9, 1024, 64, 16, 8), (5, 1023, 33, 3, 1), (300, 8, 2, 4, 2), (17, 16, 4, 16, 5),
+         (40, 30, 3, 2, 1), (11, 512, 10, 512, 77), (0, 8, 2, 1, 1)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,topk_groups", CASES)
+def test_gate(T, E, k, groups, topk_groups, score):
+    rng = np.random.default_rng(T * 7 + E)
+    for dtype in ("f32", "bf16"):
+        for with_bias in (False, True):
+            for renorm, top in ((True, 2), (False, 1)):
+                print(f"[gate] {T}x{E} k={k} g={groups}/{topk_groups} {score} {dtype} bias={with_bias}", flush=True)
+                t, l = _logits(T, E, dtype, seed=T + E)
+                bias = (0.1 * rng.standard_normal(E)).astype(np.float32) if with_bias else None
+                _check(t, l, k, score=score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=top,
+                       renormalize=renorm, scale=2.5)
+
+
+@pytest.mark.parametrize("E,k,groups,topk_groups", [(8, 3, 1, 1), (48, 6, 6, 2), (256, 8, 8, 4)])
+def test_equal_logits_and_equal_biases(E, k, groups, topk_groups):
+    """Ties go to the lower id, between groups to the lower group."""
+    t, l = _logits(64, E, "f32", 3, grid=True)
+    _check(t, l, k, groups=groups, topk_groups=topk_groups)
+    z = np.zeros((4, E), np.float32)
+    z[1, 1::2] = -0.0
+    for bias in (None, np.full(E, 0.25, np.float32)):
+        ids, _ = _check(torch.from_numpy(z), z, k, score="sigmoid", bias=bias, groups=groups, topk_groups=topk_groups)
+        assert np.array_equal(ids.cpu().numpy(), np.tile(np.arange(k, dtype=np.int32), (4, 1)))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_masked_experts_and_rows(score, with_bias, groups):
+    """-inf logits are taken last with weight 0, whatever their bias; a row of them has ids 0 .. k-1 of
+    the first groups and weights 0.  The type's lowest value is an ordinary, very small logit."""
+    E, k = 16, 6
+    t, l = _logits(32, E, "f32", 9)
+    l = l.copy()
+    l[:, 2:14] = -np.inf
+    l[5] = -np.inf
+    l[6, 1:] = -np.inf
+    l[7] = np.finfo(np.float32).min
+    bias = np.linspace(0.5, -0.5, E).astype(np.float32) if with_bias else None
+    if with_bias:
+        bias[3] = 9.0
+        bias[15] = -np.inf
+    ids, probs = _check(torch.from_numpy(l), l, k, score=score, bias=bias, groups=groups, topk_groups=groups // 2 or 1)
+    assert np.all(probs[5].cpu().numpy() == 0)
+    assert np.array_equal(ids[5].cpu().numpy(), np.arange(k))
+
+
+def test_nan_and_infinite_logits_stay_in_range():
+    E, k = 40, 5
+    for score in ("softmax", "sigmoid"):
+        for bias in (None, torch.zeros(E, device="cuda")):
+            for groups in (1, 8):
+                t, l = _logits(16, E, "f32", 4)
+                l = l.copy()
+                l[0, 7] = np.nan
+                l[1] = np.nan
+                l[2, 3] = np.inf
+                l[3, 3] = -np.nan
+                ids, probs = mel.router_gate(torch.from_numpy(l).cuda(), k, score=score, bias=bias, groups=groups,
+                                             topk_groups=min(groups, 4))
+                ids = ids.cpu().numpy()
+                assert ids.min() >= 0 and ids.max() < E
+                assert all(len(set(r)) == k for r in ids)
+                assert np.all(np.isnan(probs[1].cpu().numpy()))
+                assert np.all(np.isfinite(probs[4:].cpu().numpy()))
+                if groups == 1:
+                    assert ids[0, 0] == 7 and ids[3, 0] == 3
+
+
+def test_plain_softmax_agrees_with_the_plain_router():
+    t, l = _logits(777, 128, "f32", 21, grid=True)
+    a, b = mel.router_gate(t.cuda(), 8), mel.router_topk(t.cuda(), 8)
+    assert torch.equal(a[0], b[0])
+    torch.testing.assert_close(a[1], b[1], rtol=2e-6, atol=0)
+
+
+# ------------------------------------------------------------------------------------------- gradient
+
+def _check_backward(t, l, ids, dp, score, renorm, scale):
+    got = mel.router_gate_backward(t.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(dp).cuda(), score=score,
+                                   renormalize=renorm, scale=scale)
+    torch.cuda.synchronize()
+    assert got.dtype == t.dtype
+    got = got.float().cpu().numpy().astype(np.float64)
+    r = ref.gate_backward(l, ids, dp, score, renorm, scale)
+    s = ref.scores(l, score)
+    valid = (ids >= 0) & (ids < l.shape[1])
+    sel = np.where(valid, np.take_along_axis(s, np.where(valid, ids, 0), 1), 0)
+    d = np.where(valid, np.abs(dp.astype(np.float64) * scale), 0)
+    total = sel.sum(1, keepdims=True)
+    w = sel / np.where(total == 0, 1, total) if renorm else sel
+    mag = np.zeros_like(r)
+    dot = (d * w).sum(1)
+    for t_ in range(l.shape[0]):
+        for j in range(ids.shape[1]):
+            if valid[t_, j]:
+                mag[t_, ids[t_, j]] += w[t_, j] * (d[t_, j] + dot[t_])
+        if score == "softmax" and not renorm:
+            mag[t_] += s[t_] * dot[t_]
+    # The reference's own rounding: a renormalised softmax's gradient is zero outside the selection, which
+    # its Jacobian reaches as s_e sum_i ds_i s_i with |ds_i| s_i <= w_i (d_i + dot): a sum of k <= 64
+    # products that cancel, each and every addition right to 2^-53, so off by at most (2 k + 6) 2^-53
+    # < 2^-45 of s_e sum_i w_i (d_i + dot).
+    own = 2.0 ** -45 * s * (w * (d + dot[:, None])).sum(1, keepdims=True)
+    tol = (2 * _spread(l) + 96) * U * mag + 2.0 ** -120 + own
+    if t.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * np.abs(r)
+    assert np.all(np.isfinite(got))
+    assert np.all(np.abs(got - r) <= tol), (np.abs(got - r) / tol).max()
+    return got
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("T,E,k,_g,_t", CASES)
+def test_gate_backward(T, E, k, _g, _t, score, renorm):
+    rng = np.random.default_rng(T + 3 * E)
+    for dtype in ("f32", "bf16"):
+        print(f"[gate backward] {T}x{E} k={k} {score} {dtype}", flush=True)
+        t, l = _logits(T, E, dtype, seed=T + E + 1)
+        ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32) if T else np.zeros((0, k), np.int32)
+        dp = rng.standard_normal((T, k)).astype(np.float32)
+        _check_backward(t, l, ids, dp, score, renorm, 2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gate_backward_masked_repeated_and_invalid_ids(score, renorm):
+    t, l = _logits(24, 20, "f32", 31)
+    l = l.copy()
+    l[:, 12:] = -np.inf
+    l[3] = -np.inf
+    rng = np.random.default_rng(2)
+    ids = np.stack([rng.permutation(20)[:6] for _ in range(24)]).astype(np.int32)
+    ids[4] = 7                                            # one expert in every slot
+    ids[5, 2] = ids[5, 0]
+    ids[6, 1], ids[6, 3] = -1, 20
+    ids[7] = -5                                           # no slot at all
+    ids[8] = [12, 13, 14, 15, 16, 17]                     # masked experts alone
+    dp = rng.standard_normal((24, 6)).astype(np.float32)
+    got = _check_backward(torch.from_numpy(l), l, ids, dp, score, renorm, 1.0)
+    assert np.all(got[3] == 0) and np.all(got[7] == 0) and np.all(got[8] == 0)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_gate_backward_against_differences(score, renorm):
+    """Central differences of the gate's own weights, selection unchanged: with a step of 2^-5 the third
+    derivative (at most 2 for these scores) leaves 2^-10 / 6 * 2 and the weights' rounding 2 * 8 U / 2^-4
+    per slot."""
+    T, E, k, h = 6, 12, 4, 2.0 ** -5
+    t, l = _logits(T, E, "f32", 77)
+    l = (np.round(l * 8) / 8 + np.arange(E, dtype=np.float32) * 2.0 ** -8).astype(np.float32)
+    rng = np.random.default_rng(1)
+    dp = rng.standard_normal((T, k)).astype(np.float32)
+    kw = dict(score=score, renormalize=renorm, scale=1.0)
+    ids, _ = mel.router_gate(torch.from_numpy(l).cuda(), k, **kw)
+    got = mel.router_gate_backward(torch.from_numpy(l).cuda(), ids, torch.from_numpy(dp).cuda(), **kw).cpu().numpy()
+    bound = (2.0 ** -10 / 3 + 2 * 40 * U / (2 * h)) * np.abs(dp).sum(1)
+    checked = 0
+    for e in range(E):
+        moved = []
+        for sgn in (1, -1):
+            m = l.copy()
+            m[:, e] += np.float32(sgn * h)
+            i2, p2 = mel.router_gate(torch.from_numpy(m).cuda(), k, **kw)
+            i2, p2 = i2.cpu().numpy(), p2.cpu().numpy().astype(np.float64)
+            # the weights of the same experts, in the order of `ids` (nan: no longer chosen)
+            at = np.full((T, k), np.nan)
+            for r in range(T):
+                for j, x in enumerate(ids[r].tolist()):
+                    q = np.flatnonzero(i2[r] == x)
+                    if q.size:
+                        at[r, j] = p2[r, q[0]]
+            moved.append(at)
+        diff = ((moved[0] - moved[1]) / (2 * h) * dp).sum(1)
+        ok = np.isfinite(diff)
+        checked += ok.sum()
+        assert np.all(np.abs(diff - got[:, e])[ok] <= bound[ok])
+    assert checked > T * E // 2
+
+
+# ------------------------------------------------------------------------------------------- how it is called
+
+def test_gate_on_a_stream_and_in_a_graph():
+    """Capture of gate and gradient, replayed on new logits with eager work between; also on a stream
+    that is not the current one of the default."""
+    t, _ = _logits(500, 64, "f32", 5)
+    x = t.cuda()
+    bias = torch.linspace(-0.1, 0.1, 64, device="cuda")
+    dp = torch.randn(500, 6, device="cuda")
+    kw = dict(score="sigmoid", renormalize=True, scale=2.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        ids, p = mel.router_gate(x, 6, bias=bias, groups=8, topk_groups=4, **kw)
+        mel.router_gate_backward(x, ids, dp, **kw)
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        gi, gp = mel.router_gate(x, 6, bias=bias, groups=8, topk_groups=4, **kw)
+        gd = mel.router_gate_backward(x, gi, dp, **kw)
+    for seed in range(3):
+        x.copy_(_logits(500, 64, "f32", 50 + seed)[0])
+        ei, ep = mel.router_gate(x, 6, bias=bias, groups=8, topk_groups=4, **kw)
+        ed = mel.router_gate_backward(x, ei, dp, **kw)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(gi, ei) and torch.equal(gp, ep) and torch.equal(gd, ed)
+
+
+def test_refusals():
+    x = torch.zeros((4, 8), device="cuda")
+    for kw in (dict(k=0), dict(k=9), dict(k=2, groups=3), dict(k=3, groups=4, topk_groups=1), dict(k=1, topk_groups=2),
+               dict(k=1, group_top=3), dict(k=1, scale=float("inf")), dict(k=1, scale=float("nan"))):
+        with pytest.raises(mel.MoeError):
+            mel.router_gate(x, **kw)
+    with pytest.raises(ValueError):
+        mel.router_gate(x, 2, score="tanh")
+    with pytest.raises(ValueError):
+        mel.router_gate(x.half(), 2)
+    with pytest.raises(ValueError):
+        mel.router_gate(x[:, ::2], 2)
+    with pytest.raises(ValueError):
+        mel.router_gate(x, 2, bias=torch.zeros(7, device="cuda"))
+    with pytest.raises(ValueError):
+        mel.router_gate(x.cpu(), 2)
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        mel.router_gate_backward(x, ids, torch.zeros((4, 3), device="cuda"))

@@ -1,0 +1,324 @@
+"""The int8 operators against plain float64 forms.
+
+Tolerances.  U = 2^-24 is half a step of float32.  A product's sum is exact in int32; its conversion and
+two scalings are three roundings: 4 U relative, plus 2^-8 of the value for bfloat16 outputs.  For the
+FFN see int8_gate_reference.ffn; the layer rounds each slot's row to bfloat16 (2^-8 of probs * y) and
+sums k slots in float32 (k U each) before its own final rounding."""
+import numpy as np
+import pytest
+import torch
+
+import int8_gate_reference as ref
+import moe_expert_layer_amd as mel
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+BF = 2.0 ** -8
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    mel.library()
+
+
+def _codes(rng, *shape):
+    return rng.integers(-127, 128, shape, dtype=np.int8)
+
+
+def _scale(rng, *shape, level=0.01):
+    return (level * np.exp(0.5 * rng.standard_normal(shape))).astype(np.float32)
+
+
+def _dev(*arrays):
+    return [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in arrays]
+
+
+def _host(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+# ------------------------------------------------------------------------------------------- quantiser
+
+def _check_codes(t):
+    codes, scales = mel.int8_quantize(t.cuda())
+    torch.cuda.synchronize()
+    q, s = ref.quantize(t.float().numpy())
+    assert np.array_equal(codes.cpu().numpy().astype(np.float64), q)
+    assert np.all(np.abs(scales.cpu().numpy() - s) <= U * s + 2.0 ** -149)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (3, 7), (5, 4096), (17, 65), (64, 128), (9, 8192), (2, 20000),
+                                       (33, 8191), (4, 8200), (700, 1000), (0, 8)])
+def test_quantize(rows, cols, dtype):
+    rng = np.random.default_rng(rows * 31 + cols)
+    x = rng.standard_normal((rows, cols)) * np.exp(3 * rng.standard_normal((rows, 1)))
+    print(f"[int8 quantize] {rows}x{cols} {dtype}", flush=True)
+    _check_codes(torch.from_numpy(x).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_halves_extremes_and_zero_rows(dtype):
+    """Quotients that are exactly a half (ties to even), float32 neighbours of a half, the largest and
+    the smallest values of the type, and rows of zeros."""
+    k = np.arange(-127, 127)
+    half = np.concatenate([[127.0], k + 0.5])
+    rows = [half * 2.0 ** e for e in (0, 100, 120, -100, -133)]
+    near = np.concatenate([[127.0], np.nextafter(np.float32(k + 0.5), np.float32(200)).astype(np.float64)])
+    rows += [near, near * 2.0 ** 120]
+    third = np.concatenate([[3.0], 3.0 * (k + 0.5) / 127.0])
+    rows += [third, np.zeros(255), np.linspace(-3.3e38, 3.3e38, 255), np.full(255, 1e-45)]
+    _check_codes(torch.from_numpy(np.array(rows)).to(torch.float32).to(dtype))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_quantize_rows_that_are_not_finite(dtype):
+    x = torch.randn((6, 300)).to(dtype)
+    x[1, 5], x[2, 299], x[4, 0] = float("nan"), float("inf"), -float("inf")
+    codes, scales = mel.int8_quantize(x.cuda())
+    codes, scales = codes.cpu(), scales.cpu()
+    for r in (1, 2, 4):
+        assert torch.isnan(scales[r]) and not codes[r].any()
+    q, _ = ref.quantize(x[[0, 3, 5]].float().numpy())
+    assert np.array_equal(codes[[0, 3, 5]].numpy().astype(np.float64), q)
+
+
+# ------------------------------------------------------------------------------------------- product
+
+def _offsets(counts, gap=0):
+    return np.concatenate([[gap], gap + np.cumsum(counts)]).astype(np.int32)
+
+
+PRODUCTS = [
+    # counts of rows per group, K, N
+    ([1], 128, 128),
+    ([1, 0, 2], 256, 384),
+    ([0, 0], 128, 256),
+    ([40, 64, 65, 3], 384, 256),                 # 64-row tiles, partial sums
+    ([130, 0, 100, 161], 640, 512),              # 128-row tiles, an odd number of 128-column strips
+    ([300, 257, 1, 512], 256, 640),              # 256-row tiles, half a column tile at the end
+    ([1000], 1152, 128),
+    ([5] * 100, 128, 128),
+    ([700, 0, 900], 128, 256),
+    ([2], 16384, 256),                           # K cut 16 times
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("counts,K,N", PRODUCTS)
+def test_matmul(counts, K, N, out_dtype):
+    rng = np.random.default_rng(len(counts) + K + N)
+    G, M = len(counts), int(np.sum(counts))
+    E = G + 2
+    expert = rng.permutation(E)[:G].astype(np.int32)
+    rows, w = _codes(rng, M, K), _codes(rng, E, K, N)
+    rs, wsc = _scale(rng, M), _scale(rng, E, N)
+    off = _offsets(counts)
+    print(f"[int8 matmul] {counts[:6]} K={K} N={N}", flush=True)
+    out = mel.grouped_matmul_int8(*_dev(rows, rs, off, expert, w, wsc), out_dtype=out_dtype)
+    torch.cuda.synchronize()
+    r = np.concatenate([ref.matmul(rows[a:b], rs[a:b], w[e], wsc[e]) for a, b, e in zip(off, off[1:], expert)]) \
+        if M else np.zeros((0, N))
+    tol = (4 * U + (BF if out_dtype == torch.bfloat16 else 0)) * np.abs(r)
+    assert np.all(np.abs(_host(out) - r) <= tol)
+
+
+def test_matmul_largest_codes():
+    """All codes -128: the largest sums that K allows here, beyond 2^24."""
+    K, N = 4096, 128
+    rows, w = np.full((70, K), -128, np.int8), np.full((1, K, N), -128, np.int8)
+    one = np.ones(70, np.float32)
+    out = mel.grouped_matmul_int8(*_dev(rows, one, np.array([0, 70], np.int32), np.zeros(1, np.int32), w,
+                                        np.ones((1, N), np.float32)), out_dtype=torch.float32)
+    assert torch.all(out == 16384.0 * K)
+
+
+@pytest.mark.parametrize("counts", [[20, 30], [200, 90], [600, 333]])
+def test_matmul_leaves_other_rows_alone_and_skips_bad_experts(counts):
+    """Rows before the first and after the last group, and those of a group whose expert does not
+    exist, keep what `out` held; the status word tells of the expert."""
+    rng = np.random.default_rng(8)
+    K, N, gap = 256, 256, 5
+    M = sum(counts) + gap + 7 + 11
+    off = _offsets(counts + [7], gap)
+    expert = np.array([1, 0, 9], np.int32)
+    rows, w, rs, wsc = _codes(rng, M, K), _codes(rng, 2, K, N), _scale(rng, M), _scale(rng, 2, N)
+    out = torch.full((M, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    mel.grouped_matmul_int8(*_dev(rows, rs, off, expert, w, wsc), out=out, workspace=ws)
+    assert mel.device_status(ws) == 4
+    got = _host(out)
+    a, b = gap, gap + sum(counts)
+    assert np.all(got[:a] == 7.0) and np.all(got[b:] == 7.0)
+    for g in range(2):
+        r = ref.matmul(rows[off[g]:off[g + 1]], rs[off[g]:off[g + 1]], w[expert[g]], wsc[expert[g]])
+        assert np.all(np.abs(got[off[g]:off[g + 1]] - r) <= (4 * U + BF) * np.abs(r))
+
+
+def test_matmul_nan_scale_marks_its_row_alone():
+    rng = np.random.default_rng(12)
+    rows, w = _codes(rng, 70, 128), _codes(rng, 1, 128, 128)
+    rs, wsc = _scale(rng, 70), _scale(rng, 1, 128)
+    rs[3] = np.nan
+    out = _host(mel.grouped_matmul_int8(*_dev(rows, rs, np.array([0, 70], np.int32), np.zeros(1, np.int32), w, wsc)))
+    assert np.all(np.isnan(out[3])) and np.all(np.isfinite(np.delete(out, 3, 0)))
+
+
+# ------------------------------------------------------------------------------------------- FFN, layer
+
+def _weights(rng, E, H, F):
+    return (_codes(rng, E, H, F), _scale(rng, E, F, level=3e-4), _codes(rng, E, H, F), _scale(rng, E, F, level=3e-4),
+            _codes(rng, E, F, H), _scale(rng, E, H, level=3e-4))
+
+
+FFNS = [([1], 128, 128), ([3, 0, 5], 256, 384), ([60, 64, 1], 128, 640), ([150, 129], 384, 256),
+        ([300, 0, 270], 256, 512), ([2000], 128, 128), ([1, 1], 2048, 256)]
+
+
+@pytest.mark.parametrize("counts,H,F", FFNS)
+def test_ffn(counts, H, F):
+    rng = np.random.default_rng(H + F + len(counts))
+    G, M = len(counts), sum(counts)
+    w = _weights(rng, G, H, F)
+    rows, rs = _codes(rng, M, H), _scale(rng, M, level=0.02)
+    off, expert = _offsets(counts), rng.permutation(G).astype(np.int32)
+    print(f"[int8 ffn] {counts} H={H} F={F}", flush=True)
+    out = _host(mel.grouped_ffn_int8(*_dev(rows, rs, off, expert, *w)))
+    for a, b, e in zip(off, off[1:], expert):
+        if b > a:
+            y, slack = ref.ffn(rows[a:b], rs[a:b], *[t[e] for t in w])
+            assert np.all(np.abs(out[a:b] - y) <= slack + BF * (np.abs(y) + slack))
+
+
+LAYERS = [(1, 256, 384, 4, 2), (3, 128, 128, 1, 1), (40, 256, 256, 8, 3), (150, 128, 384, 3, 3), (900, 256, 256, 5, 2),
+          (64, 128, 128, 100, 8)]
+
+
+def _layer_ref(x_codes, x_scale, w, ids, probs):
+    T, k = ids.shape
+    H = w[4].shape[2]
+    r, tol = np.zeros((T, H)), np.zeros((T, H))
+    for e in range(w[0].shape[0]):
+        t, j = np.nonzero(ids == e)
+        if t.size:
+            y, slack = ref.ffn(x_codes[t], x_scale[t], *[a[e] for a in w])
+            p = probs[t, j].astype(np.float64)[:, None]
+            np.add.at(r, t, p * y)
+            np.add.at(tol, t, p * (slack + (BF + 2 * k * U) * (np.abs(y) + slack)))
+    return r, tol + BF * (np.abs(r) + tol)
+
+
+@pytest.mark.parametrize("T,H,F,E,k", LAYERS)
+def test_layer(T, H, F, E, k):
+    rng = np.random.default_rng(T + H + E)
+    w = _weights(rng, E, H, F)
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).bfloat16()
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    probs = rng.dirichlet(np.ones(k), T).astype(np.float32)
+    q, s = ref.quantize(x.float().numpy())
+    r, tol = _layer_ref(q, s, w, ids, probs)
+    wd, idd, pd = _dev(*w), *_dev(ids), *_dev(probs)
+    print(f"[int8 layer] T={T} H={H} F={F} E={E} k={k}", flush=True)
+    out = mel.expert_forward_int8(x.cuda(), None, *wd, idd, pd)
+    assert np.all(np.abs(_host(out) - r) <= tol + 4 * U * np.abs(r))
+    # the same from codes the caller quantised, and again on a workspace the caller keeps: bitwise
+    codes, scales = mel.int8_quantize(x.cuda())
+    prob = mel.problem(T, H, F, E, k, mel.INT8, 0, mel.FLAG_QUANTIZE_X)
+    ws = torch.full((mel.workspace_size(prob),), 255, dtype=torch.uint8, device="cuda")
+    assert torch.equal(mel.expert_forward_int8(codes, scales, *wd, idd, pd, workspace=ws), out)
+    assert torch.equal(mel.expert_forward_int8(x.cuda(), None, *wd, idd, pd, workspace=ws), out)
+
+
+def test_layer_drops_bad_ids_and_marks_nan_tokens():
+    rng = np.random.default_rng(6)
+    T, H, F, E, k = 50, 128, 256, 4, 2
+    w = _weights(rng, E, H, F)
+    x = torch.randn((T, H), dtype=torch.float32).bfloat16()
+    x[9, 3] = float("nan")
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[4] = [E, -1]
+    probs = np.full((T, k), 0.5, np.float32)
+    prob = mel.problem(T, H, F, E, k, mel.INT8, 0, mel.FLAG_QUANTIZE_X)
+    ws = torch.empty(mel.workspace_size(prob), dtype=torch.uint8, device="cuda")
+    out = _host(mel.expert_forward_int8(x.cuda(), None, *_dev(*w), *_dev(ids, probs), workspace=ws))
+    assert mel.device_status(ws) == 4
+    assert np.all(out[4] == 0) and np.all(np.isnan(out[9])) and np.all(np.isfinite(np.delete(out, 9, 0)))
+
+
+def test_gate_then_int8_layer_in_a_graph():
+    """The serving step: gate on the logits, the layer on int8 weights; captured, and replayed on other
+    tokens with eager calls and synchronizations between."""
+    rng = np.random.default_rng(3)
+    T, H, F, E, k = 96, 256, 256, 16, 4
+    w = _dev(*_weights(rng, E, H, F))
+    bias = torch.linspace(-0.05, 0.05, E, device="cuda")
+    x = torch.randn((T, H), device="cuda").bfloat16()
+    logits = torch.randn((T, E), device="cuda")
+
+    def step():
+        ids, probs = mel.router_gate(logits, k, score="sigmoid", bias=bias, groups=4, topk_groups=2, scale=1.5)
+        return mel.expert_forward_int8(x, None, *w, ids, probs)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = step()
+    for _ in range(3):
+        x.copy_(torch.randn((T, H), device="cuda"))
+        logits.copy_(torch.randn((T, E), device="cuda"))
+        eager = step()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager)
+
+
+def test_train_step_of_the_gate_through_the_layer():
+    """Gate, layer, backward, gate backward: the gradient of sum(dout * out) with respect to the logits
+    against float64 differences of the plain form (bf16 layer: 2e-2 of the largest gradient)."""
+    import oracle
+    import synth
+    from synth import device as dv
+    oracle.build()
+    T, H, F, E, k = 24, 128, 128, 6, 2
+    inp = synth.make_layer(T=T, H=H, F=F, E=E, k=k, dtype="bf16", seed=4)
+    d = dv.layer(inp)
+    rng = np.random.default_rng(2)
+    logits = rng.standard_normal((T, E)).astype(np.float32)
+    kw = dict(score="sigmoid", renormalize=True, scale=2.0)
+    ids, probs = mel.router_gate(torch.from_numpy(logits).cuda(), k, bias=torch.zeros(E, device="cuda"), **kw)
+    dout = synth.make_dout(inp)
+    grads = mel.expert_backward(d.x, d.w_gate, d.w_up, d.w_down, ids, probs, dv.tensor(dout))
+    dl = mel.router_gate_backward(torch.from_numpy(logits).cuda(), ids, grads[4], **kw)
+    inp.expert_ids, inp.probs = ids.cpu().numpy(), probs.cpu().numpy()
+    ref_dprobs = oracle.backward(inp, dout)[4]
+    r = ref.gate_backward(logits, inp.expert_ids, ref_dprobs, "sigmoid", True, 2.0)
+    assert np.abs(_host(dl) - r).max() <= 2e-2 * np.abs(r).max()
+
+
+def test_refusals():
+    rows, w = torch.zeros((4, 128), dtype=torch.int8, device="cuda"), torch.zeros((2, 128, 128), dtype=torch.int8, device="cuda")
+    rs, wsc = torch.ones(4, device="cuda"), torch.ones((2, 128), device="cuda")
+    off, ex = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda"), torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        mel.grouped_matmul_int8(rows, rs, off, ex, w, wsc, out_dtype=torch.float16)
+    with pytest.raises(ValueError):
+        mel.grouped_matmul_int8(rows, rs[:3], off, ex, w, wsc)
+    with pytest.raises(ValueError):
+        mel.grouped_matmul_int8(rows, rs, off, ex, w.transpose(1, 2), wsc)
+    with pytest.raises(mel.MoeError):
+        mel.grouped_matmul_int8(rows[:, :64].contiguous(), rs, off, ex, w[:, :64].contiguous(), wsc)
+    with pytest.raises(mel.MoeError):
+        mel.grouped_matmul_int8(rows, rs, off, ex, torch.zeros(2 * 128 * 128 + 4, dtype=torch.int8, device="cuda")[4:].view(2, 128, 128), wsc)
+    with pytest.raises(ValueError):
+        mel.grouped_matmul_int8(rows, rs, off, ex, w, wsc, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        mel.int8_quantize(torch.zeros((2, 8), dtype=torch.float16, device="cuda"))
+    x = torch.zeros((2, 128), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):
+        mel.expert_forward_int8(x, torch.ones(2, device="cuda"), w, wsc, w, wsc, w, wsc,
+                                torch.zeros((2, 1), dtype=torch.int32, device="cuda"), torch.ones((2, 1), device="cuda"))
