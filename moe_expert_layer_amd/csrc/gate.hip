@@ -7,9 +7,14 @@
 //
 // Which experts are chosen is decided as in real arithmetic: without a bias the scores rise with the
 // logits, so within the groups the logits themselves are compared; with a bias, and between groups,
-// the scores are float64 (float32 scores of neighbouring experts often round to one value).
-//
-// A group of L lanes serves one token, as in the plain router: lane l holds experts l, l + L, ...
+// the scores are float64 (float32 scores of neighbouring experts often round to one value).  Almost no
+// token needs that: L lanes per token first work in float32 with 32-bit keys, keep a bound on every
+// error, and only the tokens in which two values that matter lie within it (about one in a thousand of
+// random logits over 256 experts, and every token with a NaN) are done again in float64, one at a time
+// by the whole wave.
+#include <algorithm>
+#include <type_traits>
+
 #include "common.h"
 #include "internal.h"
 #include "moe_expert_layer.h"
@@ -18,15 +23,103 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWavesPerBlock = kThreads / 64;
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
 __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf16_to_f32(*p); }
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+__device__ __forceinline__ void load_logits4(const float* p, float (&v)[4])
+{
+    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(p);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        v[c] = w[c];
+}
+__device__ __forceinline__ void load_logits4(const uint16_t* p, float (&v)[4])
+{
+    const u32x2_t w = *reinterpret_cast<const u32x2_t*>(p);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        v[2 * c] = __uint_as_float(w[c] << 16);
+        v[2 * c + 1] = __uint_as_float(w[c] & 0xffff0000u);
+    }
+}
 
-// Keys of the same order as the values: 1 for -inf (so that 0 is free for "not a candidate"), the
-// largest for NaN.  -0 is made +0.
-__device__ __forceinline__ uint64_t key_of(double c)
+// Exchange step S (partner distance 1 << S) of a reduction over a token's lanes: inside 16 lanes by
+// data-parallel-primitive moves (the mirrors pair each quad, then each half row, with the other one,
+// which serves once the lanes of a quad / half row agree), across rows by a lane exchange.
+template <int S>
+__device__ __forceinline__ int exchange(int v)
+{
+    if constexpr (S == 0)
+        return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xf, 0xf, false);       // quad_perm 1 0 3 2
+    else if constexpr (S == 1)
+        return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xf, 0xf, false);       // quad_perm 2 3 0 1
+    else if constexpr (S == 2)
+        return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xf, 0xf, false);      // row_half_mirror
+    else if constexpr (S == 3)
+        return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xf, 0xf, false);      // row_mirror
+    else
+        return __shfl_xor(v, 1 << S);
+}
+template <int S>
+__device__ __forceinline__ float exchange(float v)
+{
+    return __int_as_float(exchange<S>(__float_as_int(v)));
+}
+template <int S>
+__device__ __forceinline__ uint32_t exchange(uint32_t v)
+{
+    return static_cast<uint32_t>(exchange<S>(static_cast<int>(v)));
+}
+
+// v combined by f over aligned runs of L lanes, on every lane.
+template <int L, int S = 0, class V, class F>
+__device__ __forceinline__ V reduce(V v, F f)
+{
+    if constexpr ((1 << S) < L)
+        return reduce<L, S + 1>(f(v, exchange<S>(v)), f);
+    else
+        return v;
+}
+struct Add {
+    template <class V>
+    __device__ __forceinline__ V operator()(V a, V b) const { return a + b; }
+};
+struct Max {
+    __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct MinU {
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return min(a, b); }
+};
+
+// exp2 on the hardware unit (1 ulp) of x log2 e; the product's rounding makes it |x| 2^-24 relative.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
+
+struct GateArgs {
+    const float* bias;       // may be null
+    int64_t T;
+    int E, k, groups, topk_groups, group_top, sigmoid, renormalize;
+    float scale;
+    int32_t* ids;
+    float* probs;
+    int group_lanes;         // lanes a group's experts cover in one vector of a token's lanes; 0: no such layout
+    int scratch;             // doubles of LDS per wave for the groups (0 without)
+};
+
+// Unsigned integers of the order of the floats (no NaN).
+__device__ __forceinline__ uint32_t ordered(float f)
+{
+    const uint32_t b = __float_as_uint(f);
+    return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t o)
+{
+    return __uint_as_float((o & 0x80000000u) != 0 ? o & 0x7fffffffu : ~o);
+}
+// 64-bit keys: 1 for -inf (so that 0 is free for "not a candidate"), the largest for NaN; -0 as +0.
+__device__ __forceinline__ uint64_t key64(double c)
 {
     if (c != c)
         return ~uint64_t{0};
@@ -34,17 +127,365 @@ __device__ __forceinline__ uint64_t key_of(double c)
     const uint64_t k = (b >> 63) != 0 ? ~b : b | (uint64_t{1} << 63);
     return c == -__builtin_inf() ? 1 : k;
 }
-__device__ __forceinline__ uint64_t key_of(float c)
+
+// One token in float64 by the whole wave: lane l holds experts l, l + 64, ...  lds: E + groups doubles
+// of this wave (with groups alone).
+template <class In, int kPer>
+__device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int64_t t, const GateArgs& a,
+                                              double* lds)
 {
-    if (c != c)
-        return ~uint64_t{0};
-    const uint32_t b = __float_as_uint(c + 0.0f);
-    const uint32_t k = (b >> 31) != 0 ? ~b : b | 0x80000000u;
-    return c == -__builtin_inff() ? 1 : static_cast<uint64_t>(k) << 32;
+    const int lane = threadIdx.x & 63;
+    const auto sum = [](double v) {
+        for (int off = 32; off >= 1; off >>= 1)
+            v += __shfl_xor(v, off);
+        return v;
+    };
+    float l[kPer];
+    float lmax = -__builtin_inff();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 64 * i;
+        l[i] = e < a.E ? load_logit(row + e) : -__builtin_inff();
+        lmax = fmaxf(lmax, l[i]);
+    }
+    double num[kPer];                                         // score = num / den
+    double den = 1.0;
+    if (a.sigmoid) {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            num[i] = 1.0 / (1.0 + exp(-static_cast<double>(l[i])));
+    } else {
+        for (int off = 32; off >= 1; off >>= 1)
+            lmax = fmaxf(lmax, __shfl_xor(lmax, off));
+        den = 0.0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            num[i] = l[i] == -__builtin_inff() ? 0.0 : exp(static_cast<double>(l[i]) - static_cast<double>(lmax));
+            den += num[i];
+        }
+        den = sum(den);
+        if (den == 0.0)
+            den = 1.0;                                        // every logit is -inf: scores 0
+    }
+    uint64_t key[kPer];                                       // 0: taken, or no candidate
+    double c[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int e = lane + 64 * i;
+        c[i] = num[i] / den + (a.bias != nullptr && e < a.E ? static_cast<double>(a.bias[e]) : 0.0);
+        if (l[i] == -__builtin_inff())
+            c[i] = -__builtin_inf();
+        // a NaN logit makes every softmax score NaN: the logits decide then (NaN first)
+        key[i] = e < a.E ? key64(a.bias != nullptr && c[i] == c[i] ? c[i] : static_cast<double>(l[i])) : 0;
+    }
+    if (a.groups > 1) {
+        double* const score = lds + a.E;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (lane + 64 * i < a.E)
+                lds[lane + 64 * i] = c[i];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        const int per = a.E / a.groups;
+        for (int q = lane; q < a.groups; q += 64) {
+            double b1 = -__builtin_inf(), b2 = -__builtin_inf();
+            for (int i = 0; i < per; ++i) {
+                const double v = lds[q * per + i];
+                b2 = fmax(b2, fmin(b1, v));
+                b1 = fmax(b1, v);
+            }
+            score[q] = a.group_top == 2 && b2 > -__builtin_inf() ? b1 + b2 : b1;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int q = min(lane + 64 * i, a.E - 1) / per;
+            const double mine = score[q];
+            int rank = 0;
+            for (int o = 0; o < a.groups; ++o)
+                rank += score[o] > mine || (score[o] == mine && o < q) ? 1 : 0;
+            if (rank >= a.topk_groups)
+                key[i] = 0;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();                      // read before the wave's next token writes
+    }
+    int my_id = 0;
+    double my_num = 0.0;
+    for (int j = 0; j < a.k; ++j) {
+        uint64_t best = 0;
+        int id = 0;
+        double n = 0.0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (key[i] > best) {                              // lower ids first: i ascends
+                best = key[i];
+                id = lane + 64 * i;
+                n = num[i];
+            }
+#pragma unroll
+        for (int off = 32; off >= 1; off >>= 1) {
+            const uint64_t ob = __shfl_xor(static_cast<unsigned long long>(best), off);
+            const int oi = __shfl_xor(id, off);
+            const double on = __shfl_xor(n, off);
+            if (ob > best || (ob == best && oi < id)) {
+                best = ob;
+                id = oi;
+                n = on;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (lane + 64 * i == id)
+                key[i] = 0;
+        if (lane == j) {
+            my_id = id;
+            my_num = n;
+        }
+    }
+    if (a.renormalize) {
+        den = sum(my_num);
+        if (den == 0.0)
+            den = 1.0;                                        // nothing but zero scores: weights 0
+    }
+    if (lane < a.k) {
+        a.ids[t * a.k + lane] = my_id;
+        a.probs[t * a.k + lane] = static_cast<float>(my_num / den * static_cast<double>(a.scale));
+    }
 }
 
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+// L lanes per token; lane g holds the vectors of four experts 4 (L i + g), i < I.
+//
+// Each candidate is one 32-bit key: the ordered bits of what it is compared by, the lowest four replaced
+// by its place in the lane (bfloat16 logits without a bias: the lower 16 bits are free, and the
+// complement of the expert's id makes the keys unique and exact).  The next key below M is
+// M - 1 - min over the keys v of (M - 1 - v), unsigned: keys at or above M wrap to large values, so
+// nothing is taken out of the registers from round to round.
+//
+// Errors, with u = 2^-24 and x = max - l.  softmax: exp(-x) is off by (2.5 x + 2) u relative (the
+// subtraction, the product with log2 e and that constant, a 1-ulp exp2), at most 3 u of the largest
+// score since x exp(-x) < 0.37, and the two products add 2 u; the sum's error (an average of x, at most
+// ln 1024, and 22 additions: 42 u) is one factor common to the token's scores.  The difference of two is
+// thus off by at most 42 + 2 * 5 = 52 u of the largest score.  sigmoid: 10 u each, with scores <= 1.
+// Adding the bias rounds by |c| u each and cutting a key drops less than 16 ulp = 32 u |c|.  So two
+// values more than 64 u = 2^-18 (largest score + |c|) apart are in the right order, and two group
+// scores (sums of two) more than 2^-17 (largest score + |c| + |c'|).  Keys of logits differ only as the
+// logits do.
+template <class In, int L, int I, bool kVec>
+__global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ logits, const GateArgs a)
+{
+    constexpr int kPer = 4 * I;
+    constexpr int kTokens = 64 / L;                           // per wave
+    extern __shared__ __attribute__((aligned(16))) double lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int g = lane & (L - 1), base = lane & ~(L - 1);
+    // LDS: each wave's scratch for the groups, then the winners of its tokens
+    double* const wide = lds + static_cast<size_t>(wave) * a.scratch;
+    float2* const won = reinterpret_cast<float2*>(lds + static_cast<size_t>(kWavesPerBlock) * a.scratch) +
+                        (static_cast<size_t>(wave) * kTokens + lane / L) * a.k;
+    const int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L;
+    const bool live = t < a.T;
+    const In* row = logits + (live ? t : a.T - 1) * a.E;
+    bool unsure = a.groups > 1 && a.group_lanes == 0;         // this token needs float64
+    if (!__all(unsure)) {
+        float l[kPer];
+#pragma unroll
+        for (int i = 0; i < I; ++i) {
+            const int e = 4 * (L * i + g);
+            float v[4] = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+            if (kVec) {
+                if (e < a.E)
+                    load_logits4(row + e, v);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    if (e + c < a.E)
+                        v[c] = load_logit(row + e + c);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                l[4 * i + c] = v[c] + 0.0f;                   // -0 becomes +0: equal logits tie
+        }
+        const bool by_logit = a.bias == nullptr;
+        float num[kPer];                                      // score = num * inv
+        float inv = 1.0f, check = 0.0f;                       // check: NaN if a logit (or bias) is
+        if (a.sigmoid) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                num[q] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[q]));
+                check += num[q];
+            }
+        } else {
+            float m = l[0];
+#pragma unroll
+            for (int q = 1; q < kPer; ++q)
+                m = fmaxf(m, l[q]);
+            m = reduce<L>(m, Max{});
+            float total = 0.0f;
+            m = m == -__builtin_inff() ? 0.0f : m;            // every logit is -inf: scores 0
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                num[q] = fast_exp(l[q] - m);
+                total += num[q];
+            }
+            check = total;
+            total = reduce<L>(total, Add{});
+            inv = total == 0.0f ? 1.0f : 1.0f / total;
+        }
+        const float top_score = a.sigmoid ? 1.0f : inv;
+        float c[kPer];                                        // what the experts are compared by
+        if (by_logit && a.groups == 1) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                c[q] = l[q];
+        } else {
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                const int e = 4 * (L * i + g);
+                float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                if (!by_logit) {
+                    if (kVec) {
+                        if (e < a.E) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                b[q] = a.bias[e + q];
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (e + q < a.E)
+                                b[q] = a.bias[e + q];
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float v = num[4 * i + q] * inv + b[q];
+                    check += v;
+                    c[4 * i + q] = l[4 * i + q] == -__builtin_inff() ? -__builtin_inff() : v;
+                }
+            }
+        }
+        check = reduce<L>(check, Add{});
+        unsure = check != check;
+        uint32_t dropped = 0;                                 // bit i: the group of vector i is out
+        if (a.groups > 1) {
+            // a group is an aligned run of group_lanes lanes of one vector
+            float* const score = reinterpret_cast<float*>(wide) + (lane / L) * a.groups;
+            float mine[I], size[I];
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                const float h1 = fmaxf(c[4 * i], c[4 * i + 1]), l1 = fminf(c[4 * i], c[4 * i + 1]);
+                const float h2 = fmaxf(c[4 * i + 2], c[4 * i + 3]), l2 = fminf(c[4 * i + 2], c[4 * i + 3]);
+                float b1 = fmaxf(h1, h2), b2 = fmaxf(fminf(h1, h2), h1 >= h2 ? l1 : l2);
+                const auto join = [&](float o1, float o2) {
+                    b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+                    b1 = fmaxf(b1, o1);
+                };
+                if (a.group_lanes > 1)
+                    join(exchange<0>(b1), exchange<0>(b2));
+                if (a.group_lanes > 2)
+                    join(exchange<1>(b1), exchange<1>(b2));
+                if (a.group_lanes > 4)
+                    join(exchange<2>(b1), exchange<2>(b2));
+                if (a.group_lanes > 8)
+                    join(exchange<3>(b1), exchange<3>(b2));
+                const bool two = a.group_top == 2 && b2 > -__builtin_inff();
+                mine[i] = two ? b1 + b2 : b1;
+                size[i] = top_score + fabsf(b1) + (two ? fabsf(b2) : 0.0f);
+                const int q = (L * i + g) / a.group_lanes;
+                if (q < a.groups && g % a.group_lanes == 0)
+                    score[q] = mine[i];
+            }
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            int rank[I] = {};
+            bool close = false;
+            for (int o = 0; o < a.groups; ++o) {
+                const float other = score[o];
+#pragma unroll
+                for (int i = 0; i < I; ++i) {
+                    const int q = (L * i + g) / a.group_lanes;
+                    rank[i] += other > mine[i] || (other == mine[i] && o < q) ? 1 : 0;
+                    close |= o != q && q < a.groups && mine[i] > -__builtin_inff() &&
+                             fabsf(other - mine[i]) <= 0x1p-17f * size[i];
+                }
+            }
+            unsure |= reduce<L>(close ? 1 : 0, Add{}) != 0;
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+                dropped |= rank[i] >= a.topk_groups ? 1u << i : 0u;
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+        }
+        constexpr bool kIdKey = std::is_same_v<In, uint16_t>;
+        const bool id_key = kIdKey && by_logit;
+        uint32_t key[kPer];                                   // 0: no candidate
+#pragma unroll
+        for (int q = 0; q < kPer; ++q) {
+            const int e = 4 * (L * (q / 4) + g) + q % 4;
+            const uint32_t o = ordered(by_logit ? l[q] : c[q]);
+            key[q] = id_key ? (o & 0xffff0000u) | (0xffffu - static_cast<uint32_t>(e)) : (o & ~15u) | static_cast<uint32_t>(q);
+            if (e >= a.E || (dropped >> (q / 4) & 1) != 0)
+                key[q] = 0;
+        }
+        uint32_t last = 0;                                    // below every key: M - 1 wraps to the top
+        float before = 0.0f, total = 0.0f, least = __builtin_inff();
+        for (int j = 0; j <= a.k; ++j) {
+            const uint32_t from = last - 1;
+            uint32_t d = from - key[0];
+#pragma unroll
+            for (int q = 1; q < kPer; ++q)
+                d = min(d, from - key[q]);
+            const uint32_t all = reduce<L>(d, MinU{});
+            const uint32_t now = from - all;                  // 0, or wrapped above `last`: none left
+            const bool none = now == 0 || (j > 0 && now >= last);
+            if (!id_key) {
+                // the one before must lie clearly above, and one lane alone may hold this one
+                const float v = now < 0x00800000u ? -__builtin_inff() : unordered(now & ~15u);
+                const float eps = by_logit || v == -__builtin_inff() ? 0.0f : 0x1p-18f * (top_score + fabsf(v));
+                const uint64_t holders = __ballot(d == all) >> base;
+                const bool sole = __popcll(L == 64 ? holders : holders & ((uint64_t{1} << (L & 63)) - 1)) == 1;
+                unsure |= !none && ((j > 0 && !(before - v > eps)) || (j < a.k && !sole));
+                before = v;
+            }
+            unsure |= none && j < a.k;
+            if (j < a.k && d == all && !none) {
+                float n = 0.0f;
+                int id = 0;
+#pragma unroll
+                for (int q = 0; q < kPer; ++q)
+                    if (key[q] == now) {
+                        n = num[q];
+                        id = 4 * (L * (q / 4) + g) + q % 4;
+                    }
+                won[j] = float2{n, __int_as_float(id)};
+                total += n;
+                least = fminf(least, n);
+            }
+            last = now;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        // scores near float32's smallest: their ratios need float64's range
+        unsure |= -reduce<L>(-least, Max{}) < 0x1p-100f;
+        const float den = a.renormalize ? 1.0f / reduce<L>(total, Add{}) : inv;
+        if (live && !unsure)
+            for (int j = g; j < a.k; j += L) {
+                const float2 w = won[j];
+                a.ids[t * a.k + j] = __float_as_int(w.y);
+                a.probs[t * a.k + j] = w.x * den * a.scale;
+            }
+    }
+    // the tokens left, one after the other
+    uint64_t todo = __ballot(live && unsure && g == 0);
+    while (todo != 0) {
+        const int first = __ffsll(static_cast<unsigned long long>(todo)) - 1;
+        todo &= todo - 1;
+        const int64_t tt = static_cast<int64_t>(blockIdx.x) * (kThreads / L) + wave * kTokens + first / L;
+        gate_token_exact<In, (4 * L * I + 63) / 64>(logits + tt * a.E, tt, a, wide);
+    }
+}
 
 template <class V>
 __device__ __forceinline__ V group_sum(V v, int L)
@@ -58,148 +499,6 @@ __device__ __forceinline__ float group_max(float v, int L)
     for (int off = L / 2; off >= 1; off >>= 1)
         v = fmaxf(v, __shfl_xor(v, off));
     return v;
-}
-
-struct GateArgs {
-    const float* bias;       // may be null
-    int64_t T;
-    int E, k, groups, topk_groups, group_top, sigmoid, renormalize;
-    float scale;
-    int32_t* ids;
-    float* probs;
-};
-
-// kWide: float64 scores, with bias and groups; otherwise float32 scores and selection by logits.
-template <class In, int L, int kPer, bool kWide>
-__global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ logits, const GateArgs a)
-{
-    using V = std::conditional_t<kWide, double, float>;
-    const int lane = threadIdx.x & 63;
-    const int g = lane & (L - 1), base = lane & ~(L - 1);
-    const int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L;
-    const bool live = t < a.T;
-    const In* row = logits + (live ? t : 0) * a.E;
-    float l[kPer];
-    float lmax = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int e = g + L * i;
-        l[i] = e < a.E ? load_logit(row + e) : -__builtin_inff();
-        lmax = fmaxf(lmax, l[i]);
-    }
-    // scores: s = num / den, den shared by the token
-    V num[kPer];
-    V den = V(1);
-    if (a.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            num[i] = V(1) / (V(1) + exp_of(-static_cast<V>(l[i])));
-    } else {
-        lmax = group_max(lmax, L);
-        den = V(0);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            num[i] = l[i] == -__builtin_inff() ? V(0) : exp_of(static_cast<V>(l[i]) - static_cast<V>(lmax));
-            den += num[i];
-        }
-        den = group_sum(den, L);
-        if (den == V(0))
-            den = V(1);                                       // every logit is -inf: scores 0
-    }
-    uint64_t key[kPer];                                       // 0: taken, or no candidate
-    if constexpr (kWide) {
-        double c[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int e = g + L * i;
-            c[i] = num[i] / den + (a.bias != nullptr && e < a.E ? static_cast<double>(a.bias[e]) : 0.0);
-            if (l[i] == -__builtin_inff())
-                c[i] = -__builtin_inf();
-            // a NaN logit makes every softmax score NaN: the logits decide then (NaN first)
-            key[i] = e < a.E ? key_of(a.bias != nullptr && c[i] == c[i] ? c[i] : static_cast<double>(l[i])) : 0;
-        }
-        if (a.groups > 1) {
-            // c of the token's experts, then the groups' scores, in LDS
-            extern __shared__ __attribute__((aligned(16))) double lds[];
-            double* const tc = lds + static_cast<size_t>(threadIdx.x / L) * (a.E + a.groups);
-            double* const score = tc + a.E;
-#pragma unroll
-            for (int i = 0; i < kPer; ++i)
-                if (g + L * i < a.E)
-                    tc[g + L * i] = c[i];
-            __syncthreads();
-            const int per = a.E / a.groups;
-            for (int q = g; q < a.groups; q += L) {
-                double b1 = -__builtin_inf(), b2 = -__builtin_inf();
-                for (int i = 0; i < per; ++i) {
-                    const double v = tc[q * per + i];
-                    b2 = fmax(b2, fmin(b1, v));
-                    b1 = fmax(b1, v);
-                }
-                score[q] = a.group_top == 2 && b2 > -__builtin_inf() ? b1 + b2 : b1;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                const int q = min(g + L * i, a.E - 1) / per;
-                const double mine = score[q];
-                int rank = 0;
-                for (int o = 0; o < a.groups; ++o)
-                    rank += score[o] > mine || (score[o] == mine && o < q) ? 1 : 0;
-                if (rank >= a.topk_groups)
-                    key[i] = 0;
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            key[i] = g + L * i < a.E ? key_of(l[i]) : 0;
-    }
-    int my_id = 0;
-    V my_num = V(0);
-    for (int j = 0; j < a.k; ++j) {
-        uint64_t best = 0;
-        int id = 0;
-        V n = V(0);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (key[i] > best) {                              // lower ids first: i ascends
-                best = key[i];
-                id = g + L * i;
-                n = num[i];
-            }
-#pragma unroll
-        for (int off = L / 2; off >= 1; off >>= 1) {
-            const uint64_t ob = __shfl_xor(static_cast<unsigned long long>(best), off);
-            const int oi = __shfl_xor(id, off);
-            const V on = __shfl_xor(n, off);
-            if (ob > best || (ob == best && oi < id)) {
-                best = ob;
-                id = oi;
-                n = on;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (g + L * i == id)
-                key[i] = 0;
-        if (g == j) {
-            my_id = id;
-            my_num = n;
-        }
-    }
-    (void)base;
-    if (g >= a.k)
-        my_num = V(0);
-    if (a.renormalize) {
-        den = group_sum(my_num, L);
-        if (den == V(0))
-            den = V(1);                                       // nothing but zero scores: weights 0
-    }
-    if (live && g < a.k) {
-        a.ids[t * a.k + g] = my_id;
-        a.probs[t * a.k + g] = static_cast<float>(my_num / den * static_cast<V>(a.scale));
-    }
 }
 
 struct GateBackwardArgs {
@@ -296,19 +595,48 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __res
     }
 }
 
-template <class In, int L, int kPer>
-hipError_t launch_gate_n(const In* logits, const GateArgs& a, bool wide, hipStream_t s)
+template <class In, int L, int I>
+hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
 {
     const int64_t blocks = ceil_div(a.T * L, kThreads);
     if (blocks >= (int64_t{1} << 31))
         return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
-    const size_t lds = a.groups > 1 ? sizeof(double) * (kThreads / L) * static_cast<size_t>(a.E + a.groups) : 0;
-    if (wide)
-        gate_kernel<In, L, kPer, true><<<grid, dim3(kThreads), lds, s>>>(logits, a);
+    // groups that are whole vectors of a power of two of neighbouring lanes (at most a row of 16)
+    const int per = a.E / a.groups;
+    a.group_lanes = a.groups > 1 && per % 4 == 0 && (per & (per - 1)) == 0 && per <= 4 * std::min(L, 16) ? per / 4 : 0;
+    // a token's experts and groups in float64, or the float32 group scores of the wave's tokens
+    a.scratch = a.groups > 1 ? std::max(a.E + a.groups, (64 / L) * a.groups / 2 + 1) : 0;
+    const size_t lds = sizeof(double) * kWavesPerBlock * static_cast<size_t>(a.scratch) +
+                       sizeof(float2) * (kThreads / L) * static_cast<size_t>(a.k);
+    const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(In)) == 0;
+    if (vec)
+        gate_kernel<In, L, I, true><<<grid, dim3(kThreads), lds, s>>>(logits, a);
     else
-        gate_kernel<In, L, kPer, false><<<grid, dim3(kThreads), 0, s>>>(logits, a);
+        gate_kernel<In, L, I, false><<<grid, dim3(kThreads), lds, s>>>(logits, a);
     return hipGetLastError();
+}
+
+// The gate's lanes per token: four experts a lane up to 64 (so that small gates fill the wave with
+// tokens), then vectors of four over 16 lanes, and the whole wave beyond 256.
+template <class In>
+hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
+{
+    if (a.E <= 8)
+        return launch_gate_n<In, 2, 1>(logits, a, s);
+    if (a.E <= 16)
+        return launch_gate_n<In, 4, 1>(logits, a, s);
+    if (a.E <= 32)
+        return launch_gate_n<In, 8, 1>(logits, a, s);
+    if (a.E <= 64)
+        return launch_gate_n<In, 16, 1>(logits, a, s);
+    if (a.E <= 128)
+        return launch_gate_n<In, 16, 2>(logits, a, s);
+    if (a.E <= 256)
+        return launch_gate_n<In, 16, 4>(logits, a, s);
+    if (a.E <= 512)
+        return launch_gate_n<In, 64, 2>(logits, a, s);
+    return launch_gate_n<In, 64, 4>(logits, a, s);
 }
 
 template <class In, int L, int kPer>
@@ -363,11 +691,8 @@ hipError_t launch_gate(const moe_gate& o, const void* logits, int dtype, const f
     a.scale = o.scale;
     a.ids = ids;
     a.probs = probs;
-    const bool wide = bias != nullptr || o.groups > 1;
-    return with_lanes(a.E, [&](auto L, auto per) {
-        return dtype == MOE_F32 ? launch_gate_n<float, L(), per()>(static_cast<const float*>(logits), a, wide, s)
-                                : launch_gate_n<uint16_t, L(), per()>(static_cast<const uint16_t*>(logits), a, wide, s);
-    });
+    return dtype == MOE_F32 ? launch_gate_t(static_cast<const float*>(logits), a, s)
+                            : launch_gate_t(static_cast<const uint16_t*>(logits), a, s);
 }
 
 hipError_t launch_gate_backward(const moe_gate& o, const void* logits, int dtype, int64_t T, int64_t E,
