@@ -46,9 +46,9 @@ __device__ __forceinline__ void load_logits4(const uint16_t* p, float (&v)[4])
     }
 }
 
-// Exchange step S (partner distance 1 << S) of a reduction over a token's lanes: inside 16 lanes by
-// data-parallel-primitive moves (the mirrors pair each quad, then each half row, with the other one,
-// which serves once the lanes of a quad / half row agree), across rows by a lane exchange.
+// Exchange step S (partner distance 1 << S) of a reduction over a token's lanes inside a row of 16, by
+// data-parallel-primitive moves: the mirrors pair each quad, then each half row, with the other one,
+// which serves once the lanes of a quad / half row agree.
 template <int S>
 __device__ __forceinline__ int exchange(int v)
 {
@@ -58,10 +58,8 @@ __device__ __forceinline__ int exchange(int v)
         return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xf, 0xf, false);       // quad_perm 2 3 0 1
     else if constexpr (S == 2)
         return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xf, 0xf, false);      // row_half_mirror
-    else if constexpr (S == 3)
-        return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xf, 0xf, false);      // row_mirror
     else
-        return __shfl_xor(v, 1 << S);
+        return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xf, 0xf, false);      // row_mirror
 }
 template <int S>
 __device__ __forceinline__ float exchange(float v)
@@ -74,14 +72,34 @@ __device__ __forceinline__ uint32_t exchange(uint32_t v)
     return static_cast<uint32_t>(exchange<S>(static_cast<int>(v)));
 }
 
-// v combined by f over aligned runs of L lanes, on every lane.
+// Steps 4 and 5: v of the lower and of the upper one of two neighbouring rows / halves, on both.
+template <int S>
+__device__ __forceinline__ void pair(int v, int& lower, int& upper)
+{
+    if constexpr (S == 4) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        lower = r[0];
+        upper = r[1];
+    } else {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        lower = r[0];
+        upper = r[1];
+    }
+}
+
+// v combined by the commutative f over aligned runs of L lanes, on every lane.
 template <int L, int S = 0, class V, class F>
 __device__ __forceinline__ V reduce(V v, F f)
 {
-    if constexpr ((1 << S) < L)
-        return reduce<L, S + 1>(f(v, exchange<S>(v)), f);
-    else
+    if constexpr ((1 << S) >= L) {
         return v;
+    } else if constexpr (S < 4) {
+        return reduce<L, S + 1>(f(v, exchange<S>(v)), f);
+    } else {
+        int lower, upper;
+        pair<S>(__builtin_bit_cast(int, v), lower, upper);
+        return reduce<L, S + 1>(f(__builtin_bit_cast(V, lower), __builtin_bit_cast(V, upper)), f);
+    }
 }
 struct Add {
     template <class V>
@@ -104,7 +122,7 @@ struct GateArgs {
     float scale;
     int32_t* ids;
     float* probs;
-    int group_lanes;         // lanes a group's experts cover in one vector of a token's lanes; 0: no such layout
+    int group_shift;         // log2 of the lanes a group's experts cover in one vector; -1: no such layout
     int scratch;             // doubles of LDS per wave for the groups (0 without)
 };
 
@@ -282,34 +300,33 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
     const int g = lane & (L - 1), base = lane & ~(L - 1);
     // LDS: each wave's scratch for the groups, then the winners of its tokens
     double* const wide = lds + static_cast<size_t>(wave) * a.scratch;
-    float2* const won = reinterpret_cast<float2*>(lds + static_cast<size_t>(kWavesPerBlock) * a.scratch) +
+    int* const won = reinterpret_cast<int*>(lds + static_cast<size_t>(kWavesPerBlock) * a.scratch) +
                         (static_cast<size_t>(wave) * kTokens + lane / L) * a.k;
     const int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L;
     const bool live = t < a.T;
     const In* row = logits + (live ? t : a.T - 1) * a.E;
-    bool unsure = a.groups > 1 && a.group_lanes == 0;         // this token needs float64
+    bool unsure = a.groups > 1 && a.group_shift < 0;         // this token needs float64
     if (!__all(unsure)) {
         float l[kPer];
 #pragma unroll
         for (int i = 0; i < I; ++i) {
             const int e = 4 * (L * i + g);
-            float v[4] = {-__builtin_inff(), -__builtin_inff(), -__builtin_inff(), -__builtin_inff()};
+            float v[4];                                       // past the row's end: its last values, replaced below
             if (kVec) {
-                if (e < a.E)
-                    load_logits4(row + e, v);
+                load_logits4(row + min(e, a.E - 4), v);
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
-                    if (e + c < a.E)
-                        v[c] = load_logit(row + e + c);
+                    v[c] = load_logit(row + min(e + c, a.E - 1));
             }
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                l[4 * i + c] = v[c] + 0.0f;                   // -0 becomes +0: equal logits tie
+                l[4 * i + c] = e + c < a.E ? v[c] + 0.0f : -__builtin_inff();   // -0 becomes +0: equal logits tie
         }
         const bool by_logit = a.bias == nullptr;
         float num[kPer];                                      // score = num * inv
         float inv = 1.0f, check = 0.0f;                       // check: NaN if a logit (or bias) is
+        float m = 0.0f;
         if (a.sigmoid) {
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
@@ -317,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 check += num[q];
             }
         } else {
-            float m = l[0];
+            m = l[0];
 #pragma unroll
             for (int q = 1; q < kPer; ++q)
                 m = fmaxf(m, l[q]);
@@ -345,23 +362,14 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 const int e = 4 * (L * i + g);
                 float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 if (!by_logit) {
-                    if (kVec) {
-                        if (e < a.E) {
 #pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                b[q] = a.bias[e + q];
-                        }
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            if (e + q < a.E)
-                                b[q] = a.bias[e + q];
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        b[q] = a.bias[kVec ? min(e, a.E - 4) + q : min(e + q, a.E - 1)];
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float v = num[4 * i + q] * inv + b[q];
-                    check += v;
+                    check += e + q < a.E ? v : 0.0f;
                     c[4 * i + q] = l[4 * i + q] == -__builtin_inff() ? -__builtin_inff() : v;
                 }
             }
@@ -370,9 +378,9 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
         unsure = check != check;
         uint32_t dropped = 0;                                 // bit i: the group of vector i is out
         if (a.groups > 1) {
-            // a group is an aligned run of group_lanes lanes of one vector
+            // a group is an aligned run of 1 << group_shift lanes of one vector
             float* const score = reinterpret_cast<float*>(wide) + (lane / L) * a.groups;
-            float mine[I], size[I];
+            float mine[I], size = 0.0f;
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 const float h1 = fmaxf(c[4 * i], c[4 * i + 1]), l1 = fminf(c[4 * i], c[4 * i + 1]);
@@ -382,39 +390,47 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                     b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
                     b1 = fmaxf(b1, o1);
                 };
-                if (a.group_lanes > 1)
+                if (a.group_shift > 0)
                     join(exchange<0>(b1), exchange<0>(b2));
-                if (a.group_lanes > 2)
+                if (a.group_shift > 1)
                     join(exchange<1>(b1), exchange<1>(b2));
-                if (a.group_lanes > 4)
+                if (a.group_shift > 2)
                     join(exchange<2>(b1), exchange<2>(b2));
-                if (a.group_lanes > 8)
+                if (a.group_shift > 3)
                     join(exchange<3>(b1), exchange<3>(b2));
                 const bool two = a.group_top == 2 && b2 > -__builtin_inff();
                 mine[i] = two ? b1 + b2 : b1;
-                size[i] = top_score + fabsf(b1) + (two ? fabsf(b2) : 0.0f);
-                const int q = (L * i + g) / a.group_lanes;
-                if (q < a.groups && g % a.group_lanes == 0)
+                size = fmaxf(size, b1 > -__builtin_inff() ? fabsf(b1) + (two ? fabsf(b2) : 0.0f) : 0.0f);
+                const int q = (L * i + g) >> a.group_shift;
+                if (q < a.groups && (g & ((1 << a.group_shift) - 1)) == 0)
                     score[q] = mine[i];
             }
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
             int rank[I] = {};
-            bool close = false;
             for (int o = 0; o < a.groups; ++o) {
                 const float other = score[o];
 #pragma unroll
-                for (int i = 0; i < I; ++i) {
-                    const int q = (L * i + g) / a.group_lanes;
-                    rank[i] += other > mine[i] || (other == mine[i] && o < q) ? 1 : 0;
-                    close |= o != q && q < a.groups && mine[i] > -__builtin_inff() &&
-                             fabsf(other - mine[i]) <= 0x1p-17f * size[i];
+                for (int i = 0; i < I; ++i)
+                    rank[i] += other > mine[i] || (other == mine[i] && o < ((L * i + g) >> a.group_shift)) ? 1 : 0;
+            }
+            // the last group kept must lie clearly above the first one dropped
+            float in = __builtin_inff(), out = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < I; ++i) {
+                if ((L * i + g) >> a.group_shift >= a.groups)
+                    continue;
+                if (rank[i] >= a.topk_groups) {
+                    dropped |= 1u << i;
+                    out = fmaxf(out, mine[i]);
+                } else {
+                    in = fminf(in, mine[i]);
                 }
             }
-            unsure |= reduce<L>(close ? 1 : 0, Add{}) != 0;
-#pragma unroll
-            for (int i = 0; i < I; ++i)
-                dropped |= rank[i] >= a.topk_groups ? 1u << i : 0u;
+            in = -reduce<L>(-in, Max{});
+            out = reduce<L>(out, Max{});
+            size = reduce<L>(size, Max{});
+            unsure |= a.topk_groups < a.groups && !(in - out > 0x1p-17f * (top_score + size));
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
         }
@@ -430,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 key[q] = 0;
         }
         uint32_t last = 0;                                    // below every key: M - 1 wraps to the top
-        float before = 0.0f, total = 0.0f, least = __builtin_inff();
+        float before = 0.0f;
         for (int j = 0; j <= a.k; ++j) {
             const uint32_t from = last - 1;
             uint32_t d = from - key[0];
@@ -450,32 +466,40 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 before = v;
             }
             unsure |= none && j < a.k;
-            if (j < a.k && d == all && !none) {
-                float n = 0.0f;
-                int id = 0;
-#pragma unroll
-                for (int q = 0; q < kPer; ++q)
-                    if (key[q] == now) {
-                        n = num[q];
-                        id = 4 * (L * (q / 4) + g) + q % 4;
-                    }
-                won[j] = float2{n, __int_as_float(id)};
-                total += n;
-                least = fminf(least, n);
-            }
+            if (j < a.k && d == all)
+                won[j] = id_key ? 0xffff - static_cast<int>(now & 0xffffu)
+                                : 4 * (L * static_cast<int>(now >> 2 & 3) + g) + static_cast<int>(now & 3);
             last = now;
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        // scores near float32's smallest: their ratios need float64's range
-        unsure |= -reduce<L>(-least, Max{}) < 0x1p-100f;
-        const float den = a.renormalize ? 1.0f / reduce<L>(total, Add{}) : inv;
-        if (live && !unsure)
-            for (int j = g; j < a.k; j += L) {
-                const float2 w = won[j];
-                a.ids[t * a.k + j] = __float_as_int(w.y);
-                a.probs[t * a.k + j] = w.x * den * a.scale;
+        if (!__all(unsure)) {
+            // the winners' scores again, one a lane
+            float total = 0.0f, least = __builtin_inff();
+            const auto score = [&](int id) {
+                const float x = load_logit(row + id);
+                return a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - m);
+            };
+            int id = 0;
+            float n = 0.0f;
+            for (int j = g; j < a.k && !unsure; j += L) {
+                id = won[j];
+                n = score(id);
+                total += n;
+                least = fminf(least, n);
             }
+            // scores near float32's smallest: their ratios need float64's range
+            unsure |= -reduce<L>(-least, Max{}) < 0x1p-100f;
+            const float factor = (a.renormalize ? 1.0f / reduce<L>(total, Add{}) : inv) * a.scale;
+            for (int j = g; j < a.k && live && !unsure; j += L) {
+                if (a.k > L) {
+                    id = won[j];
+                    n = score(id);
+                }
+                a.ids[t * a.k + j] = id;
+                a.probs[t * a.k + j] = n * factor;
+            }
+        }
     }
     // the tokens left, one after the other
     uint64_t todo = __ballot(live && unsure && g == 0);
@@ -604,11 +628,14 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
     const dim3 grid(static_cast<unsigned>(blocks));
     // groups that are whole vectors of a power of two of neighbouring lanes (at most a row of 16)
     const int per = a.E / a.groups;
-    a.group_lanes = a.groups > 1 && per % 4 == 0 && (per & (per - 1)) == 0 && per <= 4 * std::min(L, 16) ? per / 4 : 0;
+    a.group_shift = -1;
+    for (int b = 0; b <= 4; ++b)
+        if (a.groups > 1 && per == 4 << b && (1 << b) <= L)
+            a.group_shift = b;
     // a token's experts and groups in float64, or the float32 group scores of the wave's tokens
     a.scratch = a.groups > 1 ? std::max(a.E + a.groups, (64 / L) * a.groups / 2 + 1) : 0;
     const size_t lds = sizeof(double) * kWavesPerBlock * static_cast<size_t>(a.scratch) +
-                       sizeof(float2) * (kThreads / L) * static_cast<size_t>(a.k);
+                       sizeof(int) * (kThreads / L) * static_cast<size_t>(a.k);
     const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(In)) == 0;
     if (vec)
         gate_kernel<In, L, I, true><<<grid, dim3(kThreads), lds, s>>>(logits, a);
@@ -618,10 +645,13 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
 }
 
 // The gate's lanes per token: four experts a lane up to 64 (so that small gates fill the wave with
-// tokens), then vectors of four over 16 lanes, and the whole wave beyond 256.
+// tokens), then vectors of four over 16 lanes, and the whole wave beyond 256 or for few tokens (a lane's
+// work is then a quarter, and no wave waits for another).
 template <class In>
 hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
 {
+    if (a.E > 64 && a.E <= 256 && a.T <= 4 * device_info().cu_count)
+        return launch_gate_n<In, 64, 1>(logits, a, s);
     if (a.E <= 8)
         return launch_gate_n<In, 2, 1>(logits, a, s);
     if (a.E <= 16)
