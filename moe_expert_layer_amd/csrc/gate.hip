@@ -123,7 +123,7 @@ struct GateArgs {
     int32_t* ids;
     float* probs;
     int group_shift;         // log2 of the lanes a group's experts cover in one vector; -1: no such layout
-    int scratch;             // doubles of LDS per wave for the groups (0 without)
+    int scratch;             // doubles of LDS per wave for the groups (0 without): a token's experts and groups
 };
 
 // Unsigned integers of the order of the floats (no NaN).
@@ -275,37 +275,43 @@ __device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int
 
 // L lanes per token; lane g holds the vectors of four experts 4 (L i + g), i < I.
 //
-// Each candidate is one 32-bit key: the ordered bits of what it is compared by, the lowest four replaced
+// Each candidate is one 32-bit key: the ordered bits of what it is compared by, the lowest ones replaced
 // by its place in the lane (bfloat16 logits without a bias: the lower 16 bits are free, and the
 // complement of the expert's id makes the keys unique and exact).  The next key below M is
 // M - 1 - min over the keys v of (M - 1 - v), unsigned: keys at or above M wrap to large values, so
-// nothing is taken out of the registers from round to round.
+// nothing is taken out of the registers from round to round.  The lane that holds a round's key leaves
+// key and id in LDS, where the token's lanes check them and make the weights, one winner a lane.
 //
 // Errors, with u = 2^-24 and x = max - l.  softmax: exp(-x) is off by (2.5 x + 2) u relative (the
 // subtraction, the product with log2 e and that constant, a 1-ulp exp2), at most 3 u of the largest
 // score since x exp(-x) < 0.37, and the two products add 2 u; the sum's error (an average of x, at most
 // ln 1024, and 22 additions: 42 u) is one factor common to the token's scores.  The difference of two is
-// thus off by at most 42 + 2 * 5 = 52 u of the largest score.  sigmoid: 10 u each, with scores <= 1.
-// Adding the bias rounds by |c| u each and cutting a key drops less than 16 ulp = 32 u |c|.  So two
-// values more than 64 u = 2^-18 (largest score + |c|) apart are in the right order, and two group
-// scores (sums of two) more than 2^-17 (largest score + |c| + |c'|).  Keys of logits differ only as the
-// logits do.
+// thus off by at most 42 + 2 * 5 = 52 u of the largest score.  sigmoid: the exponential is off by
+// (1.5 |l| + 2) u, which s (1 - s) makes 0.9 u, and the sum and a 1-ulp reciprocal add 3 u: 8 u for two.
+// Adding the bias rounds by |c| u each, and cutting a key drops less than kPer ulp = 2 kPer u |c|.  For
+// group scores (sums of two) it is twice the scores' part, u for each |c| and for the sum.  Values that
+// lie further apart are in the right order.  Keys of logits differ only as the logits do.
 template <class In, int L, int I, bool kVec>
 __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ logits, const GateArgs a)
 {
     constexpr int kPer = 4 * I;
     constexpr int kTokens = 64 / L;                           // per wave
+    constexpr uint32_t kPlace = kPer - 1;                     // key bits of the place in the lane
+    constexpr uint32_t kMasked = 0x00800000u;                 // keys of -inf lie below, all others above
+    constexpr float u = 0x1p-24f;
+    static_assert((kPer & (kPer - 1)) == 0, "place bits");
     extern __shared__ __attribute__((aligned(16))) double lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int g = lane & (L - 1), base = lane & ~(L - 1);
-    // LDS: each wave's scratch for the groups, then the winners of its tokens
+    const int g = lane & (L - 1);
+    // LDS: with groups each wave's float64 scratch, then k + 1 places (key, id) for each token
     double* const wide = lds + static_cast<size_t>(wave) * a.scratch;
-    int* const won = reinterpret_cast<int*>(lds + static_cast<size_t>(kWavesPerBlock) * a.scratch) +
-                        (static_cast<size_t>(wave) * kTokens + lane / L) * a.k;
+    uint2* const won = reinterpret_cast<uint2*>(lds + static_cast<size_t>(kWavesPerBlock) * a.scratch) +
+                       (static_cast<size_t>(wave) * kTokens + lane / L) * (a.k + 1);
     const int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L;
     const bool live = t < a.T;
     const In* row = logits + (live ? t : a.T - 1) * a.E;
-    bool unsure = a.groups > 1 && a.group_shift < 0;         // this token needs float64
+    const bool picked = a.topk_groups < a.groups;
+    bool unsure = picked && a.group_shift < 0;                // this token needs float64
     if (!__all(unsure)) {
         float l[kPer];
 #pragma unroll
@@ -320,18 +326,17 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                     v[c] = load_logit(row + min(e + c, a.E - 1));
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                l[4 * i + c] = e + c < a.E ? v[c] + 0.0f : -__builtin_inff();   // -0 becomes +0: equal logits tie
+            for (int c = 0; c < 4; ++c)                       // -0 becomes +0: equal logits tie
+                l[4 * i + c] = (kVec ? e : e + c) < a.E ? v[c] + 0.0f : -__builtin_inff();
         }
         const bool by_logit = a.bias == nullptr;
-        float num[kPer];                                      // score = num * inv
-        float inv = 1.0f, check = 0.0f;                       // check: NaN if a logit (or bias) is
-        float m = 0.0f;
+        float inv = 1.0f, m = 0.0f, check = 0.0f;             // score = numerator * inv; check: NaN if a logit or bias is
+        float c[kPer];                                        // numerators, then what the experts are compared by
         if (a.sigmoid) {
+            if (!by_logit || picked) {
 #pragma unroll
-            for (int q = 0; q < kPer; ++q) {
-                num[q] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[q]));
-                check += num[q];
+                for (int q = 0; q < kPer; ++q)
+                    c[q] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-l[q]));
             }
         } else {
             m = l[0];
@@ -343,44 +348,38 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
             m = m == -__builtin_inff() ? 0.0f : m;            // every logit is -inf: scores 0
 #pragma unroll
             for (int q = 0; q < kPer; ++q) {
-                num[q] = fast_exp(l[q] - m);
-                total += num[q];
+                c[q] = fast_exp(l[q] - m);
+                total += c[q];
             }
-            check = total;
             total = reduce<L>(total, Add{});
+            check = total;
             inv = total == 0.0f ? 1.0f : 1.0f / total;
         }
-        const float top_score = a.sigmoid ? 1.0f : inv;
-        float c[kPer];                                        // what the experts are compared by
-        if (by_logit && a.groups == 1) {
-#pragma unroll
-            for (int q = 0; q < kPer; ++q)
-                c[q] = l[q];
-        } else {
+        const float score_err = a.sigmoid ? 8 * u : 52 * u * inv;    // of the difference of two scores
+        if (!by_logit || picked) {
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 const int e = 4 * (L * i + g);
-                float b[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                if (!by_logit) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        b[q] = a.bias[kVec ? min(e, a.E - 4) + q : min(e + q, a.E - 1)];
-                }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float v = num[4 * i + q] * inv + b[q];
-                    check += e + q < a.E ? v : 0.0f;
+                    const float b = by_logit ? 0.0f : a.bias[kVec ? min(e, a.E - 4) + q : min(e + q, a.E - 1)];
+                    const float v = c[4 * i + q] * inv + b;
+                    check += v;
                     c[4 * i + q] = l[4 * i + q] == -__builtin_inff() ? -__builtin_inff() : v;
                 }
             }
+        } else if (a.sigmoid) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                check += l[q] == -__builtin_inff() ? 0.0f : l[q];
         }
         check = reduce<L>(check, Add{});
         unsure = check != check;
         uint32_t dropped = 0;                                 // bit i: the group of vector i is out
-        if (a.groups > 1) {
+        if (picked) {
             // a group is an aligned run of 1 << group_shift lanes of one vector
-            float* const score = reinterpret_cast<float*>(wide) + (lane / L) * a.groups;
             float mine[I], size = 0.0f;
+            uint32_t gkey[I];
 #pragma unroll
             for (int i = 0; i < I; ++i) {
                 const float h1 = fmaxf(c[4 * i], c[4 * i + 1]), l1 = fminf(c[4 * i], c[4 * i + 1]);
@@ -390,63 +389,58 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                     b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
                     b1 = fmaxf(b1, o1);
                 };
-                if (a.group_shift > 0)
+                if (L > 1 && a.group_shift > 0)
                     join(exchange<0>(b1), exchange<0>(b2));
-                if (a.group_shift > 1)
+                if (L > 2 && a.group_shift > 1)
                     join(exchange<1>(b1), exchange<1>(b2));
-                if (a.group_shift > 2)
+                if (L > 4 && a.group_shift > 2)
                     join(exchange<2>(b1), exchange<2>(b2));
-                if (a.group_shift > 3)
+                if (L > 8 && a.group_shift > 3)
                     join(exchange<3>(b1), exchange<3>(b2));
                 const bool two = a.group_top == 2 && b2 > -__builtin_inff();
                 mine[i] = two ? b1 + b2 : b1;
                 size = fmaxf(size, b1 > -__builtin_inff() ? fabsf(b1) + (two ? fabsf(b2) : 0.0f) : 0.0f);
-                const int q = (L * i + g) >> a.group_shift;
-                if (q < a.groups && (g & ((1 << a.group_shift) - 1)) == 0)
-                    score[q] = mine[i];
+                gkey[i] = (L * i + g) >> a.group_shift < a.groups ? ordered(mine[i]) : 0;
             }
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
-            int rank[I] = {};
-            for (int o = 0; o < a.groups; ++o) {
-                const float other = score[o];
+            // the topk_groups-th largest score, as the experts' keys below; equal scores count once
+            uint32_t last = 0;
+            for (int j = 0; j < a.topk_groups; ++j) {
+                uint32_t d = last - 1 - gkey[0];
 #pragma unroll
-                for (int i = 0; i < I; ++i)
-                    rank[i] += other > mine[i] || (other == mine[i] && o < ((L * i + g) >> a.group_shift)) ? 1 : 0;
+                for (int i = 1; i < I; ++i)
+                    d = min(d, last - 1 - gkey[i]);
+                last = last - 1 - reduce<L>(d, MinU{});
             }
-            // the last group kept must lie clearly above the first one dropped
-            float in = __builtin_inff(), out = -__builtin_inff();
+            float out = -__builtin_inff();
+            int kept = 0;
 #pragma unroll
             for (int i = 0; i < I; ++i) {
-                if ((L * i + g) >> a.group_shift >= a.groups)
-                    continue;
-                if (rank[i] >= a.topk_groups) {
-                    dropped |= 1u << i;
-                    out = fmaxf(out, mine[i]);
+                if (gkey[i] >= last) {
+                    ++kept;
                 } else {
-                    in = fminf(in, mine[i]);
+                    dropped |= 1u << i;
+                    out = fmaxf(out, gkey[i] != 0 ? mine[i] : -__builtin_inff());
                 }
             }
-            in = -reduce<L>(-in, Max{});
+            kept = reduce<L>(kept, Add{});
             out = reduce<L>(out, Max{});
             size = reduce<L>(size, Max{});
-            unsure |= a.topk_groups < a.groups && !(in - out > 0x1p-17f * (top_score + size));
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-            __builtin_amdgcn_wave_barrier();
+            // equal scores among those kept, or the first one dropped not clearly below the last kept
+            unsure |= kept != a.topk_groups << a.group_shift ||
+                      !(unordered(last) - out > 2 * score_err + 8 * u * size);
         }
-        constexpr bool kIdKey = std::is_same_v<In, uint16_t>;
-        const bool id_key = kIdKey && by_logit;
+        const bool id_key = std::is_same_v<In, uint16_t> && by_logit;
         uint32_t key[kPer];                                   // 0: no candidate
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
-            const int e = 4 * (L * (q / 4) + g) + q % 4;
             const uint32_t o = ordered(by_logit ? l[q] : c[q]);
-            key[q] = id_key ? (o & 0xffff0000u) | (0xffffu - static_cast<uint32_t>(e)) : (o & ~15u) | static_cast<uint32_t>(q);
-            if (e >= a.E || (dropped >> (q / 4) & 1) != 0)
-                key[q] = 0;
+            key[q] = id_key ? (o & 0xffff0000u) | static_cast<uint32_t>(0xffff - (4 * (L * (q / 4) + g) + q % 4))
+                            : (o & ~kPlace) | static_cast<uint32_t>(q);
+            if (picked)
+                key[q] = (dropped >> (q / 4) & 1) != 0 ? 0 : key[q];
         }
         uint32_t last = 0;                                    // below every key: M - 1 wraps to the top
-        float before = 0.0f;
+        int wins = 0;
         for (int j = 0; j <= a.k; ++j) {
             const uint32_t from = last - 1;
             uint32_t d = from - key[0];
@@ -454,51 +448,48 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
             for (int q = 1; q < kPer; ++q)
                 d = min(d, from - key[q]);
             const uint32_t all = reduce<L>(d, MinU{});
-            const uint32_t now = from - all;                  // 0, or wrapped above `last`: none left
-            const bool none = now == 0 || (j > 0 && now >= last);
-            if (!id_key) {
-                // the one before must lie clearly above, and one lane alone may hold this one
-                const float v = now < 0x00800000u ? -__builtin_inff() : unordered(now & ~15u);
-                const float eps = by_logit || v == -__builtin_inff() ? 0.0f : 0x1p-18f * (top_score + fabsf(v));
-                const uint64_t holders = __ballot(d == all) >> base;
-                const bool sole = __popcll(L == 64 ? holders : holders & ((uint64_t{1} << (L & 63)) - 1)) == 1;
-                unsure |= !none && ((j > 0 && !(before - v > eps)) || (j < a.k && !sole));
-                before = v;
+            last = from - all;                                // nothing left: 0, or wrapped above the one before
+            if (d == all) {
+                const int id = id_key ? 0xffff - static_cast<int>(last & 0xffffu)
+                                      : 4 * (L * static_cast<int>((last & kPlace) >> 2) + g) + static_cast<int>(last & 3);
+                won[j] = uint2{last, static_cast<uint32_t>(id)};
+                wins += j < a.k ? 1 : 0;
             }
-            unsure |= none && j < a.k;
-            if (j < a.k && d == all)
-                won[j] = id_key ? 0xffff - static_cast<int>(now & 0xffffu)
-                                : 4 * (L * static_cast<int>(now >> 2 & 3) + g) + static_cast<int>(now & 3);
-            last = now;
         }
+        unsure |= reduce<L>(wins, Add{}) != a.k;              // two lanes with one key
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
-        if (!__all(unsure)) {
-            // the winners' scores again, one a lane
-            float total = 0.0f, least = __builtin_inff();
-            const auto score = [&](int id) {
-                const float x = load_logit(row + id);
-                return a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - m);
-            };
-            int id = 0;
-            float n = 0.0f;
-            for (int j = g; j < a.k && !unsure; j += L) {
-                id = won[j];
-                n = score(id);
-                total += n;
-                least = fminf(least, n);
+        // winner j on lane j % L: in order if clearly above the next one (which may not exist after the last)
+        float total = 0.0f, least = __builtin_inff(), n = 0.0f;
+        int id = 0, bad = 0;
+        const auto winner = [&](int j) {
+            id = min(static_cast<int>(won[j].y), a.E - 1);
+            const float x = load_logit(row + id);
+            n = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - m);
+        };
+        for (int j = g; j < a.k; j += L) {
+            const uint32_t here = won[j].x, next = won[j + 1].x;
+            const bool none = next == 0 || next >= here;
+            if (here < kMasked || (none && j + 1 < a.k))
+                bad = 1;
+            if (!id_key && !none) {
+                const float v = unordered(here & ~kPlace), w = unordered(next & ~kPlace);
+                const float err = by_logit ? 0.0f : score_err + (2 * kPer + 4) * u * fmaxf(fabsf(v), fabsf(w));
+                if (next >= kMasked && !(v - w > err))
+                    bad = 1;
             }
-            // scores near float32's smallest: their ratios need float64's range
-            unsure |= -reduce<L>(-least, Max{}) < 0x1p-100f;
-            const float factor = (a.renormalize ? 1.0f / reduce<L>(total, Add{}) : inv) * a.scale;
-            for (int j = g; j < a.k && live && !unsure; j += L) {
-                if (a.k > L) {
-                    id = won[j];
-                    n = score(id);
-                }
-                a.ids[t * a.k + j] = id;
-                a.probs[t * a.k + j] = n * factor;
-            }
+            winner(j);
+            total += n;
+            least = fminf(least, n);
+        }
+        // scores near float32's smallest: their ratios need float64's range
+        unsure |= reduce<L>(bad, Add{}) != 0 || -reduce<L>(-least, Max{}) < 0x1p-100f;
+        const float factor = (a.renormalize ? 1.0f / reduce<L>(total, Add{}) : inv) * a.scale;
+        for (int j = g; j < a.k && live && !unsure; j += L) {
+            if (a.k > L)
+                winner(j);
+            a.ids[t * a.k + j] = id;
+            a.probs[t * a.k + j] = n * factor;
         }
     }
     // the tokens left, one after the other
@@ -619,6 +610,16 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __res
     }
 }
 
+// Groups of `per` experts as whole vectors of 1 << b neighbouring lanes (at most a row of 16, and at most
+// a token's L): b, or -1.
+int group_shift(int per, int L)
+{
+    for (int b = 0; b <= 4; ++b)
+        if (per == 4 << b && (1 << b) <= L)
+            return b;
+    return -1;
+}
+
 template <class In, int L, int I>
 hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
 {
@@ -626,16 +627,10 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
     if (blocks >= (int64_t{1} << 31))
         return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
-    // groups that are whole vectors of a power of two of neighbouring lanes (at most a row of 16)
-    const int per = a.E / a.groups;
-    a.group_shift = -1;
-    for (int b = 0; b <= 4; ++b)
-        if (a.groups > 1 && per == 4 << b && (1 << b) <= L)
-            a.group_shift = b;
-    // a token's experts and groups in float64, or the float32 group scores of the wave's tokens
-    a.scratch = a.groups > 1 ? std::max(a.E + a.groups, (64 / L) * a.groups / 2 + 1) : 0;
+    a.group_shift = group_shift(a.E / a.groups, L);
+    a.scratch = a.groups > 1 ? a.E + a.groups : 0;
     const size_t lds = sizeof(double) * kWavesPerBlock * static_cast<size_t>(a.scratch) +
-                       sizeof(int) * (kThreads / L) * static_cast<size_t>(a.k);
+                       sizeof(uint2) * (kThreads / L) * static_cast<size_t>(a.k + 1);
     const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(In)) == 0;
     if (vec)
         gate_kernel<In, L, I, true><<<grid, dim3(kThreads), lds, s>>>(logits, a);
@@ -644,29 +639,32 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
     return hipGetLastError();
 }
 
-// The gate's lanes per token: four experts a lane up to 64 (so that small gates fill the wave with
-// tokens), then vectors of four over 16 lanes, and the whole wave beyond 256 or for few tokens (a lane's
-// work is then a quarter, and no wave waits for another).
+// The gate's lanes per token.  Few tokens: four experts a lane (shortest rounds).  Many: 8 to 32 experts
+// a lane, since what a round costs beside the keys themselves (the exchanges, the winner) is shared by
+// more tokens of the wave.  From two waves a SIMD on the second is faster.
 template <class In>
 hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
 {
-    if (a.E > 64 && a.E <= 256 && a.T <= 4 * device_info().cu_count)
-        return launch_gate_n<In, 64, 1>(logits, a, s);
+    const int few = a.E <= 8 ? 2 : a.E <= 16 ? 4 : a.E <= 32 ? 8 : a.E <= 64 ? 16 : a.E <= 128 ? 32 : 64;
+    const int lanes = a.E <= 16 ? 1 : a.E <= 32 ? 2 : a.E <= 64 ? 4 : a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32;
+    const int per = a.E / a.groups;
+    const bool fits = a.topk_groups == a.groups || group_shift(per, lanes) >= 0 || group_shift(per, few) < 0;
+    const bool many = fits && ceil_div(a.T * few, 64) >= 8 * device_info().cu_count;
     if (a.E <= 8)
-        return launch_gate_n<In, 2, 1>(logits, a, s);
+        return many ? launch_gate_n<In, 1, 2>(logits, a, s) : launch_gate_n<In, 2, 1>(logits, a, s);
     if (a.E <= 16)
-        return launch_gate_n<In, 4, 1>(logits, a, s);
+        return many ? launch_gate_n<In, 1, 4>(logits, a, s) : launch_gate_n<In, 4, 1>(logits, a, s);
     if (a.E <= 32)
-        return launch_gate_n<In, 8, 1>(logits, a, s);
+        return many ? launch_gate_n<In, 2, 4>(logits, a, s) : launch_gate_n<In, 8, 1>(logits, a, s);
     if (a.E <= 64)
-        return launch_gate_n<In, 16, 1>(logits, a, s);
+        return many ? launch_gate_n<In, 4, 4>(logits, a, s) : launch_gate_n<In, 16, 1>(logits, a, s);
     if (a.E <= 128)
-        return launch_gate_n<In, 16, 2>(logits, a, s);
+        return many ? launch_gate_n<In, 8, 4>(logits, a, s) : launch_gate_n<In, 32, 1>(logits, a, s);
     if (a.E <= 256)
-        return launch_gate_n<In, 16, 4>(logits, a, s);
+        return many ? launch_gate_n<In, 8, 8>(logits, a, s) : launch_gate_n<In, 64, 1>(logits, a, s);
     if (a.E <= 512)
-        return launch_gate_n<In, 64, 2>(logits, a, s);
-    return launch_gate_n<In, 64, 4>(logits, a, s);
+        return many ? launch_gate_n<In, 16, 8>(logits, a, s) : launch_gate_n<In, 64, 2>(logits, a, s);
+    return many ? launch_gate_n<In, 32, 8>(logits, a, s) : launch_gate_n<In, 64, 4>(logits, a, s);
 }
 
 template <class In, int L, int kPer>

@@ -75,6 +75,33 @@ def test_gate(T, E, k, groups, topk_groups, score):
                        renormalize=renorm, scale=2.5)
 
 
+@pytest.mark.parametrize("E,k,groups,topk_groups,T", [(8, 2, 1, 1, 70001), (6, 3, 1, 1, 66000), (16, 4, 4, 2, 40000),
+                                                     (30, 5, 1, 1, 20000), (64, 8, 8, 3, 9000), (128, 8, 4, 2, 5000),
+                                                     (256, 8, 8, 4, 3001), (256, 8, 4, 2, 3000), (256, 6, 1, 1, 2500),
+                                                     (500, 10, 1, 1, 2100), (1024, 8, 32, 4, 2100), (64, 64, 1, 1, 9000)])
+def test_gate_of_many_tokens(E, k, groups, topk_groups, T):
+    """Enough tokens for the layouts that share a wave among more of them; against the same gate on
+    slices of few tokens, whose layout is another: ids equal, weights within both layouts' bound."""
+    for dtype in ("f32", "bf16"):
+        for score in ("softmax", "sigmoid"):
+            for with_bias in (False, True):
+                print(f"[gate] {T}x{E} k={k} g={groups}/{topk_groups} {score} {dtype} bias={with_bias}", flush=True)
+                t, l = _logits(T, E, dtype, seed=T, grid=dtype == "f32" and score == "sigmoid")
+                x = t.cuda()
+                kw = dict(score=score, groups=groups, topk_groups=topk_groups, scale=1.5, renormalize=with_bias)
+                if with_bias:
+                    kw["bias"] = 0.1 * torch.randn(E, generator=torch.Generator().manual_seed(E)).cuda()
+                ids, probs = mel.router_gate(x, k, **kw)
+                few = [mel.router_gate(x[i:i + 300], k, **kw) for i in range(0, T, 300)]
+                assert torch.equal(ids, torch.cat([f[0] for f in few]))
+                torch.testing.assert_close(probs, torch.cat([f[1] for f in few]), rtol=2 * (5 * _spread(l) + 32) * U, atol=0)
+                at = np.random.default_rng(0).choice(T, 40, replace=False)
+                kw["bias"] = kw["bias"].cpu().numpy() if with_bias else None
+                rids, rw, _ = ref.gate(l[at], k, **kw)
+                assert np.array_equal(ids.cpu().numpy()[at], rids)
+                assert np.all(np.abs(probs.cpu().numpy()[at] - rw) <= (5 * _spread(l) + 32) * U * rw)
+
+
 @pytest.mark.parametrize("E,k,groups,topk_groups", [(8, 3, 1, 1), (48, 6, 6, 2), (256, 8, 8, 4)])
 def test_equal_logits_and_equal_biases(E, k, groups, topk_groups):
     """Ties go to the lower id, between groups to the lower group."""
