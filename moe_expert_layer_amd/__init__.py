@@ -128,11 +128,30 @@ def _check(status: int):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
+
+
+# The current stream's handle by device index; the plain query builds a Stream object, which costs more
+# than the rest of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream(t: torch.Tensor):
-    return ctypes.c_void_p(torch.cuda.current_stream(t.device).cuda_stream)
+    if _raw_stream is not None:
+        return _raw_stream(t.device.index)
+    return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _call(name: str, device, *args):
+    """Calls the library with `device` current, and raises on its error."""
+    fn = getattr(_lib or library(), name)
+    if torch.cuda.current_device() == device.index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status:
+        _check(status)
 
 
 def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
@@ -342,11 +361,10 @@ def expert_forward_int8(x, x_scale, w_gate, wg_scale, w_up, wu_scale, w_down, wd
     if out is None:
         out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
     _need(out, "out", torch.bfloat16, (T, H), dev)
-    with torch.cuda.device(dev):
-        _check(library().moe_expert_forward_int8(
-            ctypes.byref(prob), _ptr(x), _ptr(x_scale), _ptr(w_gate), _ptr(wg_scale), _ptr(w_up),
-            _ptr(wu_scale), _ptr(w_down), _ptr(wd_scale), _ptr(expert_ids), _ptr(probs), _ptr(out),
-            _ptr(ws), ws.numel(), _stream(x)))
+    _call("moe_expert_forward_int8", dev,
+          ctypes.byref(prob), _ptr(x), _ptr(x_scale), _ptr(w_gate), _ptr(wg_scale), _ptr(w_up),
+          _ptr(wu_scale), _ptr(w_down), _ptr(wd_scale), _ptr(expert_ids), _ptr(probs), _ptr(out), _ptr(ws),
+          ws.numel(), _stream(x))
     return out
 
 
@@ -510,11 +528,10 @@ def grouped_ffn_int8(rows, rows_scale, group_offsets, group_expert, w_gate, wg_s
     if out is None:
         out = torch.empty((M, H), dtype=torch.bfloat16, device=dev)
     _need(out, "out", torch.bfloat16, (M, H), dev)
-    with torch.cuda.device(dev):
-        _check(library().moe_grouped_ffn_int8(
-            ctypes.byref(prob), _ptr(rows), _ptr(rows_scale), M, _ptr(group_offsets), _ptr(group_expert), G,
-            _ptr(w_gate), _ptr(wg_scale), _ptr(w_up), _ptr(wu_scale), _ptr(w_down), _ptr(wd_scale),
-            _ptr(out), _ptr(ws), ws.numel(), _stream(rows)))
+    _call("moe_grouped_ffn_int8", dev,
+          ctypes.byref(prob), _ptr(rows), _ptr(rows_scale), M, _ptr(group_offsets), _ptr(group_expert), G,
+          _ptr(w_gate), _ptr(wg_scale), _ptr(w_up), _ptr(wu_scale), _ptr(w_down), _ptr(wd_scale), _ptr(out),
+          _ptr(ws), ws.numel(), _stream(rows))
     return out
 
 
@@ -539,10 +556,9 @@ def grouped_matmul_int8(rows, rows_scale, group_offsets, group_expert, w, w_scal
     n = ctypes.c_size_t()
     _check(library().moe_grouped_matmul_int8_workspace_size(M, G, K, N, ctypes.byref(n)))
     ws = _workspace(n.value, dev, workspace)
-    with torch.cuda.device(dev):
-        _check(library().moe_grouped_matmul_int8(
-            _ptr(rows), _ptr(rows_scale), M, _ptr(group_offsets), _ptr(group_expert), G, _ptr(w),
-            _ptr(w_scale), E, K, N, _ptr(out), _dtype_code(out), _ptr(ws), ws.numel(), _stream(rows)))
+    _call("moe_grouped_matmul_int8", dev,
+          _ptr(rows), _ptr(rows_scale), M, _ptr(group_offsets), _ptr(group_expert), G, _ptr(w), _ptr(w_scale),
+          E, K, N, _ptr(out), _dtype_code(out), _ptr(ws), ws.numel(), _stream(rows))
     return out
 
 
@@ -554,8 +570,7 @@ def int8_quantize(x):
     rows, cols = x.shape
     codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
     scales = torch.empty(rows, dtype=torch.float32, device=x.device)
-    with torch.cuda.device(x.device):
-        _check(library().moe_int8_quantize(_ptr(x), dt, rows, cols, _ptr(codes), _ptr(scales), _stream(x)))
+    _call("moe_int8_quantize", x.device, _ptr(x), dt, rows, cols, _ptr(codes), _ptr(scales), _stream(x))
     return codes, scales
 
 
@@ -582,11 +597,11 @@ def router_gate(logits, k: int, score: str = "softmax", bias=None, groups: int =
     if bias is not None:
         _need(bias, "bias", torch.float32, (E,), logits.device)
     gate = _gate(score, renormalize, groups, topk_groups, group_top, scale)
-    ids = torch.empty((T, max(int(k), 0)), dtype=torch.int32, device=logits.device)
-    probs = torch.empty((T, max(int(k), 0)), dtype=torch.float32, device=logits.device)
-    with torch.cuda.device(logits.device):
-        _check(library().moe_router_gate(ctypes.byref(gate), _ptr(logits), dt, _ptr(bias), T, E, k,
-                                         _ptr(ids), _ptr(probs), _stream(logits)))
+    k = int(k)
+    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+    probs = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    _call("moe_router_gate", logits.device,
+          ctypes.byref(gate), _ptr(logits), dt, _ptr(bias), T, E, k, _ptr(ids), _ptr(probs), _stream(logits))
     return ids, probs
 
 
@@ -602,10 +617,9 @@ def router_gate_backward(logits, expert_ids, dprobs, score: str = "softmax", ren
     _need(dprobs, "dprobs", torch.float32, (T, k), logits.device)
     gate = _gate(score, renormalize, 1, 1, 2, scale)
     dlogits = torch.empty_like(logits)
-    with torch.cuda.device(logits.device):
-        _check(library().moe_router_gate_backward(ctypes.byref(gate), _ptr(logits), dt, T, E, k,
-                                                  _ptr(expert_ids), _ptr(dprobs), _ptr(dlogits),
-                                                  _stream(logits)))
+    _call("moe_router_gate_backward", logits.device,
+          ctypes.byref(gate), _ptr(logits), dt, T, E, k, _ptr(expert_ids), _ptr(dprobs), _ptr(dlogits),
+          _stream(logits))
     return dlogits
 
 

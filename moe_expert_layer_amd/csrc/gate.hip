@@ -280,7 +280,7 @@ __device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int
 // complement of the expert's id makes the keys unique and exact).  The next key below M is
 // M - 1 - min over the keys v of (M - 1 - v), unsigned: keys at or above M wrap to large values, so
 // nothing is taken out of the registers from round to round.  The lane that holds a round's key leaves
-// key and id in LDS, where the token's lanes check them and make the weights, one winner a lane.
+// it with its number in LDS, where the token's lanes check them and make the weights, one winner a lane.
 //
 // Errors, with u = 2^-24 and x = max - l.  softmax: exp(-x) is off by (2.5 x + 2) u relative (the
 // subtraction, the product with log2 e and that constant, a 1-ulp exp2), at most 3 u of the largest
@@ -303,7 +303,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
     extern __shared__ __attribute__((aligned(16))) double lds[];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int g = lane & (L - 1);
-    // LDS: with groups each wave's float64 scratch, then k + 1 places (key, id) for each token
+    // LDS: with groups each wave's float64 scratch, then k + 1 places (key, lane) for each token
     double* const wide = lds + static_cast<size_t>(wave) * a.scratch;
     uint2* const won = reinterpret_cast<uint2*>(lds + static_cast<size_t>(kWavesPerBlock) * a.scratch) +
                        (static_cast<size_t>(wave) * kTokens + lane / L) * (a.k + 1);
@@ -326,11 +326,29 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                     v[c] = load_logit(row + min(e + c, a.E - 1));
             }
 #pragma unroll
-            for (int c = 0; c < 4; ++c)                       // -0 becomes +0: equal logits tie
-                l[4 * i + c] = (kVec ? e : e + c) < a.E ? v[c] + 0.0f : -__builtin_inff();
+            for (int c = 0; c < 4; ++c)
+                l[4 * i + c] = v[c];
+        }
+        // As unsigned integers -inf and the negative NaNs are the largest floats, as signed ones the
+        // positive NaNs.  Most tokens hold neither, and most gates fill their lanes.
+        uint32_t largest = __float_as_uint(l[0]);
+        int positive = __float_as_int(l[0]);
+#pragma unroll
+        for (int q = 1; q < kPer; ++q) {
+            largest = max(largest, __float_as_uint(l[q]));
+            positive = max(positive, __float_as_int(l[q]));
+        }
+        const bool full = a.E == 4 * L * I;
+        const bool masks = !full || __any(largest >= 0xff800000u);
+        const bool nan = largest > 0xff800000u || positive > 0x7f800000;
+        if (!full) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                if (4 * (L * (q / 4) + g) + (kVec ? 0 : q % 4) >= a.E)
+                    l[q] = -__builtin_inff();
         }
         const bool by_logit = a.bias == nullptr;
-        float inv = 1.0f, m = 0.0f, check = 0.0f;             // score = numerator * inv; check: NaN if a logit or bias is
+        float inv = 1.0f, m = 0.0f;                           // score = numerator * inv
         float c[kPer];                                        // numerators, then what the experts are compared by
         if (a.sigmoid) {
             if (!by_logit || picked) {
@@ -352,7 +370,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 total += c[q];
             }
             total = reduce<L>(total, Add{});
-            check = total;
+            unsure |= !(total <= 2048.0f);                    // a +inf logit
             inv = total == 0.0f ? 1.0f : 1.0f / total;
         }
         const float score_err = a.sigmoid ? 8 * u : 52 * u * inv;    // of the difference of two scores
@@ -363,18 +381,16 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const float b = by_logit ? 0.0f : a.bias[kVec ? min(e, a.E - 4) + q : min(e + q, a.E - 1)];
-                    const float v = c[4 * i + q] * inv + b;
-                    check += v;
-                    c[4 * i + q] = l[4 * i + q] == -__builtin_inff() ? -__builtin_inff() : v;
+                    c[4 * i + q] = c[4 * i + q] * inv + b;
                 }
             }
-        } else if (a.sigmoid) {
+            if (masks) {
 #pragma unroll
-            for (int q = 0; q < kPer; ++q)
-                check += l[q] == -__builtin_inff() ? 0.0f : l[q];
+                for (int q = 0; q < kPer; ++q)
+                    c[q] = l[q] == -__builtin_inff() ? -__builtin_inff() : c[q];
+            }
         }
-        check = reduce<L>(check, Add{});
-        unsure = check != check;
+        unsure |= reduce<L>(nan ? 1 : 0, Add{}) != 0;
         uint32_t dropped = 0;                                 // bit i: the group of vector i is out
         if (picked) {
             // a group is an aligned run of 1 << group_shift lanes of one vector
@@ -433,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
         uint32_t key[kPer];                                   // 0: no candidate
 #pragma unroll
         for (int q = 0; q < kPer; ++q) {
-            const uint32_t o = ordered(by_logit ? l[q] : c[q]);
+            const uint32_t o = ordered(by_logit ? l[q] + 0.0f : c[q]);   // -0 becomes +0: equal logits tie
             key[q] = id_key ? (o & 0xffff0000u) | static_cast<uint32_t>(0xffff - (4 * (L * (q / 4) + g) + q % 4))
                             : (o & ~kPlace) | static_cast<uint32_t>(q);
             if (picked)
@@ -450,20 +466,22 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
             const uint32_t all = reduce<L>(d, MinU{});
             last = from - all;                                // nothing left: 0, or wrapped above the one before
             if (d == all) {
-                const int id = id_key ? 0xffff - static_cast<int>(last & 0xffffu)
-                                      : 4 * (L * static_cast<int>((last & kPlace) >> 2) + g) + static_cast<int>(last & 3);
-                won[j] = uint2{last, static_cast<uint32_t>(id)};
-                wins += j < a.k ? 1 : 0;
+                won[j] = uint2{last, static_cast<uint32_t>(g)};
+                ++wins;
             }
+            if (j == a.k - 1)
+                unsure |= reduce<L>(wins, Add{}) != a.k;      // two lanes with one key
         }
-        unsure |= reduce<L>(wins, Add{}) != a.k;              // two lanes with one key
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         // winner j on lane j % L: in order if clearly above the next one (which may not exist after the last)
         float total = 0.0f, least = __builtin_inff(), n = 0.0f;
         int id = 0, bad = 0;
         const auto winner = [&](int j) {
-            id = min(static_cast<int>(won[j].y), a.E - 1);
+            const uint2 w = won[j];
+            id = id_key ? 0xffff - static_cast<int>(w.x & 0xffffu)
+                        : 4 * (L * static_cast<int>((w.x & kPlace) >> 2) + static_cast<int>(w.y)) + static_cast<int>(w.x & 3);
+            id = min(id, a.E - 1);
             const float x = load_logit(row + id);
             n = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + fast_exp(-x)) : fast_exp(x - m);
         };
@@ -639,14 +657,15 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
     return hipGetLastError();
 }
 
-// The gate's lanes per token.  Few tokens: four experts a lane (shortest rounds).  Many: 8 to 32 experts
-// a lane, since what a round costs beside the keys themselves (the exchanges, the winner) is shared by
-// more tokens of the wave.  From two waves a SIMD on the second is faster.
+// The gate's lanes per token.  Few tokens: four experts a lane (shortest rounds).  Many: up to 16 experts
+// a lane, since what a round costs beside the keys themselves (the exchanges, the winner) is then
+// shared by more tokens of the wave (65536 tokens of 256 experts, 8 groups: 16 lanes 47 us, 8 lanes of 32
+// experts the same, at 142 registers).  Taken from two waves a SIMD on.
 template <class In>
 hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
 {
     const int few = a.E <= 8 ? 2 : a.E <= 16 ? 4 : a.E <= 32 ? 8 : a.E <= 64 ? 16 : a.E <= 128 ? 32 : 64;
-    const int lanes = a.E <= 16 ? 1 : a.E <= 32 ? 2 : a.E <= 64 ? 4 : a.E <= 256 ? 8 : a.E <= 512 ? 16 : 32;
+    const int lanes = a.E <= 16 ? 1 : a.E <= 32 ? 2 : a.E <= 64 ? 4 : a.E <= 128 ? 8 : a.E <= 256 ? 16 : 32;
     const int per = a.E / a.groups;
     const bool fits = a.topk_groups == a.groups || group_shift(per, lanes) >= 0 || group_shift(per, few) < 0;
     const bool many = fits && ceil_div(a.T * few, 64) >= 8 * device_info().cu_count;
@@ -661,10 +680,10 @@ hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
     if (a.E <= 128)
         return many ? launch_gate_n<In, 8, 4>(logits, a, s) : launch_gate_n<In, 32, 1>(logits, a, s);
     if (a.E <= 256)
-        return many ? launch_gate_n<In, 8, 8>(logits, a, s) : launch_gate_n<In, 64, 1>(logits, a, s);
+        return many ? launch_gate_n<In, 16, 4>(logits, a, s) : launch_gate_n<In, 64, 1>(logits, a, s);
     if (a.E <= 512)
-        return many ? launch_gate_n<In, 16, 8>(logits, a, s) : launch_gate_n<In, 64, 2>(logits, a, s);
-    return many ? launch_gate_n<In, 32, 8>(logits, a, s) : launch_gate_n<In, 64, 4>(logits, a, s);
+        return many ? launch_gate_n<In, 32, 4>(logits, a, s) : launch_gate_n<In, 64, 2>(logits, a, s);
+    return launch_gate_n<In, 64, 4>(logits, a, s);
 }
 
 template <class In, int L, int kPer>
