@@ -520,20 +520,6 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
     }
 }
 
-template <class V>
-__device__ __forceinline__ V group_sum(V v, int L)
-{
-    for (int off = L / 2; off >= 1; off >>= 1)
-        v += __shfl_xor(v, off);
-    return v;
-}
-__device__ __forceinline__ float group_max(float v, int L)
-{
-    for (int off = L / 2; off >= 1; off >>= 1)
-        v = fmaxf(v, __shfl_xor(v, off));
-    return v;
-}
-
 struct GateBackwardArgs {
     int64_t T;
     int E, k, sigmoid, renormalize;
@@ -542,20 +528,34 @@ struct GateBackwardArgs {
     const float* dprobs;
 };
 
+__device__ __forceinline__ void store_logits4(float* p, const f32x4_t& v) { *reinterpret_cast<f32x4_t*>(p) = v; }
+__device__ __forceinline__ void store_logits4(uint16_t* p, const f32x4_t& v)
+{
+    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+
 // dl of one token.  With w_j the unscaled weights and d_j = scale dprobs_j:
 //   renormalised: q_j = w_j (d_j - sum_i d_i w_i), sigmoid times 1 - s_j; dl_e = the q_j with id e
 //   otherwise: sigmoid dl_e = d_j s_j (1 - s_j); softmax dl_e = s_e (d_j [id_j = e] - sum_i d_i s_i)
 // An id that occurs twice gets both; ids outside [0, E) are no slots.
-template <class In, int L, int kPer>
+//
+// L lanes per token (at least k: lane j holds slot j).  The token's row of dl is put together in LDS -
+// zeros (dense softmax: its exponentials), then the slots' values at their ids - and goes out in vectors
+// of four; writing it is what the kernel costs.  An id held by two lanes is found by writing the lanes'
+// numbers into the row and reading them back, and only then the lanes look at each other.
+template <class In, int L, bool kVec>
 __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __restrict__ logits,
                                                                  In* __restrict__ dlogits,
                                                                  const GateBackwardArgs a)
 {
+    extern __shared__ __attribute__((aligned(16))) float rows[];
     const int lane = threadIdx.x & 63;
     const int g = lane & (L - 1), base = lane & ~(L - 1);
     const int64_t t = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) / L;
     const bool live = t < a.T;
-    const In* row = logits + (live ? t : 0) * a.E;
+    const int64_t at = (live ? t : a.T - 1) * a.E;
+    const In* row = logits + at;
+    float* const dl = rows + static_cast<size_t>(threadIdx.x / L) * ((a.E + 3) & ~3);
     int id = -1;
     float d = 0.0f, lj = -__builtin_inff();
     if (live && g < a.k) {
@@ -567,64 +567,110 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __res
             lj = load_logit(row + id);
         }
     }
-    float dense[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i)
-        dense[i] = 0.0f;
-    float q;                                                  // this slot's part of its expert's gradient
+    const bool dense = !a.sigmoid && !a.renormalize;
+    float q, spread = 0.0f;                                   // this slot's value; dense: the factor of the exponentials
     if (a.sigmoid) {
         const float s = id >= 0 ? 1.0f / (1.0f + expf(-lj)) : 0.0f;
         const float rest = 1.0f / (1.0f + expf(lj));          // 1 - s
         if (a.renormalize) {
-            const float total = group_sum(s, L);
+            const float total = reduce<L>(s, Add{});
             const float w = total > 0.0f || total != total ? s / total : 0.0f;
-            q = w * rest * (d - group_sum(d * w, L));
+            q = w * rest * (d - reduce<L>(d * w, Add{}));
         } else {
             q = d * s * rest;
         }
     } else if (a.renormalize) {
-        const float m = group_max(lj, L);
+        const float m = reduce<L>(lj, Max{});
         const float ex = lj == -__builtin_inff() ? 0.0f : expf(lj - m);
-        const float total = group_sum(ex, L);
+        const float total = reduce<L>(ex, Add{});
         const float w = total > 0.0f || total != total ? ex / total : 0.0f;
-        q = w * (d - group_sum(d * w, L));
+        q = w * (d - reduce<L>(d * w, Add{}));
     } else {
-        float m = -__builtin_inff();
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            dense[i] = g + L * i < a.E ? load_logit(row + g + L * i) : -__builtin_inff();
-            m = fmaxf(m, dense[i]);
+        float m = -__builtin_inff(), total = 0.0f;
+        if (kVec) {
+            for (int e = 4 * g; e < a.E; e += 4 * L) {
+                float v[4];
+                load_logits4(row + e, v);
+                m = fmaxf(fmaxf(m, fmaxf(v[0], v[1])), fmaxf(v[2], v[3]));
+                *reinterpret_cast<f32x4_t*>(dl + e) = f32x4_t{v[0], v[1], v[2], v[3]};
+            }
+        } else {
+            for (int e = g; e < a.E; e += L) {
+                dl[e] = load_logit(row + e);
+                m = fmaxf(m, dl[e]);
+            }
         }
-        m = group_max(m, L);
-        float total = 0.0f;
+        m = reduce<L>(m, Max{});
+        const auto weight = [&](float v) { return v == -__builtin_inff() ? 0.0f : expf(v - m); };
+        if (kVec) {
+            for (int e = 4 * g; e < a.E; e += 4 * L) {
+                f32x4_t v = *reinterpret_cast<f32x4_t*>(dl + e);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            dense[i] = dense[i] == -__builtin_inff() ? 0.0f : expf(dense[i] - m);
-            total += dense[i];
+                for (int c = 0; c < 4; ++c) {
+                    v[c] = weight(v[c]);
+                    total += v[c];
+                }
+                *reinterpret_cast<f32x4_t*>(dl + e) = v;
+            }
+        } else {
+            for (int e = g; e < a.E; e += L) {
+                dl[e] = weight(dl[e]);
+                total += dl[e];
+            }
         }
-        total = group_sum(total, L);
+        total = reduce<L>(total, Add{});
         const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
-        const float s = lj == -__builtin_inff() ? 0.0f : expf(lj - m) * inv;
-        q = d * s;
-        const float dot = group_sum(q, L);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            dense[i] = -dense[i] * inv * dot;
+        q = d * weight(lj) * inv;
+        spread = -inv * reduce<L>(q, Add{});
     }
-    for (int j = 0; j < a.k; ++j) {
-        const int oi = __shfl(id, base + j);
-        const float oq = __shfl(q, base + j);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (oi == g + L * i)
-                dense[i] += oq;
+    // ids that several slots name: each such lane takes the sum of theirs, in slot order
+    int* const mark = reinterpret_cast<int*>(dl);
+    float under = 0.0f;                                       // dense: the exponential at this slot's id
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (dense && id >= 0)
+        under = dl[id];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (id >= 0)
+        mark[id] = g;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const bool shared = id >= 0 && mark[id] != g;
+    if (__any(shared)) {
+        float sum = 0.0f;
+        for (int j = 0; j < a.k; ++j) {
+            const int oi = __shfl(id, base + j);
+            const float oq = __shfl(q, base + j);
+            sum += oi == id ? oq : 0.0f;
+        }
+        q = sum;
     }
+    if (!dense) {
+        for (int e = 4 * g; e < a.E; e += 4 * L)              // the row has room for whole vectors
+            *reinterpret_cast<f32x4_t*>(dl + e) = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (dense) {
+        for (int e = g; e < a.E; e += L)                      // the marked places are written next
+            dl[e] *= spread;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    if (id >= 0)
+        dl[id] = dense ? under * spread + q : q;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
     if (live) {
-        In* out = dlogits + t * a.E;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (g + L * i < a.E)
-                store_logit(out + g + L * i, dense[i]);
+        In* out = dlogits + at;
+        if (kVec) {
+            for (int e = 4 * g; e < a.E; e += 4 * L)
+                store_logits4(out + e, *reinterpret_cast<f32x4_t*>(dl + e));
+        } else {
+            for (int e = g; e < a.E; e += L)
+                store_logit(out + e, dl[e]);
+        }
     }
 }
 
@@ -686,36 +732,38 @@ hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
     return launch_gate_n<In, 64, 4>(logits, a, s);
 }
 
-template <class In, int L, int kPer>
+template <class In, int L>
 hipError_t launch_backward_n(const In* logits, In* dlogits, const GateBackwardArgs& a, hipStream_t s)
 {
     const int64_t blocks = ceil_div(a.T * L, kThreads);
     if (blocks >= (int64_t{1} << 31))
         return hipErrorInvalidValue;
-    gate_backward_kernel<In, L, kPer><<<dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s>>>(logits, dlogits, a);
+    const dim3 grid(static_cast<unsigned>(blocks));
+    const size_t lds = sizeof(float) * (kThreads / L) * static_cast<size_t>((a.E + 3) & ~3);
+    const bool vec = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) % (4 * sizeof(In)) == 0;
+    if (vec)
+        gate_backward_kernel<In, L, true><<<grid, dim3(kThreads), lds, s>>>(logits, dlogits, a);
+    else
+        gate_backward_kernel<In, L, false><<<grid, dim3(kThreads), lds, s>>>(logits, dlogits, a);
     return hipGetLastError();
 }
 
-// Calls f with (lanes per token, experts per lane) for E experts.
-template <class F>
-hipError_t with_lanes(int E, F f)
+// Lanes per token: one per slot, and one per 16 experts.
+template <class In>
+hipError_t launch_backward_t(const In* logits, In* dlogits, const GateBackwardArgs& a, hipStream_t s)
 {
-    using std::integral_constant;
-    if (E <= 8)
-        return f(integral_constant<int, 8>{}, integral_constant<int, 1>{});
-    if (E <= 16)
-        return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-    if (E <= 32)
-        return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-    if (E <= 64)
-        return f(integral_constant<int, 64>{}, integral_constant<int, 1>{});
-    if (E <= 128)
-        return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-    if (E <= 256)
-        return f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
-    if (E <= 512)
-        return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
-    return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+    const int need = std::max(a.k, (a.E + 15) / 16);
+    if (need <= 2)
+        return launch_backward_n<In, 2>(logits, dlogits, a, s);
+    if (need <= 4)
+        return launch_backward_n<In, 4>(logits, dlogits, a, s);
+    if (need <= 8)
+        return launch_backward_n<In, 8>(logits, dlogits, a, s);
+    if (need <= 16)
+        return launch_backward_n<In, 16>(logits, dlogits, a, s);
+    if (need <= 32)
+        return launch_backward_n<In, 32>(logits, dlogits, a, s);
+    return launch_backward_n<In, 64>(logits, dlogits, a, s);
 }
 
 }  // namespace
@@ -756,12 +804,8 @@ hipError_t launch_gate_backward(const moe_gate& o, const void* logits, int dtype
     a.scale = o.scale;
     a.ids = ids;
     a.dprobs = dprobs;
-    return with_lanes(a.E, [&](auto L, auto per) {
-        return dtype == MOE_F32
-                   ? launch_backward_n<float, L(), per()>(static_cast<const float*>(logits), static_cast<float*>(dlogits), a, s)
-                   : launch_backward_n<uint16_t, L(), per()>(static_cast<const uint16_t*>(logits),
-                                                             static_cast<uint16_t*>(dlogits), a, s);
-    });
+    return dtype == MOE_F32 ? launch_backward_t(static_cast<const float*>(logits), static_cast<float*>(dlogits), a, s)
+                            : launch_backward_t(static_cast<const uint16_t*>(logits), static_cast<uint16_t*>(dlogits), a, s);
 }
 
 }  // namespace moe
