@@ -480,7 +480,7 @@ moe_status run_ffn(int dtype, const void* rows, const uint8_t* rows_scale, int64
 struct Int8Layout {
     RouteLayout route;
     Int8Plan fc1{}, fc2{};
-    size_t counts = 0, offsets = 0, perm = 0, pos = 0, tile_count = 0, tiles = 0, tiles_run = 0;
+    size_t counts = 0, offsets = 0, perm = 0, pos = 0, tile_count = 0, task_ctr = 0, tiles = 0, tiles_run = 0;
     size_t h = 0, h_q = 0, h_scale = 0, y_part = 0, x_q = 0, x_q_scale = 0, y = 0, total = 0;
     int64_t max_tiles = 0;
 };
@@ -498,8 +498,8 @@ struct Take {
 Int8Layout int8_layout(int64_t M, int64_t G, int64_t H, int64_t F, int64_t T, int64_t k, int64_t E, bool layer)
 {
     Int8Layout L;
-    L.fc1 = int8_plan(M, G, H, F, true);
-    L.fc2 = int8_plan(M, G, F, H, false);
+    L.fc1 = int8_plan(M, G, H, F, true, std::min(H, F));
+    L.fc2 = int8_plan(M, G, F, H, false, std::min(H, F));
     Take take{kAlign};                                        // the status word
     if (layer) {
         L.route = route_layout(T, k, E, 0);
@@ -514,6 +514,7 @@ Int8Layout int8_layout(int64_t M, int64_t G, int64_t H, int64_t F, int64_t T, in
     }
     L.max_tiles = max_mtiles(M, G, 0, L.fc1.row_tile);
     L.tile_count = take(8 * 4);
+    L.task_ctr = take(2 * kXcdCount * 4);
     L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
     L.tiles_run = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
     L.h = take(4 * M * F * (L.fc1.partial ? 2 * L.fc1.splits : 1));
@@ -541,13 +542,13 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
     const int32_t* count = tcount + 4;
     LAUNCH(s, "build_tiles",
            launch_build_tiles(offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.fc1.row_tile,
-                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0, nullptr,
-                              at<int32_t>(ws, 0), write_status, s, tiles, tcount + 4));
+                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0,
+                              at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), write_status, s, tiles, tcount + 4));
     int8_t* h_q = at<int8_t>(ws, L.h_q);
     float* h_scale = at<float>(ws, L.h_scale);
     LAUNCH(s, "fc1_i8",
            launch_gemm_i8(L.fc1, rows, rows_scale, w.gate, w.gate_scale, w.up, w.up_scale, at<void>(ws, L.h),
-                          MOE_F32, M, H, F, tiles, count, gather, gather_k, s));
+                          MOE_F32, M, H, F, tiles, count, gather, gather_k, at<int32_t>(ws, L.task_ctr), s));
     if (L.fc1.partial)
         LAUNCH(s, "int8_swiglu",
                launch_int8_swiglu_partial(at<int32_t>(ws, L.h), L.fc1.splits, rows_scale, gather, gather_k,
@@ -558,7 +559,7 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
     LAUNCH(s, "fc2_i8",
            launch_gemm_i8(L.fc2, h_q, h_scale, w.down, w.down_scale, nullptr, nullptr,
                           L.fc2.partial ? at<void>(ws, L.y_part) : y, MOE_BF16, M, F, H, tiles, count, nullptr, 1,
-                          s));
+                          at<int32_t>(ws, L.task_ctr) + kXcdCount, s));
     if (L.fc2.partial)
         LAUNCH(s, "int8_finish",
                launch_int8_finish(at<int32_t>(ws, L.y_part), L.fc2.splits, h_scale, w.down_scale, offsets,
@@ -1128,17 +1129,18 @@ namespace {
 
 struct MatmulLayout {
     Int8Plan plan{};
-    size_t tile_count = 0, tiles = 0, tiles_run = 0, part = 0, total = 0;
+    size_t tile_count = 0, task_ctr = 0, tiles = 0, tiles_run = 0, part = 0, total = 0;
     int64_t max_tiles = 0;
 };
 
 MatmulLayout matmul_layout(int64_t M, int64_t G, int64_t K, int64_t N)
 {
     MatmulLayout L;
-    L.plan = int8_plan(M, G, K, N, false);
+    L.plan = int8_plan(M, G, K, N, false, K);
     L.max_tiles = max_mtiles(M, G, 0, L.plan.row_tile);
     Take take{kAlign};
     L.tile_count = take(8 * 4);
+    L.task_ctr = take(2 * kXcdCount * 4);
     L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
     L.tiles_run = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
     if (L.plan.partial)
@@ -1185,14 +1187,14 @@ MOE_API moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows
     MTile* tiles = at<MTile>(ws, L.tiles_run);
     LAUNCH(s, "build_tiles",
            launch_build_tiles(group_offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.plan.row_tile,
-                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0, nullptr,
-                              at<int32_t>(ws, 0), true, s, tiles, tcount + 4));
+                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0,
+                              at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), true, s, tiles, tcount + 4));
     if (M == 0)
         return MOE_OK;
     LAUNCH(s, "matmul_i8",
            launch_gemm_i8(L.plan, rows, rows_scale, w, w_scale, nullptr, nullptr,
                           L.plan.partial ? at<void>(ws, L.part) : out, out_dtype, M, K, N, tiles, tcount + 4, nullptr,
-                          1, s));
+                          1, at<int32_t>(ws, L.task_ctr), s));
     if (L.plan.partial)
         LAUNCH(s, "int8_finish",
                launch_int8_finish(at<int32_t>(ws, L.part), L.plan.splits, rows_scale, w_scale, group_offsets,

@@ -17,6 +17,7 @@
 // consecutive k of its column.
 #include <algorithm>
 #include <atomic>
+#include <utility>
 
 #include "gemm_common.h"
 #include "moe_expert_layer.h"
@@ -47,6 +48,7 @@ struct Args {
     const int32_t* tile_count;
     const int32_t* gather;                     // may be null: row p of the product is row gather[p] / gather_k of A
     int gather_k;
+    int32_t* task_ctr;                         // kXcdCount zeroed counters (large tiles)
     int K, N, splits;
     int64_t M;
 };
@@ -329,39 +331,465 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
     }
 }
 
-using Large = Config<4, 2, 2, 4, 64, 4>;       // 256 rows
+// ----------------------------------------------------------------------------------- large tiles
+//
+// 256 rows x 256 weight columns per task (8 waves of 64 x 128, two per SIMD) for K >= 256: the structure
+// of the MX large-tile kernel.  A K step is 64 values (two MFMAs per block).  The weights go through
+// four stages of one step, A through two stages of a pair of steps (rows of 128 bytes, whole cache
+// lines); three steps are in flight.  Each step's MFMAs run in two halves around its one barrier
+// (weight blocks 0-1, then 2-3), each followed by its share of the step's copies and fragment reads.
+// Tasks are claimed per XCD, and the next task's first copies go out before the current epilogue.
+namespace big {
+
+constexpr int kWM = 4, kWN = 2, kTM = 2, kTN = 4;
+constexpr int BM = kWM * kTM * 32;                    // 256
+constexpr int BK = 64;
+constexpr int kStages = 4;
+constexpr int kBBytes = BK * BNB;                     // one weight stage: 16 KiB
+constexpr int kAPairBytes = BM * 2 * BK;              // one A stage: 32 KiB
+constexpr int kBRing = 2 * kAPairBytes;               // the A stages, then the weight stages
+constexpr int kOutBase = kBRing + kStages * kBBytes;  // 128 KiB
+constexpr int kOutWaveBytes = 4096;                   // epilogue staging per wave
+constexpr int kSmemBytes = kOutBase + kWaves * kOutWaveBytes;
+constexpr int kACopies = kAPairBytes / 1024 / kWaves; // 4 per wave and pair
+constexpr int kBCopies = kBBytes / 1024 / kWaves;     // 2 per wave and step
+static_assert(kSmemBytes <= 160 * 1024, "LDS");
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// Sources (uniform) and LDS destinations of this wave's copies: A at the next pair, the weights at the
+// next step.
+struct Copy {
+    const uint8_t* a;
+    const uint8_t* b;
+    uint32_t a_lds, b_lds;
+};
+
+// Copies C0 .. C1 - 1 of a step's list: its weights into stage SB when SB >= 0, then the A of a pair into
+// pair stage QA when QA >= 0 (the barriers' waits count on this order).
+template <int SB, int QA>
+constexpr int copy_count() { return (SB >= 0 ? kBCopies : 0) + (QA >= 0 ? kACopies : 0); }
+template <int SB, int QA, int C0, int C1>
+__device__ __forceinline__ void copies(const Copy& c, const uint32_t (&a_voff)[kACopies],
+                                       const uint32_t (&b_voff)[kBCopies])
+{
+    constexpr int nb = SB >= 0 ? kBCopies : 0;
+#pragma unroll
+    for (int q = C0; q < C1; ++q) {
+        if (q < nb)
+            lds_copy16(c.b, b_voff[q], c.b_lds + SB * kBBytes + q * 1024);
+        else
+            lds_copy16(c.a, a_voff[q - nb], c.a_lds + QA * kAPairBytes + (q - nb) * 1024);
+    }
+}
+
+// The lane's fragment addresses in stage 0, hidden from the optimiser so that stages and blocks stay
+// immediate offsets.
+struct LaneAddr {
+    uint32_t a[2][2];         // A, pair half hp: chunks 4 hp + h and 4 hp + 2 + h of the lane's row
+    uint32_t b[kTN];
+};
+
+struct Frag {                 // 64 k of one row or column: the two MFMAs' operands
+    i32x4_t k0, k1;
+};
+
+template <int p>
+__device__ __forceinline__ void read_a(Frag& f, const LaneAddr& la, int i)
+{
+    constexpr int S = p % kStages;
+    const uint32_t o = (S / 2) * kAPairBytes + i * (kWM * 32 * 128);
+    f.k0 = __builtin_bit_cast(i32x4_t, read16(la.a[S % 2][0] + o));
+    f.k1 = __builtin_bit_cast(i32x4_t, read16(la.a[S % 2][1] + o));
+}
+template <bool kGated, int p>
+__device__ __forceinline__ void read_b(Frag& f, const LaneAddr& la, int j)
+{
+    constexpr int kRowBytes = kGated ? 128 : 256;
+    const uint32_t at = la.b[j] + (p % kStages) * kBBytes;
+    f.k0 = read_tr16<kRowBytes>(at);
+    f.k1 = read_tr16<kRowBytes>(at + 32 * kRowBytes);
+}
+
+// MFMA mm of one half step (all blocks' first 32 k, then their second): block (row i, column j0 + jj).
+template <int NB, int J0, int mm>
+__device__ __forceinline__ void mfma(i32x16_t (&acc)[kTM][kTN], const Frag (&A)[kTM], const Frag (&b)[2])
+{
+    constexpr int m = mm % (2 * NB), i = m / 2, jj = m % 2;
+    acc[i][J0 + jj] = __builtin_amdgcn_mfma_i32_32x32x32_i8(mm < 2 * NB ? b[jj].k0 : b[jj].k1,
+                                                            mm < 2 * NB ? A[i].k0 : A[i].k1, acc[i][J0 + jj], 0, 0, 0);
+}
+
+template <bool kGated, int NB, int p, int mm>
+__device__ __forceinline__ void before(i32x16_t (&acc)[kTM][kTN], const Frag (&A)[kTM], const Frag (&b01)[2],
+                                       Frag (&b23)[2], const LaneAddr& la)
+{
+    mfma<NB, 0, mm>(acc, A, b01);
+    if constexpr (mm < 2)
+        read_b<kGated, p>(b23[mm], la, 2 + mm);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// After the barrier: the copies and the next step's reads are spread over the first half of the MFMAs,
+// so that the reads land well before the next step needs them.
+template <bool kGated, int NB, int p, int SB, int QA, int mm>
+__device__ __forceinline__ void after(i32x16_t (&acc)[kTM][kTN], const Frag (&A)[kTM], Frag (&An)[kTM],
+                                      const Frag (&b23)[2], Frag (&b01)[2], const LaneAddr& la, const Copy& cp,
+                                      const uint32_t (&a_voff)[kACopies], const uint32_t (&b_voff)[kBCopies])
+{
+    constexpr int half = 2 * NB, NC = copy_count<SB, QA>(), NR = NB + 2;
+    constexpr int pn = (p + 1) % kStages;
+    mfma<NB, 2, mm>(acc, A, b23);
+    if constexpr (mm < half) {
+        copies<SB, QA, mm * NC / half, (mm + 1) * NC / half>(cp, a_voff, b_voff);
+#pragma unroll
+        for (int r = mm * NR / half; r < (mm + 1) * NR / half; ++r) {
+            if (r == 0)
+                read_a<pn>(An[0], la, 0);
+            else if (r < 3)
+                read_b<kGated, pn>(b01[r - 1], la, r - 1);
+            else
+                read_a<pn>(An[NB - 1], la, NB - 1);
+        }
+    }
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// Copies in flight that still let "step t + 1 has landed" hold at the barrier of step t (at position p of
+// a unit).  In issue order: setup A pair 0, weights 0 .. 3, pair 1; after barrier t weights t + 4 and, t
+// odd, pair (t + 3) / 2.  Even t: what step t + 1 needs was complete a barrier before, but for t = 0, where
+// the weights of steps 2, 3 and pair 1 may be open.  Odd t: pair (t + 1) / 2 has only the weights of step
+// t + 3 behind it (nothing in a task's last unit).
+template <int p, bool kLast>
+constexpr int wait() { return p % 2 == 0 ? 2 * kBCopies + kACopies : kLast ? 0 : kBCopies; }
+constexpr int kTopWait = 3 * kBCopies + kACopies;     // step 0 has landed
+
+template <bool kGated, int NB, int p, bool kLast, int... Ms>
+__device__ __forceinline__ void step(std::integer_sequence<int, Ms...>, i32x16_t (&acc)[kTM][kTN], const Frag (&A)[kTM],
+                                     Frag (&An)[kTM], Frag (&b01)[2], Frag (&b23)[2], const LaneAddr& la, Copy& cp,
+                                     const uint32_t (&a_voff)[kACopies], const uint32_t (&b_voff)[kBCopies],
+                                     int64_t N)
+{
+    constexpr int SB = kLast ? -1 : p, QA = !kLast && p % 2 == 1 ? ((p + 3) / 2) % 2 : -1;
+    __builtin_amdgcn_sched_barrier(0);
+    (before<kGated, NB, p, Ms>(acc, A, b01, b23, la), ...);
+    if constexpr (!kLast || p + 1 < kStages)
+        step_barrier<wait<p, kLast>()>();
+    __builtin_amdgcn_sched_barrier(0);
+    // after a task's last step the reads take a stale stage, whose fragments are never used
+    if constexpr (NB > 0)
+        (after<kGated, NB, p, SB, QA, Ms>(acc, A, An, b23, b01, la, cp, a_voff, b_voff), ...);
+    else
+        copies<SB, QA, 0, copy_count<SB, QA>()>(cp, a_voff, b_voff);
+    if constexpr (SB >= 0)
+        cp.b += BK * N;
+    if constexpr (QA >= 0)
+        cp.a += 2 * BK;
+    __builtin_amdgcn_sched_barrier(0);
+}
+
+// The K loop of one task: KT even, at least 4; an odd number of pairs starts at position 2 (setup puts
+// its first copies there).  Every LDS address is a lane base plus a constant.
+template <bool kGated, int NB>
+__device__ __forceinline__ void k_loop(i32x16_t (&acc)[kTM][kTN], const LaneAddr& la, Copy cp,
+                                       const uint32_t (&a_voff)[kACopies], const uint32_t (&b_voff)[kBCopies], int KT,
+                                       int64_t N)
+{
+    constexpr auto ms = std::make_integer_sequence<int, 4 * NB>{};
+    Frag A0[kTM], A1[kTM], b01[2], b23[2];
+    const bool half = (KT & 2) != 0;
+    if constexpr (NB > 0) {
+        if (half) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                read_a<2>(A0[i], la, i);
+            read_b<kGated, 2>(b01[0], la, 0);
+            read_b<kGated, 2>(b01[1], la, 1);
+        } else {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+                read_a<0>(A0[i], la, i);
+            read_b<kGated, 0>(b01[0], la, 0);
+            read_b<kGated, 0>(b01[1], la, 1);
+        }
+    }
+    if (half) {
+        step<kGated, NB, 2, false>(ms, acc, A0, A1, b01, b23, la, cp, a_voff, b_voff, N);
+        step<kGated, NB, 3, false>(ms, acc, A1, A0, b01, b23, la, cp, a_voff, b_voff, N);
+    }
+    for (int kt = half ? 2 : 0; kt < KT - kStages; kt += kStages) {
+        step<kGated, NB, 0, false>(ms, acc, A0, A1, b01, b23, la, cp, a_voff, b_voff, N);
+        step<kGated, NB, 1, false>(ms, acc, A1, A0, b01, b23, la, cp, a_voff, b_voff, N);
+        step<kGated, NB, 2, false>(ms, acc, A0, A1, b01, b23, la, cp, a_voff, b_voff, N);
+        step<kGated, NB, 3, false>(ms, acc, A1, A0, b01, b23, la, cp, a_voff, b_voff, N);
+    }
+    step<kGated, NB, 0, true>(ms, acc, A0, A1, b01, b23, la, cp, a_voff, b_voff, N);
+    step<kGated, NB, 1, true>(ms, acc, A1, A0, b01, b23, la, cp, a_voff, b_voff, N);
+    step<kGated, NB, 2, true>(ms, acc, A0, A1, b01, b23, la, cp, a_voff, b_voff, N);
+    step<kGated, NB, 3, true>(ms, acc, A1, A0, b01, b23, la, cp, a_voff, b_voff, N);
+}
+
+template <bool kGated, int kOut>
+__global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
+{
+    constexpr int BN = kGated ? BNB / 2 : BNB;
+    constexpr int kRowBytes = kGated ? 128 : 256;
+    constexpr int kChunks = kRowBytes / 16;
+    constexpr int kRowsPerCopy = 64 / kChunks;
+    using C = Config<kWM, kWN, kTM, kTN, BK, 2>;             // the wave layout, for block_mat / block_col
+    extern __shared__ __attribute__((aligned(256))) unsigned char smem[];
+    int* const claimed = reinterpret_cast<int*>(smem + kOutBase);   // start of wave 0's staging
+    const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(
+        (__attribute__((address_space(3))) unsigned char*)(smem)));
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / kWN, wn = wave % kWN;
+    const int lrow = lane & 31, lh = lane >> 5;
+    const int K = a.K, N = a.N;
+    const int KT = K / BK;
+    const int n_nt = (N + BN - 1) / BN;
+    const int total = *a.tile_count * n_nt;
+    const int first = KT & 2;                                // position of a task's first step
+
+    const int mat = kGated ? wave / (kWaves / 2) : 0;
+    const int bi0 = kGated ? kBCopies * (wave % (kWaves / 2)) : kBCopies * wave;
+    Copy cp{};
+    cp.a_lds = lds0 + kACopies * wave * 1024;
+    cp.b_lds = lds0 + kBRing + mat * (kBBytes / 2) + bi0 * 1024;
+    LaneAddr la;
+    {
+        const int r0 = 32 * wm + lrow;
+#pragma unroll
+        for (int hp = 0; hp < 2; ++hp)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                la.a[hp][q] = lds0 + r0 * 128 + 16 * aswz<128>(4 * hp + 2 * q + lh, r0);
+        const int g = lane >> 4, sl = lane & 15;
+        const int kr = 16 * (g >> 1) + (sl >> 1);
+#pragma unroll
+        for (int j = 0; j < kTN; ++j) {
+            const int col = block_col<C, kGated>(wn, j) + 16 * (g & 1) + 8 * (sl & 1);
+            la.b[j] = lds0 + kBRing + block_mat<C, kGated>(wn, j) * (kBBytes / 2) + kr * kRowBytes +
+                      16 * bswz<kGated>(col >> 4, kr) + (col & 15);
+        }
+        asm volatile("" : "+v"(la.a[0][0]), "+v"(la.a[0][1]), "+v"(la.a[1][0]), "+v"(la.a[1][1]));
+#pragma unroll
+        for (int j = 0; j < kTN; ++j)
+            asm volatile("" : "+v"(la.b[j]));
+    }
+
+    const int xcd = blockIdx.x % kXcdCount;
+    const int blk = gridDim.x / kXcdCount;
+    MTile tile{};
+    int n0 = 0;
+    uint32_t a_voff[kACopies], b_voff[kBCopies];
+    // Gathered rows: the slot-list entries of this lane's copy rows, loaded a task ahead.
+    int gsrc[kACopies] = {};
+    const auto fetch_rows = [&](const MTile& tl) {
+        if (a.gather == nullptr)
+            return;
+        const int last = tl.row_end - tl.row_begin - 1;
+#pragma unroll
+        for (int j = 0; j < kACopies; ++j)
+            gsrc[j] = a.gather[tl.row_begin + min(8 * (kACopies * wave + j) + lane / 8, last)];
+    };
+    const auto setup = [&](const MTile& tl, int nt) {
+        tile = tl;
+        n0 = nt * BN;
+        const int rows = tile.row_end - tile.row_begin;
+#pragma unroll
+        for (int j = 0; j < kACopies; ++j) {
+            const int r = 8 * (kACopies * wave + j) + lane / 8;      // 8 lanes per 128-byte row
+            const int src = a.gather != nullptr ? gsrc[j] / a.gather_k : min(r, rows - 1);
+            a_voff[j] = static_cast<uint32_t>(src) * static_cast<uint32_t>(K) + 16u * aswz<128>(lane % 8, r);
+        }
+#pragma unroll
+        for (int j = 0; j < kBCopies; ++j) {
+            const int kr = (bi0 + j) * kRowsPerCopy + lane / kChunks;
+            const int c = bswz<kGated>(lane % kChunks, kr);
+            // columns past N (the second half of the last tile): the tile's first chunk again
+            b_voff[j] = static_cast<uint32_t>(kr) * static_cast<uint32_t>(N) + 16u * (n0 + 16 * c < N ? c : 0);
+        }
+        cp.a = a.A + (a.gather != nullptr ? 0 : static_cast<int64_t>(tile.row_begin) * K);
+        cp.b = (kGated && mat == 1 ? a.B1 : a.B0) + static_cast<int64_t>(tile.expert) * K * N + n0;
+        // A pair 0, the weights of steps 0 .. 3, A pair 1 (the waits count on this order)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+            for (int j = 0; j < kACopies; ++j)
+                lds_copy16(cp.a, a_voff[j], cp.a_lds + ((first / 2 + q) & 1) * kAPairBytes + j * 1024);
+            cp.a += 2 * BK;
+            if (q == 1)
+                continue;
+#pragma unroll
+            for (int st = 0; st < kStages; ++st) {
+#pragma unroll
+                for (int j = 0; j < kBCopies; ++j)
+                    lds_copy16(cp.b, b_voff[j], cp.b_lds + ((first + st) & 3) * kBBytes + j * 1024);
+                cp.b += static_cast<int64_t>(BK) * N;
+            }
+        }
+    };
+
+    // Claims: two ahead when gathering rows or running at least four tasks per workgroup (a task's
+    // successor is in the claim word at its top barrier, and its tile entry is loaded during its K loop),
+    // else one ahead, read after the K loop.
+    const bool ahead2 = a.gather != nullptr || total >= 4 * static_cast<int>(gridDim.x);
+    int t = claim_task(claimed, a.task_ctr, xcd, blk, wave, lane);
+    if (ahead2)
+        claim_task(claimed, a.task_ctr, xcd, blk, wave, lane);
+    if (t < total) {
+        int nt;
+        const MTile tl = decode_task(t, n_nt, a.tiles, nt);
+        fetch_rows(tl);
+        setup(tl, nt);
+    }
+    while (t < total) {
+        const int rows = tile.row_end - tile.row_begin;
+        const int nb = __builtin_amdgcn_readfirstlane(min(kTM, max(0, ((rows + 31) / 32 - wm + kWM - 1) / kWM)));
+        i32x16_t acc[kTM][kTN];
+#pragma unroll
+        for (int i = 0; i < kTM; ++i)
+#pragma unroll
+            for (int j = 0; j < kTN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[i][j][r] = 0;
+        // step 0 has landed; past this barrier every wave sees the claim of the following task
+        step_barrier<kTopWait>();
+        int t_next = total;
+        MTile tile_next{};
+        int nt_next = 0;
+        if (ahead2) {
+            const int ci = __builtin_amdgcn_readfirstlane(*claimed);
+            t_next = ((ci / blk) * kXcdCount + xcd) * blk + ci % blk;
+            if (t_next < total)
+                tile_next = decode_task(t_next, n_nt, a.tiles, nt_next);
+        }
+        const int claim_ret = claim_issue(a.task_ctr, xcd, wave, lane);
+        if (t_next < total)
+            fetch_rows(tile_next);
+        if (nb == 0)
+            k_loop<kGated, 0>(acc, la, cp, a_voff, b_voff, KT, N);
+        else if (nb == 1)
+            k_loop<kGated, 1>(acc, la, cp, a_voff, b_voff, KT, N);
+        else
+            k_loop<kGated, 2>(acc, la, cp, a_voff, b_voff, KT, N);
+        const int claim_after = claim_value(claim_ret, wave);
+        if (!ahead2) {
+            if (wave == 0)
+                *claimed = claim_after;
+            __syncthreads();
+            const int ci = __builtin_amdgcn_readfirstlane(*claimed);
+            t_next = ((ci / blk) * kXcdCount + xcd) * blk + ci % blk;
+            if (t_next < total)
+                tile_next = decode_task(t_next, n_nt, a.tiles, nt_next);
+        }
+        const MTile done = tile;
+        const int done_n0 = n0;
+        t = t_next;
+        __syncthreads();                                     // the ring is free, and the claim word read
+        if (t < total)
+            setup(tile_next, nt_next);
+
+        // Epilogue: scaled blocks through the wave's staging area (rows of 128 bytes, 16-byte chunks
+        // XOR-swizzled by row), out as whole 128-byte row pieces.  Only the stores are under a row test.
+        const uint32_t stg = lds0 + kOutBase + wave * kOutWaveBytes;
+        const float* s0 = a.s0 + static_cast<int64_t>(done.expert) * N;
+        [[maybe_unused]] const float* s1 = kGated ? a.s1 + static_cast<int64_t>(done.expert) * N : nullptr;
+        constexpr bool kWide = kGated || kOut == kOutF32;    // float32 out: one 32-column block a row piece
+        constexpr int kBlocks = kGated ? kTN / 2 : kTN;      // output blocks of this wave's columns
+        constexpr int kPiece = kWide ? 1 : 2;                // output blocks per row piece
+#pragma unroll
+        for (int i = 0; i < kTM; ++i) {
+            const int srow = min(done.row_begin + row_block<kWM>(i, wm) + lrow, done.row_end - 1);
+            const float as = a.a_scale[a.gather != nullptr ? a.gather[srow] / a.gather_k : srow];
+#pragma unroll
+            for (int ob = 0; ob < kBlocks; ob += kPiece) {
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int b = 0; b < kPiece; ++b) {
+                    const int j = kGated ? 2 * ob : ob + b;
+                    const int col = done_n0 + block_col<C, kGated>(wn, j);
+                    const float* sc = s0 + (col < N ? col : 0);
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const f32x4_t sg = *reinterpret_cast<const f32x4_t*>(sc + 8 * g + 4 * lh);
+                        f32x4_t v;
+                        if constexpr (kGated) {
+                            const f32x4_t su = *reinterpret_cast<const f32x4_t*>(s1 + col + 8 * g + 4 * lh);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = swiglu(static_cast<float>(acc[i][j][4 * g + e]) * as * sg[e],
+                                              static_cast<float>(acc[i][j + 1][4 * g + e]) * as * su[e]);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = static_cast<float>(acc[i][j][4 * g + e]) * as * sg[e];
+                        }
+                        if constexpr (kWide)
+                            *reinterpret_cast<__attribute__((address_space(3))) f32x4_t*>(
+                                stg + lrow * 128 + (((2 * g + lh) ^ (lrow & 7)) << 4)) = v;
+                        else
+                            *reinterpret_cast<__attribute__((address_space(3))) u32x2_t*>(
+                                stg + lrow * 128 + (((4 * b + g) ^ (lrow & 7)) << 4) + 8 * lh) =
+                                u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                    }
+                }
+                const int col = done_n0 + block_col<C, kGated>(wn, kGated ? 2 * ob : ob);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) {
+                    const int row = (lane >> 3) + 8 * m, chunk = lane & 7;
+                    const u32x4_t v = read16(stg + row * 128 + ((chunk ^ (row & 7)) << 4));
+                    const int grow = done.row_begin + row_block<kWM>(i, wm) + row;
+                    if (grow < done.row_end && col < N)
+                        *reinterpret_cast<u32x4_t*>(static_cast<unsigned char*>(a.out) +
+                                                    (static_cast<int64_t>(grow) * N + col) * (kWide ? 4 : 2) + 16 * chunk) = v;
+                }
+            }
+        }
+        // two ahead: the claim goes out after wave 0's last read of its staging area, which holds the word
+        if (ahead2 && wave == 0)
+            *claimed = claim_after;
+    }
+}
+
+}  // namespace big
+
 using Mid = Config<2, 4, 2, 2, 128, 3>;        // 128 rows
 using Small = Config<1, 8, 2, 1, 128, 3>;      // 64 rows; partial sums only when gated
 
-template <class C, bool kGated, int kOut>
+// Raises the kernel's LDS limit once per device and launches it, one workgroup per CU.
+template <auto kernel, int kSmem>
 hipError_t launch(const Args& a, hipStream_t s)
 {
-    static std::atomic<bool> done[64];         // per device: the LDS limit is raised
+    static std::atomic<bool> done[64];
     int dev = 0;
     if (hipError_t e = hipGetDevice(&dev); e != hipSuccess)
         return e;
-    const auto kernel = &grouped_gemm_i8<C, kGated, kOut>;
     if (dev >= 64 || !done[dev]) {
         if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, kSmem);
             e != hipSuccess)
             return e;
         if (dev < 64)
             done[dev] = true;
     }
-    kernel<<<dim3(device_info().cu_count), dim3(kThreads), C::kSmemBytes, s>>>(a);
+    kernel<<<dim3(device_info().cu_count), dim3(kThreads), kSmem, s>>>(a);
     return hipGetLastError();
 }
 
 template <bool kGated, int kOut>
 hipError_t launch_rows(int bm, const Args& a, hipStream_t s)
 {
-    if (bm == Large::BM)
-        return launch<Large, kGated, kOut>(a, s);
-    if (bm == Mid::BM)
-        return launch<Mid, kGated, kOut>(a, s);
-    if constexpr (!kGated || kOut == kOutPartial)
-        return launch<Small, kGated, kOut>(a, s);
+    if (bm == big::BM) {
+        if constexpr (kOut != kOutPartial)
+            return launch<&big::grouped_gemm_i8_dma<kGated, kOut>, big::kSmemBytes>(a, s);
+    } else if (bm == Mid::BM) {
+        return launch<&grouped_gemm_i8<Mid, kGated, kOut>, Mid::kSmemBytes>(a, s);
+    } else if constexpr (!kGated || kOut == kOutPartial) {
+        return launch<&grouped_gemm_i8<Small, kGated, kOut>, Small::kSmemBytes>(a, s);
+    }
     return hipErrorInvalidValue;
 }
 
@@ -373,13 +801,13 @@ bool int8_supported(int64_t K, int64_t N)
     return K > 0 && N > 0 && K % 128 == 0 && N % 128 == 0 && K <= kInt8MaxK;
 }
 
-Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated)
+Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int64_t least_k)
 {
     // the groups that can hold rows, and the row tiles of each height they make at most
     const int64_t groups = std::max<int64_t>(1, std::min(M, G));
     const int64_t per_group = ceil_div(std::max<int64_t>(M, 1), groups);
     Int8Plan p;
-    p.row_tile = per_group <= 64 ? 64 : per_group <= 160 ? 128 : 256;
+    p.row_tile = per_group <= 64 ? 64 : per_group <= 160 || least_k < 256 ? 128 : 256;
     const int64_t cols = ceil_div(N, gated ? i8::BNB / 2 : i8::BNB);
     const int64_t tasks = (groups + M / p.row_tile) * cols;
     const int64_t steps = K / 128;
@@ -393,7 +821,7 @@ Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated)
 hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_scale, const int8_t* w0,
                           const float* s0, const int8_t* w1, const float* s1, void* out, int out_dtype,
                           int64_t M, int64_t K, int64_t N, const MTile* tiles, const int32_t* tile_count,
-                          const int32_t* gather, int gather_k, hipStream_t s)
+                          const int32_t* gather, int gather_k, int32_t* task_ctr, hipStream_t s)
 {
     i8::Args a{};
     a.A = reinterpret_cast<const uint8_t*>(A);
@@ -407,6 +835,7 @@ hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_sca
     a.tile_count = tile_count;
     a.gather = gather;
     a.gather_k = gather_k;
+    a.task_ctr = task_ctr;
     a.K = static_cast<int>(K);
     a.N = static_cast<int>(N);
     a.splits = p.splits;

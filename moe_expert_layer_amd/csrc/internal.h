@@ -251,20 +251,22 @@ constexpr int64_t kInt8MaxK = 130944;  // |sum of K products of -128 .. 127| sta
 bool int8_supported(int64_t K, int64_t N);
 // How a grouped product of M rows in at most G groups with [K, N] weights (gated: two of them) runs:
 // the tile table's height, the cuts of K, and whether the kernel leaves int32 partial sums
-// ([splits, M, N], gated [splits, M, 2 N]) for launch_int8_finish / launch_int8_swiglu_partial.
+// ([splits, M, N], gated [splits, M, 2 N]) for launch_int8_finish / launch_int8_swiglu_partial.  least_k:
+// the smallest K among the products that share the tile table.
 struct Int8Plan {
     int row_tile;
     int splits;
     bool partial;
 };
-Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated);
+Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int64_t least_k);
 // out: [M, N] of out_dtype (MOE_F32 / MOE_BF16), gated (w1 not null) float32 swiglu of the two
 // products, or the partial sums.  gather (may be null): row p of the product is row
-// gather[p] / gather_k of A and a_scale, whose rows then lie within 2^32 bytes.
+// gather[p] / gather_k of A and a_scale, whose rows then lie within 2^32 bytes.  task_ctr: kXcdCount zeroed
+// counters for this launch (256-row tiles).
 hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_scale, const int8_t* w0,
                           const float* s0, const int8_t* w1, const float* s1, void* out, int out_dtype,
                           int64_t M, int64_t K, int64_t N, const MTile* tiles, const int32_t* tile_count,
-                          const int32_t* gather, int gather_k, hipStream_t s);
+                          const int32_t* gather, int gather_k, int32_t* task_ctr, hipStream_t s);
 // quant_i8.hip.  Rows of float32 or bfloat16 -> int8 codes and one scale per row (moe_int8_quantize).
 hipError_t launch_int8_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* codes,
                                 float* scales, hipStream_t s);

@@ -101,6 +101,10 @@ PRODUCTS = [
     ([5] * 100, 128, 128),
     ([700, 0, 900], 128, 256),
     ([2], 16384, 256),                           # K cut 16 times
+    ([513, 256, 300], 384, 384),                 # 256-row tiles, odd numbers of K pairs and column strips
+    ([900, 0, 64, 2000], 896, 1152),
+    ([3000], 1024, 256),
+    ([700] * 12, 512, 512),                      # more tasks than four per workgroup need
 ]
 
 
@@ -171,7 +175,7 @@ def _weights(rng, E, H, F):
             _codes(rng, E, F, H), _scale(rng, E, H, level=3e-4))
 
 
-FFNS = [([1], 128, 128), ([3, 0, 5], 256, 384), ([60, 64, 1], 128, 640), ([150, 129], 384, 256),
+FFNS = [([400, 290], 128, 384), ([512, 31, 600], 384, 640), ([1], 128, 128), ([3, 0, 5], 256, 384), ([60, 64, 1], 128, 640), ([150, 129], 384, 256),
         ([300, 0, 270], 256, 512), ([2000], 128, 128), ([1, 1], 2048, 256)]
 
 
