@@ -531,16 +531,19 @@ struct Int8Weights {
     const float *gate_scale, *up_scale, *down_scale;
 };
 
-// fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.
+// fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.  have_tiles: the
+// tile table is there already.  y null: the down projection's partial sums (L.fc2.partial) stay for the
+// caller.
 moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, const int32_t* offsets,
                         const int32_t* group_expert, int64_t G, int64_t E, int64_t H, int64_t F,
                         const Int8Weights& w, void* y, void* ws, const Int8Layout& L, bool write_status,
-                        hipStream_t s, const int32_t* gather, int gather_k)
+                        hipStream_t s, const int32_t* gather, int gather_k, bool have_tiles)
 {
     int32_t* tcount = at<int32_t>(ws, L.tile_count);
     MTile* tiles = at<MTile>(ws, L.tiles_run);
     const int32_t* count = tcount + 4;
-    LAUNCH(s, "build_tiles",
+    if (!have_tiles)
+        LAUNCH(s, "build_tiles",
            launch_build_tiles(offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.fc1.row_tile,
                               at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0,
                               at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), write_status, s, tiles, tcount + 4));
@@ -560,7 +563,7 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
            launch_gemm_i8(L.fc2, h_q, h_scale, w.down, w.down_scale, nullptr, nullptr,
                           L.fc2.partial ? at<void>(ws, L.y_part) : y, MOE_BF16, M, F, H, tiles, count, nullptr, 1,
                           at<int32_t>(ws, L.task_ctr) + kXcdCount, s));
-    if (L.fc2.partial)
+    if (L.fc2.partial && y != nullptr)
         LAUNCH(s, "int8_finish",
                launch_int8_finish(at<int32_t>(ws, L.y_part), L.fc2.splits, h_scale, w.down_scale, offsets,
                                   group_expert, G, E, M, H, y, MOE_BF16, s));
@@ -740,25 +743,41 @@ MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, 
     int32_t* perm = at<int32_t>(ws, L.perm);
     int32_t* pos = at<int32_t>(ws, L.pos);
     int32_t* offsets = at<int32_t>(ws, L.offsets);
-    if (moe_status st = run_route(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos, ws, L.route, s);
-        st != MOE_OK)
-        return st;
-    if (T == 0)
-        return MOE_OK;
     const int8_t* rows = static_cast<const int8_t*>(x);
     const float* rows_scale = x_scale;
     if (quantize_x) {
-        LAUNCH(s, "int8_quantize",
-               launch_int8_quantize(MOE_BF16, x, T, H, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_q_scale), s));
         rows = at<int8_t>(ws, L.x_q);
         rows_scale = at<float>(ws, L.x_q_scale);
     }
+    const bool small = T > 0 && M <= kInt8SmallSlots && L.fc1.row_tile != 256;
+    if (small) {
+        LAUNCH(s, "int8_prologue",
+               launch_int8_prologue(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos, at<int32_t>(ws, 0),
+                                    L.fc1.row_tile, at<MTile>(ws, L.tiles_run), at<int32_t>(ws, L.tile_count) + 4,
+                                    quantize_x ? static_cast<const uint16_t*>(x) : nullptr, H, at<int8_t>(ws, L.x_q),
+                                    at<float>(ws, L.x_q_scale), s));
+    } else {
+        if (moe_status st = run_route(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos, ws, L.route, s);
+            st != MOE_OK)
+            return st;
+        if (T == 0)
+            return MOE_OK;
+        if (quantize_x)
+            LAUNCH(s, "int8_quantize",
+                   launch_int8_quantize(MOE_BF16, x, T, H, at<int8_t>(ws, L.x_q), at<float>(ws, L.x_q_scale), s));
+    }
     const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
-    if (moe_status st = run_ffn_int8(rows, rows_scale, M, offsets, nullptr, E, E, H, F, w, at<void>(ws, L.y), ws, L,
-                                     false, s, perm, static_cast<int>(k));
+    if (moe_status st = run_ffn_int8(rows, rows_scale, M, offsets, nullptr, E, E, H, F, w,
+                                     L.fc2.partial ? nullptr : at<void>(ws, L.y), ws, L, false, s, perm,
+                                     static_cast<int>(k), small);
         st != MOE_OK)
         return st;
-    LAUNCH(s, "unpermute", launch_unpermute(1, at<void>(ws, L.y), pos, probs, out_bf16, T, k, M, H, s));
+    if (L.fc2.partial)
+        LAUNCH(s, "int8_combine",
+               launch_int8_combine(at<int32_t>(ws, L.y_part), L.fc2.splits, at<float>(ws, L.h_scale), wd_scale, expert_ids,
+                                   pos, probs, T, k, H, static_cast<uint16_t*>(out_bf16), s));
+    else
+        LAUNCH(s, "unpermute", launch_unpermute(1, at<void>(ws, L.y), pos, probs, out_bf16, T, k, M, H, s));
     return MOE_OK;
 }
 
@@ -1121,7 +1140,7 @@ MOE_API moe_status moe_grouped_ffn_int8(const moe_problem* p, const int8_t* rows
         return st;
     const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
     return run_ffn_int8(rows, rows_scale, M, group_offsets, group_expert, G, p->E, p->H, p->F, w, y_rows, workspace,
-                        int8_layout(M, G, p->H, p->F, 0, 1, p->E, false), true, stream, nullptr, 1);
+                        int8_layout(M, G, p->H, p->F, 0, 1, p->E, false), true, stream, nullptr, 1, false);
 }
 
 namespace moe {

@@ -17,6 +17,7 @@
 // consecutive k of its column.
 #include <algorithm>
 #include <atomic>
+#include <cmath>
 #include <utility>
 
 #include "gemm_common.h"
@@ -114,6 +115,28 @@ __device__ __forceinline__ int first_task()
     return (b % kXcdCount) * per + b / kXcdCount;
 }
 
+// A pointer that is the same on every lane, in scalar registers.
+__device__ __forceinline__ const uint8_t* scalar(const uint8_t* p)
+{
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(static_cast<int>(v));
+    const uint32_t hi = __builtin_amdgcn_readfirstlane(static_cast<int>(v >> 32));
+    return reinterpret_cast<const uint8_t*>(static_cast<uint64_t>(hi) << 32 | lo);
+}
+
+// decode_task with its results in scalar registers.
+__device__ __forceinline__ MTile uniform_task(int t, int n_nt, const MTile* __restrict__ tiles, int& nt)
+{
+    int n;
+    const MTile m = decode_task(t, n_nt, tiles, n);
+    MTile u{};
+    u.expert = __builtin_amdgcn_readfirstlane(m.expert);
+    u.row_begin = __builtin_amdgcn_readfirstlane(m.row_begin);
+    u.row_end = __builtin_amdgcn_readfirstlane(m.row_end);
+    nt = __builtin_amdgcn_readfirstlane(n);
+    return u;
+}
+
 // Column block j of wave column wn: its matrix (gated: 0 gate, 1 up; blocks alternate, in one wave or
 // from wave to wave) and its first column among the task's outputs.
 template <class C, bool kGated>
@@ -144,8 +167,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
     const int wm = wave / C::kWN, wn = wave % C::kWN;
     const int lrow = lane & 31, lh = lane >> 5;
     const int K = a.K, N = a.N;
-    const int n_nt = (N + BN - 1) / BN * a.splits;
-    const int total = *a.tile_count * n_nt;
+    const int n_nt = (N + BN - 1) / BN;
+    const int total = __builtin_amdgcn_readfirstlane(*a.tile_count * n_nt * a.splits);
 
     // fragment addresses in stage 0
     uint32_t la_a[BK / 32], la_b[C::kTN];
@@ -170,48 +193,86 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
     const uint32_t a_lds = lds0 + C::kACopies * wave * 1024;
     const uint32_t b_lds = lds0 + C::kABytes + mat * (C::kBBytes / 2) + bi0 * 1024;
 
-    for (int t = first_task(); t < total; t += static_cast<int>(gridDim.x)) {
-        int nts;
-        const MTile tile = decode_task(t, n_nt, a.tiles, nts);
-        const int nt = nts / a.splits, split = nts % a.splits;
-        const int n0 = nt * BN;
-        const int rows = tile.row_end - tile.row_begin;
-        const int steps_all = K / BK;
-        const int kt0 = static_cast<int>(static_cast<int64_t>(steps_all) * split / a.splits);
-        const int steps = static_cast<int>(static_cast<int64_t>(steps_all) * (split + 1) / a.splits) - kt0;
+    const int steps_all = K / BK;
+    const auto steps_of = [&](int task) {                    // [begin, end) of the task's cut of K
+        const int split = task % a.splits;
+        return int2{static_cast<int>(static_cast<int64_t>(steps_all) * split / a.splits),
+                    static_cast<int>(static_cast<int64_t>(steps_all) * (split + 1) / a.splits)};
+    };
+    const int grid = static_cast<int>(gridDim.x);
 
-        uint32_t a_voff[C::kACopies], b_voff[C::kBCopies];
+    // The copies run kStages - 1 steps ahead of the products through all of the workgroup's tasks: task
+    // pt is the one being copied, its successor's tile entry and slot-list entries are loaded ahead.
+    int pt = first_task() - grid, left = 0, stage = 0, fill = 0, ahead = 0;
+    MTile next_tile{};
+    int next_nt = 0;
+    int gsrc[C::kACopies] = {};
+    const auto fetch = [&](int task) {
+        if (task >= total)
+            return;
+        next_tile = uniform_task(task / a.splits, n_nt, a.tiles, next_nt);
+        const int last = next_tile.row_end - next_tile.row_begin - 1;
 #pragma unroll
         for (int j = 0; j < C::kACopies; ++j) {
-            const int r = kARows * (C::kACopies * wave + j) + lane / kALanes;
-            const int c = aswz<BK>(lane % kALanes, r);
-            const int rr = min(r, rows - 1);                 // rows past the tile's end: its last row again
-            const int src = a.gather != nullptr ? a.gather[tile.row_begin + rr] / a.gather_k : rr;
-            a_voff[j] = static_cast<uint32_t>(src) * static_cast<uint32_t>(K) + 16u * c;
+            const int r = min(kARows * (C::kACopies * wave + j) + lane / kALanes, last);   // past the tile's end: its last row
+            gsrc[j] = a.gather != nullptr ? a.gather[next_tile.row_begin + r] : r;
         }
+    };
+    uint32_t a_voff[C::kACopies], b_voff[C::kBCopies];
+    const uint8_t* ap = nullptr;
+    const uint8_t* bp = nullptr;
+    const auto issue = [&]() {
+        if (left == 0) {
+            pt += grid;
+            if (pt >= total)
+                return;
+            const int n0 = next_nt * BN;
 #pragma unroll
-        for (int j = 0; j < C::kBCopies; ++j) {
-            const int kr = (bi0 + j) * kRowsPerCopy + lane / kChunks;
-            const int c = bswz<kGated>(lane % kChunks, kr);
-            // columns past N (the second half of the last tile): the tile's first chunk again
-            const int cc = n0 + 16 * c < N ? c : 0;
-            b_voff[j] = static_cast<uint32_t>(kr) * static_cast<uint32_t>(N) + 16u * cc;
+            for (int j = 0; j < C::kACopies; ++j) {
+                const int r = kARows * (C::kACopies * wave + j) + lane / kALanes;
+                const int src = a.gather != nullptr ? gsrc[j] / a.gather_k : gsrc[j];
+                a_voff[j] = static_cast<uint32_t>(src) * static_cast<uint32_t>(K) + 16u * aswz<BK>(lane % kALanes, r);
+            }
+#pragma unroll
+            for (int j = 0; j < C::kBCopies; ++j) {
+                const int kr = (bi0 + j) * kRowsPerCopy + lane / kChunks;
+                const int c = bswz<kGated>(lane % kChunks, kr);
+                // columns past N (the second half of the last tile): the tile's first chunk again
+                b_voff[j] = static_cast<uint32_t>(kr) * static_cast<uint32_t>(N) + 16u * (n0 + 16 * c < N ? c : 0);
+            }
+            const int2 kt = steps_of(pt);
+            left = kt.y - kt.x;
+            const int64_t k0 = static_cast<int64_t>(kt.x) * BK;
+            ap = scalar(a.A + (a.gather != nullptr ? 0 : static_cast<int64_t>(next_tile.row_begin) * K) + k0);
+            bp = scalar((kGated && mat == 1 ? a.B1 : a.B0) + (static_cast<int64_t>(next_tile.expert) * K + k0) * N + n0);
+            fetch(pt + grid);
         }
-        const int64_t k0 = static_cast<int64_t>(kt0) * BK;
-        const uint8_t* ap = a.A + (a.gather != nullptr ? 0 : static_cast<int64_t>(tile.row_begin) * K) + k0;
-        const uint8_t* bp = (kGated && mat == 1 ? a.B1 : a.B0) +
-                            (static_cast<int64_t>(tile.expert) * K + k0) * N + n0;
-        const auto issue = [&](int stage) {
-            const uint32_t so = stage * C::kStageBytes;
+        const uint32_t so = fill * C::kStageBytes;
 #pragma unroll
-            for (int j = 0; j < C::kACopies; ++j)
-                lds_copy16(ap, a_voff[j], a_lds + so + j * 1024);
+        for (int j = 0; j < C::kACopies; ++j)
+            lds_copy16(ap, a_voff[j], a_lds + so + j * 1024);
 #pragma unroll
-            for (int j = 0; j < C::kBCopies; ++j)
-                lds_copy16(bp, b_voff[j], b_lds + so + j * 1024);
-            ap += BK;
-            bp += static_cast<int64_t>(BK) * N;
-        };
+        for (int j = 0; j < C::kBCopies; ++j)
+            lds_copy16(bp, b_voff[j], b_lds + so + j * 1024);
+        ap += BK;
+        bp += static_cast<int64_t>(BK) * N;
+        --left;
+        ++ahead;
+        fill = fill + 1 == C::kStages ? 0 : fill + 1;
+    };
+    fetch(pt + grid);
+#pragma unroll
+    for (int p = 0; p < C::kStages - 1; ++p)
+        issue();
+    static_assert(C::kStages == 3, "the waits below");
+
+    for (int t = first_task(); t < total; t += grid) {
+        int nt;
+        const MTile tile = uniform_task(t / a.splits, n_nt, a.tiles, nt);
+        const int n0 = nt * BN;
+        [[maybe_unused]] const int split = t % a.splits;
+        const int2 kt = steps_of(t);
+        const int steps = kt.y - kt.x;
 
         i32x16_t acc[C::kTM][C::kTN];
 #pragma unroll
@@ -222,26 +283,16 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
                 for (int r = 0; r < 16; ++r)
                     acc[i][j][r] = 0;
 
-#pragma unroll
-        for (int p = 0; p < C::kStages - 1; ++p)
-            if (p < steps)
-                issue(p);
-        int stage = 0, fill = C::kStages - 1;
-        for (int kt = 0; kt < steps; ++kt) {
-            // step kt has landed once the copies of the later steps alone are in flight
-            const int later = steps - 1 - kt;
-            if (later >= C::kStages - 2)
-                step_barrier<C::kCopies * (C::kStages - 2)>();
-            else if (C::kStages >= 4 && later == 1)
+        for (int k = 0; k < steps; ++k) {
+            // this step has landed once the copies of the one after it alone are in flight
+            --ahead;
+            if (ahead > 0)
                 step_barrier<C::kCopies>();
             else
                 step_barrier<0>();
-            // every wave has read step kt - 1: its stage takes step kt + kStages - 1
-            if (kt + C::kStages - 1 < steps)
-                issue(fill);
+            issue();                                         // into the stage that every wave has just finished
             const uint32_t so = stage * C::kStageBytes;
             stage = stage + 1 == C::kStages ? 0 : stage + 1;
-            fill = fill + 1 == C::kStages ? 0 : fill + 1;
 #pragma unroll
             for (int q = 0; q < BK / 32; ++q) {
                 i32x4_t fa[C::kTM], fb[C::kTN];
@@ -258,7 +309,6 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
                         acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[j], fa[i], acc[i][j], 0, 0, 0);
             }
         }
-        step_barrier<0>();                                   // the stages are free for the next task
 
         // Epilogue.  Only the stores are under the lane's row test (no other lane-divergent region sits
         // in the task loop); a row past the tile's end reads the last row's scale.
@@ -803,17 +853,32 @@ bool int8_supported(int64_t K, int64_t N)
 
 Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int64_t least_k)
 {
-    // the groups that can hold rows, and the row tiles of each height they make at most
-    const int64_t groups = std::max<int64_t>(1, std::min(M, G));
+    // how many groups hold rows, for rows spread evenly at random
+    const double held = G * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(G), static_cast<double>(M)));
+    const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(std::ceil(held)));
     const int64_t per_group = ceil_div(std::max<int64_t>(M, 1), groups);
     Int8Plan p;
     p.row_tile = per_group <= 64 ? 64 : per_group <= 160 || least_k < 256 ? 128 : 256;
-    const int64_t cols = ceil_div(N, gated ? i8::BNB / 2 : i8::BNB);
-    const int64_t tasks = (groups + M / p.row_tile) * cols;
-    const int64_t steps = K / 128;
-    p.splits = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({steps, 16, 512 / std::max<int64_t>(1, tasks)})));
-    if (p.row_tile == 256)
-        p.splits = 1;
+    p.splits = 1;
+    if (p.row_tile != 256) {
+        // K is cut where that evens out the workgroups' shares: the rounds over the CUs, at the cost of
+        // about one step per cut task and of writing and reading the partial sums
+        const int64_t tasks = (groups + M / p.row_tile) * ceil_div(N, gated ? i8::BNB / 2 : i8::BNB);
+        constexpr int cus = 256;                              // a host-only rule: the MI355X's, whatever is current
+        const int64_t steps = K / 128;
+        double best = 0.0;
+        for (int64_t c = 1; c <= std::min<int64_t>(16, std::max<int64_t>(1, steps / 4)); ++c) {
+            const double sums = 8.0 * static_cast<double>(M) * static_cast<double>(N) * (gated ? 2 : 1) * (c > 1 || gated ? c : 0);
+            const double weights = static_cast<double>(groups) * static_cast<double>(K) * static_cast<double>(N) * (gated ? 2 : 1);
+            const double cost = static_cast<double>(ceil_div(tasks * c, cus)) / c * (1.0 + static_cast<double>(c) / steps) *
+                                    static_cast<double>(cus) / static_cast<double>(tasks) +
+                                sums / weights;
+            if (c == 1 || cost < 0.97 * best) {
+                best = cost;
+                p.splits = static_cast<int>(c);
+            }
+        }
+    }
     p.partial = p.splits > 1 || (gated && p.row_tile == 64);
     return p;
 }

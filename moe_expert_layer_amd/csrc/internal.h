@@ -277,6 +277,17 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
                                       const int32_t* offsets, const int32_t* group_expert, int64_t G,
                                       int64_t E, int64_t M, int64_t F, int8_t* codes, float* scales,
                                       hipStream_t s);
+// The routing (as launch_route_* leave it), the table of balanced row tiles of height bm with its count,
+// and with x not null the quantised token rows, in one launch; at most kInt8SmallSlots slots.
+constexpr int64_t kInt8SmallSlots = 256;
+hipError_t launch_int8_prologue(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* counts, int32_t* offsets,
+                                int32_t* perm, int32_t* pos, int32_t* status, int bm, MTile* tiles,
+                                int32_t* tile_count, const uint16_t* x, int64_t H, int8_t* codes, float* scales,
+                                hipStream_t s);
+// The layer's output [T, N] bfloat16 from the down projection's partial sums [splits, T k, N].
+hipError_t launch_int8_combine(const int32_t* partial, int splits, const float* a_scale, const float* w_scale,
+                               const int32_t* expert_ids, const int32_t* pos, const float* probs, int64_t T, int64_t k,
+                               int64_t N, uint16_t* out, hipStream_t s);
 // out [M, N] from the partial sums [splits, M, N] of the rows that a group holds.
 hipError_t launch_int8_finish(const int32_t* partial, int splits, const float* a_scale, const float* w_scale,
                               const int32_t* offsets, const int32_t* group_expert, int64_t G, int64_t E,

@@ -16,7 +16,8 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;       // of most kernels; one row's quantisation takes kWideThreads where rows are few
+constexpr int kWideThreads = 1024;
 constexpr int kVec = 8;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
@@ -58,7 +59,8 @@ __device__ __forceinline__ int code_of(float x, const RowCode& c)
     return static_cast<int>(r);
 }
 
-// The largest of the workgroup's values, on every thread.
+// The largest of the workgroup's values, on every thread (kT threads).
+template <int kT>
 __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf)
 {
 #pragma unroll
@@ -69,7 +71,7 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf)
     __syncthreads();
     uint32_t m = buf[0];
 #pragma unroll
-    for (int w = 1; w < kThreads / 64; ++w)
+    for (int w = 1; w < kT / 64; ++w)
         m = max(m, buf[w]);
     return m;
 }
@@ -83,7 +85,7 @@ __device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets,
     if (threadIdx.x == 0)
         *found = INT32_MAX;
     __syncthreads();
-    for (int g = threadIdx.x; g < G; g += kThreads) {
+    for (int g = threadIdx.x; g < G; g += blockDim.x) {
         const int64_t rb = min(max(static_cast<int64_t>(offsets[g]), int64_t{0}), M);
         const int64_t re = min(static_cast<int64_t>(offsets[g + 1]), M);
         if (row >= rb && row < re)
@@ -100,7 +102,7 @@ __device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets,
 // One workgroup per row.  The row's values come from Src::load (kV neighbouring ones at a time); the
 // first kPer vectors of a thread stay in registers between the maximum and the codes, later ones are
 // made again.
-template <class Src, int kV, int kPer, bool kExactProduct>
+template <class Src, int kV, int kPer, bool kExactProduct, int kT = kThreads>
 __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_t* __restrict__ codes,
                                              float* __restrict__ scale, uint32_t* buf)
 {
@@ -108,7 +110,7 @@ __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_
     uint32_t amax = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kV;
+        const int64_t c = (static_cast<int64_t>(i) * kT + threadIdx.x) * kV;
         if (c < cols) {
             src.load(c, keep[i]);
 #pragma unroll
@@ -116,14 +118,14 @@ __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_
                 amax = max(amax, __float_as_uint(keep[i][v]) & 0x7fffffffu);
         }
     }
-    for (int64_t c = (static_cast<int64_t>(kPer) * kThreads + threadIdx.x) * kV; c < cols; c += kThreads * kV) {
+    for (int64_t c = (static_cast<int64_t>(kPer) * kT + threadIdx.x) * kV; c < cols; c += kT * kV) {
         float x[kV];
         src.load(c, x);
 #pragma unroll
         for (int v = 0; v < kV; ++v)
             amax = max(amax, __float_as_uint(x[v]) & 0x7fffffffu);
     }
-    const RowCode rc = row_code(block_max(amax, buf));
+    const RowCode rc = row_code(block_max<kT>(amax, buf));
     const auto store = [&](int64_t c, const float (&x)[kV]) {
         if constexpr (kV == 1) {
             codes[c] = static_cast<int8_t>(rc.finite ? code_of<kExactProduct>(x[0], rc) : 0);
@@ -143,11 +145,11 @@ __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_
     };
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * kThreads + threadIdx.x) * kV;
+        const int64_t c = (static_cast<int64_t>(i) * kT + threadIdx.x) * kV;
         if (c < cols)
             store(c, keep[i]);
     }
-    for (int64_t c = (static_cast<int64_t>(kPer) * kThreads + threadIdx.x) * kV; c < cols; c += kThreads * kV) {
+    for (int64_t c = (static_cast<int64_t>(kPer) * kT + threadIdx.x) * kV; c < cols; c += kT * kV) {
         float x[kV];
         src.load(c, x);
         store(c, x);
@@ -233,13 +235,14 @@ struct SwigluRow {
     }
 };
 
-__global__ __launch_bounds__(kThreads) void int8_swiglu_partial_kernel(
+template <int kT, int kPer>
+__global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
     const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
     const int32_t* __restrict__ gather, int gather_k, const float* __restrict__ sg, const float* __restrict__ su,
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ group_expert, int G, int E, int64_t M,
     int64_t F, int8_t* __restrict__ codes, float* __restrict__ scales)
 {
-    __shared__ uint32_t buf[kThreads / 64];
+    __shared__ uint32_t buf[kT / 64];
     __shared__ int found;
     const int64_t r = blockIdx.x;
     const int e = row_expert(offsets, group_expert, G, E, M, r, &found);
@@ -253,7 +256,23 @@ __global__ __launch_bounds__(kThreads) void int8_swiglu_partial_kernel(
     src.sg = sg + static_cast<int64_t>(e) * F;
     src.su = su + static_cast<int64_t>(e) * F;
     src.F = F;
-    quantize_row<SwigluRow, kVec, 8, false>(src, F, codes + r * F, scales + r, buf);
+    quantize_row<SwigluRow, kVec, kPer, false, kT>(src, F, codes + r * F, scales + r, buf);
+}
+
+// The four columns from c of row r's product: the partial sums added up, scaled.
+__device__ __forceinline__ f32x4_t finish4(const int32_t* __restrict__ partial, int splits, int64_t cut, int64_t at,
+                                           float a_scale, const float* __restrict__ w_scale)
+{
+    i32x4_t a = *reinterpret_cast<const i32x4_t*>(partial + at);
+#pragma unroll 4
+    for (int s = 1; s < splits; ++s)
+        a += *reinterpret_cast<const i32x4_t*>(partial + s * cut + at);
+    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(w_scale);
+    f32x4_t v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        v[i] = static_cast<float>(a[i]) * a_scale * w[i];
+    return v;
 }
 
 template <bool kBf16>
@@ -271,19 +290,143 @@ __global__ __launch_bounds__(kThreads) void int8_finish_kernel(
     const float* ws = w_scale + static_cast<int64_t>(e) * N;
     for (int64_t c = 4 * (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x); c < N;
          c += 4 * static_cast<int64_t>(gridDim.y) * kThreads) {
-        i32x4_t a = *reinterpret_cast<const i32x4_t*>(partial + r * N + c);
-        for (int s = 1; s < splits; ++s)
-            a += *reinterpret_cast<const i32x4_t*>(partial + (s * M + r) * N + c);
-        const f32x4_t w = *reinterpret_cast<const f32x4_t*>(ws + c);
-        f32x4_t v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = static_cast<float>(a[i]) * as * w[i];
+        const f32x4_t v = finish4(partial, splits, M * N, r * N + c, as, ws + c);
         if constexpr (kBf16)
             *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + r * N + c) =
                 u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
         else
             *reinterpret_cast<f32x4_t*>(static_cast<float*>(out) + r * N + c) = v;
+    }
+}
+
+// The combine of the layer straight from the down projection's partial sums: each slot's row is rounded
+// to bfloat16 as the stored rows of the other path are, and the k of a token are added in slot order
+// by fused multiply-adds from 0, as moe_unpermute does: bitwise the same output.
+__global__ __launch_bounds__(kThreads) void int8_combine_kernel(
+    const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
+    const float* __restrict__ w_scale, const int32_t* __restrict__ expert_ids, const int32_t* __restrict__ pos,
+    const float* __restrict__ probs, int k, int64_t M, int64_t N, uint16_t* __restrict__ out)
+{
+    const int64_t t = blockIdx.x;
+    const int64_t c = 4 * (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x);
+    if (c >= N)
+        return;
+    f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < k; ++j) {
+        const int64_t row = pos[t * k + j];
+        if (row < 0 || row >= M)
+            continue;
+        const int e = expert_ids[t * k + j];
+        const f32x4_t v = finish4(partial, splits, M * N, row * N + c, a_scale[row], w_scale + static_cast<int64_t>(e) * N + c);
+        const float p = probs[t * k + j];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            sum[i] = fmaf(p, bf16_to_f32(f32_to_bf16(v[i])), sum[i]);
+    }
+    *reinterpret_cast<u32x2_t*>(out + t * N + c) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+}
+
+// What a small layer call needs before its first product, in one launch: workgroup 0 routes (counts,
+// offsets, perm and pos of at most kInt8SmallSlots slots: a slot's rank among equal ids is counted
+// directly) and writes the table of balanced row tiles, the others quantise a token row each.
+__global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
+    const int32_t* __restrict__ ids, int T, int k, int E, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
+    int32_t* __restrict__ perm, int32_t* __restrict__ pos, int32_t* __restrict__ status, int bm,
+    MTile* __restrict__ tiles, int32_t* __restrict__ tile_count, const uint16_t* __restrict__ x, int64_t H,
+    int8_t* __restrict__ codes, float* __restrict__ scales)
+{
+    __shared__ uint32_t buf[kThreads / 64];
+    if (blockIdx.x > 0) {
+        const int64_t r = blockIdx.x - 1;
+        quantize_row<Bf16Row<kVec>, kVec, 4, true>(Bf16Row<kVec>{x + r * H}, H, codes + r * H, scales + r, buf);
+        return;
+    }
+    static_assert(kInt8SmallSlots <= kThreads && kMaxExperts <= 4 * kThreads, "one slot and four experts a thread");
+    __shared__ int id[kThreads];
+    __shared__ int begin[kMaxExperts + 1], tile_begin[kMaxExperts + 1];
+    __shared__ int hist[kMaxExperts];
+    __shared__ int wave_sum[2][kThreads / 64];
+    const int M = T * k, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int mine = tid < M ? ids[tid] : -1;
+    const bool valid = mine >= 0 && mine < E;
+    id[tid] = valid ? mine : -1;
+    for (int e = tid; e < E; e += kThreads)
+        hist[e] = 0;
+    __syncthreads();
+    if (valid)
+        atomicAdd(&hist[mine], 1);
+    int rank = 0;
+    for (int s = 0; s < M; ++s)
+        rank += s < tid && id[s] == mine ? 1 : 0;
+    __syncthreads();
+    // rows and row tiles before each expert: thread i scans experts 4 i .. 4 i + 3
+    int rows = 0, nt = 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int n = 4 * tid + q < E ? hist[4 * tid + q] : 0;
+        rows += n;
+        nt += (n + bm - 1) / bm;
+    }
+    int rows_in = rows, nt_in = nt;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int a = __shfl_up(rows_in, off), b = __shfl_up(nt_in, off);
+        rows_in += lane >= off ? a : 0;
+        nt_in += lane >= off ? b : 0;
+    }
+    if (lane == 63) {
+        wave_sum[0][wave] = rows_in;
+        wave_sum[1][wave] = nt_in;
+    }
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) {
+        rows_in += wave_sum[0][w];
+        nt_in += wave_sum[1][w];
+    }
+    rows_in -= rows;
+    nt_in -= nt;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int e = 4 * tid + q;
+        if (e < E) {
+            begin[e] = rows_in;
+            tile_begin[e] = nt_in;
+            counts[e] = hist[e];
+            offsets[e] = rows_in;
+            rows_in += hist[e];
+            nt_in += (hist[e] + bm - 1) / bm;
+            if (e == E - 1) {
+                begin[E] = rows_in;
+                offsets[E] = rows_in;
+                *tile_count = nt_in;
+                *status = rows_in == M ? MOE_OK : MOE_ERR_EXPERT_ID_OUT_OF_RANGE;
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < M) {
+        const int row = valid ? begin[mine] + rank : -1;
+        pos[tid] = row;
+        if (valid)
+            perm[row] = tid;
+        if (tid >= begin[E])
+            perm[tid] = -1;
+    }
+    for (int e = tid; e < E; e += kThreads) {
+        const int n = hist[e], R = (n + bm - 1) / bm, blocks = (n + 31) / 32;
+        int r0 = begin[e];
+        for (int i = 0; i < R; ++i) {
+            MTile mt;
+            mt.expert = e;
+            mt.row_begin = r0;
+            r0 = i == R - 1 ? begin[e] + n : r0 + 32 * (blocks / R + (i < blocks % R ? 1 : 0));
+            mt.row_end = r0;
+            mt.chunk = 0;
+            mt.run_begin = tile_begin[e];
+            mt.run_len = R;
+            mt.pad0 = mt.pad1 = 0;
+            tiles[tile_begin[e] + i] = mt;
+        }
     }
 }
 
@@ -319,9 +462,40 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
 {
     if (M <= 0)
         return hipSuccess;
-    int8_swiglu_partial_kernel<<<dim3(static_cast<unsigned>(M)), dim3(kThreads), 0, s>>>(
-        partial, splits, a_scale, gather, gather_k, sg, su, offsets, group_expert, static_cast<int>(G),
-        static_cast<int>(E), M, F, codes, scales);
+    const dim3 grid(static_cast<unsigned>(M));
+    const int g = static_cast<int>(G), e = static_cast<int>(E);
+    // few rows: a whole CU's threads for each (2 rows of 14336: 16.8 -> 6 us)
+    if (M <= 2 * device_info().cu_count)
+        int8_swiglu_partial_kernel<kWideThreads, 2><<<grid, dim3(kWideThreads), 0, s>>>(
+            partial, splits, a_scale, gather, gather_k, sg, su, offsets, group_expert, g, e, M, F, codes, scales);
+    else
+        int8_swiglu_partial_kernel<kThreads, 4><<<grid, dim3(kThreads), 0, s>>>(
+            partial, splits, a_scale, gather, gather_k, sg, su, offsets, group_expert, g, e, M, F, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_prologue(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* counts, int32_t* offsets,
+                                int32_t* perm, int32_t* pos, int32_t* status, int bm, MTile* tiles,
+                                int32_t* tile_count, const uint16_t* x, int64_t H, int8_t* codes, float* scales,
+                                hipStream_t s)
+{
+    if (T <= 0 || T * k > kInt8SmallSlots || E >= kMaxExperts)
+        return hipErrorInvalidValue;
+    int8_prologue_kernel<<<dim3(static_cast<unsigned>(x != nullptr ? T + 1 : 1)), dim3(kThreads), 0, s>>>(
+        ids, static_cast<int>(T), static_cast<int>(k), static_cast<int>(E), counts, offsets, perm, pos, status, bm, tiles,
+        tile_count, x, H, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_combine(const int32_t* partial, int splits, const float* a_scale, const float* w_scale,
+                               const int32_t* expert_ids, const int32_t* pos, const float* probs, int64_t T, int64_t k,
+                               int64_t N, uint16_t* out, hipStream_t s)
+{
+    if (T <= 0)
+        return hipSuccess;
+    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(ceil_div(N, 4 * kThreads)));
+    int8_combine_kernel<<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs,
+                                                        static_cast<int>(k), T * k, N, out);
     return hipGetLastError();
 }
 

@@ -100,7 +100,10 @@ PRODUCTS = [
     ([1000], 1152, 128),
     ([5] * 100, 128, 128),
     ([700, 0, 900], 128, 256),
-    ([2], 16384, 256),                           # K cut 16 times
+    ([2], 16384, 256),                           # K cut many times
+    ([30, 0, 64, 7], 2048, 384),                 # 64-row tiles, K cut
+    ([150, 100, 90], 1664, 256),                 # 128-row tiles, K cut into unequal parts
+    ([3] * 300, 256, 640),                       # several tasks per workgroup, one step or two each
     ([513, 256, 300], 384, 384),                 # 256-row tiles, odd numbers of K pairs and column strips
     ([900, 0, 64, 2000], 896, 1152),
     ([3000], 1024, 256),
@@ -194,7 +197,8 @@ def test_ffn(counts, H, F):
             assert np.all(np.abs(out[a:b] - y) <= slack + BF * (np.abs(y) + slack))
 
 
-LAYERS = [(1, 256, 384, 4, 2), (3, 128, 128, 1, 1), (40, 256, 256, 8, 3), (150, 128, 384, 3, 3), (900, 256, 256, 5, 2),
+LAYERS = [(1, 2048, 1024, 8, 2), (64, 256, 256, 16, 4), (65, 256, 256, 16, 4), (32, 128, 256, 1023, 8), (256, 128, 128, 3, 1),
+          (1, 256, 384, 4, 2), (3, 128, 128, 1, 1), (40, 256, 256, 8, 3), (150, 128, 384, 3, 3), (900, 256, 256, 5, 2),
           (64, 128, 128, 100, 8)]
 
 
@@ -247,6 +251,21 @@ def test_layer_drops_bad_ids_and_marks_nan_tokens():
     out = _host(mel.expert_forward_int8(x.cuda(), None, *_dev(*w), *_dev(ids, probs), workspace=ws))
     assert mel.device_status(ws) == 4
     assert np.all(out[4] == 0) and np.all(np.isnan(out[9])) and np.all(np.isfinite(np.delete(out, 9, 0)))
+
+
+@pytest.mark.parametrize("T", [1, 5, 100])
+def test_layer_rows_do_not_depend_on_the_batch(T):
+    """A token's output is the same alone (partial sums, one launch of preparation), in a small batch and
+    in a large one (another tile height and another cut of K): the sums are exact."""
+    rng = np.random.default_rng(T)
+    H, F, E, k = 512, 384, 4, 2
+    w = _dev(*_weights(rng, E, H, F))
+    x = torch.randn((700, H), device="cuda").bfloat16()
+    ids = torch.from_numpy(np.stack([rng.permutation(E)[:k] for _ in range(700)]).astype(np.int32)).cuda()
+    probs = torch.softmax(torch.randn((700, k), device="cuda"), 1)
+    whole = mel.expert_forward_int8(x, None, *w, ids, probs)
+    part = mel.expert_forward_int8(x[:T].contiguous(), None, *w, ids[:T].contiguous(), probs[:T].contiguous())
+    assert torch.equal(part, whole[:T])
 
 
 def test_gate_then_int8_layer_in_a_graph():
