@@ -480,8 +480,8 @@ moe_status run_ffn(int dtype, const void* rows, const uint8_t* rows_scale, int64
 struct Int8Layout {
     RouteLayout route;
     Int8Plan fc1{}, fc2{};
-    size_t counts = 0, offsets = 0, perm = 0, pos = 0, tile_count = 0, task_ctr = 0, tiles = 0, tiles_run = 0;
-    size_t h = 0, h_q = 0, h_scale = 0, y_part = 0, x_q = 0, x_q_scale = 0, y = 0, total = 0;
+    size_t counts = 0, offsets = 0, perm = 0, pos = 0, row_experts = 0, tile_count = 0, task_ctr = 0, tiles = 0;
+    size_t tiles_run = 0, h = 0, h_q = 0, h_scale = 0, y_part = 0, x_q = 0, x_q_scale = 0, y = 0, total = 0;
     int64_t max_tiles = 0;
 };
 
@@ -508,6 +508,7 @@ Int8Layout int8_layout(int64_t M, int64_t G, int64_t H, int64_t F, int64_t T, in
         L.offsets = take(4 * (E + 1));
         L.perm = take(4 * M);
         L.pos = take(4 * M);
+        L.row_experts = take(4 * std::min(M, kInt8SmallSlots));
         L.x_q = take(T * H);
         L.x_q_scale = take(4 * T);
         L.y = take(2 * M * H);
@@ -531,18 +532,18 @@ struct Int8Weights {
     const float *gate_scale, *up_scale, *down_scale;
 };
 
-// fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.  have_tiles: the
-// tile table is there already.  y null: the down projection's partial sums (L.fc2.partial) stay for the
+// fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.  row_experts
+// (may be null): the small layer's preparation has run, the tile table is there and each row's expert.  y null: the down projection's partial sums (L.fc2.partial) stay for the
 // caller.
 moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, const int32_t* offsets,
                         const int32_t* group_expert, int64_t G, int64_t E, int64_t H, int64_t F,
                         const Int8Weights& w, void* y, void* ws, const Int8Layout& L, bool write_status,
-                        hipStream_t s, const int32_t* gather, int gather_k, bool have_tiles)
+                        hipStream_t s, const int32_t* gather, int gather_k, const int32_t* row_experts)
 {
     int32_t* tcount = at<int32_t>(ws, L.tile_count);
     MTile* tiles = at<MTile>(ws, L.tiles_run);
     const int32_t* count = tcount + 4;
-    if (!have_tiles)
+    if (row_experts == nullptr)
         LAUNCH(s, "build_tiles",
            launch_build_tiles(offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.fc1.row_tile,
                               at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0,
@@ -555,8 +556,8 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
     if (L.fc1.partial)
         LAUNCH(s, "int8_swiglu",
                launch_int8_swiglu_partial(at<int32_t>(ws, L.h), L.fc1.splits, rows_scale, gather, gather_k,
-                                          w.gate_scale, w.up_scale, offsets, group_expert, G, E, M, F, h_q,
-                                          h_scale, s));
+                                          w.gate_scale, w.up_scale, row_experts, offsets, group_expert, G, E, M, F,
+                                          h_q, h_scale, s));
     else
         LAUNCH(s, "int8_quantize", launch_int8_quantize(MOE_F32, at<void>(ws, L.h), M, F, h_q, h_scale, s));
     LAUNCH(s, "fc2_i8",
@@ -752,7 +753,8 @@ MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, 
     const bool small = T > 0 && M <= kInt8SmallSlots && L.fc1.row_tile != 256;
     if (small) {
         LAUNCH(s, "int8_prologue",
-               launch_int8_prologue(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos, at<int32_t>(ws, 0),
+               launch_int8_prologue(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos,
+                                    at<int32_t>(ws, L.row_experts), at<int32_t>(ws, 0),
                                     L.fc1.row_tile, at<MTile>(ws, L.tiles_run), at<int32_t>(ws, L.tile_count) + 4,
                                     quantize_x ? static_cast<const uint16_t*>(x) : nullptr, H, at<int8_t>(ws, L.x_q),
                                     at<float>(ws, L.x_q_scale), s));
@@ -769,7 +771,7 @@ MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, 
     const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
     if (moe_status st = run_ffn_int8(rows, rows_scale, M, offsets, nullptr, E, E, H, F, w,
                                      L.fc2.partial ? nullptr : at<void>(ws, L.y), ws, L, false, s, perm,
-                                     static_cast<int>(k), small);
+                                     static_cast<int>(k), small ? at<int32_t>(ws, L.row_experts) : nullptr);
         st != MOE_OK)
         return st;
     if (L.fc2.partial)
@@ -1140,7 +1142,7 @@ MOE_API moe_status moe_grouped_ffn_int8(const moe_problem* p, const int8_t* rows
         return st;
     const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
     return run_ffn_int8(rows, rows_scale, M, group_offsets, group_expert, G, p->E, p->H, p->F, w, y_rows, workspace,
-                        int8_layout(M, G, p->H, p->F, 0, 1, p->E, false), true, stream, nullptr, 1, false);
+                        int8_layout(M, G, p->H, p->F, 0, 1, p->E, false), true, stream, nullptr, 1, nullptr);
 }
 
 namespace moe {

@@ -270,19 +270,20 @@ hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_sca
 // quant_i8.hip.  Rows of float32 or bfloat16 -> int8 codes and one scale per row (moe_int8_quantize).
 hipError_t launch_int8_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* codes,
                                 float* scales, hipStream_t s);
-// The rows that a group holds (offsets, group_expert as for launch_build_tiles) from the gated partial
-// sums [splits, M, 2 F]: h = swiglu(gate, up), quantised.
+// The rows that a group holds (offsets, group_expert as for launch_build_tiles; row_experts, where not
+// null, says each row's expert, -1 for none) from the gated partial sums [splits, M, 2 F]: h =
+// swiglu(gate, up), quantised.
 hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const float* a_scale,
                                       const int32_t* gather, int gather_k, const float* sg, const float* su,
-                                      const int32_t* offsets, const int32_t* group_expert, int64_t G,
-                                      int64_t E, int64_t M, int64_t F, int8_t* codes, float* scales,
+                                      const int32_t* row_experts, const int32_t* offsets,
+                                      const int32_t* group_expert, int64_t G, int64_t E, int64_t M, int64_t F, int8_t* codes, float* scales,
                                       hipStream_t s);
-// The routing (as launch_route_* leave it), the table of balanced row tiles of height bm with its count,
+// The routing (as launch_route_* leave it, and each row's expert), the table of balanced row tiles of height bm with its count,
 // and with x not null the quantised token rows, in one launch; at most kInt8SmallSlots slots.
 constexpr int64_t kInt8SmallSlots = 256;
 hipError_t launch_int8_prologue(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* counts, int32_t* offsets,
-                                int32_t* perm, int32_t* pos, int32_t* status, int bm, MTile* tiles,
-                                int32_t* tile_count, const uint16_t* x, int64_t H, int8_t* codes, float* scales,
+                                int32_t* perm, int32_t* pos, int32_t* row_experts, int32_t* status, int bm,
+                                MTile* tiles, int32_t* tile_count, const uint16_t* x, int64_t H, int8_t* codes, float* scales,
                                 hipStream_t s);
 // The layer's output [T, N] bfloat16 from the down projection's partial sums [splits, T k, N].
 hipError_t launch_int8_combine(const int32_t* partial, int splits, const float* a_scale, const float* w_scale,

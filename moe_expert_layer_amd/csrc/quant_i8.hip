@@ -206,57 +206,82 @@ __global__ __launch_bounds__(kThreads) void int8_quantize_kernel(const T* __rest
         quantize_row<Row<kV>, kV, kPer, kExactProduct>(Row<kV>{x + r * cols}, cols, codes + r * cols, scales + r, buf[slot]);
 }
 
-// The SwiGLU of a row's gate and up sums, cut by cut of K.
-struct SwigluRow {
-    const int32_t* p;      // the row in the first cut: gate [F], up [F]
-    int64_t cut;           // elements from one cut to the next
-    int splits;
-    float a_scale;
-    const float* sg;
-    const float* su;
-    int64_t F;
-    __device__ __forceinline__ void load(int64_t c, float (&v)[kVec]) const
-    {
-#pragma unroll
-        for (int q = 0; q < kVec / 4; ++q) {
-            const int64_t cc = c + 4 * q;
-            i32x4_t g = *reinterpret_cast<const i32x4_t*>(p + cc);
-            i32x4_t u = *reinterpret_cast<const i32x4_t*>(p + F + cc);
-            for (int s = 1; s < splits; ++s) {
-                g += *reinterpret_cast<const i32x4_t*>(p + s * cut + cc);
-                u += *reinterpret_cast<const i32x4_t*>(p + s * cut + F + cc);
-            }
-            const f32x4_t wg = *reinterpret_cast<const f32x4_t*>(sg + cc);
-            const f32x4_t wu = *reinterpret_cast<const f32x4_t*>(su + cc);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                v[4 * q + i] = swiglu(static_cast<float>(g[i]) * a_scale * wg[i], static_cast<float>(u[i]) * a_scale * wu[i]);
-        }
-    }
-};
-
+// The SwiGLU of a row's gate and up sums, quantised; one workgroup per row, whose sums stay in registers
+// (kPer vectors a thread; longer rows are summed again for the codes).  The sums are asked for before the
+// row's expert is looked up: row_expert where the caller has it, else the group that holds the row.
 template <int kT, int kPer>
 __global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
     const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
     const int32_t* __restrict__ gather, int gather_k, const float* __restrict__ sg, const float* __restrict__ su,
-    const int32_t* __restrict__ offsets, const int32_t* __restrict__ group_expert, int G, int E, int64_t M,
-    int64_t F, int8_t* __restrict__ codes, float* __restrict__ scales)
+    const int32_t* __restrict__ row_experts, const int32_t* __restrict__ offsets,
+    const int32_t* __restrict__ group_expert, int G, int E, int64_t M, int64_t F, int8_t* __restrict__ codes,
+    float* __restrict__ scales)
 {
     __shared__ uint32_t buf[kT / 64];
     __shared__ int found;
     const int64_t r = blockIdx.x;
-    const int e = row_expert(offsets, group_expert, G, E, M, r, &found);
+    const int32_t* p = partial + r * 2 * F;
+    const int64_t cut = M * 2 * F;
+    const auto sums = [&](int64_t c, i32x4_t (&g)[2], i32x4_t (&u)[2]) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            g[q] = *reinterpret_cast<const i32x4_t*>(p + c + 4 * q);
+            u[q] = *reinterpret_cast<const i32x4_t*>(p + F + c + 4 * q);
+        }
+        for (int s = 1; s < splits; ++s)
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                g[q] += *reinterpret_cast<const i32x4_t*>(p + s * cut + c + 4 * q);
+                u[q] += *reinterpret_cast<const i32x4_t*>(p + s * cut + F + c + 4 * q);
+            }
+    };
+    i32x4_t g[kPer][2], u[kPer][2];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int64_t c = (static_cast<int64_t>(i) * kT + threadIdx.x) * kVec;
+        if (c < F)
+            sums(c, g[i], u[i]);
+    }
+    const int e = row_experts != nullptr ? row_experts[r] : row_expert(offsets, group_expert, G, E, M, r, &found);
     if (e < 0)
         return;
-    SwigluRow src;
-    src.p = partial + r * 2 * F;
-    src.cut = M * 2 * F;
-    src.splits = splits;
-    src.a_scale = a_scale[gather != nullptr ? gather[r] / gather_k : r];
-    src.sg = sg + static_cast<int64_t>(e) * F;
-    src.su = su + static_cast<int64_t>(e) * F;
-    src.F = F;
-    quantize_row<SwigluRow, kVec, kPer, false, kT>(src, F, codes + r * F, scales + r, buf);
+    struct Values {
+        const decltype(sums)* again;
+        const i32x4_t (*g)[2];
+        const i32x4_t (*u)[2];
+        float a_scale;
+        const float* sg;
+        const float* su;
+        __device__ __forceinline__ void load(int64_t c, float (&v)[kVec]) const
+        {
+            i32x4_t gg[2], uu[2];
+            const int64_t i = c / (kT * kVec);
+            if (i < kPer) {
+#pragma unroll
+                for (int n = 0; n < kPer; ++n)
+                    if (n == i)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            gg[q] = g[n][q];
+                            uu[q] = u[n][q];
+                        }
+            } else {
+                (*again)(c, gg, uu);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const f32x4_t wg = *reinterpret_cast<const f32x4_t*>(sg + c + 4 * q);
+                const f32x4_t wu = *reinterpret_cast<const f32x4_t*>(su + c + 4 * q);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    v[4 * q + n] = swiglu(static_cast<float>(gg[q][n]) * a_scale * wg[n],
+                                          static_cast<float>(uu[q][n]) * a_scale * wu[n]);
+            }
+        }
+    };
+    const Values src{&sums, g, u, a_scale[gather != nullptr ? gather[r] / gather_k : r], sg + static_cast<int64_t>(e) * F,
+                     su + static_cast<int64_t>(e) * F};
+    quantize_row<Values, kVec, kPer, false, kT>(src, F, codes + r * F, scales + r, buf);
 }
 
 // The four columns from c of row r's product: the partial sums added up, scaled.
@@ -312,16 +337,18 @@ __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
     if (c >= N)
         return;
     f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
     for (int j = 0; j < k; ++j) {
+        // no branch on a dropped slot, so that the loads of several slots go out together
         const int64_t row = pos[t * k + j];
-        if (row < 0 || row >= M)
-            continue;
-        const int e = expert_ids[t * k + j];
-        const f32x4_t v = finish4(partial, splits, M * N, row * N + c, a_scale[row], w_scale + static_cast<int64_t>(e) * N + c);
+        const bool held = row >= 0 && row < M;
+        const int64_t at = held ? row : 0;
+        const int e = held ? expert_ids[t * k + j] : 0;
+        const f32x4_t v = finish4(partial, splits, M * N, at * N + c, a_scale[at], w_scale + static_cast<int64_t>(e) * N + c);
         const float p = probs[t * k + j];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            sum[i] = fmaf(p, bf16_to_f32(f32_to_bf16(v[i])), sum[i]);
+            sum[i] = held ? fmaf(p, bf16_to_f32(f32_to_bf16(v[i])), sum[i]) : sum[i];
     }
     *reinterpret_cast<u32x2_t*>(out + t * N + c) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
@@ -331,7 +358,8 @@ __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
 // directly) and writes the table of balanced row tiles, the others quantise a token row each.
 __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
     const int32_t* __restrict__ ids, int T, int k, int E, int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
-    int32_t* __restrict__ perm, int32_t* __restrict__ pos, int32_t* __restrict__ status, int bm,
+    int32_t* __restrict__ perm, int32_t* __restrict__ pos, int32_t* __restrict__ row_experts,
+    int32_t* __restrict__ status, int bm,
     MTile* __restrict__ tiles, int32_t* __restrict__ tile_count, const uint16_t* __restrict__ x, int64_t H,
     int8_t* __restrict__ codes, float* __restrict__ scales)
 {
@@ -407,10 +435,14 @@ __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
     if (tid < M) {
         const int row = valid ? begin[mine] + rank : -1;
         pos[tid] = row;
-        if (valid)
+        if (valid) {
             perm[row] = tid;
-        if (tid >= begin[E])
+            row_experts[row] = mine;
+        }
+        if (tid >= begin[E]) {
             perm[tid] = -1;
+            row_experts[tid] = -1;
+        }
     }
     for (int e = tid; e < E; e += kThreads) {
         const int n = hist[e], R = (n + bm - 1) / bm, blocks = (n + 31) / 32;
@@ -456,8 +488,8 @@ hipError_t launch_int8_quantize(int dtype, const void* x, int64_t rows, int64_t 
 
 hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const float* a_scale,
                                       const int32_t* gather, int gather_k, const float* sg, const float* su,
-                                      const int32_t* offsets, const int32_t* group_expert, int64_t G,
-                                      int64_t E, int64_t M, int64_t F, int8_t* codes, float* scales,
+                                      const int32_t* row_experts, const int32_t* offsets,
+                                      const int32_t* group_expert, int64_t G, int64_t E, int64_t M, int64_t F, int8_t* codes, float* scales,
                                       hipStream_t s)
 {
     if (M <= 0)
@@ -467,22 +499,22 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
     // few rows: a whole CU's threads for each (2 rows of 14336: 16.8 -> 6 us)
     if (M <= 2 * device_info().cu_count)
         int8_swiglu_partial_kernel<kWideThreads, 2><<<grid, dim3(kWideThreads), 0, s>>>(
-            partial, splits, a_scale, gather, gather_k, sg, su, offsets, group_expert, g, e, M, F, codes, scales);
+            partial, splits, a_scale, gather, gather_k, sg, su, row_experts, offsets, group_expert, g, e, M, F, codes, scales);
     else
         int8_swiglu_partial_kernel<kThreads, 4><<<grid, dim3(kThreads), 0, s>>>(
-            partial, splits, a_scale, gather, gather_k, sg, su, offsets, group_expert, g, e, M, F, codes, scales);
+            partial, splits, a_scale, gather, gather_k, sg, su, row_experts, offsets, group_expert, g, e, M, F, codes, scales);
     return hipGetLastError();
 }
 
 hipError_t launch_int8_prologue(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* counts, int32_t* offsets,
-                                int32_t* perm, int32_t* pos, int32_t* status, int bm, MTile* tiles,
-                                int32_t* tile_count, const uint16_t* x, int64_t H, int8_t* codes, float* scales,
+                                int32_t* perm, int32_t* pos, int32_t* row_experts, int32_t* status, int bm,
+                                MTile* tiles, int32_t* tile_count, const uint16_t* x, int64_t H, int8_t* codes, float* scales,
                                 hipStream_t s)
 {
     if (T <= 0 || T * k > kInt8SmallSlots || E >= kMaxExperts)
         return hipErrorInvalidValue;
     int8_prologue_kernel<<<dim3(static_cast<unsigned>(x != nullptr ? T + 1 : 1)), dim3(kThreads), 0, s>>>(
-        ids, static_cast<int>(T), static_cast<int>(k), static_cast<int>(E), counts, offsets, perm, pos, status, bm, tiles,
+        ids, static_cast<int>(T), static_cast<int>(k), static_cast<int>(E), counts, offsets, perm, pos, row_experts, status, bm, tiles,
         tile_count, x, H, codes, scales);
     return hipGetLastError();
 }
