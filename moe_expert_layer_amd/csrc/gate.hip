@@ -123,7 +123,9 @@ struct GateArgs {
     int32_t* ids;
     float* probs;
     int group_shift;         // log2 of the lanes a group's experts cover in one vector; -1: no such layout
-    int scratch;             // doubles of LDS per wave for the groups (0 without): a token's experts and groups
+    int part_shift;          // otherwise log2 of the lanes that share a group
+    int per, per_inverse;    // experts per group; e / per = e * per_inverse >> 20 for e < 1024
+    int scratch;             // doubles of LDS per wave for the groups (0 without): values of its experts and groups
 };
 
 // Unsigned integers of the order of the floats (no NaN).
@@ -311,7 +313,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
     const bool live = t < a.T;
     const In* row = logits + (live ? t : a.T - 1) * a.E;
     const bool picked = a.topk_groups < a.groups;
-    bool unsure = picked && a.group_shift < 0;                // this token needs float64
+    bool unsure = picked && a.groups > L;                     // this token needs float64
     if (!__all(unsure)) {
         float l[kPer];
 #pragma unroll
@@ -391,8 +393,81 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
             }
         }
         unsure |= reduce<L>(nan ? 1 : 0, Add{}) != 0;
-        uint32_t dropped = 0;                                 // bit i: the group of vector i is out
-        if (picked) {
+        uint32_t dropped = 0;                                 // bit q: the group of c[q] is out
+        // the n-th largest of the lanes' keys (V of them each); equal keys count once
+        const auto nth = [](const auto& keys, int V, int n) {
+            uint32_t last = 0;
+            for (int j = 0; j < n; ++j) {
+                uint32_t d = last - 1 - keys[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i)
+                    d = min(d, last - 1 - keys[i]);
+                last = last - 1 - reduce<L>(d, MinU{});
+            }
+            return last;
+        };
+        // the two largest over 1 << shift neighbouring lanes
+        const auto join = [](int shift, float& b1, float& b2) {
+            const auto with = [&](float o1, float o2) {
+                b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
+                b1 = fmaxf(b1, o1);
+            };
+            if (L > 1 && shift > 0)
+                with(exchange<0>(b1), exchange<0>(b2));
+            if (L > 2 && shift > 1)
+                with(exchange<1>(b1), exchange<1>(b2));
+            if (L > 4 && shift > 2)
+                with(exchange<2>(b1), exchange<2>(b2));
+            if (L > 8 && shift > 3)
+                with(exchange<3>(b1), exchange<3>(b2));
+        };
+        // equal scores among the kept groups, or the first one dropped not clearly below the last kept
+        const auto open = [&](uint32_t last, int kept, int lanes, float out, float size) {
+            return reduce<L>(kept, Add{}) != lanes ||
+                   !(unordered(last) - reduce<L>(out, Max{}) > 2 * score_err + 8 * u * reduce<L>(size, Max{}));
+        };
+        const auto group_score = [&](float b1, float b2, float& size) {
+            const bool two = a.group_top == 2 && b2 > -__builtin_inff();
+            size = fmaxf(size, b1 > -__builtin_inff() ? fabsf(b1) + (two ? fabsf(b2) : 0.0f) : 0.0f);
+            return two ? b1 + b2 : b1;
+        };
+        if (picked && a.group_shift < 0 && !__all(unsure)) {
+            // groups of any size: the values go to LDS, 1 << part_shift lanes read a group's
+            float* const cs = reinterpret_cast<float*>(wide) + (lane / L) * (a.E + a.groups);
+            float* const gs = cs + a.E;
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                if (4 * (L * (q / 4) + g) + q % 4 < a.E)
+                    cs[4 * (L * (q / 4) + g) + q % 4] = c[q];
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            const int grp = g >> a.part_shift, parts = 1 << a.part_shift;
+            float b1 = -__builtin_inff(), b2 = -__builtin_inff(), size = 0.0f, out = -__builtin_inff();
+            if (grp < a.groups)
+                for (int i = g & (parts - 1); i < a.per; i += parts) {
+                    const float v = cs[grp * a.per + i];
+                    b2 = fmaxf(b2, fminf(b1, v));
+                    b1 = fmaxf(b1, v);
+                }
+            join(a.part_shift, b1, b2);
+            const float mine = group_score(b1, b2, size);
+            const uint32_t gkey[1] = {grp < a.groups ? ordered(mine) : 0};
+            if (grp < a.groups)
+                gs[grp] = mine;
+            const uint32_t last = nth(gkey, 1, a.topk_groups);
+            const bool in = gkey[0] >= last;
+            if (!in && grp < a.groups)
+                out = mine;
+            unsure |= open(last, in ? 1 : 0, a.topk_groups << a.part_shift, out, size);
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+            __builtin_amdgcn_wave_barrier();
+            const float least = unordered(last);
+#pragma unroll
+            for (int q = 0; q < kPer; ++q) {
+                const int e = min(4 * (L * (q / 4) + g) + q % 4, a.E - 1);
+                dropped |= gs[e * a.per_inverse >> 20] >= least ? 0u : 1u << q;
+            }
+        } else if (picked) {
             // a group is an aligned run of 1 << group_shift lanes of one vector
             float mine[I], size = 0.0f;
             uint32_t gkey[I];
@@ -401,32 +476,11 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 const float h1 = fmaxf(c[4 * i], c[4 * i + 1]), l1 = fminf(c[4 * i], c[4 * i + 1]);
                 const float h2 = fmaxf(c[4 * i + 2], c[4 * i + 3]), l2 = fminf(c[4 * i + 2], c[4 * i + 3]);
                 float b1 = fmaxf(h1, h2), b2 = fmaxf(fminf(h1, h2), h1 >= h2 ? l1 : l2);
-                const auto join = [&](float o1, float o2) {
-                    b2 = fmaxf(fminf(b1, o1), fmaxf(b2, o2));
-                    b1 = fmaxf(b1, o1);
-                };
-                if (L > 1 && a.group_shift > 0)
-                    join(exchange<0>(b1), exchange<0>(b2));
-                if (L > 2 && a.group_shift > 1)
-                    join(exchange<1>(b1), exchange<1>(b2));
-                if (L > 4 && a.group_shift > 2)
-                    join(exchange<2>(b1), exchange<2>(b2));
-                if (L > 8 && a.group_shift > 3)
-                    join(exchange<3>(b1), exchange<3>(b2));
-                const bool two = a.group_top == 2 && b2 > -__builtin_inff();
-                mine[i] = two ? b1 + b2 : b1;
-                size = fmaxf(size, b1 > -__builtin_inff() ? fabsf(b1) + (two ? fabsf(b2) : 0.0f) : 0.0f);
+                join(a.group_shift, b1, b2);
+                mine[i] = group_score(b1, b2, size);
                 gkey[i] = (L * i + g) >> a.group_shift < a.groups ? ordered(mine[i]) : 0;
             }
-            // the topk_groups-th largest score, as the experts' keys below; equal scores count once
-            uint32_t last = 0;
-            for (int j = 0; j < a.topk_groups; ++j) {
-                uint32_t d = last - 1 - gkey[0];
-#pragma unroll
-                for (int i = 1; i < I; ++i)
-                    d = min(d, last - 1 - gkey[i]);
-                last = last - 1 - reduce<L>(d, MinU{});
-            }
+            const uint32_t last = nth(gkey, I, a.topk_groups);
             float out = -__builtin_inff();
             int kept = 0;
 #pragma unroll
@@ -434,16 +488,11 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 if (gkey[i] >= last) {
                     ++kept;
                 } else {
-                    dropped |= 1u << i;
+                    dropped |= 15u << (4 * i);
                     out = fmaxf(out, gkey[i] != 0 ? mine[i] : -__builtin_inff());
                 }
             }
-            kept = reduce<L>(kept, Add{});
-            out = reduce<L>(out, Max{});
-            size = reduce<L>(size, Max{});
-            // equal scores among those kept, or the first one dropped not clearly below the last kept
-            unsure |= kept != a.topk_groups << a.group_shift ||
-                      !(unordered(last) - out > 2 * score_err + 8 * u * size);
+            unsure |= open(last, kept, a.topk_groups << a.group_shift, out, size);
         }
         const bool id_key = std::is_same_v<In, uint16_t> && by_logit;
         uint32_t key[kPer];                                   // 0: no candidate
@@ -453,7 +502,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
             key[q] = id_key ? (o & 0xffff0000u) | static_cast<uint32_t>(0xffff - (4 * (L * (q / 4) + g) + q % 4))
                             : (o & ~kPlace) | static_cast<uint32_t>(q);
             if (picked)
-                key[q] = (dropped >> (q / 4) & 1) != 0 ? 0 : key[q];
+                key[q] = (dropped >> q & 1) != 0 ? 0 : key[q];
         }
         uint32_t last = 0;                                    // below every key: M - 1 wraps to the top
         int wins = 0;
@@ -692,7 +741,13 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
         return hipErrorInvalidValue;
     const dim3 grid(static_cast<unsigned>(blocks));
     a.group_shift = group_shift(a.E / a.groups, L);
-    a.scratch = a.groups > 1 ? a.E + a.groups : 0;
+    a.per = a.E / a.groups;
+    a.per_inverse = ((1 << 20) + a.per - 1) / a.per;      // 1023 * 2^-20 < 1 / per: exact
+    a.part_shift = 0;
+    while (a.part_shift < 4 && (a.groups << (a.part_shift + 1)) <= L)
+        ++a.part_shift;
+    // one token in float64, or the wave's tokens in float32
+    a.scratch = a.groups > 1 ? std::max(1, 32 / L) * (a.E + a.groups) : 0;
     const size_t lds = sizeof(double) * kWavesPerBlock * static_cast<size_t>(a.scratch) +
                        sizeof(uint2) * (kThreads / L) * static_cast<size_t>(a.k + 1);
     const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(In)) == 0;
@@ -713,7 +768,9 @@ hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
     const int few = a.E <= 8 ? 2 : a.E <= 16 ? 4 : a.E <= 32 ? 8 : a.E <= 64 ? 16 : a.E <= 128 ? 32 : 64;
     const int lanes = a.E <= 16 ? 1 : a.E <= 32 ? 2 : a.E <= 64 ? 4 : a.E <= 128 ? 8 : a.E <= 256 ? 16 : 32;
     const int per = a.E / a.groups;
-    const bool fits = a.topk_groups == a.groups || group_shift(per, lanes) >= 0 || group_shift(per, few) < 0;
+    // groups as vectors, or at least no more groups than lanes, if the few-token layout can have that
+    const bool fits = a.topk_groups == a.groups || group_shift(per, lanes) >= 0 ||
+                      (group_shift(per, few) < 0 && (a.groups <= lanes || a.groups > few));
     const bool many = fits && ceil_div(a.T * few, 64) >= 8 * device_info().cu_count;
     if (a.E <= 8)
         return many ? launch_gate_n<In, 1, 2>(logits, a, s) : launch_gate_n<In, 2, 1>(logits, a, s);
