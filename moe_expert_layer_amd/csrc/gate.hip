@@ -53,13 +53,13 @@ template <int S>
 __device__ __forceinline__ int exchange(int v)
 {
     if constexpr (S == 0)
-        return __builtin_amdgcn_update_dpp(v, v, 0xB1, 0xf, 0xf, false);       // quad_perm 1 0 3 2
+        return __builtin_amdgcn_mov_dpp(v, 0xB1, 0xf, 0xf, true);       // quad_perm 1 0 3 2
     else if constexpr (S == 1)
-        return __builtin_amdgcn_update_dpp(v, v, 0x4E, 0xf, 0xf, false);       // quad_perm 2 3 0 1
+        return __builtin_amdgcn_mov_dpp(v, 0x4E, 0xf, 0xf, true);       // quad_perm 2 3 0 1
     else if constexpr (S == 2)
-        return __builtin_amdgcn_update_dpp(v, v, 0x141, 0xf, 0xf, false);      // row_half_mirror
+        return __builtin_amdgcn_mov_dpp(v, 0x141, 0xf, 0xf, true);      // row_half_mirror
     else
-        return __builtin_amdgcn_update_dpp(v, v, 0x140, 0xf, 0xf, false);      // row_mirror
+        return __builtin_amdgcn_mov_dpp(v, 0x140, 0xf, 0xf, true);      // row_mirror
 }
 template <int S>
 __device__ __forceinline__ float exchange(float v)
@@ -393,7 +393,11 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
             }
         }
         unsure |= reduce<L>(nan ? 1 : 0, Add{}) != 0;
-        uint32_t dropped = 0;                                 // bit q: the group of c[q] is out
+        uint32_t keep[I];                                     // per vector: all ones, or 0 if its group is out
+        uint32_t dropped = 0;                                 // bit q: the group of c[q] alone is out
+#pragma unroll
+        for (int i = 0; i < I; ++i)
+            keep[i] = ~0u;
         // the n-th largest of the lanes' keys (V of them each); equal keys count once
         const auto nth = [](const auto& keys, int V, int n) {
             uint32_t last = 0;
@@ -488,7 +492,7 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
                 if (gkey[i] >= last) {
                     ++kept;
                 } else {
-                    dropped |= 15u << (4 * i);
+                    keep[i] = 0;
                     out = fmaxf(out, gkey[i] != 0 ? mine[i] : -__builtin_inff());
                 }
             }
@@ -501,8 +505,16 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
             const uint32_t o = ordered(by_logit ? l[q] + 0.0f : c[q]);   // -0 becomes +0: equal logits tie
             key[q] = id_key ? (o & 0xffff0000u) | static_cast<uint32_t>(0xffff - (4 * (L * (q / 4) + g) + q % 4))
                             : (o & ~kPlace) | static_cast<uint32_t>(q);
-            if (picked)
-                key[q] = (dropped >> q & 1) != 0 ? 0 : key[q];
+        }
+        if (picked) {
+#pragma unroll
+            for (int q = 0; q < kPer; ++q)
+                key[q] &= keep[q / 4];
+            if (a.group_shift < 0) {
+#pragma unroll
+                for (int q = 0; q < kPer; ++q)
+                    key[q] &= (dropped >> q & 1) - 1;
+            }
         }
         uint32_t last = 0;                                    // below every key: M - 1 wraps to the top
         int wins = 0;
