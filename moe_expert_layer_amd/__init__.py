@@ -9,6 +9,7 @@ the library is missing, every call raises: there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -577,11 +578,11 @@ def int8_quantize(x):
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
+@functools.lru_cache(maxsize=256)
 def _gate(score, renormalize, groups, topk_groups, group_top, scale):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
-    return MoeGate(_SCORES[score], 1 if renormalize else 0, int(groups), int(topk_groups), int(group_top),
-                   float(scale))
+    return MoeGate(_SCORES[score], renormalize, groups, topk_groups, group_top, scale)
 
 
 def router_gate(logits, k: int, score: str = "softmax", bias=None, groups: int = 1, topk_groups: int = 1,
@@ -596,7 +597,7 @@ def router_gate(logits, k: int, score: str = "softmax", bias=None, groups: int =
     T, E = logits.shape
     if bias is not None:
         _need(bias, "bias", torch.float32, (E,), logits.device)
-    gate = _gate(score, renormalize, groups, topk_groups, group_top, scale)
+    gate = _gate(score, int(bool(renormalize)), int(groups), int(topk_groups), int(group_top), float(scale))
     k = int(k)
     ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
     probs = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
@@ -615,7 +616,7 @@ def router_gate_backward(logits, expert_ids, dprobs, score: str = "softmax", ren
     k = expert_ids.shape[1]
     _need(expert_ids, "expert_ids", torch.int32, (T, k), logits.device)
     _need(dprobs, "dprobs", torch.float32, (T, k), logits.device)
-    gate = _gate(score, renormalize, 1, 1, 2, scale)
+    gate = _gate(score, int(bool(renormalize)), 1, 1, 2, float(scale))
     dlogits = torch.empty_like(logits)
     _call("moe_router_gate_backward", logits.device,
           ctypes.byref(gate), _ptr(logits), dt, T, E, k, _ptr(expert_ids), _ptr(dprobs), _ptr(dlogits),

@@ -17,6 +17,7 @@
 #include <string>
 #include <vector>
 
+#include "int8_gate.h"
 #include "internal.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
@@ -211,17 +212,37 @@ moe_status check_problem(const moe_problem* p, bool need_tokens, bool gemm = tru
     return MOE_OK;
 }
 
+constexpr int64_t kInt8MaxGroups = int64_t{1} << 24;
+
+moe_status check_int8_tasks(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gated)
+{
+    return int8_tasks_fit(p, M, G, N, gated) ? MOE_OK
+                                             : fail(MOE_ERR_UNSUPPORTED, "too many tiles for 32-bit task numbers");
+}
+
 // Sizes of an int8 grouped product.
 moe_status check_int8_product(int64_t M, int64_t G, int64_t E, int64_t K, int64_t N)
 {
     if (M < 0 || G <= 0 || E <= 0 || K <= 0 || N <= 0)
         return fail(MOE_ERR_INVALID_ARGUMENT, "bad int8 product sizes");
-    if (M > INT32_MAX || G > INT32_MAX || E >= kMaxExperts)
-        return fail(MOE_ERR_UNSUPPORTED, "int8 products need M and G below 2^31 and E below %d", kMaxExperts);
+    if (M > INT32_MAX || G > kInt8MaxGroups || E >= kMaxExperts)
+        return fail(MOE_ERR_UNSUPPORTED, "int8 products need M < 2^31, G <= %lld and E < %d", (long long)kInt8MaxGroups,
+                    kMaxExperts);
     if (!int8_supported(K, N) || N > MOE_MAX_HIDDEN)
         return fail(MOE_ERR_UNSUPPORTED, "int8 products need K and N multiples of 128, K <= %lld, N <= %d",
                     (long long)kInt8MaxK, MOE_MAX_HIDDEN);
-    return MOE_OK;
+    return check_int8_tasks(int8_plan(M, G, K, N, false, K), M, G, N, false);
+}
+
+// The two products of the FFN on M rows in G groups.
+moe_status check_int8_ffn(const moe_problem* p, int64_t M, int64_t G)
+{
+    if (G > kInt8MaxGroups)
+        return fail(MOE_ERR_UNSUPPORTED, "int8 products need G <= %lld", (long long)kInt8MaxGroups);
+    const int64_t least = std::min(p->H, p->F);
+    if (moe_status st = check_int8_tasks(int8_plan(M, G, p->H, p->F, true, least), M, G, p->F, true); st != MOE_OK)
+        return st;
+    return check_int8_tasks(int8_plan(M, G, p->F, p->H, false, least), M, G, p->H, false);
 }
 
 // A problem of the int8 layer or grouped FFN.
@@ -251,6 +272,7 @@ moe_status check_int8_problem(const moe_problem* p, bool need_tokens)
             return fail(MOE_ERR_UNSUPPORTED, "T * k exceeds int32 indexing");
         if (p->T * p->H > UINT32_MAX)
             return fail(MOE_ERR_UNSUPPORTED, "int8 needs T * H < 2^32");
+        return check_int8_ffn(p, p->T * p->k, p->E);
     }
     return MOE_OK;
 }
@@ -1054,8 +1076,8 @@ MOE_API moe_status moe_grouped_ffn_workspace_size(const moe_problem* p, int64_t 
     if (p != nullptr && p->dtype == MOE_INT8) {
         if (moe_status st = check_int8_problem(p, false); st != MOE_OK)
             return st;
-        if (G > INT32_MAX)
-            return fail(MOE_ERR_INVALID_ARGUMENT, "bad grouped sizes");
+        if (moe_status st = check_int8_ffn(p, M, G); st != MOE_OK)
+            return st;
         *bytes = int8_layout(M, G, p->H, p->F, 0, 1, p->E, false).total;
         return MOE_OK;
     }

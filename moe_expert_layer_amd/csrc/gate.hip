@@ -16,8 +16,7 @@
 #include <type_traits>
 
 #include "common.h"
-#include "internal.h"
-#include "moe_expert_layer.h"
+#include "int8_gate.h"
 
 namespace moe {
 namespace {
@@ -745,13 +744,13 @@ int group_shift(int per, int L)
     return -1;
 }
 
+// Tokens of one launch: at most 2^30 threads.
+template <int L>
+constexpr int64_t kLaunchTokens = (int64_t{1} << 30) / L;
+
 template <class In, int L, int I>
 hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
 {
-    const int64_t blocks = ceil_div(a.T * L, kThreads);
-    if (blocks >= (int64_t{1} << 31))
-        return hipErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks));
     a.group_shift = group_shift(a.E / a.groups, L);
     a.per = a.E / a.groups;
     a.per_inverse = ((1 << 20) + a.per - 1) / a.per;      // 1023 * 2^-20 < 1 / per: exact
@@ -759,15 +758,25 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
     while (a.part_shift < 4 && (a.groups << (a.part_shift + 1)) <= L)
         ++a.part_shift;
     // one token in float64, or the wave's tokens in float32
-    a.scratch = a.groups > 1 ? std::max(1, 32 / L) * (a.E + a.groups) : 0;
+    const bool wave = a.group_shift < 0 && a.groups <= L;
+    a.scratch = a.groups > 1 ? (wave ? std::max(1, 32 / L) : 1) * (a.E + a.groups) : 0;
     const size_t lds = sizeof(double) * kWavesPerBlock * static_cast<size_t>(a.scratch) +
                        sizeof(uint2) * (kThreads / L) * static_cast<size_t>(a.k + 1);
     const bool vec = a.E % 4 == 0 && reinterpret_cast<uintptr_t>(logits) % (4 * sizeof(In)) == 0;
-    if (vec)
-        gate_kernel<In, L, I, true><<<grid, dim3(kThreads), lds, s>>>(logits, a);
-    else
-        gate_kernel<In, L, I, false><<<grid, dim3(kThreads), lds, s>>>(logits, a);
-    return hipGetLastError();
+    const int64_t T = a.T;
+    for (int64_t t = 0; t < T; t += kLaunchTokens<L>) {
+        a.T = std::min(kLaunchTokens<L>, T - t);
+        const dim3 grid(static_cast<unsigned>(ceil_div(a.T * L, kThreads)));
+        if (vec)
+            gate_kernel<In, L, I, true><<<grid, dim3(kThreads), lds, s>>>(logits + t * a.E, a);
+        else
+            gate_kernel<In, L, I, false><<<grid, dim3(kThreads), lds, s>>>(logits + t * a.E, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        a.ids += a.T * a.k;
+        a.probs += a.T * a.k;
+    }
+    return hipSuccess;
 }
 
 // The gate's lanes per token.  Few tokens: four experts a lane (shortest rounds).  Many: up to 16 experts
@@ -802,19 +811,24 @@ hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
 }
 
 template <class In, int L>
-hipError_t launch_backward_n(const In* logits, In* dlogits, const GateBackwardArgs& a, hipStream_t s)
+hipError_t launch_backward_n(const In* logits, In* dlogits, GateBackwardArgs a, hipStream_t s)
 {
-    const int64_t blocks = ceil_div(a.T * L, kThreads);
-    if (blocks >= (int64_t{1} << 31))
-        return hipErrorInvalidValue;
-    const dim3 grid(static_cast<unsigned>(blocks));
     const size_t lds = sizeof(float) * (kThreads / L) * static_cast<size_t>((a.E + 3) & ~3);
     const bool vec = a.E % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(dlogits)) % (4 * sizeof(In)) == 0;
-    if (vec)
-        gate_backward_kernel<In, L, true><<<grid, dim3(kThreads), lds, s>>>(logits, dlogits, a);
-    else
-        gate_backward_kernel<In, L, false><<<grid, dim3(kThreads), lds, s>>>(logits, dlogits, a);
-    return hipGetLastError();
+    const int64_t T = a.T;
+    for (int64_t t = 0; t < T; t += kLaunchTokens<L>) {
+        a.T = std::min(kLaunchTokens<L>, T - t);
+        const dim3 grid(static_cast<unsigned>(ceil_div(a.T * L, kThreads)));
+        if (vec)
+            gate_backward_kernel<In, L, true><<<grid, dim3(kThreads), lds, s>>>(logits + t * a.E, dlogits + t * a.E, a);
+        else
+            gate_backward_kernel<In, L, false><<<grid, dim3(kThreads), lds, s>>>(logits + t * a.E, dlogits + t * a.E, a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+        a.ids += a.T * a.k;
+        a.dprobs += a.T * a.k;
+    }
+    return hipSuccess;
 }
 
 // Lanes per token: one per slot, and one per 16 experts.
@@ -847,8 +861,10 @@ hipError_t launch_gate(const moe_gate& o, const void* logits, int dtype, const f
     a.T = T;
     a.E = static_cast<int>(E);
     a.k = static_cast<int>(k);
-    a.groups = o.groups;
-    a.topk_groups = o.topk_groups;
+    // groups of one expert each choose nothing that the k largest do not
+    const bool alone = o.groups == E;
+    a.groups = alone ? 1 : o.groups;
+    a.topk_groups = alone ? 1 : o.topk_groups;
     a.group_top = o.group_top;
     a.sigmoid = o.score == MOE_SCORE_SIGMOID;
     a.renormalize = o.renormalize;

@@ -21,7 +21,7 @@
 #include <utility>
 
 #include "gemm_common.h"
-#include "moe_expert_layer.h"
+#include "int8_gate.h"
 
 namespace moe {
 namespace {
@@ -883,6 +883,12 @@ Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int64
     }
     p.partial = p.splits > 1 || (gated && p.row_tile == 64);
     return p;
+}
+
+bool int8_tasks_fit(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gated)
+{
+    // the loops over tasks step by the grid and decode_task multiplies back: kept well below 2^31
+    return max_mtiles(M, G, 0, p.row_tile) * ceil_div(N, gated ? i8::BNB / 2 : i8::BNB) * p.splits < (int64_t{1} << 30);
 }
 
 hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_scale, const int8_t* w0,

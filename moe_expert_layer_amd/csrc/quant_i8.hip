@@ -10,8 +10,7 @@
 #include <algorithm>
 
 #include "common.h"
-#include "internal.h"
-#include "moe_expert_layer.h"
+#include "int8_gate.h"
 
 namespace moe {
 namespace {
@@ -20,6 +19,20 @@ constexpr int kThreads = 256;       // of most kernels; one row's quantisation t
 constexpr int kWideThreads = 1024;
 constexpr int kVec = 8;
 constexpr uint32_t kInfBits = 0x7f800000u;
+
+// Rows (workgroups) along the grid's first axis: a launch takes less than 2^32 threads along one.  More
+// rows continue along the third axis.
+constexpr int64_t kGridRows = int64_t{1} << 21;
+
+dim3 row_grid(int64_t rows, int64_t columns = 1)
+{
+    const int64_t x = std::min(rows, kGridRows);
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(columns), static_cast<unsigned>(ceil_div(rows, x)));
+}
+__device__ __forceinline__ int64_t grid_row()
+{
+    return static_cast<int64_t>(blockIdx.z) * gridDim.x + blockIdx.x;
+}
 
 // A row's constants: y = x * 2^-e lies in (-2, 2).
 struct RowCode {
@@ -219,7 +232,9 @@ __global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
 {
     __shared__ uint32_t buf[kT / 64];
     __shared__ int found;
-    const int64_t r = blockIdx.x;
+    const int64_t r = grid_row();
+    if (r >= M)
+        return;
     const int32_t* p = partial + r * 2 * F;
     const int64_t cut = M * 2 * F;
     const auto sums = [&](int64_t c, i32x4_t (&g)[2], i32x4_t (&u)[2]) {
@@ -307,7 +322,9 @@ __global__ __launch_bounds__(kThreads) void int8_finish_kernel(
     const int32_t* __restrict__ group_expert, int G, int E, int64_t M, int64_t N, void* __restrict__ out)
 {
     __shared__ int found;
-    const int64_t r = blockIdx.x;
+    const int64_t r = grid_row();
+    if (r >= M)
+        return;
     const int e = row_expert(offsets, group_expert, G, E, M, r, &found);
     if (e < 0)
         return;
@@ -330,11 +347,11 @@ __global__ __launch_bounds__(kThreads) void int8_finish_kernel(
 __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
     const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
     const float* __restrict__ w_scale, const int32_t* __restrict__ expert_ids, const int32_t* __restrict__ pos,
-    const float* __restrict__ probs, int k, int64_t M, int64_t N, uint16_t* __restrict__ out)
+    const float* __restrict__ probs, int64_t T, int k, int64_t M, int64_t N, uint16_t* __restrict__ out)
 {
-    const int64_t t = blockIdx.x;
+    const int64_t t = grid_row();
     const int64_t c = 4 * (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x);
-    if (c >= N)
+    if (t >= T || c >= N)
         return;
     f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
@@ -465,7 +482,7 @@ __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
 template <class T, template <int> class Row, bool kExactProduct>
 hipError_t launch_quantize(const T* x, int64_t rows, int64_t cols, int8_t* codes, float* scales, hipStream_t s)
 {
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>(rows, int64_t{1} << 30));
+    const unsigned grid = static_cast<unsigned>(std::min(rows, kGridRows));
     const bool aligned = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
     if (cols % kVec == 0 && aligned)
         int8_quantize_kernel<T, Row, kVec, 4, kExactProduct><<<dim3(grid), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
@@ -494,7 +511,7 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
 {
     if (M <= 0)
         return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(M));
+    const dim3 grid = row_grid(M);
     const int g = static_cast<int>(G), e = static_cast<int>(E);
     // few rows: a whole CU's threads for each (2 rows of 14336: 16.8 -> 6 us)
     if (M <= 2 * device_info().cu_count)
@@ -525,8 +542,8 @@ hipError_t launch_int8_combine(const int32_t* partial, int splits, const float* 
 {
     if (T <= 0)
         return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(T), static_cast<unsigned>(ceil_div(N, 4 * kThreads)));
-    int8_combine_kernel<<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs,
+    const dim3 grid = row_grid(T, ceil_div(N, 4 * kThreads));
+    int8_combine_kernel<<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs, T,
                                                         static_cast<int>(k), T * k, N, out);
     return hipGetLastError();
 }
@@ -537,7 +554,7 @@ hipError_t launch_int8_finish(const int32_t* partial, int splits, const float* a
 {
     if (M <= 0)
         return hipSuccess;
-    const dim3 grid(static_cast<unsigned>(M), static_cast<unsigned>(std::min<int64_t>(ceil_div(N, 4 * kThreads), 16)));
+    const dim3 grid = row_grid(M, std::min<int64_t>(ceil_div(N, 4 * kThreads), 16));
     if (out_dtype == MOE_F32)
         int8_finish_kernel<false><<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, offsets, group_expert,
                                                                   static_cast<int>(G), static_cast<int>(E), M, N, out);

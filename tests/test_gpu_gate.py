@@ -59,7 +59,8 @@ CASES = [(1, 1, 1, 1, 1), (1, 256, 8, 8, 4), (7, 3, 3, 1, 1), (33, 65, 5, 5, 2),
          (20, 200, 16, 4, 4), (9, 1024, 64, 16, 8), (5, 1023, 33, 3, 1), (300, 8, 2, 4, 2), (17, 16, 4, 16, 5),
          (40, 30, 3, 2, 1), (11, 512, 10, 512, 77), (0, 8, 2, 1, 1), (70, 8, 3, 2, 1), (70, 16, 3, 4, 2),
          (50, 32, 5, 8, 3), (50, 64, 6, 16, 4), (40, 36, 4, 2, 1), (40, 148, 7, 4, 3),
-         (40, 248, 9, 8, 5), (40, 511, 9, 7, 2), (20, 1000, 12, 8, 3), (30, 250, 5, 50, 9), (30, 9, 3, 3, 2), (50, 128, 8, 2, 1), (30, 512, 12, 8, 3), (6, 700, 9, 1, 1)]
+         (40, 248, 9, 8, 5), (40, 511, 9, 7, 2), (20, 1000, 12, 8, 3), (30, 250, 5, 50, 9), (30, 9, 3, 3, 2), (6, 1024, 64, 512, 40),
+         (6, 1024, 7, 1024, 20), (20, 16, 16, 16, 16), (12, 8, 3, 8, 5), (50, 128, 8, 2, 1), (30, 512, 12, 8, 3), (6, 700, 9, 1, 1)]
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
@@ -80,7 +81,7 @@ def test_gate(T, E, k, groups, topk_groups, score):
                                                      (30, 5, 1, 1, 20000), (64, 8, 8, 3, 9000), (128, 8, 4, 2, 5000),
                                                      (256, 8, 8, 4, 3001), (256, 8, 4, 2, 3000), (256, 6, 1, 1, 2500),
                                                      (500, 10, 1, 1, 2100), (120, 6, 8, 3, 5000), (74, 5, 2, 1, 6000),
-                                                     (15, 3, 5, 2, 40000), (336, 8, 4, 2, 2100), (250, 6, 2, 1, 2500), (1024, 8, 32, 4, 2100), (64, 64, 1, 1, 9000)])
+                                                     (15, 3, 5, 2, 40000), (16, 16, 16, 16, 40000), (16, 8, 8, 6, 40000), (336, 8, 4, 2, 2100), (250, 6, 2, 1, 2500), (1024, 8, 32, 4, 2100), (64, 64, 1, 1, 9000)])
 def test_gate_of_many_tokens(E, k, groups, topk_groups, T):
     """Enough tokens for the layouts that share a wave among more of them; against the same gate on
     slices of few tokens, whose layout is another: ids equal, weights within both layouts' bound."""

@@ -237,6 +237,58 @@ def test_layer(T, H, F, E, k):
     assert torch.equal(mel.expert_forward_int8(x.cuda(), None, *wd, idd, pd, workspace=ws), out)
 
 
+def test_no_tokens_and_no_rows():
+    rng = np.random.default_rng(0)
+    w = _dev(*_weights(rng, 2, 128, 256))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    x = torch.empty((0, 128), dtype=torch.bfloat16, device="cuda")
+    out = mel.expert_forward_int8(x, None, *w, torch.empty((0, 2), **i32), torch.empty((0, 2), device="cuda"))
+    assert out.shape == (0, 128)
+    off, ex = torch.zeros(3, **i32), torch.arange(2, **i32)
+    y = mel.grouped_ffn_int8(torch.empty((0, 128), dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda"), off, ex, *w)
+    assert y.shape == (0, 128)
+    # rows, but no group holds any
+    y = torch.full((5, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+    mel.grouped_ffn_int8(torch.ones((5, 128), dtype=torch.int8, device="cuda"), torch.ones(5, device="cuda"), off, ex, *w, out=y)
+    assert torch.all(y == 3.0)
+
+
+def test_one_expert_in_every_slot_of_a_token():
+    """A token may name an expert twice: both slots count."""
+    rng = np.random.default_rng(5)
+    T, H, F, E, k = 30, 128, 128, 3, 2
+    w = _weights(rng, E, H, F)
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).bfloat16()
+    ids = np.full((T, k), 1, np.int32)
+    ids[::3] = [[0, 2]]
+    probs = rng.dirichlet(np.ones(k), T).astype(np.float32)
+    q, s = ref.quantize(x.float().numpy())
+    r, tol = _layer_ref(q, s, w, ids, probs)
+    out = _host(mel.expert_forward_int8(x.cuda(), None, *_dev(*w), *_dev(ids, probs)))
+    assert np.all(np.abs(out - r) <= tol + 4 * U * np.abs(r))
+
+
+def test_two_streams_at_once():
+    """Two layer calls in flight on two streams, each on its own workspace."""
+    rng = np.random.default_rng(7)
+    T, H, F, E, k = 400, 512, 512, 4, 2
+    w = _dev(*_weights(rng, E, H, F))
+    xs = [torch.randn((T, H), device="cuda").bfloat16() for _ in range(2)]
+    ids = torch.from_numpy(np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)).cuda()
+    probs = torch.softmax(torch.randn((T, k), device="cuda"), 1)
+    alone = [mel.expert_forward_int8(x, None, *w, ids, probs) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = []
+    for _ in range(3):
+        for x, s in zip(xs, streams):
+            with torch.cuda.stream(s):
+                outs.append(mel.expert_forward_int8(x, None, *w, ids, probs))
+    torch.cuda.synchronize()
+    for i, o in enumerate(outs):
+        assert torch.equal(o, alone[i % 2])
+
+
 def test_layer_drops_bad_ids_and_marks_nan_tokens():
     rng = np.random.default_rng(6)
     T, H, F, E, k = 50, 128, 256, 4, 2

@@ -45,6 +45,9 @@ def test_int8_calls_refuse_before_enqueue(mel):
     assert size(100, 4, 256, 128, ctypes.byref(n)) == 0
     assert size(-1, 4, 256, 128, ctypes.byref(n)) == 1 and size(1, 0, 256, 128, ctypes.byref(n)) == 1
     assert size(1, 1, 64, 128, ctypes.byref(n)) == 2 and size(1, 1, 128, 130, ctypes.byref(n)) == 2
+    assert size(1, (1 << 24) + 1, 128, 128, ctypes.byref(n)) == 2
+    # 2^24 row tiles x 2^14 column tiles: more tasks than 32 bits number
+    assert size((1 << 31) - 1, 1 << 24, 128, 1 << 22, ctypes.byref(n)) == 2
     assert size(1, 1, 131072, 128, ctypes.byref(n)) == 2 and size(1 << 31, 1, 128, 128, ctypes.byref(n)) == 2
     size(100, 4, 256, 128, ctypes.byref(n))
     call = lib.moe_grouped_matmul_int8
