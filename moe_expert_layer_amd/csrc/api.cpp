@@ -231,7 +231,7 @@ moe_status check_int8_product(int64_t M, int64_t G, int64_t E, int64_t K, int64_
     if (!int8_supported(K, N) || N > MOE_MAX_HIDDEN)
         return fail(MOE_ERR_UNSUPPORTED, "int8 products need K and N multiples of 128, K <= %lld, N <= %d",
                     (long long)kInt8MaxK, MOE_MAX_HIDDEN);
-    return check_int8_tasks(int8_plan(M, G, K, N, false, K), M, G, N, false);
+    return check_int8_tasks(int8_plan(M, G, K, N), M, G, N, false);
 }
 
 // The two products of the FFN on M rows in G groups.
@@ -239,10 +239,11 @@ moe_status check_int8_ffn(const moe_problem* p, int64_t M, int64_t G)
 {
     if (G > kInt8MaxGroups)
         return fail(MOE_ERR_UNSUPPORTED, "int8 products need G <= %lld", (long long)kInt8MaxGroups);
-    const int64_t least = std::min(p->H, p->F);
-    if (moe_status st = check_int8_tasks(int8_plan(M, G, p->H, p->F, true, least), M, G, p->F, true); st != MOE_OK)
+    Int8Plan fc1{}, fc2{};
+    int8_ffn_plans(M, G, p->H, p->F, fc1, fc2);
+    if (moe_status st = check_int8_tasks(fc1, M, G, p->F, true); st != MOE_OK)
         return st;
-    return check_int8_tasks(int8_plan(M, G, p->F, p->H, false, least), M, G, p->H, false);
+    return check_int8_tasks(fc2, M, G, p->H, false);
 }
 
 // A problem of the int8 layer or grouped FFN.
@@ -520,8 +521,7 @@ struct Take {
 Int8Layout int8_layout(int64_t M, int64_t G, int64_t H, int64_t F, int64_t T, int64_t k, int64_t E, bool layer)
 {
     Int8Layout L;
-    L.fc1 = int8_plan(M, G, H, F, true, std::min(H, F));
-    L.fc2 = int8_plan(M, G, F, H, false, std::min(H, F));
+    int8_ffn_plans(M, G, H, F, L.fc1, L.fc2);
     Take take{kAlign};                                        // the status word
     if (layer) {
         L.route = route_layout(T, k, E, 0);
@@ -1179,7 +1179,7 @@ struct MatmulLayout {
 MatmulLayout matmul_layout(int64_t M, int64_t G, int64_t K, int64_t N)
 {
     MatmulLayout L;
-    L.plan = int8_plan(M, G, K, N, false, K);
+    L.plan = int8_plan(M, G, K, N);
     L.max_tiles = max_mtiles(M, G, 0, L.plan.row_tile);
     Take take{kAlign};
     L.tile_count = take(8 * 4);

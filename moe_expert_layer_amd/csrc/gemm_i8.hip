@@ -107,12 +107,19 @@ __device__ __forceinline__ i32x4_t read_tr16(uint32_t p)
     return i32x4_t{r0[0], r0[1], r1[0], r1[1]};
 }
 
-// (XCD, place in it) -> a task order in which an XCD's workgroups hold neighbouring tasks, which
-// share weight strips and A rows in its L2.
-__device__ __forceinline__ int first_task()
+// Neighbouring tasks that one XCD works on at a time (they share weight strips and A rows in its L2): one
+// for each of its workgroups, or an eighth of them all where there are fewer, so that every XCD has its
+// part of the HBM traffic (64 tasks on two XCDs instead of eight: 111 against 76 us).
+__device__ __forceinline__ int xcd_run(int total)
 {
-    const int b = static_cast<int>(blockIdx.x), per = static_cast<int>(gridDim.x) / kXcdCount;
-    return (b % kXcdCount) * per + b / kXcdCount;
+    return max(1, min(static_cast<int>(gridDim.x) / kXcdCount, (total + kXcdCount - 1) / kXcdCount));
+}
+// The workgroup's first task; `total` if it has none.
+__device__ __forceinline__ int first_task(int total)
+{
+    const int xcd = static_cast<int>(blockIdx.x) % kXcdCount, place = static_cast<int>(blockIdx.x) / kXcdCount;
+    const int run = xcd_run(total);
+    return place < run ? xcd * run + place : total;
 }
 
 // A pointer that is the same on every lane, in scalar registers.
@@ -203,7 +210,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
 
     // The copies run kStages - 1 steps ahead of the products through all of the workgroup's tasks: task
     // pt is the one being copied, its successor's tile entry and slot-list entries are loaded ahead.
-    int pt = first_task() - grid, left = 0, stage = 0, fill = 0, ahead = 0;
+    int pt = first_task(total) - grid, left = 0, stage = 0, fill = 0, ahead = 0;
     MTile next_tile{};
     int next_nt = 0;
     int gsrc[C::kACopies] = {};
@@ -211,10 +218,10 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
         if (task >= total)
             return;
         next_tile = uniform_task(task / a.splits, n_nt, a.tiles, next_nt);
-        const int last = next_tile.row_end - next_tile.row_begin - 1;
+        const int rows = next_tile.row_end - next_tile.row_begin;
 #pragma unroll
         for (int j = 0; j < C::kACopies; ++j) {
-            const int r = min(kARows * (C::kACopies * wave + j) + lane / kALanes, last);   // past the tile's end: its last row
+            const int r = (kARows * (C::kACopies * wave + j) + lane / kALanes) % rows;   // past the tile's end: its rows again
             gsrc[j] = a.gather != nullptr ? a.gather[next_tile.row_begin + r] : r;
         }
     };
@@ -266,7 +273,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
         issue();
     static_assert(C::kStages == 3, "the waits below");
 
-    for (int t = first_task(); t < total; t += grid) {
+    for (int t = first_task(total); t < total; t += grid) {
         int nt;
         const MTile tile = uniform_task(t / a.splits, n_nt, a.tiles, nt);
         const int n0 = nt * BN;
@@ -598,7 +605,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
     const int K = a.K, N = a.N;
     const int KT = K / BK;
     const int n_nt = (N + BN - 1) / BN;
-    const int total = *a.tile_count * n_nt;
+    const int total = __builtin_amdgcn_readfirstlane(*a.tile_count * n_nt);
     const int first = KT & 2;                                // position of a task's first step
 
     const int mat = kGated ? wave / (kWaves / 2) : 0;
@@ -629,7 +636,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
     }
 
     const int xcd = blockIdx.x % kXcdCount;
-    const int blk = gridDim.x / kXcdCount;
+    const int blk = xcd_run(total);
     MTile tile{};
     int n0 = 0;
     uint32_t a_voff[kACopies], b_voff[kBCopies];
@@ -851,38 +858,93 @@ bool int8_supported(int64_t K, int64_t N)
     return K > 0 && N > 0 && K % 128 == 0 && N % 128 == 0 && K <= kInt8MaxK;
 }
 
-Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int64_t least_k)
+namespace {
+
+// Estimated microseconds of one grouped product with row tiles of `tile` rows and K in `cuts`, for M rows
+// spread evenly at random over G groups.  A step of 128 values of K takes a workgroup between `lone`
+// (few workgroups: latency) and `full` (all CUs busy: LDS copies, for 256 rows the MFMAs); the weights
+// come at 5 TB/s; a cut product writes its sums and has them read again by one more launch.  The
+// constants are fitted to 1500 timings (K x N of 4096 x 14336, 7168 x 2048, 2048 x 768, 1024 x 4096, 1 to 32
+// groups of 1 to 700 rows, tiles of 64, 128 and 256 rows, 1 to 8 cuts): the plan taken is within 12% of
+// the best one everywhere, 0.3% on average, where one choice by rows per group lost up to 2.8x (7168 x
+// 2048, one group of 200 rows: 73 us with 256-row tiles, 26 us with 64 rows and 8 cuts).
+double product_cost(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int tile, int cuts)
 {
-    // how many groups hold rows, for rows spread evenly at random
-    const double held = G * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(G), static_cast<double>(M)));
-    const int64_t groups = std::max<int64_t>(1, static_cast<int64_t>(std::ceil(held)));
-    const int64_t per_group = ceil_div(std::max<int64_t>(M, 1), groups);
-    Int8Plan p;
-    p.row_tile = per_group <= 64 ? 64 : per_group <= 160 || least_k < 256 ? 128 : 256;
-    p.splits = 1;
-    if (p.row_tile != 256) {
-        // K is cut where that evens out the workgroups' shares: the rounds over the CUs, at the cost of
-        // about one step per cut task and of writing and reading the partial sums, whose bytes weigh
-        // three times the weights' (measured: 8 rows on 8 experts of 4096 x 14336 uncut 78 us, in two cuts
-        // 71 us, in three 64 us; 1000 rows on 128 experts of 2048 x 768, gated, uncut 71 us, in two 78 us)
-        const int64_t tasks = (groups + M / p.row_tile) * ceil_div(N, gated ? i8::BNB / 2 : i8::BNB);
-        constexpr int cus = 256;                              // a host-only rule: the MI355X's, whatever is current
-        const int64_t steps = K / 128;
-        double best = 0.0;
-        for (int64_t c = 1; c <= std::min<int64_t>(16, std::max<int64_t>(1, steps / 4)); ++c) {
-            const double sums = 8.0 * static_cast<double>(M) * static_cast<double>(N) * (gated ? 2 : 1) * (c > 1 || gated ? c : 0);
-            const double weights = static_cast<double>(groups) * static_cast<double>(K) * static_cast<double>(N) * (gated ? 2 : 1);
-            const double cost = static_cast<double>(ceil_div(tasks * c, cus)) / c * (1.0 + static_cast<double>(c) / steps) *
-                                    static_cast<double>(cus) / static_cast<double>(tasks) +
-                                3.0 * sums / weights;
-            if (c == 1 || cost < 0.97 * best) {
-                best = cost;
-                p.splits = static_cast<int>(c);
-            }
+    const double lone = tile == 64 ? 0.43 : tile == 128 ? 0.75 : 1.1, full = tile == 64 ? 0.91 : tile == 128 ? 1.3 : 1.9;
+    constexpr double cus = 256;                // a host-only rule: the MI355X's, whatever device is current
+    const double rows = static_cast<double>(std::max<int64_t>(M, 1));
+    const double held = std::max(1.0, static_cast<double>(G) * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(G), rows)));
+    const double per_group = rows / held;
+    const double tasks = held * std::ceil(per_group / tile) * static_cast<double>(ceil_div(N, gated ? i8::BNB / 2 : i8::BNB)) * cuts;
+    double step = lone + (full - lone) * std::min(1.0, tasks / cus);
+    if (tile == 256)
+        step *= 0.75 + 0.25 * std::min(1.0, per_group / tile);
+    const double work = std::ceil(tasks / cus) * (std::ceil(static_cast<double>(K / 128) / cuts) + 1.5) * step;
+    const double values = rows * static_cast<double>(N) * (gated ? 2 : 1);
+    const double weights = held * static_cast<double>(K) * static_cast<double>(N) * (gated ? 2 : 1) / 5e6;
+    double cost = std::max(work, weights) + 0.25 * std::min(work, weights);
+    if (cuts > 1 || (gated && tile == 64))
+        cost += 8.0 * values * cuts / 5e6 + (gated ? 0.0 : 6.1);   // int32 sums out and in; h's quantiser runs anyway
+    else if (gated)
+        cost += 4.0 * values / 5e6;                               // float32 h out and in
+    return cost;
+}
+
+// The best number of cuts for the tile height, and its cost.
+double best_cuts(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int tile, int& cuts)
+{
+    cuts = 1;
+    double best = product_cost(M, G, K, N, gated, tile, 1);
+    for (int c : {2, 3, 4, 6, 8, 12, 16}) {
+        if (tile == 256 || K / 128 < 4 * c)
+            break;
+        const double cost = product_cost(M, G, K, N, gated, tile, c);
+        if (cost < best) {
+            best = cost;
+            cuts = c;
         }
     }
-    p.partial = p.splits > 1 || (gated && p.row_tile == 64);
+    return best;
+}
+
+Int8Plan make_plan(int tile, int cuts, bool gated)
+{
+    return Int8Plan{tile, cuts, cuts > 1 || (gated && tile == 64)};
+}
+
+}  // namespace
+
+Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N)
+{
+    Int8Plan p{};
+    double best = 0.0;
+    for (int tile : {64, 128, 256}) {
+        if (tile == 256 && K < 256)
+            break;
+        int cuts = 1;
+        const double cost = best_cuts(M, G, K, N, false, tile, cuts);
+        if (tile == 64 || cost < best) {
+            best = cost;
+            p = make_plan(tile, cuts, false);
+        }
+    }
     return p;
+}
+
+void int8_ffn_plans(int64_t M, int64_t G, int64_t H, int64_t F, Int8Plan& fc1, Int8Plan& fc2)
+{
+    double best = 0.0;
+    for (int tile : {64, 128, 256}) {
+        if (tile == 256 && std::min(H, F) < 256)
+            break;
+        int c1 = 1, c2 = 1;
+        const double cost = best_cuts(M, G, H, F, true, tile, c1) + best_cuts(M, G, F, H, false, tile, c2);
+        if (tile == 64 || cost < best) {
+            best = cost;
+            fc1 = make_plan(tile, c1, true);
+            fc2 = make_plan(tile, c2, false);
+        }
+    }
 }
 
 bool int8_tasks_fit(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gated)

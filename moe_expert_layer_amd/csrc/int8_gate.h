@@ -18,14 +18,15 @@ constexpr int64_t kInt8MaxK = 130944;  // |sum of K products of -128 .. 127| sta
 bool int8_supported(int64_t K, int64_t N);
 // How a grouped product of M rows in at most G groups with [K, N] weights (gated: two of them) runs:
 // the tile table's height, the cuts of K, and whether the kernel leaves int32 partial sums
-// ([splits, M, N], gated [splits, M, 2 N]) for launch_int8_finish / launch_int8_swiglu_partial.  least_k:
-// the smallest K among the products that share the tile table.
+// ([splits, M, N], gated [splits, M, 2 N]) for launch_int8_finish / launch_int8_swiglu_partial.
 struct Int8Plan {
     int row_tile;
     int splits;
     bool partial;
 };
-Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int64_t least_k);
+Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N);
+// The same for the two products of an FFN, which share a tile table.
+void int8_ffn_plans(int64_t M, int64_t G, int64_t H, int64_t F, Int8Plan& fc1, Int8Plan& fc2);
 // Whether the plan's tasks (row tiles x column tiles x cuts) can be numbered in 32 bits.
 bool int8_tasks_fit(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gated);
 // out: [M, N] of out_dtype (MOE_F32 / MOE_BF16), gated (w1 not null) float32 swiglu of the two

@@ -89,25 +89,31 @@ def _offsets(counts, gap=0):
     return np.concatenate([[gap], gap + np.cumsum(counts)]).astype(np.int32)
 
 
+# The library picks the row tile (64, 128 or 256) and the cuts of K from M, the number of groups, K and N;
+# the comments name what these sizes take.
 PRODUCTS = [
     # counts of rows per group, K, N
     ([1], 128, 128),
     ([1, 0, 2], 256, 384),
     ([0, 0], 128, 256),
-    ([40, 64, 65, 3], 384, 256),                 # 64-row tiles, partial sums
-    ([130, 0, 100, 161], 640, 512),              # 128-row tiles, an odd number of 128-column strips
-    ([300, 257, 1, 512], 256, 640),              # 256-row tiles, half a column tile at the end
+    ([40, 64, 65, 3], 384, 256),
+    ([130, 0, 100, 161], 640, 512),
+    ([300, 257, 1, 512], 256, 640),
     ([1000], 1152, 128),
     ([5] * 100, 128, 128),
     ([700, 0, 900], 128, 256),
-    ([2], 16384, 256),                           # K cut many times
-    ([30, 0, 64, 7], 2048, 384),                 # 64-row tiles, K cut
-    ([150, 100, 90], 1664, 256),                 # 128-row tiles, K cut into unequal parts
-    ([3] * 300, 256, 640),                       # several tasks per workgroup, one step or two each
-    ([513, 256, 300], 384, 384),                 # 256-row tiles, odd numbers of K pairs and column strips
+    ([3] * 300, 256, 640),                                   # several tasks per workgroup, two steps each
+    ([2], 16384, 256),                                       # 64 rows, 16 cuts
+    ([30, 0, 64, 7], 2048, 384),                             # cuts
+    ([150, 100, 90], 1664, 256),                             # cuts of unequal length
+    ([130, 0, 65, 65, 100, 30, 64, 66], 256, 4224),          # 128 rows
+    ([130, 0, 65, 65, 100, 30, 64, 66], 384, 4224),
+    ([65] * 30 + [0] * 5 + [130] * 5, 4096, 128),            # 128 rows, 4 cuts
+    ([300, 0, 257, 13, 130, 1, 32, 307], 256, 4224),         # 256 rows, half a column tile at the end
+    ([300, 0, 257, 13, 130, 1, 32, 307], 384, 4224),         # 256 rows, an odd number of K pairs
+    ([513, 256, 300], 384, 384),
     ([900, 0, 64, 2000], 896, 1152),
-    ([3000], 1024, 256),
-    ([700] * 12, 512, 512),                      # more tasks than four per workgroup need
+    ([700] * 12, 512, 512),
 ]
 
 
@@ -128,6 +134,22 @@ def test_matmul(counts, K, N, out_dtype):
         if M else np.zeros((0, N))
     tol = (4 * U + (BF if out_dtype == torch.bfloat16 else 0)) * np.abs(r)
     assert np.all(np.abs(_host(out) - r) <= tol)
+
+
+@pytest.mark.parametrize("K", [256, 640])
+def test_matmul_of_many_tasks(K):
+    """256-row tiles, more than four tasks per workgroup (claimed two ahead); sampled rows of every tile."""
+    rng = np.random.default_rng(K)
+    counts, N = [5000, 3000, 0, 1, 4099, 2900, 6000, 3000], 4224
+    M, off = sum(counts), _offsets(counts)
+    rows, w, rs, wsc = _codes(rng, M, K), _codes(rng, 8, K, N), _scale(rng, M), _scale(rng, 8, N)
+    out = mel.grouped_matmul_int8(*_dev(rows, rs, off, np.arange(8, dtype=np.int32), w, wsc))
+    for a, b, e in zip(off, off[1:], range(8)):
+        at = np.unique(np.concatenate([np.arange(a, b, 37), np.arange(max(a, b - 3), b)]))
+        if at.size:
+            r = ref.matmul(rows[at], rs[at], w[e], wsc[e])
+            got = _host(out[torch.from_numpy(at).cuda()])
+            assert np.all(np.abs(got - r) <= (4 * U + BF) * np.abs(r))
 
 
 def test_matmul_largest_codes():
@@ -178,8 +200,16 @@ def _weights(rng, E, H, F):
             _codes(rng, E, F, H), _scale(rng, E, H, level=3e-4))
 
 
-FFNS = [([400, 290], 128, 384), ([512, 31, 600], 384, 640), ([1], 128, 128), ([3, 0, 5], 256, 384), ([60, 64, 1], 128, 640), ([150, 129], 384, 256),
-        ([300, 0, 270], 256, 512), ([2000], 128, 128), ([1, 1], 2048, 256)]
+FFNS = [
+    ([1], 128, 128), ([3, 0, 5], 256, 384), ([60, 64, 1], 128, 640), ([150, 129], 384, 256), ([300, 0, 270], 256, 512),
+    ([2000], 128, 128), ([1, 1], 2048, 256), ([400, 290], 128, 384), ([512, 31, 600], 384, 640),
+    ([33], 1024, 4096),                                      # 64 rows, both products cut
+    ([1800, 900, 0, 900, 900, 899, 1, 1800], 256, 128),      # 128 rows
+    ([200, 0, 190], 256, 4096),                              # 128 rows, the second product cut
+    ([65] * 40, 1024, 128),                                  # 128 rows, the first product cut
+    ([260, 0, 130, 257, 3] + [130] * 11, 256, 1152),         # 256 rows
+    ([260, 0, 130, 257, 3] + [130] * 11, 384, 1152),         # 256 rows, odd numbers of K pairs
+]
 
 
 @pytest.mark.parametrize("counts,H,F", FFNS)
@@ -197,7 +227,7 @@ def test_ffn(counts, H, F):
             assert np.all(np.abs(out[a:b] - y) <= slack + BF * (np.abs(y) + slack))
 
 
-LAYERS = [(1, 2048, 1024, 8, 2), (64, 256, 256, 16, 4), (65, 256, 256, 16, 4), (32, 128, 256, 1023, 8), (256, 128, 128, 3, 1),
+LAYERS = [(1040, 256, 1152, 16, 2), (1040, 384, 1152, 16, 2), (1, 2048, 1024, 8, 2), (64, 256, 256, 16, 4), (65, 256, 256, 16, 4), (32, 128, 256, 1023, 8), (256, 128, 128, 3, 1),
           (1, 256, 384, 4, 2), (3, 128, 128, 1, 1), (40, 256, 256, 8, 3), (150, 128, 384, 3, 3), (900, 256, 256, 5, 2),
           (64, 128, 128, 100, 8)]
 
