@@ -214,12 +214,6 @@ moe_status check_problem(const moe_problem* p, bool need_tokens, bool gemm = tru
 
 constexpr int64_t kInt8MaxGroups = int64_t{1} << 24;
 
-moe_status check_int8_tasks(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gated)
-{
-    return int8_tasks_fit(p, M, G, N, gated) ? MOE_OK
-                                             : fail(MOE_ERR_UNSUPPORTED, "too many tiles for 32-bit task numbers");
-}
-
 // Sizes of an int8 grouped product.
 moe_status check_int8_product(int64_t M, int64_t G, int64_t E, int64_t K, int64_t N)
 {
@@ -231,19 +225,7 @@ moe_status check_int8_product(int64_t M, int64_t G, int64_t E, int64_t K, int64_
     if (!int8_supported(K, N) || N > MOE_MAX_HIDDEN)
         return fail(MOE_ERR_UNSUPPORTED, "int8 products need K and N multiples of 128, K <= %lld, N <= %d",
                     (long long)kInt8MaxK, MOE_MAX_HIDDEN);
-    return check_int8_tasks(int8_plan(M, G, K, N), M, G, N, false);
-}
-
-// The two products of the FFN on M rows in G groups.
-moe_status check_int8_ffn(const moe_problem* p, int64_t M, int64_t G)
-{
-    if (G > kInt8MaxGroups)
-        return fail(MOE_ERR_UNSUPPORTED, "int8 products need G <= %lld", (long long)kInt8MaxGroups);
-    Int8Plan fc1{}, fc2{};
-    int8_ffn_plans(M, G, p->H, p->F, fc1, fc2);
-    if (moe_status st = check_int8_tasks(fc1, M, G, p->F, true); st != MOE_OK)
-        return st;
-    return check_int8_tasks(fc2, M, G, p->H, false);
+    return MOE_OK;
 }
 
 // A problem of the int8 layer or grouped FFN.
@@ -273,7 +255,6 @@ moe_status check_int8_problem(const moe_problem* p, bool need_tokens)
             return fail(MOE_ERR_UNSUPPORTED, "T * k exceeds int32 indexing");
         if (p->T * p->H > UINT32_MAX)
             return fail(MOE_ERR_UNSUPPORTED, "int8 needs T * H < 2^32");
-        return check_int8_ffn(p, p->T * p->k, p->E);
     }
     return MOE_OK;
 }
@@ -549,10 +530,34 @@ Int8Layout int8_layout(int64_t M, int64_t G, int64_t H, int64_t F, int64_t T, in
     return L;
 }
 
+// Whether L's products have few enough tasks for their numbers.
+moe_status check_tasks(const Int8Layout& L, int64_t M, int64_t G, int64_t H, int64_t F)
+{
+    return int8_tasks_fit(L.fc1, M, G, F, true) && int8_tasks_fit(L.fc2, M, G, H, false)
+               ? MOE_OK
+               : fail(MOE_ERR_UNSUPPORTED, "too many tiles for 32-bit task numbers");
+}
+
 struct Int8Weights {
     const int8_t *gate, *up, *down;
     const float *gate_scale, *up_scale, *down_scale;
 };
+
+// The tile table of the int8 products, in tiles_run and count[4]; the general builder, for more groups
+// than the one-workgroup kernel takes, needs room for its other table too.
+moe_status int8_tiles(const int32_t* offsets, const int32_t* group_expert, int64_t G, int64_t E, int64_t M, int bm,
+                      MTile* tiles, MTile* tiles_run, int64_t max_tiles, int32_t* count, int32_t* task_ctr,
+                      int32_t* status, bool write_status, hipStream_t s)
+{
+    if (G <= kInt8TileGroups)
+        LAUNCH(s, "int8_tiles",
+               launch_int8_tiles(offsets, group_expert, G, E, M, bm, tiles_run, count + 4, task_ctr, status, write_status, s));
+    else
+        LAUNCH(s, "build_tiles",
+               launch_build_tiles(offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), bm, tiles, max_tiles, count,
+                                  nullptr, nullptr, 1, 0, task_ctr, status, write_status, s, tiles_run, count + 4));
+    return MOE_OK;
+}
 
 // fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.  row_experts
 // (may be null): the small layer's preparation has run, the tile table is there and each row's expert.  y null: the down projection's partial sums (L.fc2.partial) stay for the
@@ -566,10 +571,11 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
     MTile* tiles = at<MTile>(ws, L.tiles_run);
     const int32_t* count = tcount + 4;
     if (row_experts == nullptr)
-        LAUNCH(s, "build_tiles",
-           launch_build_tiles(offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.fc1.row_tile,
-                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0,
-                              at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), write_status, s, tiles, tcount + 4));
+        if (moe_status st = int8_tiles(offsets, group_expert, G, E, M, L.fc1.row_tile, at<MTile>(ws, L.tiles), tiles,
+                                       L.max_tiles, tcount, at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0),
+                                       write_status, s);
+            st != MOE_OK)
+            return st;
     int8_t* h_q = at<int8_t>(ws, L.h_q);
     float* h_scale = at<float>(ws, L.h_scale);
     LAUNCH(s, "fc1_i8",
@@ -607,8 +613,9 @@ MOE_API moe_status moe_workspace_size(const moe_problem* p, size_t* bytes)
     if (p != nullptr && p->dtype == MOE_INT8) {
         if (moe_status st = check_int8_problem(p, true); st != MOE_OK)
             return st;
-        *bytes = int8_layout(p->T * p->k, p->E, p->H, p->F, p->T, p->k, p->E, true).total;
-        return MOE_OK;
+        const Int8Layout L = int8_layout(p->T * p->k, p->E, p->H, p->F, p->T, p->k, p->E, true);
+        *bytes = L.total;
+        return check_tasks(L, p->T * p->k, p->E, p->H, p->F);
     }
     if (moe_status st = check_problem(p, true); st != MOE_OK)
         return st;
@@ -751,6 +758,8 @@ MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, 
         return fail(MOE_ERR_INVALID_ARGUMENT, "with MOE_FLAG_QUANTIZE_X, x is bfloat16 and x_scale must be null");
     const int64_t T = p->T, k = p->k, M = T * k, H = p->H, F = p->F, E = p->E;
     const Int8Layout L = int8_layout(M, E, H, F, T, k, E, true);
+    if (moe_status st = check_tasks(L, M, E, H, F); st != MOE_OK)
+        return st;
     if (workspace == nullptr || workspace_bytes < L.total)
         return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes, got %zu", L.total,
                     workspace == nullptr ? size_t{0} : workspace_bytes);
@@ -1076,10 +1085,11 @@ MOE_API moe_status moe_grouped_ffn_workspace_size(const moe_problem* p, int64_t 
     if (p != nullptr && p->dtype == MOE_INT8) {
         if (moe_status st = check_int8_problem(p, false); st != MOE_OK)
             return st;
-        if (moe_status st = check_int8_ffn(p, M, G); st != MOE_OK)
-            return st;
-        *bytes = int8_layout(M, G, p->H, p->F, 0, 1, p->E, false).total;
-        return MOE_OK;
+        if (G > kInt8MaxGroups)
+            return fail(MOE_ERR_UNSUPPORTED, "int8 products need G <= %lld", (long long)kInt8MaxGroups);
+        const Int8Layout L = int8_layout(M, G, p->H, p->F, 0, 1, p->E, false);
+        *bytes = L.total;
+        return check_tasks(L, M, G, p->H, p->F);
     }
     if (moe_status st = check_problem(p, false); st != MOE_OK)
         return st;
@@ -1192,6 +1202,12 @@ MatmulLayout matmul_layout(int64_t M, int64_t G, int64_t K, int64_t N)
     return L;
 }
 
+moe_status check_tasks(const MatmulLayout& L, int64_t M, int64_t G, int64_t N)
+{
+    return int8_tasks_fit(L.plan, M, G, N, false) ? MOE_OK
+                                                  : fail(MOE_ERR_UNSUPPORTED, "too many tiles for 32-bit task numbers");
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -1202,8 +1218,9 @@ MOE_API moe_status moe_grouped_matmul_int8_workspace_size(int64_t M, int64_t G, 
         return fail(MOE_ERR_INVALID_ARGUMENT, "bytes is null");
     if (moe_status st = check_int8_product(M, G, 1, K, N); st != MOE_OK)
         return st;
-    *bytes = matmul_layout(M, G, K, N).total;
-    return MOE_OK;
+    const MatmulLayout L = matmul_layout(M, G, K, N);
+    *bytes = L.total;
+    return check_tasks(L, M, G, N);
 }
 
 MOE_API moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows_scale, int64_t M,
@@ -1217,6 +1234,8 @@ MOE_API moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows
     if (out_dtype != MOE_F32 && out_dtype != MOE_BF16)
         return fail(MOE_ERR_UNSUPPORTED, "out_dtype must be MOE_F32 or MOE_BF16");
     const MatmulLayout L = matmul_layout(M, G, K, N);
+    if (moe_status st = check_tasks(L, M, G, N); st != MOE_OK)
+        return st;
     if (workspace == nullptr || workspace_bytes < L.total)
         return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes", L.total);
     if (group_offsets == nullptr || group_expert == nullptr ||
@@ -1228,10 +1247,10 @@ MOE_API moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows
     void* ws = workspace;
     int32_t* tcount = at<int32_t>(ws, L.tile_count);
     MTile* tiles = at<MTile>(ws, L.tiles_run);
-    LAUNCH(s, "build_tiles",
-           launch_build_tiles(group_offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), L.plan.row_tile,
-                              at<MTile>(ws, L.tiles), L.max_tiles, tcount, nullptr, nullptr, 1, 0,
-                              at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), true, s, tiles, tcount + 4));
+    if (moe_status st = int8_tiles(group_offsets, group_expert, G, E, M, L.plan.row_tile, at<MTile>(ws, L.tiles), tiles,
+                                   L.max_tiles, tcount, at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), true, s);
+        st != MOE_OK)
+        return st;
     if (M == 0)
         return MOE_OK;
     LAUNCH(s, "matmul_i8",

@@ -861,44 +861,55 @@ bool int8_supported(int64_t K, int64_t N)
 namespace {
 
 // Estimated microseconds of one grouped product with row tiles of `tile` rows and K in `cuts`, for M rows
-// spread evenly at random over G groups.  A step of 128 values of K takes a workgroup between `lone`
-// (few workgroups: latency) and `full` (all CUs busy: LDS copies, for 256 rows the MFMAs); the weights
-// come at 5 TB/s; a cut product writes its sums and has them read again by one more launch.  The
-// constants are fitted to 1500 timings (K x N of 4096 x 14336, 7168 x 2048, 2048 x 768, 1024 x 4096, 1 to 32
-// groups of 1 to 700 rows, tiles of 64, 128 and 256 rows, 1 to 8 cuts): the plan taken is within 12% of
-// the best one everywhere, 0.3% on average, where one choice by rows per group lost up to 2.8x (7168 x
-// 2048, one group of 200 rows: 73 us with 256-row tiles, 26 us with 64 rows and 8 cuts).
-double product_cost(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int tile, int cuts)
+// spread evenly at random over G groups: the rounds of tasks over the CUs, each as long as its steps (of
+// 128 values of K: between `lone` for a workgroup by itself, latency, and `full` with all CUs busy, LDS
+// copies or for 256 rows the MFMAs; 2.5 more steps to fill and to finish) or its share of the weights
+// at 5.9 TB/s, and a part of the shorter one; a cut product has its sums written and, by one more
+// launch, read.  Constants fitted to 1500 timings (K x N of 4096 x 14336, 7168 x 2048, 2048 x 768, 1024 x
+// 4096, 1 to 32 groups of 1 to 700 rows, tiles of 64, 128 and 256 rows, 1 to 8 cuts): the plan taken is
+// within 12% of the best one everywhere and 0.2% on average, where a choice by rows per group alone lost
+// up to 2.8x (7168 x 2048, one group of 200 rows: 73 us with 256-row tiles, 26 us with 64 rows and 8 cuts).
+struct Spread {                                // M rows over the groups that hold some
+    double rows, held, per_group;
+    Spread(int64_t M, int64_t G)
+    {
+        rows = static_cast<double>(std::max<int64_t>(M, 1));
+        held = std::max(1.0, static_cast<double>(G) * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(G), rows)));
+        per_group = rows / held;
+    }
+};
+
+double product_cost(const Spread& x, int64_t K, int64_t N, bool gated, int tile, int cuts)
 {
-    const double lone = tile == 64 ? 0.43 : tile == 128 ? 0.75 : 1.1, full = tile == 64 ? 0.91 : tile == 128 ? 1.3 : 1.9;
+    const double lone = tile == 64 ? 0.47 : tile == 128 ? 0.7 : 1.2, full = tile == 64 ? 0.82 : tile == 128 ? 1.3 : 1.9;
     constexpr double cus = 256;                // a host-only rule: the MI355X's, whatever device is current
-    const double rows = static_cast<double>(std::max<int64_t>(M, 1));
-    const double held = std::max(1.0, static_cast<double>(G) * (1.0 - std::pow(1.0 - 1.0 / static_cast<double>(G), rows)));
-    const double per_group = rows / held;
-    const double tasks = held * std::ceil(per_group / tile) * static_cast<double>(ceil_div(N, gated ? i8::BNB / 2 : i8::BNB)) * cuts;
-    double step = lone + (full - lone) * std::min(1.0, tasks / cus);
-    if (tile == 256)
-        step *= 0.75 + 0.25 * std::min(1.0, per_group / tile);
-    const double work = std::ceil(tasks / cus) * (std::ceil(static_cast<double>(K / 128) / cuts) + 1.5) * step;
-    const double values = rows * static_cast<double>(N) * (gated ? 2 : 1);
-    const double weights = held * static_cast<double>(K) * static_cast<double>(N) * (gated ? 2 : 1) / 5e6;
-    double cost = std::max(work, weights) + 0.25 * std::min(work, weights);
+    const double tasks = x.held * std::ceil(x.per_group / tile) * static_cast<double>(ceil_div(N, gated ? i8::BNB / 2 : i8::BNB)) * cuts;
+    const double weights = x.held * static_cast<double>(K) * static_cast<double>(N) * (gated ? 2 : 1) / 5.9e6 / tasks;
+    const double steps = std::ceil(static_cast<double>(K / 128) / cuts) + 2.5;
+    const auto round = [&](double n) {
+        const double step = (lone + (full - lone) * std::min(1.0, n / cus)) *
+                            (tile == 256 ? 0.75 + 0.25 * std::min(1.0, x.per_group / tile) : 1.0);
+        return std::max(steps * step, n * weights) + 0.21 * std::min(steps * step, n * weights);
+    };
+    const double whole = std::floor(tasks / cus), rest = tasks - whole * cus;
+    double cost = (whole > 0 ? whole * round(cus) : 0.0) + (rest > 0 ? round(rest) : 0.0);
+    const double values = x.rows * static_cast<double>(N) * (gated ? 2 : 1);
     if (cuts > 1 || (gated && tile == 64))
-        cost += 8.0 * values * cuts / 5e6 + (gated ? 0.0 : 6.1);   // int32 sums out and in; h's quantiser runs anyway
+        cost += 8.0 * values * cuts / 5.2e6 + (gated ? 0.0 : 7.6);   // int32 sums out and in; h's quantiser runs anyway
     else if (gated)
-        cost += 4.0 * values / 5e6;                               // float32 h out and in
+        cost += 4.0 * values / 5.2e6;                               // float32 h out and in
     return cost;
 }
 
 // The best number of cuts for the tile height, and its cost.
-double best_cuts(int64_t M, int64_t G, int64_t K, int64_t N, bool gated, int tile, int& cuts)
+double best_cuts(const Spread& x, int64_t K, int64_t N, bool gated, int tile, int& cuts)
 {
     cuts = 1;
-    double best = product_cost(M, G, K, N, gated, tile, 1);
+    double best = product_cost(x, K, N, gated, tile, 1);
     for (int c : {2, 3, 4, 6, 8, 12, 16}) {
         if (tile == 256 || K / 128 < 4 * c)
             break;
-        const double cost = product_cost(M, G, K, N, gated, tile, c);
+        const double cost = product_cost(x, K, N, gated, tile, c);
         if (cost < best) {
             best = cost;
             cuts = c;
@@ -916,13 +927,14 @@ Int8Plan make_plan(int tile, int cuts, bool gated)
 
 Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N)
 {
+    const Spread x(M, G);
     Int8Plan p{};
     double best = 0.0;
     for (int tile : {64, 128, 256}) {
         if (tile == 256 && K < 256)
             break;
         int cuts = 1;
-        const double cost = best_cuts(M, G, K, N, false, tile, cuts);
+        const double cost = best_cuts(x, K, N, false, tile, cuts);
         if (tile == 64 || cost < best) {
             best = cost;
             p = make_plan(tile, cuts, false);
@@ -933,12 +945,13 @@ Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N)
 
 void int8_ffn_plans(int64_t M, int64_t G, int64_t H, int64_t F, Int8Plan& fc1, Int8Plan& fc2)
 {
+    const Spread x(M, G);
     double best = 0.0;
     for (int tile : {64, 128, 256}) {
         if (tile == 256 && std::min(H, F) < 256)
             break;
         int c1 = 1, c2 = 1;
-        const double cost = best_cuts(M, G, H, F, true, tile, c1) + best_cuts(M, G, F, H, false, tile, c2);
+        const double cost = best_cuts(x, H, F, true, tile, c1) + best_cuts(x, F, H, false, tile, c2);
         if (tile == 64 || cost < best) {
             best = cost;
             fc1 = make_plan(tile, c1, true);

@@ -16,7 +16,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;       // of most kernels; one row's quantisation takes kWideThreads where rows are few
-constexpr int kWideThreads = 1024;
+constexpr int kWideThreads = kInt8TileGroups;
 constexpr int kVec = 8;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
@@ -370,6 +370,88 @@ __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
     *reinterpret_cast<u32x2_t*>(out + t * N + c) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
 
+// Tile i of the R balanced ones of a group of n rows from row `begin`: its 32-row blocks are dealt as
+// evenly as possible, the last tile ends the group (the in-run table of launch_build_tiles).
+__device__ __forceinline__ MTile balanced_tile(int expert, int begin, int n, int R, int i, int run_begin)
+{
+    const int blocks = (n + 31) / 32, each = blocks / R, more = blocks % R;
+    MTile t;
+    t.expert = expert;
+    t.row_begin = begin + 32 * (each * i + min(i, more));
+    t.row_end = i == R - 1 ? begin + n : begin + 32 * (each * (i + 1) + min(i + 1, more));
+    t.chunk = 0;
+    t.run_begin = run_begin;
+    t.run_len = R;
+    t.pad0 = t.pad1 = 0;
+    return t;
+}
+
+// The table of balanced tiles alone, for at most kWideThreads groups: a thread per group, a scan, then a
+// thread per tile, which finds its group by bisection.  One workgroup, three barriers (8 groups 3 us
+// where the general builder with its two tables takes 5.5).
+__global__ __launch_bounds__(kWideThreads) void int8_tiles_kernel(
+    const int32_t* __restrict__ offsets, const int32_t* __restrict__ group_expert, int G, int E, int64_t M, int bm,
+    MTile* __restrict__ tiles, int32_t* __restrict__ tile_count, int32_t* __restrict__ task_ctr,
+    int32_t* __restrict__ status, int write_status)
+{
+    __shared__ int first[kWideThreads + 1], begin[kWideThreads], rows[kWideThreads], expert[kWideThreads];
+    __shared__ int wave_sum[kWideThreads / 64];
+    const int g = threadIdx.x, lane = g & 63, wave = g >> 6;
+    int64_t rb = 0, re = 0;
+    int e = 0;
+    bool bad = false;
+    if (g < G) {
+        rb = min(max(static_cast<int64_t>(offsets[g]), int64_t{0}), M);
+        re = min(max(static_cast<int64_t>(offsets[g + 1]), rb), M);
+        e = group_expert != nullptr ? group_expert[g] : g;
+        if (e < 0 || e >= E) {
+            bad = re > rb;
+            re = rb;                                          // skipped
+        }
+    }
+    const int n = static_cast<int>(re - rb);
+    const int mine = (n + bm - 1) / bm;
+    int before = mine;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const int v = __shfl_up(before, off);
+        before += lane >= off ? v : 0;
+    }
+    if (lane == 63)
+        wave_sum[wave] = before;
+    const int any_bad = __syncthreads_or(bad ? 1 : 0);
+    for (int w = 0; w < wave; ++w)
+        before += wave_sum[w];
+    first[g + 1] = before;
+    if (g == 0)
+        first[0] = 0;
+    begin[g] = static_cast<int>(rb);
+    rows[g] = n;
+    expert[g] = e;
+    if (g < 2 * kXcdCount)
+        task_ctr[g] = 0;
+    __syncthreads();
+    const int total = first[kWideThreads];
+    for (int t = g; t < total; t += kWideThreads) {
+        int lo = 0, hi = G - 1;                               // the last group whose first tile is at most t
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (first[mid] <= t)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        tiles[t] = balanced_tile(expert[lo], begin[lo], rows[lo], first[lo + 1] - first[lo], t - first[lo], first[lo]);
+    }
+    if (g == 0) {
+        *tile_count = total;
+        if (write_status)
+            *status = any_bad ? MOE_ERR_EXPERT_ID_OUT_OF_RANGE : MOE_OK;
+        else if (any_bad)
+            *status = MOE_ERR_EXPERT_ID_OUT_OF_RANGE;
+    }
+}
+
 // What a small layer call needs before its first product, in one launch: workgroup 0 routes (counts,
 // offsets, perm and pos of at most kInt8SmallSlots slots: a slot's rank among equal ids is counted
 // directly) and writes the table of balanced row tiles, the others quantise a token row each.
@@ -462,20 +544,9 @@ __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
         }
     }
     for (int e = tid; e < E; e += kThreads) {
-        const int n = hist[e], R = (n + bm - 1) / bm, blocks = (n + 31) / 32;
-        int r0 = begin[e];
-        for (int i = 0; i < R; ++i) {
-            MTile mt;
-            mt.expert = e;
-            mt.row_begin = r0;
-            r0 = i == R - 1 ? begin[e] + n : r0 + 32 * (blocks / R + (i < blocks % R ? 1 : 0));
-            mt.row_end = r0;
-            mt.chunk = 0;
-            mt.run_begin = tile_begin[e];
-            mt.run_len = R;
-            mt.pad0 = mt.pad1 = 0;
-            tiles[tile_begin[e] + i] = mt;
-        }
+        const int n = hist[e], R = (n + bm - 1) / bm;
+        for (int i = 0; i < R; ++i)
+            tiles[tile_begin[e] + i] = balanced_tile(e, begin[e], n, R, i, tile_begin[e]);
     }
 }
 
@@ -520,6 +591,18 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
     else
         int8_swiglu_partial_kernel<kThreads, 4><<<grid, dim3(kThreads), 0, s>>>(
             partial, splits, a_scale, gather, gather_k, sg, su, row_experts, offsets, group_expert, g, e, M, F, codes, scales);
+    return hipGetLastError();
+}
+
+hipError_t launch_int8_tiles(const int32_t* offsets, const int32_t* group_expert, int64_t G, int64_t E, int64_t M,
+                             int bm, MTile* tiles, int32_t* tile_count, int32_t* task_ctr, int32_t* status,
+                             bool write_status, hipStream_t s)
+{
+    if (G > kWideThreads)
+        return hipErrorInvalidValue;
+    int8_tiles_kernel<<<dim3(1), dim3(kWideThreads), 0, s>>>(offsets, group_expert, static_cast<int>(G),
+                                                             static_cast<int>(E), M, bm, tiles, tile_count, task_ctr,
+                                                             status, write_status ? 1 : 0);
     return hipGetLastError();
 }
 

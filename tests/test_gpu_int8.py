@@ -103,6 +103,8 @@ PRODUCTS = [
     ([5] * 100, 128, 128),
     ([700, 0, 900], 128, 256),
     ([3] * 300, 256, 640),                                   # several tasks per workgroup, two steps each
+    ([2, 0, 1] * 400, 128, 128),                             # more groups than the short tile builder takes
+    ([1] * 1024, 128, 128),
     ([2], 16384, 256),                                       # 64 rows, 16 cuts
     ([30, 0, 64, 7], 2048, 384),                             # cuts
     ([150, 100, 90], 1664, 256),                             # cuts of unequal length
@@ -122,8 +124,8 @@ PRODUCTS = [
 def test_matmul(counts, K, N, out_dtype):
     rng = np.random.default_rng(len(counts) + K + N)
     G, M = len(counts), int(np.sum(counts))
-    E = G + 2
-    expert = rng.permutation(E)[:G].astype(np.int32)
+    E = min(G + 2, 1000)
+    expert = rng.permutation(max(E, G))[:G].astype(np.int32) % E
     rows, w = _codes(rng, M, K), _codes(rng, E, K, N)
     rs, wsc = _scale(rng, M), _scale(rng, E, N)
     off = _offsets(counts)
