@@ -110,7 +110,7 @@ PRODUCTS = [
     ([150, 100, 90], 1664, 256),                             # cuts of unequal length
     ([130, 0, 65, 65, 100, 30, 64, 66], 256, 4224),          # 128 rows
     ([130, 0, 65, 65, 100, 30, 64, 66], 384, 4224),
-    ([65] * 30 + [0] * 5 + [130] * 5, 4096, 128),            # 128 rows, 4 cuts
+    ([65] * 30 + [0] * 5 + [130] * 5, 4096, 128),            # cuts
     ([300, 0, 257, 13, 130, 1, 32, 307], 256, 4224),         # 256 rows, half a column tile at the end
     ([300, 0, 257, 13, 130, 1, 32, 307], 384, 4224),         # 256 rows, an odd number of K pairs
     ([513, 256, 300], 384, 384),
@@ -206,11 +206,11 @@ FFNS = [
     ([1], 128, 128), ([3, 0, 5], 256, 384), ([60, 64, 1], 128, 640), ([150, 129], 384, 256), ([300, 0, 270], 256, 512),
     ([2000], 128, 128), ([1, 1], 2048, 256), ([400, 290], 128, 384), ([512, 31, 600], 384, 640),
     ([33], 1024, 4096),                                      # 64 rows, both products cut
-    ([1800, 900, 0, 900, 900, 899, 1, 1800], 256, 128),      # 128 rows
+    ([130, 0, 66, 1, 63] + [65] * 9 + [195, 0], 256, 1152),  # 128 rows
     ([200, 0, 190], 256, 4096),                              # 128 rows, the second product cut
-    ([65] * 40, 1024, 128),                                  # 128 rows, the first product cut
-    ([260, 0, 130, 257, 3] + [130] * 11, 256, 1152),         # 256 rows
-    ([260, 0, 130, 257, 3] + [130] * 11, 384, 1152),         # 256 rows, odd numbers of K pairs
+    ([65] * 38 + [130, 0], 2048, 256),                       # 128 rows, the first product cut
+    ([260, 0, 257, 3] + [130] * 36, 256, 640),               # 256 rows
+    ([260, 0, 257, 3] + [130] * 36, 384, 640),               # 256 rows, odd numbers of K pairs
 ]
 
 
@@ -229,7 +229,7 @@ def test_ffn(counts, H, F):
             assert np.all(np.abs(out[a:b] - y) <= slack + BF * (np.abs(y) + slack))
 
 
-LAYERS = [(1040, 256, 1152, 16, 2), (1040, 384, 1152, 16, 2), (1, 2048, 1024, 8, 2), (64, 256, 256, 16, 4), (65, 256, 256, 16, 4), (32, 128, 256, 1023, 8), (256, 128, 128, 3, 1),
+LAYERS = [(2600, 256, 640, 40, 2), (2600, 384, 640, 40, 2), (520, 256, 1152, 16, 2), (1, 2048, 1024, 8, 2), (64, 256, 256, 16, 4), (65, 256, 256, 16, 4), (32, 128, 256, 1023, 8), (256, 128, 128, 3, 1),
           (1, 256, 384, 4, 2), (3, 128, 128, 1, 1), (40, 256, 256, 8, 3), (150, 128, 384, 3, 3), (900, 256, 256, 5, 2),
           (64, 128, 128, 100, 8)]
 
