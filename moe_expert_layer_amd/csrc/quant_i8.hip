@@ -7,6 +7,9 @@
 // at least 2^-9 away from one, and one residual step makes the quotient right to less than an ulp (and
 // exact where it is a half), so the rounding cannot go to the wrong side.  For float32 values a
 // quotient within 2^-12 of a half is decided again in float64, where 127 x is exact.
+//
+// Bound by memory: every value is read once and kept in registers between the two steps (16384 x 8192
+// float32 rows in 127 us, 5.3 TB/s of reads and writes; 16384 x 7168 bfloat16 in 71 us).
 #include <algorithm>
 
 #include "common.h"
@@ -72,21 +75,23 @@ __device__ __forceinline__ int code_of(float x, const RowCode& c)
     return static_cast<int>(r);
 }
 
-// The largest of the workgroup's values, on every thread (kT threads).
+// The largest value over the kT threads of a row, on each of them: lanes of one wave, or the workgroup.
 template <int kT>
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* buf)
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf)
 {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
+    for (int off = (kT < 64 ? kT : 64) / 2; off >= 1; off >>= 1)
         v = max(v, static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), off)));
-    if ((threadIdx.x & 63) == 0)
-        buf[threadIdx.x >> 6] = v;
-    __syncthreads();
-    uint32_t m = buf[0];
+    if constexpr (kT > 64) {
+        if ((threadIdx.x & 63) == 0)
+            buf[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = buf[0];
 #pragma unroll
-    for (int w = 1; w < kT / 64; ++w)
-        m = max(m, buf[w]);
-    return m;
+        for (int w = 1; w < kT / 64; ++w)
+            v = max(v, buf[w]);
+    }
+    return v;
 }
 
 // The group that holds `row` (offsets clamped into [0, M] as in the tile table) and its expert, or
@@ -112,111 +117,132 @@ __device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets,
     return e >= 0 && e < E ? e : -1;
 }
 
-// One workgroup per row.  The row's values come from Src::load (kV neighbouring ones at a time); the
-// first kPer vectors of a thread stay in registers between the maximum and the codes, later ones are
-// made again.
-template <class Src, int kV, int kPer, bool kExactProduct, int kT = kThreads>
+// A row by kT threads (`me` among them; a part of a wave, or the workgroup).  The row's values come from
+// Src::load, eight neighbouring ones at a time (fewer at the row's end); the first kPer vectors of a thread
+// stay in registers between the maximum and the codes, as loaded (bfloat16 rows need half the registers
+// that way: 56 for 96, eight waves a SIMD for five), later ones are made again.  kWhole: cols is a multiple
+// of eight.
+template <class Src, int kPer, bool kExactProduct, int kT, bool kWhole = true>
 __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_t* __restrict__ codes,
-                                             float* __restrict__ scale, uint32_t* buf)
+                                             float* __restrict__ scale, uint32_t* buf, int me)
 {
-    float keep[kPer][kV];
+    typename Src::Raw keep[kPer];
     uint32_t amax = 0;
+    const auto count = [&](int64_t c) { return kWhole ? kVec : static_cast<int>(min(cols - c, static_cast<int64_t>(kVec))); };
+    const auto take = [&](const typename Src::Raw& raw) {
+        float x[kVec];
+        src.values(raw, x);
+#pragma unroll
+        for (int v = 0; v < kVec; ++v)
+            amax = max(amax, __float_as_uint(x[v]) & 0x7fffffffu);
+    };
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * kT + threadIdx.x) * kV;
+        const int64_t c = (static_cast<int64_t>(i) * kT + me) * kVec;
         if (c < cols) {
-            src.load(c, keep[i]);
-#pragma unroll
-            for (int v = 0; v < kV; ++v)
-                amax = max(amax, __float_as_uint(keep[i][v]) & 0x7fffffffu);
+            keep[i] = src.load(c, count(c));
+            take(keep[i]);
         }
     }
-    for (int64_t c = (static_cast<int64_t>(kPer) * kT + threadIdx.x) * kV; c < cols; c += kT * kV) {
-        float x[kV];
-        src.load(c, x);
-#pragma unroll
-        for (int v = 0; v < kV; ++v)
-            amax = max(amax, __float_as_uint(x[v]) & 0x7fffffffu);
+    for (int64_t c = (static_cast<int64_t>(kPer) * kT + me) * kVec; c < cols; c += kT * kVec) {
+        take(src.load(c, count(c)));
     }
-    const RowCode rc = row_code(block_max<kT>(amax, buf));
-    const auto store = [&](int64_t c, const float (&x)[kV]) {
-        if constexpr (kV == 1) {
-            codes[c] = static_cast<int8_t>(rc.finite ? code_of<kExactProduct>(x[0], rc) : 0);
+    const RowCode rc = row_code(row_max<kT>(amax, buf));
+    const auto store = [&](int64_t c, const typename Src::Raw& raw) {
+        float x[kVec];
+        src.values(raw, x);
+        u32x2_t w = {0, 0};
+#pragma unroll
+        for (int v = 0; v < kVec; ++v) {
+            const int code = rc.finite ? code_of<kExactProduct>(x[v], rc) : 0;
+            w[v / 4] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * (v % 4));
+        }
+        if (kWhole || c + kVec <= cols) {
+            __builtin_memcpy(codes + c, &w, kVec);
         } else {
-            uint32_t w[kV / 4];
-#pragma unroll
-            for (int q = 0; q < kV / 4; ++q) {
-                w[q] = 0;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const int code = rc.finite ? code_of<kExactProduct>(x[4 * q + b], rc) : 0;
-                    w[q] |= (static_cast<uint32_t>(code) & 0xffu) << (8 * b);
-                }
-            }
-            *reinterpret_cast<u32x2_t*>(codes + c) = u32x2_t{w[0], w[1]};
+            for (int v = 0; v < cols - c; ++v)
+                codes[c + v] = static_cast<int8_t>(w[v / 4] >> (8 * (v % 4)));
         }
     };
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * kT + threadIdx.x) * kV;
+        const int64_t c = (static_cast<int64_t>(i) * kT + me) * kVec;
         if (c < cols)
             store(c, keep[i]);
     }
-    for (int64_t c = (static_cast<int64_t>(kPer) * kT + threadIdx.x) * kV; c < cols; c += kT * kV) {
-        float x[kV];
-        src.load(c, x);
-        store(c, x);
+    for (int64_t c = (static_cast<int64_t>(kPer) * kT + me) * kVec; c < cols; c += kT * kVec) {
+        store(c, src.load(c, count(c)));
     }
-    if (threadIdx.x == 0)
+    if (me == 0)
         *scale = rc.scale;
 }
 
-template <int kV>
+// Rows in memory, of any alignment: the copies become unaligned vector loads.
 struct Bf16Row {
+    using Raw = u32x4_t;
     const uint16_t* x;
-    __device__ __forceinline__ void load(int64_t c, float (&v)[kV]) const
+    __device__ __forceinline__ Raw load(int64_t c, int n) const
     {
-        if constexpr (kV == 1) {
-            v[0] = bf16_to_f32(x[c]);
-        } else {
-            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(x + c);
+        Raw w = {0, 0, 0, 0};
+        if (n == kVec)
+            __builtin_memcpy(&w, x + c, 16);
+        else
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-            }
+            for (int i = 0; i < kVec; ++i)
+                w[i / 2] |= i < n ? static_cast<uint32_t>(x[c + i]) << (16 * (i % 2)) : 0u;
+        return w;
+    }
+    __device__ __forceinline__ void values(const Raw& w, float (&v)[kVec]) const
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
 };
 
-template <int kV>
+struct Floats {
+    f32x4_t half[2];
+};
+__device__ __forceinline__ void floats_of(const Floats& w, float (&v)[kVec])
+{
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+        v[i] = w.half[i / 4][i % 4];
+}
+
 struct F32Row {
+    using Raw = Floats;
     const float* x;
-    __device__ __forceinline__ void load(int64_t c, float (&v)[kV]) const
+    __device__ __forceinline__ Raw load(int64_t c, int n) const
     {
-        if constexpr (kV == 1) {
-            v[0] = x[c];
+        Raw w = {};
+        if (n == kVec) {
+            __builtin_memcpy(&w, x + c, 32);
         } else {
-            const f32x4_t lo = *reinterpret_cast<const f32x4_t*>(x + c);
-            const f32x4_t hi = *reinterpret_cast<const f32x4_t*>(x + c + 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = lo[i];
-                v[4 + i] = hi[i];
-            }
+            for (int i = 0; i < kVec; ++i)
+                w.half[i / 4][i % 4] = i < n ? x[c + i] : 0.0f;
         }
+        return w;
     }
+    __device__ __forceinline__ void values(const Raw& w, float (&v)[kVec]) const { floats_of(w, v); }
 };
 
-template <class T, template <int> class Row, int kV, int kPer, bool kExactProduct>
+// kT threads per row (kThreads / kT rows per workgroup).
+template <class T, class Row, int kT, int kPer, bool kExactProduct, bool kWhole>
 __global__ __launch_bounds__(kThreads) void int8_quantize_kernel(const T* __restrict__ x, int64_t rows,
                                                                  int64_t cols, int8_t* __restrict__ codes,
                                                                  float* __restrict__ scales)
 {
+    constexpr int kRows = kThreads / kT;
     __shared__ uint32_t buf[2][kThreads / 64];
     int slot = 0;                                        // two slots: a row's maxima are read while the next row's are written
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, slot ^= 1)
-        quantize_row<Row<kV>, kV, kPer, kExactProduct>(Row<kV>{x + r * cols}, cols, codes + r * cols, scales + r, buf[slot]);
+    const int me = threadIdx.x % kT;
+    for (int64_t r = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kT; r < rows;
+         r += static_cast<int64_t>(gridDim.x) * kRows, slot ^= 1)
+        quantize_row<Row, kPer, kExactProduct, kT, kWhole>(Row{x + r * cols}, cols, codes + r * cols, scales + r, buf[slot], me);
 }
 
 // The SwiGLU of a row's gate and up sums, quantised; one workgroup per row, whose sums stay in registers
@@ -261,14 +287,17 @@ __global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
     if (e < 0)
         return;
     struct Values {
+        using Raw = Floats;
         const decltype(sums)* again;
         const i32x4_t (*g)[2];
         const i32x4_t (*u)[2];
         float a_scale;
         const float* sg;
         const float* su;
-        __device__ __forceinline__ void load(int64_t c, float (&v)[kVec]) const
+        __device__ __forceinline__ void values(const Raw& w, float (&v)[kVec]) const { floats_of(w, v); }
+        __device__ __forceinline__ Raw load(int64_t c, int) const   // F is whole vectors
         {
+            Raw w;
             i32x4_t gg[2], uu[2];
             const int64_t i = c / (kT * kVec);
             if (i < kPer) {
@@ -289,14 +318,15 @@ __global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
                 const f32x4_t wu = *reinterpret_cast<const f32x4_t*>(su + c + 4 * q);
 #pragma unroll
                 for (int n = 0; n < 4; ++n)
-                    v[4 * q + n] = swiglu(static_cast<float>(gg[q][n]) * a_scale * wg[n],
+                    w.half[q][n] = swiglu(static_cast<float>(gg[q][n]) * a_scale * wg[n],
                                           static_cast<float>(uu[q][n]) * a_scale * wu[n]);
             }
+            return w;
         }
     };
     const Values src{&sums, g, u, a_scale[gather != nullptr ? gather[r] / gather_k : r], sg + static_cast<int64_t>(e) * F,
                      su + static_cast<int64_t>(e) * F};
-    quantize_row<Values, kVec, kPer, false, kT>(src, F, codes + r * F, scales + r, buf);
+    quantize_row<Values, kPer, false, kT>(src, F, codes + r * F, scales + r, buf, threadIdx.x);
 }
 
 // The four columns from c of row r's product: the partial sums added up, scaled.
@@ -465,7 +495,7 @@ __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
     __shared__ uint32_t buf[kThreads / 64];
     if (blockIdx.x > 0) {
         const int64_t r = blockIdx.x - 1;
-        quantize_row<Bf16Row<kVec>, kVec, 4, true>(Bf16Row<kVec>{x + r * H}, H, codes + r * H, scales + r, buf);
+        quantize_row<Bf16Row, 4, true, kThreads>(Bf16Row{x + r * H}, H, codes + r * H, scales + r, buf, threadIdx.x);
         return;
     }
     static_assert(kInt8SmallSlots <= kThreads && kMaxExperts <= 4 * kThreads, "one slot and four experts a thread");
@@ -550,15 +580,20 @@ __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
     }
 }
 
-template <class T, template <int> class Row, bool kExactProduct>
+// Threads per row: 16 up to 256 columns, a wave up to 2048 (no barrier, and more lanes have values), then
+// the workgroup.  Measured where a workgroup took each row and where a wave does (16384 bfloat16 rows, us):
+// 128 columns 13.8 -> 8.6 (16 threads), 1024 17.1 -> 11.6, 1031 33.4 -> 17.9, 1951 (13918 rows) 34.7 ->
+// 23.6, 2048 21.5 -> 20.5; float32 2048 32.3 -> 32.9; float32 8192: 260 by a wave, 127 by the workgroup.
+template <class T, class Row, bool kExactProduct, bool kWhole>
 hipError_t launch_quantize(const T* x, int64_t rows, int64_t cols, int8_t* codes, float* scales, hipStream_t s)
 {
-    const unsigned grid = static_cast<unsigned>(std::min(rows, kGridRows));
-    const bool aligned = (reinterpret_cast<uintptr_t>(x) & 15) == 0 && (reinterpret_cast<uintptr_t>(codes) & 7) == 0;
-    if (cols % kVec == 0 && aligned)
-        int8_quantize_kernel<T, Row, kVec, 4, kExactProduct><<<dim3(grid), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
+    const auto grid = [&](int per_block) { return dim3(static_cast<unsigned>(std::min(ceil_div(rows, per_block), kGridRows))); };
+    if (cols <= 256)
+        int8_quantize_kernel<T, Row, 16, 2, kExactProduct, kWhole><<<grid(16), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
+    else if (cols <= 2048)
+        int8_quantize_kernel<T, Row, 64, 4, kExactProduct, kWhole><<<grid(4), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
     else
-        int8_quantize_kernel<T, Row, 1, 16, kExactProduct><<<dim3(grid), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
+        int8_quantize_kernel<T, Row, kThreads, 4, kExactProduct, kWhole><<<grid(1), dim3(kThreads), 0, s>>>(x, rows, cols, codes, scales);
     return hipGetLastError();
 }
 
@@ -569,9 +604,14 @@ hipError_t launch_int8_quantize(int dtype, const void* x, int64_t rows, int64_t 
 {
     if (rows <= 0)
         return hipSuccess;
-    if (dtype == MOE_F32)
-        return launch_quantize<float, F32Row, false>(static_cast<const float*>(x), rows, cols, codes, scales, s);
-    return launch_quantize<uint16_t, Bf16Row, true>(static_cast<const uint16_t*>(x), rows, cols, codes, scales, s);
+    if (dtype == MOE_F32) {
+        const auto* v = static_cast<const float*>(x);
+        return cols % kVec == 0 ? launch_quantize<float, F32Row, false, true>(v, rows, cols, codes, scales, s)
+                                : launch_quantize<float, F32Row, false, false>(v, rows, cols, codes, scales, s);
+    }
+    const auto* v = static_cast<const uint16_t*>(x);
+    return cols % kVec == 0 ? launch_quantize<uint16_t, Bf16Row, true, true>(v, rows, cols, codes, scales, s)
+                            : launch_quantize<uint16_t, Bf16Row, true, false>(v, rows, cols, codes, scales, s);
 }
 
 hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const float* a_scale,

@@ -58,6 +58,30 @@ def test_quantize(rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols", [(37, 256), (37, 257), (100, 40), (21, 1032), (21, 2047), (5, 2048), (6, 2056)])
+@pytest.mark.parametrize("shift", [0, 1, 3])
+def test_quantize_rows_at_any_address(rows, cols, shift, dtype):
+    """Rows of each kernel's widths from a base that only its own type aligns."""
+    rng = np.random.default_rng(rows + cols + shift)
+    flat = torch.from_numpy(rng.standard_normal(rows * cols + shift)).to(dtype).cuda()
+    x = flat[shift:].view(rows, cols)
+    codes, scales = mel.int8_quantize(x)
+    torch.cuda.synchronize()
+    q, s = ref.quantize(_host(x))
+    assert np.array_equal(codes.cpu().numpy().astype(np.float64), q)
+    assert np.all(np.abs(scales.cpu().numpy() - s) <= U * s + 2.0 ** -149)
+
+
+def test_quantize_more_rows_than_a_grid_has():
+    """Rows of one column: the code is the value's sign times 127, the scale its 127th part."""
+    x = torch.randn((1 << 25) + 5, 1, device="cuda").to(torch.bfloat16)
+    codes, scales = mel.int8_quantize(x)
+    assert torch.equal(codes.float(), 127 * torch.sign(x.float()))
+    want = x.double().abs().view(-1) / 127
+    assert bool(((scales.double() - want).abs() <= U * want + 2.0 ** -149).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_quantize_halves_extremes_and_zero_rows(dtype):
     """Quotients that are exactly a half (ties to even), float32 neighbours of a half, the largest and
     the smallest values of the type, and rows of zeros."""
