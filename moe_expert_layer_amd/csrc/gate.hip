@@ -110,6 +110,9 @@ struct Max {
 struct MinU {
     __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return min(a, b); }
 };
+struct MaxU {
+    __device__ __forceinline__ uint32_t operator()(uint32_t a, uint32_t b) const { return max(a, b); }
+};
 
 // exp2 on the hardware unit (1 ulp) of x log2 e; the product's rounding makes it |x| 2^-24 relative.
 __device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.4426950408889634f); }
@@ -234,7 +237,7 @@ __device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int
     double my_num = 0.0;
     for (int j = 0; j < a.k; ++j) {
         uint64_t best = 0;
-        int id = 0;
+        uint32_t id = 0;
         double n = 0.0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
@@ -243,24 +246,20 @@ __device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int
                 id = lane + 64 * i;
                 n = num[i];
             }
-#pragma unroll
-        for (int off = 32; off >= 1; off >>= 1) {
-            const uint64_t ob = __shfl_xor(static_cast<unsigned long long>(best), off);
-            const int oi = __shfl_xor(id, off);
-            const double on = __shfl_xor(n, off);
-            if (ob > best || (ob == best && oi < id)) {
-                best = ob;
-                id = oi;
-                n = on;
-            }
-        }
+        // the largest key by halves, then the lowest id that has it
+        const uint32_t hi = reduce<64>(static_cast<uint32_t>(best >> 32), MaxU{});
+        const uint32_t low = static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0;
+        const uint32_t lo = reduce<64>(low, MaxU{});
+        const bool tops = best == (static_cast<uint64_t>(hi) << 32 | lo);
+        const uint32_t first = reduce<64>(tops ? id : ~0u, MinU{});
+        const double won = __shfl(n, __ffsll(static_cast<unsigned long long>(__ballot(tops && id == first))) - 1);
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
-            if (lane + 64 * i == id)
+            if (static_cast<uint32_t>(lane + 64 * i) == first)
                 key[i] = 0;
         if (lane == j) {
-            my_id = id;
-            my_num = n;
+            my_id = static_cast<int>(first);
+            my_num = won;
         }
     }
     if (a.renormalize) {
@@ -779,26 +778,27 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
     return hipSuccess;
 }
 
-// The gate's lanes per token.  Few tokens: four experts a lane (shortest rounds).  Many: up to 16 experts
-// a lane, since what a round costs beside the keys themselves (the exchanges, the winner) is then
-// shared by more tokens of the wave (65536 tokens of 256 experts, 8 groups: 16 lanes 47 us, 8 lanes of 32
-// experts the same, at 142 registers).  Taken from two waves a SIMD on.
+// The gate's lanes per token.  Four experts a lane where possible: shortest rounds.  With many tokens of more
+// than 32 experts, up to 16 experts a lane: what a round costs beside the keys themselves (the exchanges,
+// the winner) is then shared by more tokens of the wave.  Measured (us, four experts a lane / 16): 65536
+// tokens of 32 experts 10 / 12, of 64 18 / 15, of 256 54 / 26; 8192 tokens of 64 experts 7.3 / 8.4, of 256
+// 11.6 / 10.4: taken from 32 waves a CU on.
 template <class In>
 hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
 {
-    const int few = a.E <= 8 ? 2 : a.E <= 16 ? 4 : a.E <= 32 ? 8 : a.E <= 64 ? 16 : a.E <= 128 ? 32 : 64;
-    const int lanes = a.E <= 16 ? 1 : a.E <= 32 ? 2 : a.E <= 64 ? 4 : a.E <= 128 ? 8 : a.E <= 256 ? 16 : 32;
+    if (a.E <= 8)
+        return launch_gate_n<In, 2, 1>(logits, a, s);
+    if (a.E <= 16)
+        return launch_gate_n<In, 4, 1>(logits, a, s);
+    if (a.E <= 32)
+        return launch_gate_n<In, 8, 1>(logits, a, s);
+    const int few = a.E <= 64 ? 16 : a.E <= 128 ? 32 : 64;
+    const int lanes = a.E <= 64 ? 4 : a.E <= 128 ? 8 : a.E <= 256 ? 16 : 32;
+    // groups as vectors, or at least no more groups than lanes, if the wider layout can have that
     const int per = a.E / a.groups;
-    // groups as vectors, or at least no more groups than lanes, if the few-token layout can have that
     const bool fits = a.topk_groups == a.groups || group_shift(per, lanes) >= 0 ||
                       (group_shift(per, few) < 0 && (a.groups <= lanes || a.groups > few));
-    const bool many = fits && ceil_div(a.T * few, 64) >= 8 * device_info().cu_count;
-    if (a.E <= 8)
-        return many ? launch_gate_n<In, 1, 2>(logits, a, s) : launch_gate_n<In, 2, 1>(logits, a, s);
-    if (a.E <= 16)
-        return many ? launch_gate_n<In, 1, 4>(logits, a, s) : launch_gate_n<In, 4, 1>(logits, a, s);
-    if (a.E <= 32)
-        return many ? launch_gate_n<In, 2, 4>(logits, a, s) : launch_gate_n<In, 8, 1>(logits, a, s);
+    const bool many = fits && ceil_div(a.T * few, 64) >= 32 * device_info().cu_count;
     if (a.E <= 64)
         return many ? launch_gate_n<In, 4, 4>(logits, a, s) : launch_gate_n<In, 16, 1>(logits, a, s);
     if (a.E <= 128)

@@ -77,7 +77,9 @@ def test_gate(T, E, k, groups, topk_groups, score):
                        renormalize=renorm, scale=2.5)
 
 
-@pytest.mark.parametrize("E,k,groups,topk_groups,T", [(8, 2, 1, 1, 70001), (6, 3, 1, 1, 66000), (16, 4, 4, 2, 40000),
+@pytest.mark.parametrize("E,k,groups,topk_groups,T", [(64, 8, 8, 3, 33000), (128, 8, 4, 2, 16500), (256, 8, 8, 4, 8200),
+                                                     (250, 6, 2, 1, 8300), (500, 10, 1, 1, 8200), (64, 64, 1, 1, 33000),
+                                                     (120, 6, 8, 3, 17000), (8, 2, 1, 1, 70001), (6, 3, 1, 1, 66000), (16, 4, 4, 2, 40000),
                                                      (30, 5, 1, 1, 20000), (64, 8, 8, 3, 9000), (128, 8, 4, 2, 5000),
                                                      (256, 8, 8, 4, 3001), (256, 8, 4, 2, 3000), (256, 6, 1, 1, 2500),
                                                      (500, 10, 1, 1, 2100), (120, 6, 8, 3, 5000), (74, 5, 2, 1, 6000),
