@@ -290,8 +290,9 @@ moe_status moe_grouped_ffn_int8(const moe_problem* p, const int8_t* rows, const 
  * (MOE_BF16 or MOE_F32).  Groups as for moe_grouped_ffn (a group expert outside [0, E) skips the
  * group and sets the status word); rows that no group holds are left as they were.  The sum is exact
  * int32; one conversion to float32, two float32 products, one rounding to out_dtype.
- * K and N multiples of 128, K <= 130944, N <= MOE_MAX_HIDDEN, E < 1024, M < 2^31, G <= 2^24.  All pointers
- * aligned to 16 bytes. */
+ * K and N multiples of 128, K <= 130944, N <= MOE_MAX_HIDDEN, E < 1024, M < 2^31, G <= 2^24.  The rows, the
+ * weights, their scales, out and the workspace are aligned to 16 bytes.  Offsets should not fall: in the
+ * int8 calls a group begins no earlier than any offset before it. */
 moe_status moe_grouped_matmul_int8_workspace_size(int64_t M, int64_t G, int64_t K, int64_t N,
                                                   size_t* bytes /* host */);
 moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows_scale, int64_t M,

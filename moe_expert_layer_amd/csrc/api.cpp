@@ -478,15 +478,14 @@ moe_status run_ffn(int dtype, const void* rows, const uint8_t* rows_scale, int64
     return MOE_OK;
 }
 
-// Workspace of the int8 calls.  Tile tables of both forms (build_tiles writes the first, the kernels
-// take the second: each group one run of balanced tiles), h as float32 or as partial sums, its codes
-// and scales, the partial sums of y, and for the layer the routing, the quantised x and the rows y.
+// Workspace of the int8 calls: the tile table (each group one run of balanced tiles), h as float32 or as
+// partial sums, its codes and scales, the partial sums of y, and for the layer the routing, the quantised
+// x and the rows y.
 struct Int8Layout {
     RouteLayout route;
     Int8Plan fc1{}, fc2{};
     size_t counts = 0, offsets = 0, perm = 0, pos = 0, row_experts = 0, tile_count = 0, task_ctr = 0, tiles = 0;
-    size_t tiles_run = 0, h = 0, h_q = 0, h_scale = 0, y_part = 0, x_q = 0, x_q_scale = 0, y = 0, total = 0;
-    int64_t max_tiles = 0;
+    size_t h = 0, h_q = 0, h_scale = 0, y_part = 0, x_q = 0, x_q_scale = 0, y = 0, total = 0;
 };
 
 struct Take {
@@ -516,11 +515,9 @@ Int8Layout int8_layout(int64_t M, int64_t G, int64_t H, int64_t F, int64_t T, in
         L.x_q_scale = take(4 * T);
         L.y = take(2 * M * H);
     }
-    L.max_tiles = max_mtiles(M, G, 0, L.fc1.row_tile);
-    L.tile_count = take(8 * 4);
+    L.tile_count = take(4);
     L.task_ctr = take(2 * kXcdCount * 4);
-    L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
-    L.tiles_run = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
+    L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * max_mtiles(M, G, 0, L.fc1.row_tile));
     L.h = take(4 * M * F * (L.fc1.partial ? 2 * L.fc1.splits : 1));
     L.h_q = take(M * F);
     L.h_scale = take(4 * M);
@@ -543,39 +540,20 @@ struct Int8Weights {
     const float *gate_scale, *up_scale, *down_scale;
 };
 
-// The tile table of the int8 products, in tiles_run and count[4]; the general builder, for more groups
-// than the one-workgroup kernel takes, needs room for its other table too.
-moe_status int8_tiles(const int32_t* offsets, const int32_t* group_expert, int64_t G, int64_t E, int64_t M, int bm,
-                      MTile* tiles, MTile* tiles_run, int64_t max_tiles, int32_t* count, int32_t* task_ctr,
-                      int32_t* status, bool write_status, hipStream_t s)
-{
-    if (G <= kInt8TileGroups)
-        LAUNCH(s, "int8_tiles",
-               launch_int8_tiles(offsets, group_expert, G, E, M, bm, tiles_run, count + 4, task_ctr, status, write_status, s));
-    else
-        LAUNCH(s, "build_tiles",
-               launch_build_tiles(offsets, group_expert, G, E, M, std::max<int64_t>(M, 1), bm, tiles, max_tiles, count,
-                                  nullptr, nullptr, 1, 0, task_ctr, status, write_status, s, tiles_run, count + 4));
-    return MOE_OK;
-}
-
 // fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.  row_experts
-// (may be null): the small layer's preparation has run, the tile table is there and each row's expert.  y null: the down projection's partial sums (L.fc2.partial) stay for the
-// caller.
+// (may be null): the small layer's preparation has run, the tile table is there and each row's expert.
+// y null: the down projection's partial sums (L.fc2.partial) stay for the caller.
 moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, const int32_t* offsets,
                         const int32_t* group_expert, int64_t G, int64_t E, int64_t H, int64_t F,
                         const Int8Weights& w, void* y, void* ws, const Int8Layout& L, bool write_status,
                         hipStream_t s, const int32_t* gather, int gather_k, const int32_t* row_experts)
 {
-    int32_t* tcount = at<int32_t>(ws, L.tile_count);
-    MTile* tiles = at<MTile>(ws, L.tiles_run);
-    const int32_t* count = tcount + 4;
+    int32_t* count = at<int32_t>(ws, L.tile_count);
+    MTile* tiles = at<MTile>(ws, L.tiles);
     if (row_experts == nullptr)
-        if (moe_status st = int8_tiles(offsets, group_expert, G, E, M, L.fc1.row_tile, at<MTile>(ws, L.tiles), tiles,
-                                       L.max_tiles, tcount, at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0),
-                                       write_status, s);
-            st != MOE_OK)
-            return st;
+        LAUNCH(s, "int8_tiles",
+               launch_int8_tiles(offsets, group_expert, G, E, M, L.fc1.row_tile, tiles, count, at<int32_t>(ws, L.task_ctr),
+                                 at<int32_t>(ws, 0), write_status, s));
     int8_t* h_q = at<int8_t>(ws, L.h_q);
     float* h_scale = at<float>(ws, L.h_scale);
     LAUNCH(s, "fc1_i8",
@@ -786,7 +764,7 @@ MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, 
         LAUNCH(s, "int8_prologue",
                launch_int8_prologue(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos,
                                     at<int32_t>(ws, L.row_experts), at<int32_t>(ws, 0),
-                                    L.fc1.row_tile, at<MTile>(ws, L.tiles_run), at<int32_t>(ws, L.tile_count) + 4,
+                                    L.fc1.row_tile, at<MTile>(ws, L.tiles), at<int32_t>(ws, L.tile_count),
                                     quantize_x ? static_cast<const uint16_t*>(x) : nullptr, H, at<int8_t>(ws, L.x_q),
                                     at<float>(ws, L.x_q_scale), s));
     } else {
@@ -1182,20 +1160,17 @@ namespace {
 
 struct MatmulLayout {
     Int8Plan plan{};
-    size_t tile_count = 0, task_ctr = 0, tiles = 0, tiles_run = 0, part = 0, total = 0;
-    int64_t max_tiles = 0;
+    size_t tile_count = 0, task_ctr = 0, tiles = 0, part = 0, total = 0;
 };
 
 MatmulLayout matmul_layout(int64_t M, int64_t G, int64_t K, int64_t N)
 {
     MatmulLayout L;
     L.plan = int8_plan(M, G, K, N);
-    L.max_tiles = max_mtiles(M, G, 0, L.plan.row_tile);
     Take take{kAlign};
-    L.tile_count = take(8 * 4);
+    L.tile_count = take(4);
     L.task_ctr = take(2 * kXcdCount * 4);
-    L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
-    L.tiles_run = take(static_cast<int64_t>(sizeof(MTile)) * L.max_tiles);
+    L.tiles = take(static_cast<int64_t>(sizeof(MTile)) * max_mtiles(M, G, 0, L.plan.row_tile));
     if (L.plan.partial)
         L.part = take(4 * M * N * L.plan.splits);
     L.total = take.off;
@@ -1245,17 +1220,16 @@ MOE_API moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows
         return st;
     hipStream_t s = stream;
     void* ws = workspace;
-    int32_t* tcount = at<int32_t>(ws, L.tile_count);
-    MTile* tiles = at<MTile>(ws, L.tiles_run);
-    if (moe_status st = int8_tiles(group_offsets, group_expert, G, E, M, L.plan.row_tile, at<MTile>(ws, L.tiles), tiles,
-                                   L.max_tiles, tcount, at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), true, s);
-        st != MOE_OK)
-        return st;
+    int32_t* count = at<int32_t>(ws, L.tile_count);
+    MTile* tiles = at<MTile>(ws, L.tiles);
+    LAUNCH(s, "int8_tiles",
+           launch_int8_tiles(group_offsets, group_expert, G, E, M, L.plan.row_tile, tiles, count,
+                             at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), true, s));
     if (M == 0)
         return MOE_OK;
     LAUNCH(s, "matmul_i8",
            launch_gemm_i8(L.plan, rows, rows_scale, w, w_scale, nullptr, nullptr,
-                          L.plan.partial ? at<void>(ws, L.part) : out, out_dtype, M, K, N, tiles, tcount + 4, nullptr,
+                          L.plan.partial ? at<void>(ws, L.part) : out, out_dtype, M, K, N, tiles, count, nullptr,
                           1, at<int32_t>(ws, L.task_ctr), s));
     if (L.plan.partial)
         LAUNCH(s, "int8_finish",

@@ -49,8 +49,7 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
                                       const int32_t* group_expert, int64_t G, int64_t E, int64_t M,
                                       int64_t F, int8_t* codes, float* scales, hipStream_t s);
 // The table of balanced row tiles alone (the in-run table of launch_build_tiles, with its count at
-// tile_count, the counters and the status word as there), for at most kInt8TileGroups groups.
-constexpr int kInt8TileGroups = 1024;
+// tile_count, the counters and the status word as there), at most max_mtiles of them whatever the offsets.
 hipError_t launch_int8_tiles(const int32_t* offsets, const int32_t* group_expert, int64_t G, int64_t E, int64_t M,
                              int bm, MTile* tiles, int32_t* tile_count, int32_t* task_ctr, int32_t* status,
                              bool write_status, hipStream_t s);

@@ -19,7 +19,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;       // of most kernels; one row's quantisation takes kWideThreads where rows are few
-constexpr int kWideThreads = kInt8TileGroups;
+constexpr int kWideThreads = 1024;
 constexpr int kVec = 8;
 constexpr uint32_t kInfBits = 0x7f800000u;
 
@@ -416,65 +416,85 @@ __device__ __forceinline__ MTile balanced_tile(int expert, int begin, int n, int
     return t;
 }
 
-// The table of balanced tiles alone, for at most kWideThreads groups: a thread per group, a scan, then a
-// thread per tile, which finds its group by bisection.  One workgroup, three barriers (8 groups 3 us
-// where the general builder with its two tables takes 5.5).
+// The table of balanced tiles alone: a thread per group (kWideThreads of them at a time), a scan, then a
+// thread per tile, which finds its group by bisection.  One workgroup, few barriers (8 groups 4.8 us, 128
+// groups 5.6 us, where the general builder with its two tables takes 5.5 and 9.4).  A group begins no
+// earlier than any offset before it, so that no row is in two groups and the tiles fit the table
+// whatever the offsets.
 __global__ __launch_bounds__(kWideThreads) void int8_tiles_kernel(
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ group_expert, int G, int E, int64_t M, int bm,
     MTile* __restrict__ tiles, int32_t* __restrict__ tile_count, int32_t* __restrict__ task_ctr,
     int32_t* __restrict__ status, int write_status)
 {
+    constexpr int kWaves = kWideThreads / 64;
     __shared__ int first[kWideThreads + 1], begin[kWideThreads], rows[kWideThreads], expert[kWideThreads];
-    __shared__ int wave_sum[kWideThreads / 64];
-    const int g = threadIdx.x, lane = g & 63, wave = g >> 6;
-    int64_t rb = 0, re = 0;
-    int e = 0;
+    __shared__ int wave_max[kWaves], wave_sum[kWaves];
+    const int me = threadIdx.x, lane = me & 63, wave = me >> 6, limit = static_cast<int>(M);
+    int done = 0, reached = 0;                                // tiles and largest offset of the groups so far
     bool bad = false;
-    if (g < G) {
-        rb = min(max(static_cast<int64_t>(offsets[g]), int64_t{0}), M);
-        re = min(max(static_cast<int64_t>(offsets[g + 1]), rb), M);
-        e = group_expert != nullptr ? group_expert[g] : g;
-        if (e < 0 || e >= E) {
-            bad = re > rb;
-            re = rb;                                          // skipped
-        }
-    }
-    const int n = static_cast<int>(re - rb);
-    const int mine = (n + bm - 1) / bm;
-    int before = mine;
+    if (me < 2 * kXcdCount)
+        task_ctr[me] = 0;
+    for (int base = 0; base < G; base += kWideThreads) {
+        const int held = min(G - base, kWideThreads);
+        const bool mine = me < held;
+        const int g = base + (mine ? me : 0);
+        const int o = mine ? min(max(offsets[g], 0), limit) : 0;
+        const int end = mine ? min(max(offsets[g + 1], 0), limit) : 0;
+        int e = mine ? (group_expert != nullptr ? group_expert[g] : g) : 0;
+        int rb = o;
 #pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const int v = __shfl_up(before, off);
-        before += lane >= off ? v : 0;
-    }
-    if (lane == 63)
-        wave_sum[wave] = before;
-    const int any_bad = __syncthreads_or(bad ? 1 : 0);
-    for (int w = 0; w < wave; ++w)
-        before += wave_sum[w];
-    first[g + 1] = before;
-    if (g == 0)
-        first[0] = 0;
-    begin[g] = static_cast<int>(rb);
-    rows[g] = n;
-    expert[g] = e;
-    if (g < 2 * kXcdCount)
-        task_ctr[g] = 0;
-    __syncthreads();
-    const int total = first[kWideThreads];
-    for (int t = g; t < total; t += kWideThreads) {
-        int lo = 0, hi = G - 1;                               // the last group whose first tile is at most t
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (first[mid] <= t)
-                lo = mid;
-            else
-                hi = mid - 1;
+        for (int off = 1; off < 64; off <<= 1)
+            rb = max(rb, __shfl_up(rb, off));                 // a lane below `off` gets its own value
+        if (lane == 63)
+            wave_max[wave] = rb;
+        __syncthreads();
+        rb = max(rb, reached);
+        for (int w = 0; w < kWaves; ++w) {
+            rb = w < wave ? max(rb, wave_max[w]) : rb;
+            reached = max(reached, wave_max[w]);
         }
-        tiles[t] = balanced_tile(expert[lo], begin[lo], rows[lo], first[lo + 1] - first[lo], t - first[lo], first[lo]);
+        int n = max(end - rb, 0);
+        if (e < 0 || e >= E) {
+            bad |= n > 0;
+            n = 0;                                            // skipped
+        }
+        const int count = (n + bm - 1) / bm;
+        int before = count;
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const int v = __shfl_up(before, off);
+            before += lane >= off ? v : 0;
+        }
+        if (lane == 63)
+            wave_sum[wave] = before;
+        __syncthreads();
+        for (int w = 0; w < wave; ++w)
+            before += wave_sum[w];
+        first[me + 1] = before;
+        if (me == 0)
+            first[0] = 0;
+        begin[me] = rb;
+        rows[me] = n;
+        expert[me] = e;
+        __syncthreads();
+        const int total = first[kWideThreads];
+        for (int t = me; t < total; t += kWideThreads) {
+            int lo = 0, hi = held - 1;                        // the last group whose first tile is at most t
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) / 2;
+                if (first[mid] <= t)
+                    lo = mid;
+                else
+                    hi = mid - 1;
+            }
+            tiles[done + t] = balanced_tile(expert[lo], begin[lo], rows[lo], first[lo + 1] - first[lo], t - first[lo], done + first[lo]);
+        }
+        done += total;
+        __syncthreads();                                      // read before the next groups are written
     }
-    if (g == 0) {
-        *tile_count = total;
+    const int any_bad = __syncthreads_or(bad ? 1 : 0);
+    if (me == 0) {
+        *tile_count = done;
         if (write_status)
             *status = any_bad ? MOE_ERR_EXPERT_ID_OUT_OF_RANGE : MOE_OK;
         else if (any_bad)
@@ -624,7 +644,7 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
         return hipSuccess;
     const dim3 grid = row_grid(M);
     const int g = static_cast<int>(G), e = static_cast<int>(E);
-    // few rows: a whole CU's threads for each (2 rows of 14336: 16.8 -> 6 us)
+    // few rows: a whole CU's threads for each (2 rows of 14336: 16.8 -> 7.3 us)
     if (M <= 2 * device_info().cu_count)
         int8_swiglu_partial_kernel<kWideThreads, 2><<<grid, dim3(kWideThreads), 0, s>>>(
             partial, splits, a_scale, gather, gather_k, sg, su, row_experts, offsets, group_expert, g, e, M, F, codes, scales);
@@ -638,8 +658,6 @@ hipError_t launch_int8_tiles(const int32_t* offsets, const int32_t* group_expert
                              int bm, MTile* tiles, int32_t* tile_count, int32_t* task_ctr, int32_t* status,
                              bool write_status, hipStream_t s)
 {
-    if (G > kWideThreads)
-        return hipErrorInvalidValue;
     int8_tiles_kernel<<<dim3(1), dim3(kWideThreads), 0, s>>>(offsets, group_expert, static_cast<int>(G),
                                                              static_cast<int>(E), M, bm, tiles, tile_count, task_ctr,
                                                              status, write_status ? 1 : 0);

@@ -127,7 +127,7 @@ PRODUCTS = [
     ([5] * 100, 128, 128),
     ([700, 0, 900], 128, 256),
     ([3] * 300, 256, 640),                                   # several tasks per workgroup, two steps each
-    ([2, 0, 1] * 400, 128, 128),                             # more groups than the short tile builder takes
+    ([2, 0, 1] * 400, 128, 128),                             # more groups than one pass of the tile builder takes
     ([1] * 1024, 128, 128),
     ([2], 16384, 256),                                       # 64 rows, 16 cuts
     ([30, 0, 64, 7], 2048, 384),                             # cuts
@@ -208,6 +208,36 @@ def test_matmul_leaves_other_rows_alone_and_skips_bad_experts(counts):
     for g in range(2):
         r = ref.matmul(rows[off[g]:off[g + 1]], rs[off[g]:off[g + 1]], w[expert[g]], wsc[expert[g]])
         assert np.all(np.abs(got[off[g]:off[g + 1]] - r) <= (4 * U + BF) * np.abs(r))
+
+
+@pytest.mark.parametrize("rows,groups", [(90, 3), (90, 1500), (700, 64), (2000, 3000)])
+def test_matmul_offsets_that_fall(rows, groups):
+    """Offsets 0, M, 0, M, ...: every second group would hold all rows.  The first keeps them."""
+    rng = np.random.default_rng(rows + groups)
+    K, N = 256, 256
+    off = np.array([rows * (g % 2) for g in range(groups + 1)], np.int32)
+    a, w, rs, wsc = _codes(rng, rows, K), _codes(rng, 2, K, N), _scale(rng, rows), _scale(rng, 2, N)
+    out = mel.grouped_matmul_int8(*_dev(a, rs, off, np.arange(groups, dtype=np.int32) % 2, w, wsc))
+    r = ref.matmul(a, rs, w[0], wsc[0])
+    assert np.all(np.abs(_host(out) - r) <= (4 * U + BF) * np.abs(r))
+
+
+def test_matmul_of_thousands_of_groups():
+    """Three passes of the tile builder, empty groups at their borders."""
+    rng = np.random.default_rng(77)
+    counts = rng.integers(0, 3, 2100)
+    counts[[0, 1023, 1024, 2047, 2048, 2099]] = 0
+    counts[[1022, 1025, 2049]] = [70, 130, 65]
+    K, N, E = 128, 128, 9
+    off, M = _offsets(counts), int(counts.sum())
+    expert = rng.integers(0, E, len(counts)).astype(np.int32)
+    a, w, rs, wsc = _codes(rng, M, K), _codes(rng, E, K, N), _scale(rng, M), _scale(rng, E, N)
+    out = _host(mel.grouped_matmul_int8(*_dev(a, rs, off, expert, w, wsc)))
+    row_expert = np.repeat(expert, counts)
+    for e in range(E):
+        at = row_expert == e
+        r = ref.matmul(a[at], rs[at], w[e], wsc[e])
+        assert np.all(np.abs(out[at] - r) <= (4 * U + BF) * np.abs(r))
 
 
 def test_matmul_nan_scale_marks_its_row_alone():
