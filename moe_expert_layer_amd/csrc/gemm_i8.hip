@@ -15,6 +15,11 @@
 // a step.  A rows lie in LDS as in memory, 16-byte chunks XOR-swizzled by row; the weights lie as in
 // memory ([K, N], N contiguous), and the transposing LDS read (ds_read_b64_tr_b8) hands each lane 8
 // consecutive k of its column.
+//
+// Few rows are bound by the weights' bytes: 64-row tiles, copies that run ahead across a workgroup's tasks
+// and K cut until the CUs are evenly busy (1000 rows on 128 experts of 2048 x 768: gate and up 72 us for
+// at most 403 MB, 5.6 TB/s).  Many rows are bound by the matrix instructions: 256-row tiles (16384 rows, 2
+// experts of 4096 x 14336: 0.86-0.93 ms, 2.1-2.2 POP/s).  product_cost below chooses.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -396,6 +401,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
 // lines); three steps are in flight.  Each step's MFMAs run in two halves around its one barrier
 // (weight blocks 0-1, then 2-3), each followed by its share of the step's copies and fragment reads.
 // Tasks are claimed per XCD, and the next task's first copies go out before the current epilogue.
+// Measured against the ring kernel above with 256-row tiles: 16384 x 4096 x 14336 1.07 -> 0.92 ms, 65536
+// rows on 32 experts of 7168 x 2048 1.95 -> 1.63 ms (gate and up) and 1.28 -> 1.02 ms (down).
 namespace big {
 
 constexpr int kWM = 4, kWN = 2, kTM = 2, kTN = 4;
