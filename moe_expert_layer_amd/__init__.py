@@ -132,9 +132,10 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-# The current stream's handle by device index; the plain query builds a Stream object, which costs more
-# than the rest of a small call.
+# The current stream's handle by device index, and the current device's index; the plain queries build
+# a Stream object, which costs more than the rest of a small call, and look again whether CUDA is set up.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(t: torch.Tensor):
@@ -146,7 +147,7 @@ def _stream(t: torch.Tensor):
 def _call(name: str, device, *args):
     """Calls the library with `device` current, and raises on its error."""
     fn = getattr(_lib or library(), name)
-    if torch.cuda.current_device() == device.index:
+    if _current_device() == device.index:
         status = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -164,7 +165,7 @@ def _need(t: torch.Tensor, name: str, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -569,8 +570,8 @@ def int8_quantize(x):
     _need(x, "x")
     dt = _dtype_code(x)
     rows, cols = x.shape
-    codes = torch.empty((rows, cols), dtype=torch.int8, device=x.device)
-    scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    codes = x.new_empty((rows, cols), dtype=torch.int8)
+    scales = x.new_empty(rows, dtype=torch.float32)
     _call("moe_int8_quantize", x.device, _ptr(x), dt, rows, cols, _ptr(codes), _ptr(scales), _stream(x))
     return codes, scales
 
@@ -599,8 +600,9 @@ def router_gate(logits, k: int, score: str = "softmax", bias=None, groups: int =
         _need(bias, "bias", torch.float32, (E,), logits.device)
     gate = _gate(score, int(bool(renormalize)), int(groups), int(topk_groups), int(group_top), float(scale))
     k = int(k)
-    ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
-    probs = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    size = (T, k if k > 0 else 0)
+    ids = logits.new_empty(size, dtype=torch.int32)
+    probs = logits.new_empty(size, dtype=torch.float32)
     _call("moe_router_gate", logits.device,
           ctypes.byref(gate), _ptr(logits), dt, _ptr(bias), T, E, k, _ptr(ids), _ptr(probs), _stream(logits))
     return ids, probs
