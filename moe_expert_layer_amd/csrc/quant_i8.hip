@@ -118,7 +118,8 @@ __device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets,
 }
 
 // A row by kT threads (`me` among them; a part of a wave, or the workgroup).  The row's values come from
-// Src::load, eight neighbouring ones at a time (fewer at the row's end); the first kPer vectors of a thread
+// Src::load (the thread's vector i < kPer, or kPer: the one at a column), eight neighbouring ones at a time (fewer
+// at the row's end); the first kPer vectors of a thread
 // stay in registers between the maximum and the codes, as loaded (bfloat16 rows need half the registers
 // that way: 56 for 96, eight waves a SIMD for five), later ones are made again.  kWhole: cols is a multiple
 // of eight.
@@ -140,12 +141,12 @@ __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_
     for (int i = 0; i < kPer; ++i) {
         const int64_t c = (static_cast<int64_t>(i) * kT + me) * kVec;
         if (c < cols) {
-            keep[i] = src.load(c, count(c));
+            keep[i] = src.load(i, c, count(c));
             take(keep[i]);
         }
     }
     for (int64_t c = (static_cast<int64_t>(kPer) * kT + me) * kVec; c < cols; c += kT * kVec) {
-        take(src.load(c, count(c)));
+        take(src.load(kPer, c, count(c)));
     }
     const RowCode rc = row_code(row_max<kT>(amax, buf));
     const auto store = [&](int64_t c, const typename Src::Raw& raw) {
@@ -171,7 +172,7 @@ __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_
             store(c, keep[i]);
     }
     for (int64_t c = (static_cast<int64_t>(kPer) * kT + me) * kVec; c < cols; c += kT * kVec) {
-        store(c, src.load(c, count(c)));
+        store(c, src.load(kPer, c, count(c)));
     }
     if (me == 0)
         *scale = rc.scale;
@@ -181,7 +182,7 @@ __device__ __forceinline__ void quantize_row(const Src& src, int64_t cols, int8_
 struct Bf16Row {
     using Raw = u32x4_t;
     const uint16_t* x;
-    __device__ __forceinline__ Raw load(int64_t c, int n) const
+    __device__ __forceinline__ Raw load(int, int64_t c, int n) const
     {
         Raw w = {0, 0, 0, 0};
         if (n == kVec)
@@ -215,7 +216,7 @@ __device__ __forceinline__ void floats_of(const Floats& w, float (&v)[kVec])
 struct F32Row {
     using Raw = Floats;
     const float* x;
-    __device__ __forceinline__ Raw load(int64_t c, int n) const
+    __device__ __forceinline__ Raw load(int, int64_t c, int n) const
     {
         Raw w = {};
         if (n == kVec) {
@@ -276,13 +277,21 @@ __global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
                 u[q] += *reinterpret_cast<const i32x4_t*>(p + s * cut + F + c + 4 * q);
             }
     };
+    const int64_t source = gather != nullptr ? gather[r] : r;
     i32x4_t g[kPer][2], u[kPer][2];
+    for (int s = 0; s < splits; ++s)                          // the loads of a cut go out together
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        const int64_t c = (static_cast<int64_t>(i) * kT + threadIdx.x) * kVec;
-        if (c < F)
-            sums(c, g[i], u[i]);
-    }
+        for (int i = 0; i < kPer; ++i) {
+            const int64_t c = (static_cast<int64_t>(i) * kT + threadIdx.x) * kVec;
+            if (c < F)
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const i32x4_t mine = *reinterpret_cast<const i32x4_t*>(p + s * cut + c + 4 * q);
+                    const i32x4_t other = *reinterpret_cast<const i32x4_t*>(p + s * cut + F + c + 4 * q);
+                    g[i][q] = s == 0 ? mine : g[i][q] + mine;
+                    u[i][q] = s == 0 ? other : u[i][q] + other;
+                }
+        }
     const int e = row_experts != nullptr ? row_experts[r] : row_expert(offsets, group_expert, G, E, M, r, &found);
     if (e < 0)
         return;
@@ -295,20 +304,16 @@ __global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
         const float* sg;
         const float* su;
         __device__ __forceinline__ void values(const Raw& w, float (&v)[kVec]) const { floats_of(w, v); }
-        __device__ __forceinline__ Raw load(int64_t c, int) const   // F is whole vectors
+        __device__ __forceinline__ Raw load(int i, int64_t c, int) const   // F is whole vectors
         {
             Raw w;
             i32x4_t gg[2], uu[2];
-            const int64_t i = c / (kT * kVec);
             if (i < kPer) {
 #pragma unroll
-                for (int n = 0; n < kPer; ++n)
-                    if (n == i)
-#pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            gg[q] = g[n][q];
-                            uu[q] = u[n][q];
-                        }
+                for (int q = 0; q < 2; ++q) {
+                    gg[q] = g[i][q];
+                    uu[q] = u[i][q];
+                }
             } else {
                 (*again)(c, gg, uu);
             }
@@ -324,20 +329,36 @@ __global__ __launch_bounds__(kT) void int8_swiglu_partial_kernel(
             return w;
         }
     };
-    const Values src{&sums, g, u, a_scale[gather != nullptr ? gather[r] / gather_k : r], sg + static_cast<int64_t>(e) * F,
+    const Values src{&sums, g, u, a_scale[gather != nullptr ? source / gather_k : r], sg + static_cast<int64_t>(e) * F,
                      su + static_cast<int64_t>(e) * F};
     quantize_row<Values, kPer, false, kT>(src, F, codes + r * F, scales + r, buf, threadIdx.x);
 }
 
-// The four columns from c of row r's product: the partial sums added up, scaled.
-__device__ __forceinline__ f32x4_t finish4(const int32_t* __restrict__ partial, int splits, int64_t cut, int64_t at,
-                                           float a_scale, const float* __restrict__ w_scale)
+// Four columns' partial sums of all cuts (from part[i], cut apart) added up, for kRows rows.  A cut past the last
+// is read as the last one and not added, so that the loads go out together, not one after the other.
+template <int kRows, int kTogether>
+__device__ __forceinline__ void add_cuts(const int32_t* const (&part)[kRows], int splits, int64_t cut, i32x4_t (&a)[kRows])
 {
-    i32x4_t a = *reinterpret_cast<const i32x4_t*>(partial + at);
-#pragma unroll 4
-    for (int s = 1; s < splits; ++s)
-        a += *reinterpret_cast<const i32x4_t*>(partial + s * cut + at);
-    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(w_scale);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+        a[i] = *reinterpret_cast<const i32x4_t*>(part[i]);
+    for (int s = 1; s < splits; s += kTogether) {
+        i32x4_t v[kRows][kTogether];
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                v[i][q] = *reinterpret_cast<const i32x4_t*>(part[i] + min(s + q, splits - 1) * cut);
+#pragma unroll
+        for (int q = 0; q < kTogether; ++q)
+#pragma unroll
+            for (int i = 0; i < kRows; ++i)
+                a[i] += s + q < splits ? v[i][q] : i32x4_t{0, 0, 0, 0};
+    }
+}
+
+__device__ __forceinline__ f32x4_t scaled(const i32x4_t& a, float a_scale, const f32x4_t& w)
+{
     f32x4_t v;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -358,14 +379,30 @@ __global__ __launch_bounds__(kThreads) void int8_finish_kernel(
     const int64_t r = grid_row();
     if (r >= M)
         return;
+    // the first columns' sums are asked for before the row's group is looked up
+    const int64_t begin = 4 * (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x);
+    const int32_t* sums = partial + r * N;
+    const auto total = [&](int64_t c) {
+        const int32_t* const part[1] = {sums + c};
+        i32x4_t a[1];
+        if (splits <= 4)
+            add_cuts<1, 3>(part, splits, M * N, a);
+        else
+            add_cuts<1, 7>(part, splits, M * N, a);
+        return a[0];
+    };
+    i32x4_t sum = {0, 0, 0, 0};
+    if (begin < N)
+        sum = total(begin);
+    const float as = a_scale[r];
     const int e = row_expert(offsets, group_expert, G, E, M, r, &found);
     if (e < 0)
         return;
-    const float as = a_scale[r];
     const float* ws = w_scale + static_cast<int64_t>(e) * N;
-    for (int64_t c = 4 * (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x); c < N;
-         c += 4 * static_cast<int64_t>(gridDim.y) * kThreads) {
-        const f32x4_t v = finish4(partial, splits, M * N, r * N + c, as, ws + c);
+    for (int64_t c = begin; c < N; c += 4 * static_cast<int64_t>(gridDim.y) * kThreads) {
+        if (c != begin)
+            sum = total(c);
+        const f32x4_t v = scaled(sum, as, *reinterpret_cast<const f32x4_t*>(ws + c));
         if constexpr (kBf16)
             *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(out) + r * N + c) =
                 u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
@@ -377,7 +414,8 @@ __global__ __launch_bounds__(kThreads) void int8_finish_kernel(
 // The combine of the layer straight from the down projection's partial sums: each slot's row is rounded
 // to bfloat16 as the stored rows of the other path are, and the k of a token are added in slot order
 // by fused multiply-adds from 0, as moe_unpermute does: bitwise the same output.  A chain of three loads
-// bounds it at few tokens (one token of 4096, 8 cuts: 6.3 us).
+// bounds it at few tokens (one token of 4096, 8 cuts: 6.3 us slot by slot and four cuts at a time, 4.6 us so).
+template <int kTogether>
 __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
     const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
     const float* __restrict__ w_scale, const int32_t* __restrict__ expert_ids, const int32_t* __restrict__ pos,
@@ -388,18 +426,33 @@ __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
     if (t >= T || c >= N)
         return;
     f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int j = 0; j < k; ++j) {
-        // no branch on a dropped slot, so that the loads of several slots go out together
-        const int64_t row = pos[t * k + j];
-        const bool held = row >= 0 && row < M;
-        const int64_t at = held ? row : 0;
-        const int e = held ? expert_ids[t * k + j] : 0;
-        const f32x4_t v = finish4(partial, splits, M * N, at * N + c, a_scale[at], w_scale + static_cast<int64_t>(e) * N + c);
-        const float p = probs[t * k + j];
+    for (int j = 0; j < k; j += kTogether) {
+        // no branch on a dropped slot or one past the last, so that the loads of several slots go out together
+        const int32_t* part[kTogether];
+        i32x4_t a[kTogether];
+        f32x4_t w[kTogether];
+        float scale[kTogether], p[kTogether];
+        bool held[kTogether];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            sum[i] = held ? fmaf(p, bf16_to_f32(f32_to_bf16(v[i])), sum[i]) : sum[i];
+        for (int i = 0; i < kTogether; ++i) {
+            const int64_t slot = t * k + min(j + i, k - 1);
+            const int64_t row = pos[slot];
+            const int id = expert_ids[slot];
+            held[i] = j + i < k && row >= 0 && row < M;
+            const int64_t at = held[i] ? row : 0;
+            part[i] = partial + at * N + c;
+            w[i] = *reinterpret_cast<const f32x4_t*>(w_scale + static_cast<int64_t>(held[i] ? id : 0) * N + c);
+            scale[i] = a_scale[at];
+            p[i] = probs[slot];
+        }
+        add_cuts<kTogether, 14 / kTogether>(part, splits, M * N, a);
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+            const f32x4_t v = scaled(a[i], scale[i], w[i]);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                sum[n] = held[i] ? fmaf(p[i], bf16_to_f32(f32_to_bf16(v[n])), sum[n]) : sum[n];
+        }
     }
     *reinterpret_cast<u32x2_t*>(out + t * N + c) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
@@ -689,8 +742,13 @@ hipError_t launch_int8_combine(const int32_t* partial, int splits, const float* 
     if (T <= 0)
         return hipSuccess;
     const dim3 grid = row_grid(T, ceil_div(N, 4 * kThreads));
-    int8_combine_kernel<<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs, T,
-                                                        static_cast<int>(k), T * k, N, out);
+    // slots whose loads go out together
+    if (k <= 2)
+        int8_combine_kernel<2><<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs, T,
+                                                               static_cast<int>(k), T * k, N, out);
+    else
+        int8_combine_kernel<4><<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs, T,
+                                                               static_cast<int>(k), T * k, N, out);
     return hipGetLastError();
 }
 
