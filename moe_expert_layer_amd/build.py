@@ -23,7 +23,7 @@ PROBE_LIB_PATH = os.path.join(HERE, "libmoe_expert_layer_probe.so")
 
 SOURCES = ["api.cpp", "route.hip", "permute.hip", "gemm_f32.hip", "gemm_bf16.hip", "gemm_mx.hip",
            "router.hip", "gemm_bwd.hip", "gate.hip", "gemm_i8.hip", "quant_i8.hip"]
-HEADERS = ["common.h", "internal.h", "gemm_common.h", "int8_gate.h"]
+HEADERS = ["common.h", "internal.h", "gemm_common.h", "int8_gate.h", "int8_tiles.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

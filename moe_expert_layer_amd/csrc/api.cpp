@@ -548,17 +548,24 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
                         const Int8Weights& w, void* y, void* ws, const Int8Layout& L, bool write_status,
                         hipStream_t s, const int32_t* gather, int gather_k, const int32_t* row_experts)
 {
-    int32_t* count = at<int32_t>(ws, L.tile_count);
-    MTile* tiles = at<MTile>(ws, L.tiles);
-    if (row_experts == nullptr)
-        LAUNCH(s, "int8_tiles",
-               launch_int8_tiles(offsets, group_expert, G, E, M, L.fc1.row_tile, tiles, count, at<int32_t>(ws, L.task_ctr),
-                                 at<int32_t>(ws, 0), write_status, s));
+    // the large layer's status word is the routing's: no group has a bad expert there
+    Int8Groups groups{offsets, group_expert, static_cast<int>(G), static_cast<int>(E),
+                      write_status ? at<int32_t>(ws, 0) : nullptr, nullptr, nullptr};
+    if (!int8_own_tiles(L.fc1, M, G)) {
+        groups.tiles = at<MTile>(ws, L.tiles);
+        groups.tile_count = at<int32_t>(ws, L.tile_count);
+        if (row_experts == nullptr)
+            LAUNCH(s, "int8_tiles",
+                   launch_int8_tiles(offsets, group_expert, G, E, M, L.fc1.row_tile, at<MTile>(ws, L.tiles),
+                                     at<int32_t>(ws, L.tile_count), at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0),
+                                     write_status, s));
+    }
     int8_t* h_q = at<int8_t>(ws, L.h_q);
     float* h_scale = at<float>(ws, L.h_scale);
     LAUNCH(s, "fc1_i8",
            launch_gemm_i8(L.fc1, rows, rows_scale, w.gate, w.gate_scale, w.up, w.up_scale, at<void>(ws, L.h),
-                          MOE_F32, M, H, F, tiles, count, gather, gather_k, at<int32_t>(ws, L.task_ctr), s));
+                          MOE_F32, M, H, F, groups, gather, gather_k, at<int32_t>(ws, L.task_ctr), s));
+    groups.status = nullptr;
     if (L.fc1.partial)
         LAUNCH(s, "int8_swiglu",
                launch_int8_swiglu_partial(at<int32_t>(ws, L.h), L.fc1.splits, rows_scale, gather, gather_k,
@@ -568,7 +575,7 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
         LAUNCH(s, "int8_quantize", launch_int8_quantize(MOE_F32, at<void>(ws, L.h), M, F, h_q, h_scale, s));
     LAUNCH(s, "fc2_i8",
            launch_gemm_i8(L.fc2, h_q, h_scale, w.down, w.down_scale, nullptr, nullptr,
-                          L.fc2.partial ? at<void>(ws, L.y_part) : y, MOE_BF16, M, F, H, tiles, count, nullptr, 1,
+                          L.fc2.partial ? at<void>(ws, L.y_part) : y, MOE_BF16, M, F, H, groups, nullptr, 1,
                           at<int32_t>(ws, L.task_ctr) + kXcdCount, s));
     if (L.fc2.partial && y != nullptr)
         LAUNCH(s, "int8_finish",
@@ -764,7 +771,8 @@ MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, 
         LAUNCH(s, "int8_prologue",
                launch_int8_prologue(expert_ids, T, k, E, at<int32_t>(ws, L.counts), offsets, perm, pos,
                                     at<int32_t>(ws, L.row_experts), at<int32_t>(ws, 0),
-                                    L.fc1.row_tile, at<MTile>(ws, L.tiles), at<int32_t>(ws, L.tile_count),
+                                    L.fc1.row_tile, int8_own_tiles(L.fc1, M, E) ? nullptr : at<MTile>(ws, L.tiles),
+                                    at<int32_t>(ws, L.tile_count),
                                     quantize_x ? static_cast<const uint16_t*>(x) : nullptr, H, at<int8_t>(ws, L.x_q),
                                     at<float>(ws, L.x_q_scale), s));
     } else {
@@ -1220,16 +1228,18 @@ MOE_API moe_status moe_grouped_matmul_int8(const int8_t* rows, const float* rows
         return st;
     hipStream_t s = stream;
     void* ws = workspace;
-    int32_t* count = at<int32_t>(ws, L.tile_count);
-    MTile* tiles = at<MTile>(ws, L.tiles);
-    LAUNCH(s, "int8_tiles",
-           launch_int8_tiles(group_offsets, group_expert, G, E, M, L.plan.row_tile, tiles, count,
-                             at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), true, s));
-    if (M == 0)
-        return MOE_OK;
+    Int8Groups groups{group_offsets, group_expert, static_cast<int>(G), static_cast<int>(E), at<int32_t>(ws, 0), nullptr,
+                      nullptr};
+    if (!int8_own_tiles(L.plan, M, G)) {
+        groups.tiles = at<MTile>(ws, L.tiles);
+        groups.tile_count = at<int32_t>(ws, L.tile_count);
+        LAUNCH(s, "int8_tiles",
+               launch_int8_tiles(group_offsets, group_expert, G, E, M, L.plan.row_tile, at<MTile>(ws, L.tiles),
+                                 at<int32_t>(ws, L.tile_count), at<int32_t>(ws, L.task_ctr), at<int32_t>(ws, 0), true, s));
+    }
     LAUNCH(s, "matmul_i8",
            launch_gemm_i8(L.plan, rows, rows_scale, w, w_scale, nullptr, nullptr,
-                          L.plan.partial ? at<void>(ws, L.part) : out, out_dtype, M, K, N, tiles, count, nullptr,
+                          L.plan.partial ? at<void>(ws, L.part) : out, out_dtype, M, K, N, groups, nullptr,
                           1, at<int32_t>(ws, L.task_ctr), s));
     if (L.plan.partial)
         LAUNCH(s, "int8_finish",

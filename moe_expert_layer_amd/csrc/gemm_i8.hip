@@ -27,6 +27,7 @@
 
 #include "gemm_common.h"
 #include "int8_gate.h"
+#include "int8_tiles.h"
 
 namespace moe {
 namespace {
@@ -39,6 +40,9 @@ typedef __attribute__((address_space(3))) i32x2_t lds_i32x2_t;
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 constexpr int BNB = 256;                       // weight columns per task (both matrices of a gated task)
+constexpr int kOwnTiles = 512;                 // of the table that a workgroup builds for itself: a group per thread
+constexpr int kOwnTableBytes = 16 * kOwnTiles + 8 * kWaves;    // and the scan's words
+static_assert(kOwnTiles <= kThreads && kMaxExperts < 1 << 23, "the own table's scan and entries");
 
 enum Out { kOutBf16, kOutF32, kOutPartial };
 
@@ -50,8 +54,7 @@ struct Args {
     const float* s0;                           // [E, N]
     const float* s1;
     void* out;                                 // [M, N], or int32 partial sums [splits, M, N or 2N]
-    const MTile* tiles;
-    const int32_t* tile_count;
+    Int8Groups groups;
     const int32_t* gather;                     // may be null: row p of the product is row gather[p] / gather_k of A
     int gather_k;
     int32_t* task_ctr;                         // kXcdCount zeroed counters (large tiles)
@@ -72,7 +75,7 @@ struct Config {
     static constexpr int kCopies = kACopies + kBCopies;
     static_assert(kWM * kWN == kWaves && kWN * kTN * 32 == BNB, "wave grid");
     static_assert(kABytes % (1024 * kWaves) == 0 && kBBytes % (1024 * kWaves) == 0, "copies per wave");
-    static_assert(kSmemBytes <= 160 * 1024, "LDS");
+    static_assert(kSmemBytes + kOwnTableBytes <= 160 * 1024, "LDS");
     static_assert(BK == 64 || BK == 128, "A swizzle");
 };
 
@@ -149,6 +152,21 @@ __device__ __forceinline__ MTile uniform_task(int t, int n_nt, const MTile* __re
     return u;
 }
 
+// A tile of the table that a workgroup builds for itself in LDS: first row, rows | expert << 8, and its run.
+typedef __attribute__((address_space(3))) i32x4_t lds_tile_t;
+__device__ __forceinline__ MTile uniform_task(int t, int n_nt, const lds_tile_t* tiles, int& nt)
+{
+    const i32x4_t head = tiles[t / n_nt];
+    const int local = t - n_nt * head[2];
+    nt = __builtin_amdgcn_readfirstlane(local / head[3]);
+    const i32x4_t m = tiles[head[2] + local % head[3]];
+    MTile u{};
+    u.row_begin = __builtin_amdgcn_readfirstlane(m[0]);
+    u.row_end = u.row_begin + __builtin_amdgcn_readfirstlane(m[1] & 255);
+    u.expert = __builtin_amdgcn_readfirstlane(m[1] >> 8);
+    return u;
+}
+
 // Column block j of wave column wn: its matrix (gated: 0 gate, 1 up; blocks alternate, in one wave or
 // from wave to wave) and its first column among the task's outputs.
 template <class C, bool kGated>
@@ -162,7 +180,7 @@ __device__ __forceinline__ constexpr int block_col(int wn, int j)
     return !kGated ? 32 * (C::kTN * wn + j) : C::kTN > 1 ? 16 * C::kTN * wn + 32 * (j >> 1) : 32 * (wn >> 1);
 }
 
-template <class C, bool kGated, int kOut>
+template <class C, bool kGated, int kOut, bool kOwn>
 __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
 {
     constexpr int BN = kGated ? BNB / 2 : BNB;               // output columns per task
@@ -180,7 +198,36 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
     const int lrow = lane & 31, lh = lane >> 5;
     const int K = a.K, N = a.N;
     const int n_nt = (N + BN - 1) / BN;
-    const int total = __builtin_amdgcn_readfirstlane(*a.tile_count * n_nt * a.splits);
+    // The row tiles: a table in memory, or for few groups one that each workgroup builds in LDS, which costs
+    // under a microsecond where a launch for the table costs five (1000 rows on 128 experts of 2048 x 1536: 73.8
+    // -> 69.7 us; 500 rows on 8 of 2048 x 4096: 22.1 -> 18.6 us)
+    [[maybe_unused]] lds_tile_t* const own = reinterpret_cast<lds_tile_t*>(lds0 + C::kSmemBytes);
+    int row_tiles;
+    if constexpr (kOwn) {
+        int* const wave_max = reinterpret_cast<int*>(smem + C::kSmemBytes + 16 * kOwnTiles);
+        int* const wave_sum = wave_max + kWaves;
+        int reached = 0;
+        const GroupRows r = scan_groups<kWaves>(a.groups.offsets, a.groups.expert, 0, a.groups.G, a.groups.E, a.M, C::BM,
+                                                reached, wave_max, wave_sum);
+        const int R = (r.rows + C::BM - 1) / C::BM;
+        for (int i = 0; i < R; ++i) {
+            const MTile m = balanced_tile(r.expert, r.begin, r.rows, R, i, r.first);
+            own[r.first + i] = i32x4_t{m.row_begin, (m.row_end - m.row_begin) | m.expert << 8, m.run_begin, R};
+        }
+        const int bad = __syncthreads_or(r.bad ? 1 : 0);
+        if (a.groups.status != nullptr && blockIdx.x == 0 && threadIdx.x == 0)
+            *a.groups.status = bad ? MOE_ERR_EXPERT_ID_OUT_OF_RANGE : MOE_OK;
+        row_tiles = r.total;
+    } else {
+        row_tiles = *a.groups.tile_count;
+    }
+    const int total = __builtin_amdgcn_readfirstlane(row_tiles * n_nt * a.splits);
+    const auto task_tile = [&](int t, int& nt) {
+        if constexpr (kOwn)
+            return uniform_task(t / a.splits, n_nt, own, nt);
+        else
+            return uniform_task(t / a.splits, n_nt, a.groups.tiles, nt);
+    };
 
     // fragment addresses in stage 0
     uint32_t la_a[BK / 32], la_b[C::kTN];
@@ -222,12 +269,19 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
     const auto fetch = [&](int task) {
         if (task >= total)
             return;
-        next_tile = uniform_task(task / a.splits, n_nt, a.tiles, next_nt);
+        next_tile = task_tile(task, next_nt);
         const int rows = next_tile.row_end - next_tile.row_begin;
 #pragma unroll
-        for (int j = 0; j < C::kACopies; ++j) {
-            const int r = (kARows * (C::kACopies * wave + j) + lane / kALanes) % rows;   // past the tile's end: its rows again
-            gsrc[j] = a.gather != nullptr ? a.gather[next_tile.row_begin + r] : r;
+        for (int j = 0; j < C::kACopies; ++j)
+            gsrc[j] = (kARows * (C::kACopies * wave + j) + lane / kALanes) % rows;   // past the tile's end: its rows again
+        if (a.gather != nullptr) {
+#pragma unroll
+            for (int j = 0; j < C::kACopies; ++j)
+                gsrc[j] = a.gather[next_tile.row_begin + gsrc[j]];
+            // waited for here: left in flight, they would put a wait for every copy into each step
+#pragma unroll
+            for (int j = 0; j < C::kACopies; ++j)
+                asm volatile("" : "+v"(gsrc[j]));
         }
     };
     uint32_t a_voff[C::kACopies], b_voff[C::kBCopies];
@@ -259,7 +313,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
             bp = scalar((kGated && mat == 1 ? a.B1 : a.B0) + (static_cast<int64_t>(next_tile.expert) * K + k0) * N + n0);
             fetch(pt + grid);
         }
-        const uint32_t so = fill * C::kStageBytes;
+        const uint32_t so = __builtin_amdgcn_readfirstlane(fill) * C::kStageBytes;
 #pragma unroll
         for (int j = 0; j < C::kACopies; ++j)
             lds_copy16(ap, a_voff[j], a_lds + so + j * 1024);
@@ -280,7 +334,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
 
     for (int t = first_task(total); t < total; t += grid) {
         int nt;
-        const MTile tile = uniform_task(t / a.splits, n_nt, a.tiles, nt);
+        const MTile tile = task_tile(t, nt);
         const int n0 = nt * BN;
         [[maybe_unused]] const int split = t % a.splits;
         const int2 kt = steps_of(t);
@@ -323,18 +377,39 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
         }
 
         // Epilogue.  Only the stores are under the lane's row test (no other lane-divergent region sits
-        // in the task loop); a row past the tile's end reads the last row's scale.
-        const float* s0 = a.s0 + static_cast<int64_t>(tile.expert) * N;
-        [[maybe_unused]] const float* s1 = kGated ? a.s1 + static_cast<int64_t>(tile.expert) * N : nullptr;
+        // in the task loop); a row past the tile's end reads the last row's scale.  All scales are loaded
+        // first, in one wait: each wait also waits for the copies in flight and for the stores before it.
+        [[maybe_unused]] f32x4_t scale[C::kTN][4];            // of column block j (gated: of its matrix)
+        [[maybe_unused]] float row_scale[C::kTM];
+        if constexpr (kOut != kOutPartial) {
+#pragma unroll
+            for (int j = 0; j < C::kTN; ++j) {
+                const int col = n0 + block_col<C, kGated>(wn, j);
+                const float* sc = (kGated && block_mat<C, kGated>(wn, j) == 1 ? a.s1 : a.s0) +
+                                  static_cast<int64_t>(tile.expert) * N + (col < N ? col : 0);
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    scale[j][g] = *reinterpret_cast<const f32x4_t*>(sc + 8 * g + 4 * lh);
+            }
+#pragma unroll
+            for (int i = 0; i < C::kTM; ++i) {
+                const int r = min(tile.row_begin + row_block<C::kWM>(i, wm) + lrow, tile.row_end - 1);
+                row_scale[i] = a.a_scale[a.gather != nullptr ? a.gather[r] / a.gather_k : r];
+            }
+#pragma unroll
+            for (int j = 0; j < C::kTN; ++j)
+#pragma unroll
+                for (int g = 0; g < 4; ++g)
+                    asm volatile("" : "+v"(scale[j][g]));     // not to be loaded between the stores
+#pragma unroll
+            for (int i = 0; i < C::kTM; ++i)
+                asm volatile("" : "+v"(row_scale[i]));
+        }
 #pragma unroll
         for (int i = 0; i < C::kTM; ++i) {
             const int grow = tile.row_begin + row_block<C::kWM>(i, wm) + lrow;
             const bool live = grow < tile.row_end;
-            [[maybe_unused]] float as = 0.0f;
-            if constexpr (kOut != kOutPartial) {
-                const int r = min(grow, tile.row_end - 1);
-                as = a.a_scale[a.gather != nullptr ? a.gather[r] / a.gather_k : r];
-            }
+            [[maybe_unused]] const float as = kOut != kOutPartial ? row_scale[i] : 0.0f;
 #pragma unroll
             for (int j = 0; j < C::kTN; ++j) {
                 if constexpr (kOut == kOutPartial) {
@@ -356,28 +431,25 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
                             const int c = 8 * g + 4 * lh;
-                            const f32x4_t sg = *reinterpret_cast<const f32x4_t*>(s0 + col + c);
-                            const f32x4_t su = *reinterpret_cast<const f32x4_t*>(s1 + col + c);
+                            const int up = (j + 1) % C::kTN;
                             f32x4_t h;
 #pragma unroll
                             for (int v = 0; v < 4; ++v)
-                                h[v] = swiglu(static_cast<float>(acc[i][j][4 * g + v]) * as * sg[v],
-                                              static_cast<float>(acc[i][(j + 1) % C::kTN][4 * g + v]) * as * su[v]);
+                                h[v] = swiglu(static_cast<float>(acc[i][j][4 * g + v]) * as * scale[j][g][v],
+                                              static_cast<float>(acc[i][up][4 * g + v]) * as * scale[up][g][v]);
                             if (live)
                                 *reinterpret_cast<f32x4_t*>(dst + c) = h;
                         }
                     }
                 } else {
                     const int col = n0 + block_col<C, kGated>(wn, j);
-                    const float* sc = s0 + (col < N ? col : 0);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const int c = 8 * g + 4 * lh;
-                        const f32x4_t s = *reinterpret_cast<const f32x4_t*>(sc + c);
                         f32x4_t v;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            v[e] = static_cast<float>(acc[i][j][4 * g + e]) * as * s[e];
+                            v[e] = static_cast<float>(acc[i][j][4 * g + e]) * as * scale[j][g][e];
                         const int64_t at = static_cast<int64_t>(grow) * N + col + c;
                         if (live && col < N) {
                             if constexpr (kOut == kOutF32)
@@ -612,7 +684,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
     const int K = a.K, N = a.N;
     const int KT = K / BK;
     const int n_nt = (N + BN - 1) / BN;
-    const int total = __builtin_amdgcn_readfirstlane(*a.tile_count * n_nt);
+    const int total = __builtin_amdgcn_readfirstlane(*a.groups.tile_count * n_nt);
     const int first = KT & 2;                                // position of a task's first step
 
     const int mat = kGated ? wave / (kWaves / 2) : 0;
@@ -704,7 +776,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
         claim_task(claimed, a.task_ctr, xcd, blk, wave, lane);
     if (t < total) {
         int nt;
-        const MTile tl = decode_task(t, n_nt, a.tiles, nt);
+        const MTile tl = decode_task(t, n_nt, a.groups.tiles, nt);
         fetch_rows(tl);
         setup(tl, nt);
     }
@@ -728,7 +800,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
             const int ci = __builtin_amdgcn_readfirstlane(*claimed);
             t_next = ((ci / blk) * kXcdCount + xcd) * blk + ci % blk;
             if (t_next < total)
-                tile_next = decode_task(t_next, n_nt, a.tiles, nt_next);
+                tile_next = decode_task(t_next, n_nt, a.groups.tiles, nt_next);
         }
         const int claim_ret = claim_issue(a.task_ctr, xcd, wave, lane);
         if (t_next < total)
@@ -747,7 +819,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
             const int ci = __builtin_amdgcn_readfirstlane(*claimed);
             t_next = ((ci / blk) * kXcdCount + xcd) * blk + ci % blk;
             if (t_next < total)
-                tile_next = decode_task(t_next, n_nt, a.tiles, nt_next);
+                tile_next = decode_task(t_next, n_nt, a.groups.tiles, nt_next);
         }
         const MTile done = tile;
         const int done_n0 = n0;
@@ -850,9 +922,13 @@ hipError_t launch_rows(int bm, const Args& a, hipStream_t s)
         if constexpr (kOut != kOutPartial)
             return launch<&big::grouped_gemm_i8_dma<kGated, kOut>, big::kSmemBytes>(a, s);
     } else if (bm == Mid::BM) {
-        return launch<&grouped_gemm_i8<Mid, kGated, kOut>, Mid::kSmemBytes>(a, s);
+        return a.groups.tiles == nullptr
+                   ? launch<&grouped_gemm_i8<Mid, kGated, kOut, true>, Mid::kSmemBytes + kOwnTableBytes>(a, s)
+                   : launch<&grouped_gemm_i8<Mid, kGated, kOut, false>, Mid::kSmemBytes>(a, s);
     } else if constexpr (!kGated || kOut == kOutPartial) {
-        return launch<&grouped_gemm_i8<Small, kGated, kOut>, Small::kSmemBytes>(a, s);
+        return a.groups.tiles == nullptr
+                   ? launch<&grouped_gemm_i8<Small, kGated, kOut, true>, Small::kSmemBytes + kOwnTableBytes>(a, s)
+                   : launch<&grouped_gemm_i8<Small, kGated, kOut, false>, Small::kSmemBytes>(a, s);
     }
     return hipErrorInvalidValue;
 }
@@ -967,6 +1043,11 @@ void int8_ffn_plans(int64_t M, int64_t G, int64_t H, int64_t F, Int8Plan& fc1, I
     }
 }
 
+bool int8_own_tiles(const Int8Plan& p, int64_t M, int64_t G)
+{
+    return p.row_tile != i8::big::BM && max_mtiles(M, G, 0, p.row_tile) <= i8::kOwnTiles;
+}
+
 bool int8_tasks_fit(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gated)
 {
     // the loops over tasks step by the grid and decode_task multiplies back: kept well below 2^31
@@ -975,7 +1056,7 @@ bool int8_tasks_fit(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gat
 
 hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_scale, const int8_t* w0,
                           const float* s0, const int8_t* w1, const float* s1, void* out, int out_dtype,
-                          int64_t M, int64_t K, int64_t N, const MTile* tiles, const int32_t* tile_count,
+                          int64_t M, int64_t K, int64_t N, const Int8Groups& groups,
                           const int32_t* gather, int gather_k, int32_t* task_ctr, hipStream_t s)
 {
     i8::Args a{};
@@ -986,8 +1067,7 @@ hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_sca
     a.s0 = s0;
     a.s1 = s1;
     a.out = out;
-    a.tiles = tiles;
-    a.tile_count = tile_count;
+    a.groups = groups;
     a.gather = gather;
     a.gather_k = gather_k;
     a.task_ctr = task_ctr;

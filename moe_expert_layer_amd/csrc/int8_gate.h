@@ -29,13 +29,25 @@ Int8Plan int8_plan(int64_t M, int64_t G, int64_t K, int64_t N);
 void int8_ffn_plans(int64_t M, int64_t G, int64_t H, int64_t F, Int8Plan& fc1, Int8Plan& fc2);
 // Whether the plan's tasks (row tiles x column tiles x cuts) can be numbered in 32 bits.
 bool int8_tasks_fit(const Int8Plan& p, int64_t M, int64_t G, int64_t N, bool gated);
+// The groups of a product's M rows (offsets [G + 1]; expert [G], null: group g is expert g).  tiles: the table of
+// launch_int8_tiles with its count; null, where int8_own_tiles allows it: each workgroup builds the table for
+// itself, and the first one writes the status word unless that is null.
+struct Int8Groups {
+    const int32_t* offsets;
+    const int32_t* expert;
+    int G, E;
+    int32_t* status;
+    const MTile* tiles;
+    const int32_t* tile_count;
+};
+bool int8_own_tiles(const Int8Plan& p, int64_t M, int64_t G);
 // out: [M, N] of out_dtype (MOE_F32 / MOE_BF16), gated (w1 not null) float32 swiglu of the two
 // products, or the partial sums.  gather (may be null): row p of the product is row
 // gather[p] / gather_k of A and a_scale, whose rows then lie within 2^32 bytes.  task_ctr: kXcdCount zeroed
 // counters for this launch (256-row tiles).
 hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_scale, const int8_t* w0,
                           const float* s0, const int8_t* w1, const float* s1, void* out, int out_dtype,
-                          int64_t M, int64_t K, int64_t N, const MTile* tiles, const int32_t* tile_count,
+                          int64_t M, int64_t K, int64_t N, const Int8Groups& groups,
                           const int32_t* gather, int gather_k, int32_t* task_ctr, hipStream_t s);
 // quant_i8.hip.  Rows of float32 or bfloat16 -> int8 codes and one scale per row (moe_int8_quantize).
 hipError_t launch_int8_quantize(int dtype, const void* x, int64_t rows, int64_t cols, int8_t* codes,
@@ -55,7 +67,7 @@ hipError_t launch_int8_tiles(const int32_t* offsets, const int32_t* group_expert
                              bool write_status, hipStream_t s);
 // The routing (as launch_route_* leave it, and each row's expert), the table of balanced row tiles of
 // height bm with its count, and with x not null the quantised token rows, in one launch; at most
-// kInt8SmallSlots slots.
+// kInt8SmallSlots slots.  tiles null: no table.
 constexpr int64_t kInt8SmallSlots = 256;
 hipError_t launch_int8_prologue(const int32_t* ids, int64_t T, int64_t k, int64_t E, int32_t* counts, int32_t* offsets,
                                 int32_t* perm, int32_t* pos, int32_t* row_experts, int32_t* status, int bm,

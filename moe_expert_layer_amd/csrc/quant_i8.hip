@@ -14,6 +14,7 @@
 
 #include "common.h"
 #include "int8_gate.h"
+#include "int8_tiles.h"
 
 namespace moe {
 namespace {
@@ -457,84 +458,33 @@ __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
     *reinterpret_cast<u32x2_t*>(out + t * N + c) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
 }
 
-// Tile i of the R balanced ones of a group of n rows from row `begin`: its 32-row blocks are dealt as
-// evenly as possible, the last tile ends the group (the in-run table of launch_build_tiles).
-__device__ __forceinline__ MTile balanced_tile(int expert, int begin, int n, int R, int i, int run_begin)
-{
-    const int blocks = (n + 31) / 32, each = blocks / R, more = blocks % R;
-    MTile t;
-    t.expert = expert;
-    t.row_begin = begin + 32 * (each * i + min(i, more));
-    t.row_end = i == R - 1 ? begin + n : begin + 32 * (each * (i + 1) + min(i + 1, more));
-    t.chunk = 0;
-    t.run_begin = run_begin;
-    t.run_len = R;
-    t.pad0 = t.pad1 = 0;
-    return t;
-}
-
 // The table of balanced tiles alone: a thread per group (kWideThreads of them at a time), a scan, then a
 // thread per tile, which finds its group by bisection.  One workgroup, few barriers (8 groups 4.8 us, 128
-// groups 5.6 us, where the general builder with its two tables takes 5.5 and 9.4).  A group begins no
-// earlier than any offset before it, so that no row is in two groups and the tiles fit the table
-// whatever the offsets.
+// groups 5.6 us, where the general builder with its two tables takes 5.5 and 9.4).
 __global__ __launch_bounds__(kWideThreads) void int8_tiles_kernel(
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ group_expert, int G, int E, int64_t M, int bm,
     MTile* __restrict__ tiles, int32_t* __restrict__ tile_count, int32_t* __restrict__ task_ctr,
     int32_t* __restrict__ status, int write_status)
 {
-    constexpr int kWaves = kWideThreads / 64;
     __shared__ int first[kWideThreads + 1], begin[kWideThreads], rows[kWideThreads], expert[kWideThreads];
-    __shared__ int wave_max[kWaves], wave_sum[kWaves];
-    const int me = threadIdx.x, lane = me & 63, wave = me >> 6, limit = static_cast<int>(M);
+    __shared__ int wave_max[kWideThreads / 64], wave_sum[kWideThreads / 64];
+    const int me = threadIdx.x;
     int done = 0, reached = 0;                                // tiles and largest offset of the groups so far
     bool bad = false;
     if (me < 2 * kXcdCount)
         task_ctr[me] = 0;
     for (int base = 0; base < G; base += kWideThreads) {
         const int held = min(G - base, kWideThreads);
-        const bool mine = me < held;
-        const int g = base + (mine ? me : 0);
-        const int o = mine ? min(max(offsets[g], 0), limit) : 0;
-        const int end = mine ? min(max(offsets[g + 1], 0), limit) : 0;
-        int e = mine ? (group_expert != nullptr ? group_expert[g] : g) : 0;
-        int rb = o;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1)
-            rb = max(rb, __shfl_up(rb, off));                 // a lane below `off` gets its own value
-        if (lane == 63)
-            wave_max[wave] = rb;
-        __syncthreads();
-        rb = max(rb, reached);
-        for (int w = 0; w < kWaves; ++w) {
-            rb = w < wave ? max(rb, wave_max[w]) : rb;
-            reached = max(reached, wave_max[w]);
-        }
-        int n = max(end - rb, 0);
-        if (e < 0 || e >= E) {
-            bad |= n > 0;
-            n = 0;                                            // skipped
-        }
-        const int count = (n + bm - 1) / bm;
-        int before = count;
-#pragma unroll
-        for (int off = 1; off < 64; off <<= 1) {
-            const int v = __shfl_up(before, off);
-            before += lane >= off ? v : 0;
-        }
-        if (lane == 63)
-            wave_sum[wave] = before;
-        __syncthreads();
-        for (int w = 0; w < wave; ++w)
-            before += wave_sum[w];
-        first[me + 1] = before;
+        const GroupRows r = scan_groups<kWideThreads / 64>(offsets, group_expert, base, G, E, M, bm, reached, wave_max, wave_sum);
+        bad |= r.bad;
+        first[me] = r.first;
         if (me == 0)
-            first[0] = 0;
-        begin[me] = rb;
-        rows[me] = n;
-        expert[me] = e;
+            first[kWideThreads] = r.total;
+        begin[me] = r.begin;
+        rows[me] = r.rows;
+        expert[me] = r.expert;
         __syncthreads();
-        const int total = first[kWideThreads];
+        const int total = r.total;
         for (int t = me; t < total; t += kWideThreads) {
             int lo = 0, hi = held - 1;                        // the last group whose first tile is at most t
             while (lo < hi) {
@@ -633,7 +583,8 @@ __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
             if (e == E - 1) {
                 begin[E] = rows_in;
                 offsets[E] = rows_in;
-                *tile_count = nt_in;
+                if (tiles != nullptr)
+                    *tile_count = nt_in;
                 *status = rows_in == M ? MOE_OK : MOE_ERR_EXPERT_ID_OUT_OF_RANGE;
             }
         }
@@ -653,7 +604,7 @@ __global__ __launch_bounds__(kThreads) void int8_prologue_kernel(
     }
     for (int e = tid; e < E; e += kThreads) {
         const int n = hist[e], R = (n + bm - 1) / bm;
-        for (int i = 0; i < R; ++i)
+        for (int i = 0; i < R && tiles != nullptr; ++i)
             tiles[tile_begin[e] + i] = balanced_tile(e, begin[e], n, R, i, tile_begin[e]);
     }
 }
