@@ -17,8 +17,8 @@
 // consecutive k of its column.
 //
 // Few rows are bound by the weights' bytes: 64-row tiles, copies that run ahead across a workgroup's tasks
-// and K cut until the CUs are evenly busy (1000 rows on 128 experts of 2048 x 768: gate and up 72 us for
-// at most 403 MB, 5.6 TB/s).  Many rows are bound by the matrix instructions: 256-row tiles (16384 rows, 2
+// and K cut until the CUs are evenly busy (1000 rows on 128 experts of 2048 x 768: gate and up 73 us for
+// at most 403 MB, 5.5 TB/s).  Many rows are bound by the matrix instructions: 256-row tiles (16384 rows, 2
 // experts of 4096 x 14336: 0.86-0.93 ms, 2.1-2.2 POP/s).  product_cost below chooses.
 #include <algorithm>
 #include <atomic>

@@ -653,7 +653,7 @@ hipError_t launch_int8_swiglu_partial(const int32_t* partial, int splits, const 
         return hipSuccess;
     const dim3 grid = row_grid(M);
     const int g = static_cast<int>(G), e = static_cast<int>(E);
-    // few rows: a whole CU's threads for each (2 rows of 14336: 16.8 -> 7.3 us)
+    // few rows: a whole CU's threads for each (2 rows of 14336: 16.8 -> 7.5 us)
     if (M <= 2 * device_info().cu_count)
         int8_swiglu_partial_kernel<kWideThreads, 2><<<grid, dim3(kWideThreads), 0, s>>>(
             partial, splits, a_scale, gather, gather_k, sg, su, row_experts, offsets, group_expert, g, e, M, F, codes, scales);
