@@ -787,8 +787,8 @@ hipError_t launch_gate_n(const In* logits, GateArgs a, hipStream_t s)
 // The gate's lanes per token.  Four experts a lane where possible: shortest rounds.  With many tokens of more
 // than 32 experts, up to 16 experts a lane: what a round costs beside the keys themselves (the exchanges,
 // the winner) is then shared by more tokens of the wave.  Measured (us, four experts a lane / 16): 65536
-// tokens of 32 experts 10 / 12, of 64 18 / 15, of 256 54 / 26; 8192 tokens of 64 experts 7.3 / 8.4, of 256
-// 11.6 / 10.4: taken from 32 waves a CU on.
+// tokens of 32 experts 10 / 12, of 64 14.7 / 12.4, of 256 53 / 22; 8192 tokens of 64 experts 5.8 / 6.9, of 256
+// 8.9 / 5.1; 4096 tokens of 256 6.5 / 7.2: taken from 32 waves a CU on.
 template <class In>
 hipError_t launch_gate_t(const In* logits, const GateArgs& a, hipStream_t s)
 {
