@@ -240,6 +240,22 @@ def test_matmul_of_thousands_of_groups():
         assert np.all(np.abs(out[at] - r) <= (4 * U + BF) * np.abs(r))
 
 
+@pytest.mark.parametrize("groups,rows", [(480, 1920), (481, 1920), (510, 1), (511, 1), (8, 32000), (1, 32512), (3, 65000)])
+def test_matmul_about_the_largest_own_table(groups, rows):
+    """Row tiles about the most that a workgroup lists for itself, few and many to a group; K one step."""
+    rng = np.random.default_rng(groups + rows)
+    K, N, E = 128, 128, 5
+    off = np.concatenate([[0], np.sort(rng.integers(0, rows + 1, groups - 1)), [rows]]).astype(np.int32)
+    expert = rng.integers(0, E, groups).astype(np.int32)
+    a, w, rs, wsc = _codes(rng, rows, K), _codes(rng, E, K, N), _scale(rng, rows), _scale(rng, E, N)
+    out = _host(mel.grouped_matmul_int8(*_dev(a, rs, off, expert, w, wsc)))
+    row_expert = np.repeat(expert, np.diff(off))
+    for e in range(E):
+        at = row_expert == e
+        r = ref.matmul(a[at], rs[at], w[e], wsc[e])
+        assert np.all(np.abs(out[at] - r) <= (4 * U + BF) * np.abs(r))
+
+
 def test_matmul_nan_scale_marks_its_row_alone():
     rng = np.random.default_rng(12)
     rows, w = _codes(rng, 70, 128), _codes(rng, 1, 128, 128)
