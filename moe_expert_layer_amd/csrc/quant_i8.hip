@@ -95,8 +95,10 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* buf)
     return v;
 }
 
-// The group that holds `row` (offsets clamped into [0, M] as in the tile table) and its expert, or
-// -1 where no group does or its expert is outside [0, E).  All threads call it.
+// The expert of the group that holds `row`, or -1 where no group does or its expert is outside [0, E); a group
+// begins no earlier than any offset before it, as in the tile table (scan_groups).  That leaves the first
+// group g whose end lies past the row, and only if the row is not before the first offset: every later group
+// has that end before it, and offsets 1 .. g are ends that do not lie past the row.  All threads call it.
 __device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets,
                                           const int32_t* __restrict__ group_expert, int G, int E, int64_t M,
                                           int64_t row, int* found)
@@ -112,7 +114,7 @@ __device__ __forceinline__ int row_expert(const int32_t* __restrict__ offsets,
     }
     __syncthreads();
     const int g = *found;
-    if (g == INT32_MAX)
+    if (g == INT32_MAX || row < offsets[0])
         return -1;
     const int e = group_expert != nullptr ? group_expert[g] : g;
     return e >= 0 && e < E ? e : -1;

@@ -499,3 +499,68 @@ def test_refusals():
     with pytest.raises(ValueError):
         mel.expert_forward_int8(x, torch.ones(2, device="cuda"), w, wsc, w, wsc, w, wsc,
                                 torch.zeros((2, 1), dtype=torch.int32, device="cuda"), torch.ones((2, 1), device="cuda"))
+
+
+# ------------------------------------------------------------------------------------------- offsets that fall
+
+def _row_experts(off, expert, E, M):
+    """Each row's expert, -1 for none: a group begins no earlier than any offset before it."""
+    held, reached = np.full(M, -1), 0
+    for g in range(len(expert)):
+        reached = max(reached, min(max(off[g], 0), M))
+        if 0 <= expert[g] < E:
+            held[reached:max(reached, min(max(off[g + 1], 0), M))] = expert[g]
+    return held
+
+
+FALLING = [
+    ([40, 10, 60], [1, 0], 60),
+    ([5, 0, 10], [0, 1], 12),
+    ([5, 3, 30, 8, 50], [0, 1, 0, 1], 55),                   # falls twice
+    ([0, 20, 5, 30], [9, 0, 1], 33),                         # the first group's expert does not exist
+    ([30, 2, 40, 33, 64], [1, 9, 0, 1], 70),                 # a later one's does not
+    ([-3, 6, 2, 500], [1, 0, 1], 50),                        # offsets outside the rows
+    ([64, 64, 0, 64], [0, 1, 0], 64),                        # no row is held
+]
+
+
+# 8192 values of K are cut for so few rows (the sums are joined by a launch of their own), 256 are not.
+@pytest.mark.parametrize("K", [256, 2048, 8192])
+@pytest.mark.parametrize("off,expert,M", FALLING)
+def test_matmul_rows_of_offsets_that_fall(off, expert, M, K):
+    rng = np.random.default_rng(K + M)
+    N = 256
+    rows, w, rs, wsc = _codes(rng, M, K), _codes(rng, 2, K, N), _scale(rng, M), _scale(rng, 2, N)
+    held = _row_experts(off, expert, 2, M)
+    for dtype in (torch.bfloat16, torch.float32):
+        print(f"[int8 matmul] offsets {off} K={K} {dtype}", flush=True)
+        out = torch.full((M, N), 7.0, dtype=dtype, device="cuda")
+        ws = torch.full((64 << 20,), 85, dtype=torch.uint8, device="cuda")
+        mel.grouped_matmul_int8(*_dev(rows, rs, np.array(off, np.int32), np.array(expert, np.int32), w, wsc), out=out,
+                                out_dtype=dtype, workspace=ws)
+        got = _host(out)
+        assert np.all(got[held < 0] == 7.0)
+        for e in range(2):
+            at = held == e
+            r = ref.matmul(rows[at], rs[at], w[e], wsc[e])
+            assert np.all(np.abs(got[at] - r) <= (4 * U + (BF if dtype == torch.bfloat16 else 0)) * np.abs(r))
+
+
+@pytest.mark.parametrize("H,F", [(256, 256), (1024, 4096)])      # whole products, both products cut
+@pytest.mark.parametrize("off,expert,M", FALLING)
+def test_ffn_rows_of_offsets_that_fall(off, expert, M, H, F):
+    rng = np.random.default_rng(H + M)
+    w = _weights(rng, 2, H, F)
+    rows, rs = _codes(rng, M, H), _scale(rng, M, level=0.02)
+    held = _row_experts(off, expert, 2, M)
+    print(f"[int8 ffn] offsets {off} H={H} F={F}", flush=True)
+    out = torch.full((M, H), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((256 << 20,), 85, dtype=torch.uint8, device="cuda")
+    mel.grouped_ffn_int8(*_dev(rows, rs, np.array(off, np.int32), np.array(expert, np.int32), *w), out=out, workspace=ws)
+    got = _host(out)
+    assert np.all(got[held < 0] == 7.0)
+    for e in range(2):
+        at = held == e
+        if at.any():
+            y, slack = ref.ffn(rows[at], rs[at], *[t[e] for t in w])
+            assert np.all(np.abs(got[at] - y) <= slack + BF * (np.abs(y) + slack))
