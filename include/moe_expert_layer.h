@@ -324,7 +324,8 @@ moe_status moe_router_topk(const float* logits, int64_t T, int64_t E, int64_t k,
  *   top-k      the k largest c of the experts that stay, in descending order, equal c to the lower id
  *              (so -inf ones are taken last, in ascending id)
  *   weights    probs[t,j] = scale * s_j, divided by the sum of the k s_j with renormalize != 0; where
- *              all k scores are zero (every selected logit -inf) the weights are 0
+ *              all k scores are zero (every selected logit -inf, or sigmoids of logits below -709.78,
+ *              which float64 does not hold) the weights are 0
  * Without a bias the logits themselves are compared; with one, and between groups, scores and sums are
  * float64: the selection is that of real arithmetic up to float64 rounding.  A NaN logit counts as the
  * largest and makes the weights NaN (with sigmoid scores: its own, and all of them with renormalize);

@@ -583,6 +583,9 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
     }
 }
 
+// 1 + exp(-l) is infinite in float64 from here down: the largest float32 that is (-709.78271 of -709.782713).
+constexpr float kZeroSigmoid = -0x1.62e430p9f;
+
 struct GateBackwardArgs {
     int64_t T;
     int E, k, sigmoid, renormalize;
@@ -635,14 +638,19 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __res
     const bool dense = !a.sigmoid && !a.renormalize;
     float q, spread = 0.0f;                                   // this slot's value; dense: the factor of the exponentials
     if (a.sigmoid) {
-        const float s = id >= 0 ? 1.0f / (1.0f + expf(-lj)) : 0.0f;
-        const float rest = 1.0f / (1.0f + expf(lj));          // 1 - s
+        // s = exp(min(l, 0)) / (1 + exp(-|l|)), 1 - s the other part of 1.  Renormalised, only the ratios of the s count:
+        // all are divided by exp(min(largest l, 0)), which keeps them in float32's range however small they are.
+        // Scores that float64 does not hold are zero, as in the gate.
+        const float e = expf(-fabsf(lj)), part = 1.0f / (1.0f + e);
+        const float rest = lj >= 0.0f ? e * part : part;
         if (a.renormalize) {
+            const float m = fminf(reduce<L>(lj > kZeroSigmoid ? lj : -__builtin_inff(), Max{}), 0.0f);
+            const float s = lj <= kZeroSigmoid ? 0.0f : (lj < 0.0f ? expf(lj - m) : 1.0f) * part;
             const float total = reduce<L>(s, Add{});
             const float w = total > 0.0f || total != total ? s / total : 0.0f;
             q = w * rest * (d - reduce<L>(d * w, Add{}));
         } else {
-            q = d * s * rest;
+            q = d * (lj < 0.0f ? e : 1.0f) * part * rest;
         }
     } else if (a.renormalize) {
         const float m = reduce<L>(lj, Max{});

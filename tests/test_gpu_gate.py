@@ -349,3 +349,40 @@ def test_refusals():
     ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
     with pytest.raises(ValueError):
         mel.router_gate_backward(x, ids, torch.zeros((4, 3), device="cuda"))
+
+
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_gate_backward_of_very_small_sigmoids(dtype, renorm):
+    """Selected logits about and far below the one whose sigmoid float32 can hold (-87), alone and beside ordinary
+    ones.  Renormalised, what counts is their ratio.  Scores that float64 does not hold (below -709.78) are zero."""
+    T, E, k = 96, 20, 6
+    t, l = _logits(T, E, dtype, 41)
+    rng = np.random.default_rng(6)
+    l = l.copy()
+    for i, level in enumerate((0, 60, 80, 87, 88, 89, 90, 100, 103, 120, 300, 700)):
+        l[i::24] -= level                                # the whole token
+        l[12 + i::24, ::2] -= level                      # every other expert
+    l[5, 3:] = -800
+    l[6] = -800
+    l[7, ::3] = -np.inf
+    t = torch.from_numpy(l).to(t.dtype)
+    l = t.float().numpy()
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    dp = rng.standard_normal((T, k)).astype(np.float32)
+    got = _check_backward(t, l, ids, dp, "sigmoid", renorm, 2.0)
+    assert np.all(got[6] == 0)
+    if renorm:
+        low = [i for i in range(T) if i % 24 < 12 and i not in (5, 6)]
+        assert np.all(np.abs(got[low]).max(1) > 0)
+
+
+def test_gate_backward_of_two_small_sigmoids():
+    """By hand: weights 1 / (1 + 1/e) and 1 / (1 + e) for logits one apart, far below 0; dlogits = w (1 - s) (d - sum d w)."""
+    for top in (-80.0, -88.0, -90.0, -200.0):
+        l = torch.tensor([[top, top - 1.0, 3.0]], device="cuda")
+        ids = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")
+        got = mel.router_gate_backward(l, ids, torch.tensor([[1.0, -1.0]], device="cuda"), score="sigmoid").cpu().numpy()[0]
+        a = 1 / (1 + np.exp(-1.0))
+        want = 2 * a * (1 - a)
+        assert np.all(np.abs(got - [want, -want, 0.0]) <= 64 * U * want)
