@@ -328,8 +328,10 @@ moe_status moe_router_topk(const float* logits, int64_t T, int64_t E, int64_t k,
  *              which float64 does not hold) the weights are 0
  * Without a bias the logits themselves are compared; with one, and between groups, scores and sums are
  * float64: the selection is that of real arithmetic up to float64 rounding.  A NaN logit counts as the
- * largest and makes the weights NaN (with sigmoid scores: its own, and all of them with renormalize);
- * with softmax a +inf logit does as well.  The ids are distinct and inside [0, E) in any case. */
+ * largest, its group's score too, and makes the weights NaN (with sigmoid scores: its own, and all of
+ * them with renormalize).  With softmax a +inf logit makes them NaN as well; a token without finite
+ * scores is selected by its logits alone.  The ids are distinct and inside [0, E) in any case; with a NaN
+ * in the bias the choice is unspecified. */
 enum moe_score_code { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 typedef struct moe_gate {
     int32_t score;        /* enum moe_score_code                                                 */

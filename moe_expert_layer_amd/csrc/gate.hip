@@ -193,19 +193,20 @@ __device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int
         if (den == 0.0)
             den = 1.0;                                        // every logit is -inf: scores 0
     }
+    // a NaN or +inf logit makes every softmax score NaN: the logits decide then, NaN first
+    const bool lost = !a.sigmoid && den != den;
     uint64_t key[kPer];                                       // 0: taken, or no candidate
     double c[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int e = lane + 64 * i;
         c[i] = num[i] / den + (a.bias != nullptr && e < a.E ? static_cast<double>(a.bias[e]) : 0.0);
-        if (l[i] == -__builtin_inff())
-            c[i] = -__builtin_inf();
-        // a NaN logit makes every softmax score NaN: the logits decide then (NaN first)
-        key[i] = e < a.E ? key64(a.bias != nullptr && c[i] == c[i] ? c[i] : static_cast<double>(l[i])) : 0;
+        if (lost || l[i] == -__builtin_inff())
+            c[i] = static_cast<double>(l[i]);
+        key[i] = e < a.E ? key64(a.bias != nullptr ? c[i] : static_cast<double>(l[i])) : 0;
     }
     if (a.groups > 1) {
-        double* const score = lds + a.E;
+        uint64_t* const score = reinterpret_cast<uint64_t*>(lds + a.E);   // keys: a NaN in a group makes it the largest
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
             if (lane + 64 * i < a.E)
@@ -215,19 +216,21 @@ __device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int
         const int per = a.E / a.groups;
         for (int q = lane; q < a.groups; q += 64) {
             double b1 = -__builtin_inf(), b2 = -__builtin_inf();
+            bool nan = false;
             for (int i = 0; i < per; ++i) {
                 const double v = lds[q * per + i];
+                nan |= v != v;
                 b2 = fmax(b2, fmin(b1, v));
                 b1 = fmax(b1, v);
             }
-            score[q] = a.group_top == 2 && b2 > -__builtin_inf() ? b1 + b2 : b1;
+            score[q] = nan ? ~uint64_t{0} : key64(a.group_top == 2 && b2 > -__builtin_inf() ? b1 + b2 : b1);
         }
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int q = min(lane + 64 * i, a.E - 1) / per;
-            const double mine = score[q];
+            const uint64_t mine = score[q];
             int rank = 0;
             for (int o = 0; o < a.groups; ++o)
                 rank += score[o] > mine || (score[o] == mine && o < q) ? 1 : 0;
@@ -266,7 +269,7 @@ __device__ __forceinline__ void gate_token_exact(const In* __restrict__ row, int
             my_num = won;
         }
     }
-    if (a.renormalize) {
+    if (a.renormalize && !lost) {
         den = sum(my_num);
         if (den == 0.0)
             den = 1.0;                                        // nothing but zero scores: weights 0

@@ -386,3 +386,57 @@ def test_gate_backward_of_two_small_sigmoids():
         a = 1 / (1 + np.exp(-1.0))
         want = 2 * a * (1 - a)
         assert np.all(np.abs(got - [want, -want, 0.0]) <= 64 * U * want)
+
+
+def _chosen_with_a_nan(l, k, score, bias, groups, topk_groups, group_top):
+    """The choice for one token with a NaN (or, with softmax, +inf) logit: the NaN counts as the largest, for its expert
+    and for its group.  A softmax has no scores then: the logits are compared, without the bias."""
+    if score == "softmax":
+        c = l.astype(np.float64)
+    else:
+        with np.errstate(over="ignore"):
+            c = 1 / (1 + np.exp(-l.astype(np.float64))) + (0 if bias is None else bias)
+    by = c if bias is not None or score == "softmax" else l.astype(np.float64)
+    c, by = np.where(np.isnan(c), 1e300, c), np.where(np.isnan(by), 1e300, by)
+    c, by = np.where(np.isneginf(l), -np.inf, c), np.where(np.isneginf(l), -np.inf, by)
+    per = l.size // groups
+    top = [np.sort(c[g * per:(g + 1) * per])[::-1][:group_top] for g in range(groups)]
+    sums = [v[v > -np.inf].sum() if (v > -np.inf).any() else -np.inf for v in top]
+    kept = sorted(range(groups), key=lambda g: (-sums[g], g))[:topk_groups]
+    return sorted((e for g in kept for e in range(g * per, (g + 1) * per)), key=lambda e: (-by[e], e))[:k]
+
+
+@pytest.mark.parametrize("E,groups,topk_groups", [(40, 8, 3), (64, 8, 2), (64, 4, 1), (250, 5, 2), (24, 24, 5)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_a_nan_logit_is_chosen_in_any_group(E, groups, topk_groups, score, with_bias):
+    """A NaN in a token's last, first or middle group (with softmax also +inf): its expert comes first, the weights
+    are NaN (sigmoid without renormalising: its own alone), and the other tokens are as ever."""
+    rng = np.random.default_rng(E + groups)
+    T, k = 24, 4
+    t, l = _logits(T, E, "f32", 17)
+    l = l.copy()
+    where = {}
+    for i, e in enumerate((E - 1, 0, E // 2, E - 2, E // 3, 1)):
+        value = [np.nan, -np.nan, np.inf][i % 3 if score == "softmax" else i % 2]
+        l[3 * i, e] = value
+        where[3 * i] = e
+        if i >= 3:
+            l[3 * i, rng.permutation(np.delete(np.arange(E), e))[:E // 4]] = -np.inf
+    bias = (0.3 * rng.standard_normal(E)).astype(np.float32) if with_bias else None
+    for top in (1, 2):
+        for renorm in (True, False):
+            ids, probs = mel.router_gate(torch.from_numpy(l).cuda(), k, score=score, groups=groups, topk_groups=topk_groups,
+                                         bias=None if bias is None else torch.from_numpy(bias).cuda(), group_top=top,
+                                         renormalize=renorm)
+            ids, probs = ids.cpu().numpy(), probs.cpu().numpy()
+            for row, e in where.items():
+                assert ids[row].tolist() == _chosen_with_a_nan(l[row], k, score, bias, groups, topk_groups, top)
+                assert ids[row, 0] == e
+                nan = np.isnan(probs[row])
+                assert nan.all() if renorm or score == "softmax" else nan.tolist() == [True] + [False] * (k - 1)
+            rest = [r for r in range(T) if r not in where]
+            rids, rw, _ = ref.gate(l[rest], k, score=score, bias=bias, groups=groups, topk_groups=topk_groups, group_top=top,
+                                   renormalize=renorm)
+            assert np.array_equal(ids[rest], rids)
+            assert np.all(np.abs(probs[rest] - rw) <= (5 * _spread(l[rest]) + 32) * U * rw)
