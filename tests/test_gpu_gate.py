@@ -440,3 +440,29 @@ def test_a_nan_logit_is_chosen_in_any_group(E, groups, topk_groups, score, with_
                                    renormalize=renorm)
             assert np.array_equal(ids[rest], rids)
             assert np.all(np.abs(probs[rest] - rw) <= (5 * _spread(l[rest]) + 32) * U * rw)
+
+
+@pytest.mark.parametrize("E,T,groups", [(8, 300, 1), (64, 300, 1), (64, 33000, 1), (256, 300, 8), (256, 9000, 8), (1000, 100, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_weights_far_from_the_largest(E, T, groups, score, renorm):
+    """Weights to float32's accuracy whatever the logits' distance.  A chosen expert's exponential is within 4 U: the
+    argument's rounding is made good, a 1-ulp exp (2 U), with sigmoid an addition and a quotient.  Of k <= 8 chosen ones
+    the sum adds 3 U, quotient and scale 2 U: 13 U, and 16 U here.  A softmax over all experts sums up to 1024 terms that
+    are off by (2.5 x + 2) U each at the distance x, on average at most ln 1024, by up to 22 additions: 20 + 22 + 4 + 2 = 48 U."""
+    rng = np.random.default_rng(E + T)
+    l = (1.5 * rng.standard_normal((T, E))).astype(np.float32)
+    far = rng.choice([0.0, 7.0, 20.0, 40.0, 60.0], T).astype(np.float32)[:, None]
+    if score == "sigmoid":
+        l -= far
+    else:
+        l[np.arange(T), rng.integers(0, E, T)] += far[:, 0]
+    k = min(8, E // 2)
+    kw = dict(score=score, renormalize=renorm, groups=groups, topk_groups=max(1, groups // 2), scale=1.5)
+    ids, probs = mel.router_gate(torch.from_numpy(l).cuda(), k, **kw)
+    at = np.arange(T) if T <= 300 else np.random.default_rng(1).choice(T, 300, replace=False)
+    rids, rw, _ = ref.gate(l[at], k, **kw)
+    assert np.array_equal(ids.cpu().numpy()[at], rids)
+    err = np.abs(probs.cpu().numpy()[at].astype(np.float64) - rw) / rw
+    print(f"[gate weights] E={E} T={T} {score} renorm={renorm}: {err.max() / U:.1f} U", flush=True)
+    assert err.max() <= (48 if score == "softmax" and not renorm else 16) * U
