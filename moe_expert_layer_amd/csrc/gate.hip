@@ -579,12 +579,12 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
         }
         // scores near float32's smallest: their ratios need float64's range
         unsure |= reduce<L>(bad, Add{}) != 0 || -reduce<L>(-least, Max{}) < 0x1p-100f;
-        const float factor = (a.renormalize ? 1.0f / reduce<L>(total, Add{}) : inv) * a.scale;
+        const float factor = a.renormalize ? 1.0f / reduce<L>(total, Add{}) : inv;   // scale comes last: it may be of any size
         for (int j = g; j < a.k && live && !unsure; j += L) {
             if (a.k > L)
                 winner(j);
             a.ids[t * a.k + j] = id;
-            a.probs[t * a.k + j] = n * factor;
+            a.probs[t * a.k + j] = n * factor * a.scale;
         }
     }
     // the tokens left, one after the other
@@ -614,7 +614,7 @@ __device__ __forceinline__ void store_logits4(uint16_t* p, const f32x4_t& v)
     *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
 }
 
-// dl of one token.  With w_j the unscaled weights and d_j = scale dprobs_j:
+// dl of one token, scale times the following.  With w_j the unscaled weights and d_j = dprobs_j:
 //   renormalised: q_j = w_j (d_j - sum_i d_i w_i), sigmoid times 1 - s_j; dl_e = the q_j with id e
 //   otherwise: sigmoid dl_e = d_j s_j (1 - s_j); softmax dl_e = s_e (d_j [id_j = e] - sum_i d_i s_i)
 // An id that occurs twice gets both; ids outside [0, E) are no slots.
@@ -645,7 +645,7 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __res
         if (id < 0 || id >= a.E)
             id = -1;
         else {
-            d = a.scale * a.dprobs[t * a.k + g];
+            d = a.dprobs[t * a.k + g];
             lj = load_logit(row + id);
         }
     }
@@ -708,8 +708,9 @@ __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __res
         total = reduce<L>(total, Add{});
         const float inv = total > 0.0f || total != total ? 1.0f / total : 0.0f;
         q = d * weight(lj) * inv;
-        spread = -inv * reduce<L>(q, Add{});
+        spread = -inv * reduce<L>(q, Add{}) * a.scale;
     }
+    q *= a.scale;
     // ids that several slots name: each such lane takes the sum of theirs, in slot order
     int* const mark = reinterpret_cast<int*>(dl);
     float under = 0.0f;                                       // dense: the exponential at this slot's id

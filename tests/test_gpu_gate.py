@@ -466,3 +466,25 @@ def test_weights_far_from_the_largest(E, T, groups, score, renorm):
     err = np.abs(probs.cpu().numpy()[at].astype(np.float64) - rw) / rw
     print(f"[gate weights] E={E} T={T} {score} renorm={renorm}: {err.max() / U:.1f} U", flush=True)
     assert err.max() <= (48 if score == "softmax" and not renorm else 16) * U
+
+
+@pytest.mark.parametrize("E,T", [(8, 50), (64, 50), (64, 33000)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [True, False])
+@pytest.mark.parametrize("scale", [2.0 ** 126, 2.0 ** 100, 2.0 ** -100])
+def test_any_finite_scale(E, T, score, renorm, scale):
+    """Weights and gradient are those of scale 1 (at most 1 in size) times a power of two: exact, but for values that
+    float32's subnormal steps of 2^-149 hold.  The scores, and the sums of the chosen ones, are small."""
+    l = _logits(T, E, "f32", E)[0]
+    if score == "sigmoid":
+        l = l - 40.0
+    l, k = l.cuda(), 4
+    ids, one = mel.router_gate(l, k, score=score, renormalize=renorm)
+    again, probs = mel.router_gate(l, k, score=score, renormalize=renorm, scale=scale)
+    assert torch.equal(ids, again)
+    torch.testing.assert_close(probs.double(), one.double() * scale, rtol=0, atol=2.0 ** -148)
+    dp = torch.randn((T, k), generator=torch.Generator().manual_seed(1)).cuda()
+    dp[:, 1] *= 8
+    small = mel.router_gate_backward(l, ids, dp / 64, score=score, renormalize=renorm)
+    large = mel.router_gate_backward(l, ids, dp / 64, score=score, renormalize=renorm, scale=scale)
+    torch.testing.assert_close(large.double(), small.double() * scale, rtol=0, atol=2.0 ** -140)
