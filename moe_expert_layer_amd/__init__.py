@@ -583,6 +583,9 @@ _SCORES = {"softmax": 0, "sigmoid": 1}
 def _gate(score, renormalize, groups, topk_groups, group_top, scale):
     if score not in _SCORES:
         raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    for name, v in (("groups", groups), ("topk_groups", topk_groups), ("group_top", group_top)):
+        if not -2 ** 31 <= v < 2 ** 31:                  # ctypes would keep the low 32 bits
+            raise ValueError(f"{name} = {v} does not fit an int32")
     return MoeGate(_SCORES[score], renormalize, groups, topk_groups, group_top, scale)
 
 

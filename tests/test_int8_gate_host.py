@@ -125,3 +125,14 @@ def test_plain_gate_against_a_sort():
     np.testing.assert_allclose(w.sum(1), 1.0)
     ids, _, _ = ref.gate(l, 6, groups=4, topk_groups=1, group_top=1)
     assert np.array_equal(ids[:, 0], l.argmax(1)) and np.all(ids // 6 == ids[:, :1] // 6)
+
+
+@pytest.mark.parametrize("place", [2, 3, 4])
+def test_gate_settings_that_do_not_fit(mel, place):
+    """Group settings of more than 32 bits are refused, not cut to their low bits."""
+    args = ["softmax", 1, 1, 1, 1, 1.0]
+    assert mel._gate(*args).groups == 1
+    for v in (2 ** 32 + 1, -2 ** 32 + 1, 2 ** 31):
+        args[place] = v
+        with pytest.raises(ValueError):
+            mel._gate(*args)
