@@ -40,7 +40,9 @@
  *                   expert and output channel (wg_scale / wu_scale [E, F], wd_scale [E, H]): a value
  *                   is code * scale.  Products are exact int32 sums, scaled in float32; h is float32
  *                   and quantised per row (the rule of moe_int8_quantize) before the down projection.
- *                   The output is bfloat16.
+ *                   The layer rounds each slot's sums of the down projection to float16's 11 bits
+ *                   (after a power of two; 2^-11 of the value) before scales and the sum over the k
+ *                   slots, which are float32.  The output is bfloat16.
  */
 #ifndef MOE_EXPERT_LAYER_H
 #define MOE_EXPERT_LAYER_H

@@ -480,7 +480,7 @@ moe_status run_ffn(int dtype, const void* rows, const uint8_t* rows_scale, int64
 
 // Workspace of the int8 calls: the tile table (each group one run of balanced tiles), h as float32 or as
 // partial sums, its codes and scales, the partial sums of y, and for the layer the routing, the quantised
-// x and the rows y.
+// x and the rows y (float16 sums).
 struct Int8Layout {
     RouteLayout route;
     Int8Plan fc1{}, fc2{};
@@ -542,10 +542,10 @@ struct Int8Weights {
 
 // fc1, SwiGLU with the quantisation of h, fc2 over grouped rows.  gather as for run_ffn.  row_experts
 // (may be null): the small layer's preparation has run, the tile table is there and each row's expert.
-// y null: the down projection's partial sums (L.fc2.partial) stay for the caller.
+// y: rows of y_type, MOE_BF16 or kInt8HalfSums; null: the down projection's partial sums (L.fc2.partial) stay for the caller.
 moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, const int32_t* offsets,
                         const int32_t* group_expert, int64_t G, int64_t E, int64_t H, int64_t F,
-                        const Int8Weights& w, void* y, void* ws, const Int8Layout& L, bool write_status,
+                        const Int8Weights& w, void* y, int y_type, void* ws, const Int8Layout& L, bool write_status,
                         hipStream_t s, const int32_t* gather, int gather_k, const int32_t* row_experts)
 {
     // the large layer's status word is the routing's: no group has a bad expert there
@@ -575,7 +575,7 @@ moe_status run_ffn_int8(const int8_t* rows, const float* rows_scale, int64_t M, 
         LAUNCH(s, "int8_quantize", launch_int8_quantize(MOE_F32, at<void>(ws, L.h), M, F, h_q, h_scale, s));
     LAUNCH(s, "fc2_i8",
            launch_gemm_i8(L.fc2, h_q, h_scale, w.down, w.down_scale, nullptr, nullptr,
-                          L.fc2.partial ? at<void>(ws, L.y_part) : y, MOE_BF16, M, F, H, groups, nullptr, 1,
+                          L.fc2.partial ? at<void>(ws, L.y_part) : y, y_type, M, F, H, groups, nullptr, 1,
                           at<int32_t>(ws, L.task_ctr) + kXcdCount, s));
     if (L.fc2.partial && y != nullptr)
         LAUNCH(s, "int8_finish",
@@ -787,16 +787,14 @@ MOE_API moe_status moe_expert_forward_int8(const moe_problem* p, const void* x, 
     }
     const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
     if (moe_status st = run_ffn_int8(rows, rows_scale, M, offsets, nullptr, E, E, H, F, w,
-                                     L.fc2.partial ? nullptr : at<void>(ws, L.y), ws, L, false, s, perm,
+                                     L.fc2.partial ? nullptr : at<void>(ws, L.y), kInt8HalfSums, ws, L, false, s, perm,
                                      static_cast<int>(k), small ? at<int32_t>(ws, L.row_experts) : nullptr);
         st != MOE_OK)
         return st;
-    if (L.fc2.partial)
-        LAUNCH(s, "int8_combine",
-               launch_int8_combine(at<int32_t>(ws, L.y_part), L.fc2.splits, at<float>(ws, L.h_scale), wd_scale, expert_ids,
-                                   pos, probs, T, k, H, static_cast<uint16_t*>(out_bf16), s));
-    else
-        LAUNCH(s, "unpermute", launch_unpermute(1, at<void>(ws, L.y), pos, probs, out_bf16, T, k, M, H, s));
+    LAUNCH(s, "int8_combine",
+           launch_int8_combine(at<void>(ws, L.fc2.partial ? L.y_part : L.y), L.fc2.partial ? L.fc2.splits : 0, F,
+                               at<float>(ws, L.h_scale), wd_scale, expert_ids, pos, probs, T, k, H,
+                               static_cast<uint16_t*>(out_bf16), s));
     return MOE_OK;
 }
 
@@ -1159,7 +1157,8 @@ MOE_API moe_status moe_grouped_ffn_int8(const moe_problem* p, const int8_t* rows
         st != MOE_OK)
         return st;
     const Int8Weights w{w_gate, w_up, w_down, wg_scale, wu_scale, wd_scale};
-    return run_ffn_int8(rows, rows_scale, M, group_offsets, group_expert, G, p->E, p->H, p->F, w, y_rows, workspace,
+    return run_ffn_int8(rows, rows_scale, M, group_offsets, group_expert, G, p->E, p->H, p->F, w, y_rows, MOE_BF16,
+                        workspace,
                         int8_layout(M, G, p->H, p->F, 0, 1, p->E, false), true, stream, nullptr, 1, nullptr);
 }
 

@@ -44,7 +44,7 @@ constexpr int kOwnTiles = 512;                 // of the table that a workgroup 
 constexpr int kOwnTableBytes = 16 * kOwnTiles + 8 * kWaves;    // and the scan's words
 static_assert(kOwnTiles <= kThreads && kMaxExperts < 1 << 23, "the own table's scan and entries");
 
-enum Out { kOutBf16, kOutF32, kOutPartial };
+enum Out { kOutBf16, kOutF32, kOutPartial, kOutHalf };     // kOutHalf: the sums times `unit`, as float16
 
 struct Args {
     const uint8_t* A;                          // int8 rows
@@ -60,6 +60,7 @@ struct Args {
     int32_t* task_ctr;                         // kXcdCount zeroed counters (large tiles)
     int K, N, splits;
     int64_t M;
+    float unit;
 };
 
 // WM x WN waves of TM x TN blocks of 32 x 32, S stages of BK values of K.
@@ -381,7 +382,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
         // first, in one wait: each wait also waits for the copies in flight and for the stores before it.
         [[maybe_unused]] f32x4_t scale[C::kTN][4];            // of column block j (gated: of its matrix)
         [[maybe_unused]] float row_scale[C::kTM];
-        if constexpr (kOut != kOutPartial) {
+        if constexpr (kOut == kOutBf16 || kOut == kOutF32) {
 #pragma unroll
             for (int j = 0; j < C::kTN; ++j) {
                 const int col = n0 + block_col<C, kGated>(wn, j);
@@ -409,7 +410,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
         for (int i = 0; i < C::kTM; ++i) {
             const int grow = tile.row_begin + row_block<C::kWM>(i, wm) + lrow;
             const bool live = grow < tile.row_end;
-            [[maybe_unused]] const float as = kOut != kOutPartial ? row_scale[i] : 0.0f;
+            [[maybe_unused]] const float as = kOut == kOutBf16 || kOut == kOutF32 ? row_scale[i] : a.unit;
 #pragma unroll
             for (int j = 0; j < C::kTN; ++j) {
                 if constexpr (kOut == kOutPartial) {
@@ -449,14 +450,16 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8(const Args a)
                         f32x4_t v;
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            v[e] = static_cast<float>(acc[i][j][4 * g + e]) * as * scale[j][g][e];
+                            v[e] = kOut == kOutHalf ? static_cast<float>(acc[i][j][4 * g + e]) * as
+                                                    : static_cast<float>(acc[i][j][4 * g + e]) * as * scale[j][g][e];
                         const int64_t at = static_cast<int64_t>(grow) * N + col + c;
                         if (live && col < N) {
                             if constexpr (kOut == kOutF32)
                                 *reinterpret_cast<f32x4_t*>(static_cast<float*>(a.out) + at) = v;
                             else
                                 *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(a.out) + at) =
-                                    u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                                    kOut == kOutHalf ? u32x2_t{pack_half2(v[0], v[1]), pack_half2(v[2], v[3])}
+                                                     : u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                         }
                     }
                 }
@@ -839,7 +842,7 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
 #pragma unroll
         for (int i = 0; i < kTM; ++i) {
             const int srow = min(done.row_begin + row_block<kWM>(i, wm) + lrow, done.row_end - 1);
-            const float as = a.a_scale[a.gather != nullptr ? a.gather[srow] / a.gather_k : srow];
+            const float as = kOut == kOutHalf ? a.unit : a.a_scale[a.gather != nullptr ? a.gather[srow] / a.gather_k : srow];
 #pragma unroll
             for (int ob = 0; ob < kBlocks; ob += kPiece) {
                 __builtin_amdgcn_sched_barrier(0);
@@ -850,7 +853,9 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
                     const float* sc = s0 + (col < N ? col : 0);
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
-                        const f32x4_t sg = *reinterpret_cast<const f32x4_t*>(sc + 8 * g + 4 * lh);
+                        f32x4_t sg = {1.0f, 1.0f, 1.0f, 1.0f};
+                        if constexpr (kOut != kOutHalf)
+                            sg = *reinterpret_cast<const f32x4_t*>(sc + 8 * g + 4 * lh);
                         f32x4_t v;
                         if constexpr (kGated) {
                             const f32x4_t su = *reinterpret_cast<const f32x4_t*>(s1 + col + 8 * g + 4 * lh);
@@ -869,7 +874,8 @@ __global__ __launch_bounds__(kThreads, 1) void grouped_gemm_i8_dma(const Args a)
                         else
                             *reinterpret_cast<__attribute__((address_space(3))) u32x2_t*>(
                                 stg + lrow * 128 + (((4 * b + g) ^ (lrow & 7)) << 4) + 8 * lh) =
-                                u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+                                kOut == kOutHalf ? u32x2_t{pack_half2(v[0], v[1]), pack_half2(v[2], v[3])}
+                                                 : u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
                     }
                 }
                 const int col = done_n0 + block_col<C, kGated>(wn, kGated ? 2 * ob : ob);
@@ -1075,12 +1081,15 @@ hipError_t launch_gemm_i8(const Int8Plan& p, const int8_t* A, const float* a_sca
     a.N = static_cast<int>(N);
     a.splits = p.splits;
     a.M = M;
+    a.unit = int8_half_unit(K);
     const bool gated = w1 != nullptr;
     if (p.partial)
         return gated ? i8::launch_rows<true, i8::kOutPartial>(p.row_tile, a, s)
                      : i8::launch_rows<false, i8::kOutPartial>(p.row_tile, a, s);
     if (gated)
         return i8::launch_rows<true, i8::kOutF32>(p.row_tile, a, s);
+    if (out_dtype == kInt8HalfSums)
+        return i8::launch_rows<false, i8::kOutHalf>(p.row_tile, a, s);
     return out_dtype == MOE_F32 ? i8::launch_rows<false, i8::kOutF32>(p.row_tile, a, s)
                                 : i8::launch_rows<false, i8::kOutBf16>(p.row_tile, a, s);
 }

@@ -41,7 +41,17 @@ struct Int8Groups {
     const int32_t* tile_count;
 };
 bool int8_own_tiles(const Int8Plan& p, int64_t M, int64_t G);
-// out: [M, N] of out_dtype (MOE_F32 / MOE_BF16), gated (w1 not null) float32 swiglu of the two
+// The layer keeps the down projection's sums as float16, times a power of two (of K) that brings the largest
+// possible one, 127 * 128 * K, to at most 2^15: 11 bits of each sum, where a scaled bfloat16 row would keep 8.
+constexpr int kInt8HalfSums = 100;          // out_dtype of launch_gemm_i8, beside the public ones
+inline float int8_half_unit(int64_t K)
+{
+    int bits = 0;
+    while ((int64_t{1} << bits) < K)
+        ++bits;
+    return bits > 1 ? 1.0f / static_cast<float>(1 << (bits - 1)) : 1.0f;
+}
+// out: [M, N] of out_dtype (MOE_F32 / MOE_BF16 / kInt8HalfSums), gated (w1 not null) float32 swiglu of the two
 // products, or the partial sums.  gather (may be null): row p of the product is row
 // gather[p] / gather_k of A and a_scale, whose rows then lie within 2^32 bytes.  task_ctr: kXcdCount zeroed
 // counters for this launch (256-row tiles).
@@ -73,8 +83,9 @@ hipError_t launch_int8_prologue(const int32_t* ids, int64_t T, int64_t k, int64_
                                 int32_t* perm, int32_t* pos, int32_t* row_experts, int32_t* status, int bm,
                                 MTile* tiles, int32_t* tile_count, const uint16_t* x, int64_t H, int8_t* codes, float* scales,
                                 hipStream_t s);
-// The layer's output [T, N] bfloat16 from the down projection's partial sums [splits, T k, N].
-hipError_t launch_int8_combine(const int32_t* partial, int splits, const float* a_scale, const float* w_scale,
+// The layer's output [T, N] bfloat16 from the down projection's sums: partial sums [splits, T k, N] int32, or with
+// splits 0 float16 rows [T k, N] (kInt8HalfSums).  K: the down projection's, for the rows' unit.
+hipError_t launch_int8_combine(const void* sums, int splits, int64_t K, const float* a_scale, const float* w_scale,
                                const int32_t* expert_ids, const int32_t* pos, const float* probs, int64_t T, int64_t k,
                                int64_t N, uint16_t* out, hipStream_t s);
 // out [M, N] from the partial sums [splits, M, N] of the rows that a group holds.

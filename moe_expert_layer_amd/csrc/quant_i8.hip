@@ -414,13 +414,39 @@ __global__ __launch_bounds__(kThreads) void int8_finish_kernel(
     }
 }
 
-// The combine of the layer straight from the down projection's partial sums: each slot's row is rounded
-// to bfloat16 as the stored rows of the other path are, and the k of a token are added in slot order
-// by fused multiply-adds from 0, as moe_unpermute does: bitwise the same output.  A chain of three loads
+// What the combine uses of a token's slots j .. j + kTogether - 1: no branch on a dropped slot or one past the last, so
+// that the loads of several slots go out together.
+template <int kTogether>
+struct Slots {
+    int64_t row[kTogether];                                   // of the sums (0 where not held)
+    const float* w[kTogether];                                // the expert's column scales
+    float scale[kTogether], p[kTogether];
+    bool held[kTogether];
+    __device__ __forceinline__ Slots(const int32_t* __restrict__ expert_ids, const int32_t* __restrict__ pos,
+                                     const float* __restrict__ probs, const float* __restrict__ a_scale,
+                                     const float* __restrict__ w_scale, int64_t t, int j, int k, int64_t M, int64_t N)
+    {
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i) {
+            const int64_t slot = t * k + min(j + i, k - 1);
+            const int64_t at = pos[slot];
+            const int id = expert_ids[slot];
+            held[i] = j + i < k && at >= 0 && at < M;
+            row[i] = held[i] ? at : 0;
+            w[i] = w_scale + static_cast<int64_t>(held[i] ? id : 0) * N;
+            scale[i] = a_scale[row[i]];
+            p[i] = probs[slot];
+        }
+    }
+};
+
+// The combine of the layer from the down projection's partial sums.  Each slot's sum is rounded to float16 as
+// the stored rows of the other path are (int8_combine_rows_kernel), scaled in float32, and the k of a token are
+// added in slot order by fused multiply-adds from 0: bitwise the same output.  A chain of three loads
 // bounds it at few tokens (one token of 4096, 8 cuts: 6.3 us slot by slot and four cuts at a time, 4.6 us so).
 template <int kTogether>
 __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
-    const int32_t* __restrict__ partial, int splits, const float* __restrict__ a_scale,
+    const int32_t* __restrict__ partial, int splits, float unit, const float* __restrict__ a_scale,
     const float* __restrict__ w_scale, const int32_t* __restrict__ expert_ids, const int32_t* __restrict__ pos,
     const float* __restrict__ probs, int64_t T, int k, int64_t M, int64_t N, uint16_t* __restrict__ out)
 {
@@ -428,36 +454,66 @@ __global__ __launch_bounds__(kThreads) void int8_combine_kernel(
     const int64_t c = 4 * (static_cast<int64_t>(blockIdx.y) * kThreads + threadIdx.x);
     if (t >= T || c >= N)
         return;
+    const float back = 1.0f / unit;
     f32x4_t sum = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int j = 0; j < k; j += kTogether) {
-        // no branch on a dropped slot or one past the last, so that the loads of several slots go out together
+        const Slots<kTogether> s(expert_ids, pos, probs, a_scale, w_scale, t, j, k, M, N);
         const int32_t* part[kTogether];
         i32x4_t a[kTogether];
         f32x4_t w[kTogether];
-        float scale[kTogether], p[kTogether];
-        bool held[kTogether];
 #pragma unroll
         for (int i = 0; i < kTogether; ++i) {
-            const int64_t slot = t * k + min(j + i, k - 1);
-            const int64_t row = pos[slot];
-            const int id = expert_ids[slot];
-            held[i] = j + i < k && row >= 0 && row < M;
-            const int64_t at = held[i] ? row : 0;
-            part[i] = partial + at * N + c;
-            w[i] = *reinterpret_cast<const f32x4_t*>(w_scale + static_cast<int64_t>(held[i] ? id : 0) * N + c);
-            scale[i] = a_scale[at];
-            p[i] = probs[slot];
+            part[i] = partial + s.row[i] * N + c;
+            w[i] = *reinterpret_cast<const f32x4_t*>(s.w[i] + c);
         }
         add_cuts<kTogether, 14 / kTogether>(part, splits, M * N, a);
 #pragma unroll
-        for (int i = 0; i < kTogether; ++i) {
-            const f32x4_t v = scaled(a[i], scale[i], w[i]);
+        for (int i = 0; i < kTogether; ++i)
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
-                sum[n] = held[i] ? fmaf(p[i], bf16_to_f32(f32_to_bf16(v[n])), sum[n]) : sum[n];
-        }
+            for (int n = 0; n < 4; ++n) {
+                const float v = half_to_f32(static_cast<uint16_t>(pack_half2(static_cast<float>(a[i][n]) * unit, 0.0f)));
+                sum[n] = s.held[i] ? fmaf(s.p[i], v * back * s.scale[i] * w[i][n], sum[n]) : sum[n];
+            }
     }
     *reinterpret_cast<u32x2_t*>(out + t * N + c) = u32x2_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3])};
+}
+
+// The same from stored float16 rows, a thread per eight columns of a token (16384 tokens of 7168, 4 slots each: 243 us
+// where the sum of scaled bfloat16 rows took 187; the product that writes the rows unscaled takes 80 us less).
+template <int kTogether>
+__global__ __launch_bounds__(kThreads) void int8_combine_rows_kernel(
+    const uint16_t* __restrict__ rows, float unit, const float* __restrict__ a_scale, const float* __restrict__ w_scale,
+    const int32_t* __restrict__ expert_ids, const int32_t* __restrict__ pos, const float* __restrict__ probs, int64_t T,
+    int k, int64_t M, int64_t N, uint16_t* __restrict__ out)
+{
+    const int64_t t = grid_row();
+    const int64_t c = 8 * (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x);
+    if (t >= T || c >= N)
+        return;
+    const float back = 1.0f / unit;
+    float sum[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j = 0; j < k; j += kTogether) {
+        const Slots<kTogether> s(expert_ids, pos, probs, a_scale, w_scale, t, j, k, M, N);
+        u32x4_t v[kTogether];
+        f32x4_t w[kTogether][2];
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i)
+            v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(rows + s.row[i] * N + c));
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+                w[i][q] = *reinterpret_cast<const f32x4_t*>(s.w[i] + c + 4 * q);
+#pragma unroll
+        for (int i = 0; i < kTogether; ++i)
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+                const float h = half_to_f32(static_cast<uint16_t>(v[i][n / 2] >> (16 * (n % 2))));
+                sum[n] = s.held[i] ? fmaf(s.p[i], h * back * s.scale[i] * w[i][n / 4][n % 4], sum[n]) : sum[n];
+            }
+    }
+    *reinterpret_cast<u32x4_t*>(out + t * N + c) =
+        u32x4_t{pack_bf16x2(sum[0], sum[1]), pack_bf16x2(sum[2], sum[3]), pack_bf16x2(sum[4], sum[5]), pack_bf16x2(sum[6], sum[7])};
 }
 
 // The table of balanced tiles alone: a thread per group (kWideThreads of them at a time), a scan, then a
@@ -688,20 +744,35 @@ hipError_t launch_int8_prologue(const int32_t* ids, int64_t T, int64_t k, int64_
     return hipGetLastError();
 }
 
-hipError_t launch_int8_combine(const int32_t* partial, int splits, const float* a_scale, const float* w_scale,
+hipError_t launch_int8_combine(const void* sums, int splits, int64_t K, const float* a_scale, const float* w_scale,
                                const int32_t* expert_ids, const int32_t* pos, const float* probs, int64_t T, int64_t k,
                                int64_t N, uint16_t* out, hipStream_t s)
 {
     if (T <= 0)
         return hipSuccess;
+    const float unit = int8_half_unit(K);
+    const int n = static_cast<int>(k);
+    // kTogether: slots whose loads go out together
+    if (splits == 0) {
+        const unsigned threads = static_cast<unsigned>(std::min<int64_t>(kThreads, ceil_div(N / 8, 64) * 64));
+        const dim3 grid = row_grid(T, ceil_div(N / 8, threads));
+        const auto* rows = static_cast<const uint16_t*>(sums);
+        if (k <= 2)
+            int8_combine_rows_kernel<2><<<grid, dim3(threads), 0, s>>>(rows, unit, a_scale, w_scale, expert_ids, pos, probs, T,
+                                                                       n, T * k, N, out);
+        else
+            int8_combine_rows_kernel<4><<<grid, dim3(threads), 0, s>>>(rows, unit, a_scale, w_scale, expert_ids, pos, probs, T,
+                                                                       n, T * k, N, out);
+        return hipGetLastError();
+    }
     const dim3 grid = row_grid(T, ceil_div(N, 4 * kThreads));
-    // slots whose loads go out together
+    const auto* partial = static_cast<const int32_t*>(sums);
     if (k <= 2)
-        int8_combine_kernel<2><<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs, T,
-                                                               static_cast<int>(k), T * k, N, out);
+        int8_combine_kernel<2><<<grid, dim3(kThreads), 0, s>>>(partial, splits, unit, a_scale, w_scale, expert_ids, pos, probs,
+                                                               T, n, T * k, N, out);
     else
-        int8_combine_kernel<4><<<grid, dim3(kThreads), 0, s>>>(partial, splits, a_scale, w_scale, expert_ids, pos, probs, T,
-                                                               static_cast<int>(k), T * k, N, out);
+        int8_combine_kernel<4><<<grid, dim3(kThreads), 0, s>>>(partial, splits, unit, a_scale, w_scale, expert_ids, pos, probs,
+                                                               T, n, T * k, N, out);
     return hipGetLastError();
 }
 

@@ -564,3 +564,27 @@ def test_ffn_rows_of_offsets_that_fall(off, expert, M, H, F):
         if at.any():
             y, slack = ref.ffn(rows[at], rs[at], *[t[e] for t in w])
             assert np.all(np.abs(got[at] - y) <= slack + BF * (np.abs(y) + slack))
+
+
+@pytest.mark.parametrize("T,H,F,E,k", [(1, 2048, 1024, 8, 8), (64, 256, 256, 16, 8), (2600, 256, 640, 40, 4), (900, 256, 256, 12, 8),
+                                       (300, 128, 1152, 8, 3), (520, 384, 4096, 4, 2), (70, 128, 16384, 2, 2), (2100, 3200, 256, 6, 6)])
+def test_layer_slots_are_summed_beyond_bfloat16(T, H, F, E, k):
+    """A slot's sum keeps float16's 11 bits (2^-11 of probs * y) where a bfloat16 row would keep 8; the rest as in
+    test_layer.  Weights of either sign, so that the slots' rows cancel and their roundings show."""
+    rng = np.random.default_rng(T + H + E)
+    w = _weights(rng, E, H, F)
+    x = torch.from_numpy(rng.standard_normal((T, H)).astype(np.float32)).bfloat16()
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    probs = (rng.dirichlet(np.ones(k), T) * rng.choice([-1.0, 1.0], (T, k))).astype(np.float32)
+    q, s = ref.quantize(x.float().numpy())
+    r, tol = np.zeros((T, H)), np.zeros((T, H))
+    for e in range(E):
+        t, j = np.nonzero(ids == e)
+        y, slack = ref.ffn(q[t], s[t], *[a[e] for a in w])
+        p = probs[t, j].astype(np.float64)[:, None]
+        np.add.at(r, t, p * y)
+        np.add.at(tol, t, np.abs(p) * (slack + (2.0 ** -11 + (2 * k + 8) * U) * (np.abs(y) + slack)))
+    print(f"[int8 layer] T={T} H={H} F={F} E={E} k={k}", flush=True)
+    out = _host(mel.expert_forward_int8(x.cuda(), None, *_dev(*w), *_dev(ids, probs)))
+    tol = tol + BF * (np.abs(r) + tol)
+    assert np.all(np.abs(out - r) <= tol)
