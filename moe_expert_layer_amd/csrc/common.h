@@ -36,17 +36,6 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi)
     return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
 }
 
-// Two floats to float16, round to nearest even, lo in the low half; and back.
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
-{
-    return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(lo))) |
-           static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(hi))) << 16;
-}
-__device__ __forceinline__ float half_to_f32(uint16_t h)
-{
-    return static_cast<float>(__builtin_bit_cast(_Float16, h));
-}
-
 // SwiGLU ("NPU Training Operators - MC2", 执行路径 step 8): silu(g) * u with silu(z) = z / (1 + e^-z).
 // e^-z is computed as 2^(-z log2 e) on the hardware exp2 unit and the quotient through the hardware
 // reciprocal (1 ulp).

@@ -1,10 +1,21 @@
-// Device side of the int8 products' row tiles: the rows of each group, and a group's balanced tiles.
+// Device side shared by the int8 kernels: the rows of each group, a group's balanced row tiles, float16 values.
 #pragma once
 
 #include "common.h"
 #include "internal.h"
 
 namespace moe {
+
+// Two floats to float16, round to nearest even, lo in the low half; and back.
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi)
+{
+    return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(lo))) |
+           static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<_Float16>(hi))) << 16;
+}
+__device__ __forceinline__ float half_to_f32(uint16_t h)
+{
+    return static_cast<float>(__builtin_bit_cast(_Float16, h));
+}
 
 // What a thread's group holds: its rows, the tiles before it and the tiles of all groups of the pass.
 struct GroupRows {
