@@ -588,3 +588,44 @@ def test_layer_slots_are_summed_beyond_bfloat16(T, H, F, E, k):
     out = _host(mel.expert_forward_int8(x.cuda(), None, *_dev(*w), *_dev(ids, probs)))
     tol = tol + BF * (np.abs(r) + tol)
     assert np.all(np.abs(out - r) <= tol)
+
+
+# Row tiles of 64 (small calls, cut products), 128 and 256 rows; k of both combines.
+@pytest.mark.parametrize("T,H,F,E,k", [(3, 2048, 1024, 8, 2), (200, 512, 512, 16, 8), (900, 256, 2048, 4, 2), (4000, 512, 640, 24, 4)])
+def test_captured_calls_replayed_on_one_workspace(T, H, F, E, k):
+    """Layer, grouped FFN and product captured into two graphs that share each call's workspace, replayed in turn on
+    new inputs with eager calls between: every replay bitwise the eager result, which repeats itself."""
+    rng = np.random.default_rng(T)
+    w = _dev(*_weights(rng, E, H, F))
+    x = torch.randn((T, H), device="cuda").bfloat16()
+    ids = torch.from_numpy(np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)).cuda()
+    probs = torch.softmax(torch.randn((T, k), device="cuda"), 1)
+    rows, rs = _dev(_codes(rng, T, H), _scale(rng, T, level=0.02))
+    off = _dev(np.concatenate([[0], np.sort(rng.integers(0, T + 1, E - 1)), [T]]).astype(np.int32))[0]
+    ex = torch.arange(E, dtype=torch.int32, device="cuda")
+    ws = [torch.full((256 << 20,), 255, dtype=torch.uint8, device="cuda") for _ in range(3)]
+
+    def step(spaces):
+        return (mel.expert_forward_int8(x, None, *w, ids, probs, workspace=spaces[0]),
+                mel.grouped_ffn_int8(rows, rs, off, ex, *w, workspace=spaces[1]),
+                mel.grouped_matmul_int8(rows, rs, off, ex, w[0], w[1], workspace=spaces[2]))
+
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs = step(ws)
+        graphs.append((g, outs))
+    for i in range(4):
+        x.copy_(torch.randn((T, H), device="cuda"))
+        rows.copy_(torch.randint(-127, 128, (T, H), device="cuda"))
+        off[1:-1] = torch.randint(0, T + 1, (E - 1,), device="cuda").sort().values
+        eager = step([None] * 3)
+        assert all(torch.equal(a, b) for a, b in zip(eager, step(ws)))
+        for g, outs in graphs:
+            for o in outs:
+                o.fill_(3.0)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(eager, outs))
