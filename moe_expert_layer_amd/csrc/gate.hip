@@ -13,9 +13,10 @@
 // random logits over 256 experts, and every token with a NaN) are done again in float64, one at a time
 // by the whole wave.
 //
-// Bound by vector arithmetic, not by its bytes: 65536 tokens of 256 experts in 8 groups, float32, take 42 us
-// (1.8 TB/s; a copy of the bytes would take 15), 83% of the cycles issuing it; in float64 throughout, a wave
-// per token, it took 247 us.  One token takes 4.3 us, a launch and a chain of reductions.
+// Bound by vector arithmetic, not by its bytes: 65536 tokens of 256 experts in 8 groups, float32, take 39-41 us
+// a call (a copy of the bytes would take 15), 68 vector instructions an expert that issue in 88% of the busy
+// cycles; in float64 throughout, a wave per token, it took 247 us.  One token takes 4.3 us, a launch and a
+// chain of reductions.
 #include <algorithm>
 #include <type_traits>
 
@@ -329,7 +330,9 @@ __global__ __launch_bounds__(kThreads) void gate_kernel(const In* __restrict__ l
     const bool live = t < a.T;
     const In* row = logits + (live ? t : a.T - 1) * a.E;
     const bool picked = a.topk_groups < a.groups;
-    bool unsure = picked && a.groups > L;                     // this token needs float64
+    // this token needs float64: all do with more groups than lanes (65536 tokens of 64 experts 81 us in 8 groups,
+    // 13 us in 4; of 256 experts 206 us in 32, 38 us in 16)
+    bool unsure = picked && a.groups > L;
     if (!__all(unsure)) {
         float l[kPer];
 #pragma unroll
@@ -622,9 +625,10 @@ __device__ __forceinline__ void store_logits4(uint16_t* p, const f32x4_t& v)
 // L lanes per token (at least k: lane j holds slot j).  The token's row of dl is put together in LDS -
 // zeros (dense softmax: its exponentials), then the slots' values at their ids - and goes out in vectors
 // of four; writing it is what the kernel costs.  An id held by two lanes is found by writing the lanes'
-// numbers into the row and reading them back, and only then the lanes look at each other.  Bound by the
-// stores: 65536 x 256 bfloat16 10.4-11.9 us (30.4 us where every lane stored its own experts), 8192 x 128
-// float32 of a dense softmax 5.7 us.
+// numbers into the row and reading them back, and only then the lanes look at each other.  Bound by
+// memory: 65536 x 256 bfloat16 in 11.3 us a call (30.4 us where every lane stored its own experts) moves 68
+// MB at 6 TB/s, half of them stores; a token's 8 chosen logits lie in 3.6 of its row's 4 lines of 128 bytes.
+// 8192 x 128 float32 of a dense softmax 5.8 us.
 template <class In, int L, bool kVec>
 __global__ __launch_bounds__(kThreads) void gate_backward_kernel(const In* __restrict__ logits,
                                                                  In* __restrict__ dlogits,

@@ -954,10 +954,12 @@ namespace {
 // 128 values of K: between `lone` for a workgroup by itself, latency, and `full` with all CUs busy, LDS
 // copies or for 256 rows the MFMAs; 2.5 more steps to fill and to finish) or its share of the weights
 // at 5.9 TB/s, and a part of the shorter one; a cut product has its sums written and, by one more
-// launch, read.  Constants fitted to 1500 timings (K x N of 4096 x 14336, 7168 x 2048, 2048 x 768, 1024 x
-// 4096, 1 to 32 groups of 1 to 700 rows, tiles of 64, 128 and 256 rows, 1 to 8 cuts): the plan taken is
-// within 12% of the best one everywhere and 0.2% on average, where a choice by rows per group alone lost
-// up to 2.8x (7168 x 2048, one group of 200 rows: 73 us with 256-row tiles, 26 us with 64 rows and 8 cuts).
+// launch, read.  Constants fitted to 1500 timings of whole calls (K x N of 4096 x 14336, 7168 x 2048, 2048 x
+// 768, 1024 x 4096, 1 to 32 groups of 1 to 700 rows, tiles of 64, 128 and 256 rows, 1 to 8 cuts), taken with
+// a launch for the tile table in each: the plan chosen was within 12% of the best of them, where a choice by
+// rows per group alone lost up to 2.8x (7168 x 2048, one group of 200 rows: 73 us with 256-row tiles, 26 us
+// with 64 rows and 8 cuts).  Products of less than some 20 us (2048 x 768, 1024 x 4096 with few groups) all
+// timed as the host's part of a call, so theirs is the other shapes' estimate; no shape was left out to check.
 struct Spread {                                // M rows over the groups that hold some
     double rows, held, per_group;
     Spread(int64_t M, int64_t G)

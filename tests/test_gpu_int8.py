@@ -2,8 +2,9 @@
 
 Tolerances.  U = 2^-24 is half a step of float32.  A product's sum is exact in int32; its conversion and
 two scalings are three roundings: 4 U relative, plus 2^-8 of the value for bfloat16 outputs.  For the
-FFN see int8_gate_reference.ffn; the layer rounds each slot's row to bfloat16 (2^-8 of probs * y) and
-sums k slots in float32 (k U each) before its own final rounding."""
+FFN see int8_gate_reference.ffn; the layer may round each slot's row to bfloat16 (2^-8 of probs * y; it
+keeps 2^-11, to which test_layer_slots_are_summed_beyond_bfloat16 holds it) and sums k slots in float32 (k U
+each) before its own final rounding."""
 import numpy as np
 import pytest
 import torch
