@@ -357,6 +357,7 @@ moe_status moe_router_gate(const moe_gate* gate, const void* logits, int32_t dty
  * the bias).  Of `gate`, score, renormalize and scale are used.  Every element of dlogits is written
  * (zero where no gradient arrives).  float32 arithmetic, no atomics.  An id that a token names twice
  * gets both slots' gradients; a slot whose id is outside [0, E) is skipped, as if it were not there.
+ * Where the gate takes a sigmoid for zero (logits below -709.78), so does its gradient.
  * Errors as for moe_router_gate. */
 moe_status moe_router_gate_backward(const moe_gate* gate, const void* logits, int32_t dtype, int64_t T,
                                     int64_t E, int64_t k, const int32_t* expert_ids,
