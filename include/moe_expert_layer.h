@@ -394,6 +394,96 @@ moe_status moe_mx_fc1_epilogue_encode(const float* v, int64_t rows, int64_t cols
                                       hipStream_t stream);
 
 /* ---------------------------------------------------------------------------------------------
+ * The shared expert: the dense feed-forward that every token passes beside its routed experts.  No
+ * page prints it; the definitions are this library's own.  dtype is MOE_F32 or MOE_BF16 for all
+ * tensors of a call; sums are float32 (bfloat16 products and float32 ones alike), with one rounding
+ * to the output's type.  Sizes are any numbers from 1 on (rows from 0 on).  Pointers need no more than
+ * their elements' alignment (rng: 8 bytes, the workspace: 16), except that the gated block reads
+ * bfloat16 operands whose rows are whole 16-byte chunks where they lie: x with H % 8 == 0, w_gate and
+ * w_up with F % 8 == 0 must be aligned to 16 bytes.  In the gated block's float32 products an infinite
+ * factor makes the sums it takes part in NaN.  Deterministic.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Dropout, wherever a call below takes `dropout` (p) and `rng`: D(v)[r,c] = 0 where bits(r,c) <
+ * round(65536 p), else v[r,c] * 65536 / (65536 - round(65536 p)): p counts to the nearest multiple of
+ * 2^-16.  bits(r,c) are 16 bits of Philox 4x32-10 (Salmon et al., "Parallel random numbers: as easy as
+ * 1, 2, 3", 2011) with key = rng[0] and counter words (c / 8, r, low and high half of rng[1]); output
+ * word (c % 8) / 2, its low half for even c.  rng [2] (seed and offset) is read on the device, so a
+ * captured call draws another mask when the values there change; no mask is stored, a call with the
+ * same rng draws the same one.  A dropped infinity or NaN is zero.  With round(65536 p) = 0 nothing is
+ * dropped and rng may be NULL; p = 1 drops everything. */
+
+/* out = D(x), or residual + D(x) with residual not NULL; x, residual, out [rows, cols] of dtype.  The
+ * gradient is the same call on dout without the residual (whose own gradient is dout).  out may be x
+ * or residual.  rows < 2^31, cols <= MOE_MAX_HIDDEN.  Errors: MOE_ERR_INVALID_ARGUMENT for bad sizes, a
+ * p outside [0, 1] or null pointers, MOE_ERR_UNSUPPORTED for another dtype (nothing enqueued). */
+moe_status moe_dropout(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t cols,
+                       double p, const int64_t* rng, void* out, hipStream_t stream);
+
+/* The gated block: both projections, the activation, the product and dropout,
+ *   g = x Wg, u = x Wu, h = D(act(g) * u)
+ * act: silu(z) = z / (1 + exp(-z)); gelu(z) = z (1 + erf(z / sqrt 2)) / 2; its tanh form
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
+enum moe_activation_code { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_GELU_TANH = 2 };
+typedef struct moe_gated {
+    int64_t T;            /* tokens, below 2^31                                                  */
+    int64_t H;            /* width of x, at most MOE_MAX_HIDDEN                                  */
+    int64_t F;            /* width of h, at most MOE_MAX_HIDDEN; T H, T F and H F at most 2^40   */
+    int32_t dtype;        /* MOE_F32 or MOE_BF16                                                 */
+    int32_t activation;   /* enum moe_activation_code                                            */
+    double dropout;       /* p in [0, 1]                                                         */
+} moe_gated;
+
+/* Host only.  Workspace bytes of moe_gated_projection (backward 0) or of its gradient (backward 1). */
+moe_status moe_gated_workspace_size(const moe_gated* g, int32_t backward, size_t* bytes /* host */);
+
+/* x [T,H], w_gate and w_up [H,F] -> h [T,F].  saved_gu: NULL, or [2,T,F] that receives g and u, rounded
+ * to dtype, for the gradient (h comes from the unrounded ones).  Errors: MOE_ERR_INVALID_ARGUMENT for
+ * bad sizes, an unknown activation, p outside [0, 1] or null pointers, MOE_ERR_UNSUPPORTED for another
+ * dtype or sizes over the limits, MOE_ERR_WORKSPACE_TOO_SMALL (nothing enqueued). */
+moe_status moe_gated_projection(const moe_gated* g, const void* x, const void* w_gate, const void* w_up,
+                                const int64_t* rng, void* h, void* saved_gu, void* workspace,
+                                size_t workspace_bytes, hipStream_t stream);
+
+/* Gradients of sum(dh * h): with d = D(dh) (the forward's mask, drawn again from the same rng),
+ *   dg = d u act'(g), du = d act(g)
+ *   dx = dg Wg^T + du Wu^T     dw_gate = x^T dg     dw_up = x^T du
+ * dh [T,F] -> dx [T,H], dw_gate and dw_up [H,F], all of dtype.  saved_gu: what the forward kept, or
+ * NULL: g and u are computed again and never leave the registers.  For the products dg and du are
+ * rounded to bfloat16 (MOE_BF16) or kept to 24 bits (MOE_F32).  Where d is zero (a dropped place among
+ * them) dg and du are zero, whatever g and u are.  T = 0 gives zero weight gradients.
+ * Errors as for moe_gated_projection. */
+moe_status moe_gated_projection_backward(const moe_gated* g, const void* x, const void* w_gate,
+                                         const void* w_up, const void* dh, const int64_t* rng,
+                                         const void* saved_gu, void* dx, void* dw_gate, void* dw_up,
+                                         void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* Low-rank adapters of many requests at once beside a shared projection: with a = ids[t],
+ *   out[t] = base[t] + scale[a] * (x[t] A[a][:, :r]) B[a][:r, :],   r = ranks[a]
+ * base (the projection's output) [T,N], x [T,K], a [L,K,R], b [L,R,N], out [T,N] of dtype; ids [T] int32;
+ * scale [L] float32 or NULL (1); ranks [L] int32 or NULL (R), clamped into [0, R]: an adapter's columns
+ * and rows from its rank on are not read.  A row whose id lies outside [0, L) has no adapter: out[t] =
+ * base[t].  x A is kept in float32.  out may be base; no other buffers may overlap it. */
+typedef struct moe_adapter {
+    int64_t T;            /* rows, below 2^31                                                    */
+    int64_t K;            /* width of x, at most MOE_MAX_HIDDEN                                  */
+    int64_t N;            /* width of base and out, at most MOE_MAX_HIDDEN                       */
+    int64_t L;            /* adapters, 1 .. 65536                                                */
+    int64_t R;            /* largest rank, 1 .. 256                                              */
+    int32_t dtype;        /* MOE_F32 or MOE_BF16                                                 */
+    int32_t reserved;     /* must be 0                                                           */
+} moe_adapter;
+
+/* Host only.  Workspace bytes of moe_adapter_add. */
+moe_status moe_adapter_workspace_size(const moe_adapter* p, size_t* bytes /* host */);
+
+/* Errors: MOE_ERR_INVALID_ARGUMENT for bad sizes or null pointers, MOE_ERR_UNSUPPORTED for another dtype
+ * or sizes over the limits, MOE_ERR_WORKSPACE_TOO_SMALL (nothing enqueued). */
+moe_status moe_adapter_add(const moe_adapter* p, const void* base, const void* x, const void* a,
+                           const void* b, const int32_t* ids, const float* scale, const int32_t* ranks,
+                           void* out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
  * Status, errors, diagnostics.
  * ------------------------------------------------------------------------------------------- */
 

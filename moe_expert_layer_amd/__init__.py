@@ -24,6 +24,8 @@ __all__ = [
     "intermediate_h", "quantized_x",
     "router_topk", "router_gate", "router_gate_backward", "int8_quantize", "grouped_matmul_int8",
     "grouped_ffn_int8", "expert_forward_int8",
+    "dropout", "gated_projection", "gated_projection_backward", "gated_workspace_size", "adapter_add",
+    "adapter_workspace_size",
     "timing_enable", "timing_collect", "timing_reset",
 ]
 
@@ -47,6 +49,16 @@ class MoeProblem(ctypes.Structure):
 class MoeGate(ctypes.Structure):
     _fields_ = [("score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("groups", ctypes.c_int32),
                 ("topk_groups", ctypes.c_int32), ("group_top", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class MoeGated(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("H", ctypes.c_int64), ("F", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("dropout", ctypes.c_double)]
+
+
+class MoeAdapter(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("L", ctypes.c_int64),
+                ("R", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class MoeError(RuntimeError):
@@ -86,6 +98,12 @@ _SIGS = {
     "moe_grouped_ffn_int8": [ctypes.POINTER(MoeProblem), _P, _P, _I64, _P, _P, _I64, _P, _P, _P,
                              _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_expert_forward_int8": [ctypes.POINTER(MoeProblem)] + [_P] * 12 + [ctypes.c_size_t, _P],
+    "moe_dropout": [_P, _P, ctypes.c_int32, _I64, _I64, ctypes.c_double, _P, _P, _P],
+    "moe_gated_workspace_size": [ctypes.POINTER(MoeGated), ctypes.c_int32, ctypes.POINTER(ctypes.c_size_t)],
+    "moe_gated_projection": [ctypes.POINTER(MoeGated)] + [_P] * 7 + [ctypes.c_size_t, _P],
+    "moe_gated_projection_backward": [ctypes.POINTER(MoeGated)] + [_P] * 10 + [ctypes.c_size_t, _P],
+    "moe_adapter_workspace_size": [ctypes.POINTER(MoeAdapter), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_adapter_add": [ctypes.POINTER(MoeAdapter)] + [_P] * 9 + [ctypes.c_size_t, _P],
     "moe_query_device_status": [_P, _P, ctypes.POINTER(ctypes.c_int32)],
     "moe_chunk_counters": [ctypes.POINTER(MoeProblem), _P, ctypes.c_size_t, _I64,
                            ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_I64)],
@@ -659,6 +677,152 @@ def mx_fc1_epilogue_encode(v, large_tiles: bool = True):
     _check(library().moe_mx_fc1_epilogue_encode(_ptr(v), rows, cols, 1 if large_tiles else 0,
                                                 _ptr(codes), _ptr(scales), _stream(v)))
     return codes, scales
+
+
+# ---------------------------------------------------------------------------------------------- shared expert
+
+_ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _need_rng(rng, p, device):
+    """rng is read where something can be dropped (p counts to the nearest multiple of 2^-16)."""
+    if rng is not None:
+        _need(rng, "rng", torch.int64, (2,), device)
+    elif not p * 65536 < 0.5:
+        raise ValueError("dropout needs rng, an int64 tensor [seed, offset] on the device")
+
+
+def dropout(x, p: float, rng=None, residual=None, out=None):
+    """D(x), or residual + D(x), for float32 or bfloat16 rows [rows, cols]: each value is dropped with
+    probability p (to the nearest multiple of 2^-16) and the kept ones are divided by 1 - p.  rng: int64
+    [2] on the device, seed and offset; the mask is drawn from these and the value's place (Philox, see
+    the C header), so the gradient is the same call on dout.  out may be x or residual."""
+    _need(x, "x")
+    dt = _dtype_code(x)
+    rows, cols = x.shape
+    p = float(p)
+    _need_rng(rng, p, x.device)
+    if residual is not None:
+        _need(residual, "residual", x.dtype, (rows, cols), x.device)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _need(out, "out", x.dtype, (rows, cols), x.device)
+    _call("moe_dropout", x.device, _ptr(x), _ptr(residual), dt, rows, cols, p, _ptr(rng), _ptr(out), _stream(x))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _gated(T, H, F, dtype, activation, p, backward):
+    """The call's MoeGated and its workspace bytes."""
+    if activation not in _ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(_ACTIVATIONS)}, got {activation!r}")
+    g = MoeGated(T, H, F, dtype, _ACTIVATIONS[activation], p)
+    n = ctypes.c_size_t()
+    _check(library().moe_gated_workspace_size(ctypes.byref(g), backward, ctypes.byref(n)))
+    return g, n.value
+
+
+def gated_workspace_size(T: int, H: int, F: int, dtype: int, backward: bool = False) -> int:
+    """Workspace bytes of gated_projection, or of its gradient, for F32 or BF16."""
+    return _gated(int(T), int(H), int(F), int(dtype), "silu", 0.0, int(bool(backward)))[1]
+
+
+def gated_projection(x, w_gate, w_up, activation: str = "silu", dropout: float = 0.0, rng=None, saved_gu=None,
+                     out=None, workspace=None):
+    """h = D(act(x w_gate) * (x w_up)): the gated block of a shared expert, float32 or bfloat16 x [T, H]
+    and weights [H, F] of any sizes; act "silu", "gelu" or "gelu_tanh"; D is dropout() with probability
+    `dropout`.  saved_gu: a tensor [2, T, F] that receives the gate and up values for the gradient."""
+    _need(x, "x")
+    dt = _dtype_code(x)
+    T, H = x.shape
+    F = w_gate.shape[1]
+    dev = x.device
+    _need(w_gate, "w_gate", x.dtype, (H, F), dev)
+    _need(w_up, "w_up", x.dtype, (H, F), dev)
+    p = float(dropout)
+    _need_rng(rng, p, dev)
+    if saved_gu is not None:
+        _need(saved_gu, "saved_gu", x.dtype, (2, T, F), dev)
+    g, nbytes = _gated(T, H, F, dt, activation, p, 0)
+    ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
+    if out is None:
+        out = x.new_empty((T, F))
+    else:
+        _need(out, "out", x.dtype, (T, F), dev)
+    _call("moe_gated_projection", dev, ctypes.byref(g), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(rng), _ptr(out),
+          _ptr(saved_gu), _ptr(ws), nbytes, _stream(x))
+    return out
+
+
+def gated_projection_backward(x, w_gate, w_up, dh, activation: str = "silu", dropout: float = 0.0, rng=None,
+                              saved_gu=None, workspace=None):
+    """Gradients of sum(dh * gated_projection(x, w_gate, w_up, ...)): (dx [T, H], dw_gate [H, F], dw_up
+    [H, F]) in x's dtype.  dropout and rng as in the forward; saved_gu: what it kept (else the gate and up
+    values are computed again)."""
+    _need(x, "x")
+    dt = _dtype_code(x)
+    T, H = x.shape
+    F = w_gate.shape[1]
+    dev = x.device
+    _need(w_gate, "w_gate", x.dtype, (H, F), dev)
+    _need(w_up, "w_up", x.dtype, (H, F), dev)
+    _need(dh, "dh", x.dtype, (T, F), dev)
+    p = float(dropout)
+    _need_rng(rng, p, dev)
+    if saved_gu is not None:
+        _need(saved_gu, "saved_gu", x.dtype, (2, T, F), dev)
+    g, nbytes = _gated(T, H, F, dt, activation, p, 1)
+    ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
+    dx = torch.empty_like(x)
+    dwg = torch.empty_like(w_gate)
+    dwu = torch.empty_like(w_up)
+    _call("moe_gated_projection_backward", dev, ctypes.byref(g), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(dh), _ptr(rng),
+          _ptr(saved_gu), _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(ws), nbytes, _stream(x))
+    return dx, dwg, dwu
+
+
+@functools.lru_cache(maxsize=256)
+def _adapter(T, K, N, L, R, dtype):
+    """The call's MoeAdapter and its workspace bytes."""
+    p = MoeAdapter(T, K, N, L, R, dtype, 0)
+    n = ctypes.c_size_t()
+    _check(library().moe_adapter_workspace_size(ctypes.byref(p), ctypes.byref(n)))
+    return p, n.value
+
+
+def adapter_workspace_size(T: int, K: int, N: int, L: int, R: int, dtype: int) -> int:
+    """Workspace bytes of adapter_add for F32 or BF16."""
+    return _adapter(int(T), int(K), int(N), int(L), int(R), int(dtype))[1]
+
+
+def adapter_add(base, x, a, b, ids, scale=None, ranks=None, out=None, workspace=None):
+    """out[t] = base[t] + scale[i] * (x[t] a[i][:, :r]) b[i][:r], i = ids[t], r = ranks[i]: each row's
+    low-rank adapter, added to the output of a shared projection.  base [T, N], x [T, K], a [L, K, R] and
+    b [L, R, N] float32 or bfloat16; ids int32 [T] (outside [0, L): the row has no adapter); scale float32
+    [L] (default 1); ranks int32 [L] (default R).  out may be base."""
+    _need(base, "base")
+    dt = _dtype_code(base)
+    T, N = base.shape
+    L, K, R = a.shape
+    dev = base.device
+    _need(x, "x", base.dtype, (T, K), dev)
+    _need(a, "a", base.dtype, (L, K, R), dev)
+    _need(b, "b", base.dtype, (L, R, N), dev)
+    _need(ids, "ids", torch.int32, (T,), dev)
+    if scale is not None:
+        _need(scale, "scale", torch.float32, (L,), dev)
+    if ranks is not None:
+        _need(ranks, "ranks", torch.int32, (L,), dev)
+    p, nbytes = _adapter(T, K, N, L, R, dt)
+    ws = None if nbytes == 0 else _workspace(nbytes, dev, workspace)
+    if out is None:
+        out = torch.empty_like(base)
+    else:
+        _need(out, "out", base.dtype, (T, N), dev)
+    _call("moe_adapter_add", dev, ctypes.byref(p), _ptr(base), _ptr(x), _ptr(a), _ptr(b), _ptr(ids), _ptr(scale),
+          _ptr(ranks), _ptr(out), _ptr(ws), nbytes, _stream(base))
+    return out
 
 
 # ---------------------------------------------------------------------------------------------- status

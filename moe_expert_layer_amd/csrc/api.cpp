@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>     // __device__ data: the allocation-free route's scratch
 #include <hip/hip_runtime_api.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -19,6 +20,7 @@
 
 #include "int8_gate.h"
 #include "internal.h"
+#include "shared_expert.h"
 
 #define MOE_API extern "C" __attribute__((visibility("default")))
 
@@ -1504,6 +1506,203 @@ MOE_API moe_status moe_timing_reset(void)
     }
     t.pending.clear();
     t.totals.clear();
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------- the shared expert
+
+namespace moe {
+namespace {
+
+// p and rng as the kernels take them.
+moe_status make_dropout(double p, const int64_t* rng, Dropout& d)
+{
+    if (!(p >= 0.0 && p <= 1.0))                         // a NaN as well
+        return fail(MOE_ERR_INVALID_ARGUMENT, "dropout must lie in [0, 1]");
+    d.threshold = static_cast<uint32_t>(std::floor(p * 65536.0 + 0.5));
+    d.scale = d.threshold < 65536 ? 65536.0f / static_cast<float>(65536 - d.threshold) : 0.0f;
+    d.rng = rng;
+    if (d.threshold != 0 && (rng == nullptr || (reinterpret_cast<uintptr_t>(rng) & 7) != 0))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "dropout needs rng, aligned to 8 bytes");
+    return MOE_OK;
+}
+
+moe_status check_plain_dtype(int32_t dtype)
+{
+    if (dtype != MOE_F32 && dtype != MOE_BF16)
+        return fail(MOE_ERR_UNSUPPORTED, "dtype must be MOE_F32 or MOE_BF16");
+    return MOE_OK;
+}
+
+// Pointers to values of dtype: not null and aligned to a value.
+moe_status check_values(int32_t dtype, std::initializer_list<const void*> pointers)
+{
+    const uintptr_t mask = static_cast<uintptr_t>(elem_bytes(dtype)) - 1;
+    for (const void* q : pointers) {
+        if (q == nullptr)
+            return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+        if ((reinterpret_cast<uintptr_t>(q) & mask) != 0)
+            return fail(MOE_ERR_INVALID_ARGUMENT, "pointer not aligned to its elements");
+    }
+    return MOE_OK;
+}
+
+moe_status check_workspace(const void* workspace, size_t bytes, size_t need)
+{
+    if (need > 0 && (workspace == nullptr || bytes < need))
+        return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes", need);
+    if ((reinterpret_cast<uintptr_t>(workspace) & 15) != 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "workspace must be aligned to 16 bytes");
+    return MOE_OK;
+}
+
+moe_status check_gated(const moe_gated* g)
+{
+    if (g == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "gated is null");
+    if (g->T < 0 || g->H <= 0 || g->F <= 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0, H and F positive");
+    if (g->T > INT32_MAX || g->H > MOE_MAX_HIDDEN || g->F > MOE_MAX_HIDDEN)
+        return fail(MOE_ERR_UNSUPPORTED, "T must be below 2^31, H and F at most %d", MOE_MAX_HIDDEN);
+    // the tiles of every product can then be numbered in 32 bits
+    if (std::max({g->T * g->H, g->T * g->F, g->H * g->F}) > int64_t{1} << 40)
+        return fail(MOE_ERR_UNSUPPORTED, "T * H, T * F and H * F must be at most 2^40");
+    if (g->activation != MOE_ACT_SILU && g->activation != MOE_ACT_GELU && g->activation != MOE_ACT_GELU_TANH)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "unknown activation %d", g->activation);
+    if (!(g->dropout >= 0.0 && g->dropout <= 1.0))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "dropout must lie in [0, 1]");
+    return check_plain_dtype(g->dtype);
+}
+
+// bfloat16 operands whose rows are whole 16-byte chunks are read where they lie, which needs the first row aligned too.
+moe_status check_gated_operands(const moe_gated* g, const void* x, const void* w_gate, const void* w_up)
+{
+    const auto off = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) != 0; };
+    if (g->dtype == MOE_BF16 && ((g->H % 8 == 0 && off(x)) || (g->F % 8 == 0 && (off(w_gate) || off(w_up)))))
+        return fail(MOE_ERR_INVALID_ARGUMENT, "bfloat16 x (H a multiple of 8) and weights (F a multiple of 8) must be "
+                                              "aligned to 16 bytes");
+    return MOE_OK;
+}
+
+moe_status check_adapter(const moe_adapter* p)
+{
+    if (p == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "adapter is null");
+    if (p->reserved != 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "reserved not 0");
+    if (p->T < 0 || p->K <= 0 || p->N <= 0 || p->L <= 0 || p->R <= 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0, K, N, L and R positive");
+    if (p->T > INT32_MAX || p->K > MOE_MAX_HIDDEN || p->N > MOE_MAX_HIDDEN || p->L > kMaxAdapters || p->R > kMaxRank)
+        return fail(MOE_ERR_UNSUPPORTED, "T must be below 2^31, K and N at most %d, L at most %d, R at most %d", MOE_MAX_HIDDEN,
+                    kMaxAdapters, kMaxRank);
+    return check_plain_dtype(p->dtype);
+}
+
+}  // namespace
+}  // namespace moe
+
+MOE_API moe_status moe_dropout(const void* x, const void* residual, int32_t dtype, int64_t rows, int64_t cols, double p,
+                               const int64_t* rng, void* out, hipStream_t stream)
+{
+    if (rows < 0 || cols <= 0)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "rows must be >= 0 and cols positive");
+    if (rows > INT32_MAX || cols > MOE_MAX_HIDDEN)
+        return fail(MOE_ERR_UNSUPPORTED, "rows must be below 2^31, cols at most %d", MOE_MAX_HIDDEN);
+    if (moe_status st = check_plain_dtype(dtype); st != MOE_OK)
+        return st;
+    Dropout d;
+    if (moe_status st = make_dropout(p, rng, d); st != MOE_OK)
+        return st;
+    if (rows == 0)
+        return MOE_OK;
+    if (moe_status st = check_values(dtype, {x, residual != nullptr ? residual : x, out}); st != MOE_OK)
+        return st;
+    LAUNCH(stream, "dropout", launch_dropout(x, residual, dtype, rows, cols, d, out, stream));
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_gated_workspace_size(const moe_gated* g, int32_t backward, size_t* bytes)
+{
+    if (moe_status st = check_gated(g); st != MOE_OK)
+        return st;
+    if (bytes == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+    *bytes = gated_layout(*g, backward != 0).total;
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_gated_projection(const moe_gated* g, const void* x, const void* w_gate, const void* w_up,
+                                        const int64_t* rng, void* h, void* saved_gu, void* workspace,
+                                        size_t workspace_bytes, hipStream_t stream)
+{
+    if (moe_status st = check_gated(g); st != MOE_OK)
+        return st;
+    Dropout d;
+    if (moe_status st = make_dropout(g->dropout, rng, d); st != MOE_OK)
+        return st;
+    if (g->T == 0)
+        return MOE_OK;
+    if (moe_status st = check_values(g->dtype, {x, w_gate, w_up, h, saved_gu != nullptr ? saved_gu : h}); st != MOE_OK)
+        return st;
+    if (moe_status st = check_gated_operands(g, x, w_gate, w_up); st != MOE_OK)
+        return st;
+    if (moe_status st = check_workspace(workspace, workspace_bytes, gated_layout(*g, false).total); st != MOE_OK)
+        return st;
+    LAUNCH(stream, "gated", launch_gated(*g, d, x, w_gate, w_up, h, saved_gu, workspace, stream));
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_gated_projection_backward(const moe_gated* g, const void* x, const void* w_gate, const void* w_up,
+                                                 const void* dh, const int64_t* rng, const void* saved_gu, void* dx,
+                                                 void* dw_gate, void* dw_up, void* workspace, size_t workspace_bytes,
+                                                 hipStream_t stream)
+{
+    if (moe_status st = check_gated(g); st != MOE_OK)
+        return st;
+    Dropout d;
+    if (moe_status st = make_dropout(g->dropout, rng, d); st != MOE_OK)
+        return st;
+    if (moe_status st = check_values(g->dtype, {dw_gate, dw_up}); st != MOE_OK)
+        return st;
+    if (g->T > 0) {
+        if (moe_status st = check_values(g->dtype, {x, w_gate, w_up, dh, dx, saved_gu != nullptr ? saved_gu : x}); st != MOE_OK)
+            return st;
+        if (moe_status st = check_gated_operands(g, x, w_gate, w_up); st != MOE_OK)
+            return st;
+    }
+    if (moe_status st = check_workspace(workspace, workspace_bytes, gated_layout(*g, true).total); st != MOE_OK)
+        return st;
+    LAUNCH(stream, "gated_backward",
+           launch_gated_backward(*g, d, x, w_gate, w_up, dh, saved_gu, dx, dw_gate, dw_up, workspace, stream));
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_adapter_workspace_size(const moe_adapter* p, size_t* bytes)
+{
+    if (moe_status st = check_adapter(p); st != MOE_OK)
+        return st;
+    if (bytes == nullptr)
+        return fail(MOE_ERR_INVALID_ARGUMENT, "null pointer");
+    *bytes = adapter_layout(*p).total;
+    return MOE_OK;
+}
+
+MOE_API moe_status moe_adapter_add(const moe_adapter* p, const void* base, const void* x, const void* a, const void* b,
+                                   const int32_t* ids, const float* scale, const int32_t* ranks, void* out,
+                                   void* workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    if (moe_status st = check_adapter(p); st != MOE_OK)
+        return st;
+    if (p->T == 0)
+        return MOE_OK;
+    if (moe_status st = check_values(p->dtype, {base, x, a, b, out}); st != MOE_OK)
+        return st;
+    if (moe_status st = check_values(MOE_F32, {ids, scale != nullptr ? static_cast<const void*>(scale) : ids,
+                                               ranks != nullptr ? ranks : ids}); st != MOE_OK)
+        return st;
+    if (moe_status st = check_workspace(workspace, workspace_bytes, adapter_layout(*p).total); st != MOE_OK)
+        return st;
+    LAUNCH(stream, "adapter", launch_adapter(*p, base, x, a, b, ids, scale, ranks, out, workspace, stream));
     return MOE_OK;
 }
 
