@@ -463,13 +463,14 @@ moe_status moe_gated_projection_backward(const moe_gated* g, const void* x, cons
  * base (the projection's output) [T,N], x [T,K], a [L,K,R], b [L,R,N], out [T,N] of dtype; ids [T] int32;
  * scale [L] float32 or NULL (1); ranks [L] int32 or NULL (R), clamped into [0, R]: an adapter's columns
  * and rows from its rank on are not read.  A row whose id lies outside [0, L) has no adapter: out[t] =
- * base[t].  x A is kept in float32.  out may be base; no other buffers may overlap it. */
+ * base[t].  x A is a float32 sum, kept to 16 bits (MOE_BF16) or 24 (MOE_F32) for the second product.  out
+ * may be base; no other buffers may overlap it. */
 typedef struct moe_adapter {
     int64_t T;            /* rows, below 2^31                                                    */
     int64_t K;            /* width of x, at most MOE_MAX_HIDDEN                                  */
     int64_t N;            /* width of base and out, at most MOE_MAX_HIDDEN                       */
-    int64_t L;            /* adapters, 1 .. 65536                                                */
-    int64_t R;            /* largest rank, 1 .. 256                                              */
+    int64_t L;            /* adapters, 1 .. 1023                                                 */
+    int64_t R;            /* largest rank, 1 .. 128                                              */
     int32_t dtype;        /* MOE_F32 or MOE_BF16                                                 */
     int32_t reserved;     /* must be 0                                                           */
 } moe_adapter;

@@ -10,22 +10,17 @@
 //   forward  A = x (kKC), B = Wg and Wu (kNC), both in one tile: the epilogue holds g and u of the same columns
 //   dx       A = dg, then du (kKC), B = Wg, then Wu (kKC): two segments of one sum
 //   dWg|dWu  A = x (kNC, M = H), B = dg | du (kNC): K = T
-// bfloat16 operands go to v_mfma_f32_32x32x16_bf16 as they are.  float32 operands are split exactly into three bfloat16
-// planes (x = x0 + x1 + x2, each the nearest to what is left, so |x1| <= 2^-8 |x| and |x2| <= 2^-16 |x|); six of the nine
-// products of planes make the sum, and the three left out are together at most 2^-23 of |a| |b|, the size of one float32
-// rounding.  Six bfloat16 MFMAs have about 2.6 times the rate of one float32 MFMA.  The small products go first, so that
-// the partial sums stay small until the last sixth of the additions.
+// bfloat16 operands go to v_mfma_f32_32x32x16_bf16 as they are, float32 operands as three bfloat16 planes (planes.h): six
+// segments of one sum, the small products first, so that the partial sums stay small until the last sixth of the additions.
 #include <algorithm>
 #include <atomic>
 #include <utility>
 
 #include "dropout.h"
+#include "planes.h"
 
 namespace moe {
 namespace {
-
-typedef short i16x4_t __attribute__((ext_vector_type(4)));
-typedef __attribute__((address_space(3))) i16x4_t lds_i16x4_t;
 
 enum Layout { kKC = 0, kNC = 1 };
 enum Epi {
@@ -367,20 +362,6 @@ struct Gemm {
     }
 };
 
-// Columns 16 p + 8 (lane / 32) .. + 7 of row lane % 32 of a transposed 32 x 32 block.  A lane holds columns 8 q + 4
-// (lane / 32) + e in register 4 q + e: exchanging halves of the registers of q = 2 p and 2 p + 1 between lanes i and
-// i + 32 makes runs of eight.
-__device__ __forceinline__ void run8(const f32x16_t& acc, int p, float (&v)[8])
-{
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[8 * p + e]), __float_as_uint(acc[8 * p + 4 + e]),
-                                                        false, false);
-        v[e] = __uint_as_float(r[0]);
-        v[4 + e] = __uint_as_float(r[1]);
-    }
-}
-
 // act(g) and its slope.  silu and gelu's tanh form are g s(z) with the logistic function s: z = g, and
 // z = 2 sqrt(2 / pi) (g + 0.044715 g^3) since (1 + tanh y) / 2 = s(2 y).  bfloat16 results take exponential and quotient
 // from the hardware's 1-ulp units, float32 ones from the exact functions.
@@ -412,36 +393,16 @@ __device__ __forceinline__ void activation(int act, float g, float& value, float
     slope = s + (st == 0.0f ? 0.0f : g * st * dz);
 }
 
-// A float32 value as three bfloat16 planes, each the nearest to what is left (x0 rounds towards zero where the nearest
-// would be infinite); the differences are exact, and what is left for x2 has at most 8 bits.  An infinity becomes
-// infinity and NaN, so that sums it takes part in are NaN.
-__device__ __forceinline__ void split3(float x, uint16_t (&p)[3])
-{
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        const uint32_t down = __float_as_uint(x) >> 16;
-        uint16_t b = f32_to_bf16(x);
-        if ((b & 0x7FFFu) == 0x7F80u && (__float_as_uint(x) & 0x7F800000u) != 0x7F800000u)
-            b = static_cast<uint16_t>(down);
-        p[i] = b;
-        x -= bf16_to_f32(b);
-    }
-}
-
 // Eight values to the planes at p (one bfloat16 plane, rounded, or three); p aligned to 16 bytes.
 template <bool kF32>
 __device__ __forceinline__ void store_planes(uint16_t* p, int64_t plane, const float (&v)[8])
 {
     if constexpr (kF32) {
-        uint16_t s[8][3];
+        u32x4_t q[3];
+        split8<3>(v, q);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            split3(v[i], s[i]);
-#pragma unroll
-        for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<u32x4_t*>(p + q * plane) =
-                u32x4_t{s[0][q] | static_cast<uint32_t>(s[1][q]) << 16, s[2][q] | static_cast<uint32_t>(s[3][q]) << 16,
-                        s[4][q] | static_cast<uint32_t>(s[5][q]) << 16, s[6][q] | static_cast<uint32_t>(s[7][q]) << 16};
+        for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<u32x4_t*>(p + i * plane) = q[i];
     } else {
         *reinterpret_cast<u32x4_t*>(p) = pack8_bf16(v);
     }
@@ -664,10 +625,9 @@ hipError_t launch_gemm(const GemmArgs& g, int dtype, hipStream_t s)
 // plane numbers (four bits each).
 void add_segments(GemmArgs& g, int dtype, int a0, int b0)
 {
-    static constexpr int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
     for (int i = dtype == MOE_F32 ? 0 : 5; i < 6; ++i) {
-        g.a_idx |= static_cast<uint64_t>(a0 + kPairs[i][0]) << (4 * g.nseg);
-        g.b_idx |= static_cast<uint64_t>(b0 + kPairs[i][1]) << (4 * g.nseg);
+        g.a_idx |= static_cast<uint64_t>(a0 + kPlanePairs[i][0]) << (4 * g.nseg);
+        g.b_idx |= static_cast<uint64_t>(b0 + kPlanePairs[i][1]) << (4 * g.nseg);
         ++g.nseg;
     }
 }
@@ -675,11 +635,10 @@ void add_segments(GemmArgs& g, int dtype, int a0, int b0)
 // dx's two sums interleaved by size: the small products of both first.
 void add_segments_pair(GemmArgs& g, int dtype, int a1)
 {
-    static constexpr int kPairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
     for (int i = dtype == MOE_F32 ? 0 : 5; i < 6; ++i)
         for (int m = 0; m < 2; ++m) {
-            g.a_idx |= static_cast<uint64_t>(m * a1 + kPairs[i][0]) << (4 * g.nseg);
-            g.b_idx |= static_cast<uint64_t>(8 * m + kPairs[i][1]) << (4 * g.nseg);
+            g.a_idx |= static_cast<uint64_t>(m * a1 + kPlanePairs[i][0]) << (4 * g.nseg);
+            g.b_idx |= static_cast<uint64_t>(8 * m + kPlanePairs[i][1]) << (4 * g.nseg);
             ++g.nseg;
         }
 }

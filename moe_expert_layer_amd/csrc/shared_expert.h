@@ -48,12 +48,13 @@ hipError_t launch_gated_backward(const moe_gated& g, const Dropout& d, const voi
                                  const void* dh, const void* saved_gu, void* dx, void* dwg, void* dwu, void* workspace,
                                  hipStream_t s);
 
-constexpr int kMaxAdapters = 65536;
-constexpr int kMaxRank = 256;
+constexpr int kMaxAdapters = 1023;
+constexpr int kMaxRank = 128;
 
 // adapter.hip: out = base + each row's adapter (moe_adapter_add).
 struct AdapterLayout {
-    size_t v = 0;                      // x A, float32 [T, R]
+    size_t count = 0, perm = 0, tiles = 0;   // the rows sorted by adapter
+    size_t v = 0;                            // x A, float32 partial sums
     size_t total = 0;
 };
 AdapterLayout adapter_layout(const moe_adapter& p);

@@ -258,7 +258,10 @@ def test_gated_float32_keeps_24_bits():
 @TYPES
 @pytest.mark.parametrize("T,K,N,L,R", [(1, 1, 1, 1, 1), (1, 64, 64, 2, 8), (3, 33, 9, 4, 3), (16, 128, 256, 5, 16),
                                        (17, 100, 130, 3, 13), (64, 520, 72, 40, 32), (200, 64, 1000, 7, 64), (90, 257, 65, 2, 100),
-                                       (33, 1024, 40, 9, 128), (40, 48, 48, 3, 256), (300, 72, 520, 1, 4)])
+                                       (33, 1024, 40, 9, 128), (40, 48, 48, 3, 128), (300, 72, 520, 1, 4),
+                                       # beyond what single rows are used for: every width of rank and of tile
+                                       (1, 14336, 264, 2, 128), (700, 4096, 1024, 9, 96), (130, 9000, 300, 3, 61),
+                                       (2500, 1000, 4104, 1023, 32), (600, 5001, 2003, 5, 24)])
 def test_adapter(dtype, T, K, N, L, R):
     base, x = randn(1, T, N, dtype=dtype), randn(2, T, K, dtype=dtype)
     a, b = randn(3, L, K, R, dtype=dtype, scale=K ** -0.5), randn(4, L, R, N, dtype=dtype, scale=R ** -0.5)

@@ -111,9 +111,9 @@ def _adapter(mel, **kw):
 
 
 @pytest.mark.parametrize("kw,expected", [
-    (dict(), 0), (dict(T=0), 0), (dict(K=1, N=1, L=1, R=1), 0), (dict(R=256, L=65536), 0), (dict(dtype=0), 0),
+    (dict(), 0), (dict(T=0), 0), (dict(K=1, N=1, L=1, R=1), 0), (dict(R=128, L=1023), 0), (dict(dtype=0), 0),
     (dict(T=-1), 1), (dict(K=0), 1), (dict(N=0), 1), (dict(L=0), 1), (dict(R=0), 1), (dict(reserved=1), 1),
-    (dict(R=257), 2), (dict(L=65537), 2), (dict(dtype=2), 2), (dict(T=1 << 31), 2), (dict(K=(1 << 22) + 1), 2),
+    (dict(R=129), 2), (dict(L=1024), 2), (dict(dtype=2), 2), (dict(T=1 << 31), 2), (dict(K=(1 << 22) + 1), 2),
     (dict(N=(1 << 22) + 1), 2),
 ])
 def test_adapter_sizes(mel, kw, expected):
@@ -131,7 +131,7 @@ def test_adapter_refusals(mel):
     def call(p, base=ok, x=ok, a=ok, b=ok, ids=ok, scale=None, ranks=None, out=ok, ws=ok, n=1 << 40):
         return lib.moe_adapter_add(ctypes.byref(p), base, x, a, b, ids, scale, ranks, out, ws, n, None)
 
-    p = _adapter(mel)
+    p = _adapter(mel, T=4000, K=4096, N=4096, R=128)           # sizes that need a workspace
     for name in ("base", "x", "a", "b", "ids", "out"):
         assert call(p, **{name: None}) == 1
     for name in ("scale", "ranks", "ids"):
