@@ -25,7 +25,7 @@ SOURCES = ["api.cpp", "route.hip", "permute.hip", "gemm_f32.hip", "gemm_bf16.hip
            "router.hip", "gemm_bwd.hip", "gate.hip", "gemm_i8.hip", "quant_i8.hip", "gated.hip", "dropout.hip",
            "adapter.hip"]
 HEADERS = ["common.h", "internal.h", "gemm_common.h", "int8_gate.h", "int8_tiles.h", "shared_expert.h",
-           "dropout.h", "planes.h"]
+           "dropout.h", "planes.h", "vec8.h"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

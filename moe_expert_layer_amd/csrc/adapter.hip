@@ -38,22 +38,25 @@ struct Args {
     const int32_t *ids, *ranks;
     const float* scale;
     int T, K, N, L, R;
-    bool vec_k, vec_r, vec_n;             // rows of x, of A, of B / base / out are whole, aligned 16-byte chunks
 };
 
 __device__ __forceinline__ int rank_of(const Args& g, int a) { return g.ranks == nullptr ? g.R : min(max(g.ranks[a], 0), g.R); }
 
 // ------------------------------------------------------------------------------------------------ few rows
 
+constexpr int kRowThreads = 1024;         // 16 waves: a CU has one or two of these workgroups, and 128 KiB in flight
+constexpr int kRowWaves = kRowThreads / 64;
+
 // Workgroup (t, c): row t, output columns [c cols, (c + 1) cols).  Threads take (k, 8 columns of A) and add over k, then
-// (r, 8 columns of B) and add over r, both joined through LDS in a fixed order.
-template <class T>
-__global__ __launch_bounds__(kThreads) void row_kernel(Args g, int cols)
+// (r, 8 columns of B) and add over r; both are joined in a fixed order, within the wave and then through LDS.  Loads go
+// out in batches, and what does not wait for v (the first rows of B, base) at the start.
+template <class T, bool kWhole>
+__global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
 {
-    constexpr int kJoin = 32;                              // partial sums of a column that one thread adds in a row
-    __shared__ float part[kThreads * 8];
+    constexpr int kBatch = 8;
+    __shared__ float part[kRowThreads * 8];
     __shared__ float v[kMaxRank];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int64_t t = blockIdx.x;
     const T* const base = static_cast<const T*>(g.base) + t * g.N;
     T* const out = static_cast<T*>(g.out) + t * g.N;
@@ -63,87 +66,117 @@ __global__ __launch_bounds__(kThreads) void row_kernel(Args g, int cols)
     const int rank = on ? rank_of(g, a) : 0;
     if (rank == 0) {                                       // uniform: the row is copied
         if (g.base != g.out)
-            for (int n = n0 + 8 * tid; n < n1; n += 8 * kThreads) {
+            for (int n = n0 + 8 * tid; n < n1; n += 8 * kRowThreads) {
                 float w[8];
-                load8(w, base + n, n1 - n, g.vec_n);
-                store8(out + n, w, n1 - n, g.vec_n);
+                load8(w, base + n, n1 - n);
+                store8(out + n, w, n1 - n);
             }
         return;
     }
+    const float scale = g.scale == nullptr ? 1.0f : g.scale[a];
+    // threads per run of 8 output columns: as many as the run of columns leaves, at most the rank
+    const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(a) * g.R * g.N;
+    const int runs = min(kRowThreads, (n1 - n0 + 7) / 8), lanes = max(1, min(rank, kRowThreads / runs));
+    const int q = tid % runs, rr = tid / runs;
+    const int left0 = n1 - n0 - 8 * q;
+    Raw8<T> b0 = load_raw<kWhole>(B + static_cast<int64_t>(rr) * g.N + n0 + 8 * q, rr < lanes ? left0 : 0);
+    Raw8<T> base0 = load_raw<kWhole>(base + n0 + 8 * q, rr == 0 ? left0 : 0);
     {
         const T* const x = static_cast<const T*>(g.x) + t * g.K;
         const T* const A = static_cast<const T*>(g.a) + static_cast<int64_t>(a) * g.K * g.R;
-        const int chunks = (rank + 7) / 8, lanes = kThreads / chunks;   // threads per column chunk
-        const int c = tid % chunks, kk = tid / chunks;
+        // a power of two of column chunks, so that the lanes of one chunk are whole strides of the wave
+        const int bits = rank <= 8 ? 0 : 32 - __clz((rank - 1) >> 3), chunks = 1 << bits;
+        const int c = tid & (chunks - 1), stride = kRowThreads >> bits;
+        const int width = 8 * c < rank ? g.R - 8 * c : 0;
         float sum[8] = {};
-        if (kk < lanes) {
-#pragma unroll 8
-            for (int k = kk; k < g.K; k += lanes) {
-                float w[8];
-                load8(w, A + static_cast<int64_t>(k) * g.R + 8 * c, rank - 8 * c, g.vec_r);
-                const float xk = to_float(x[k]);
+        for (int k0 = tid >> bits; k0 < g.K; k0 += kBatch * stride) {
+            Raw8<T> w[kBatch];
+            T xk[kBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sum[i] = fmaf(xk, w[i], sum[i]);
+            for (int i = 0; i < kBatch; ++i) {
+                const int k = k0 + i * stride;
+                w[i] = load_raw<kWhole>(A + static_cast<int64_t>(k) * g.R + 8 * c, k < g.K ? width : 0);
+                xk[i] = x[min(k, g.K - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                float f[8];
+                w[i].values(f);
+                const float m = k0 + i * stride < g.K ? to_float(xk[i]) : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum[e] = fmaf(m, f[e], sum[e]);
             }
         }
+        for (int d = 32; d >= chunks; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            part[i * kThreads + tid] = sum[i];
-        // column r = 8 c + i: parts part[i][c + chunks kk]; halve them until a thread can add them in a row
-        int left = lanes;
-        while (left > kJoin) {
-            __syncthreads();
-            const int half = (left + 1) / 2;
-            if (kk < left - half)
+            for (int i = 0; i < 8; ++i)
+                sum[i] += __shfl_xor(sum[i], d);
+        if (lane < chunks)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    part[i * kThreads + tid] += part[i * kThreads + tid + half * chunks];
-            left = half;
-        }
+            for (int i = 0; i < 8; ++i)
+                part[wave * kMaxRank + 8 * lane + i] = sum[i];
         __syncthreads();
         if (tid < rank) {
             float s = 0.0f;
-            for (int q = 0; q < left; ++q)
-                s += part[(tid % 8) * kThreads + tid / 8 + chunks * q];
-            v[tid] = g.scale == nullptr ? s : s * g.scale[a];
+#pragma unroll
+            for (int w = 0; w < kRowWaves; ++w)
+                s += part[w * kMaxRank + tid];
+            v[tid] = s * scale;
         }
         __syncthreads();
     }
-    const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(a) * g.R * g.N;
-    // threads per run of 8 output columns: as many as the run of columns leaves, at most the rank
-    const int runs = min(kThreads, (n1 - n0 + 7) / 8), lanes = max(1, min(rank, kThreads / runs));
     for (int first = n0; first < n1; first += 8 * runs) {      // the same number of passes for every thread
-        const int q = tid % runs, rr = tid / runs, n = first + 8 * q;
+        const int n = first + 8 * q;
         float sum[8] = {};
-        if (rr < lanes && n < n1)
-#pragma unroll 4
-            for (int r = rr; r < rank; r += lanes) {
-                float w[8];
-                load8(w, B + static_cast<int64_t>(r) * g.N + n, n1 - n, g.vec_n);
+        if (rr < lanes && n < n1) {
+            if (first != n0)
+                b0 = load_raw<kWhole>(B + static_cast<int64_t>(rr) * g.N + n, n1 - n);
+            for (int r0 = rr + lanes; ; r0 += kBatch * lanes) {
+                Raw8<T> w[kBatch];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sum[i] = fmaf(v[r], w[i], sum[i]);
+                for (int i = 0; i < kBatch; ++i)
+                    w[i] = load_raw<kWhole>(B + static_cast<int64_t>(r0 + i * lanes) * g.N + n, r0 + i * lanes < rank ? n1 - n : 0);
+                float f[8];
+                if (r0 == rr + lanes) {                        // the row that was loaded first
+                    b0.values(f);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum[e] = v[rr] * f[e];
+                }
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    w[i].values(f);
+                    const float m = r0 + i * lanes < rank ? v[r0 + i * lanes] : 0.0f;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        sum[e] = fmaf(m, f[e], sum[e]);
+                }
+                if (r0 + kBatch * lanes >= rank)
+                    break;
             }
+        }
         if (lanes > 1) {
             __syncthreads();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                part[i * kThreads + tid] = sum[i];
+                part[i * kRowThreads + tid] = sum[i];
             __syncthreads();
             if (rr == 0)
                 for (int p = 1; p < lanes; ++p)
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        sum[i] += part[i * kThreads + tid + p * runs];
+                        sum[i] += part[i * kRowThreads + tid + p * runs];
         }
         if (rr == 0 && n < n1) {
-            float w[8];
-            load8(w, base + n, n1 - n, g.vec_n);
+            if (first != n0)
+                base0 = load_raw<kWhole>(base + n, n1 - n);
+            float f[8];
+            base0.values(f);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                w[i] += sum[i];
-            store8(out + n, w, n1 - n, g.vec_n);
+                sum[i] += f[i];
+            store8(out + n, sum, n1 - n);
         }
     }
 }
@@ -165,12 +198,24 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
 {
     __shared__ int rows[kPlanThreads + 1], tile0[kPlanThreads + 1], place[kPlanThreads], sums[2][kPlanThreads / 64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    // Adds the lanes' rows to their bins' counters, returns each lane's place.  Rows of one request lie side by side:
+    // a wave of one bin adds once (64 additions to one counter would take turns).
+    const auto add = [&](uint32_t t) {
+        const int a = ids[t], bin = a >= 0 && a < L ? a : L;
+        if (__all(bin == __builtin_amdgcn_readfirstlane(bin))) {
+            const uint64_t active = __ballot(1);
+            const int before = __popcll(active & ((uint64_t{1} << lane) - 1));
+            int first = 0;
+            if (before == 0)
+                first = atomicAdd(&place[bin], __popcll(active));
+            return __builtin_amdgcn_readfirstlane(first) + before;
+        }
+        return atomicAdd(&place[bin], 1);
+    };
     place[tid] = 0;
     __syncthreads();
-    for (uint32_t t = tid; t < static_cast<uint32_t>(T); t += kPlanThreads) {   // T + 1024 may pass 2^31
-        const int a = ids[t];
-        atomicAdd(&place[a >= 0 && a < L ? a : L], 1);
-    }
+    for (uint32_t t = tid; t < static_cast<uint32_t>(T); t += kPlanThreads)   // T + 1024 may pass 2^31
+        add(t);
     __syncthreads();
     // exclusive sums over the bins of rows and of tiles
     const int n = place[tid], nt = (n + kTile - 1) / kTile;
@@ -197,10 +242,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
         rows[0] = tile0[0] = 0;
     place[tid] = s0 - n;
     __syncthreads();
-    for (uint32_t t = tid; t < static_cast<uint32_t>(T); t += kPlanThreads) {   // T + 1024 may pass 2^31
-        const int a = ids[t];
-        perm[atomicAdd(&place[a >= 0 && a < L ? a : L], 1)] = static_cast<int32_t>(t);
-    }
+    for (uint32_t t = tid; t < static_cast<uint32_t>(T); t += kPlanThreads)
+        perm[add(t)] = static_cast<int32_t>(t);
     const int total = tile0[L + 1];
     if (tid == 0)
         count[0] = total;
@@ -243,10 +286,10 @@ __device__ __forceinline__ f32x16_t mfma_planes(const bf16x8_t (&w)[PB], const b
 }
 
 // v of a tile's rows over one cut of K.  Waves: 2 row halves of 32 x 2 halves of each K step; kRB column blocks of 32.
-template <class T, int kRB>
+template <class T, int kRB, bool kWhole>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
 {
-    constexpr int P = Raw8<T>::kPlanes;
+    constexpr int P = kPlanesOf<T>;
     constexpr int kStep = kRB == 4 ? 64 : 128, kGroups = kStep / 32;       // MFMA steps of 16 k per wave and K step
     constexpr int kCols = 32 * kRB, kRow = 2 * kCols + 16;                 // bytes of one k row in LDS
     constexpr int kPlane = kStep * kRow, kLoads = kStep * kCols / 8 / kThreads;
@@ -278,14 +321,12 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int c = (tid + i * kThreads) % (kCols / 8), k = k0 + (tid + i * kThreads) / (kCols / 8);
-            ar[i] = load_raw(A + static_cast<int64_t>(k) * g.R + 8 * c, k < g.K ? rank - 8 * c : 0, g.vec_r);
+            ar[i] = load_raw<kWhole>(A + static_cast<int64_t>(k) * g.R + 8 * c, k < g.K ? g.R - 8 * c : 0);
         }
-        if (busy)
-#pragma unroll
-            for (int s = 0; s < kGroups; ++s) {
-                const int k = k0 + (kStep / 2) * wk + 16 * s + 8 * (lane >> 5);
-                xr[s] = load_raw(x + k, g.K - k, g.vec_k);
-            }
+    };
+    const auto fetch_x = [&](int step, int s) {
+        const int k = step * kStep + (kStep / 2) * wk + 16 * s + 8 * (lane >> 5);
+        xr[s] = load_raw<kWhole>(x + k, busy ? g.K - k : 0);
     };
     f32x16_t acc[kRB];
 #pragma unroll
@@ -293,33 +334,37 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             acc[j][e] = 0.0f;
-    if (step0 < step1)
+    if (step0 < step1) {
         fetch(step0);
+#pragma unroll
+        for (int s = 0; s < kGroups; ++s)
+            fetch_x(step0, s);
+    }
     for (int step = step0; step < step1; ++step) {
         __syncthreads();                                  // the stage of the step before is read
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int at = tid + i * kThreads;
             u32x4_t pl[P];
-            ar[i].planes(pl);
+            planes8(ar[i], pl);
 #pragma unroll
             for (int q = 0; q < P; ++q)
                 *reinterpret_cast<u32x4_t*>(smem + q * kPlane + (at / (kCols / 8)) * kRow + 16 * (at % (kCols / 8))) = pl[q];
         }
-        u32x4_t xp[kGroups][P];
-#pragma unroll
-        for (int s = 0; s < kGroups; ++s)
-            xr[s].planes(xp[s]);
         __syncthreads();
         if (step + 1 < step1)
             fetch(step + 1);
         if (busy)
 #pragma unroll
             for (int s = 0; s < kGroups; ++s) {
+                u32x4_t xp[P];
+                planes8(xr[s], xp);
                 bf16x8_t r[P];
 #pragma unroll
                 for (int q = 0; q < P; ++q)
-                    r[q] = __builtin_bit_cast(bf16x8_t, xp[s][q]);
+                    r[q] = __builtin_bit_cast(bf16x8_t, xp[q]);
+                if (step + 1 < step1)
+                    fetch_x(step + 1, s);
 #pragma unroll
                 for (int j = 0; j < kRB; ++j) {
                     bf16x8_t w[P];
@@ -340,7 +385,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
             for (int h = 0; h < 2; ++h) {
                 float w[8];
                 run8(acc[j], h, w);
-                store8(join + 32 * j + 16 * h, w, 8, true);
+                store8(join + 32 * j + 16 * h, w, 8);
             }
     __syncthreads();
     if (busy && wk == 0) {
@@ -352,22 +397,23 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
             for (int h = 0; h < 2; ++h) {
                 float w[8], u[8];
                 run8(acc[j], h, w);
-                load8(u, join + 32 * j + 16 * h, 8, true);
+                load8(u, join + 32 * j + 16 * h, 8);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     w[i] = (w[i] + u[i]) * f;
                 if (32 * wr + (lane & 31) < n)
-                    store8(v + 32 * j + 16 * h, w, 8, true);
+                    store8(v + 32 * j + 16 * h, w, 8);
             }
     }
 }
 
 // out of a tile's rows over `cols` columns (a multiple of 128).  Waves: 2 row halves x 2 halves of 128 columns.
-template <class T, int kRB>
+template <class T, int kRB, bool kWhole>
 __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p, int cols)
 {
-    constexpr int PB = Raw8<T>::kPlanes, PV = PB == 1 ? 2 : 3;
+    constexpr int PB = kPlanesOf<T>, PV = PB == 1 ? 2 : 3;
     constexpr int kR = 32 * kRB, kRow = 2 * 128 + 16, kPlane = kR * kRow, kLoads = kR * 16 / kThreads;
+    constexpr int kVRow = 2 * kR + 16, kVPlane = kTile * kVRow;        // v's planes, after B's
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     if (static_cast<int>(blockIdx.x) >= p.count[0])
         return;
@@ -381,8 +427,8 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p, in
                 const int64_t at = static_cast<int64_t>(p.perm[tile.begin + r]) * g.N;
                 for (int c = n0 + 8 * lane; c < n1; c += 512) {
                     float w[8];
-                    load8(w, static_cast<const T*>(g.base) + at + c, n1 - c, g.vec_n);
-                    store8(static_cast<T*>(g.out) + at + c, w, n1 - c, g.vec_n);
+                    load8(w, static_cast<const T*>(g.base) + at + c, n1 - c);
+                    store8(static_cast<T*>(g.out) + at + c, w, n1 - c);
                 }
             }
         return;
@@ -400,44 +446,47 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p, in
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int r = (tid + i * kThreads) / 16, c = c0 + 8 * (tid % 16);
-            br[i] = load_raw(B + static_cast<int64_t>(r) * g.N + c, r < rank ? n1 - c : 0, g.vec_n);
+            br[i] = load_raw<kWhole>(B + static_cast<int64_t>(r) * g.N + c, r < rank ? n1 - c : 0);
         }
         if (busy)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const int c = c0 + 64 * wc + 16 * q + 8 * (lane >> 5);
-                base[q] = load_raw(static_cast<const T*>(g.base) + row + c, real ? n1 - c : 0, g.vec_n);
+                base[q] = load_raw<kWhole>(static_cast<const T*>(g.base) + row + c, real ? n1 - c : 0);
             }
     };
     fetch(n0);
-    // v of this lane's row, 8 of every 16 columns, as planes
-    bf16x8_t v[2 * kRB][PV];
+    // v of the tile's rows as planes, each thread 8 columns of a row at a time
 #pragma unroll
-    for (int s = 0; s < 2 * kRB; ++s) {
+    for (int i = 0; i < kTile * kR / 8 / kThreads; ++i) {
+        const int r = (tid + i * kThreads) / (kR / 8), c = 8 * ((tid + i * kThreads) % (kR / 8));
+        const float* const v = p.v + (static_cast<int64_t>(tile.begin) + min(r, n - 1)) * kR + c;
         float sum[8] = {};
+#pragma unroll 4
         for (int q = 0; q < p.splits; ++q) {
             float w[8];
-            load8(w, p.v + (static_cast<int64_t>(q) * g.T + tile.begin + safe) * kR + 16 * s + 8 * (lane >> 5), 8, true);
+            load8(w, v + static_cast<int64_t>(q) * g.T * kR, 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                sum[i] += w[i];
+            for (int e = 0; e < 8; ++e)
+                sum[e] += w[e];
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (16 * s + 8 * (lane >> 5) + i >= rank)
-                sum[i] = 0.0f;
+        for (int e = 0; e < 8; ++e)
+            if (c + e >= rank)
+                sum[e] = 0.0f;
         u32x4_t pl[PV];
         split8<PV>(sum, pl);
 #pragma unroll
         for (int q = 0; q < PV; ++q)
-            v[s][q] = __builtin_bit_cast(bf16x8_t, pl[q]);
+            *reinterpret_cast<u32x4_t*>(smem + PB * kPlane + q * kVPlane + r * kVRow + 2 * c) = pl[q];
     }
+    const unsigned char* const mine_v = smem + PB * kPlane + (32 * wr + (lane & 31)) * kVRow + 16 * (lane >> 5);
     for (int c0 = n0; c0 < n1; c0 += 128) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             u32x4_t pl[PB];
-            br[i].planes(pl);
+            planes8(br[i], pl);
 #pragma unroll
             for (int q = 0; q < PB; ++q)
                 *reinterpret_cast<u32x4_t*>(smem + q * kPlane + ((tid + i * kThreads) / 16) * kRow + 16 * (tid % 16)) = pl[q];
@@ -459,11 +508,14 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p, in
                 acc[e] = 0.0f;
 #pragma unroll
             for (int s = 0; s < 2 * kRB; ++s) {
-                bf16x8_t w[PB];
+                bf16x8_t w[PB], v[PV];
+#pragma unroll
+                for (int q = 0; q < PV; ++q)
+                    v[q] = *reinterpret_cast<const bf16x8_t*>(mine_v + q * kVPlane + 32 * s);
 #pragma unroll
                 for (int q = 0; q < PB; ++q)
                     w[q] = read_tr(lds + q * kPlane + 16 * s * kRow + 2 * (64 * wc + 32 * j) + tr_offset(lane, kRow), kRow);
-                acc = mfma_planes<PV, PB>(w, v[s], acc);
+                acc = mfma_planes<PV, PB>(w, v, acc);
             }
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -475,7 +527,7 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p, in
                     w[i] += u[i];
                 const int c = c0 + 64 * wc + 32 * j + 16 * h + 8 * (lane >> 5);
                 if (real && c < n1)
-                    store8(static_cast<T*>(g.out) + row + c, w, n1 - c, g.vec_n);
+                    store8(static_cast<T*>(g.out) + row + c, w, n1 - c);
             }
         }
     }
@@ -508,24 +560,26 @@ Plan plan(const moe_adapter& p)
     q.max_tiles = ceil_div(p.T, kTile) + std::min(p.T, p.L + 1);
     const int64_t tiles = ceil_div(p.T, kTile);
     q.splits = static_cast<int>(std::clamp<int64_t>(ceil_div(512, tiles), 1, std::clamp<int64_t>(q.steps / 4, 1, 16)));
-    const int64_t per_tile = std::clamp<int64_t>(ceil_div(1024, tiles), 1, ceil_div(p.N, 128));
+    const int64_t per_tile = std::clamp<int64_t>(ceil_div(640, tiles), 1, ceil_div(p.N, 128));
     q.cols = static_cast<int>(ceil_div(ceil_div(p.N, per_tile), 128) * 128);
     return q;
 }
 
-template <class T, int kRB>
+bool whole(const moe_adapter& p) { return p.K % 8 == 0 && p.N % 8 == 0 && p.R % 8 == 0; }
+
+template <class T, int kRB, bool kWhole>
 hipError_t launch_tiles(const Args& g, const TileArgs& t, const Plan& q, hipStream_t s)
 {
-    constexpr int kExpandLds = Raw8<T>::kPlanes * 32 * kRB * (2 * 128 + 16);
-    if (kExpandLds > 65536)
-        if (hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&expand_kernel<T, kRB>),
-                                               hipFuncAttributeMaxDynamicSharedMemorySize, kExpandLds); e != hipSuccess)
-            return e;
+    constexpr int kPB = kPlanesOf<T>, kPV = kPB == 1 ? 2 : 3;
+    constexpr int kExpandLds = kPB * 32 * kRB * (2 * 128 + 16) + kPV * kTile * (64 * kRB + 16);
+    static LdsLimit limit;
+    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&expand_kernel<T, kRB, kWhole>), kExpandLds); e != hipSuccess)
+        return e;
     const unsigned tiles = static_cast<unsigned>(q.max_tiles);
-    shrink_kernel<T, kRB><<<dim3(tiles, q.splits), kThreads, 0, s>>>(g, t);
+    shrink_kernel<T, kRB, kWhole><<<dim3(tiles, q.splits), kThreads, 0, s>>>(g, t);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
-    expand_kernel<T, kRB><<<dim3(tiles, static_cast<unsigned>(ceil_div(g.N, q.cols))), kThreads, kExpandLds, s>>>(g, t, q.cols);
+    expand_kernel<T, kRB, kWhole><<<dim3(tiles, static_cast<unsigned>(ceil_div(g.N, q.cols))), kThreads, kExpandLds, s>>>(g, t, q.cols);
     return hipGetLastError();
 }
 
@@ -534,7 +588,11 @@ hipError_t launch(const moe_adapter& p, const Args& g, unsigned char* ws, hipStr
 {
     const Plan q = plan(p);
     if (q.rows) {
-        row_kernel<T><<<dim3(static_cast<unsigned>(p.T), static_cast<unsigned>(ceil_div(p.N, q.cols))), kThreads, 0, s>>>(g, q.cols);
+        const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>(ceil_div(p.N, q.cols)));
+        if (whole(p))
+            row_kernel<T, true><<<grid, kRowThreads, 0, s>>>(g, q.cols);
+        else
+            row_kernel<T, false><<<grid, kRowThreads, 0, s>>>(g, q.cols);
         return hipGetLastError();
     }
     const AdapterLayout L = adapter_layout(p);
@@ -545,8 +603,13 @@ hipError_t launch(const moe_adapter& p, const Args& g, unsigned char* ws, hipStr
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     const TileArgs t{tiles, count, perm, reinterpret_cast<float*>(ws + L.v), q.splits, q.steps};
-    return q.blocks == 1 ? launch_tiles<T, 1>(g, t, q, s) : q.blocks == 2 ? launch_tiles<T, 2>(g, t, q, s)
-                                                                         : launch_tiles<T, 4>(g, t, q, s);
+    // rows of whole runs of eight values need no code for a run that ends early
+    const auto by_blocks = [&](auto whole) {
+        constexpr bool kWhole = decltype(whole)::value;
+        return q.blocks == 1 ? launch_tiles<T, 1, kWhole>(g, t, q, s) : q.blocks == 2 ? launch_tiles<T, 2, kWhole>(g, t, q, s)
+                                                                                     : launch_tiles<T, 4, kWhole>(g, t, q, s);
+    };
+    return whole(p) ? by_blocks(std::true_type{}) : by_blocks(std::false_type{});
 }
 
 }  // namespace
@@ -574,13 +637,8 @@ hipError_t launch_adapter(const moe_adapter& p, const void* base, const void* x,
                           const int32_t* ids, const float* scale, const int32_t* ranks, void* out, void* workspace,
                           hipStream_t s)
 {
-    const auto aligned = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; };
-    const int64_t size = p.dtype == MOE_F32 ? 4 : 2;
-    Args g{base, x, a, b, out, ids, ranks, scale, static_cast<int>(p.T), static_cast<int>(p.K), static_cast<int>(p.N),
-           static_cast<int>(p.L), static_cast<int>(p.R), false, false, false};
-    g.vec_k = p.K * size % 16 == 0 && aligned(x);
-    g.vec_r = p.R * size % 16 == 0 && aligned(a);
-    g.vec_n = p.N * size % 16 == 0 && aligned(b) && aligned(base) && aligned(out);
+    const Args g{base, x, a, b, out, ids, ranks, scale, static_cast<int>(p.T), static_cast<int>(p.K), static_cast<int>(p.N),
+                 static_cast<int>(p.L), static_cast<int>(p.R)};
     unsigned char* const ws = static_cast<unsigned char*>(workspace);
     return p.dtype == MOE_F32 ? launch<float>(p, g, ws, s) : launch<uint16_t>(p, g, ws, s);
 }

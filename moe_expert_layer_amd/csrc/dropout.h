@@ -8,11 +8,10 @@
 // as long as moving 4 bfloat16 values in and out of memory at 5.7 TB/s.
 #pragma once
 
-#include <math.h>
 #include <stdint.h>
 
-#include "common.h"
 #include "shared_expert.h"
+#include "vec8.h"
 
 namespace moe {
 
@@ -55,70 +54,6 @@ __device__ __forceinline__ void drop8(float (&v)[8], const Dropout& d, const Dro
     for (int i = 0; i < 8; ++i) {
         const uint32_t b = i % 2 == 0 ? bits[i / 2] & 0xFFFFu : bits[i / 2] >> 16;
         v[i] = b >= d.threshold ? v[i] * d.scale : 0.0f;
-    }
-}
-
-// Eight adjacent values of float32 or bfloat16 memory, of which the first n exist (the others read as zero and are
-// not written).  vec: the eight lie within the row and are aligned to 16 bytes.
-template <class T>
-__device__ __forceinline__ void load8(float (&v)[8], const T* p, int n, bool vec)
-{
-    if constexpr (sizeof(T) == 2) {
-        if (vec && n >= 8) {
-            const u32x4_t w = *reinterpret_cast<const u32x4_t*>(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[2 * i] = __uint_as_float(w[i] << 16);
-                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = i < n ? bf16_to_f32(p[i]) : 0.0f;
-    } else {
-        if (vec && n >= 8) {
-            const f32x4_t a = reinterpret_cast<const f32x4_t*>(p)[0], b = reinterpret_cast<const f32x4_t*>(p)[1];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = i < n ? p[i] : 0.0f;
-    }
-}
-
-__device__ __forceinline__ u32x4_t pack8_bf16(const float (&v)[8])
-{
-    return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-}
-
-template <class T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8], int n, bool vec)
-{
-    if constexpr (sizeof(T) == 2) {
-        if (vec && n >= 8) {
-            *reinterpret_cast<u32x4_t*>(p) = pack8_bf16(v);
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                p[i] = f32_to_bf16(v[i]);
-    } else {
-        if (vec && n >= 8) {
-            reinterpret_cast<f32x4_t*>(p)[0] = f32x4_t{v[0], v[1], v[2], v[3]};
-            reinterpret_cast<f32x4_t*>(p)[1] = f32x4_t{v[4], v[5], v[6], v[7]};
-            return;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < n)
-                p[i] = v[i];
     }
 }
 

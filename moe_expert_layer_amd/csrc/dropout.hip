@@ -13,10 +13,10 @@ constexpr int kPer = 4;            // groups of 8 columns per thread, loaded tog
 // n groups of 8 columns (below 2^31), rows of `groups` of them; the first row is row0 of the call.
 template <class T, bool kResidual>
 __global__ __launch_bounds__(kThreads) void dropout_kernel(const T* x, const T* residual, T* out, int n, Divisor groups,
-                                                           int cols, int64_t row0, bool vec, Dropout d)
+                                                           int cols, int64_t row0, Dropout d)
 {
     const DropKey key = drop_key(d);
-    float v[kPer][8], r[kPer][8];
+    Raw8<T> v[kPer], r[kPer];
     int row[kPer], group[kPer];
     const int first = blockIdx.x * (kThreads * kPer) + threadIdx.x;
 #pragma unroll
@@ -28,22 +28,25 @@ __global__ __launch_bounds__(kThreads) void dropout_kernel(const T* x, const T* 
             group[i] = -1;
         if (group[i] >= 0) {
             const int64_t p = (row0 + row[i]) * cols + 8 * group[i];
-            load8(v[i], x + p, cols - 8 * group[i], vec);
+            v[i] = load_raw<false>(x + p, cols - 8 * group[i]);
             if constexpr (kResidual)
-                load8(r[i], residual + p, cols - 8 * group[i], vec);
+                r[i] = load_raw<false>(residual + p, cols - 8 * group[i]);
         }
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (group[i] < 0)
             continue;
-        drop8(v[i], d, key, static_cast<uint32_t>(group[i]), static_cast<uint32_t>(row0 + row[i]));
+        float y[8], w[8];
+        v[i].values(y);
+        drop8(y, d, key, static_cast<uint32_t>(group[i]), static_cast<uint32_t>(row0 + row[i]));
         if constexpr (kResidual) {
+            r[i].values(w);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                v[i][e] += r[i][e];
+                y[e] += w[e];
         }
-        store8(out + (row0 + row[i]) * cols + 8 * group[i], v[i], cols - 8 * group[i], vec);
+        store8(out + (row0 + row[i]) * cols + 8 * group[i], y, cols - 8 * group[i]);
     }
 }
 
@@ -51,8 +54,6 @@ template <class T>
 hipError_t launch(const void* x, const void* residual, int64_t rows, int64_t cols, const Dropout& d, void* out,
                   hipStream_t s)
 {
-    const auto aligned = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; };
-    const bool vec = cols * sizeof(T) % 16 == 0 && aligned(x) && aligned(out) && (residual == nullptr || aligned(residual));
     const int64_t groups = ceil_div(cols, 8);
     const Divisor div = divisor(static_cast<int>(groups));
     // the group numbers of one launch stay below 2^31 - 1024, whatever the workgroup
@@ -62,10 +63,10 @@ hipError_t launch(const void* x, const void* residual, int64_t rows, int64_t col
         const dim3 grid(static_cast<unsigned>(ceil_div(n, kThreads * kPer)));
         if (residual != nullptr)
             dropout_kernel<T, true><<<grid, kThreads, 0, s>>>(static_cast<const T*>(x), static_cast<const T*>(residual),
-                                                              static_cast<T*>(out), n, div, static_cast<int>(cols), r, vec, d);
+                                                              static_cast<T*>(out), n, div, static_cast<int>(cols), r, d);
         else
             dropout_kernel<T, false><<<grid, kThreads, 0, s>>>(static_cast<const T*>(x), nullptr, static_cast<T*>(out), n,
-                                                               div, static_cast<int>(cols), r, vec, d);
+                                                               div, static_cast<int>(cols), r, d);
         if (hipError_t e = hipGetLastError(); e != hipSuccess)
             return e;
     }

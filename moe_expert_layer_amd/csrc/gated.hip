@@ -58,10 +58,9 @@ struct GemmArgs {
     // epilogue
     void *o0, *o1;                              // outputs of matrix 0 and 1 (kEpiOut), h (kEpiGated)
     int ldo;
-    int vec;                                    // outputs can be written 16 bytes at a time
     void *save_g, *save_u;                      // g and u, laid out as h (or null)
     const void* dh;                             // kEpiGatedBwd: [M, ld_dh], of which n_dh columns exist
-    int ld_dh, vec_dh;
+    int ld_dh;
     uint16_t* dgu;                              // planes of dg, then of du, [M, ldb] each
     int64_t dgu_plane;
     int act;
@@ -420,8 +419,8 @@ __device__ __forceinline__ void finish_gated(const GemmArgs& e, const DropKey& k
     const int n = e.N - col;
     const int64_t at = row * e.ldo + col;
     if (e.save_g != nullptr) {
-        store8(static_cast<T*>(e.save_g) + at, g, n, e.vec);
-        store8(static_cast<T*>(e.save_u) + at, u, n, e.vec);
+        store8(static_cast<T*>(e.save_g) + at, g, n);
+        store8(static_cast<T*>(e.save_u) + at, u, n);
     }
     float h[8], slope;
 #pragma unroll
@@ -431,7 +430,7 @@ __device__ __forceinline__ void finish_gated(const GemmArgs& e, const DropKey& k
     }
     if (e.drop.threshold != 0)
         drop8(h, e.drop, key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row));
-    store8(static_cast<T*>(e.o0) + at, h, n, e.vec);
+    store8(static_cast<T*>(e.o0) + at, h, n);
 }
 
 // dg and du of eight columns; columns from N on (up to ldb) are written as zero, they pad the products' K.
@@ -442,7 +441,7 @@ __device__ __forceinline__ void finish_gated_bwd(const GemmArgs& e, const DropKe
     using T = Value<kF32>;
     const int n = e.N - col;
     float d[8];
-    load8(d, static_cast<const T*>(e.dh) + row * e.ld_dh + col, n, e.vec_dh);
+    load8(d, static_cast<const T*>(e.dh) + row * e.ld_dh + col, n);
     if (e.drop.threshold != 0)
         drop8(d, e.drop, key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row));
 #pragma unroll
@@ -513,7 +512,7 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
                 else if constexpr (kEpi == kEpiGatedBwd)
                     finish_gated_bwd<kF32>(g, key, v, w, row, col);
                 else
-                    store8(static_cast<Value<kF32>*>(mat ? g.o1 : g.o0) + row * g.ldo + col, v, g.N - col, g.vec);
+                    store8(static_cast<Value<kF32>*>(mat ? g.o1 : g.o0) + row * g.ldo + col, v, g.N - col);
             }
         }
     }
@@ -531,16 +530,15 @@ __global__ __launch_bounds__(256) void act_grad_kernel(GemmArgs e, Divisor group
     const int col = 8 * (at - r * groups.d);
     const int64_t row = row0 + r;
     float g[8], u[8];
-    load8(g, static_cast<const T*>(e.save_g) + row * e.ldo + col, e.N - col, e.vec);
-    load8(u, static_cast<const T*>(e.save_u) + row * e.ldo + col, e.N - col, e.vec);
+    load8(g, static_cast<const T*>(e.save_g) + row * e.ldo + col, e.N - col);
+    load8(u, static_cast<const T*>(e.save_u) + row * e.ldo + col, e.N - col);
     finish_gated_bwd<kF32>(e, drop_key(e.drop), g, u, row, col);
 }
 
 // A matrix [rows, cols] of any alignment as planes [rows, ld] of bfloat16, the columns from cols on zero.
 template <bool kF32>
 __global__ __launch_bounds__(256) void pack_kernel(const Value<kF32>* __restrict__ src, uint16_t* __restrict__ dst,
-                                                   int64_t plane, Divisor groups, int n, int64_t row0, int cols, int ld,
-                                                   bool vec)
+                                                   int64_t plane, Divisor groups, int n, int64_t row0, int cols, int ld)
 {
     const int at = blockIdx.x * 256 + threadIdx.x;
     if (at >= n)
@@ -549,7 +547,7 @@ __global__ __launch_bounds__(256) void pack_kernel(const Value<kF32>* __restrict
     const int col = 8 * (at - r * groups.d);
     const int64_t row = row0 + r;
     float v[8];
-    load8(v, src + row * cols + col, cols - col, vec);
+    load8(v, src + row * cols + col, cols - col);
     store_planes<kF32>(dst + row * ld + col, plane, v);
 }
 
@@ -566,8 +564,6 @@ hipError_t for_groups(int64_t rows, int64_t groups, F launch)
     }
     return hipSuccess;
 }
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // A matrix as the products take it: planes of bfloat16, rows of ld values.
 struct Planes {
@@ -589,15 +585,14 @@ hipError_t prepare(int dtype, const void* src, int64_t rows, int64_t cols, void*
         return hipSuccess;
     uint16_t* const dst = static_cast<uint16_t*>(room);
     out = Planes{dst, rows * ld, static_cast<int>(ld)};
-    const bool vec = cols * (dtype == MOE_F32 ? 4 : 2) % 16 == 0 && aligned16(src);
     const Divisor div = divisor(static_cast<int>(ld / 8));
     return for_groups(rows, ld / 8, [&](int64_t r, int n, dim3 grid) {
         if (dtype == MOE_F32)
             pack_kernel<true><<<grid, 256, 0, s>>>(static_cast<const float*>(src), dst, rows * ld, div, n, r,
-                                                   static_cast<int>(cols), static_cast<int>(ld), vec);
+                                                   static_cast<int>(cols), static_cast<int>(ld));
         else
             pack_kernel<false><<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(src), dst, rows * ld, div, n, r,
-                                                    static_cast<int>(cols), static_cast<int>(ld), vec);
+                                                    static_cast<int>(cols), static_cast<int>(ld));
     });
 }
 
@@ -715,7 +710,6 @@ hipError_t launch_gated(const moe_gated& q, const Dropout& d, const void* x, con
     g.ldo = static_cast<int>(q.F);
     g.save_g = saved_gu;
     g.save_u = saved_gu == nullptr ? nullptr : static_cast<unsigned char*>(saved_gu) + q.T * q.F * size;
-    g.vec = q.F * size % 16 == 0 && aligned16(h) && aligned16(saved_gu);
     return launch_gemm<kKC, kNC, kEpiGated>(g, q.dtype, s);
 }
 
@@ -737,7 +731,6 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
         g.ldb = static_cast<int>(ldf);
         g.dh = dh;
         g.ld_dh = static_cast<int>(q.F);
-        g.vec_dh = q.F * size % 16 == 0 && aligned16(dh);
         g.dgu = dgu;
         g.dgu_plane = dgu_plane;
         if (saved_gu == nullptr) {
@@ -747,7 +740,6 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
             g.save_g = const_cast<void*>(saved_gu);
             g.save_u = const_cast<unsigned char*>(static_cast<const unsigned char*>(saved_gu)) + q.T * q.F * size;
             g.ldo = static_cast<int>(q.F);
-            g.vec = q.F * size % 16 == 0 && aligned16(saved_gu);
             const Divisor div = divisor(static_cast<int>(ldf / 8));
             const hipError_t e = for_groups(q.T, ldf / 8, [&](int64_t r, int n, dim3 grid) {
                 if (q.dtype == MOE_F32)
@@ -773,7 +765,6 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
         c.mats = 1;
         c.o0 = dx;
         c.ldo = static_cast<int>(q.H);
-        c.vec = q.H * size % 16 == 0 && aligned16(dx);
         if (hipError_t e = launch_gemm<kKC, kKC, kEpiOut>(c, q.dtype, s); e != hipSuccess)
             return e;
     }
@@ -795,7 +786,6 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
     w.o0 = dwg;
     w.o1 = dwu;
     w.ldo = static_cast<int>(q.F);
-    w.vec = q.F * size % 16 == 0 && aligned16(dwg) && aligned16(dwu);
     return launch_gemm<kNC, kNC, kEpiOut>(w, q.dtype, s);
 }
 

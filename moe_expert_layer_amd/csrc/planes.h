@@ -1,5 +1,4 @@
-// Float32 operands on the bfloat16 matrix cores: a value as the sum of bfloat16 planes, and eight adjacent values of
-// memory as a lane loads them and turns them into the planes of an MFMA operand.
+// Float32 operands on the bfloat16 matrix cores: a value as the sum of bfloat16 planes.
 //
 // Three planes hold a float32 value exactly (x = x0 + x1 + x2, each the nearest to what is left, so |x1| <= 2^-8 |x| and
 // |x2| <= 2^-16 |x|).  Six of the nine products of two values' planes make their product; the three left out are together
@@ -7,7 +6,7 @@
 // float32 MFMA.
 #pragma once
 
-#include "common.h"
+#include "vec8.h"
 
 namespace moe {
 
@@ -45,74 +44,15 @@ __device__ __forceinline__ void split8(const float (&v)[8], u32x4_t (&out)[P])
                          s[4][q] | static_cast<uint32_t>(s[5][q]) << 16, s[6][q] | static_cast<uint32_t>(s[7][q]) << 16};
 }
 
-// Eight adjacent values as loaded: bfloat16 in one 16-byte register group, float32 in two.
+// The planes of an MFMA operand: bfloat16 values are one, float32 values three.
 template <class T>
-struct Raw8;
-template <>
-struct Raw8<uint16_t> {
-    u32x4_t w;
-    static constexpr int kPlanes = 1;
-    __device__ __forceinline__ void values(float (&v)[8]) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    }
-    __device__ __forceinline__ void planes(u32x4_t (&p)[1]) const { p[0] = w; }
-};
-template <>
-struct Raw8<float> {
-    f32x4_t a, b;
-    static constexpr int kPlanes = 3;
-    __device__ __forceinline__ void values(float (&v)[8]) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    }
-    __device__ __forceinline__ void planes(u32x4_t (&p)[3]) const
-    {
-        float v[8];
-        values(v);
-        split8<3>(v, p);
-    }
-};
-
-// The first n of eight values at p (the others zero and not read); vec: p is aligned to 16 bytes.
-__device__ __forceinline__ Raw8<uint16_t> load_raw(const uint16_t* p, int n, bool vec)
+constexpr int kPlanesOf = sizeof(T) == 2 ? 1 : 3;
+__device__ __forceinline__ void planes8(const Raw8<uint16_t>& r, u32x4_t (&p)[1]) { p[0] = r.w; }
+__device__ __forceinline__ void planes8(const Raw8<float>& r, u32x4_t (&p)[3])
 {
-    Raw8<uint16_t> r;
-    if (vec && n >= 8) {
-        r.w = *reinterpret_cast<const u32x4_t*>(p);
-        return r;
-    }
-    uint16_t e[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        e[i] = i < n ? p[i] : static_cast<uint16_t>(0);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        r.w[i] = e[2 * i] | static_cast<uint32_t>(e[2 * i + 1]) << 16;
-    return r;
-}
-__device__ __forceinline__ Raw8<float> load_raw(const float* p, int n, bool vec)
-{
-    Raw8<float> r;
-    if (vec && n >= 8) {
-        r.a = reinterpret_cast<const f32x4_t*>(p)[0];
-        r.b = reinterpret_cast<const f32x4_t*>(p)[1];
-        return r;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.a[i] = i < n ? p[i] : 0.0f;
-        r.b[i] = 4 + i < n ? p[4 + i] : 0.0f;
-    }
-    return r;
+    float v[8];
+    r.values(v);
+    split8<3>(v, p);
 }
 
 // Columns 16 p + 8 (lane / 32) .. + 7 of row lane % 32 of a transposed 32 x 32 accumulator block.  A lane holds columns 8 q

@@ -2,6 +2,8 @@
 // adapters; launchers shared by api.cpp and the kernels.
 #pragma once
 
+#include <atomic>
+
 #include "internal.h"
 #include "moe_expert_layer.h"
 
@@ -30,6 +32,25 @@ inline Divisor divisor(int d)
         ++l;
     return Divisor{(uint64_t{1} << (31 + l)) / static_cast<uint64_t>(d) + 1, 31 + l, d};
 }
+
+// Raises one kernel's limit of dynamic LDS to `bytes` (more than 64 KiB), once per device.
+struct LdsLimit {
+    std::atomic<bool> done[64];
+    hipError_t ensure(const void* kernel, int bytes)
+    {
+        int dev = 0;
+        if (bytes <= 65536)
+            return hipSuccess;
+        if (hipError_t e = hipGetDevice(&dev); e != hipSuccess)
+            return e;
+        if (dev < 64 && done[dev])
+            return hipSuccess;
+        const hipError_t e = hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == hipSuccess && dev < 64)
+            done[dev] = true;
+        return e;
+    }
+};
 
 // dropout.hip: out = [residual +] D(x), rows x cols values of MOE_F32 or MOE_BF16 (moe_dropout).
 hipError_t launch_dropout(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, const Dropout& d,
