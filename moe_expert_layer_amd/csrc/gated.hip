@@ -16,19 +16,12 @@
 #include <atomic>
 #include <utility>
 
-#include "dropout.h"
-#include "planes.h"
+#include "gated_epilogue.h"
 
 namespace moe {
 namespace {
 
 enum Layout { kKC = 0, kNC = 1 };
-enum Epi {
-    kEpiGated,       // h, and g and u where they are kept
-    kEpiGatedBwd,    // dg and du
-    kEpiOut          // the product itself
-};
-
 constexpr int kBK = 64;                         // K values per step: 128-byte rows of a kKC operand, whole cache lines
 constexpr uint32_t kOob = 0xC0000000u;          // a buffer offset past any num_records used here: reads as zero
 
@@ -53,18 +46,10 @@ struct GemmArgs {
     uint64_t a_idx, b_idx;
     int nseg, kt;                               // segments, steps of kBK per segment
     int lda, ldb;                               // values between rows, multiples of 8
-    int M, N, K;                                // rows, columns (of one matrix), the rows of a kNC operand
+    int M, N;                                   // rows, columns (of one matrix)
+    int K, kc;                                  // the rows of a kNC operand, the values of a kKC operand's row (K, padded)
     int mt, nt, mats;                           // row tiles, column tiles (of one matrix), matrices of columns
-    // epilogue
-    void *o0, *o1;                              // outputs of matrix 0 and 1 (kEpiOut), h (kEpiGated)
-    int ldo;
-    void *save_g, *save_u;                      // g and u, laid out as h (or null)
-    const void* dh;                             // kEpiGatedBwd: [M, ld_dh], of which n_dh columns exist
-    int ld_dh;
-    uint16_t* dgu;                              // planes of dg, then of du, [M, ldb] each
-    int64_t dgu_plane;
-    int act;
-    Dropout drop;
+    EpiArgs e;
 };
 
 __device__ __forceinline__ void copy16(const i32x4_t& rsrc, uint32_t voff, uint32_t lds)
@@ -247,19 +232,19 @@ struct Gemm {
         __builtin_amdgcn_sched_barrier(0);
     }
 
-    // The next step to copy: segment and first k.
+    // The next step to copy: segment, first k, and the steps left.
     struct Feed {
-        int seg, kk;
+        int seg, kk, left;
     };
 
-    // Points the lane's buffer resources at step f (nothing is read past the last segment), returns the K values left.
+    // Points the lane's buffer resources at step f (nothing is read past the last step), returns the K values left.
     static __device__ __forceinline__ int aim(const GemmArgs& g, const Feed& f, Lane& ln, int m0, int n0, int mat)
     {
         const int seg = f.seg;
         const uint16_t* a = g.a + ((g.a_idx >> (4 * seg)) & 15) * g.a_plane;
         const int bi = static_cast<int>((g.b_idx >> (4 * seg)) & 15);
         const uint16_t* b = ((bi >> 3) ^ mat ? g.b1 : g.b0) + (bi & 7) * g.b_plane;
-        const bool on = seg < g.nseg;
+        const bool on = f.left > 0;
         // kKC: rows [m0, M) of lda values from kk on; kNC: rows [kk, K) from column m0 on
         const int64_t an = kLA == kKC ? min(S::BM, g.M - m0) : min(kBK, g.K - f.kk);
         const int64_t bn = kLB == kKC ? min(BN, g.N - n0) : min(kBK, g.K - f.kk);
@@ -267,11 +252,12 @@ struct Gemm {
         b += kLB == kKC ? static_cast<int64_t>(n0) * g.ldb + f.kk : static_cast<int64_t>(f.kk) * g.ldb + n0;
         ln.ra = make_rsrc(a, on && an > 0 ? 2 * (an * g.lda - (kLA == kKC ? f.kk : m0)) : 0);
         ln.rb = make_rsrc(b, on && bn > 0 ? 2 * (bn * g.ldb - (kLB == kKC ? f.kk : n0)) : 0);
-        return (kLA == kKC ? g.lda : g.ldb) - f.kk;
+        return g.kc - f.kk;
     }
 
     static __device__ __forceinline__ void advance(const GemmArgs& g, Feed& f)
     {
+        --f.left;
         f.kk += kBK;
         if (f.kk >= g.kt * kBK) {
             f.kk = 0;
@@ -279,9 +265,9 @@ struct Gemm {
         }
     }
 
-    // The sum of the tile's steps.
+    // The sum of the tile's steps [step0, step1).
     static __device__ __forceinline__ void k_loop(const GemmArgs& g, f32x16_t (&acc)[S::kTM][S::kTN], int m0, int n0,
-                                                  int mat0)
+                                                  int mat0, int step0, int step1)
     {
         extern __shared__ __attribute__((aligned(256))) unsigned char smem[];
         const uint32_t lds0 = static_cast<uint32_t>(
@@ -323,7 +309,7 @@ struct Gemm {
         constexpr int kC = S::kAC + S::kBC;
         using AllCopies = std::make_integer_sequence<int, kC>;
         using AllMfmas = std::make_integer_sequence<int, S::kTM * S::kTN>;
-        Feed f{0, 0};
+        Feed f{g.kt > 0 ? step0 / g.kt : 0, g.kt > 0 ? step0 % g.kt * kBK : 0, step1 - step0};
         int krem = aim(g, f, ln, m0, n0, mat);
         copies<0>(AllCopies{}, ln, krem);
         advance(g, f);
@@ -337,8 +323,7 @@ struct Gemm {
         Frags f0, f1;
         reads<0, 0>(std::make_integer_sequence<int, kReads>{}, f0, ln);
         int delta = S::kStage;
-        const int steps = g.nseg * g.kt;
-        for (int t = 0; t < steps; ++t) {
+        for (int t = step0; t < step1; ++t) {
             slots<1, false>(AllMfmas{}, acc, f0, f1, ln, 0);
             slots<2, false>(AllMfmas{}, acc, f1, f0, ln, 0);
             krem = aim(g, f, ln, m0, n0, mat);
@@ -361,114 +346,18 @@ struct Gemm {
     }
 };
 
-// act(g) and its slope.  silu and gelu's tanh form are g s(z) with the logistic function s: z = g, and
-// z = 2 sqrt(2 / pi) (g + 0.044715 g^3) since (1 + tanh y) / 2 = s(2 y).  bfloat16 results take exponential and quotient
-// from the hardware's 1-ulp units, float32 ones from the exact functions.
-template <bool kF32>
-__device__ __forceinline__ void activation(int act, float g, float& value, float& slope)
-{
-    if (act == MOE_ACT_GELU) {
-        const float c = 0.5f * erfcf(-0.70710678118654752f * g);
-        value = g * c;
-        const float e = kF32 ? expf(-0.5f * g * g) : __builtin_amdgcn_exp2f(-0.72134752044448170f * g * g);
-        slope = c + (e == 0.0f ? 0.0f : g * e * 0.39894228040143268f);
-        return;
-    }
-    constexpr float kA = 1.5957691216057308f, kB = 0.044715f;
-    const float z = act == MOE_ACT_SILU ? g : kA * (g + kB * g * g * g);
-    const float dz = act == MOE_ACT_SILU ? 1.0f : kA * (1.0f + 3.0f * kB * g * g);
-    float s, t;                                                // s(z) and 1 - s(z)
-    if constexpr (kF32) {
-        const float e = expf(-fabsf(z)), r = 1.0f / (1.0f + e);
-        s = z < 0.0f ? e * r : r;
-        t = z < 0.0f ? r : e * r;
-    } else {
-        const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
-        s = z < 0.0f ? e * r : r;
-        t = z < 0.0f ? r : e * r;
-    }
-    value = g * s;
-    const float st = s * t;
-    slope = s + (st == 0.0f ? 0.0f : g * st * dz);
-}
-
-// Eight values to the planes at p (one bfloat16 plane, rounded, or three); p aligned to 16 bytes.
-template <bool kF32>
-__device__ __forceinline__ void store_planes(uint16_t* p, int64_t plane, const float (&v)[8])
-{
-    if constexpr (kF32) {
-        u32x4_t q[3];
-        split8<3>(v, q);
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<u32x4_t*>(p + i * plane) = q[i];
-    } else {
-        *reinterpret_cast<u32x4_t*>(p) = pack8_bf16(v);
-    }
-}
-
-template <bool kF32>
-using Value = std::conditional_t<kF32, float, uint16_t>;
-
-// h of eight columns from col on in one row (col < F), and g and u where they are kept.
-template <bool kF32>
-__device__ __forceinline__ void finish_gated(const GemmArgs& e, const DropKey& key, float (&g)[8], const float (&u)[8],
-                                             int64_t row, int col)
-{
-    using T = Value<kF32>;
-    const int n = e.N - col;
-    const int64_t at = row * e.ldo + col;
-    if (e.save_g != nullptr) {
-        store8(static_cast<T*>(e.save_g) + at, g, n);
-        store8(static_cast<T*>(e.save_u) + at, u, n);
-    }
-    float h[8], slope;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        activation<kF32>(e.act, g[i], h[i], slope);
-        h[i] *= u[i];
-    }
-    if (e.drop.threshold != 0)
-        drop8(h, e.drop, key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row));
-    store8(static_cast<T*>(e.o0) + at, h, n);
-}
-
-// dg and du of eight columns; columns from N on (up to ldb) are written as zero, they pad the products' K.
-template <bool kF32>
-__device__ __forceinline__ void finish_gated_bwd(const GemmArgs& e, const DropKey& key, float (&g)[8], float (&u)[8],
-                                                 int64_t row, int col)
-{
-    using T = Value<kF32>;
-    const int n = e.N - col;
-    float d[8];
-    load8(d, static_cast<const T*>(e.dh) + row * e.ld_dh + col, n);
-    if (e.drop.threshold != 0)
-        drop8(d, e.drop, key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float value, slope;
-        activation<kF32>(e.act, g[i], value, slope);
-        // a dropped place has no gradient whatever its g and u
-        g[i] = d[i] == 0.0f || i >= n ? 0.0f : d[i] * u[i] * slope;
-        u[i] = d[i] == 0.0f || i >= n ? 0.0f : d[i] * value;
-    }
-    constexpr int kPlanes = kF32 ? 3 : 1;
-    uint16_t* const p = e.dgu + row * e.ldb + col;
-    store_planes<kF32>(p, e.dgu_plane, g);
-    store_planes<kF32>(p + kPlanes * e.dgu_plane, e.dgu_plane, u);
-}
-
 template <class S, int kLA, int kLB, int kEpi, bool kF32>
 __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
 {
     using G = Gemm<S, kLA, kLB, kEpi, kF32>;
     // consecutive tiles go to one XCD (workgroup b runs on XCD b % 8), in groups of 8 row tiles, so that the
     // workgroups of an XCD share rows of A and columns of B in its L2
-    const int cols = g.nt * g.mats, total = g.mt * cols;
+    const int cols = g.nt * g.mats, tiles = g.mt * cols, total = tiles * g.e.parts;
     const int per = (total + kXcdCount - 1) / kXcdCount;
-    const int t = static_cast<int>(blockIdx.x % kXcdCount) * per + static_cast<int>(blockIdx.x / kXcdCount);
-    if (static_cast<int>(blockIdx.x / kXcdCount) >= per || t >= total)
+    const int id = static_cast<int>(blockIdx.x % kXcdCount) * per + static_cast<int>(blockIdx.x / kXcdCount);
+    if (id >= total)
         return;
+    const int part = id / tiles, t = id - part * tiles;
     constexpr int kGroup = 8;
     const int band = t / (kGroup * cols), in_band = t - band * kGroup * cols;
     const int height = min(kGroup, g.mt - band * kGroup);
@@ -485,12 +374,14 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
 #pragma unroll
             for (int r = 0; r < 16; ++r)
                 acc[i][j][r] = 0.0f;
-    G::k_loop(g, acc, m0, n0, mat);
+    const int64_t steps = static_cast<int64_t>(g.nseg) * g.kt;
+    G::k_loop(g, acc, m0, n0, mat, static_cast<int>(steps * part / g.e.parts), static_cast<int>(steps * (part + 1) / g.e.parts));
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / S::kWN, wn = wave % S::kWN;
-    const DropKey key = drop_key(g.drop);
+    const EpiArgs& e = g.e;
+    const DropKey key = kEpi == kEpiOut ? DropKey{} : drop_key(e.drop);
 #pragma unroll
     for (int i = 0; i < S::kTM; ++i) {
         const int64_t row = m0 + 32 * (wm * S::kTM + i) + (lane & 31);
@@ -505,14 +396,15 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
                 run8(acc[i][j], p, v);
                 if constexpr (G::kDual)
                     run8(acc[i][j + 1], p, w);
-                if (row >= g.M || col >= (kEpi == kEpiGatedBwd ? g.ldb : g.N))
+                if (row >= g.M || col >= g.N)
                     continue;
-                if constexpr (kEpi == kEpiGated)
-                    finish_gated<kF32>(g, key, v, w, row, col);
-                else if constexpr (kEpi == kEpiGatedBwd)
-                    finish_gated_bwd<kF32>(g, key, v, w, row, col);
-                else
-                    store8(static_cast<Value<kF32>*>(mat ? g.o1 : g.o0) + row * g.ldo + col, v, g.N - col);
+                if (e.partial != nullptr) {
+                    store8(partial_at(e, part, mat, row, col), v, 8);
+                    if constexpr (G::kDual)
+                        store8(partial_at(e, part, 1, row, col), w, 8);
+                } else {
+                    finish8<kEpi, kF32>(e, key, v, w, mat, row, col);
+                }
             }
         }
     }
@@ -520,7 +412,7 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
 
 // dg and du from the kept g and u.
 template <bool kF32>
-__global__ __launch_bounds__(256) void act_grad_kernel(GemmArgs e, Divisor groups, int n, int64_t row0)
+__global__ __launch_bounds__(256) void act_grad_kernel(EpiArgs e, Divisor groups, int n, int64_t row0)
 {
     using T = Value<kF32>;
     const int at = blockIdx.x * 256 + threadIdx.x;
@@ -530,39 +422,36 @@ __global__ __launch_bounds__(256) void act_grad_kernel(GemmArgs e, Divisor group
     const int col = 8 * (at - r * groups.d);
     const int64_t row = row0 + r;
     float g[8], u[8];
-    load8(g, static_cast<const T*>(e.save_g) + row * e.ldo + col, e.N - col);
-    load8(u, static_cast<const T*>(e.save_u) + row * e.ldo + col, e.N - col);
+    load8(g, static_cast<const T*>(e.save_g) + row * e.N + col, e.N - col);
+    load8(u, static_cast<const T*>(e.save_u) + row * e.N + col, e.N - col);
     finish_gated_bwd<kF32>(e, drop_key(e.drop), g, u, row, col);
 }
 
-// A matrix [rows, cols] of any alignment as planes [rows, ld] of bfloat16, the columns from cols on zero.
+// Matrices [rows, cols] of any alignment as planes [rows, ld] of bfloat16, the columns from cols up to the next multiple of
+// 8 zero; up to three of them in one launch (blockIdx.y).
+struct PackArgs {
+    struct One {
+        const void* src;
+        uint16_t* dst;
+        int64_t plane;
+        Divisor groups;
+        int n, cols, ld;                          // groups of 8 columns in all, columns, values between rows of dst
+    } m[3];
+    int64_t row0;
+};
 template <bool kF32>
-__global__ __launch_bounds__(256) void pack_kernel(const Value<kF32>* __restrict__ src, uint16_t* __restrict__ dst,
-                                                   int64_t plane, Divisor groups, int n, int64_t row0, int cols, int ld)
+__global__ __launch_bounds__(256) void pack_kernel(PackArgs g)
 {
+    const PackArgs::One& m = blockIdx.y == 0 ? g.m[0] : blockIdx.y == 1 ? g.m[1] : g.m[2];
     const int at = blockIdx.x * 256 + threadIdx.x;
-    if (at >= n)
+    if (at >= m.n)
         return;
-    const int r = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(at)) * groups.m) >> groups.shift);
-    const int col = 8 * (at - r * groups.d);
-    const int64_t row = row0 + r;
+    const int r = static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(at)) * m.groups.m) >> m.groups.shift);
+    const int col = 8 * (at - r * m.groups.d);
+    const int64_t row = g.row0 + r;
     float v[8];
-    load8(v, src + row * cols + col, cols - col);
-    store_planes<kF32>(dst + row * ld + col, plane, v);
-}
-
-// Runs `launch(first row, groups of 8 columns, ...)` over rows of `groups` groups, below 2^31 groups a launch.
-template <class F>
-hipError_t for_groups(int64_t rows, int64_t groups, F launch)
-{
-    const int64_t step = ((int64_t{1} << 31) - 256) / groups;
-    for (int64_t r = 0; r < rows; r += step) {
-        const int n = static_cast<int>(std::min(step, rows - r) * groups);
-        launch(r, n, dim3(static_cast<unsigned>(ceil_div(n, 256))));
-        if (hipError_t e = hipGetLastError(); e != hipSuccess)
-            return e;
-    }
-    return hipSuccess;
+    load8(v, static_cast<const Value<kF32>*>(m.src) + row * m.cols + col, m.cols - col);
+    store_planes<kF32>(m.dst + row * m.ld + col, m.plane, v);
 }
 
 // A matrix as the products take it: planes of bfloat16, rows of ld values.
@@ -574,46 +463,136 @@ struct Planes {
 
 int planes_of(int dtype) { return dtype == MOE_F32 ? 3 : 1; }
 int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }
+// Values between rows of what is laid out here: whole cache lines (rows that start inside one cost the copies of K up to
+// a third: 512 x 1024 x 2056, two segments, 46 against 60 us).
+int64_t own_ld(int64_t cols) { return (cols + 63) / 64 * 64; }
 // Whether a matrix of that width has to be laid out anew.
 bool needs_pack(int dtype, int64_t cols) { return dtype == MOE_F32 || cols % 8 != 0; }
 
-hipError_t prepare(int dtype, const void* src, int64_t rows, int64_t cols, void* room, Planes& out, hipStream_t s)
+struct Source {
+    const void* src;
+    int64_t rows, cols;
+    void* room;
+};
+
+// Lays out up to three matrices where their widths need it.
+template <int kCount>
+hipError_t prepare(int dtype, const Source (&in)[kCount], Planes* (&out)[kCount], hipStream_t s)
 {
-    const int64_t ld = padded(cols);
-    out = Planes{static_cast<const uint16_t*>(src), 0, static_cast<int>(ld)};
-    if (!needs_pack(dtype, cols))
-        return hipSuccess;
-    uint16_t* const dst = static_cast<uint16_t*>(room);
-    out = Planes{dst, rows * ld, static_cast<int>(ld)};
-    const Divisor div = divisor(static_cast<int>(ld / 8));
-    return for_groups(rows, ld / 8, [&](int64_t r, int n, dim3 grid) {
+    int64_t first[3], most = 0, widest = 1;
+    PackArgs a{};
+    int count = 0;
+    for (int i = 0; i < kCount; ++i) {
+        const Source& q = in[i];
+        *out[i] = Planes{static_cast<const uint16_t*>(q.src), 0, static_cast<int>(q.cols)};
+        if (!needs_pack(dtype, q.cols))
+            continue;
+        const int64_t ld = own_ld(q.cols);
+        uint16_t* const dst = static_cast<uint16_t*>(q.room);
+        *out[i] = Planes{dst, q.rows * ld, static_cast<int>(ld)};
+        const int64_t groups = ceil_div(q.cols, 8);
+        a.m[count] = PackArgs::One{q.src, dst, q.rows * ld, divisor(static_cast<int>(groups)), 0, static_cast<int>(q.cols),
+                                   static_cast<int>(ld)};
+        first[count++] = q.rows;
+        most = std::max(most, q.rows);
+        widest = std::max(widest, groups);
+    }
+    const int64_t step = ((int64_t{1} << 31) - 256) / widest;              // rows per launch: fewer than 2^31 groups
+    for (int64_t r = 0; r < most; r += step) {
+        int64_t threads = 0;
+        a.row0 = r;
+        for (int i = 0; i < count; ++i) {
+            a.m[i].n = static_cast<int>(std::clamp<int64_t>(first[i] - r, 0, step) * a.m[i].groups.d);
+            threads = std::max<int64_t>(threads, a.m[i].n);
+        }
+        const dim3 grid(static_cast<unsigned>(ceil_div(threads, 256)), count);
         if (dtype == MOE_F32)
-            pack_kernel<true><<<grid, 256, 0, s>>>(static_cast<const float*>(src), dst, rows * ld, div, n, r,
-                                                   static_cast<int>(cols), static_cast<int>(ld));
+            pack_kernel<true><<<grid, 256, 0, s>>>(a);
         else
-            pack_kernel<false><<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(src), dst, rows * ld, div, n, r,
-                                                    static_cast<int>(cols), static_cast<int>(ld));
-    });
+            pack_kernel<false><<<grid, 256, 0, s>>>(a);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
+// Large tiles: 256 x 256, 8 waves of 64 x 128, one workgroup per CU.  Small ones: 128 x 128, 4 waves of 64 x 64, two.
+using Large = Shape<4, 2, 2, 4, 1>;
 using Small = Shape<2, 2, 2, 2, 2>;
+
+// How a product runs: its tiles, and into how many parts its steps are cut.
+struct GemmPlan {
+    bool large;
+    int parts;
+};
+
+// M rows, N staged columns in all (both matrices'), `steps` steps of K.  The times that decide, in us, are measured ones
+// (4096 x 4096 x 28672 and 512 x 1024 x 4096): a step of a large tile 1.75; of a small one 0.7, or 1.05 for two that
+// share a CU; a workgroup's start and end 8 and 6.  Parts cost a launch of 4 and two passes of float32 sums at 3.5 TB/s,
+// and give workgroups to CUs that had none: they are taken only below one small tile per CU.
+GemmPlan plan_gemm(int64_t M, int64_t N, int64_t steps)
+{
+    const int64_t large = ceil_div(M, Large::BM) * ceil_div(N, Large::BNB), small = ceil_div(M, Small::BM) * ceil_div(N, Small::BNB);
+    constexpr int64_t kCus = 256;
+    const auto small_time = [&](int64_t tiles, int64_t n) {
+        const int64_t rest = tiles % (2 * kCus);
+        const double rounds = 1.05 * static_cast<double>(tiles / (2 * kCus)) + (rest == 0 ? 0.0 : rest <= kCus ? 0.7 : 1.05);
+        return rounds * static_cast<double>(n) + 6.0 * static_cast<double>(ceil_div(tiles, 2 * kCus));
+    };
+    GemmPlan best{true, 1};
+    double time = static_cast<double>(ceil_div(large, kCus)) * (1.75 * static_cast<double>(steps) + 8.0);
+    for (int64_t p = 1; p <= 16 && (p == 1 || (small * p <= 2 * kCus && steps >= 3 * p)); ++p) {
+        const double t = small_time(small * p, ceil_div(steps, p)) +
+                         (p == 1 ? 0.0 : 4.0 + static_cast<double>(8 * p * M * N) / 3.5e6);
+        if (t < time) {
+            time = t;
+            best = GemmPlan{false, static_cast<int>(p)};
+        }
+    }
+    return best;
+}
 
 template <class S, int kLA, int kLB, int kEpi, bool kF32>
 hipError_t launch_shape(GemmArgs g, hipStream_t s)
 {
     using G = Gemm<S, kLA, kLB, kEpi, kF32>;
+    static LdsLimit limit;
+    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gemm<S, kLA, kLB, kEpi, kF32>), S::kSmem); e != hipSuccess)
+        return e;
     g.mt = static_cast<int>(ceil_div(g.M, S::BM));
-    g.nt = static_cast<int>(ceil_div(kEpi == kEpiGatedBwd ? g.ldb : g.N, G::BN));
-    const int64_t total = static_cast<int64_t>(g.mt) * g.nt * g.mats;
+    g.nt = static_cast<int>(ceil_div(g.N, G::BN));
+    const int64_t total = static_cast<int64_t>(g.mt) * g.nt * g.mats * g.e.parts;
     gemm<S, kLA, kLB, kEpi, kF32><<<dim3(static_cast<unsigned>(ceil_div(total, kXcdCount) * kXcdCount)), S::kThreads,
                                     S::kSmem, s>>>(g);
     return hipGetLastError();
 }
 
+// A product by its plan; parts of K leave their sums at `partial`, and a second launch makes the results of them.
 template <int kLA, int kLB, int kEpi>
-hipError_t launch_gemm(const GemmArgs& g, int dtype, hipStream_t s)
+hipError_t launch_gemm(GemmArgs g, int dtype, float* partial, hipStream_t s)
 {
-    return dtype == MOE_F32 ? launch_shape<Small, kLA, kLB, kEpi, true>(g, s) : launch_shape<Small, kLA, kLB, kEpi, false>(g, s);
+    constexpr bool kGated = kEpi != kEpiOut;
+    const int mats = kGated ? 2 : g.mats;
+    const GemmPlan plan = plan_gemm(g.M, static_cast<int64_t>(mats) * g.N, static_cast<int64_t>(g.nseg) * g.kt);
+    g.e.M = g.M;
+    g.e.N = g.N;
+    g.e.mats = mats;
+    g.e.parts = plan.parts;
+    g.e.partial = plan.parts > 1 ? partial : nullptr;
+    g.e.ld_part = static_cast<int>(padded(g.N));
+    hipError_t e;
+    if (dtype == MOE_F32)
+        e = plan.large ? launch_shape<Large, kLA, kLB, kEpi, true>(g, s) : launch_shape<Small, kLA, kLB, kEpi, true>(g, s);
+    else
+        e = plan.large ? launch_shape<Large, kLA, kLB, kEpi, false>(g, s) : launch_shape<Small, kLA, kLB, kEpi, false>(g, s);
+    return e != hipSuccess || plan.parts == 1 ? e : launch_gated_finish(static_cast<Epi>(kEpi), dtype, g.e, s);
+}
+
+// Bytes of the partial sums of such a product.
+int64_t partial_bytes(int64_t M, int64_t N, int mats, int64_t steps)
+{
+    const GemmPlan plan = plan_gemm(M, mats * N, steps);
+    return plan.parts > 1 ? int64_t{4} * plan.parts * mats * M * padded(N) : 0;
 }
 
 // The segments of a product of planes: one for bfloat16, six for float32, small products first.  a0, b0: added to the
@@ -643,56 +622,86 @@ void add_segments_pair(GemmArgs& g, int dtype, int a1)
 GatedLayout gated_layout(const moe_gated& g, bool backward)
 {
     GatedLayout L;
-    const int64_t P = planes_of(g.dtype);
+    const int64_t P = planes_of(g.dtype), products = g.dtype == MOE_F32 ? 6 : 1;
     size_t off = 0;
-    const auto take = [&](size_t& at, int64_t values) {
+    const auto take = [&](size_t& at, int64_t bytes) {
         at = off;
-        off = align_up(off + static_cast<size_t>(values) * 2);
+        off = align_up(off + static_cast<size_t>(bytes));
     };
-    if (needs_pack(g.dtype, g.H))
-        take(L.x, P * g.T * padded(g.H));
-    if (needs_pack(g.dtype, g.F)) {
-        take(L.wg, P * g.H * padded(g.F));
-        take(L.wu, P * g.H * padded(g.F));
+    const bool rows = g.T <= kMaxRows;                    // the forward product takes its operands as they are
+    if (needs_pack(g.dtype, g.H) && (backward || !rows))
+        take(L.x, 2 * P * g.T * own_ld(g.H));
+    if (needs_pack(g.dtype, g.F) && (backward || !rows)) {
+        take(L.wg, 2 * P * g.H * own_ld(g.F));
+        take(L.wu, 2 * P * g.H * own_ld(g.F));
     }
     if (backward)
-        take(L.dgu, 2 * P * g.T * padded(g.F));
+        take(L.dgu, 2 * 2 * P * g.T * own_ld(g.F));
+    int64_t partial = 0;                                  // of one product after the other
+    if (g.T > 0) {
+        const int64_t parts = rows ? gated_rows_parts(g.T, g.H, g.F) : 1;
+        partial = rows ? (parts > 1 ? 4 * 2 * parts * g.T * padded(g.F) : 0)
+                       : partial_bytes(g.T, g.F, 2, products * ceil_div(g.H, kBK));
+        if (backward) {
+            partial = std::max(partial, partial_bytes(g.T, g.H, 1, 2 * products * ceil_div(g.F, kBK)));
+            partial = std::max(partial, partial_bytes(g.H, g.F, 2, products * ceil_div(g.T, kBK)));
+        }
+    }
+    take(L.partial, partial);
     L.total = off;
     return L;
 }
 
 namespace {
 
+struct Prepared {
+    Planes x, wg, wu;
+};
+
 // x and both weights laid out for the products.
 hipError_t prepare_all(const moe_gated& q, const void* x, const void* wg, const void* wu, const GatedLayout& L,
-                       unsigned char* ws, Planes& px, Planes& pg, Planes& pu, hipStream_t s)
+                       unsigned char* ws, Prepared& p, hipStream_t s)
 {
-    if (hipError_t e = prepare(q.dtype, x, q.T, q.H, ws + L.x, px, s); e != hipSuccess)
-        return e;
-    if (hipError_t e = prepare(q.dtype, wg, q.H, q.F, ws + L.wg, pg, s); e != hipSuccess)
-        return e;
-    return prepare(q.dtype, wu, q.H, q.F, ws + L.wu, pu, s);
+    const Source in[3] = {{x, q.T, q.H, ws + L.x}, {wg, q.H, q.F, ws + L.wg}, {wu, q.H, q.F, ws + L.wu}};
+    Planes* out[3] = {&p.x, &p.wg, &p.wu};
+    return prepare(q.dtype, in, out, s);
 }
 
-GemmArgs forward_args(const moe_gated& q, const Dropout& d, const Planes& px, const Planes& pg, const Planes& pu)
+// g and u of all rows with epilogue kEpi (kEpiGated or kEpiGatedBwd); p is not read for few rows.
+template <int kEpi>
+hipError_t launch_gu(const moe_gated& q, const void* x, const void* wg, const void* wu, const Prepared& p, EpiArgs e,
+                     float* partial, hipStream_t s)
 {
+    e.M = static_cast<int>(q.T);
+    e.N = static_cast<int>(q.F);
+    e.mats = 2;
+    e.act = q.activation;
+    if (q.T <= kMaxRows) {
+        e.parts = gated_rows_parts(q.T, q.H, q.F);
+        e.partial = e.parts > 1 ? partial : nullptr;
+        e.ld_part = static_cast<int>(padded(q.F));
+        const RowsArgs r{x, wg, wu, static_cast<int>(q.H), e};
+        if (hipError_t err = launch_gated_rows(static_cast<Epi>(kEpi), q.dtype, r, s); err != hipSuccess || e.parts == 1)
+            return err;
+        return launch_gated_finish(static_cast<Epi>(kEpi), q.dtype, e, s);
+    }
     GemmArgs g{};
-    g.a = px.p;
-    g.b0 = pg.p;
-    g.b1 = pu.p;
-    g.a_plane = px.plane;
-    g.b_plane = pg.plane;
+    g.a = p.x.p;
+    g.b0 = p.wg.p;
+    g.b1 = p.wu.p;
+    g.a_plane = p.x.plane;
+    g.b_plane = p.wg.plane;
     add_segments(g, q.dtype, 0, 0);
     g.kt = static_cast<int>(ceil_div(q.H, kBK));
-    g.lda = px.ld;
-    g.ldb = pg.ld;
+    g.lda = p.x.ld;
+    g.ldb = p.wg.ld;
     g.M = static_cast<int>(q.T);
     g.N = static_cast<int>(q.F);
     g.K = static_cast<int>(q.H);
+    g.kc = static_cast<int>(padded(q.H));
     g.mats = 1;
-    g.act = q.activation;
-    g.drop = d;
-    return g;
+    g.e = e;
+    return launch_gemm<kKC, kNC, kEpi>(g, q.dtype, partial, s);
 }
 
 }  // namespace
@@ -701,16 +710,18 @@ hipError_t launch_gated(const moe_gated& q, const Dropout& d, const void* x, con
                         void* saved_gu, void* workspace, hipStream_t s)
 {
     const GatedLayout L = gated_layout(q, false);
-    Planes px, pg, pu;
-    if (hipError_t e = prepare_all(q, x, wg, wu, L, static_cast<unsigned char*>(workspace), px, pg, pu, s); e != hipSuccess)
-        return e;
+    unsigned char* const ws = static_cast<unsigned char*>(workspace);
+    Prepared p{};
+    if (q.T > kMaxRows)
+        if (hipError_t e = prepare_all(q, x, wg, wu, L, ws, p, s); e != hipSuccess)
+            return e;
     const int64_t size = q.dtype == MOE_F32 ? 4 : 2;
-    GemmArgs g = forward_args(q, d, px, pg, pu);
-    g.o0 = h;
-    g.ldo = static_cast<int>(q.F);
-    g.save_g = saved_gu;
-    g.save_u = saved_gu == nullptr ? nullptr : static_cast<unsigned char*>(saved_gu) + q.T * q.F * size;
-    return launch_gemm<kKC, kNC, kEpiGated>(g, q.dtype, s);
+    EpiArgs e{};
+    e.o0 = h;
+    e.save_g = saved_gu;
+    e.save_u = saved_gu == nullptr ? nullptr : static_cast<unsigned char*>(saved_gu) + q.T * q.F * size;
+    e.drop = d;
+    return launch_gu<kEpiGated>(q, x, wg, wu, p, e, reinterpret_cast<float*>(ws + L.partial), s);
 }
 
 hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const void* x, const void* wg, const void* wu,
@@ -719,74 +730,79 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
 {
     const GatedLayout L = gated_layout(q, true);
     unsigned char* const ws = static_cast<unsigned char*>(workspace);
-    Planes px, pg, pu;
-    if (hipError_t e = prepare_all(q, x, wg, wu, L, ws, px, pg, pu, s); e != hipSuccess)
-        return e;
-    const int64_t size = q.dtype == MOE_F32 ? 4 : 2, ldf = padded(q.F);
+    Prepared p{};
+    if (q.T > 0)                                          // without tokens x and the weights may be null
+        if (hipError_t e = prepare_all(q, x, wg, wu, L, ws, p, s); e != hipSuccess)
+            return e;
+    const int64_t size = q.dtype == MOE_F32 ? 4 : 2, ldf = own_ld(q.F);
+    float* const partial = reinterpret_cast<float*>(ws + L.partial);
     const int P = planes_of(q.dtype);
     uint16_t* const dgu = reinterpret_cast<uint16_t*>(ws + L.dgu);
     const int64_t dgu_plane = q.T * ldf;
     if (q.T > 0) {
-        GemmArgs g = forward_args(q, d, px, pg, pu);
-        g.ldb = static_cast<int>(ldf);
-        g.dh = dh;
-        g.ld_dh = static_cast<int>(q.F);
-        g.dgu = dgu;
-        g.dgu_plane = dgu_plane;
+        EpiArgs e{};
+        e.dh = dh;
+        e.dgu = dgu;
+        e.dgu_plane = dgu_plane;
+        e.ld_dgu = static_cast<int>(ldf);
+        e.drop = d;
         if (saved_gu == nullptr) {
-            if (hipError_t e = launch_gemm<kKC, kNC, kEpiGatedBwd>(g, q.dtype, s); e != hipSuccess)
-                return e;
+            if (hipError_t err = launch_gu<kEpiGatedBwd>(q, x, wg, wu, p, e, partial, s);
+                err != hipSuccess)
+                return err;
         } else {
-            g.save_g = const_cast<void*>(saved_gu);
-            g.save_u = const_cast<unsigned char*>(static_cast<const unsigned char*>(saved_gu)) + q.T * q.F * size;
-            g.ldo = static_cast<int>(q.F);
-            const Divisor div = divisor(static_cast<int>(ldf / 8));
-            const hipError_t e = for_groups(q.T, ldf / 8, [&](int64_t r, int n, dim3 grid) {
+            e.M = static_cast<int>(q.T);
+            e.N = static_cast<int>(q.F);
+            e.act = q.activation;
+            e.save_g = const_cast<void*>(saved_gu);
+            e.save_u = static_cast<unsigned char*>(e.save_g) + q.T * q.F * size;
+            const Divisor div = divisor(static_cast<int>(ceil_div(q.F, 8)));
+            const hipError_t err = for_groups(q.T, ceil_div(q.F, 8), [&](int64_t r, int n, unsigned grid) {
                 if (q.dtype == MOE_F32)
-                    act_grad_kernel<true><<<grid, 256, 0, s>>>(g, div, n, r);
+                    act_grad_kernel<true><<<grid, 256, 0, s>>>(e, div, n, r);
                 else
-                    act_grad_kernel<false><<<grid, 256, 0, s>>>(g, div, n, r);
+                    act_grad_kernel<false><<<grid, 256, 0, s>>>(e, div, n, r);
             });
-            if (e != hipSuccess)
-                return e;
+            if (err != hipSuccess)
+                return err;
         }
         // dx [T, H]: K = F, the gate part, then the up part
         GemmArgs c{};
         c.a = dgu;
         c.a_plane = dgu_plane;
-        c.b0 = pg.p;
-        c.b1 = pu.p;
-        c.b_plane = pg.plane;
+        c.b0 = p.wg.p;
+        c.b1 = p.wu.p;
+        c.b_plane = p.wg.plane;
         add_segments_pair(c, q.dtype, P);
-        c.kt = static_cast<int>(ceil_div(ldf, kBK));
-        c.lda = c.ldb = static_cast<int>(ldf);
+        c.kt = static_cast<int>(ceil_div(q.F, kBK));
+        c.kc = static_cast<int>(padded(q.F));
+        c.lda = static_cast<int>(ldf);
+        c.ldb = p.wg.ld;
         c.M = static_cast<int>(q.T);
         c.N = static_cast<int>(q.H);
         c.mats = 1;
-        c.o0 = dx;
-        c.ldo = static_cast<int>(q.H);
-        if (hipError_t e = launch_gemm<kKC, kKC, kEpiOut>(c, q.dtype, s); e != hipSuccess)
-            return e;
+        c.e.o0 = dx;
+        if (hipError_t err = launch_gemm<kKC, kKC, kEpiOut>(c, q.dtype, partial, s); err != hipSuccess)
+            return err;
     }
     // dWg and dWu [H, F]: K = T
     GemmArgs w{};
-    w.a = px.p;
-    w.a_plane = px.plane;
+    w.a = p.x.p;
+    w.a_plane = p.x.plane;
     w.b0 = dgu;
     w.b1 = dgu + P * dgu_plane;
     w.b_plane = dgu_plane;
     add_segments(w, q.dtype, 0, 0);
     w.kt = static_cast<int>(ceil_div(q.T, kBK));
-    w.lda = px.ld;
+    w.lda = p.x.ld;
     w.ldb = static_cast<int>(ldf);
     w.M = static_cast<int>(q.H);
     w.N = static_cast<int>(q.F);
     w.K = static_cast<int>(q.T);
     w.mats = 2;
-    w.o0 = dwg;
-    w.o1 = dwu;
-    w.ldo = static_cast<int>(q.F);
-    return launch_gemm<kNC, kNC, kEpiOut>(w, q.dtype, s);
+    w.e.o0 = dwg;
+    w.e.o1 = dwu;
+    return launch_gemm<kNC, kNC, kEpiOut>(w, q.dtype, partial, s);
 }
 
 }  // namespace moe

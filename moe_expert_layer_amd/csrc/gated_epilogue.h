@@ -1,0 +1,162 @@
+// What the gated block's kernels do with their sums: the activation and its slope, h, the gradients of g and u, and the
+// joining of sums that several workgroups took over parts of K.
+#pragma once
+
+#include <type_traits>
+
+#include "dropout.h"
+#include "planes.h"
+
+namespace moe {
+
+enum Epi {
+    kEpiGated,       // h, and g and u where they are kept
+    kEpiGatedBwd,    // dg and du
+    kEpiOut          // the product itself
+};
+
+struct EpiArgs {
+    int M, N;                                   // rows, columns (of one matrix)
+    void *o0, *o1;                              // outputs [M, N] of matrix 0 and 1 (kEpiOut), h (kEpiGated)
+    void *save_g, *save_u;                      // kEpiGated: g and u, laid out as h (or null)
+    const void* dh;                             // kEpiGatedBwd: [M, N]
+    uint16_t* dgu;                              // planes of dg, then of du, [M, ld_dgu] each
+    int64_t dgu_plane;
+    int ld_dgu;                                 // the columns from N up to the next multiple of 8 are zero
+    int act;
+    Dropout drop;
+    float* partial;                             // not null: sums of one part of K each, [part, matrix, M, ld_part]
+    int ld_part, parts, mats;                   // N rounded up to 8; parts of K; matrices (two in the gated ones)
+};
+
+// act(g) and its slope.  silu and gelu's tanh form are g s(z) with the logistic function s: z = g, and
+// z = 2 sqrt(2 / pi) (g + 0.044715 g^3) since (1 + tanh y) / 2 = s(2 y).  bfloat16 results take exponential and quotient
+// from the hardware's 1-ulp units, float32 ones from the exact functions.
+template <bool kF32>
+__device__ __forceinline__ void activation(int act, float g, float& value, float& slope)
+{
+    if (act == MOE_ACT_GELU) {
+        const float c = 0.5f * erfcf(-0.70710678118654752f * g);
+        value = g * c;
+        const float e = kF32 ? expf(-0.5f * g * g) : __builtin_amdgcn_exp2f(-0.72134752044448170f * g * g);
+        slope = c + (e == 0.0f ? 0.0f : g * e * 0.39894228040143268f);
+        return;
+    }
+    constexpr float kA = 1.5957691216057308f, kB = 0.044715f;
+    const float z = act == MOE_ACT_SILU ? g : kA * (g + kB * g * g * g);
+    const float dz = act == MOE_ACT_SILU ? 1.0f : kA * (1.0f + 3.0f * kB * g * g);
+    float s, t;                                                // s(z) and 1 - s(z)
+    if constexpr (kF32) {
+        const float e = expf(-fabsf(z)), r = 1.0f / (1.0f + e);
+        s = z < 0.0f ? e * r : r;
+        t = z < 0.0f ? r : e * r;
+    } else {
+        const float e = __builtin_amdgcn_exp2f(-1.4426950408889634f * fabsf(z)), r = __builtin_amdgcn_rcpf(1.0f + e);
+        s = z < 0.0f ? e * r : r;
+        t = z < 0.0f ? r : e * r;
+    }
+    value = g * s;
+    const float st = s * t;
+    slope = s + (st == 0.0f ? 0.0f : g * st * dz);
+}
+
+// Eight values to the planes at p (one bfloat16 plane, rounded, or three); p aligned to 16 bytes.
+template <bool kF32>
+__device__ __forceinline__ void store_planes(uint16_t* p, int64_t plane, const float (&v)[8])
+{
+    if constexpr (kF32) {
+        u32x4_t q[3];
+        split8<3>(v, q);
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<u32x4_t*>(p + i * plane) = q[i];
+    } else {
+        *reinterpret_cast<u32x4_t*>(p) = pack8_bf16(v);
+    }
+}
+
+template <bool kF32>
+using Value = std::conditional_t<kF32, float, uint16_t>;
+
+// h of eight columns from col on in one row (col < F), and g and u where they are kept.
+template <bool kF32>
+__device__ __forceinline__ void finish_gated(const EpiArgs& e, const DropKey& key, float (&g)[8], const float (&u)[8],
+                                             int64_t row, int col)
+{
+    using T = Value<kF32>;
+    const int n = e.N - col;
+    const int64_t at = row * e.N + col;
+    if (e.save_g != nullptr) {
+        store8(static_cast<T*>(e.save_g) + at, g, n);
+        store8(static_cast<T*>(e.save_u) + at, u, n);
+    }
+    float h[8], slope;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        activation<kF32>(e.act, g[i], h[i], slope);
+        h[i] *= u[i];
+    }
+    if (e.drop.threshold != 0)
+        drop8(h, e.drop, key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row));
+    store8(static_cast<T*>(e.o0) + at, h, n);
+}
+
+// dg and du of eight columns; columns from N on are written as zero, they pad the products' K.
+template <bool kF32>
+__device__ __forceinline__ void finish_gated_bwd(const EpiArgs& e, const DropKey& key, float (&g)[8], float (&u)[8],
+                                                 int64_t row, int col)
+{
+    using T = Value<kF32>;
+    const int n = e.N - col;
+    float d[8];
+    load8(d, static_cast<const T*>(e.dh) + row * e.N + col, n);
+    if (e.drop.threshold != 0)
+        drop8(d, e.drop, key, static_cast<uint32_t>(col >> 3), static_cast<uint32_t>(row));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        float value, slope;
+        activation<kF32>(e.act, g[i], value, slope);
+        // a dropped place has no gradient whatever its g and u
+        g[i] = d[i] == 0.0f || i >= n ? 0.0f : d[i] * u[i] * slope;
+        u[i] = d[i] == 0.0f || i >= n ? 0.0f : d[i] * value;
+    }
+    constexpr int kPlanes = kF32 ? 3 : 1;
+    uint16_t* const p = e.dgu + row * e.ld_dgu + col;
+    store_planes<kF32>(p, e.dgu_plane, g);
+    store_planes<kF32>(p + kPlanes * e.dgu_plane, e.dgu_plane, u);
+}
+
+
+// One run of eight columns to where the epilogue puts it: v (and, gated, w: u where v is g), of matrix mat.
+template <int kEpi, bool kF32>
+__device__ __forceinline__ void finish8(const EpiArgs& e, const DropKey& key, float (&v)[8], float (&w)[8], int mat,
+                                        int64_t row, int col)
+{
+    if constexpr (kEpi == kEpiGated)
+        finish_gated<kF32>(e, key, v, w, row, col);
+    else if constexpr (kEpi == kEpiGatedBwd)
+        finish_gated_bwd<kF32>(e, key, v, w, row, col);
+    else
+        store8(static_cast<Value<kF32>*>(mat ? e.o1 : e.o0) + row * e.N + col, v, e.N - col);
+}
+
+// Where a part's sums of one matrix row lie.
+__device__ __forceinline__ float* partial_at(const EpiArgs& e, int part, int mat, int64_t row, int col)
+{
+    return e.partial + ((static_cast<int64_t>(part) * e.mats + mat) * e.M + row) * e.ld_part + col;
+}
+
+// gated_rows.hip: the gated product of few rows, weights straight from memory to the matrix cores.
+struct RowsArgs {
+    const void *x, *wg, *wu;                    // [M, K], [K, N] of the call's type, any alignment
+    int K;
+    EpiArgs e;
+};
+constexpr int kMaxRows = 64;
+// Parts of K for M rows (1: the kernel writes the results itself; otherwise partial sums).
+int gated_rows_parts(int64_t M, int64_t K, int64_t N);
+hipError_t launch_gated_rows(Epi epi, int dtype, const RowsArgs& g, hipStream_t s);
+// The results from partial sums (EpiArgs.partial).
+hipError_t launch_gated_finish(Epi epi, int dtype, const EpiArgs& e, hipStream_t s);
+
+}  // namespace moe

@@ -33,6 +33,21 @@ inline Divisor divisor(int d)
     return Divisor{(uint64_t{1} << (31 + l)) / static_cast<uint64_t>(d) + 1, 31 + l, d};
 }
 
+// Runs launch(first row, threads, workgroups of 256) over rows of `groups` groups of 8 columns, a thread each, with fewer
+// than 2^31 threads a launch.
+template <class F>
+hipError_t for_groups(int64_t rows, int64_t groups, F launch)
+{
+    const int64_t step = ((int64_t{1} << 31) - 256) / groups;
+    for (int64_t r = 0; r < rows; r += step) {
+        const int n = static_cast<int>((rows - r < step ? rows - r : step) * groups);
+        launch(r, n, static_cast<unsigned>(ceil_div(n, 256)));
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
 // Raises one kernel's limit of dynamic LDS to `bytes` (more than 64 KiB), once per device.
 struct LdsLimit {
     std::atomic<bool> done[64];
@@ -60,6 +75,7 @@ hipError_t launch_dropout(const void* x, const void* residual, int dtype, int64_
 struct GatedLayout {
     size_t x = 0, wg = 0, wu = 0;      // operands laid out for the products, where the caller's are not already
     size_t dgu = 0;                    // backward: the gradients of g and u
+    size_t partial = 0;                // sums over parts of K
     size_t total = 0;
 };
 GatedLayout gated_layout(const moe_gated& g, bool backward);

@@ -128,7 +128,9 @@ def block_inputs(T, H, F, dtype, seed=0):
 
 SIZES = [(1, 1, 1), (1, 8, 8), (2, 7, 9), (1, 64, 64), (3, 65, 63), (16, 72, 136), (17, 128, 100), (33, 200, 264),
          (64, 64, 128), (65, 127, 129), (127, 320, 72), (128, 256, 256), (129, 130, 257), (200, 520, 328), (257, 1001, 130),
-         (300, 96, 1032), (1, 1000, 520), (5, 2056, 24), (31, 24, 2000)]
+         (300, 96, 1032), (1, 1000, 520), (5, 2056, 24), (31, 24, 2000),
+         # few rows: every row block, K cut over workgroups and not, many columns
+         (1, 4096, 264), (16, 2047, 65), (17, 1030, 8), (32, 777, 1003), (48, 600, 70), (64, 4100, 33), (3, 40, 8200)]
 
 
 @TYPES
@@ -178,7 +180,8 @@ def test_gated_extreme_values(dtype):
 
 
 BWD_SIZES = [(1, 1, 1), (1, 8, 16), (2, 7, 9), (16, 72, 136), (33, 65, 63), (64, 128, 64), (65, 200, 100), (129, 257, 130),
-             (130, 128, 264), (200, 136, 520), (300, 1000, 24), (7, 24, 1001)]
+             (130, 128, 264), (200, 136, 520), (300, 1000, 24), (7, 24, 1001),
+             (2, 2050, 70), (30, 1000, 40), (61, 3000, 200)]
 
 
 @TYPES

@@ -84,7 +84,7 @@ def test_gated_refusals(mel):
     assert backward(d) == 1 and forward(d, rng=P(0x10004)) == 1
     # workspaces: the backward always needs one, the forward where operands are laid out anew
     assert backward(g, ws=None) == 3 and backward(g, n=1) == 3 and backward(g, ws=P(0x10008)) == 1
-    odd = _gated(mel, H=15)
+    odd = _gated(mel, T=100, H=15)
     assert forward(odd, ws=None) == 3 and forward(odd, n=1) == 3
     # no tokens: nothing to do in the forward
     assert forward(_gated(mel, T=0), x=None, wg=None, wu=None, h=None, ws=None, n=0) == 0
