@@ -7,9 +7,8 @@
 //     itself, which reads the adapter's A again from the L2 but saves a launch and a pass through memory;
 //   - many rows: the rows are sorted by adapter into tiles of up to 64 (plan_kernel, one workgroup), then v and v B run
 //     on the matrix cores, tile by tile (shrink_kernel, expand_kernel).  x goes from memory to the MFMA's registers, the
-//     adapter's matrices through LDS; K is cut so that there are workgroups enough, the cuts' float32 sums joined when
-//     the second product reads them.  v enters that product as two bfloat16 planes (16 bits) for bfloat16 tensors, as
-//     three for float32 ones.
+//     adapter's matrices through LDS; K is cut so that there are workgroups enough, and join_kernel adds the cuts' float32
+//     sums.  v enters the second product as two bfloat16 planes (16 bits) for bfloat16 tensors, as three for float32 ones.
 // A row's result does not depend on the tile that it falls into, so neither the order in which the plan's counters hand
 // out places nor other rows change it.
 #include <algorithm>
@@ -22,6 +21,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;                 // rows per tile
+constexpr int kExpandGrid = 768;         // expand_kernel: three workgroups per CU (512: 54 us against 48 at 8192 x 4096, rank 64)
 
 template <class T>
 __device__ __forceinline__ float to_float(T v)
@@ -264,7 +264,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
 struct TileArgs {
     const Tile* tiles;
     const int32_t *count, *perm;
-    float* v;                             // partial sums [splits, T, 32 kRB] in sorted order
+    float* part;                          // sums over one cut of K each, [splits, T, 32 kRB] in sorted order
+    uint16_t* v;                          // v's planes [2 or 3, T, 32 kRB] in sorted order
     int splits, steps;                    // cuts of K, K steps of all of them
 };
 
@@ -283,6 +284,18 @@ __device__ __forceinline__ f32x16_t mfma_planes(const bf16x8_t (&w)[PB], const b
             acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(w[0], r[i], acc, 0, 0, 0);
     }
     return acc;
+}
+
+// Eight values of v as the planes that enter the second product.
+template <class T>
+__device__ __forceinline__ void store_v(uint16_t* p, int64_t plane, const float (&w)[8])
+{
+    constexpr int PV = kPlanesOf<T> == 1 ? 2 : 3;
+    u32x4_t pl[PV];
+    split8<PV>(w, pl);
+#pragma unroll
+    for (int q = 0; q < PV; ++q)
+        *reinterpret_cast<u32x4_t*>(p + q * plane) = pl[q];
 }
 
 // v of a tile's rows over one cut of K.  Waves: 2 row halves of 32 x 2 halves of each K step; kRB column blocks of 32.
@@ -315,18 +328,20 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(smem)));
 
-    Raw8<T> xr[kGroups], ar[kLoads];
-    const auto fetch = [&](int step) {
-        const int k0 = step * kStep;
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int c = (tid + i * kThreads) % (kCols / 8), k = k0 + (tid + i * kThreads) / (kCols / 8);
-            ar[i] = load_raw<kWhole>(A + static_cast<int64_t>(k) * g.R + 8 * c, k < g.K ? g.R - 8 * c : 0);
-        }
+    // Steps of whole kStep run with kSets of them in flight: unconditional loads (past the rank's and the last step's end
+    // they repeat what is there), each into the registers that its step's predecessor has just left.
+    constexpr int kSets = P == 1 ? 2 : 1;
+    Raw8<T> xr[kSets][kGroups], ar[kSets][kLoads];
+    const auto fetch_a = [&](Raw8<T>& r, int step, int i, bool partial) {
+        const int c = (tid + i * kThreads) % (kCols / 8), k = step * kStep + (tid + i * kThreads) / (kCols / 8);
+        if (kWhole && !partial)
+            r = load_raw<true>(A + static_cast<int64_t>(k) * g.R + min(8 * c, g.R - 8), 8);
+        else
+            r = load_raw<kWhole>(A + static_cast<int64_t>(k) * g.R + 8 * c, k < g.K ? g.R - 8 * c : 0);
     };
-    const auto fetch_x = [&](int step, int s) {
+    const auto fetch_x = [&](Raw8<T>& r, int step, int s, bool partial) {
         const int k = step * kStep + (kStep / 2) * wk + 16 * s + 8 * (lane >> 5);
-        xr[s] = load_raw<kWhole>(x + k, busy ? g.K - k : 0);
+        r = partial ? load_raw<false>(x + k, g.K - k) : load_raw<true>(x + k, 8);
     };
     f32x16_t acc[kRB];
 #pragma unroll
@@ -334,46 +349,71 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
 #pragma unroll
         for (int e = 0; e < 16; ++e)
             acc[j][e] = 0.0f;
-    if (step0 < step1) {
-        fetch(step0);
-#pragma unroll
-        for (int s = 0; s < kGroups; ++s)
-            fetch_x(step0, s);
-    }
-    for (int step = step0; step < step1; ++step) {
+    // one step from one set of registers, which then take step `next` (more: there is one)
+    const auto run = [&](auto more, Raw8<T> (&av)[kLoads], Raw8<T> (&xv)[kGroups], int next) {
+        constexpr bool kMore = decltype(more)::value;
         __syncthreads();                                  // the stage of the step before is read
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int at = tid + i * kThreads;
             u32x4_t pl[P];
-            planes8(ar[i], pl);
+            planes8(av[i], pl);
 #pragma unroll
             for (int q = 0; q < P; ++q)
                 *reinterpret_cast<u32x4_t*>(smem + q * kPlane + (at / (kCols / 8)) * kRow + 16 * (at % (kCols / 8))) = pl[q];
         }
         __syncthreads();
-        if (step + 1 < step1)
-            fetch(step + 1);
-        if (busy)
+        if constexpr (kMore)
 #pragma unroll
-            for (int s = 0; s < kGroups; ++s) {
-                u32x4_t xp[P];
-                planes8(xr[s], xp);
-                bf16x8_t r[P];
+            for (int i = 0; i < kLoads; ++i)
+                fetch_a(av[i], next, i, false);
+#pragma unroll
+        for (int s = 0; s < kGroups; ++s) {
+            u32x4_t xp[P];
+            planes8(xv[s], xp);
+            bf16x8_t r[P];
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+                r[q] = __builtin_bit_cast(bf16x8_t, xp[q]);
+            if constexpr (kMore)
+                fetch_x(xv[s], next, s, false);
+#pragma unroll
+            for (int j = 0; j < kRB; ++j) {
+                bf16x8_t w[P];
 #pragma unroll
                 for (int q = 0; q < P; ++q)
-                    r[q] = __builtin_bit_cast(bf16x8_t, xp[q]);
-                if (step + 1 < step1)
-                    fetch_x(step + 1, s);
-#pragma unroll
-                for (int j = 0; j < kRB; ++j) {
-                    bf16x8_t w[P];
-#pragma unroll
-                    for (int q = 0; q < P; ++q)
-                        w[q] = read_tr(lds + q * kPlane + ((kStep / 2) * wk + 16 * s) * kRow + 64 * j + tr_offset(lane, kRow), kRow);
-                    acc[j] = mfma_planes<P, P>(w, r, acc[j]);
-                }
+                    w[q] = read_tr(lds + q * kPlane + ((kStep / 2) * wk + 16 * s) * kRow + 64 * j + tr_offset(lane, kRow), kRow);
+                acc[j] = mfma_planes<P, P>(w, r, acc[j]);
             }
+        }
+    };
+    const int whole1 = min(step1, g.K / kStep);            // steps [step0, whole1) lie within K
+    if (step0 < whole1) {
+#pragma unroll
+        for (int u = 0; u < kSets; ++u) {
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                fetch_a(ar[u][i], min(step0 + u, whole1 - 1), i, false);
+#pragma unroll
+            for (int s = 0; s < kGroups; ++s)
+                fetch_x(xr[u][s], min(step0 + u, whole1 - 1), s, false);
+        }
+        int step = step0;
+        for (; step + kSets <= whole1; step += kSets)
+#pragma unroll
+            for (int u = 0; u < kSets; ++u)
+                run(std::true_type{}, ar[u], xr[u], min(step + u + kSets, whole1 - 1));
+        if (step < whole1)
+            run(std::false_type{}, ar[0], xr[0], 0);
+    }
+    if (whole1 < step1) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            fetch_a(ar[0][i], whole1, i, true);
+#pragma unroll
+        for (int s = 0; s < kGroups; ++s)
+            fetch_x(xr[0][s], whole1, s, true);
+        run(std::false_type{}, ar[0], xr[0], 0);
     }
     // the two K halves join through LDS
     __syncthreads();
@@ -390,145 +430,185 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
     __syncthreads();
     if (busy && wk == 0) {
         const float f = g.scale == nullptr ? 1.0f : g.scale[tile.adapter];
-        float* const v = p.v + (static_cast<int64_t>(split) * g.T + tile.begin + 32 * wr + (lane & 31)) * kCols + 8 * (lane >> 5);
+        const int64_t at = static_cast<int64_t>(tile.begin + 32 * wr + (lane & 31)) * kCols;
 #pragma unroll
         for (int j = 0; j < kRB; ++j)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                const int c = 32 * j + 16 * h + 8 * (lane >> 5);
                 float w[8], u[8];
                 run8(acc[j], h, w);
                 load8(u, join + 32 * j + 16 * h, 8);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    w[i] = (w[i] + u[i]) * f;
-                if (32 * wr + (lane & 31) < n)
-                    store8(v + 32 * j + 16 * h, w, 8);
+                    w[i] = c + i < rank ? (w[i] + u[i]) * f : 0.0f;
+                if (32 * wr + (lane & 31) >= n)
+                    continue;
+                if (p.splits == 1)
+                    store_v<T>(p.v + at + c, static_cast<int64_t>(g.T) * kCols, w);
+                else
+                    store8(p.part + static_cast<int64_t>(split) * g.T * kCols + at + c, w, 8);
             }
     }
 }
 
-// out of a tile's rows over `cols` columns (a multiple of 128).  Waves: 2 row halves x 2 halves of 128 columns.
-template <class T, int kRB, bool kWhole>
-__global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p, int cols)
+// v from the cuts' sums; n groups of 8 values.
+template <class T>
+__global__ __launch_bounds__(kThreads) void join_kernel(const float* __restrict__ part, uint16_t* __restrict__ v, int splits,
+                                                        int64_t n)
 {
-    constexpr int PB = kPlanesOf<T>, PV = PB == 1 ? 2 : 3;
-    constexpr int kR = 32 * kRB, kRow = 2 * 128 + 16, kPlane = kR * kRow, kLoads = kR * 16 / kThreads;
-    constexpr int kVRow = 2 * kR + 16, kVPlane = kTile * kVRow;        // v's planes, after B's
-    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
-    if (static_cast<int>(blockIdx.x) >= p.count[0])
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+    if (at >= n)
         return;
-    const Tile tile = p.tiles[blockIdx.x];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int n0 = blockIdx.y * cols, n1 = min(n0 + cols, g.N), n = tile.end - tile.begin;
-    const int rank = tile.adapter < g.L ? rank_of(g, tile.adapter) : 0;
-    if (rank == 0) {                                      // the rows are copied, a wave each
-        if (g.base != g.out)
-            for (int r = wave; r < n; r += kThreads / 64) {
-                const int64_t at = static_cast<int64_t>(p.perm[tile.begin + r]) * g.N;
-                for (int c = n0 + 8 * lane; c < n1; c += 512) {
-                    float w[8];
-                    load8(w, static_cast<const T*>(g.base) + at + c, n1 - c);
-                    store8(static_cast<T*>(g.out) + at + c, w, n1 - c);
-                }
-            }
-        return;
-    }
-    const int wr = wave >> 1, wc = wave & 1;
-    const int mine = 32 * wr + (lane & 31), safe = min(mine, n - 1);
-    const bool busy = 32 * wr < n, real = mine < n;
-    const int64_t row = static_cast<int64_t>(p.perm[tile.begin + safe]) * g.N;
-    const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(tile.adapter) * g.R * g.N;
-    const uint32_t lds = static_cast<uint32_t>(
-        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(smem)));
-
-    Raw8<T> br[kLoads], base[4];
-    const auto fetch = [&](int c0) {
+    constexpr int kAhead = 4;                             // cuts whose loads go out together
+    float sum[8] = {};
+    for (int q0 = 0; q0 < splits; q0 += kAhead) {
+        Raw8<float> w[kAhead];
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int r = (tid + i * kThreads) / 16, c = c0 + 8 * (tid % 16);
-            br[i] = load_raw<kWhole>(B + static_cast<int64_t>(r) * g.N + c, r < rank ? n1 - c : 0);
-        }
-        if (busy)
+        for (int i = 0; i < kAhead; ++i)
+            w[i] = load_raw<true>(part + 8 * (at + (q0 + i) * n), q0 + i < splits ? 8 : 0);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int c = c0 + 64 * wc + 16 * q + 8 * (lane >> 5);
-                base[q] = load_raw<kWhole>(static_cast<const T*>(g.base) + row + c, real ? n1 - c : 0);
-            }
-    };
-    fetch(n0);
-    // v of the tile's rows as planes, each thread 8 columns of a row at a time
-#pragma unroll
-    for (int i = 0; i < kTile * kR / 8 / kThreads; ++i) {
-        const int r = (tid + i * kThreads) / (kR / 8), c = 8 * ((tid + i * kThreads) % (kR / 8));
-        const float* const v = p.v + (static_cast<int64_t>(tile.begin) + min(r, n - 1)) * kR + c;
-        float sum[8] = {};
-#pragma unroll 4
-        for (int q = 0; q < p.splits; ++q) {
-            float w[8];
-            load8(w, v + static_cast<int64_t>(q) * g.T * kR, 8);
+        for (int i = 0; i < kAhead; ++i) {
+            float f[8];
+            w[i].values(f);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                sum[e] += w[e];
+                sum[e] += f[e];
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (c + e >= rank)
-                sum[e] = 0.0f;
-        u32x4_t pl[PV];
-        split8<PV>(sum, pl);
-#pragma unroll
-        for (int q = 0; q < PV; ++q)
-            *reinterpret_cast<u32x4_t*>(smem + PB * kPlane + q * kVPlane + r * kVRow + 2 * c) = pl[q];
     }
-    const unsigned char* const mine_v = smem + PB * kPlane + (32 * wr + (lane & 31)) * kVRow + 16 * (lane >> 5);
-    for (int c0 = n0; c0 < n1; c0 += 128) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            u32x4_t pl[PB];
-            planes8(br[i], pl);
-#pragma unroll
-            for (int q = 0; q < PB; ++q)
-                *reinterpret_cast<u32x4_t*>(smem + q * kPlane + ((tid + i * kThreads) / 16) * kRow + 16 * (tid % 16)) = pl[q];
-        }
-        Raw8<T> now[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-            now[q] = base[q];
-        __syncthreads();
-        if (c0 + 128 < n1)
-            fetch(c0 + 128);
-        if (!busy)
+    store_v<T>(v + 8 * at, 8 * n, sum);
+}
+
+// LDS of expand_kernel: B's rows of one run, then v's planes.  The run's product takes the place of B once that is read.
+template <class T, int kRB>
+struct ExpandLds {
+    static constexpr int PB = kPlanesOf<T>, PV = PB == 1 ? 2 : 3, kR = 32 * kRB;
+    static constexpr int kRow = 2 * 128 + 16, kPlane = kR * kRow;         // B: bytes of a row, of a plane
+    static constexpr int kOutRow = 4 * 128 + 16;                           // the product, float32
+    static constexpr int kVRow = 2 * kR + 16, kVPlane = kTile * kVRow;
+    static constexpr int kV = PB * kPlane > kTile * kOutRow ? PB * kPlane : kTile * kOutRow;   // where v begins
+    static constexpr int kBytes = kV + PV * kVPlane;
+};
+
+// out.  The work is the (tile, run of 128 columns) pairs in order, in equal shares for the workgroups of the grid.  For the
+// product each of the four waves takes 32 columns of all 64 rows; for base and out, whole rows of a run (256 or 512 bytes;
+// with pieces of 32 rows, as the accumulators hold them, 8192 x 4096 of rank 64 took 60 us instead of 54).
+template <class T, int kRB>
+__global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
+{
+    using M = ExpandLds<T, kRB>;
+    constexpr int PB = M::PB, PV = M::PV, kR = M::kR, kLoads = kR * 16 / kThreads;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const uint32_t lds = static_cast<uint32_t>(
+        reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(smem)));
+    const int runs = (g.N + 127) / 128, col = 8 * (tid % 16), row0 = tid / 16;   // this thread: rows row0 + 16 i
+    const int64_t items = static_cast<int64_t>(p.count[0]) * runs;
+    const int64_t item1 = items * (blockIdx.x + 1) / gridDim.x;
+    for (int64_t item = items * blockIdx.x / gridDim.x; item < item1;) {
+        const int ti = static_cast<int>(item / runs), run0 = static_cast<int>(item - static_cast<int64_t>(ti) * runs);
+        const int run1 = static_cast<int>(min(static_cast<int64_t>(runs), run0 + item1 - item));
+        item += run1 - run0;
+        const Tile tile = p.tiles[ti];
+        const int n0 = 128 * run0, n1 = min(128 * run1, g.N), n = tile.end - tile.begin;
+        const int rank = tile.adapter < g.L ? rank_of(g, tile.adapter) : 0;
+        if (rank == 0) {                                  // the rows are copied, a wave each
+            if (g.base != g.out)
+                for (int r = wave; r < n; r += kThreads / 64) {
+                    const int64_t at = static_cast<int64_t>(p.perm[tile.begin + r]) * g.N;
+                    for (int c = n0 + 8 * lane; c < n1; c += 512) {
+                        float w[8];
+                        load8(w, static_cast<const T*>(g.base) + at + c, n1 - c);
+                        store8(static_cast<T*>(g.out) + at + c, w, n1 - c);
+                    }
+                }
             continue;
+        }
+        int64_t at[4];                                    // rows past the last repeat it and are not written
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            f32x16_t acc;
+        for (int i = 0; i < 4; ++i)
+            at[i] = static_cast<int64_t>(p.perm[tile.begin + min(row0 + 16 * i, n - 1)]) * g.N + col;
+        const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(tile.adapter) * g.R * g.N + col;
+        Raw8<T> bv[kLoads], base[4];
+        const auto fetch = [&](int c0) {
+            const int left = g.N - c0 - col;
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                acc[e] = 0.0f;
+            for (int i = 0; i < kLoads; ++i)
+                bv[i] = load_raw<false>(B + static_cast<int64_t>(min(row0 + 16 * i, rank - 1)) * g.N + c0, left);
 #pragma unroll
-            for (int s = 0; s < 2 * kRB; ++s) {
-                bf16x8_t w[PB], v[PV];
+            for (int i = 0; i < 4; ++i)
+                base[i] = load_raw<false>(static_cast<const T*>(g.base) + at[i] + c0, left);
+        };
+        fetch(n0);
+        // v of the tile's rows (once the tile before is done with its own)
+        __syncthreads();
 #pragma unroll
-                for (int q = 0; q < PV; ++q)
-                    v[q] = *reinterpret_cast<const bf16x8_t*>(mine_v + q * kVPlane + 32 * s);
+        for (int i = 0; i < kTile * kR / 8 / kThreads; ++i) {
+            const int r = (tid + i * kThreads) / (kR / 8), c = 8 * ((tid + i * kThreads) % (kR / 8));
+            const uint16_t* const v = p.v + (static_cast<int64_t>(tile.begin) + min(r, n - 1)) * kR + c;
+#pragma unroll
+            for (int q = 0; q < PV; ++q)
+                *reinterpret_cast<u32x4_t*>(smem + M::kV + q * M::kVPlane + r * M::kVRow + 2 * c) =
+                    *reinterpret_cast<const u32x4_t*>(v + static_cast<int64_t>(q) * g.T * kR);
+        }
+        const unsigned char* const mine_v = smem + M::kV + (lane & 31) * M::kVRow + 16 * (lane >> 5);
+        for (int c0 = n0; c0 < n1; c0 += 128) {
+            __syncthreads();                              // the product of the run before is read
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {            // B's rows from the rank on are zero
+                u32x4_t pl[PB];
+                planes8(bv[i], pl);
 #pragma unroll
                 for (int q = 0; q < PB; ++q)
-                    w[q] = read_tr(lds + q * kPlane + 16 * s * kRow + 2 * (64 * wc + 32 * j) + tr_offset(lane, kRow), kRow);
-                acc = mfma_planes<PV, PB>(w, v, acc);
+                    *reinterpret_cast<u32x4_t*>(smem + q * M::kPlane + (row0 + 16 * i) * M::kRow + 2 * col) =
+                        row0 + 16 * i < rank ? pl[q] : u32x4_t{0, 0, 0, 0};
             }
+            __syncthreads();
+            f32x16_t acc[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float w[8], u[8];
-                run8(acc, h, w);
-                now[2 * j + h].values(u);
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] += u[i];
-                const int c = c0 + 64 * wc + 32 * j + 16 * h + 8 * (lane >> 5);
-                if (real && c < n1)
-                    store8(static_cast<T*>(g.out) + row + c, w, n1 - c);
+                for (int e = 0; e < 16; ++e)
+                    acc[b][e] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 2 * kRB; ++k) {
+                bf16x8_t w[PB];
+#pragma unroll
+                for (int q = 0; q < PB; ++q)
+                    w[q] = read_tr(lds + q * M::kPlane + 16 * k * M::kRow + 64 * wave + tr_offset(lane, M::kRow), M::kRow);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    bf16x8_t v[PV];
+#pragma unroll
+                    for (int q = 0; q < PV; ++q)
+                        v[q] = *reinterpret_cast<const bf16x8_t*>(mine_v + q * M::kVPlane + 32 * b * M::kVRow + 32 * k);
+                    acc[b] = mfma_planes<PV, PB>(w, v, acc[b]);
+                }
             }
+            __syncthreads();
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)               // columns 8 q + 4 (lane / 32) .. + 3 of the wave's 32
+                    *reinterpret_cast<f32x4_t*>(smem + (32 * b + (lane & 31)) * M::kOutRow +
+                                                4 * (32 * wave + 8 * q + 4 * (lane >> 5))) =
+                        f32x4_t{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float sum[8], u[8];
+                load8(sum, reinterpret_cast<const float*>(smem + (row0 + 16 * i) * M::kOutRow) + col, 8);
+                base[i].values(u);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    sum[e] += u[e];
+                if (row0 + 16 * i < n && c0 + col < g.N)
+                    store8(static_cast<T*>(g.out) + at[i] + c0, sum, g.N - c0 - col);
+            }
+            // the next run's values are loaded when their registers are free: copying them would wait for the loads
+            __builtin_amdgcn_sched_barrier(0);
+            if (c0 + 128 < n1)
+                fetch(c0 + 128);
         }
     }
 }
@@ -538,7 +618,7 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p, in
 // How a call runs.
 struct Plan {
     bool rows;                // row_kernel
-    int cols;                 // output columns per workgroup
+    int cols;                 // row_kernel: output columns per workgroup
     int blocks;               // column blocks of 32 that hold the rank (1, 2 or 4)
     int splits, steps;
     int64_t max_tiles;
@@ -560,8 +640,6 @@ Plan plan(const moe_adapter& p)
     q.max_tiles = ceil_div(p.T, kTile) + std::min(p.T, p.L + 1);
     const int64_t tiles = ceil_div(p.T, kTile);
     q.splits = static_cast<int>(std::clamp<int64_t>(ceil_div(512, tiles), 1, std::clamp<int64_t>(q.steps / 4, 1, 16)));
-    const int64_t per_tile = std::clamp<int64_t>(ceil_div(640, tiles), 1, ceil_div(p.N, 128));
-    q.cols = static_cast<int>(ceil_div(ceil_div(p.N, per_tile), 128) * 128);
     return q;
 }
 
@@ -570,16 +648,22 @@ bool whole(const moe_adapter& p) { return p.K % 8 == 0 && p.N % 8 == 0 && p.R % 
 template <class T, int kRB, bool kWhole>
 hipError_t launch_tiles(const Args& g, const TileArgs& t, const Plan& q, hipStream_t s)
 {
-    constexpr int kPB = kPlanesOf<T>, kPV = kPB == 1 ? 2 : 3;
-    constexpr int kExpandLds = kPB * 32 * kRB * (2 * 128 + 16) + kPV * kTile * (64 * kRB + 16);
+    constexpr int kExpandLds = ExpandLds<T, kRB>::kBytes;
     static LdsLimit limit;
-    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&expand_kernel<T, kRB, kWhole>), kExpandLds); e != hipSuccess)
+    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&expand_kernel<T, kRB>), kExpandLds); e != hipSuccess)
         return e;
     const unsigned tiles = static_cast<unsigned>(q.max_tiles);
     shrink_kernel<T, kRB, kWhole><<<dim3(tiles, q.splits), kThreads, 0, s>>>(g, t);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
-    expand_kernel<T, kRB, kWhole><<<dim3(tiles, static_cast<unsigned>(ceil_div(g.N, q.cols))), kThreads, kExpandLds, s>>>(g, t, q.cols);
+    if (t.splits > 1) {
+        const int64_t n = static_cast<int64_t>(g.T) * 4 * kRB;
+        join_kernel<T><<<dim3(static_cast<unsigned>(ceil_div(n, kThreads))), kThreads, 0, s>>>(t.part, t.v, t.splits, n);
+        if (hipError_t e = hipGetLastError(); e != hipSuccess)
+            return e;
+    }
+    const int64_t items = q.max_tiles * ceil_div(g.N, 128);
+    expand_kernel<T, kRB><<<dim3(static_cast<unsigned>(std::min<int64_t>(items, kExpandGrid))), kThreads, kExpandLds, s>>>(g, t);
     return hipGetLastError();
 }
 
@@ -602,14 +686,15 @@ hipError_t launch(const moe_adapter& p, const Args& g, unsigned char* ws, hipStr
     plan_kernel<<<1, kPlanThreads, 0, s>>>(g.ids, g.T, g.L, perm, tiles, count);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
-    const TileArgs t{tiles, count, perm, reinterpret_cast<float*>(ws + L.v), q.splits, q.steps};
-    // rows of whole runs of eight values need no code for a run that ends early
+    const TileArgs t{tiles, count, perm, reinterpret_cast<float*>(ws + L.part), reinterpret_cast<uint16_t*>(ws + L.v), q.splits,
+                     q.steps};
+    // ranks of whole runs of eight values need no code for a run that ends early
     const auto by_blocks = [&](auto whole) {
         constexpr bool kWhole = decltype(whole)::value;
         return q.blocks == 1 ? launch_tiles<T, 1, kWhole>(g, t, q, s) : q.blocks == 2 ? launch_tiles<T, 2, kWhole>(g, t, q, s)
                                                                                      : launch_tiles<T, 4, kWhole>(g, t, q, s);
     };
-    return whole(p) ? by_blocks(std::true_type{}) : by_blocks(std::false_type{});
+    return p.R % 8 == 0 ? by_blocks(std::true_type{}) : by_blocks(std::false_type{});
 }
 
 }  // namespace
@@ -628,7 +713,9 @@ AdapterLayout adapter_layout(const moe_adapter& p)
     take(L.count, sizeof(int32_t));
     take(L.perm, static_cast<size_t>(p.T) * sizeof(int32_t));
     take(L.tiles, static_cast<size_t>(q.max_tiles) * sizeof(Tile));
-    take(L.v, static_cast<size_t>(q.splits) * p.T * 32 * q.blocks * sizeof(float));
+    take(L.v, static_cast<size_t>(p.dtype == MOE_F32 ? 3 : 2) * p.T * 32 * q.blocks * sizeof(uint16_t));
+    if (q.splits > 1)
+        take(L.part, static_cast<size_t>(q.splits) * p.T * 32 * q.blocks * sizeof(float));
     L.total = off;
     return L;
 }

@@ -619,6 +619,13 @@ void add_segments_pair(GemmArgs& g, int dtype, int a1)
 
 }  // namespace
 
+namespace {
+
+// Whether g and u come from the kernels for few rows.
+bool few_rows(const moe_gated& g) { return g.T <= kMaxRows && g.F >= kMinCols; }
+
+}  // namespace
+
 GatedLayout gated_layout(const moe_gated& g, bool backward)
 {
     GatedLayout L;
@@ -628,7 +635,7 @@ GatedLayout gated_layout(const moe_gated& g, bool backward)
         at = off;
         off = align_up(off + static_cast<size_t>(bytes));
     };
-    const bool rows = g.T <= kMaxRows;                    // the forward product takes its operands as they are
+    const bool rows = few_rows(g);                  // the forward product takes its operands as they are
     if (needs_pack(g.dtype, g.H) && (backward || !rows))
         take(L.x, 2 * P * g.T * own_ld(g.H));
     if (needs_pack(g.dtype, g.F) && (backward || !rows)) {
@@ -639,9 +646,8 @@ GatedLayout gated_layout(const moe_gated& g, bool backward)
         take(L.dgu, 2 * 2 * P * g.T * own_ld(g.F));
     int64_t partial = 0;                                  // of one product after the other
     if (g.T > 0) {
-        const int64_t parts = rows ? gated_rows_parts(g.T, g.H, g.F) : 1;
-        partial = rows ? (parts > 1 ? 4 * 2 * parts * g.T * padded(g.F) : 0)
-                       : partial_bytes(g.T, g.F, 2, products * ceil_div(g.H, kBK));
+        if (!rows)
+            partial = partial_bytes(g.T, g.F, 2, products * ceil_div(g.H, kBK));
         if (backward) {
             partial = std::max(partial, partial_bytes(g.T, g.H, 1, 2 * products * ceil_div(g.F, kBK)));
             partial = std::max(partial, partial_bytes(g.H, g.F, 2, products * ceil_div(g.T, kBK)));
@@ -676,15 +682,8 @@ hipError_t launch_gu(const moe_gated& q, const void* x, const void* wg, const vo
     e.N = static_cast<int>(q.F);
     e.mats = 2;
     e.act = q.activation;
-    if (q.T <= kMaxRows) {
-        e.parts = gated_rows_parts(q.T, q.H, q.F);
-        e.partial = e.parts > 1 ? partial : nullptr;
-        e.ld_part = static_cast<int>(padded(q.F));
-        const RowsArgs r{x, wg, wu, static_cast<int>(q.H), e};
-        if (hipError_t err = launch_gated_rows(static_cast<Epi>(kEpi), q.dtype, r, s); err != hipSuccess || e.parts == 1)
-            return err;
-        return launch_gated_finish(static_cast<Epi>(kEpi), q.dtype, e, s);
-    }
+    if (few_rows(q))
+        return launch_gated_rows(static_cast<Epi>(kEpi), q.dtype, RowsArgs{x, wg, wu, static_cast<int>(q.H), e}, s);
     GemmArgs g{};
     g.a = p.x.p;
     g.b0 = p.wg.p;
@@ -712,7 +711,7 @@ hipError_t launch_gated(const moe_gated& q, const Dropout& d, const void* x, con
     const GatedLayout L = gated_layout(q, false);
     unsigned char* const ws = static_cast<unsigned char*>(workspace);
     Prepared p{};
-    if (q.T > kMaxRows)
+    if (!few_rows(q))
         if (hipError_t e = prepare_all(q, x, wg, wu, L, ws, p, s); e != hipSuccess)
             return e;
     const int64_t size = q.dtype == MOE_F32 ? 4 : 2;

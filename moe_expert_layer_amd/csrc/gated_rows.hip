@@ -1,14 +1,16 @@
-// The gated product of few rows (up to 64) on gfx950: g = x Wg and u = x Wu with the epilogues of the gated block, and the
-// joining of sums over parts of K.
+// The gated product of few rows (up to 64) on gfx950: g = x Wg and u = x Wu with the epilogues of the gated block; and the
+// results from sums that the products of many rows took over parts of K.
 //
 // What bounds it is the weights' way from memory, so they take the shortest: a lane loads 4 adjacent columns of 8
 // consecutive k rows (of one matrix) straight into registers.  bfloat16: v_perm_b32 turns the 8 x 4 block into four MFMA
 // operands of 8 k each (v_mfma_f32_16x16x32_bf16, the weights as the first operand); lane l of operand j holds column
-// 4 (l % 16) + j, which leaves every lane of the result with 16 adjacent columns of one row.  float32: the words are
+// 4 (l % 16) + j, which leaves every lane of the result with 16 adjacent columns of one row (with 32 columns: 2 adjacent
+// columns a lane, two operands, 8 columns).  float32: the words are
 // v_mfma_f32_16x16x4_f32 operands as they are, eight of one k per lane group, exact products.  Nothing of the weights goes
 // through LDS, and rows of any width and alignment are read the same way.
-// A workgroup takes 64 columns of both matrices; its waves take K in turn, 32 rows at a time with the next 32 in flight,
-// and join their sums through LDS in a fixed order.  With few columns K is cut over workgroups too.
+// A workgroup takes 64 columns of both matrices, or 32 where 64 would leave half of the CUs without work; its waves take K
+// in turn, 32 rows at a time with the next 32 in flight, and join their sums through LDS in a fixed order.  K is not cut
+// over workgroups: joining them would take a second launch (7 us) and saves less than that.
 #include <algorithm>
 
 #include "gated_epilogue.h"
@@ -16,65 +18,74 @@
 namespace moe {
 namespace {
 
-constexpr int kCols = 64;                 // columns per workgroup and matrix
 constexpr int kBatch = 32;                // k rows per wave and step
 
-// Four adjacent values as loaded.
-template <class T>
-struct Raw4;
-template <>
-struct Raw4<uint16_t> {
-    u32x2_t w;
+// kN (4 or 2) adjacent values as loaded.
+template <class T, int kN>
+struct RawN {
+    static constexpr int kWords = kN * sizeof(T) / 4;
+    uint32_t w[kWords];
 };
-template <>
-struct Raw4<float> {
-    f32x4_t w;
-};
-typedef u32x2_t __attribute__((aligned(2))) u32x2_any_t;
 
-// The first n of four values at p, the others zero and not read.
-__device__ __forceinline__ Raw4<uint16_t> load4(const uint16_t* p, int n)
+// kN values at p.
+template <class T, int kN>
+__device__ __forceinline__ RawN<T, kN> load_n(const T* p)
 {
-    Raw4<uint16_t> r{u32x2_t{0, 0}};
-    if (n >= 4) {
-        r.w = *reinterpret_cast<const u32x2_any_t*>(p);
-    } else if (n > 0) {
+    RawN<T, kN> r;
+    if constexpr (RawN<T, kN>::kWords == 4) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_any_t*>(p);
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < n)
-                r.w[i / 2] |= static_cast<uint32_t>(p[i]) << (16 * (i % 2));
-    }
-    return r;
-}
-__device__ __forceinline__ Raw4<float> load4(const float* p, int n)
-{
-    Raw4<float> r{f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}};
-    if (n >= 4) {
-        r.w = *reinterpret_cast<const f32x4_any_t*>(p);
-    } else if (n > 0) {
-#pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < n)
-                r.w[i] = p[i];
+        for (int i = 0; i < 4; ++i)
+            r.w[i] = v[i];
+    } else if constexpr (RawN<T, kN>::kWords == 2) {
+        typedef u32x2_t __attribute__((aligned(2))) u32x2_any_t;
+        const u32x2_t v = *reinterpret_cast<const u32x2_any_t*>(p);
+        r.w[0] = v[0];
+        r.w[1] = v[1];
+    } else {
+        typedef uint32_t __attribute__((aligned(2))) u32_any_t;
+        r.w[0] = *reinterpret_cast<const u32_any_t*>(p);
     }
     return r;
 }
 
-// One step of a wave: 32 k of 64 columns of both matrices, and of kRB blocks of 16 rows of x.
-template <class T, int kRB>
+// The last kN - skip of the values first, zeros after them.
+template <class T, int kN>
+__device__ __forceinline__ void shift_down(RawN<T, kN>& r, int skip)
+{
+    if constexpr (RawN<T, kN>::kWords == 1) {
+        r.w[0] = skip >= 2 ? 0u : r.w[0] >> (16 * skip);
+    } else if constexpr (RawN<T, kN>::kWords == 2) {
+        const uint64_t v = (static_cast<uint64_t>(r.w[1]) << 32 | r.w[0]) >> min(8 * static_cast<int>(sizeof(T)) * skip, 63);
+        r.w[0] = skip >= kN ? 0u : static_cast<uint32_t>(v);
+        r.w[1] = skip >= kN ? 0u : static_cast<uint32_t>(v >> 32);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t v = 0;
+#pragma unroll
+            for (int s = 0; s + i < 4; ++s)
+                v = skip == s ? r.w[i + s] : v;
+            r.w[i] = v;
+        }
+    }
+}
+
+// One step of a wave: 32 k of 16 kN columns of both matrices, and of kRB blocks of 16 rows of x.
+template <class T, int kN, int kRB>
 struct Step {
-    Raw4<T> w[2][8];
+    RawN<T, kN> w[2][8];
     Raw8<T> x[kRB];
 };
 
-template <class T, int kRB>
-__device__ __forceinline__ void multiply(f32x4_t (&acc)[2][4][kRB], const Step<T, kRB>& s)
+template <class T, int kN, int kRB>
+__device__ __forceinline__ void multiply(f32x4_t (&acc)[2][kN][kRB], const Step<T, kN, kRB>& s)
 {
     if constexpr (sizeof(T) == 2) {
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kN; ++j) {
                 u32x4_t f;
                 const uint32_t sel = (j & 1) ? 0x07060302u : 0x05040100u;
 #pragma unroll
@@ -92,75 +103,110 @@ __device__ __forceinline__ void multiply(f32x4_t (&acc)[2][4][kRB], const Step<T
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int j = 0; j < kN; ++j)
 #pragma unroll
                     for (int b = 0; b < kRB; ++b)
                         acc[m][j][b] = __builtin_amdgcn_mfma_f32_16x16x4f32(
-                            s.w[m][i].w[j], i < 4 ? s.x[b].a[i & 3] : s.x[b].b[i & 3], acc[m][j][b], 0, 0, 0);
+                            __uint_as_float(s.w[m][i].w[j]), i < 4 ? s.x[b].a[i & 3] : s.x[b].b[i & 3], acc[m][j][b], 0, 0, 0);
     }
 }
 
-template <class T, int kRB, int kWaves, int kEpi>
-__global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 && kRB == 1 ? 2 : 1) void gated_rows_kernel(RowsArgs g)
+template <class T, int kN, int kRB, int kWaves, int kDepth, int kEpi>
+__global__ __launch_bounds__(64 * kWaves) void gated_rows_kernel(RowsArgs g)
 {
+    constexpr int kRuns = kN / 2;                          // runs of 8 columns of a lane's result
     extern __shared__ __attribute__((aligned(16))) unsigned char smem[];
     f32x4_t* const join = reinterpret_cast<f32x4_t*>(smem);            // [wave][matrix][j][row block][lane]
     const EpiArgs& e = g.e;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * kCols, part = blockIdx.y;
-    const int batches = (g.K + kBatch - 1) / kBatch;
-    const int b0 = static_cast<int>(static_cast<int64_t>(batches) * part / e.parts);
-    const int b1 = static_cast<int>(static_cast<int64_t>(batches) * (part + 1) / e.parts);
-    const int kg = 8 * (lane >> 4), col = n0 + 4 * (lane & 15), left = e.N - col;
-    const T* const w0 = static_cast<const T*>(g.wg) + col;
-    const T* const w1 = static_cast<const T*>(g.wu) + col;
+    const int n0 = blockIdx.x * 16 * kN;
+    // A lane whose kN columns pass the row's end reads the row's last kN (skip > 0: the first of them belong to lanes
+    // before it); in the last workgroup alone, whose lanes shift them into place.
+    const int kg = 8 * (lane >> 4), col = n0 + kN * (lane & 15), from = min(col, e.N - kN), skip = col - from;
+    const bool ragged = n0 + 16 * kN > e.N;
+    const T* const w0 = static_cast<const T*>(g.wg) + from;
+    const T* const w1 = static_cast<const T*>(g.wu) + from;
     const T* x[kRB];
 #pragma unroll
     for (int b = 0; b < kRB; ++b)                          // rows past the last repeat it and are not written
         x[b] = static_cast<const T*>(g.x) + static_cast<int64_t>(min(16 * b + (lane & 15), e.M - 1)) * g.K;
 
-    const auto load = [&](Step<T, kRB>& s, int batch) {
-        const int k = kBatch * batch + kg, n = batch < b1 ? left : 0;
+    // whole: all 32 k exist, and nothing stands between the loads
+    const auto load = [&](auto whole, Step<T, kN, kRB>& s, int batch) {
+        constexpr bool kWhole = decltype(whole)::value;
+        const int k = kBatch * batch + kg;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t at = static_cast<int64_t>(k + i) * e.N;
-            s.w[0][i] = load4(w0 + at, k + i < g.K ? n : 0);
-            s.w[1][i] = load4(w1 + at, k + i < g.K ? n : 0);
+            const int64_t at = static_cast<int64_t>(kWhole ? k + i : min(k + i, g.K - 1)) * e.N;
+            s.w[0][i] = load_n<T, kN>(w0 + at);
+            s.w[1][i] = load_n<T, kN>(w1 + at);
         }
 #pragma unroll
         for (int b = 0; b < kRB; ++b)
-            s.x[b] = load_raw<false>(x[b] + k, batch < b1 ? g.K - k : 0);
+            s.x[b] = load_raw<kWhole>(x[b] + k, kWhole ? 8 : g.K - k);
+        if constexpr (!kWhole) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (k + i >= g.K)
+                    s.w[0][i] = s.w[1][i] = RawN<T, kN>{};
+        }
     };
-    f32x4_t acc[2][4][kRB];
+    f32x4_t acc[2][kN][kRB];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kN; ++j)
 #pragma unroll
             for (int b = 0; b < kRB; ++b)
                 acc[m][j][b] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-    Step<T, kRB> s0, s1;
-    load(s0, b0 + wave);
-    for (int b = b0 + wave; b < b1; b += 2 * kWaves) {
-        load(s1, b + kWaves);
-        multiply<T, kRB>(acc, s0);
-        load(s0, b + 2 * kWaves);
-        multiply<T, kRB>(acc, s1);
+    const auto add = [&](Step<T, kN, kRB>& s) {
+        if (ragged)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                shift_down<T, kN>(s.w[0][i], skip);
+                shift_down<T, kN>(s.w[1][i], skip);
+            }
+        multiply<T, kN, kRB>(acc, s);
+        __builtin_amdgcn_sched_barrier(0);                 // the next loads go out when these registers are free
+    };
+    // this wave's whole steps: wave, wave + kWaves, ..; kDepth of them in flight
+    const int whole = g.K / kBatch, mine = whole > wave ? (whole - wave + kWaves - 1) / kWaves : 0;
+    Step<T, kN, kRB> s[kDepth];
+    if (mine > 0) {
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u)
+            load(std::true_type{}, s[u], wave + kWaves * min(u, mine - 1));
+        int i = 0;
+        for (; i + kDepth <= mine; i += kDepth)
+#pragma unroll
+            for (int u = 0; u < kDepth; ++u) {
+                add(s[u]);
+                load(std::true_type{}, s[u], wave + kWaves * min(i + u + kDepth, mine - 1));
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+        for (int u = 0; u < kDepth - 1; ++u)
+            if (i + u < mine)
+                add(s[u]);
+    }
+    if (kBatch * whole < g.K && wave == whole % kWaves) {  // the last k, fewer than 32
+        load(std::false_type{}, s[0], whole);
+        add(s[0]);
     }
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kN; ++j)
 #pragma unroll
             for (int b = 0; b < kRB; ++b)
-                join[(((wave * 2 + m) * 4 + j) * kRB + b) * 64 + lane] = acc[m][j][b];
+                join[(((wave * 2 + m) * kN + j) * kRB + b) * 64 + lane] = acc[m][j][b];
     __syncthreads();
     const DropKey key = drop_key(e.drop);
-    // a lane's 16 columns of a row (register r, operand j: column 4 r + j) in two runs of 8
-    for (int u = tid; u < 128 * kRB; u += 64 * kWaves) {
-        const int h = u & 1, l = (u >> 1) & 63, b = u >> 7;
-        const int row = 16 * b + (l & 15), c = n0 + 16 * (l >> 4) + 8 * h;
+    // a lane's columns of a row: operand j, register r is column kN r + j
+    for (int u = tid; u < 64 * kRuns * kRB; u += 64 * kWaves) {
+        const int h = u % kRuns, l = u / kRuns % 64, b = u / (64 * kRuns);
+        const int row = 16 * b + (l & 15), c = n0 + 4 * kN * (l >> 4) + 8 * h;
         if (row >= e.M || c >= e.N)
             continue;
         float v[2][8] = {};
@@ -168,17 +214,13 @@ __global__ __launch_bounds__(64 * kWaves, sizeof(T) == 2 && kRB == 1 ? 2 : 1) vo
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float* p = reinterpret_cast<const float*>(&join[(((w * 2 + m) * 4 + j) * kRB + b) * 64 + l]) + 2 * h;
-                    v[m][j] += p[0];
-                    v[m][4 + j] += p[1];
+                for (int j = 0; j < kN; ++j) {
+                    const float* p = reinterpret_cast<const float*>(&join[(((w * 2 + m) * kN + j) * kRB + b) * 64 + l]);
+#pragma unroll
+                    for (int r = 0; r < 8 / kN; ++r)
+                        v[m][kN * r + j] += p[8 / kN * h + r];
                 }
-        if (e.partial != nullptr) {
-            store8(partial_at(e, part, 0, row, c), v[0], 8);
-            store8(partial_at(e, part, 1, row, c), v[1], 8);
-        } else {
-            finish8<kEpi, sizeof(T) == 4>(e, key, v[0], v[1], 0, row, c);
-        }
+        finish8<kEpi, sizeof(T) == 4>(e, key, v[0], v[1], 0, row, c);
     }
 }
 
@@ -217,33 +259,34 @@ __global__ __launch_bounds__(256) void gated_finish_kernel(EpiArgs e, Divisor gr
     finish8<kEpi, kF32>(e, key, v[0], v[1], mat, row, col);
 }
 
-template <class T, int kRB, int kWaves, int kEpi>
+template <class T, int kN, int kRB, int kWaves, int kDepth, int kEpi>
 hipError_t launch_rows(const RowsArgs& g, hipStream_t s)
 {
-    constexpr int kLds = kWaves * kRB * 8 * 64 * 16;
+    constexpr int kLds = kWaves * kRB * 2 * kN * 64 * 16;
     static LdsLimit limit;
-    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gated_rows_kernel<T, kRB, kWaves, kEpi>), kLds);
+    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gated_rows_kernel<T, kN, kRB, kWaves, kDepth, kEpi>), kLds);
         e != hipSuccess)
         return e;
-    const dim3 grid(static_cast<unsigned>(ceil_div(g.e.N, kCols)), g.e.parts);
-    gated_rows_kernel<T, kRB, kWaves, kEpi><<<grid, 64 * kWaves, kLds, s>>>(g);
+    const dim3 grid(static_cast<unsigned>(ceil_div(g.e.N, 16 * kN)));
+    gated_rows_kernel<T, kN, kRB, kWaves, kDepth, kEpi><<<grid, 64 * kWaves, kLds, s>>>(g);
     return hipGetLastError();
 }
 
+// Waves per workgroup and steps in flight: what registers (sums 8 kN kRB, a step 4 kN sizeof(T) + 4 kRB or 8 kRB) and
+// LDS (2 kN kRB KiB a wave) leave.
 template <class T, int kEpi>
 hipError_t launch_blocks(const RowsArgs& g, hipStream_t s)
 {
-    return g.e.M <= 16 ? launch_rows<T, 1, 8, kEpi>(g, s) : g.e.M <= 32 ? launch_rows<T, 2, 8, kEpi>(g, s)
-                                                                     : launch_rows<T, 4, 4, kEpi>(g, s);
+    constexpr bool kShort = sizeof(T) == 2;
+    if (ceil_div(g.e.N, 64) >= 128)
+        return g.e.M <= 16 ? launch_rows<T, 4, 1, 8, 2, kEpi>(g, s) : g.e.M <= 32 ? launch_rows<T, 4, 2, 8, 2, kEpi>(g, s)
+                                                                             : launch_rows<T, 4, 4, 4, 2, kEpi>(g, s);
+    return g.e.M <= 16   ? launch_rows<T, 2, 1, 8, kShort ? 6 : 3, kEpi>(g, s)
+           : g.e.M <= 32 ? launch_rows<T, 2, 2, 8, kShort ? 4 : 2, kEpi>(g, s)
+                         : launch_rows<T, 2, 4, kShort ? 8 : 4, 3, kEpi>(g, s);
 }
 
 }  // namespace
-
-int gated_rows_parts(int64_t M, int64_t K, int64_t N)
-{
-    const int64_t tiles = ceil_div(N, kCols), waves = M <= 32 ? 8 : 4;
-    return tiles >= 128 ? 1 : static_cast<int>(std::clamp<int64_t>(256 / tiles, 1, std::max<int64_t>(1, ceil_div(K, kBatch) / waves)));
-}
 
 hipError_t launch_gated_rows(Epi epi, int dtype, const RowsArgs& g, hipStream_t s)
 {

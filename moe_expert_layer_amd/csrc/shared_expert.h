@@ -91,7 +91,7 @@ constexpr int kMaxRank = 128;
 // adapter.hip: out = base + each row's adapter (moe_adapter_add).
 struct AdapterLayout {
     size_t count = 0, perm = 0, tiles = 0;   // the rows sorted by adapter
-    size_t v = 0;                            // x A, float32 partial sums
+    size_t v = 0, part = 0;                  // x A, and its sums over parts of K
     size_t total = 0;
 };
 AdapterLayout adapter_layout(const moe_adapter& p);

@@ -87,12 +87,12 @@ __device__ __forceinline__ u32x4_t pack8_bf16(const float (&v)[8])
     return u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
 }
 
-// Writes the first n of eight values, rounded to T.
-template <class T>
+// Writes the first n of eight values, rounded to T.  kWhole: n is at least 8.
+template <class T, bool kWhole = false>
 __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n)
 {
     if constexpr (sizeof(T) == 2) {
-        if (n >= 8) {
+        if (kWhole || n >= 8) {
             *reinterpret_cast<u32x4_any_t*>(p) = pack8_bf16(v);
             return;
         }
@@ -101,7 +101,7 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8], int n)
             if (i < n)
                 p[i] = f32_to_bf16(v[i]);
     } else {
-        if (n >= 8) {
+        if (kWhole || n >= 8) {
             reinterpret_cast<f32x4_any_t*>(p)[0] = f32x4_t{v[0], v[1], v[2], v[3]};
             reinterpret_cast<f32x4_any_t*>(p)[1] = f32x4_t{v[4], v[5], v[6], v[7]};
             return;

@@ -4,14 +4,14 @@ hold the kernels to.  Tensors of any device; the results are float64 on that dev
 Bounds.  A sum of K products of float32 or bfloat16 values, taken in float32 in any order, is off by at most
 K 2^-23 sum|a b| (each addition rounds to, or truncates at, one part in 2^23 of a partial sum, which sum|a b| bounds;
 bfloat16 products are exact, float32 ones lose at most 2^-23 more): ``sum_error``.  Functions of one value are taken to
-FUNCTION relative error (exponential and reciprocal of 1 ulp each, the argument's own rounding: below 2^-19 while the
-exponent stays below 2^7).  One final rounding adds half a step of the output's type."""
+FUNCTION relative error: float32 a few roundings and fits of 3e-7, bfloat16 an exponential whose argument, below 2^7, is off
+by 2^-24 of itself.  One final rounding adds half a step of the output's type."""
 import math
 
 import torch
 
 HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
-FUNCTION = 2.0 ** -19
+FUNCTION = {torch.bfloat16: 2.0 ** -16, torch.float32: 2.0 ** -20}
 
 
 def sum_error(K, magnitude):
@@ -69,20 +69,21 @@ def activation(g, act):
 
 def gated(x, wg, wu, act, mask=None):
     """(h, its bound without the final rounding, g, u, their bounds)."""
+    function = FUNCTION[x.dtype]
     x, wg, wu = x.double(), wg.double(), wu.double()
     K = x.shape[1]
     g, u = x @ wg, x @ wu
     eg, eu = sum_error(K, x.abs() @ wg.abs()), sum_error(K, x.abs() @ wu.abs())
     a, slope = activation(g, act)
     # slopes vary by less than 1.2 per unit of g, and eg is far below one unit
-    ea = (slope.abs() + 1.2 * eg) * eg + FUNCTION * (a.abs() + eg)
+    ea = (slope.abs() + 1.2 * eg) * eg + function * (a.abs() + eg)
     eh = ea * (u.abs() + eu) + a.abs() * eu
     return drop(a * u, mask), drop(eh, mask), g, u, eg, eu
 
 
 def gated_backward(x, wg, wu, dh, act, mask=None, saved=None):
     """((dx, dwg, dwu), their bounds without the final rounding) for operands of x's type."""
-    half = HALF_STEP[x.dtype]
+    half, function = HALF_STEP[x.dtype], FUNCTION[x.dtype]
     x, wg, wu = x.double(), wg.double(), wu.double()
     K = x.shape[1]
     if saved is None:
@@ -95,7 +96,7 @@ def gated_backward(x, wg, wu, dh, act, mask=None, saved=None):
     a, slope = activation(g, act)
     dg, du = d * u * slope, d * a
     # the second derivatives of the three activations stay below 1.2
-    eslope, ea = 1.2 * eg + FUNCTION * (1 + g.abs()), (slope.abs() + 1.2 * eg) * eg + FUNCTION * (a.abs() + eg)
+    eslope, ea = 1.2 * eg + function * (1 + g.abs()), (slope.abs() + 1.2 * eg) * eg + function * (a.abs() + eg)
     edg = d.abs() * ((u.abs() + eu) * eslope + eu * slope.abs()) + 2 * half * dg.abs()
     edu = d.abs() * ea + 2 * half * du.abs()
     F, T = wg.shape[1], x.shape[0]
