@@ -426,9 +426,9 @@ moe_status moe_dropout(const void* x, const void* residual, int32_t dtype, int64
  * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2. */
 enum moe_activation_code { MOE_ACT_SILU = 0, MOE_ACT_GELU = 1, MOE_ACT_GELU_TANH = 2 };
 typedef struct moe_gated {
-    int64_t T;            /* tokens, below 2^31                                                  */
+    int64_t T;            /* tokens, at most 2^28                                                */
     int64_t H;            /* width of x, at most MOE_MAX_HIDDEN                                  */
-    int64_t F;            /* width of h, at most MOE_MAX_HIDDEN; T H, T F and H F at most 2^40   */
+    int64_t F;            /* width of h, at most MOE_MAX_HIDDEN; T H, T F and H F at most 2^37   */
     int32_t dtype;        /* MOE_F32 or MOE_BF16                                                 */
     int32_t activation;   /* enum moe_activation_code                                            */
     double dropout;       /* p in [0, 1]                                                         */
@@ -466,7 +466,7 @@ moe_status moe_gated_projection_backward(const moe_gated* g, const void* x, cons
  * base[t].  x A is a float32 sum, kept to 16 bits (MOE_BF16) or 24 (MOE_F32) for the second product.  out
  * may be base; no other buffers may overlap it. */
 typedef struct moe_adapter {
-    int64_t T;            /* rows, below 2^31                                                    */
+    int64_t T;            /* rows, at most 2^28                                                  */
     int64_t K;            /* width of x, at most MOE_MAX_HIDDEN                                  */
     int64_t N;            /* width of base and out, at most MOE_MAX_HIDDEN                       */
     int64_t L;            /* adapters, 1 .. 1023                                                 */

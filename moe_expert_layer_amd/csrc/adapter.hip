@@ -3,8 +3,8 @@
 //
 // Memory is what bounds it: x and base once, out once, each used adapter's A and B once; the products are R operations a
 // byte.  Two ways:
-//   - few rows (row_kernel): one launch, a workgroup per (row, run of output columns).  Each computes its row's v for
-//     itself, which reads the adapter's A again from the L2 but saves a launch and a pass through memory;
+//   - few rows (row_kernel; rule in plan()): one launch, a workgroup per (row, run of output columns).  Each computes its
+//     row's v for itself, which reads the adapter's A again from the L2 but saves a launch and a pass through memory;
 //   - many rows: the rows are sorted by adapter into tiles of up to 64 (plan_kernel, one workgroup), then v and v B run
 //     on the matrix cores, tile by tile (shrink_kernel, expand_kernel).  x goes from memory to the MFMA's registers, the
 //     adapter's matrices through LDS; K is cut so that there are workgroups enough, and join_kernel adds the cuts' float32
@@ -42,18 +42,67 @@ struct Args {
 
 __device__ __forceinline__ int rank_of(const Args& g, int a) { return g.ranks == nullptr ? g.R : min(max(g.ranks[a], 0), g.R); }
 
+// Eight values of A from `at` on (values from the tensor's start): what lies past the row belongs to columns that nobody
+// reads, and only past the tensor's end (total values, at least 8) the last eight are read and shifted into place.
+template <class T>
+__device__ __forceinline__ Raw8<T> load_a(const T* a, int64_t at, int64_t total)
+{
+    return load_raw<true>(a + min(at, total - 8), 8);
+}
+__device__ __forceinline__ void shift_a(Raw8<uint16_t>& r, int skip)
+{
+    u32x4_t v = r.w;
+    for (int i = 0; i < skip; ++i)
+        v = u32x4_t{__builtin_amdgcn_alignbit(v[1], v[0], 16), __builtin_amdgcn_alignbit(v[2], v[1], 16),
+                    __builtin_amdgcn_alignbit(v[3], v[2], 16), v[3] >> 16};
+    r.w = v;
+}
+__device__ __forceinline__ void shift_a(Raw8<float>& r, int skip)
+{
+    for (int i = 0; i < skip; ++i) {
+        r.a = f32x4_t{r.a[1], r.a[2], r.a[3], r.b[0]};
+        r.b = f32x4_t{r.b[1], r.b[2], r.b[3], 0.0f};
+    }
+}
+// Whether loads of an adapter's A may pass the tensor's end: the last adapter, with rows that are not whole runs of eight.
+__device__ __forceinline__ bool past_end(const Args& g, int a) { return a == g.L - 1 && g.R % 8 != 0; }
+
+// Writes eight columns [from, from + 8) of a row, those before `first` left out (they are another thread's).
+template <class T>
+__device__ __forceinline__ void store_from(T* row, int from, int first, const float (&v)[8])
+{
+    if (from == first) {
+        store8<T, true>(row + from, v, 8);
+        return;
+    }
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+        if (from + i >= first) {
+            if constexpr (sizeof(T) == 2)
+                row[from + i] = f32_to_bf16(v[i]);
+            else
+                row[from + i] = v[i];
+        }
+}
+
 // ------------------------------------------------------------------------------------------------ few rows
 
 constexpr int kRowThreads = 1024;         // 16 waves: a CU has one or two of these workgroups, and 128 KiB in flight
 constexpr int kRowWaves = kRowThreads / 64;
+// Rows up to which row_kernel is taken.  8 x 128 -> 128: 512 rows 13 us against 23 and three more launches, 2048 rows 49
+// against 23; 16 x 4096 -> 4096: 1000 rows 31 against 28.  Its reads of A and B count too, see plan(): 300 rows of rank 64,
+// 300 MiB, 36 us against 26.
+constexpr int64_t kMaxRowTokens = 1024;
+constexpr int64_t kMaxRowReads = int64_t{256} << 20;
 
 // Workgroup (t, c): row t, output columns [c cols, (c + 1) cols).  Threads take (k, 8 columns of A) and add over k, then
 // (r, 8 columns of B) and add over r; both are joined in a fixed order, within the wave and then through LDS.  Loads go
-// out in batches, and what does not wait for v (the first rows of B, base) at the start.
-template <class T, bool kWhole>
+// out in batches, and what does not wait for v (the first rows of B, base) at the start.  A run of 8 columns that would
+// pass the row's end is the row's last 8.
+template <class T>
 __global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
 {
-    constexpr int kBatch = 8;
+    constexpr int kBatch = sizeof(T) == 2 ? 8 : 4;         // 128 registers a thread
     __shared__ float part[kRowThreads * 8];
     __shared__ float v[kMaxRank];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -68,8 +117,9 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
         if (g.base != g.out)
             for (int n = n0 + 8 * tid; n < n1; n += 8 * kRowThreads) {
                 float w[8];
-                load8(w, base + n, n1 - n);
-                store8(out + n, w, n1 - n);
+                const int from = min(n, g.N - 8);
+                load_raw<true>(base + from, 8).values(w);
+                store_from(out, from, n, w);
             }
         return;
     }
@@ -77,35 +127,40 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
     // threads per run of 8 output columns: as many as the run of columns leaves, at most the rank
     const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(a) * g.R * g.N;
     const int runs = min(kRowThreads, (n1 - n0 + 7) / 8), lanes = max(1, min(rank, kRowThreads / runs));
-    const int q = tid % runs, rr = tid / runs;
-    const int left0 = n1 - n0 - 8 * q;
-    Raw8<T> b0 = load_raw<kWhole>(B + static_cast<int64_t>(rr) * g.N + n0 + 8 * q, rr < lanes ? left0 : 0);
-    Raw8<T> base0 = load_raw<kWhole>(base + n0 + 8 * q, rr == 0 ? left0 : 0);
+    const int q = tid % runs, rr = min(tid / runs, lanes);
+    const int first = n0 + 8 * q, from0 = min(first, g.N - 8);
+    Raw8<T> b0 = load_raw<true>(B + static_cast<int64_t>(min(rr, rank - 1)) * g.N + from0, 8);
+    Raw8<T> base0 = load_raw<true>(base + from0, 8);
     {
         const T* const x = static_cast<const T*>(g.x) + t * g.K;
-        const T* const A = static_cast<const T*>(g.a) + static_cast<int64_t>(a) * g.K * g.R;
+        const T* const A = static_cast<const T*>(g.a);
+        const int64_t a0 = static_cast<int64_t>(a) * g.K * g.R, total = static_cast<int64_t>(g.L) * g.K * g.R;
         // a power of two of column chunks, so that the lanes of one chunk are whole strides of the wave
         const int bits = rank <= 8 ? 0 : 32 - __clz((rank - 1) >> 3), chunks = 1 << bits;
-        const int c = tid & (chunks - 1), stride = kRowThreads >> bits;
-        const int width = 8 * c < rank ? g.R - 8 * c : 0;
+        const int c = 8 * min(tid & (chunks - 1), (rank - 1) >> 3), stride = kRowThreads >> bits;
         float sum[8] = {};
         for (int k0 = tid >> bits; k0 < g.K; k0 += kBatch * stride) {
             Raw8<T> w[kBatch];
             T xk[kBatch];
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
-                const int k = k0 + i * stride;
-                w[i] = load_raw<kWhole>(A + static_cast<int64_t>(k) * g.R + 8 * c, k < g.K ? width : 0);
-                xk[i] = x[min(k, g.K - 1)];
+                const int k = min(k0 + i * stride, g.K - 1);
+                w[i] = load_a(A, a0 + static_cast<int64_t>(k) * g.R + c, total);
+                xk[i] = x[k];
             }
+            if (past_end(g, a))
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i)
+                    shift_a(w[i], max(0, static_cast<int>(a0 + static_cast<int64_t>(min(k0 + i * stride, g.K - 1)) * g.R + c + 8 - total)));
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 float f[8];
                 w[i].values(f);
-                const float m = k0 + i * stride < g.K ? to_float(xk[i]) : 0.0f;
+                const float m = to_float(xk[i]);
+                if (k0 + i * stride < g.K)
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum[e] = fmaf(m, f[e], sum[e]);
+                    for (int e = 0; e < 8; ++e)
+                        sum[e] = fmaf(m, f[e], sum[e]);
             }
         }
         for (int d = 32; d >= chunks; d >>= 1)
@@ -126,34 +181,33 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
         }
         __syncthreads();
     }
-    for (int first = n0; first < n1; first += 8 * runs) {      // the same number of passes for every thread
-        const int n = first + 8 * q;
+    for (int pass = n0; pass < n1; pass += 8 * runs) {         // the same number of passes for every thread
+        const int n = pass + 8 * q, from = min(n, g.N - 8);
         float sum[8] = {};
         if (rr < lanes && n < n1) {
-            if (first != n0)
-                b0 = load_raw<kWhole>(B + static_cast<int64_t>(rr) * g.N + n, n1 - n);
-            for (int r0 = rr + lanes; ; r0 += kBatch * lanes) {
+            if (pass != n0) {
+                b0 = load_raw<true>(B + static_cast<int64_t>(rr) * g.N + from, 8);
+                base0 = load_raw<true>(base + from, 8);
+            }
+            float f[8];
+            b0.values(f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                sum[e] = v[rr] * f[e];
+            for (int r0 = rr + lanes; r0 < rank; r0 += kBatch * lanes) {
                 Raw8<T> w[kBatch];
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
-                    w[i] = load_raw<kWhole>(B + static_cast<int64_t>(r0 + i * lanes) * g.N + n, r0 + i * lanes < rank ? n1 - n : 0);
-                float f[8];
-                if (r0 == rr + lanes) {                        // the row that was loaded first
-                    b0.values(f);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum[e] = v[rr] * f[e];
-                }
+                    w[i] = load_raw<true>(B + static_cast<int64_t>(min(r0 + i * lanes, rank - 1)) * g.N + from, 8);
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i) {
                     w[i].values(f);
-                    const float m = r0 + i * lanes < rank ? v[r0 + i * lanes] : 0.0f;
+                    const int r = r0 + i * lanes;
+                    if (r < rank)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        sum[e] = fmaf(m, f[e], sum[e]);
+                        for (int e = 0; e < 8; ++e)
+                            sum[e] = fmaf(v[r], f[e], sum[e]);
                 }
-                if (r0 + kBatch * lanes >= rank)
-                    break;
             }
         }
         if (lanes > 1) {
@@ -169,14 +223,50 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
                         sum[i] += part[i * kRowThreads + tid + p * runs];
         }
         if (rr == 0 && n < n1) {
-            if (first != n0)
-                base0 = load_raw<kWhole>(base + n, n1 - n);
             float f[8];
             base0.values(f);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 sum[i] += f[i];
-            store8(out + n, sum, n1 - n);
+            store_from(out, from, n, sum);
+        }
+    }
+}
+
+// Rows of fewer than 8 columns, or fewer than 8 values of A in all: nothing that is read 8 values at a time exists.
+template <class T>
+__global__ __launch_bounds__(kThreads) void narrow_kernel(Args g)
+{
+    __shared__ float part[kThreads], v[kMaxRank];
+    const int tid = threadIdx.x;
+    for (int64_t t = blockIdx.x; t < g.T; t += gridDim.x) {
+        const int a = g.ids[t], rank = a >= 0 && a < g.L ? rank_of(g, a) : 0;
+        const T* const x = static_cast<const T*>(g.x) + t * g.K;
+        for (int r = 0; r < rank; ++r) {
+            const T* const A = static_cast<const T*>(g.a) + static_cast<int64_t>(a) * g.K * g.R + r;
+            float s = 0.0f;
+            for (int k = tid; k < g.K; k += kThreads)
+                s = fmaf(to_float(x[k]), to_float(A[static_cast<int64_t>(k) * g.R]), s);
+            part[tid] = s;
+            for (int d = kThreads / 2; d > 0; d /= 2) {
+                __syncthreads();
+                if (tid < d)
+                    part[tid] += part[tid + d];
+            }
+            if (tid == 0)
+                v[r] = g.scale == nullptr ? part[0] : part[0] * g.scale[a];
+            __syncthreads();
+        }
+        const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(rank > 0 ? a : 0) * g.R * g.N;
+        for (int n = tid; n < g.N; n += kThreads) {
+            float s = 0.0f;
+            for (int r = 0; r < rank; ++r)
+                s = fmaf(v[r], to_float(B[static_cast<int64_t>(r) * g.N + n]), s);
+            s += to_float(static_cast<const T*>(g.base)[t * g.N + n]);
+            if constexpr (sizeof(T) == 2)
+                static_cast<T*>(g.out)[t * g.N + n] = f32_to_bf16(s);
+            else
+                static_cast<T*>(g.out)[t * g.N + n] = s;
         }
     }
 }
@@ -299,7 +389,7 @@ __device__ __forceinline__ void store_v(uint16_t* p, int64_t plane, const float 
 }
 
 // v of a tile's rows over one cut of K.  Waves: 2 row halves of 32 x 2 halves of each K step; kRB column blocks of 32.
-template <class T, int kRB, bool kWhole>
+template <class T, int kRB>
 __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
 {
     constexpr int P = kPlanesOf<T>;
@@ -324,7 +414,8 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
     const bool busy = 32 * wr < n;                        // this wave has rows
     const int row = p.perm[tile.begin + min(32 * wr + (lane & 31), n - 1)];
     const T* const x = static_cast<const T*>(g.x) + static_cast<int64_t>(row) * g.K;
-    const T* const A = static_cast<const T*>(g.a) + static_cast<int64_t>(tile.adapter) * g.K * g.R;
+    const T* const A = static_cast<const T*>(g.a);
+    const int64_t a0 = static_cast<int64_t>(tile.adapter) * g.K * g.R, total = static_cast<int64_t>(g.L) * g.K * g.R;
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(smem)));
 
@@ -332,13 +423,11 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
     // they repeat what is there), each into the registers that its step's predecessor has just left.
     constexpr int kSets = P == 1 ? 2 : 1;
     Raw8<T> xr[kSets][kGroups], ar[kSets][kLoads];
-    const auto fetch_a = [&](Raw8<T>& r, int step, int i, bool partial) {
+    const auto place = [&](int step, int i) {              // of this thread's value i of A in a step, from the tensor's start
         const int c = (tid + i * kThreads) % (kCols / 8), k = step * kStep + (tid + i * kThreads) / (kCols / 8);
-        if (kWhole && !partial)
-            r = load_raw<true>(A + static_cast<int64_t>(k) * g.R + min(8 * c, g.R - 8), 8);
-        else
-            r = load_raw<kWhole>(A + static_cast<int64_t>(k) * g.R + 8 * c, k < g.K ? g.R - 8 * c : 0);
+        return a0 + static_cast<int64_t>(min(k, g.K - 1)) * g.R + min(8 * c, (g.R - 1) / 8 * 8);
     };
+    const auto fetch_a = [&](Raw8<T>& r, int step, int i) { r = load_a(A, place(step, i), total); };
     const auto fetch_x = [&](Raw8<T>& r, int step, int s, bool partial) {
         const int k = step * kStep + (kStep / 2) * wk + 16 * s + 8 * (lane >> 5);
         r = partial ? load_raw<false>(x + k, g.K - k) : load_raw<true>(x + k, 8);
@@ -350,8 +439,12 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
         for (int e = 0; e < 16; ++e)
             acc[j][e] = 0.0f;
     // one step from one set of registers, which then take step `next` (more: there is one)
-    const auto run = [&](auto more, Raw8<T> (&av)[kLoads], Raw8<T> (&xv)[kGroups], int next) {
+    const auto run = [&](auto more, Raw8<T> (&av)[kLoads], Raw8<T> (&xv)[kGroups], int step, int next) {
         constexpr bool kMore = decltype(more)::value;
+        if (past_end(g, tile.adapter))
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+                shift_a(av[i], max(0, static_cast<int>(place(step, i) + 8 - total)));
         __syncthreads();                                  // the stage of the step before is read
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
@@ -360,13 +453,14 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
             planes8(av[i], pl);
 #pragma unroll
             for (int q = 0; q < P; ++q)
-                *reinterpret_cast<u32x4_t*>(smem + q * kPlane + (at / (kCols / 8)) * kRow + 16 * (at % (kCols / 8))) = pl[q];
+                *reinterpret_cast<u32x4_t*>(smem + q * kPlane + (at / (kCols / 8)) * kRow + 16 * (at % (kCols / 8))) =
+                    step * kStep + at / (kCols / 8) < g.K ? pl[q] : u32x4_t{0, 0, 0, 0};
         }
         __syncthreads();
         if constexpr (kMore)
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                fetch_a(av[i], next, i, false);
+                fetch_a(av[i], next, i);
 #pragma unroll
         for (int s = 0; s < kGroups; ++s) {
             u32x4_t xp[P];
@@ -393,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
         for (int u = 0; u < kSets; ++u) {
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                fetch_a(ar[u][i], min(step0 + u, whole1 - 1), i, false);
+                fetch_a(ar[u][i], min(step0 + u, whole1 - 1), i);
 #pragma unroll
             for (int s = 0; s < kGroups; ++s)
                 fetch_x(xr[u][s], min(step0 + u, whole1 - 1), s, false);
@@ -402,18 +496,18 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
         for (; step + kSets <= whole1; step += kSets)
 #pragma unroll
             for (int u = 0; u < kSets; ++u)
-                run(std::true_type{}, ar[u], xr[u], min(step + u + kSets, whole1 - 1));
+                run(std::true_type{}, ar[u], xr[u], step + u, min(step + u + kSets, whole1 - 1));
         if (step < whole1)
-            run(std::false_type{}, ar[0], xr[0], 0);
+            run(std::false_type{}, ar[0], xr[0], step, 0);
     }
     if (whole1 < step1) {
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
-            fetch_a(ar[0][i], whole1, i, true);
+            fetch_a(ar[0][i], whole1, i);
 #pragma unroll
         for (int s = 0; s < kGroups; ++s)
             fetch_x(xr[0][s], whole1, s, true);
-        run(std::false_type{}, ar[0], xr[0], 0);
+        run(std::false_type{}, ar[0], xr[0], whole1, 0);
     }
     // the two K halves join through LDS
     __syncthreads();
@@ -527,17 +621,17 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
         int64_t at[4];                                    // rows past the last repeat it and are not written
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            at[i] = static_cast<int64_t>(p.perm[tile.begin + min(row0 + 16 * i, n - 1)]) * g.N + col;
-        const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(tile.adapter) * g.R * g.N + col;
+            at[i] = static_cast<int64_t>(p.perm[tile.begin + min(row0 + 16 * i, n - 1)]) * g.N;
+        const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(tile.adapter) * g.R * g.N;
         Raw8<T> bv[kLoads], base[4];
         const auto fetch = [&](int c0) {
-            const int left = g.N - c0 - col;
+            const int from = min(c0 + col, g.N - 8);      // the row's last 8 columns where these would pass its end
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                bv[i] = load_raw<false>(B + static_cast<int64_t>(min(row0 + 16 * i, rank - 1)) * g.N + c0, left);
+                bv[i] = load_raw<true>(B + static_cast<int64_t>(min(row0 + 16 * i, rank - 1)) * g.N + from, 8);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                base[i] = load_raw<false>(static_cast<const T*>(g.base) + at[i] + c0, left);
+                base[i] = load_raw<true>(static_cast<const T*>(g.base) + at[i] + from, 8);
         };
         fetch(n0);
         // v of the tile's rows (once the tile before is done with its own)
@@ -603,7 +697,7 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
                 for (int e = 0; e < 8; ++e)
                     sum[e] += u[e];
                 if (row0 + 16 * i < n && c0 + col < g.N)
-                    store8(static_cast<T*>(g.out) + at[i] + c0, sum, g.N - c0 - col);
+                    store_from(static_cast<T*>(g.out) + at[i], min(c0 + col, g.N - 8), c0 + col, sum);
             }
             // the next run's values are loaded when their registers are free: copying them would wait for the loads
             __builtin_amdgcn_sched_barrier(0);
@@ -617,6 +711,7 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
 
 // How a call runs.
 struct Plan {
+    bool narrow;              // narrow_kernel
     bool rows;                // row_kernel
     int cols;                 // row_kernel: output columns per workgroup
     int blocks;               // column blocks of 32 that hold the rank (1, 2 or 4)
@@ -628,7 +723,11 @@ Plan plan(const moe_adapter& p)
 {
     Plan q{};
     const int64_t size = p.dtype == MOE_F32 ? 4 : 2;
-    q.rows = p.K * p.R * size <= (int64_t{1} << 20) && p.T * (p.K + p.N) * p.R * size <= (int64_t{384} << 20);
+    q.narrow = p.N < 8 || p.L * p.K * p.R < 8;
+    if (q.narrow)
+        return q;
+    q.rows = p.T <= kMaxRowTokens && p.K * p.R * size <= (int64_t{1} << 20) &&
+             p.T * (p.K + p.N) * p.R * size <= kMaxRowReads;
     if (q.rows) {
         // about 256 workgroups, 64 columns at least
         const int64_t per_row = std::clamp<int64_t>(ceil_div(256, std::max<int64_t>(p.T, 1)), 1, ceil_div(p.N, 64));
@@ -643,9 +742,7 @@ Plan plan(const moe_adapter& p)
     return q;
 }
 
-bool whole(const moe_adapter& p) { return p.K % 8 == 0 && p.N % 8 == 0 && p.R % 8 == 0; }
-
-template <class T, int kRB, bool kWhole>
+template <class T, int kRB>
 hipError_t launch_tiles(const Args& g, const TileArgs& t, const Plan& q, hipStream_t s)
 {
     constexpr int kExpandLds = ExpandLds<T, kRB>::kBytes;
@@ -653,7 +750,7 @@ hipError_t launch_tiles(const Args& g, const TileArgs& t, const Plan& q, hipStre
     if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&expand_kernel<T, kRB>), kExpandLds); e != hipSuccess)
         return e;
     const unsigned tiles = static_cast<unsigned>(q.max_tiles);
-    shrink_kernel<T, kRB, kWhole><<<dim3(tiles, q.splits), kThreads, 0, s>>>(g, t);
+    shrink_kernel<T, kRB><<<dim3(tiles, q.splits), kThreads, 0, s>>>(g, t);
     if (hipError_t e = hipGetLastError(); e != hipSuccess)
         return e;
     if (t.splits > 1) {
@@ -671,12 +768,13 @@ template <class T>
 hipError_t launch(const moe_adapter& p, const Args& g, unsigned char* ws, hipStream_t s)
 {
     const Plan q = plan(p);
+    if (q.narrow) {
+        narrow_kernel<T><<<dim3(static_cast<unsigned>(std::min<int64_t>(p.T, 65536))), kThreads, 0, s>>>(g);
+        return hipGetLastError();
+    }
     if (q.rows) {
         const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>(ceil_div(p.N, q.cols)));
-        if (whole(p))
-            row_kernel<T, true><<<grid, kRowThreads, 0, s>>>(g, q.cols);
-        else
-            row_kernel<T, false><<<grid, kRowThreads, 0, s>>>(g, q.cols);
+        row_kernel<T><<<grid, kRowThreads, 0, s>>>(g, q.cols);
         return hipGetLastError();
     }
     const AdapterLayout L = adapter_layout(p);
@@ -688,13 +786,8 @@ hipError_t launch(const moe_adapter& p, const Args& g, unsigned char* ws, hipStr
         return e;
     const TileArgs t{tiles, count, perm, reinterpret_cast<float*>(ws + L.part), reinterpret_cast<uint16_t*>(ws + L.v), q.splits,
                      q.steps};
-    // ranks of whole runs of eight values need no code for a run that ends early
-    const auto by_blocks = [&](auto whole) {
-        constexpr bool kWhole = decltype(whole)::value;
-        return q.blocks == 1 ? launch_tiles<T, 1, kWhole>(g, t, q, s) : q.blocks == 2 ? launch_tiles<T, 2, kWhole>(g, t, q, s)
-                                                                                     : launch_tiles<T, 4, kWhole>(g, t, q, s);
-    };
-    return p.R % 8 == 0 ? by_blocks(std::true_type{}) : by_blocks(std::false_type{});
+    return q.blocks == 1 ? launch_tiles<T, 1>(g, t, q, s) : q.blocks == 2 ? launch_tiles<T, 2>(g, t, q, s)
+                                                                         : launch_tiles<T, 4>(g, t, q, s);
 }
 
 }  // namespace
@@ -703,7 +796,7 @@ AdapterLayout adapter_layout(const moe_adapter& p)
 {
     AdapterLayout L;
     const Plan q = plan(p);
-    if (q.rows)
+    if (q.narrow || q.rows)
         return L;
     size_t off = 0;
     const auto take = [&](size_t& at, size_t bytes) {

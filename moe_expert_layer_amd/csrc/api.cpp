@@ -1562,11 +1562,11 @@ moe_status check_gated(const moe_gated* g)
         return fail(MOE_ERR_INVALID_ARGUMENT, "gated is null");
     if (g->T < 0 || g->H <= 0 || g->F <= 0)
         return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0, H and F positive");
-    if (g->T > INT32_MAX || g->H > MOE_MAX_HIDDEN || g->F > MOE_MAX_HIDDEN)
-        return fail(MOE_ERR_UNSUPPORTED, "T must be below 2^31, H and F at most %d", MOE_MAX_HIDDEN);
-    // the tiles of every product can then be numbered in 32 bits
-    if (std::max({g->T * g->H, g->T * g->F, g->H * g->F}) > int64_t{1} << 40)
-        return fail(MOE_ERR_UNSUPPORTED, "T * H, T * F and H * F must be at most 2^40");
+    if (g->T > kMaxSharedRows || g->H > MOE_MAX_HIDDEN || g->F > MOE_MAX_HIDDEN)
+        return fail(MOE_ERR_UNSUPPORTED, "T must be at most 2^28, H and F at most %d", MOE_MAX_HIDDEN);
+    // the threads of every product then number fewer than 2^32
+    if (std::max({g->T * g->H, g->T * g->F, g->H * g->F}) > int64_t{1} << 37)
+        return fail(MOE_ERR_UNSUPPORTED, "T * H, T * F and H * F must be at most 2^37");
     if (g->activation != MOE_ACT_SILU && g->activation != MOE_ACT_GELU && g->activation != MOE_ACT_GELU_TANH)
         return fail(MOE_ERR_INVALID_ARGUMENT, "unknown activation %d", g->activation);
     if (!(g->dropout >= 0.0 && g->dropout <= 1.0))
@@ -1592,8 +1592,8 @@ moe_status check_adapter(const moe_adapter* p)
         return fail(MOE_ERR_INVALID_ARGUMENT, "reserved not 0");
     if (p->T < 0 || p->K <= 0 || p->N <= 0 || p->L <= 0 || p->R <= 0)
         return fail(MOE_ERR_INVALID_ARGUMENT, "T must be >= 0, K, N, L and R positive");
-    if (p->T > INT32_MAX || p->K > MOE_MAX_HIDDEN || p->N > MOE_MAX_HIDDEN || p->L > kMaxAdapters || p->R > kMaxRank)
-        return fail(MOE_ERR_UNSUPPORTED, "T must be below 2^31, K and N at most %d, L at most %d, R at most %d", MOE_MAX_HIDDEN,
+    if (p->T > kMaxSharedRows || p->K > MOE_MAX_HIDDEN || p->N > MOE_MAX_HIDDEN || p->L > kMaxAdapters || p->R > kMaxRank)
+        return fail(MOE_ERR_UNSUPPORTED, "T must be at most 2^28, K and N at most %d, L at most %d, R at most %d", MOE_MAX_HIDDEN,
                     kMaxAdapters, kMaxRank);
     return check_plain_dtype(p->dtype);
 }

@@ -646,8 +646,9 @@ GatedLayout gated_layout(const moe_gated& g, bool backward)
         take(L.dgu, 2 * 2 * P * g.T * own_ld(g.F));
     int64_t partial = 0;                                  // of one product after the other
     if (g.T > 0) {
-        if (!rows)
-            partial = partial_bytes(g.T, g.F, 2, products * ceil_div(g.H, kBK));
+        const int64_t parts = rows ? gated_rows_parts(g.dtype, g.T, g.H, g.F) : 1;
+        partial = !rows ? partial_bytes(g.T, g.F, 2, products * ceil_div(g.H, kBK))
+                        : parts > 1 ? 4 * 2 * parts * g.T * padded(g.F) : 0;
         if (backward) {
             partial = std::max(partial, partial_bytes(g.T, g.H, 1, 2 * products * ceil_div(g.F, kBK)));
             partial = std::max(partial, partial_bytes(g.H, g.F, 2, products * ceil_div(g.T, kBK)));
@@ -682,8 +683,13 @@ hipError_t launch_gu(const moe_gated& q, const void* x, const void* wg, const vo
     e.N = static_cast<int>(q.F);
     e.mats = 2;
     e.act = q.activation;
-    if (few_rows(q))
-        return launch_gated_rows(static_cast<Epi>(kEpi), q.dtype, RowsArgs{x, wg, wu, static_cast<int>(q.H), e}, s);
+    if (few_rows(q)) {
+        e.parts = gated_rows_parts(q.dtype, q.T, q.H, q.F);
+        e.partial = e.parts > 1 ? partial : nullptr;
+        e.ld_part = static_cast<int>(padded(q.F));
+        const hipError_t err = launch_gated_rows(static_cast<Epi>(kEpi), q.dtype, RowsArgs{x, wg, wu, static_cast<int>(q.H), e}, s);
+        return err != hipSuccess || e.parts == 1 ? err : launch_gated_finish(static_cast<Epi>(kEpi), q.dtype, e, s);
+    }
     GemmArgs g{};
     g.a = p.x.p;
     g.b0 = p.wg.p;

@@ -180,6 +180,8 @@ struct RowsArgs {
     EpiArgs e;
 };
 constexpr int kMaxRows = 64, kMinCols = 4;   // at most, at least
+// Parts of K that the kernel takes (1: it writes the results itself; otherwise partial sums).
+int gated_rows_parts(int dtype, int64_t M, int64_t K, int64_t N);
 hipError_t launch_gated_rows(Epi epi, int dtype, const RowsArgs& g, hipStream_t s);
 // The results from partial sums (EpiArgs.partial).
 hipError_t launch_gated_finish(Epi epi, int dtype, const EpiArgs& e, hipStream_t s);

@@ -8,9 +8,9 @@
 // columns a lane, two operands, 8 columns).  float32: the words are
 // v_mfma_f32_16x16x4_f32 operands as they are, eight of one k per lane group, exact products.  Nothing of the weights goes
 // through LDS, and rows of any width and alignment are read the same way.
-// A workgroup takes 64 columns of both matrices, or 32 where 64 would leave half of the CUs without work; its waves take K
-// in turn, 32 rows at a time with the next 32 in flight, and join their sums through LDS in a fixed order.  K is not cut
-// over workgroups: joining them would take a second launch (7 us) and saves less than that.
+// A workgroup takes 64 or 32 columns of both matrices; its waves take K in turn, 32 rows at a time with more of them in
+// flight, and join their sums through LDS in a fixed order.  One CU moves 70 GB/s with 128-byte rows, 35 with 64-byte ones:
+// where the columns give few workgroups, K is cut over workgroups too, which costs a second launch (plan).
 #include <algorithm>
 
 #include "gated_epilogue.h"
@@ -120,7 +120,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_rows_kernel(RowsArgs g)
     const EpiArgs& e = g.e;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 16 * kN;
+    const int n0 = blockIdx.x * 16 * kN, part = blockIdx.y;
     // A lane whose kN columns pass the row's end reads the row's last kN (skip > 0: the first of them belong to lanes
     // before it); in the last workgroup alone, whose lanes shift them into place.
     const int kg = 8 * (lane >> 4), col = n0 + kN * (lane & 15), from = min(col, e.N - kN), skip = col - from;
@@ -170,19 +170,22 @@ __global__ __launch_bounds__(64 * kWaves) void gated_rows_kernel(RowsArgs g)
         multiply<T, kN, kRB>(acc, s);
         __builtin_amdgcn_sched_barrier(0);                 // the next loads go out when these registers are free
     };
-    // this wave's whole steps: wave, wave + kWaves, ..; kDepth of them in flight
-    const int whole = g.K / kBatch, mine = whole > wave ? (whole - wave + kWaves - 1) / kWaves : 0;
+    // this wave's whole steps of the workgroup's part of K: first, first + kWaves, ..; kDepth of them in flight
+    const int whole = g.K / kBatch;
+    const int step0 = static_cast<int>(static_cast<int64_t>(whole) * part / e.parts);
+    const int step1 = static_cast<int>(static_cast<int64_t>(whole) * (part + 1) / e.parts);
+    const int first = step0 + wave, mine = step1 > first ? (step1 - first + kWaves - 1) / kWaves : 0;
     Step<T, kN, kRB> s[kDepth];
     if (mine > 0) {
 #pragma unroll
         for (int u = 0; u < kDepth; ++u)
-            load(std::true_type{}, s[u], wave + kWaves * min(u, mine - 1));
+            load(std::true_type{}, s[u], first + kWaves * min(u, mine - 1));
         int i = 0;
         for (; i + kDepth <= mine; i += kDepth)
 #pragma unroll
             for (int u = 0; u < kDepth; ++u) {
                 add(s[u]);
-                load(std::true_type{}, s[u], wave + kWaves * min(i + u + kDepth, mine - 1));
+                load(std::true_type{}, s[u], first + kWaves * min(i + u + kDepth, mine - 1));
                 __builtin_amdgcn_sched_barrier(0);
             }
 #pragma unroll
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(64 * kWaves) void gated_rows_kernel(RowsArgs g)
             if (i + u < mine)
                 add(s[u]);
     }
-    if (kBatch * whole < g.K && wave == whole % kWaves) {  // the last k, fewer than 32
+    if (kBatch * whole < g.K && part == e.parts - 1 && wave == (step1 - step0) % kWaves) {   // the last k, fewer than 32
         load(std::false_type{}, s[0], whole);
         add(s[0]);
     }
@@ -220,7 +223,12 @@ __global__ __launch_bounds__(64 * kWaves) void gated_rows_kernel(RowsArgs g)
                     for (int r = 0; r < 8 / kN; ++r)
                         v[m][kN * r + j] += p[8 / kN * h + r];
                 }
-        finish8<kEpi, sizeof(T) == 4>(e, key, v[0], v[1], 0, row, c);
+        if (e.partial != nullptr) {
+            store8<float, true>(partial_at(e, part, 0, row, c), v[0], 8);
+            store8<float, true>(partial_at(e, part, 1, row, c), v[1], 8);
+        } else {
+            finish8<kEpi, sizeof(T) == 4>(e, key, v[0], v[1], 0, row, c);
+        }
     }
 }
 
@@ -267,9 +275,41 @@ hipError_t launch_rows(const RowsArgs& g, hipStream_t s)
     if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gated_rows_kernel<T, kN, kRB, kWaves, kDepth, kEpi>), kLds);
         e != hipSuccess)
         return e;
-    const dim3 grid(static_cast<unsigned>(ceil_div(g.e.N, 16 * kN)));
+    const dim3 grid(static_cast<unsigned>(ceil_div(g.e.N, 16 * kN)), g.e.parts);
     gated_rows_kernel<T, kN, kRB, kWaves, kDepth, kEpi><<<grid, 64 * kWaves, kLds, s>>>(g);
     return hipGetLastError();
+}
+
+struct Plan {
+    int n, parts;                                          // columns per lane (4 or 2), parts of K
+};
+
+// The shortest time of the ways there are, in us, from measured rates: a workgroup moves 70 KB (n = 4) or 35 KB (n = 2) a
+// us, 35 KB or 26 KB with more than 32 rows, and, float32, adds 0.45 TFLOP/s in blocks of 16 rows, the chip moves 5.1 MB a
+// us; a launch takes 4, a second one with its passes over the parts' sums 6 and 3 MB a us.  (16 x 8192 x 128 in one part 30
+// us, 63 x 5578 x 512 in float32 94; 33 x 2048 x 768 with n = 4 20 us, with n = 2 14 us.)
+Plan plan(int64_t M, int64_t K, int64_t N, int64_t size)
+{
+    Plan best{};
+    double time = 1e30;
+    const double rows = M <= 16 ? 16.0 : M <= 32 ? 32.0 : 64.0;
+    for (int n : {4, 2})
+        for (int p = 1; p <= 16 && (p == 1 || K / p >= 256); ++p) {
+            const double groups = static_cast<double>(ceil_div(N, 16 * n) * p), k = static_cast<double>(K) / p;
+            const double rate = M <= 32 ? (n == 4 ? 70e3 : 35e3) : (n == 4 ? 35e3 : 26e3);
+            double one = k * 32.0 * n * static_cast<double>(size) / rate;
+            if (size == 4)
+                one = std::max(one, rows * k * 64.0 * n / 0.45e6);
+            const double rounds = std::max(1.0, groups / 256.0);
+            double t = 4.0 + std::max(one * rounds, 2.0 * static_cast<double>(K * N * size) / 5.1e6);
+            if (p > 1)
+                t += 6.0 + 8.0 * p * static_cast<double>(M * N) / 3e6;
+            if (t < time) {
+                time = t;
+                best = Plan{n, p};
+            }
+        }
+    return best;
 }
 
 // Waves per workgroup and steps in flight: what registers (sums 8 kN kRB, a step 4 kN sizeof(T) + 4 kRB or 8 kRB) and
@@ -278,7 +318,7 @@ template <class T, int kEpi>
 hipError_t launch_blocks(const RowsArgs& g, hipStream_t s)
 {
     constexpr bool kShort = sizeof(T) == 2;
-    if (ceil_div(g.e.N, 64) >= 128)
+    if (plan(g.e.M, g.K, g.e.N, sizeof(T)).n == 4)
         return g.e.M <= 16 ? launch_rows<T, 4, 1, 8, 2, kEpi>(g, s) : g.e.M <= 32 ? launch_rows<T, 4, 2, 8, 2, kEpi>(g, s)
                                                                              : launch_rows<T, 4, 4, 4, 2, kEpi>(g, s);
     return g.e.M <= 16   ? launch_rows<T, 2, 1, 8, kShort ? 6 : 3, kEpi>(g, s)
@@ -287,6 +327,8 @@ hipError_t launch_blocks(const RowsArgs& g, hipStream_t s)
 }
 
 }  // namespace
+
+int gated_rows_parts(int dtype, int64_t M, int64_t K, int64_t N) { return plan(M, K, N, dtype == MOE_F32 ? 4 : 2).parts; }
 
 hipError_t launch_gated_rows(Epi epi, int dtype, const RowsArgs& g, hipStream_t s)
 {

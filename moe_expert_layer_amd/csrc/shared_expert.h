@@ -71,6 +71,9 @@ struct LdsLimit {
 hipError_t launch_dropout(const void* x, const void* residual, int dtype, int64_t rows, int64_t cols, const Dropout& d,
                           void* out, hipStream_t s);
 
+// Rows of a gated block or an adapter call: their number and 32-bit counters of tiles and steps of K stay far apart.
+constexpr int64_t kMaxSharedRows = int64_t{1} << 28;
+
 // gated.hip: the gated block and its gradient (moe_gated_projection, moe_gated_projection_backward).
 struct GatedLayout {
     size_t x = 0, wg = 0, wu = 0;      // operands laid out for the products, where the caller's are not already

@@ -130,7 +130,8 @@ SIZES = [(1, 1, 1), (1, 8, 8), (2, 7, 9), (1, 64, 64), (3, 65, 63), (16, 72, 136
          (64, 64, 128), (65, 127, 129), (127, 320, 72), (128, 256, 256), (129, 130, 257), (200, 520, 328), (257, 1001, 130),
          (300, 96, 1032), (1, 1000, 520), (5, 2056, 24), (31, 24, 2000),
          # few rows: every row block, K cut over workgroups and not, many columns
-         (1, 4096, 264), (16, 2047, 65), (17, 1030, 8), (32, 777, 1003), (48, 600, 70), (64, 4100, 33), (3, 40, 8200)]
+         (1, 4096, 264), (16, 2047, 65), (17, 1030, 8), (32, 777, 1003), (48, 600, 70), (64, 4100, 33), (3, 40, 8200),
+         (16, 4100, 130), (63, 3001, 70), (2, 8190, 9), (8, 33, 4), (50, 2000, 3), (64, 31, 6)]
 
 
 @TYPES
@@ -262,9 +263,13 @@ def test_gated_float32_keeps_24_bits():
 @pytest.mark.parametrize("T,K,N,L,R", [(1, 1, 1, 1, 1), (1, 64, 64, 2, 8), (3, 33, 9, 4, 3), (16, 128, 256, 5, 16),
                                        (17, 100, 130, 3, 13), (64, 520, 72, 40, 32), (200, 64, 1000, 7, 64), (90, 257, 65, 2, 100),
                                        (33, 1024, 40, 9, 128), (40, 48, 48, 3, 128), (300, 72, 520, 1, 4),
+                                       # rows and adapters of a few values, whatever is last in its tensor
+                                       (4, 3, 8, 1, 2), (4, 4, 9, 1, 2), (70, 5, 7, 2, 9), (6, 50, 11, 3, 9), (1, 7, 8, 1, 1),
                                        # beyond what single rows are used for: every width of rank and of tile
                                        (1, 14336, 264, 2, 128), (700, 4096, 1024, 9, 96), (130, 9000, 300, 3, 61),
-                                       (2500, 1000, 4104, 1023, 32), (600, 5001, 2003, 5, 24)])
+                                       (2500, 1000, 4104, 1023, 32), (600, 5001, 2003, 5, 24), (900, 2053, 1021, 4, 13),
+                                       (2000, 1030, 15, 2, 100), (3000, 513, 130, 1, 5),
+                                       (1024, 40, 24, 3, 4), (1025, 40, 24, 3, 4), (70000, 5, 7, 3, 2)])
 def test_adapter(dtype, T, K, N, L, R):
     base, x = randn(1, T, N, dtype=dtype), randn(2, T, K, dtype=dtype)
     a, b = randn(3, L, K, R, dtype=dtype, scale=K ** -0.5), randn(4, L, R, N, dtype=dtype, scale=R ** -0.5)
@@ -303,13 +308,14 @@ def test_adapter_many_rows(dtype, order):
 
 
 @TYPES
-def test_adapter_leaves_unread_what_lies_past_a_rank(dtype):
+@pytest.mark.parametrize("T", [20, 1200])
+def test_adapter_leaves_unread_what_lies_past_a_rank(dtype, T):
     """NaN in the columns and rows past an adapter's rank, in unused adapters, and in rows without one."""
-    T, K, N, L, R = 20, 96, 80, 4, 16
+    K, N, L, R = 96, 80, 4, 16
     base, x = randn(1, T, N, dtype=dtype), randn(2, T, K, dtype=dtype)
     a, b = randn(3, L, K, R, dtype=dtype), randn(4, L, R, N, dtype=dtype)
     ranks = torch.tensor([5, 0, 16, -3], dtype=torch.int32, device="cuda")
-    ids = torch.tensor([0, 1, 3, -1] * 5, dtype=torch.int32, device="cuda")
+    ids = torch.tensor([0, 1, 3, -1] * (T // 4), dtype=torch.int32, device="cuda")
     want, bound = ref.adapter(base, x, a, b, ids, None, ranks)
     nan = float("nan")
     a[0, :, 5:], b[0, 5:] = nan, nan

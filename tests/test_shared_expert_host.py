@@ -45,7 +45,8 @@ NAN = float("nan")
     (dict(T=-1), 1), (dict(H=0), 1), (dict(F=-5), 1), (dict(activation=3), 1), (dict(activation=-1), 1),
     (dict(dropout=-0.1), 1), (dict(dropout=1.1), 1), (dict(dropout=NAN), 1), (dict(dropout=1.0), 0),
     (dict(dtype=2), 2), (dict(dtype=3), 2), (dict(T=1 << 31), 2), (dict(H=(1 << 22) + 1), 2), (dict(F=(1 << 22) + 1), 2),
-    (dict(T=(1 << 31) - 1, H=512, F=512), 0), (dict(T=(1 << 31) - 1, H=513), 2), (dict(H=1 << 22, F=1 << 19), 2),
+    (dict(T=(1 << 31) - 1, H=512, F=512), 2), (dict(T=1 << 28, H=512, F=512), 0), (dict(T=(1 << 28) + 1), 2),
+    (dict(T=1 << 28, H=513), 2), (dict(H=1 << 22, F=1 << 19), 2),
 ])
 def test_gated_sizes(mel, kw, expected):
     lib = mel.library()
@@ -113,7 +114,7 @@ def _adapter(mel, **kw):
 @pytest.mark.parametrize("kw,expected", [
     (dict(), 0), (dict(T=0), 0), (dict(K=1, N=1, L=1, R=1), 0), (dict(R=128, L=1023), 0), (dict(dtype=0), 0),
     (dict(T=-1), 1), (dict(K=0), 1), (dict(N=0), 1), (dict(L=0), 1), (dict(R=0), 1), (dict(reserved=1), 1),
-    (dict(R=129), 2), (dict(L=1024), 2), (dict(dtype=2), 2), (dict(T=1 << 31), 2), (dict(K=(1 << 22) + 1), 2),
+    (dict(R=129), 2), (dict(L=1024), 2), (dict(dtype=2), 2), (dict(T=(1 << 28) + 1), 2), (dict(K=(1 << 22) + 1), 2),
     (dict(N=(1 << 22) + 1), 2),
 ])
 def test_adapter_sizes(mel, kw, expected):
