@@ -10,8 +10,8 @@
 //   forward  A = x (kKC), B = Wg and Wu (kNC), both in one tile: the epilogue holds g and u of the same columns
 //   dx       A = dg, then du (kKC), B = Wg, then Wu (kKC): two segments of one sum
 //   dWg|dWu  A = x (kNC, M = H), B = dg | du (kNC): K = T
-// bfloat16 operands go to v_mfma_f32_32x32x16_bf16 as they are, float32 operands as three bfloat16 planes (planes.h): six
-// segments of one sum, the small products first, so that the partial sums stay small until the last sixth of the additions.
+// bfloat16 operands go to v_mfma_f32_32x32x16_bf16 as they are, float32 operands as three bfloat16 planes (planes.h), all
+// of them in one stage: the product of the first planes has a sum of its own, the five small ones share another.
 #include <algorithm>
 #include <atomic>
 #include <utility>
@@ -22,48 +22,52 @@ namespace moe {
 namespace {
 
 enum Layout { kKC = 0, kNC = 1 };
-constexpr int kBK = 64;                         // K values per step: 128-byte rows of a kKC operand, whole cache lines
 constexpr uint32_t kOob = 0xC0000000u;          // a buffer offset past any num_records used here: reads as zero
 
-// Tile shape: kWM x kWN waves, each kTM x kTN accumulator blocks of 32 x 32.
-template <int kWM_, int kWN_, int kTM_, int kTN_, int kBlocks_>
+// Tile shape: kWM x kWN waves, each kTM x kTN accumulator blocks of 32 x 32; kP planes of kBK values of K per stage,
+// kStages of them in LDS.
+template <int kWM_, int kWN_, int kTM_, int kTN_, int kBlocks_, int kBK_, int kP_, int kStages_>
 struct Shape {
-    static constexpr int kWM = kWM_, kWN = kWN_, kTM = kTM_, kTN = kTN_, kBlocks = kBlocks_;
+    static constexpr int kWM = kWM_, kWN = kWN_, kTM = kTM_, kTN = kTN_, kBlocks = kBlocks_, kBK = kBK_, kP = kP_;
+    static constexpr int kStages = kStages_, kSubs = kBK / 16;         // sub-steps: one MFMA of 16 k deep
     static constexpr int kWaves = kWM * kWN, kThreads = kWaves * 64;
     static constexpr int BM = 32 * kWM * kTM, BNB = 32 * kWN * kTN;    // rows, staged columns of B
-    static constexpr int kABytes = BM * kBK * 2, kBBytes = BNB * kBK * 2, kStage = kABytes + kBBytes;
-    static constexpr int kSmem = 2 * kStage;
-    static constexpr int kAC = kABytes / 1024 / kWaves, kBC = kBBytes / 1024 / kWaves;   // 1 KiB copies per wave
-    static_assert(kAC * kWaves * 1024 == kABytes && kBC * kWaves * 1024 == kBBytes, "whole copies");
-    static_assert(kAC % 2 == 0 && kBC % 2 == 0 && kWaves % 2 == 0 && kTN % 2 == 0, "pairs");
+    static constexpr int kAPlane = BM * kBK * 2, kBPlane = BNB * kBK * 2;
+    static constexpr int kABytes = kP * kAPlane, kStage = kABytes + kP * kBPlane, kSmem = kStages * kStage;
+    static constexpr int kAC = kAPlane / 1024 / kWaves, kBC = kBPlane / 1024 / kWaves;   // 1 KiB copies per wave and plane
+    static constexpr int kPairs = kP == 1 ? 1 : 6, kSums = kP == 1 ? 1 : 2;
+    static constexpr int kMfmas = kPairs * kTM * kTN;                  // per wave and sub-step
+    static_assert(kAC * kWaves * 1024 == kAPlane && kBC * kWaves * 1024 == kBPlane, "whole copies");
+    static_assert(kAC % 2 == 0 && kBC % 2 == 0 && kWaves % 2 == 0 && kTN % 2 == 0 && kSubs % 2 == 0, "pairs");
+    static_assert(kSmem * kBlocks <= 160 * 1024, "LDS of one CU");
 };
 
 struct GemmArgs {
-    // operand planes: segment s multiplies plane (a_idx >> 4 s) & 15 of a with plane (b_idx >> 4 s) & 7 of b0, or of
-    // b1 where bit 3 is set; a gated tile, and the second half of the column tiles with mats = 2, take the other one
-    const uint16_t *a, *b0, *b1;
-    int64_t a_plane, b_plane;                   // values between planes
-    uint64_t a_idx, b_idx;
-    int nseg, kt;                               // segments, steps of kBK per segment
+    // segment s multiplies a[s] with b[s]; a gated tile's second columns, and the second half of the column tiles with
+    // mats = 2, take the other of b
+    const uint16_t *a[2], *b[2];
+    int nseg, kt;                               // segments, steps of K per segment
     int lda, ldb;                               // values between rows, multiples of 8
+    int a_plane, b_plane;                       // values between the planes of a row
     int M, N;                                   // rows, columns (of one matrix)
     int K, kc;                                  // the rows of a kNC operand, the values of a kKC operand's row (K, padded)
     int mt, nt, mats;                           // row tiles, column tiles (of one matrix), matrices of columns
     EpiArgs e;
 };
 
-__device__ __forceinline__ void copy16(const i32x4_t& rsrc, uint32_t voff, uint32_t lds)
+__device__ __forceinline__ void copy16(const i32x4_t& rsrc, uint32_t voff, uint32_t soff, uint32_t lds)
 {
     // LDS DMA of 16 bytes per lane through a buffer resource: lane i writes LDS byte lds + 16 i; offsets past the
     // resource's end read as zero.  Counts in vmcnt; the waits are explicit (step_barrier).
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(lds) : "memory");
+    asm volatile("s_mov_b32 m0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %2 offen lds"
+                 :: "v"(voff), "s"(rsrc), "s"(soff), "s"(lds) : "memory");
 }
 
-// This wave's copies and LDS reads are complete, then the workgroup's.
+// This wave's copies but the last kLater and its LDS reads are complete, then the workgroup's.
+template <int kLater>
 __device__ __forceinline__ void step_barrier()
 {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" :: "n"(kLater) : "memory");
 }
 
 __device__ __forceinline__ i32x4_t make_rsrc(const uint16_t* p, int64_t bytes)
@@ -74,14 +78,15 @@ __device__ __forceinline__ i32x4_t make_rsrc(const uint16_t* p, int64_t bytes)
                    __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), 0x00027000};
 }
 
-// One operand's share of an LDS stage: kCols rows (kKC) or columns (kNC) of 64 k.
-//   kKC: row r is 128 bytes, its 16-byte chunk c (8 k) lies at c ^ ((r >> 1) & 7): 16 rows' reads of one chunk cover
-//        all 16 bank groups
+// One operand plane's share of an LDS stage: kCols rows (kKC) or columns (kNC) of kBK k.
+//   kKC: row r is 128 (64) bytes, its 16-byte chunk c (8 k) lies at c ^ ((r >> 1) & 7) (c ^ ((r >> 2) & 3)): 16 rows'
+//        reads of one chunk cover all 16 bank groups
 //   kNC: k row kr is 2 kCols bytes, chunk c (8 columns) lies at c ^ swizzle(kr): the four k rows of a transposing read
 //        land in four different 64-byte quarters of a 256-byte bank window
-template <int kLayout, int kCols>
+template <int kLayout, int kCols, int kBK>
 struct Region {
-    static constexpr int kRow = kLayout == kKC ? 128 : 2 * kCols;
+    static_assert(kBK == 64 || kBK == 32, "rows of 8 or 4 chunks");
+    static constexpr int kRow = kLayout == kKC ? 2 * kBK : 2 * kCols;
     static constexpr int kChunks = kRow / 16;
     static constexpr int kRowsPerCopy = 64 / kChunks;
     static constexpr int kBytes = kCols * kBK * 2;
@@ -89,7 +94,7 @@ struct Region {
     static __device__ __forceinline__ int swizzle(int r)
     {
         if constexpr (kLayout == kKC)
-            return (r >> 1) & 7;
+            return kBK == 64 ? (r >> 1) & 7 : (r >> 2) & 3;
         else
             return kChunks == 8 ? 4 * ((r >> 1) & 1) : 4 * (r & 3);
     }
@@ -107,37 +112,47 @@ struct Region {
     {
         if constexpr (kLayout == kKC) {
             const int r = lane & 31;
-            return (32 * block0 + r) * 128 + 16 * ((2 * i + (lane >> 5)) ^ swizzle(r));
+            return (32 * block0 + r) * kRow + 16 * ((2 * i + (lane >> 5)) ^ swizzle(r));
         } else {
             const int g = lane >> 4, e = (lane >> 2) & 3, q = lane & 3;
             const int kr = 8 * (g >> 1) + e, col = 32 * (block0 + i) + 16 * (g & 1) + 4 * q;
             return kr * kRow + 16 * ((col >> 3) ^ swizzle(kr)) + 2 * (col & 7);
         }
     }
-    static constexpr int bases(int blocks) { return kLayout == kKC ? 4 : blocks; }
+    static constexpr int bases(int blocks) { return kLayout == kKC ? kBK / 16 : blocks; }
+    // The k of this lane's chunk in copy ci (kKC).
+    static __device__ __forceinline__ int chunk_k(int ci, int lane)
+    {
+        return 8 * ((lane % kChunks) ^ swizzle(ci * kRowsPerCopy + lane / kChunks));
+    }
 };
 
 // The kernel for one tile shape, operand layouts and epilogue.
-template <class S, int kLA, int kLB, int kEpi, bool kF32>
+template <class S, int kLA, int kLB, int kEpi>
 struct Gemm {
     static constexpr bool kDual = kEpi != kEpiOut;
+    static constexpr int kBK = S::kBK;
     static constexpr int BN = kDual ? S::BNB / 2 : S::BNB;               // output columns per tile
-    using RA = Region<kLA, S::BM>;
-    using RB = Region<kLB, BN>;                                          // one matrix's columns
+    using RA = Region<kLA, S::BM, kBK>;
+    using RB = Region<kLB, BN, kBK>;                                     // one matrix's columns
     static constexpr int kNA = RA::bases(S::kTM), kNB = RB::bases(S::kTN);
     static constexpr int kReadsA = kLA == kKC ? 1 : 2, kReadsB = kLB == kKC ? 1 : 2;   // LDS reads per fragment
-    static constexpr int kReads = S::kTM * kReadsA + S::kTN * kReadsB;
+    static constexpr int kReadsPlane = S::kTM * kReadsA + S::kTN * kReadsB, kReads = S::kP * kReadsPlane;
+    static constexpr int kC = S::kP * (S::kAC + S::kBC);                 // copies per wave and step
     static_assert(!kDual || kLB == kNC, "gated tiles take N-contiguous weights");
+    static_assert((S::kStages - 1) * kC < 64, "vmcnt");
 
     struct Frags {
-        bf16x8_t a[S::kTM], b[S::kTN];
+        bf16x8_t a[S::kP][S::kTM], b[S::kP][S::kTN];
         i16x4_t lo;
     };
+    using Acc = f32x16_t[S::kSums][S::kTM][S::kTN];
     struct Lane {
         uint32_t a_voff[S::kAC], b_voff[S::kBC];
         uint32_t a_base[kNA], b_base[kNB];
         int k8[2];                       // kKC: the k of this lane's chunk, by the copy's parity
         uint32_t a_lds, b_lds;           // this wave's first copies in the stage being filled
+        uint32_t a_plane, b_plane;       // bytes between planes
         i32x4_t ra, rb;
     };
 
@@ -156,24 +171,24 @@ struct Gemm {
         }
     }
 
-    // Read Q of a sub-step, in the order the MFMAs take them: A block 0, the B blocks, the other A blocks.
+    // Read Q of a sub-step, plane by plane in the order the MFMAs take them: A block 0, the B blocks, the other A blocks.
     template <int kSub, int Q>
     static __device__ __forceinline__ void read_one(Frags& f, const Lane& ln)
     {
-        constexpr int kB0 = kReadsA, kA1 = kReadsA + S::kTN * kReadsB;
-        if constexpr (Q >= kB0 && Q < kA1) {
-            constexpr int j = (Q - kB0) / kReadsB, h = (Q - kB0) % kReadsB;
+        constexpr int p = Q / kReadsPlane, Q1 = Q % kReadsPlane, kB0 = kReadsA, kA1 = kReadsA + S::kTN * kReadsB;
+        if constexpr (Q1 >= kB0 && Q1 < kA1) {
+            constexpr int j = (Q1 - kB0) / kReadsB, h = (Q1 - kB0) % kReadsB;
             if constexpr (kLB == kKC)
-                read_frag<kKC, RB, kSub, 0>(f.b[j], f.lo, ln.b_base[kSub] + j * 32 * 128);
+                read_frag<kKC, RB, kSub, 0>(f.b[p][j], f.lo, ln.b_base[kSub] + p * S::kBPlane + j * 32 * RB::kRow);
             else
-                read_frag<kNC, RB, kSub, h>(f.b[j], f.lo, ln.b_base[j]);
+                read_frag<kNC, RB, kSub, h>(f.b[p][j], f.lo, ln.b_base[j] + p * S::kBPlane);
         } else {
-            constexpr int q = Q < kB0 ? Q : Q - S::kTN * kReadsB;
+            constexpr int q = Q1 < kB0 ? Q1 : Q1 - S::kTN * kReadsB;
             constexpr int i = q / kReadsA, h = q % kReadsA;
             if constexpr (kLA == kKC)
-                read_frag<kKC, RA, kSub, 0>(f.a[i], f.lo, ln.a_base[kSub] + i * 32 * 128);
+                read_frag<kKC, RA, kSub, 0>(f.a[p][i], f.lo, ln.a_base[kSub] + p * S::kAPlane + i * 32 * RA::kRow);
             else
-                read_frag<kNC, RA, kSub, h>(f.a[i], f.lo, ln.a_base[i]);
+                read_frag<kNC, RA, kSub, h>(f.a[p][i], f.lo, ln.a_base[i] + p * S::kAPlane);
         }
     }
 
@@ -183,21 +198,23 @@ struct Gemm {
         (read_one<kSub, Q0 + Is>(f, ln), ...);
     }
 
-    // Copy C of a step: A's, then B's.  krem: K values left from the step's first one (kKC chunks past them read zero).
+    // Copy C of a step: A's planes, then B's.  krem: K values left from the step's first one (kKC chunks past them read
+    // zero).
     template <int C>
     static __device__ __forceinline__ void copy_one(const Lane& ln, int krem)
     {
-        if constexpr (C < S::kAC) {
-            uint32_t v = ln.a_voff[C];
+        if constexpr (C < S::kP * S::kAC) {
+            constexpr int p = C / S::kAC, i = C % S::kAC;
+            uint32_t v = ln.a_voff[i];
             if constexpr (kLA == kKC)
-                v = ln.k8[C % 2] < krem ? v : kOob;
-            copy16(ln.ra, v, ln.a_lds + C * 1024);
+                v = ln.k8[i % 2] < krem ? v : kOob;
+            copy16(ln.ra, v, p * ln.a_plane, ln.a_lds + p * S::kAPlane + i * 1024);
         } else {
-            constexpr int j = C - S::kAC;
+            constexpr int p = (C - S::kP * S::kAC) / S::kBC, j = (C - S::kP * S::kAC) % S::kBC;
             uint32_t v = ln.b_voff[j];
             if constexpr (kLB == kKC)
                 v = ln.k8[j % 2] < krem ? v : kOob;
-            copy16(ln.rb, v, ln.b_lds + j * 1024);
+            copy16(ln.rb, v, p * ln.b_plane, ln.b_lds + p * S::kBPlane + j * 1024);
         }
     }
 
@@ -210,13 +227,14 @@ struct Gemm {
     // MFMA M of a sub-step, then this slot's share of the fragment reads of sub-step kNext (over the first half of the
     // MFMAs, so that they have landed when the sub-step ends) and of the copies (over all of them).
     template <int kNext, bool kCopy, int M>
-    static __device__ __forceinline__ void slot(f32x16_t (&acc)[S::kTM][S::kTN], const Frags& use, Frags& load,
-                                                const Lane& ln, int krem)
+    static __device__ __forceinline__ void slot(Acc& acc, const Frags& use, Frags& load, const Lane& ln, int krem)
     {
-        constexpr int NM = S::kTM * S::kTN, RF = NM / 2, NC = kCopy ? S::kAC + S::kBC : 0;
-        constexpr int i = M / S::kTN, j = M % S::kTN;
+        constexpr int NM = S::kMfmas, RF = NM / 2, NC = kCopy ? kC : 0;
+        constexpr int pair = M / (S::kTM * S::kTN), i = M / S::kTN % S::kTM, j = M % S::kTN;
+        constexpr int pa = S::kP == 1 ? 0 : kPlanePairs[pair][0], pb = S::kP == 1 ? 0 : kPlanePairs[pair][1];
+        f32x16_t& sum = acc[S::kP > 1 && pa + pb > 0 ? 1 : 0][i][j];
         // B as the first operand: the block is transposed, a lane holds one row of C and runs of four columns
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(use.b[j], use.a[i], acc[i][j], 0, 0, 0);
+        sum = __builtin_amdgcn_mfma_f32_32x32x16_bf16(use.b[pb][j], use.a[pa][i], sum, 0, 0, 0);
         if constexpr (M < RF)
             reads<kNext, M * kReads / RF>(std::make_integer_sequence<int, (M + 1) * kReads / RF - M * kReads / RF>{}, load, ln);
         copies<M * NC / NM>(std::make_integer_sequence<int, (M + 1) * NC / NM - M * NC / NM>{}, ln, krem);
@@ -224,8 +242,8 @@ struct Gemm {
     }
 
     template <int kNext, bool kCopy, int... Ms>
-    static __device__ __forceinline__ void slots(std::integer_sequence<int, Ms...>, f32x16_t (&acc)[S::kTM][S::kTN],
-                                                 const Frags& use, Frags& load, const Lane& ln, int krem)
+    static __device__ __forceinline__ void slots(std::integer_sequence<int, Ms...>, Acc& acc, const Frags& use, Frags& load,
+                                                 const Lane& ln, int krem)
     {
         __builtin_amdgcn_sched_barrier(0);
         (slot<kNext, kCopy, Ms>(acc, use, load, ln, krem), ...);
@@ -241,9 +259,8 @@ struct Gemm {
     static __device__ __forceinline__ int aim(const GemmArgs& g, const Feed& f, Lane& ln, int m0, int n0, int mat)
     {
         const int seg = f.seg;
-        const uint16_t* a = g.a + ((g.a_idx >> (4 * seg)) & 15) * g.a_plane;
-        const int bi = static_cast<int>((g.b_idx >> (4 * seg)) & 15);
-        const uint16_t* b = ((bi >> 3) ^ mat ? g.b1 : g.b0) + (bi & 7) * g.b_plane;
+        const uint16_t* a = seg != 0 ? g.a[1] : g.a[0];
+        const uint16_t* b = (seg ^ mat) & 1 ? g.b[1] : g.b[0];
         const bool on = f.left > 0;
         // kKC: rows [m0, M) of lda values from kk on; kNC: rows [kk, K) from column m0 on
         const int64_t an = kLA == kKC ? min(S::BM, g.M - m0) : min(kBK, g.K - f.kk);
@@ -265,9 +282,19 @@ struct Gemm {
         }
     }
 
+    // Sub-steps kSub - 1 .. kSubs - 2 of a step with the reads of their successors; the last one's use is left.
+    template <int kSub>
+    static __device__ __forceinline__ void inner(Acc& acc, Frags& f0, Frags& f1, const Lane& ln)
+    {
+        using All = std::make_integer_sequence<int, S::kMfmas>;
+        if constexpr (kSub < S::kSubs) {
+            slots<kSub, false>(All{}, acc, kSub % 2 ? f0 : f1, kSub % 2 ? f1 : f0, ln, 0);
+            inner<kSub + 1>(acc, f0, f1, ln);
+        }
+    }
+
     // The sum of the tile's steps [step0, step1).
-    static __device__ __forceinline__ void k_loop(const GemmArgs& g, f32x16_t (&acc)[S::kTM][S::kTN], int m0, int n0,
-                                                  int mat0, int step0, int step1)
+    static __device__ __forceinline__ void k_loop(const GemmArgs& g, Acc& acc, int m0, int n0, int mat0, int step0, int step1)
     {
         extern __shared__ __attribute__((aligned(256))) unsigned char smem[];
         const uint32_t lds0 = static_cast<uint32_t>(
@@ -287,10 +314,11 @@ struct Gemm {
         for (int j = 0; j < S::kBC; ++j)
             ln.b_voff[j] = RB::voff(ci_b + j, lane, g.ldb, g.N - n0);
 #pragma unroll
-        for (int j = 0; j < 2; ++j)                        // the swizzle's row part: 8 j + lane / 8
-            ln.k8[j] = 8 * ((lane & 7) ^ ((4 * j + (lane >> 4)) & 7));
-        ln.a_lds = lds0 + S::kAC * wave * 1024;
-        ln.b_lds = lds0 + S::kABytes + S::kBC * wave * 1024;
+        for (int j = 0; j < 2; ++j)                        // a wave's first copy has an even number
+            ln.k8[j] = Region<kKC, S::BM, kBK>::chunk_k(j, lane);
+        const uint32_t a_lds = lds0 + S::kAC * wave * 1024, b_lds = lds0 + S::kABytes + S::kBC * wave * 1024;
+        ln.a_plane = 2 * static_cast<uint32_t>(g.a_plane);
+        ln.b_plane = 2 * static_cast<uint32_t>(g.b_plane);
 #pragma unroll
         for (int i = 0; i < kNA; ++i) {
             ln.a_base[i] = lds0 + RA::read_base(lane, i, wm * S::kTM);
@@ -306,50 +334,48 @@ struct Gemm {
             asm volatile("" : "+v"(ln.b_base[i]));
         }
 
-        constexpr int kC = S::kAC + S::kBC;
         using AllCopies = std::make_integer_sequence<int, kC>;
-        using AllMfmas = std::make_integer_sequence<int, S::kTM * S::kTN>;
+        using AllMfmas = std::make_integer_sequence<int, S::kMfmas>;
         Feed f{g.kt > 0 ? step0 / g.kt : 0, g.kt > 0 ? step0 % g.kt * kBK : 0, step1 - step0};
-        int krem = aim(g, f, ln, m0, n0, mat);
-        copies<0>(AllCopies{}, ln, krem);
-        advance(g, f);
-        krem = aim(g, f, ln, m0, n0, mat);
-        ln.a_lds += S::kStage;
-        ln.b_lds += S::kStage;
-        copies<0>(AllCopies{}, ln, krem);
-        advance(g, f);
-        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"(kC) : "memory");
+#pragma unroll
+        for (int i = 0; i < S::kStages; ++i) {
+            ln.a_lds = a_lds + i * S::kStage;
+            ln.b_lds = b_lds + i * S::kStage;
+            const int krem = aim(g, f, ln, m0, n0, mat);
+            copies<0>(AllCopies{}, ln, krem);
+            advance(g, f);
+        }
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" :: "n"((S::kStages - 1) * kC) : "memory");
 
         Frags f0, f1;
         reads<0, 0>(std::make_integer_sequence<int, kReads>{}, f0, ln);
-        int delta = S::kStage;
+        int stage = 0;                    // the step's own; its successor's fragments come from the next one
         for (int t = step0; t < step1; ++t) {
-            slots<1, false>(AllMfmas{}, acc, f0, f1, ln, 0);
-            slots<2, false>(AllMfmas{}, acc, f1, f0, ln, 0);
-            krem = aim(g, f, ln, m0, n0, mat);
-            slots<3, false>(AllMfmas{}, acc, f0, f1, ln, 0);
-            step_barrier();               // step t + 1 has landed, step t's stage is free
+            inner<1>(acc, f0, f1, ln);
+            const int krem = aim(g, f, ln, m0, n0, mat);
+            step_barrier<(S::kStages - 2) * kC>();         // step t + 1 has landed, step t's stage is free
+            const int next = stage + 1 == S::kStages ? 0 : stage + 1, delta = (next - stage) * S::kStage;
 #pragma unroll
             for (int i = 0; i < kNA; ++i)
                 ln.a_base[i] += delta;
 #pragma unroll
             for (int i = 0; i < kNB; ++i)
                 ln.b_base[i] += delta;
-            ln.a_lds -= delta;
-            ln.b_lds -= delta;
+            ln.a_lds = a_lds + stage * S::kStage;
+            ln.b_lds = b_lds + stage * S::kStage;
             slots<0, true>(AllMfmas{}, acc, f1, f0, ln, krem);
             advance(g, f);
-            delta = -delta;
+            stage = next;
         }
         // the copies past the last step (of nothing, into LDS) end before the workgroup does
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     }
 };
 
-template <class S, int kLA, int kLB, int kEpi, bool kF32>
+template <class S, int kLA, int kLB, int kEpi>
 __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
 {
-    using G = Gemm<S, kLA, kLB, kEpi, kF32>;
+    using G = Gemm<S, kLA, kLB, kEpi>;
     // consecutive tiles go to one XCD (workgroup b runs on XCD b % 8), in groups of 8 row tiles, so that the
     // workgroups of an XCD share rows of A and columns of B in its L2
     const int cols = g.nt * g.mats, tiles = g.mt * cols, total = tiles * g.e.parts;
@@ -366,14 +392,16 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
     const int mat = ct >= g.nt ? 1 : 0;
     const int n0 = (ct - mat * g.nt) * G::BN;
 
-    f32x16_t acc[S::kTM][S::kTN];
+    typename G::Acc acc;
 #pragma unroll
-    for (int i = 0; i < S::kTM; ++i)
+    for (int q = 0; q < S::kSums; ++q)
 #pragma unroll
-        for (int j = 0; j < S::kTN; ++j)
+        for (int i = 0; i < S::kTM; ++i)
 #pragma unroll
-            for (int r = 0; r < 16; ++r)
-                acc[i][j][r] = 0.0f;
+            for (int j = 0; j < S::kTN; ++j)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    acc[q][i][j][r] = 0.0f;
     const int64_t steps = static_cast<int64_t>(g.nseg) * g.kt;
     G::k_loop(g, acc, m0, n0, mat, static_cast<int>(steps * part / g.e.parts), static_cast<int>(steps * (part + 1) / g.e.parts));
 
@@ -382,6 +410,12 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
     const int wm = wave / S::kWN, wn = wave % S::kWN;
     const EpiArgs& e = g.e;
     const DropKey key = kEpi == kEpiOut ? DropKey{} : drop_key(e.drop);
+    if constexpr (S::kSums == 2)
+#pragma unroll
+        for (int i = 0; i < S::kTM; ++i)
+#pragma unroll
+            for (int j = 0; j < S::kTN; ++j)
+                acc[0][i][j] += acc[1][i][j];
 #pragma unroll
     for (int i = 0; i < S::kTM; ++i) {
         const int64_t row = m0 + 32 * (wm * S::kTM + i) + (lane & 31);
@@ -393,9 +427,9 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
                 const int block = wn * S::kTN + j;
                 const int col = n0 + 32 * (G::kDual ? block / 2 : block) + 16 * p + 8 * (lane >> 5);
                 float v[8], w[8];
-                run8(acc[i][j], p, v);
+                run8(acc[0][i][j], p, v);
                 if constexpr (G::kDual)
-                    run8(acc[i][j + 1], p, w);
+                    run8(acc[0][i][j + 1], p, w);
                 if (row >= g.M || col >= g.N)
                     continue;
                 if (e.partial != nullptr) {
@@ -403,7 +437,7 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
                     if constexpr (G::kDual)
                         store8(partial_at(e, part, 1, row, col), w, 8);
                 } else {
-                    finish8<kEpi, kF32>(e, key, v, w, mat, row, col);
+                    finish8<kEpi, (S::kP > 1)>(e, key, v, w, mat, row, col);
                 }
             }
         }
@@ -427,13 +461,13 @@ __global__ __launch_bounds__(256) void act_grad_kernel(EpiArgs e, Divisor groups
     finish_gated_bwd<kF32>(e, drop_key(e.drop), g, u, row, col);
 }
 
-// Matrices [rows, cols] of any alignment as planes [rows, ld] of bfloat16, the columns from cols up to the next multiple of
-// 8 zero; up to three of them in one launch (blockIdx.y).
+// Matrices [rows, cols] of any alignment as bfloat16, the planes of a row one after the other, each one's columns from cols
+// up to the next multiple of 8 zero; up to three matrices in one launch (blockIdx.y).
 struct PackArgs {
     struct One {
         const void* src;
         uint16_t* dst;
-        int64_t plane;
+        int plane;                                // values between the planes of a row
         Divisor groups;
         int n, cols, ld;                          // groups of 8 columns in all, columns, values between rows of dst
     } m[3];
@@ -454,18 +488,18 @@ __global__ __launch_bounds__(256) void pack_kernel(PackArgs g)
     store_planes<kF32>(m.dst + row * m.ld + col, m.plane, v);
 }
 
-// A matrix as the products take it: planes of bfloat16, rows of ld values.
+// A matrix as the products take it: rows of ld values, the planes of a row `plane` values apart.
 struct Planes {
     const uint16_t* p;
-    int64_t plane;
-    int ld;
+    int plane, ld;
 };
 
 int planes_of(int dtype) { return dtype == MOE_F32 ? 3 : 1; }
 int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }
-// Values between rows of what is laid out here: whole cache lines (rows that start inside one cost the copies of K up to
-// a third: 512 x 1024 x 2056, two segments, 46 against 60 us).
-int64_t own_ld(int64_t cols) { return (cols + 63) / 64 * 64; }
+// Values per plane of a row of what is laid out here: whole cache lines (rows that start inside one cost the copies of K
+// up to a third: 512 x 1024 x 2056, two segments, 46 against 60 us).
+int64_t own_plane(int64_t cols) { return (cols + 63) / 64 * 64; }
+int64_t own_ld(int dtype, int64_t cols) { return planes_of(dtype) * own_plane(cols); }
 // Whether a matrix of that width has to be laid out anew.
 bool needs_pack(int dtype, int64_t cols) { return dtype == MOE_F32 || cols % 8 != 0; }
 
@@ -487,12 +521,11 @@ hipError_t prepare(int dtype, const Source (&in)[kCount], Planes* (&out)[kCount]
         *out[i] = Planes{static_cast<const uint16_t*>(q.src), 0, static_cast<int>(q.cols)};
         if (!needs_pack(dtype, q.cols))
             continue;
-        const int64_t ld = own_ld(q.cols);
+        const int ld = static_cast<int>(own_ld(dtype, q.cols)), plane = static_cast<int>(own_plane(q.cols));
         uint16_t* const dst = static_cast<uint16_t*>(q.room);
-        *out[i] = Planes{dst, q.rows * ld, static_cast<int>(ld)};
+        *out[i] = Planes{dst, plane, ld};
         const int64_t groups = ceil_div(q.cols, 8);
-        a.m[count] = PackArgs::One{q.src, dst, q.rows * ld, divisor(static_cast<int>(groups)), 0, static_cast<int>(q.cols),
-                                   static_cast<int>(ld)};
+        a.m[count] = PackArgs::One{q.src, dst, plane, divisor(static_cast<int>(groups)), 0, static_cast<int>(q.cols), ld};
         first[count++] = q.rows;
         most = std::max(most, q.rows);
         widest = std::max(widest, groups);
@@ -516,9 +549,15 @@ hipError_t prepare(int dtype, const Source (&in)[kCount], Planes* (&out)[kCount]
     return hipSuccess;
 }
 
-// Large tiles: 256 x 256, 8 waves of 64 x 128, one workgroup per CU.  Small ones: 128 x 128, 4 waves of 64 x 64, two.
-using Large = Shape<4, 2, 2, 4, 1>;
-using Small = Shape<2, 2, 2, 2, 2>;
+// bfloat16: large tiles of 256 x 256, 8 waves of 64 x 128, one workgroup per CU; small ones of 128 x 128, 4 waves of
+// 64 x 64, two.  float32: 128 x 128, 4 waves of 64 x 64, one.
+using Large = Shape<4, 2, 2, 4, 1, 64, 1, 2>;
+using Small = Shape<2, 2, 2, 2, 2, 64, 1, 2>;
+using Float = Shape<2, 2, 2, 2, 1, 32, 3, 3>;
+
+// Steps of a sum over K values.
+int64_t steps_of(int dtype, int64_t K) { return ceil_div(K, dtype == MOE_F32 ? Float::kBK : Small::kBK); }
+static_assert(Large::kBK == Small::kBK, "one K step for bfloat16");
 
 // How a product runs: its tiles, and into how many parts its steps are cut.
 struct GemmPlan {
@@ -528,20 +567,23 @@ struct GemmPlan {
 
 // M rows, N staged columns in all (both matrices'), `steps` steps of K.  The times that decide, in us, are measured ones
 // (4096 x 4096 x 28672 and 512 x 1024 x 4096): a step of a large tile 1.75; of a small one 0.7, or 1.05 for two that
-// share a CU; a workgroup's start and end 8 and 6.  Parts cost a launch of 4 and two passes of float32 sums at 3.5 TB/s,
-// and give workgroups to CUs that had none: they are taken only below one small tile per CU.
-GemmPlan plan_gemm(int64_t M, int64_t N, int64_t steps)
+// share a CU; of a float32 one 1.3; a workgroup's start and end 8 and 6.  Parts cost a launch of 4 and two passes of float32
+// sums at 3.5 TB/s, and give workgroups to CUs that had none: they are taken only below one small tile per CU.
+GemmPlan plan_gemm(int dtype, int64_t M, int64_t N, int64_t steps)
 {
+    const bool f32 = dtype == MOE_F32;
     const int64_t large = ceil_div(M, Large::BM) * ceil_div(N, Large::BNB), small = ceil_div(M, Small::BM) * ceil_div(N, Small::BNB);
     constexpr int64_t kCus = 256;
+    const int64_t slots = f32 ? kCus : 2 * kCus;
+    const double one = f32 ? 1.3 : 0.7, full = f32 ? 1.3 : 1.05;
     const auto small_time = [&](int64_t tiles, int64_t n) {
-        const int64_t rest = tiles % (2 * kCus);
-        const double rounds = 1.05 * static_cast<double>(tiles / (2 * kCus)) + (rest == 0 ? 0.0 : rest <= kCus ? 0.7 : 1.05);
-        return rounds * static_cast<double>(n) + 6.0 * static_cast<double>(ceil_div(tiles, 2 * kCus));
+        const int64_t rest = tiles % slots;
+        const double rounds = full * static_cast<double>(tiles / slots) + (rest == 0 ? 0.0 : rest <= kCus ? one : full);
+        return rounds * static_cast<double>(n) + 6.0 * static_cast<double>(ceil_div(tiles, slots));
     };
-    GemmPlan best{true, 1};
-    double time = static_cast<double>(ceil_div(large, kCus)) * (1.75 * static_cast<double>(steps) + 8.0);
-    for (int64_t p = 1; p <= 16 && (p == 1 || (small * p <= 2 * kCus && steps >= 3 * p)); ++p) {
+    GemmPlan best{!f32, 1};
+    double time = f32 ? 1e30 : static_cast<double>(ceil_div(large, kCus)) * (1.75 * static_cast<double>(steps) + 8.0);
+    for (int64_t p = 1; p <= 16 && (p == 1 || (small * p <= slots && steps >= 3 * p)); ++p) {
         const double t = small_time(small * p, ceil_div(steps, p)) +
                          (p == 1 ? 0.0 : 4.0 + static_cast<double>(8 * p * M * N) / 3.5e6);
         if (t < time) {
@@ -551,19 +593,20 @@ GemmPlan plan_gemm(int64_t M, int64_t N, int64_t steps)
     }
     return best;
 }
+static_assert(Float::BM == Small::BM && Float::BNB == Small::BNB, "counted alike");
 
-template <class S, int kLA, int kLB, int kEpi, bool kF32>
+template <class S, int kLA, int kLB, int kEpi>
 hipError_t launch_shape(GemmArgs g, hipStream_t s)
 {
-    using G = Gemm<S, kLA, kLB, kEpi, kF32>;
+    using G = Gemm<S, kLA, kLB, kEpi>;
     static LdsLimit limit;
-    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gemm<S, kLA, kLB, kEpi, kF32>), S::kSmem); e != hipSuccess)
+    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gemm<S, kLA, kLB, kEpi>), S::kSmem); e != hipSuccess)
         return e;
     g.mt = static_cast<int>(ceil_div(g.M, S::BM));
     g.nt = static_cast<int>(ceil_div(g.N, G::BN));
     const int64_t total = static_cast<int64_t>(g.mt) * g.nt * g.mats * g.e.parts;
-    gemm<S, kLA, kLB, kEpi, kF32><<<dim3(static_cast<unsigned>(ceil_div(total, kXcdCount) * kXcdCount)), S::kThreads,
-                                    S::kSmem, s>>>(g);
+    gemm<S, kLA, kLB, kEpi><<<dim3(static_cast<unsigned>(ceil_div(total, kXcdCount) * kXcdCount)), S::kThreads, S::kSmem,
+                              s>>>(g);
     return hipGetLastError();
 }
 
@@ -573,7 +616,7 @@ hipError_t launch_gemm(GemmArgs g, int dtype, float* partial, hipStream_t s)
 {
     constexpr bool kGated = kEpi != kEpiOut;
     const int mats = kGated ? 2 : g.mats;
-    const GemmPlan plan = plan_gemm(g.M, static_cast<int64_t>(mats) * g.N, static_cast<int64_t>(g.nseg) * g.kt);
+    const GemmPlan plan = plan_gemm(dtype, g.M, static_cast<int64_t>(mats) * g.N, static_cast<int64_t>(g.nseg) * g.kt);
     g.e.M = g.M;
     g.e.N = g.N;
     g.e.mats = mats;
@@ -582,44 +625,18 @@ hipError_t launch_gemm(GemmArgs g, int dtype, float* partial, hipStream_t s)
     g.e.ld_part = static_cast<int>(padded(g.N));
     hipError_t e;
     if (dtype == MOE_F32)
-        e = plan.large ? launch_shape<Large, kLA, kLB, kEpi, true>(g, s) : launch_shape<Small, kLA, kLB, kEpi, true>(g, s);
+        e = launch_shape<Float, kLA, kLB, kEpi>(g, s);
     else
-        e = plan.large ? launch_shape<Large, kLA, kLB, kEpi, false>(g, s) : launch_shape<Small, kLA, kLB, kEpi, false>(g, s);
+        e = plan.large ? launch_shape<Large, kLA, kLB, kEpi>(g, s) : launch_shape<Small, kLA, kLB, kEpi>(g, s);
     return e != hipSuccess || plan.parts == 1 ? e : launch_gated_finish(static_cast<Epi>(kEpi), dtype, g.e, s);
 }
 
 // Bytes of the partial sums of such a product.
-int64_t partial_bytes(int64_t M, int64_t N, int mats, int64_t steps)
+int64_t partial_bytes(int dtype, int64_t M, int64_t N, int mats, int64_t steps)
 {
-    const GemmPlan plan = plan_gemm(M, mats * N, steps);
+    const GemmPlan plan = plan_gemm(dtype, M, mats * N, steps);
     return plan.parts > 1 ? int64_t{4} * plan.parts * mats * M * padded(N) : 0;
 }
-
-// The segments of a product of planes: one for bfloat16, six for float32, small products first.  a0, b0: added to the
-// plane numbers (four bits each).
-void add_segments(GemmArgs& g, int dtype, int a0, int b0)
-{
-    for (int i = dtype == MOE_F32 ? 0 : 5; i < 6; ++i) {
-        g.a_idx |= static_cast<uint64_t>(a0 + kPlanePairs[i][0]) << (4 * g.nseg);
-        g.b_idx |= static_cast<uint64_t>(b0 + kPlanePairs[i][1]) << (4 * g.nseg);
-        ++g.nseg;
-    }
-}
-
-// dx's two sums interleaved by size: the small products of both first.
-void add_segments_pair(GemmArgs& g, int dtype, int a1)
-{
-    for (int i = dtype == MOE_F32 ? 0 : 5; i < 6; ++i)
-        for (int m = 0; m < 2; ++m) {
-            g.a_idx |= static_cast<uint64_t>(m * a1 + kPlanePairs[i][0]) << (4 * g.nseg);
-            g.b_idx |= static_cast<uint64_t>(8 * m + kPlanePairs[i][1]) << (4 * g.nseg);
-            ++g.nseg;
-        }
-}
-
-}  // namespace
-
-namespace {
 
 // Whether g and u come from the kernels for few rows.
 bool few_rows(const moe_gated& g) { return g.T <= kMaxRows && g.F >= kMinCols; }
@@ -629,7 +646,6 @@ bool few_rows(const moe_gated& g) { return g.T <= kMaxRows && g.F >= kMinCols; }
 GatedLayout gated_layout(const moe_gated& g, bool backward)
 {
     GatedLayout L;
-    const int64_t P = planes_of(g.dtype), products = g.dtype == MOE_F32 ? 6 : 1;
     size_t off = 0;
     const auto take = [&](size_t& at, int64_t bytes) {
         at = off;
@@ -637,21 +653,21 @@ GatedLayout gated_layout(const moe_gated& g, bool backward)
     };
     const bool rows = few_rows(g);                  // the forward product takes its operands as they are
     if (needs_pack(g.dtype, g.H) && (backward || !rows))
-        take(L.x, 2 * P * g.T * own_ld(g.H));
+        take(L.x, 2 * g.T * own_ld(g.dtype, g.H));
     if (needs_pack(g.dtype, g.F) && (backward || !rows)) {
-        take(L.wg, 2 * P * g.H * own_ld(g.F));
-        take(L.wu, 2 * P * g.H * own_ld(g.F));
+        take(L.wg, 2 * g.H * own_ld(g.dtype, g.F));
+        take(L.wu, 2 * g.H * own_ld(g.dtype, g.F));
     }
     if (backward)
-        take(L.dgu, 2 * 2 * P * g.T * own_ld(g.F));
+        take(L.dgu, 2 * 2 * g.T * own_ld(g.dtype, g.F));
     int64_t partial = 0;                                  // of one product after the other
     if (g.T > 0) {
         const int64_t parts = rows ? gated_rows_parts(g.dtype, g.T, g.H, g.F) : 1;
-        partial = !rows ? partial_bytes(g.T, g.F, 2, products * ceil_div(g.H, kBK))
+        partial = !rows ? partial_bytes(g.dtype, g.T, g.F, 2, steps_of(g.dtype, g.H))
                         : parts > 1 ? 4 * 2 * parts * g.T * padded(g.F) : 0;
         if (backward) {
-            partial = std::max(partial, partial_bytes(g.T, g.H, 1, 2 * products * ceil_div(g.F, kBK)));
-            partial = std::max(partial, partial_bytes(g.H, g.F, 2, products * ceil_div(g.T, kBK)));
+            partial = std::max(partial, partial_bytes(g.dtype, g.T, g.H, 1, 2 * steps_of(g.dtype, g.F)));
+            partial = std::max(partial, partial_bytes(g.dtype, g.H, g.F, 2, steps_of(g.dtype, g.T)));
         }
     }
     take(L.partial, partial);
@@ -691,13 +707,13 @@ hipError_t launch_gu(const moe_gated& q, const void* x, const void* wg, const vo
         return err != hipSuccess || e.parts == 1 ? err : launch_gated_finish(static_cast<Epi>(kEpi), q.dtype, e, s);
     }
     GemmArgs g{};
-    g.a = p.x.p;
-    g.b0 = p.wg.p;
-    g.b1 = p.wu.p;
+    g.a[0] = p.x.p;
+    g.b[0] = p.wg.p;
+    g.b[1] = p.wu.p;
     g.a_plane = p.x.plane;
     g.b_plane = p.wg.plane;
-    add_segments(g, q.dtype, 0, 0);
-    g.kt = static_cast<int>(ceil_div(q.H, kBK));
+    g.nseg = 1;
+    g.kt = static_cast<int>(steps_of(q.dtype, q.H));
     g.lda = p.x.ld;
     g.ldb = p.wg.ld;
     g.M = static_cast<int>(q.T);
@@ -739,17 +755,18 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
     if (q.T > 0)                                          // without tokens x and the weights may be null
         if (hipError_t e = prepare_all(q, x, wg, wu, L, ws, p, s); e != hipSuccess)
             return e;
-    const int64_t size = q.dtype == MOE_F32 ? 4 : 2, ldf = own_ld(q.F);
+    const int64_t size = q.dtype == MOE_F32 ? 4 : 2, ldf = own_ld(q.dtype, q.F);
     float* const partial = reinterpret_cast<float*>(ws + L.partial);
-    const int P = planes_of(q.dtype);
-    uint16_t* const dgu = reinterpret_cast<uint16_t*>(ws + L.dgu);
-    const int64_t dgu_plane = q.T * ldf;
+    uint16_t* const dg = reinterpret_cast<uint16_t*>(ws + L.dgu);
+    uint16_t* const du = dg + q.T * ldf;
+    const int plane = static_cast<int>(own_plane(q.F));
     if (q.T > 0) {
         EpiArgs e{};
         e.dh = dh;
-        e.dgu = dgu;
-        e.dgu_plane = dgu_plane;
-        e.ld_dgu = static_cast<int>(ldf);
+        e.dg = dg;
+        e.du = du;
+        e.d_plane = plane;
+        e.ld_d = static_cast<int>(ldf);
         e.drop = d;
         if (saved_gu == nullptr) {
             if (hipError_t err = launch_gu<kEpiGatedBwd>(q, x, wg, wu, p, e, partial, s);
@@ -773,13 +790,14 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
         }
         // dx [T, H]: K = F, the gate part, then the up part
         GemmArgs c{};
-        c.a = dgu;
-        c.a_plane = dgu_plane;
-        c.b0 = p.wg.p;
-        c.b1 = p.wu.p;
+        c.a[0] = dg;
+        c.a[1] = du;
+        c.a_plane = plane;
+        c.b[0] = p.wg.p;
+        c.b[1] = p.wu.p;
         c.b_plane = p.wg.plane;
-        add_segments_pair(c, q.dtype, P);
-        c.kt = static_cast<int>(ceil_div(q.F, kBK));
+        c.nseg = 2;
+        c.kt = static_cast<int>(steps_of(q.dtype, q.F));
         c.kc = static_cast<int>(padded(q.F));
         c.lda = static_cast<int>(ldf);
         c.ldb = p.wg.ld;
@@ -792,13 +810,13 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
     }
     // dWg and dWu [H, F]: K = T
     GemmArgs w{};
-    w.a = p.x.p;
+    w.a[0] = p.x.p;
     w.a_plane = p.x.plane;
-    w.b0 = dgu;
-    w.b1 = dgu + P * dgu_plane;
-    w.b_plane = dgu_plane;
-    add_segments(w, q.dtype, 0, 0);
-    w.kt = static_cast<int>(ceil_div(q.T, kBK));
+    w.b[0] = dg;
+    w.b[1] = du;
+    w.b_plane = plane;
+    w.nseg = 1;
+    w.kt = static_cast<int>(steps_of(q.dtype, q.T));
     w.lda = p.x.ld;
     w.ldb = static_cast<int>(ldf);
     w.M = static_cast<int>(q.H);

@@ -20,9 +20,8 @@ struct EpiArgs {
     void *o0, *o1;                              // outputs [M, N] of matrix 0 and 1 (kEpiOut), h (kEpiGated)
     void *save_g, *save_u;                      // kEpiGated: g and u, laid out as h (or null)
     const void* dh;                             // kEpiGatedBwd: [M, N]
-    uint16_t* dgu;                              // planes of dg, then of du, [M, ld_dgu] each
-    int64_t dgu_plane;
-    int ld_dgu;                                 // the columns from N up to the next multiple of 8 are zero
+    uint16_t *dg, *du;                          // kEpiGatedBwd: rows of ld_d values, the planes of one d_plane apart;
+    int d_plane, ld_d;                          // the columns from N up to the next multiple of 8 are zero
     int act;
     Dropout drop;
     float* partial;                             // not null: sums of one part of K each, [part, matrix, M, ld_part]
@@ -147,12 +146,10 @@ __device__ __forceinline__ void finish_gated_bwd(const EpiArgs& e, const DropKey
         g[i] = d[i] == 0.0f || i >= n ? 0.0f : d[i] * u[i] * slope;
         u[i] = d[i] == 0.0f || i >= n ? 0.0f : d[i] * value;
     }
-    constexpr int kPlanes = kF32 ? 3 : 1;
-    uint16_t* const p = e.dgu + row * e.ld_dgu + col;
-    store_planes<kF32>(p, e.dgu_plane, g);
-    store_planes<kF32>(p + kPlanes * e.dgu_plane, e.dgu_plane, u);
+    const int64_t at = row * e.ld_d + col;
+    store_planes<kF32>(e.dg + at, e.d_plane, g);
+    store_planes<kF32>(e.du + at, e.d_plane, u);
 }
-
 
 // One run of eight columns to where the epilogue puts it: v (and, gated, w: u where v is g), of matrix mat.
 template <int kEpi, bool kF32>

@@ -10,7 +10,7 @@
 
 namespace moe {
 
-// The planes' products, small ones first: the partial sums stay small until the last one.
+// The planes' products, small ones first.
 constexpr int kPlanePairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0}};
 
 // x as the sum of its first P planes (x0 rounds towards zero where the nearest would be infinite).  P = 2 keeps 16 bits
