@@ -372,15 +372,16 @@ struct Gemm {
     }
 };
 
+// Workgroup `block` of one product.
 template <class S, int kLA, int kLB, int kEpi>
-__global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
+__device__ __forceinline__ void gemm_block(const GemmArgs& g, unsigned block)
 {
     using G = Gemm<S, kLA, kLB, kEpi>;
     // consecutive tiles go to one XCD (workgroup b runs on XCD b % 8), in groups of 8 row tiles, so that the
     // workgroups of an XCD share rows of A and columns of B in its L2
     const int cols = g.nt * g.mats, tiles = g.mt * cols, total = tiles * g.e.parts;
     const int per = (total + kXcdCount - 1) / kXcdCount;
-    const int id = static_cast<int>(blockIdx.x % kXcdCount) * per + static_cast<int>(blockIdx.x / kXcdCount);
+    const int id = static_cast<int>(block % kXcdCount) * per + static_cast<int>(block / kXcdCount);
     if (id >= total)
         return;
     const int part = id / tiles, t = id - part * tiles;
@@ -442,6 +443,23 @@ __global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
             }
         }
     }
+}
+
+template <class S, int kLA, int kLB, int kEpi>
+__global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm(GemmArgs g)
+{
+    gemm_block<S, kLA, kLB, kEpi>(g, blockIdx.x);
+}
+
+// dx (workgroups below `first`, a multiple of the XCDs) and the weights' gradients in one launch: neither waits for the
+// other.
+template <class S>
+__global__ __launch_bounds__(S::kThreads, S::kBlocks) void gemm_pair(GemmArgs dx, GemmArgs dw, unsigned first)
+{
+    if (blockIdx.x < first)
+        gemm_block<S, kKC, kKC, kEpiOut>(dx, blockIdx.x);
+    else
+        gemm_block<S, kNC, kNC, kEpiOut>(dw, blockIdx.x - first);
 }
 
 // dg and du from the kept g and u.
@@ -559,42 +577,107 @@ using Float = Shape<2, 2, 2, 2, 1, 32, 3, 3>;
 int64_t steps_of(int dtype, int64_t K) { return ceil_div(K, dtype == MOE_F32 ? Float::kBK : Small::kBK); }
 static_assert(Large::kBK == Small::kBK, "one K step for bfloat16");
 
+// A product's size: M rows, N staged columns in all (both matrices'), steps of K.
+struct Size {
+    int64_t M, N, steps;
+    int64_t small() const { return ceil_div(M, Small::BM) * ceil_div(N, Small::BNB); }
+};
+static_assert(Float::BM == Small::BM && Float::BNB == Small::BNB, "counted alike");
+
 // How a product runs: its tiles, and into how many parts its steps are cut.
 struct GemmPlan {
     bool large;
     int parts;
+    double time;
 };
 
-// M rows, N staged columns in all (both matrices'), `steps` steps of K.  The times that decide, in us, are measured ones
-// (4096 x 4096 x 28672 and 512 x 1024 x 4096): a step of a large tile 1.75; of a small one 0.7, or 1.05 for two that
-// share a CU; of a float32 one 1.3; a workgroup's start and end 8 and 6.  Parts cost a launch of 4 and two passes of float32
-// sums at 3.5 TB/s, and give workgroups to CUs that had none: they are taken only below one small tile per CU.
-GemmPlan plan_gemm(int dtype, int64_t M, int64_t N, int64_t steps)
+// The times that decide, in us, are measured ones (4096 x 4096 x 28672 and 512 x 1024 x 4096): a step of a large tile 1.75;
+// of a small one 0.7, or 1.05 for two that share a CU; of a float32 one 1.3; a workgroup's start and end 8 and 6.
+constexpr int64_t kCus = 256;
+int64_t slots_of(int dtype) { return dtype == MOE_F32 ? kCus : 2 * kCus; }
+double step_time(int dtype, int64_t tiles) { return dtype == MOE_F32 ? 1.3 : tiles <= kCus ? 0.7 : 1.05; }
+// Parts cost a launch of 4 and two passes of float32 sums at 3.5 TB/s, and give workgroups to CUs that had none: a product
+// is cut only where all of its workgroups are resident at once, two together up to twice as many (22 x 2880 x 602, float32:
+// 230 workgroups of one step beside 23 of 38).
+double parts_time(const Size& z, int64_t parts)
 {
-    const bool f32 = dtype == MOE_F32;
-    const int64_t large = ceil_div(M, Large::BM) * ceil_div(N, Large::BNB), small = ceil_div(M, Small::BM) * ceil_div(N, Small::BNB);
-    constexpr int64_t kCus = 256;
-    const int64_t slots = f32 ? kCus : 2 * kCus;
-    const double one = f32 ? 1.3 : 0.7, full = f32 ? 1.3 : 1.05;
-    const auto small_time = [&](int64_t tiles, int64_t n) {
-        const int64_t rest = tiles % slots;
-        const double rounds = full * static_cast<double>(tiles / slots) + (rest == 0 ? 0.0 : rest <= kCus ? one : full);
-        return rounds * static_cast<double>(n) + 6.0 * static_cast<double>(ceil_div(tiles, slots));
-    };
-    GemmPlan best{!f32, 1};
-    double time = f32 ? 1e30 : static_cast<double>(ceil_div(large, kCus)) * (1.75 * static_cast<double>(steps) + 8.0);
-    for (int64_t p = 1; p <= 16 && (p == 1 || (small * p <= slots && steps >= 3 * p)); ++p) {
-        const double t = small_time(small * p, ceil_div(steps, p)) +
-                         (p == 1 ? 0.0 : 4.0 + static_cast<double>(8 * p * M * N) / 3.5e6);
-        if (t < time) {
-            time = t;
-            best = GemmPlan{false, static_cast<int>(p)};
-        }
+    return parts == 1 ? 0.0 : 4.0 + static_cast<double>(8 * parts * z.M * z.N) / 3.5e6;
+}
+constexpr int64_t kParts[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16};
+
+GemmPlan plan_gemm(int dtype, const Size& z)
+{
+    const int64_t large = ceil_div(z.M, Large::BM) * ceil_div(z.N, Large::BNB), small = z.small(), slots = slots_of(dtype);
+    GemmPlan best{true, 1, 1e30};
+    if (dtype != MOE_F32)
+        best.time = static_cast<double>(ceil_div(large, kCus)) * (1.75 * static_cast<double>(z.steps) + 8.0);
+    for (int64_t p : kParts) {
+        if (p > 1 && (small * p > slots || z.steps < 3 * p))
+            break;
+        const int64_t tiles = small * p, rest = tiles % slots;
+        const double rounds = step_time(dtype, slots) * static_cast<double>(tiles / slots) + (rest == 0 ? 0.0 : step_time(dtype, rest));
+        const double t = rounds * static_cast<double>(ceil_div(z.steps, p)) + 6.0 * static_cast<double>(ceil_div(tiles, slots)) +
+                         parts_time(z, p);
+        if (t < best.time)
+            best = GemmPlan{false, static_cast<int>(p), t};
     }
     return best;
 }
-static_assert(Float::BM == Small::BM && Float::BNB == Small::BNB, "counted alike");
 
+// How dx and the weights' gradients run: both in one launch of small tiles, or one after the other (5 us between them).
+struct PairPlan {
+    bool together;
+    GemmPlan dx, dw;
+};
+PairPlan plan_pair(int dtype, const Size& x, const Size& w)
+{
+    PairPlan best{false, plan_gemm(dtype, x), plan_gemm(dtype, w)};
+    double time = dtype == MOE_F32 ? 1e30 : best.dx.time + 5.0 + best.dw.time;
+    const int64_t slots = slots_of(dtype);
+    for (int64_t p : kParts)
+        for (int64_t q : kParts) {
+            const int64_t tx = x.small() * p, tw = w.small() * q, tiles = tx + tw;
+            if ((p > 1 && x.steps < 3 * p) || (q > 1 && w.steps < 3 * q) || (p * q > 1 && tiles > 2 * slots))
+                break;
+            const int64_t nx = ceil_div(x.steps, p), nw = ceil_div(w.steps, q);
+            // a launch of more workgroups than are resident evens out but for its last ones
+            const double steps = tiles <= slots ? static_cast<double>(std::max(nx, nw))
+                                                : static_cast<double>(tx * nx + tw * nw) / static_cast<double>(slots) +
+                                                      0.5 * static_cast<double>(std::max(nx, nw));
+            const double t = step_time(dtype, tiles) * steps + 6.0 * static_cast<double>(ceil_div(tiles, slots)) +
+                             parts_time(x, p) + parts_time(w, q);
+            if (t < time) {
+                time = t;
+                best = PairPlan{true, {false, static_cast<int>(p), 0.0}, {false, static_cast<int>(q), 0.0}};
+            }
+        }
+    return best;
+}
+
+// Bytes of a product's partial sums.
+int64_t partial_bytes(const Size& z, int parts) { return parts > 1 ? int64_t{4} * parts * z.M * z.N : 0; }
+
+// The rest of a product's arguments, by its plan.
+void set_plan(GemmArgs& g, const GemmPlan& plan, float* partial)
+{
+    g.e.M = g.M;
+    g.e.N = g.N;
+    g.e.mats = g.mats;
+    g.e.parts = plan.parts;
+    g.e.partial = plan.parts > 1 ? partial : nullptr;
+    g.e.ld_part = static_cast<int>(padded(g.N));
+}
+
+// Tiles of shape S, BN output columns each; returns the workgroups.
+template <class S>
+int64_t set_tiles(GemmArgs& g, int BN)
+{
+    g.mt = static_cast<int>(ceil_div(g.M, S::BM));
+    g.nt = static_cast<int>(ceil_div(g.N, BN));
+    return ceil_div(static_cast<int64_t>(g.mt) * g.nt * g.mats * g.e.parts, kXcdCount) * kXcdCount;
+}
+
+// A gated product's two matrices are columns of one tile.
 template <class S, int kLA, int kLB, int kEpi>
 hipError_t launch_shape(GemmArgs g, hipStream_t s)
 {
@@ -602,41 +685,69 @@ hipError_t launch_shape(GemmArgs g, hipStream_t s)
     static LdsLimit limit;
     if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gemm<S, kLA, kLB, kEpi>), S::kSmem); e != hipSuccess)
         return e;
-    g.mt = static_cast<int>(ceil_div(g.M, S::BM));
-    g.nt = static_cast<int>(ceil_div(g.N, G::BN));
-    const int64_t total = static_cast<int64_t>(g.mt) * g.nt * g.mats * g.e.parts;
-    gemm<S, kLA, kLB, kEpi><<<dim3(static_cast<unsigned>(ceil_div(total, kXcdCount) * kXcdCount)), S::kThreads, S::kSmem,
-                              s>>>(g);
+    if (G::kDual)
+        g.mats = 1;
+    const int64_t blocks = set_tiles<S>(g, G::BN);
+    gemm<S, kLA, kLB, kEpi><<<dim3(static_cast<unsigned>(blocks)), S::kThreads, S::kSmem, s>>>(g);
     return hipGetLastError();
 }
 
-// A product by its plan; parts of K leave their sums at `partial`, and a second launch makes the results of them.
-template <int kLA, int kLB, int kEpi>
-hipError_t launch_gemm(GemmArgs g, int dtype, float* partial, hipStream_t s)
+// Parts of K leave their sums; a second launch makes the results of them.
+hipError_t finish_parts(Epi epi, int dtype, const GemmArgs& g, hipStream_t s)
 {
-    constexpr bool kGated = kEpi != kEpiOut;
-    const int mats = kGated ? 2 : g.mats;
-    const GemmPlan plan = plan_gemm(dtype, g.M, static_cast<int64_t>(mats) * g.N, static_cast<int64_t>(g.nseg) * g.kt);
-    g.e.M = g.M;
-    g.e.N = g.N;
-    g.e.mats = mats;
-    g.e.parts = plan.parts;
-    g.e.partial = plan.parts > 1 ? partial : nullptr;
-    g.e.ld_part = static_cast<int>(padded(g.N));
-    hipError_t e;
-    if (dtype == MOE_F32)
-        e = launch_shape<Float, kLA, kLB, kEpi>(g, s);
-    else
-        e = plan.large ? launch_shape<Large, kLA, kLB, kEpi>(g, s) : launch_shape<Small, kLA, kLB, kEpi>(g, s);
-    return e != hipSuccess || plan.parts == 1 ? e : launch_gated_finish(static_cast<Epi>(kEpi), dtype, g.e, s);
+    return g.e.parts == 1 ? hipSuccess : launch_gated_finish(epi, dtype, g.e, s);
 }
 
-// Bytes of the partial sums of such a product.
-int64_t partial_bytes(int dtype, int64_t M, int64_t N, int mats, int64_t steps)
+// A product by its plan (float32 gradients run together, launch_pair).
+template <int kLA, int kLB, int kEpi>
+hipError_t launch_gemm(GemmArgs g, int dtype, const GemmPlan& plan, float* partial, hipStream_t s)
 {
-    const GemmPlan plan = plan_gemm(dtype, M, mats * N, steps);
-    return plan.parts > 1 ? int64_t{4} * plan.parts * mats * M * padded(N) : 0;
+    if (g.M == 0)
+        return hipSuccess;
+    set_plan(g, plan, partial);
+    hipError_t e = hipSuccess;
+    if (plan.large)
+        e = launch_shape<Large, kLA, kLB, kEpi>(g, s);
+    else if (dtype != MOE_F32)
+        e = launch_shape<Small, kLA, kLB, kEpi>(g, s);
+    else if constexpr (kEpi != kEpiOut)
+        e = launch_shape<Float, kLA, kLB, kEpi>(g, s);
+    return e != hipSuccess ? e : finish_parts(static_cast<Epi>(kEpi), dtype, g, s);
 }
+
+template <class S>
+hipError_t launch_together(GemmArgs& dx, GemmArgs& dw, hipStream_t s)
+{
+    static LdsLimit limit;
+    if (hipError_t e = limit.ensure(reinterpret_cast<const void*>(&gemm_pair<S>), S::kSmem); e != hipSuccess)
+        return e;
+    const int64_t first = set_tiles<S>(dx, S::BNB), rest = set_tiles<S>(dw, S::BNB);
+    gemm_pair<S><<<dim3(static_cast<unsigned>(first + rest)), S::kThreads, S::kSmem, s>>>(dx, dw, static_cast<unsigned>(first));
+    return hipGetLastError();
+}
+
+// dx and the weights' gradients by their plan.
+hipError_t launch_pair(GemmArgs& dx, GemmArgs& dw, int dtype, const PairPlan& plan, float* partial, int64_t dx_bytes,
+                       hipStream_t s)
+{
+    float* const dw_partial = partial + dx_bytes / 4;
+    if (!plan.together) {
+        const hipError_t e = launch_gemm<kKC, kKC, kEpiOut>(dx, dtype, plan.dx, partial, s);
+        return e != hipSuccess ? e : launch_gemm<kNC, kNC, kEpiOut>(dw, dtype, plan.dw, dw_partial, s);
+    }
+    set_plan(dx, plan.dx, partial);
+    set_plan(dw, plan.dw, dw_partial);
+    hipError_t e = dtype == MOE_F32 ? launch_together<Float>(dx, dw, s) : launch_together<Small>(dx, dw, s);
+    if (e == hipSuccess)
+        e = finish_parts(kEpiOut, dtype, dx, s);
+    return e != hipSuccess ? e : finish_parts(kEpiOut, dtype, dw, s);
+}
+
+// The products of a call.
+Size size_gu(const moe_gated& g) { return {g.T, 2 * padded(g.F), steps_of(g.dtype, g.H)}; }
+Size size_dx(const moe_gated& g) { return {g.T, padded(g.H), 2 * steps_of(g.dtype, g.F)}; }
+Size size_dw(const moe_gated& g) { return {g.H, 2 * padded(g.F), steps_of(g.dtype, g.T)}; }
+PairPlan plan_backward(const moe_gated& g) { return plan_pair(g.dtype, size_dx(g), size_dw(g)); }
 
 // Whether g and u come from the kernels for few rows.
 bool few_rows(const moe_gated& g) { return g.T <= kMaxRows && g.F >= kMinCols; }
@@ -663,12 +774,13 @@ GatedLayout gated_layout(const moe_gated& g, bool backward)
     int64_t partial = 0;                                  // of one product after the other
     if (g.T > 0) {
         const int64_t parts = rows ? gated_rows_parts(g.dtype, g.T, g.H, g.F) : 1;
-        partial = !rows ? partial_bytes(g.dtype, g.T, g.F, 2, steps_of(g.dtype, g.H))
-                        : parts > 1 ? 4 * 2 * parts * g.T * padded(g.F) : 0;
-        if (backward) {
-            partial = std::max(partial, partial_bytes(g.dtype, g.T, g.H, 1, 2 * steps_of(g.dtype, g.F)));
-            partial = std::max(partial, partial_bytes(g.dtype, g.H, g.F, 2, steps_of(g.dtype, g.T)));
-        }
+        partial = rows ? parts > 1 ? 4 * 2 * parts * g.T * padded(g.F) : 0
+                       : partial_bytes(size_gu(g), plan_gemm(g.dtype, size_gu(g)).parts);
+    }
+    if (backward) {
+        const PairPlan p = plan_backward(g);
+        L.dx_partial = partial_bytes(size_dx(g), p.dx.parts);
+        partial = std::max(partial, L.dx_partial + partial_bytes(size_dw(g), p.dw.parts));
     }
     take(L.partial, partial);
     L.total = off;
@@ -720,9 +832,9 @@ hipError_t launch_gu(const moe_gated& q, const void* x, const void* wg, const vo
     g.N = static_cast<int>(q.F);
     g.K = static_cast<int>(q.H);
     g.kc = static_cast<int>(padded(q.H));
-    g.mats = 1;
+    g.mats = 2;
     g.e = e;
-    return launch_gemm<kKC, kNC, kEpi>(g, q.dtype, partial, s);
+    return launch_gemm<kKC, kNC, kEpi>(g, q.dtype, plan_gemm(q.dtype, size_gu(q)), partial, s);
 }
 
 }  // namespace
@@ -788,26 +900,24 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
             if (err != hipSuccess)
                 return err;
         }
-        // dx [T, H]: K = F, the gate part, then the up part
-        GemmArgs c{};
-        c.a[0] = dg;
-        c.a[1] = du;
-        c.a_plane = plane;
-        c.b[0] = p.wg.p;
-        c.b[1] = p.wu.p;
-        c.b_plane = p.wg.plane;
-        c.nseg = 2;
-        c.kt = static_cast<int>(steps_of(q.dtype, q.F));
-        c.kc = static_cast<int>(padded(q.F));
-        c.lda = static_cast<int>(ldf);
-        c.ldb = p.wg.ld;
-        c.M = static_cast<int>(q.T);
-        c.N = static_cast<int>(q.H);
-        c.mats = 1;
-        c.e.o0 = dx;
-        if (hipError_t err = launch_gemm<kKC, kKC, kEpiOut>(c, q.dtype, partial, s); err != hipSuccess)
-            return err;
     }
+    // dx [T, H]: K = F, the gate part, then the up part
+    GemmArgs c{};
+    c.a[0] = dg;
+    c.a[1] = du;
+    c.a_plane = plane;
+    c.b[0] = p.wg.p;
+    c.b[1] = p.wu.p;
+    c.b_plane = p.wg.plane;
+    c.nseg = 2;
+    c.kt = static_cast<int>(steps_of(q.dtype, q.F));
+    c.kc = static_cast<int>(padded(q.F));
+    c.lda = static_cast<int>(ldf);
+    c.ldb = p.wg.ld;
+    c.M = static_cast<int>(q.T);
+    c.N = static_cast<int>(q.H);
+    c.mats = 1;
+    c.e.o0 = dx;
     // dWg and dWu [H, F]: K = T
     GemmArgs w{};
     w.a[0] = p.x.p;
@@ -825,7 +935,7 @@ hipError_t launch_gated_backward(const moe_gated& q, const Dropout& d, const voi
     w.mats = 2;
     w.e.o0 = dwg;
     w.e.o1 = dwu;
-    return launch_gemm<kNC, kNC, kEpiOut>(w, q.dtype, partial, s);
+    return launch_pair(c, w, q.dtype, plan_backward(q), partial, L.dx_partial, s);
 }
 
 }  // namespace moe

@@ -79,6 +79,7 @@ struct GatedLayout {
     size_t x = 0, wg = 0, wu = 0;      // operands laid out for the products, where the caller's are not already
     size_t dgu = 0;                    // backward: the gradients of g and u
     size_t partial = 0;                // sums over parts of K
+    int64_t dx_partial = 0;            // backward: bytes of dx's own, before those of the weights' gradients
     size_t total = 0;
 };
 GatedLayout gated_layout(const moe_gated& g, bool backward);
