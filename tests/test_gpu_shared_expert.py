@@ -131,7 +131,9 @@ SIZES = [(1, 1, 1), (1, 8, 8), (2, 7, 9), (1, 64, 64), (3, 65, 63), (16, 72, 136
          (300, 96, 1032), (1, 1000, 520), (5, 2056, 24), (31, 24, 2000),
          # few rows: every row block, K cut over workgroups and not, many columns
          (1, 4096, 264), (16, 2047, 65), (17, 1030, 8), (32, 777, 1003), (48, 600, 70), (64, 4100, 33), (3, 40, 8200),
-         (16, 4100, 130), (63, 3001, 70), (2, 8190, 9), (8, 33, 4), (50, 2000, 3), (64, 31, 6)]
+         (16, 4100, 130), (63, 3001, 70), (2, 8190, 9), (8, 33, 4), (50, 2000, 3), (64, 31, 6),
+         # the largest tiles, and more tiles than are resident at once
+         (2100, 1000, 2056), (1500, 129, 4001)]
 
 
 @TYPES
@@ -182,7 +184,9 @@ def test_gated_extreme_values(dtype):
 
 BWD_SIZES = [(1, 1, 1), (1, 8, 16), (2, 7, 9), (16, 72, 136), (33, 65, 63), (64, 128, 64), (65, 200, 100), (129, 257, 130),
              (130, 128, 264), (200, 136, 520), (300, 1000, 24), (7, 24, 1001),
-             (2, 2050, 70), (30, 1000, 40), (61, 3000, 200)]
+             (2, 2050, 70), (30, 1000, 40), (61, 3000, 200),
+             # both gradients in one launch in parts, and one after the other in tiles of every size
+             (700, 136, 520), (22, 2880, 602), (1300, 1000, 72), (4001, 4001, 264), (2001, 4001, 4001)]
 
 
 @TYPES
