@@ -290,8 +290,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     // Adds the lanes' rows to their bins' counters, returns each lane's place.  Rows of one request lie side by side:
     // a wave of one bin adds once (64 additions to one counter would take turns).
-    const auto add = [&](uint32_t t) {
-        const int a = ids[t], bin = a >= 0 && a < L ? a : L;
+    const auto add = [&](int a) {
+        const int bin = a >= 0 && a < L ? a : L;
         if (__all(bin == __builtin_amdgcn_readfirstlane(bin))) {
             const uint64_t active = __ballot(1);
             const int before = __popcll(active & ((uint64_t{1} << lane) - 1));
@@ -302,10 +302,23 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
         }
         return atomicAdd(&place[bin], 1);
     };
+    // Runs over this thread's rows, the loads of eight at a time ahead of their counters (one by one 8192 rows took 10 us).
+    const auto each = [&](auto use) {
+        constexpr int kAhead = 8;
+        for (int t0 = tid; t0 < T; t0 += kAhead * kPlanThreads) {
+            int id[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                id[i] = ids[min(t0 + i * kPlanThreads, T - 1)];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (t0 + i * kPlanThreads < T)
+                    use(id[i], t0 + i * kPlanThreads);
+        }
+    };
     place[tid] = 0;
     __syncthreads();
-    for (uint32_t t = tid; t < static_cast<uint32_t>(T); t += kPlanThreads)   // T + 1024 may pass 2^31
-        add(t);
+    each([&](int a, int) { add(a); });
     __syncthreads();
     // exclusive sums over the bins of rows and of tiles
     const int n = place[tid], nt = (n + kTile - 1) / kTile;
@@ -332,8 +345,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(const int32_t* __res
         rows[0] = tile0[0] = 0;
     place[tid] = s0 - n;
     __syncthreads();
-    for (uint32_t t = tid; t < static_cast<uint32_t>(T); t += kPlanThreads)
-        perm[add(t)] = static_cast<int32_t>(t);
+    each([&](int a, int t) { perm[add(a)] = t; });
     const int total = tile0[L + 1];
     if (tid == 0)
         count[0] = total;
