@@ -401,7 +401,7 @@ moe_status moe_mx_fc1_epilogue_encode(const float* v, int64_t rows, int64_t cols
  * their elements' alignment (rng: 8 bytes, the workspace: 16), except that the gated block reads
  * bfloat16 operands whose rows are whole 16-byte chunks where they lie: x with H % 8 == 0, w_gate and
  * w_up with F % 8 == 0 must be aligned to 16 bytes.  In the gated block's float32 products an infinite
- * factor makes the sums it takes part in NaN.  Deterministic.
+ * factor may make the sums it takes part in NaN.  Deterministic.
  * ------------------------------------------------------------------------------------------- */
 
 /* Dropout, wherever a call below takes `dropout` (p) and `rng`: D(v)[r,c] = 0 where bits(r,c) <
@@ -449,7 +449,7 @@ moe_status moe_gated_projection(const moe_gated* g, const void* x, const void* w
  *   dg = d u act'(g), du = d act(g)
  *   dx = dg Wg^T + du Wu^T     dw_gate = x^T dg     dw_up = x^T du
  * dh [T,F] -> dx [T,H], dw_gate and dw_up [H,F], all of dtype.  saved_gu: what the forward kept, or
- * NULL: g and u are computed again and never leave the registers.  For the products dg and du are
+ * NULL: g and u are computed again, in float32.  For the products dg and du are
  * rounded to bfloat16 (MOE_BF16) or kept to 24 bits (MOE_F32).  Where d is zero (a dropped place among
  * them) dg and du are zero, whatever g and u are.  T = 0 gives zero weight gradients.
  * Errors as for moe_gated_projection. */

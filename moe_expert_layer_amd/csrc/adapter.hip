@@ -11,6 +11,9 @@
 //     sums.  v enters the second product as two bfloat16 planes (16 bits) for bfloat16 tensors, as three for float32 ones.
 // A row's result does not depend on the tile that it falls into, so neither the order in which the plan's counters hand
 // out places nor other rows change it.
+// Measured: one row 4096 -> 14336 of rank 16 7.6 us, 64 rows of 32 adapters 4096 -> 4096 9.5; 8192 rows 14336 -> 4096 of
+// rank 64: plan 6.4, shrink 61-66 (3.7 TB/s), join 5, expand 49-58 (2.7 TB/s of base and out, whole rows of 256 bytes a run;
+// more workgroups, deeper loads or leaving out single parts change it by less than 10%).
 #include <algorithm>
 
 #include "dropout.h"
@@ -21,7 +24,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;                 // rows per tile
-constexpr int kExpandGrid = 768;         // expand_kernel: three workgroups per CU (512: 54 us against 48 at 8192 x 4096, rank 64)
+constexpr int kExpandGrid = 768;          // expand_kernel: three workgroups per CU (512: 54 us against 48 at 8192 x 4096, rank 64)
 
 template <class T>
 __device__ __forceinline__ float to_float(T v)

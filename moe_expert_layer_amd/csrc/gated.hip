@@ -567,8 +567,15 @@ hipError_t prepare(int dtype, const Source (&in)[kCount], Planes* (&out)[kCount]
     return hipSuccess;
 }
 
-// bfloat16: large tiles of 256 x 256, 8 waves of 64 x 128, one workgroup per CU; small ones of 128 x 128, 4 waves of
-// 64 x 64, two.  float32: 128 x 128, 4 waves of 64 x 64, one.
+// bfloat16: large tiles of 256 x 256, 8 waves of 64 x 128, one workgroup per CU.  4096 tokens, H = 4096, F = 14336: the
+// gated product 810-860 us, dx 740-770, dWg and dWu 790-835 (1.1-1.3 PF).  The matrix cores are busy 60-66% of the cycles
+// at the 1.7 GHz that the chip's power leaves (2.5 GHz in short products): stages of 32 k, four or five of them, took 4-8%
+// longer, other groupings of tiles, orders of the copies and wave priorities nothing off.
+// Small ones of 128 x 128, 4 waves of 64 x 64, two workgroups per CU, for products that leave CUs without a large tile: LDS
+// bounds them (16 KiB of fragments per 16 MFMAs); 4 stages of 32 k: the same times.
+// float32: 128 x 128, 4 waves of 64 x 64, one.  A stage holds all planes, so six products come of the reads that one plane
+// product takes twice: 1000 x 1001 x 1365 54 us with the products one after the other, 46 so; the matrix cores are busy
+// 41-50% of the cycles of the CUs that have a tile.  Planes interleaved in memory, for longer runs: the same time.
 using Large = Shape<4, 2, 2, 4, 1, 64, 1, 2>;
 using Small = Shape<2, 2, 2, 2, 2, 64, 1, 2>;
 using Float = Shape<2, 2, 2, 2, 1, 32, 3, 3>;
