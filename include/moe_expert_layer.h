@@ -401,7 +401,8 @@ moe_status moe_mx_fc1_epilogue_encode(const float* v, int64_t rows, int64_t cols
  * their elements' alignment (rng: 8 bytes, the workspace: 16), except that the gated block reads
  * bfloat16 operands whose rows are whole 16-byte chunks where they lie: x with H % 8 == 0, w_gate and
  * w_up with F % 8 == 0 must be aligned to 16 bytes.  In the gated block's float32 products an infinite
- * factor may make the sums it takes part in NaN.  Deterministic.
+ * factor may make the sums it takes part in NaN.  Outputs and workspace overlap no other buffer except
+ * where a call says so.  Deterministic.
  * ------------------------------------------------------------------------------------------- */
 
 /* Dropout, wherever a call below takes `dropout` (p) and `rng`: D(v)[r,c] = 0 where bits(r,c) <

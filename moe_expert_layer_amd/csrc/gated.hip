@@ -13,7 +13,6 @@
 // bfloat16 operands go to v_mfma_f32_32x32x16_bf16 as they are, float32 operands as three bfloat16 planes (planes.h), all
 // of them in one stage: the product of the first planes has a sum of its own, the five small ones share another.
 #include <algorithm>
-#include <atomic>
 #include <utility>
 
 #include "gated_epilogue.h"
