@@ -469,7 +469,7 @@ moe_status moe_gated_projection_backward(const moe_gated* g, const void* x, cons
 typedef struct moe_adapter {
     int64_t T;            /* rows, at most 2^28                                                  */
     int64_t K;            /* width of x, at most MOE_MAX_HIDDEN                                  */
-    int64_t N;            /* width of base and out, at most MOE_MAX_HIDDEN                       */
+    int64_t N;            /* width of base and out, at most MOE_MAX_HIDDEN; T K, T N at most 2^37 */
     int64_t L;            /* adapters, 1 .. 1023                                                 */
     int64_t R;            /* largest rank, 1 .. 128                                              */
     int32_t dtype;        /* MOE_F32 or MOE_BF16                                                 */

@@ -611,34 +611,42 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const uint32_t lds = static_cast<uint32_t>(
         reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) unsigned char*)(smem)));
-    const int runs = (g.N + 127) / 128, col = 8 * (tid % 16), row0 = tid / 16;   // this thread: rows row0 + 16 i
-    const int64_t items = static_cast<int64_t>(p.count[0]) * runs;
-    const int64_t item1 = items * (blockIdx.x + 1) / gridDim.x;
-    for (int64_t item = items * blockIdx.x / gridDim.x; item < item1;) {
-        const int ti = static_cast<int>(item / runs), run0 = static_cast<int>(item - static_cast<int64_t>(ti) * runs);
-        const int run1 = static_cast<int>(min(static_cast<int64_t>(runs), run0 + item1 - item));
+    const uint32_t runs = (g.N + 127) / 128;
+    const int col = 8 * (tid % 16), row0 = tid / 16;   // this thread: rows row0 + 16 i
+    // T N is at most 2^37: fewer than 2^32 pairs
+    const uint32_t items = static_cast<uint32_t>(p.count[0]) * runs, per = items / gridDim.x, more = items % gridDim.x;
+    const uint32_t item1 = per * (blockIdx.x + 1) + min(blockIdx.x + 1, more);
+    for (uint32_t item = per * blockIdx.x + min(blockIdx.x, more); item < item1;) {
+        const int ti = static_cast<int>(item / runs), run0 = static_cast<int>(item - static_cast<uint32_t>(ti) * runs);
+        const int run1 = static_cast<int>(min(runs, run0 + item1 - item));
         item += run1 - run0;
         const Tile tile = p.tiles[ti];
         const int n0 = 128 * run0, n1 = min(128 * run1, g.N), n = tile.end - tile.begin;
         const int rank = tile.adapter < g.L ? rank_of(g, tile.adapter) : 0;
-        if (rank == 0) {                                  // the rows are copied, a wave each
-            if (g.base != g.out)
-                for (int r = wave; r < n; r += kThreads / 64) {
-                    const int64_t at = static_cast<int64_t>(p.perm[tile.begin + r]) * g.N;
-                    for (int c = n0 + 8 * lane; c < n1; c += 512) {
-                        float w[8];
-                        load8(w, static_cast<const T*>(g.base) + at + c, n1 - c);
-                        store8(static_cast<T*>(g.out) + at + c, w, n1 - c);
-                    }
-                }
+        if (rank == 0 && g.base == g.out)
             continue;
-        }
         int64_t at[4];                                    // rows past the last repeat it and are not written
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             at[i] = static_cast<int64_t>(p.perm[tile.begin + min(row0 + 16 * i, n - 1)]) * g.N;
-        const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(tile.adapter) * g.R * g.N;
         Raw8<T> bv[kLoads], base[4];
+        if (rank == 0) {                                  // the rows are copied (one by one a tile took 9 us)
+            for (int c = n0 + col; c < n1; c += 128) {
+                const int from = min(c, g.N - 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    base[i] = load_raw<true>(static_cast<const T*>(g.base) + at[i] + from, 8);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float w[8];
+                    base[i].values(w);
+                    if (row0 + 16 * i < n)
+                        store_from(static_cast<T*>(g.out) + at[i], from, c, w);
+                }
+            }
+            continue;
+        }
+        const T* const B = static_cast<const T*>(g.b) + static_cast<int64_t>(tile.adapter) * g.R * g.N;
         const auto fetch = [&](int c0) {
             const int from = min(c0 + col, g.N - 8);      // the row's last 8 columns where these would pass its end
 #pragma unroll

@@ -1595,6 +1595,8 @@ moe_status check_adapter(const moe_adapter* p)
     if (p->T > kMaxSharedRows || p->K > MOE_MAX_HIDDEN || p->N > MOE_MAX_HIDDEN || p->L > kMaxAdapters || p->R > kMaxRank)
         return fail(MOE_ERR_UNSUPPORTED, "T must be at most 2^28, K and N at most %d, L at most %d, R at most %d", MOE_MAX_HIDDEN,
                     kMaxAdapters, kMaxRank);
+    if (std::max(p->T * p->K, p->T * p->N) > int64_t{1} << 37)
+        return fail(MOE_ERR_UNSUPPORTED, "T * K and T * N must be at most 2^37");
     return check_plain_dtype(p->dtype);
 }
 

@@ -115,6 +115,7 @@ def _adapter(mel, **kw):
     (dict(), 0), (dict(T=0), 0), (dict(K=1, N=1, L=1, R=1), 0), (dict(R=128, L=1023), 0), (dict(dtype=0), 0),
     (dict(T=-1), 1), (dict(K=0), 1), (dict(N=0), 1), (dict(L=0), 1), (dict(R=0), 1), (dict(reserved=1), 1),
     (dict(R=129), 2), (dict(L=1024), 2), (dict(dtype=2), 2), (dict(T=(1 << 28) + 1), 2), (dict(K=(1 << 22) + 1), 2),
+    (dict(T=1 << 28, K=512, N=512), 0), (dict(T=1 << 28, K=513), 2), (dict(T=1 << 28, N=513), 2),
     (dict(N=(1 << 22) + 1), 2),
 ])
 def test_adapter_sizes(mel, kw, expected):
