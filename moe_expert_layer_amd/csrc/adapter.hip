@@ -12,8 +12,7 @@
 // A row's result does not depend on the tile that it falls into, so neither the order in which the plan's counters hand
 // out places nor other rows change it.
 // Measured: one row 4096 -> 14336 of rank 16 7.6 us, 64 rows of 32 adapters 4096 -> 4096 9.5; 8192 rows 14336 -> 4096 of
-// rank 64: plan 6.4, shrink 61-66 (3.7 TB/s), join 5, expand 49-58 (2.7 TB/s of base and out, whole rows of 256 bytes a run;
-// more workgroups, deeper loads or leaving out single parts change it by less than 10%).
+// rank 64: plan 6.5, shrink 54-67 (3.5-4.3 TB/s), join 5, expand 32 (4.4 TB/s of base, out and v).
 #include <algorithm>
 
 #include "dropout.h"
@@ -24,7 +23,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTile = 64;                 // rows per tile
-constexpr int kExpandGrid = 768;          // expand_kernel: three workgroups per CU (512: 54 us against 48 at 8192 x 4096, rank 64)
 
 template <class T>
 __device__ __forceinline__ float to_float(T v)
@@ -92,11 +90,12 @@ __device__ __forceinline__ void store_from(T* row, int from, int first, const fl
 
 constexpr int kRowThreads = 1024;         // 16 waves: a CU has one or two of these workgroups, and 128 KiB in flight
 constexpr int kRowWaves = kRowThreads / 64;
-// Rows up to which row_kernel is taken.  8 x 128 -> 128: 512 rows 13 us against 23 and three more launches, 2048 rows 49
-// against 23; 16 x 4096 -> 4096: 1000 rows 31 against 28.  Its reads of A and B count too, see plan(): 300 rows of rank 64,
-// 300 MiB, 36 us against 26.
-constexpr int64_t kMaxRowTokens = 1024;
-constexpr int64_t kMaxRowReads = int64_t{256} << 20;
+// Rows and bytes of A and B up to which row_kernel is taken (us of single rows against tiles with 1.5 between launches).
+// Rows: 128 -> 128 of rank 8 bfloat16, 700 rows 14.6 / 17.4, 1024 rows 19.0 / 17.8; 1024 -> 1024 of rank 16, 700 rows 19.2
+// / 22.5, 1000 rows 25.3 / 23.2.  Bytes, 4096 -> 4096: bfloat16 of rank 16, 131 MB 18.3 / 24.3, 184 MB 24.6 / 25.2, of rank
+// 64, 157 MB 30.3 / 25.5; float32, whose planes make the tiles dearer, of rank 16, 268 MB 25.5 / 44.8.
+constexpr int64_t kMaxRowTokens = 896;
+constexpr int64_t max_row_reads(int64_t size) { return int64_t{size == 2 ? 144 : 256} << 20; }
 
 // Workgroup (t, c): row t, output columns [c cols, (c + 1) cols).  Threads take (k, 8 columns of A) and add over k, then
 // (r, 8 columns of B) and add over r; both are joined in a fixed order, within the wave and then through LDS.  Loads go
@@ -597,11 +596,14 @@ struct ExpandLds {
     static constexpr int kVRow = 2 * kR + 16, kVPlane = kTile * kVRow;
     static constexpr int kV = PB * kPlane > kTile * kOutRow ? PB * kPlane : kTile * kOutRow;   // where v begins
     static constexpr int kBytes = kV + PV * kVPlane;
+    // Workgroups: those resident, three per CU at most (8192 x 4096, rank 64: 32 us, 512 of them 35, 1024 36; rank 100,
+    // where two fit: 2000 x 11776 36, 768 of them 41).
+    static constexpr int kGrid = 256 * (160 * 1024 / kBytes < 3 ? 160 * 1024 / kBytes : 3);
 };
 
 // out.  The work is the (tile, run of 128 columns) pairs in order, in equal shares for the workgroups of the grid.  For the
 // product each of the four waves takes 32 columns of all 64 rows; for base and out, whole rows of a run (256 or 512 bytes;
-// with pieces of 32 rows, as the accumulators hold them, 8192 x 4096 of rank 64 took 60 us instead of 54).
+// with pieces of 32 rows, as the accumulators hold them, 8192 x 4096 of rank 64 took 6 us longer).
 template <class T, int kRB>
 __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
 {
@@ -750,7 +752,7 @@ Plan plan(const moe_adapter& p)
     if (q.narrow)
         return q;
     q.rows = p.T <= kMaxRowTokens && p.K * p.R * size <= (int64_t{1} << 20) &&
-             p.T * (p.K + p.N) * p.R * size <= kMaxRowReads;
+             p.T * (p.K + p.N) * p.R * size <= max_row_reads(size);
     if (q.rows) {
         // about 256 workgroups, 64 columns at least
         const int64_t per_row = std::clamp<int64_t>(ceil_div(256, std::max<int64_t>(p.T, 1)), 1, ceil_div(p.N, 64));
@@ -761,7 +763,8 @@ Plan plan(const moe_adapter& p)
     q.steps = static_cast<int>(ceil_div(p.K, q.blocks == 4 ? 64 : 128));
     q.max_tiles = ceil_div(p.T, kTile) + std::min(p.T, p.L + 1);
     const int64_t tiles = ceil_div(p.T, kTile);
-    q.splits = static_cast<int>(std::clamp<int64_t>(ceil_div(512, tiles), 1, std::clamp<int64_t>(q.steps / 4, 1, 16)));
+    // about 1024 workgroups of the shrink (512: 5000 x 11776 of rank 32 52 us against 40, float32 of rank 128 105 against 80)
+    q.splits = static_cast<int>(std::clamp<int64_t>(ceil_div(1024, tiles), 1, std::clamp<int64_t>(q.steps / 4, 1, 16)));
     return q;
 }
 
@@ -783,7 +786,7 @@ hipError_t launch_tiles(const Args& g, const TileArgs& t, const Plan& q, hipStre
             return e;
     }
     const int64_t items = q.max_tiles * ceil_div(g.N, 128);
-    expand_kernel<T, kRB><<<dim3(static_cast<unsigned>(std::min<int64_t>(items, kExpandGrid))), kThreads, kExpandLds, s>>>(g, t);
+    expand_kernel<T, kRB><<<dim3(static_cast<unsigned>(std::min<int64_t>(items, ExpandLds<T, kRB>::kGrid))), kThreads, kExpandLds, s>>>(g, t);
     return hipGetLastError();
 }
 
