@@ -65,8 +65,17 @@ __device__ __forceinline__ void shift_a(Raw8<float>& r, int skip)
         r.b = f32x4_t{r.b[1], r.b[2], r.b[3], 0.0f};
     }
 }
-// Whether loads of an adapter's A may pass the tensor's end: the last adapter, with rows that are not whole runs of eight.
-__device__ __forceinline__ bool past_end(const Args& g, int a) { return a == g.L - 1 && g.R % 8 != 0; }
+// Whether loads of an adapter's A may pass the tensor's end: rows that are not whole runs of eight, and fewer than eight
+// values behind the adapter (it is the last one, or the ones after it hold few).
+__device__ __forceinline__ bool past_end(const Args& g, int a)
+{
+    return g.R % 8 != 0 && static_cast<int64_t>(g.L - 1 - a) * g.K * g.R < 8;
+}
+// How far the load of eight values from `at` on was moved back to end with the tensor.
+__device__ __forceinline__ int moved_back(int64_t at, int64_t total)
+{
+    return static_cast<int>(max(at + 8 - total, static_cast<int64_t>(0)));
+}
 
 // Writes eight columns [from, from + 8) of a row, those before `first` left out (they are another thread's).
 template <class T>
@@ -153,7 +162,7 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
             if (past_end(g, a))
 #pragma unroll
                 for (int i = 0; i < kBatch; ++i)
-                    shift_a(w[i], max(0, static_cast<int>(a0 + static_cast<int64_t>(min(k0 + i * stride, g.K - 1)) * g.R + c + 8 - total)));
+                    shift_a(w[i], moved_back(a0 + static_cast<int64_t>(min(k0 + i * stride, g.K - 1)) * g.R + c, total));
 #pragma unroll
             for (int i = 0; i < kBatch; ++i) {
                 float f[8];
@@ -458,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
         if (past_end(g, tile.adapter))
 #pragma unroll
             for (int i = 0; i < kLoads; ++i)
-                shift_a(av[i], max(0, static_cast<int>(place(step, i) + 8 - total)));
+                shift_a(av[i], moved_back(place(step, i), total));
         __syncthreads();                                  // the stage of the step before is read
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {

@@ -1,0 +1,56 @@
+"""The shared expert's operators on the GPU where their kernels change hands or their values stop being ordinary: few values,
+infinities, the tails of the activations, operands that need all their bits, the limits between the ways a call runs."""
+import pytest
+
+import shared_expert_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+mel = pytest.importorskip("moe_expert_layer_amd")
+
+BF, F32 = torch.bfloat16, torch.float32
+TYPES = pytest.mark.parametrize("dtype", [BF, F32], ids=["bf16", "f32"])
+ACTS = pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    torch.cuda.set_device(0)
+
+
+def randn(seed, *shape, dtype=F32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (scale * torch.randn(shape, generator=g)).to(dtype).cuda()
+
+
+def poisoned(nbytes):
+    """A workspace that holds NaN in every type."""
+    return torch.full((max(nbytes, 1),), 0xFF, dtype=torch.uint8, device="cuda")
+
+
+def adapter_ops(T, K, N, L, R, dtype):
+    """base, x, A, B and ids, every adapter used and some rows without one."""
+    ids = (torch.arange(T) % (L + 1) - 1).to(torch.int32).cuda()
+    return (randn(1, T, N, dtype=dtype), randn(2, T, K, dtype=dtype), randn(3, L, K, R, dtype=dtype, scale=K ** -0.5),
+            randn(4, L, R, N, dtype=dtype, scale=R ** -0.5), ids)
+
+
+def add_adapters(base, x, a, b, ids, **kw):
+    (T, K), (L, _, R), N = x.shape, a.shape, base.shape[1]
+    ws = poisoned(mel.adapter_workspace_size(T, K, N, L, R, mel.BF16 if x.dtype == BF else mel.F32))
+    return mel.adapter_add(base, x, a, b, ids, workspace=ws, **kw)
+
+
+# ------------------------------------------------------------------------------------------- adapters
+
+@TYPES
+@pytest.mark.parametrize("T", [25, 1000])
+@pytest.mark.parametrize("K,R,L", [(1, 1, 16), (1, 3, 5), (2, 2, 2), (4, 1, 2), (6, 1, 3), (3, 2, 9), (1, 7, 3), (7, 1, 2)])
+def test_adapters_of_fewer_than_eight_values(dtype, T, K, R, L):
+    """Eight values from inside such an adapter on may pass the tensor's end, whichever adapter it is; single rows and tiles."""
+    ops = adapter_ops(T, K, 19, L, R, dtype)
+    ref.close(add_adapters(*ops), *ref.adapter(*ops, None, None), "adapter")
