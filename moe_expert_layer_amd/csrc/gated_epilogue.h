@@ -59,7 +59,8 @@ __device__ __forceinline__ void activation(int act, float g, float& value, float
     if (act == MOE_ACT_GELU) {
         const float x = 0.70710678118654752f * fabsf(g), x2 = x * x;
         const float e = exp_minus<kF32>(x2, fmaf(x, x, -x2));
-        const float t = reciprocal(fmaf(0.54f, x, 1.0f));
+        // the reciprocal of infinity would come out NaN; e is zero from far below 1e18 on
+        const float t = reciprocal(fmaf(0.54f, fminf(x, 1e18f), 1.0f));
         float p = 0.022005289793014526f;
         p = fmaf(p, t, -0.13662242889404297f);
         p = fmaf(p, t, 0.3370496928691864f);

@@ -54,3 +54,43 @@ def test_adapters_of_fewer_than_eight_values(dtype, T, K, R, L):
     """Eight values from inside such an adapter on may pass the tensor's end, whichever adapter it is; single rows and tiles."""
     ops = adapter_ops(T, K, 19, L, R, dtype)
     ref.close(add_adapters(*ops), *ref.adapter(*ops, None, None), "adapter")
+
+
+# ------------------------------------------------------------------------------------------- gated block: values
+
+def coded(t):
+    """Numbers that compare in place of infinities and NaN."""
+    return torch.nan_to_num(t.double(), nan=7e40, posinf=1e40, neginf=-1e40)
+
+
+@TYPES
+@ACTS
+@pytest.mark.parametrize("T", [1, 70])
+def test_gated_gates_that_are_not_finite(dtype, act, T):
+    """Finite factors whose product is past the type's range, and a NaN.  By the formulas act(+inf) is +inf; act(-inf) is
+    -inf times zero, NaN."""
+    x = torch.full((T, 1), 3e38, dtype=dtype, device="cuda")
+    wg = torch.tensor([[2.0, -2.0, NAN, 0.0, 2.0]], dtype=dtype, device="cuda")
+    wu = torch.tensor([[2.0 ** -120, 2.0 ** -120, 2.0 ** -120, 2.0 ** -120, -(2.0 ** -120)]], dtype=dtype, device="cuda")
+    kept = torch.empty((2, T, 5), dtype=dtype, device="cuda")
+    h = mel.gated_projection(x, wg, wu, activation=act, saved_gu=kept)
+    want = torch.tensor([INF, NAN, NAN, 0.0, -INF], device="cuda").expand(T, 5)
+    assert torch.equal(coded(h), coded(want)), h[0]
+    gates = torch.tensor([INF, -INF, NAN, 0.0, INF], device="cuda").expand(T, 5)
+    assert torch.equal(coded(kept[0]), coded(gates)), kept[0, 0]
+
+
+@TYPES
+@ACTS
+def test_gated_backward_from_infinite_gates(dtype, act):
+    """At g = +inf the slope is 1: dg = d u, and du = +inf.  A NaN gate gives NaN in its own column alone."""
+    T = 5
+    kept = torch.ones((2, T, 3), dtype=dtype, device="cuda")
+    kept[0, :, 0], kept[0, :, 1], kept[0, :, 2], kept[1] = INF, 0.0, NAN, 2.0
+    one = torch.ones((T, 3), dtype=dtype, device="cuda")
+    x, w = torch.ones((T, 1), dtype=dtype, device="cuda"), torch.ones((1, 3), dtype=dtype, device="cuda")
+    _, dwg, dwu = mel.gated_projection_backward(x, w, w, one, activation=act, saved_gu=kept)
+    assert float(dwg[0, 0]) == 2.0 * T and float(dwg[0, 1]) == T and bool(torch.isnan(dwg[0, 2]))
+    assert float(dwu[0, 1]) == 0.0 and bool(torch.isnan(dwu[0, 2]))
+    if dtype == BF:                                        # float32 products of an infinite factor may be NaN
+        assert float(dwu[0, 0]) == INF
