@@ -28,8 +28,8 @@ struct EpiArgs {
     int ld_part, parts, mats;                   // N rounded up to 8; parts of K; matrices (two in the gated ones)
 };
 
-// exp(-x) for x >= 0 (lo: what x lacks of the exact argument).  kF32: the parts of x log2 e that its rounding loses are
-// put back, which leaves the hardware's 2^y (1 ulp) as the error; else the error is that of the argument, 2^-24 of it.
+// exp(-x) for x >= 0 (lo: what x lacks of the exact argument).  kF32: lo and the parts of x log2 e that its rounding loses
+// are put back, which leaves the hardware's 2^y (1 ulp) as the error; else the error is that of the argument: 2^-23 of it.
 template <bool kF32>
 __device__ __forceinline__ float exp_minus(float x, float lo = 0.0f)
 {
@@ -49,16 +49,36 @@ __device__ __forceinline__ float reciprocal(float x)
     return fmaf(r, fmaf(-x, r, 1.0f), r);
 }
 
-// act(g) and its slope.  silu and gelu's tanh form are g s(z) with the logistic function s: z = g, and
-// z = 2 sqrt(2 / pi) (g + 0.044715 g^3) since (1 + tanh y) / 2 = s(2 y).  gelu takes the normal distribution function from
-// exp(-x^2) erfcx(x) / 2 with x = |g| / sqrt 2, erfcx(x) / 2 = t P(t), t = 1 / (1 + 0.54 x): P of degree 9 was fitted to
-// float64 values of erfcx on [0, 14.5] by weighted least squares, relative error 3e-7 in float32.
+// z = 2 sqrt(2 / pi) (g + 0.044715 g^3) and what it lacks of the exact value (kF32), every product's and sum's rest taken
+// along: rounded alone, z of -66 at g = -9 would put 1.4e-5 into exp(z).
+template <bool kF32>
+__device__ __forceinline__ float tanh_argument(float g, float& lo)
+{
+    constexpr float kA = 1.5957691669464111328125f, kALow = -4.534068e-8f;         // 2 sqrt(2 / pi) and what it lacks
+    constexpr float kB = 0.0447149984538555145263671875f, kBLow = 1.5461445e-9f;    // 0.044715 and what it lacks
+    const float s = g * g, p = fmaf(kB, s, 1.0f), v = g * p, z = kA * v;
+    if constexpr (kF32) {
+        // p - 1 is exact
+        const float p_lo = fmaf(kB, s, 1.0f - p) + fmaf(kB, fmaf(g, g, -s), kBLow * s);
+        const float v_lo = fmaf(g, p_lo, fmaf(g, p, -v));
+        lo = fmaf(kA, v, -z) + fmaf(kA, v_lo, kALow * v);
+    } else {
+        lo = 0.0f;
+    }
+    return z;
+}
+
+// act(g) and its slope.  silu and gelu's tanh form are g s(z) with the logistic function s: z = g, or tanh_argument since
+// (1 + tanh y) / 2 = s(2 y).  gelu takes the normal distribution function from exp(-g^2 / 2) erfcx(x) / 2 with
+// x = |g| / sqrt 2, erfcx(x) / 2 = t P(t), t = 1 / (1 + 0.54 x): P of degree 9 was fitted to float64 values of erfcx on
+// [0, 14.5] by weighted least squares, relative error 3e-7 in float32.  The exponent is taken from g, whose half is exact,
+// not from the rounded x (1.2e-5 at g = -13).  Values are right to 2^-20 in float32 calls.
 template <bool kF32>
 __device__ __forceinline__ void activation(int act, float g, float& value, float& slope)
 {
     if (act == MOE_ACT_GELU) {
-        const float x = 0.70710678118654752f * fabsf(g), x2 = x * x;
-        const float e = exp_minus<kF32>(x2, fmaf(x, x, -x2));
+        const float x = 0.70710678118654752f * fabsf(g), half = 0.5f * g, x2 = half * g;
+        const float e = exp_minus<kF32>(x2, fmaf(half, g, -x2));
         // the reciprocal of infinity would come out NaN; e is zero from far below 1e18 on
         const float t = reciprocal(fmaf(0.54f, fminf(x, 1e18f), 1.0f));
         float p = 0.022005289793014526f;
@@ -78,9 +98,10 @@ __device__ __forceinline__ void activation(int act, float g, float& value, float
         return;
     }
     constexpr float kA = 1.5957691216057308f, kB = 0.044715f;
-    const float z = act == MOE_ACT_SILU ? g : kA * (g + kB * g * g * g);
+    float lo = 0.0f;
+    const float z = act == MOE_ACT_SILU ? g : tanh_argument<kF32>(g, lo);
     const float dz = act == MOE_ACT_SILU ? 1.0f : kA * (1.0f + 3.0f * kB * g * g);
-    const float e = exp_minus<kF32>(fabsf(z)), r = reciprocal(1.0f + e);
+    const float e = exp_minus<kF32>(fabsf(z), z < 0.0f ? -lo : lo), r = reciprocal(1.0f + e);
     const float s = z < 0.0f ? e * r : r, t = z < 0.0f ? r : e * r;    // s(z) and 1 - s(z)
     value = g * s;
     const float st = s * t;

@@ -1,5 +1,7 @@
 """The shared expert's operators on the GPU where their kernels change hands or their values stop being ordinary: few values,
 infinities, the tails of the activations, operands that need all their bits, the limits between the ways a call runs."""
+import math
+
 import pytest
 
 import shared_expert_reference as ref
@@ -94,3 +96,37 @@ def test_gated_backward_from_infinite_gates(dtype, act):
     assert float(dwu[0, 1]) == 0.0 and bool(torch.isnan(dwu[0, 2]))
     if dtype == BF:                                        # float32 products of an infinite factor may be NaN
         assert float(dwu[0, 0]) == INF
+
+
+def activation(g, act):
+    """Value and slope in float64; the tanh form by the logistic function, (1 + tanh y) / 2 = s(2 y), since 1 + tanh y cancels
+    to nothing far out."""
+    if act != "gelu_tanh":
+        return ref.activation(g, act)
+    a, b = (8 / math.pi) ** 0.5, 0.044715
+    z = a * (g + b * g ** 3)
+    s = torch.sigmoid(z)
+    return g * s, s + g * s * torch.sigmoid(-z) * a * (1 + 3 * b * g * g)
+
+
+@ACTS
+@pytest.mark.parametrize("T", [1, 70])
+def test_activations_to_float32(act, T):
+    """One product by 1, so that the gate is exact: what is left is the function.  Its roundings: the hardware's 2^y 2^-23
+    and what puts the argument's rest back 2^-24; the reciprocal and 1 + e 2^-23 and 2^-24; three products 3 2^-24; gelu's
+    fit 3e-7 < 5 2^-24 and its argument 2^-23: at most 15 2^-24, below 2^-20.  Down to where e^-z leaves float32's range."""
+    low = {"silu": -80.0, "gelu": -12.5, "gelu_tanh": -9.5}[act]
+    g = torch.cat([torch.linspace(low, 12.0, 4001), torch.logspace(-20, -1, 200), -torch.logspace(-20, -1, 200)]).cuda()[None]
+    one = torch.ones((T, 1), device="cuda")
+    h = mel.gated_projection(one, g, torch.ones_like(g), activation=act)
+    want = activation(g.double(), act)[0].expand(T, -1)
+    assert bool(((h.double() - want).abs() <= 2.0 ** -20 * want.abs()).all()), \
+        float(((h.double() - want).abs() / want.abs()).max())
+    # the slope, from the gradient's first factor: dwg = x dh u act'(g)
+    dh = torch.zeros((T, g.shape[1]), device="cuda")
+    dh[0] = 1.0
+    dwg = mel.gated_projection_backward(one, g, torch.ones_like(g), dh, activation=act)[1]
+    value, slope = activation(g.double(), act)
+    # s + g s (1 - s) z' and its like, which cancel near the slope's zero; the second term has a few roundings more
+    terms = slope.abs() + 2 * (slope - value / g.double()).abs()
+    assert bool(((dwg.double() - slope).abs() <= 2.0 ** -19 * terms + 1e-37).all())
