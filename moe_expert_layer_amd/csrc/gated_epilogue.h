@@ -28,18 +28,44 @@ struct EpiArgs {
     int ld_part, parts, mats;                   // N rounded up to 8; parts of K; matrices (two in the gated ones)
 };
 
-// exp(-x) for x >= 0 (lo: what x lacks of the exact argument).  kF32: lo and the parts of x log2 e that its rounding loses
-// are put back, which leaves the hardware's 2^y (1 ulp) as the error; else the error is that of the argument: 2^-23 of it.
+// An argument of 2^-y, y >= 0, and (kF32) what it lacks of the exact value.
+struct Exponent {
+    float y, rest;
+};
+
+// x log2 e (lo: what x >= 0 lacks itself).
 template <bool kF32>
-__device__ __forceinline__ float exp_minus(float x, float lo = 0.0f)
+__device__ __forceinline__ Exponent exponent(float x, float lo = 0.0f)
 {
     constexpr float kL = 1.44269502162933349609375f, kLow = 1.92596299112661746887e-8f;   // log2 e and what it lacks
     const float y = x * kL;
-    const float e = __builtin_amdgcn_exp2f(-y);
+    return {y, kF32 ? fmaf(lo, kL, fmaf(x, kLow, fmaf(x, kL, -y))) : 0.0f};
+}
+
+// 2 sqrt(2 / pi) log2 e (x + 0.044715 x^3) for x >= 0, every product's and sum's rest taken along: rounded alone, 95 at x = 9
+// would put 1.4e-5 into 2^-y.
+template <bool kF32>
+__device__ __forceinline__ Exponent tanh_exponent(float x)
+{
+    constexpr float kA = 2.302208185195923f, kALow = 1.29484020e-8f;                // 2 sqrt(2 / pi) log2 e and what it lacks
+    constexpr float kB = 0.0447149984538555145263671875f, kBLow = 1.54614449e-9f;   // 0.044715 and what it lacks
+    const float s = x * x, p = fmaf(kB, s, 1.0f), v = x * p, y = kA * v;
+    if constexpr (!kF32)
+        return {y, 0.0f};
+    const float p_rest = fmaf(kB, s, 1.0f - p) + fmaf(kB, fmaf(x, x, -s), kBLow * s);   // p - 1 is exact
+    const float v_rest = fmaf(x, p_rest, fmaf(x, p, -v));
+    return {y, fmaf(kA, v_rest, fmaf(kALow, v, fmaf(kA, v, -y)))};
+}
+
+// 2^-y.  kF32: the rest is put back, which leaves the hardware's 2^y (1 ulp) as the error; else the error is that of the
+// argument, about 2^-23 of it.
+template <bool kF32>
+__device__ __forceinline__ float exp2_minus(const Exponent& x)
+{
+    const float e = __builtin_amdgcn_exp2f(-x.y);
     if constexpr (!kF32)
         return e;
-    const float r = fmaf(lo, kL, fmaf(x, kLow, fmaf(x, kL, -y)));
-    return y < 150.0f ? fmaf(e, -0.6931471805599453f * r, e) : e;
+    return x.y < 150.0f ? fmaf(e, -0.6931471805599453f * x.rest, e) : e;
 }
 
 // 1 / x for x >= 1, to 1 ulp.
@@ -49,27 +75,8 @@ __device__ __forceinline__ float reciprocal(float x)
     return fmaf(r, fmaf(-x, r, 1.0f), r);
 }
 
-// z = 2 sqrt(2 / pi) (g + 0.044715 g^3) and what it lacks of the exact value (kF32), every product's and sum's rest taken
-// along: rounded alone, z of -66 at g = -9 would put 1.4e-5 into exp(z).
-template <bool kF32>
-__device__ __forceinline__ float tanh_argument(float g, float& lo)
-{
-    constexpr float kA = 1.5957691669464111328125f, kALow = -4.534068e-8f;         // 2 sqrt(2 / pi) and what it lacks
-    constexpr float kB = 0.0447149984538555145263671875f, kBLow = 1.5461445e-9f;    // 0.044715 and what it lacks
-    const float s = g * g, p = fmaf(kB, s, 1.0f), v = g * p, z = kA * v;
-    if constexpr (kF32) {
-        // p - 1 is exact
-        const float p_lo = fmaf(kB, s, 1.0f - p) + fmaf(kB, fmaf(g, g, -s), kBLow * s);
-        const float v_lo = fmaf(g, p_lo, fmaf(g, p, -v));
-        lo = fmaf(kA, v, -z) + fmaf(kA, v_lo, kALow * v);
-    } else {
-        lo = 0.0f;
-    }
-    return z;
-}
-
-// act(g) and its slope.  silu and gelu's tanh form are g s(z) with the logistic function s: z = g, or tanh_argument since
-// (1 + tanh y) / 2 = s(2 y).  gelu takes the normal distribution function from exp(-g^2 / 2) erfcx(x) / 2 with
+// act(g) and its slope.  silu and gelu's tanh form are g s(z) with the logistic function s: z = g, and
+// z = 2 sqrt(2 / pi) (g + 0.044715 g^3) since (1 + tanh y) / 2 = s(2 y).  gelu takes the normal distribution function from exp(-g^2 / 2) erfcx(x) / 2 with
 // x = |g| / sqrt 2, erfcx(x) / 2 = t P(t), t = 1 / (1 + 0.54 x): P of degree 9 was fitted to float64 values of erfcx on
 // [0, 14.5] by weighted least squares, relative error 3e-7 in float32.  The exponent is taken from g, whose half is exact,
 // not from the rounded x (1.2e-5 at g = -13).  Values are right to 2^-20 in float32 calls.
@@ -78,7 +85,7 @@ __device__ __forceinline__ void activation(int act, float g, float& value, float
 {
     if (act == MOE_ACT_GELU) {
         const float x = 0.70710678118654752f * fabsf(g), half = 0.5f * g, x2 = half * g;
-        const float e = exp_minus<kF32>(x2, fmaf(half, g, -x2));
+        const float e = exp2_minus<kF32>(exponent<kF32>(x2, fmaf(half, g, -x2)));
         // the reciprocal of infinity would come out NaN; e is zero from far below 1e18 on
         const float t = reciprocal(fmaf(0.54f, fminf(x, 1e18f), 1.0f));
         float p = 0.022005289793014526f;
@@ -98,11 +105,10 @@ __device__ __forceinline__ void activation(int act, float g, float& value, float
         return;
     }
     constexpr float kA = 1.5957691216057308f, kB = 0.044715f;
-    float lo = 0.0f;
-    const float z = act == MOE_ACT_SILU ? g : tanh_argument<kF32>(g, lo);
+    const Exponent z = act == MOE_ACT_SILU ? exponent<kF32>(fabsf(g)) : tanh_exponent<kF32>(fabsf(g));
     const float dz = act == MOE_ACT_SILU ? 1.0f : kA * (1.0f + 3.0f * kB * g * g);
-    const float e = exp_minus<kF32>(fabsf(z), z < 0.0f ? -lo : lo), r = reciprocal(1.0f + e);
-    const float s = z < 0.0f ? e * r : r, t = z < 0.0f ? r : e * r;    // s(z) and 1 - s(z)
+    const float e = exp2_minus<kF32>(z), r = reciprocal(1.0f + e);
+    const float s = g < 0.0f ? e * r : r, t = g < 0.0f ? r : e * r;    // s(z) and 1 - s(z)
     value = g * s;
     const float st = s * t;
     slope = s + (st == 0.0f ? 0.0f : g * st * dz);
