@@ -39,6 +39,7 @@ struct Args {
     const int32_t *ids, *ranks;
     const float* scale;
     int T, K, N, L, R;
+    int tail;                             // the first adapter whose reads of A may pass the tensor's end (first_tail)
 };
 
 __device__ __forceinline__ int rank_of(const Args& g, int a) { return g.ranks == nullptr ? g.R : min(max(g.ranks[a], 0), g.R); }
@@ -65,12 +66,7 @@ __device__ __forceinline__ void shift_a(Raw8<float>& r, int skip)
         r.b = f32x4_t{r.b[1], r.b[2], r.b[3], 0.0f};
     }
 }
-// Whether loads of an adapter's A may pass the tensor's end: rows that are not whole runs of eight, and fewer than eight
-// values behind the adapter (it is the last one, or the ones after it hold few).
-__device__ __forceinline__ bool past_end(const Args& g, int a)
-{
-    return g.R % 8 != 0 && static_cast<int64_t>(g.L - 1 - a) * g.K * g.R < 8;
-}
+__device__ __forceinline__ bool past_end(const Args& g, int a) { return a >= g.tail; }
 // How far the load of eight values from `at` on was moved back to end with the tensor.
 __device__ __forceinline__ int moved_back(int64_t at, int64_t total)
 {
@@ -743,6 +739,13 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
 
 // ------------------------------------------------------------------------------------------------ the host's side
 
+// The first adapter with fewer than eight values of A behind it, where rows are not whole runs of eight: loads of eight
+// values from inside such an adapter on may pass the tensor's end.
+int first_tail(const moe_adapter& p)
+{
+    return static_cast<int>(p.R % 8 == 0 ? p.L : std::max<int64_t>(p.L - ceil_div(8, p.K * p.R), 0));
+}
+
 // How a call runs.
 struct Plan {
     bool narrow;              // narrow_kernel
@@ -853,7 +856,7 @@ hipError_t launch_adapter(const moe_adapter& p, const void* base, const void* x,
                           hipStream_t s)
 {
     const Args g{base, x, a, b, out, ids, ranks, scale, static_cast<int>(p.T), static_cast<int>(p.K), static_cast<int>(p.N),
-                 static_cast<int>(p.L), static_cast<int>(p.R)};
+                 static_cast<int>(p.L), static_cast<int>(p.R), first_tail(p)};
     unsigned char* const ws = static_cast<unsigned char*>(workspace);
     return p.dtype == MOE_F32 ? launch<float>(p, g, ws, s) : launch<uint16_t>(p, g, ws, s);
 }
