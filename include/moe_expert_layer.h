@@ -462,10 +462,11 @@ moe_status moe_gated_projection_backward(const moe_gated* g, const void* x, cons
 /* Low-rank adapters of many requests at once beside a shared projection: with a = ids[t],
  *   out[t] = base[t] + scale[a] * (x[t] A[a][:, :r]) B[a][:r, :],   r = ranks[a]
  * base (the projection's output) [T,N], x [T,K], a [L,K,R], b [L,R,N], out [T,N] of dtype; ids [T] int32;
- * scale [L] float32 or NULL (1); ranks [L] int32 or NULL (R), clamped into [0, R]: an adapter's columns
+ * scale [L] finite float32 or NULL (1); ranks [L] int32 or NULL (R), clamped into [0, R]: an adapter's columns
  * and rows from its rank on count for nothing, whatever they hold.  A row whose id lies outside [0, L) has no adapter: out[t] =
- * base[t].  x A is a float32 sum, kept to 16 bits (MOE_BF16) or 24 (MOE_F32) for the second product.  out
- * may be base; no other buffers may overlap it. */
+ * base[t].  x A is a float32 sum, kept to 16 bits (MOE_BF16) or 24 (MOE_F32) for the second product.  Infinities and
+ * NaN in x, A and B give what the formula gives, however many rows a call has.  out may be base; no other
+ * buffers may overlap it. */
 typedef struct moe_adapter {
     int64_t T;            /* rows, at most 2^28                                                  */
     int64_t K;            /* width of x, at most MOE_MAX_HIDDEN                                  */

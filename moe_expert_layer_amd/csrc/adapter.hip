@@ -10,7 +10,9 @@
 //     adapter's matrices through LDS; K is cut so that there are workgroups enough, and join_kernel adds the cuts' float32
 //     sums.  v enters the second product as two bfloat16 planes (16 bits) for bfloat16 tensors, as three for float32 ones.
 // A row's result does not depend on the tile that it falls into, so neither the order in which the plan's counters hand
-// out places nor other rows change it.
+// out places nor other rows change it.  Planes of infinite values can make a product NaN that is infinite by the formula:
+// a sum that comes out NaN is taken again from the values themselves (resum), as single rows have it
+// (1% of float32 calls, less of bfloat16 ones: 4000 x 4096 x 4096 of rank 128 187 -> 190 us).
 // Measured: one row 4096 -> 14336 of rank 16 7.6 us, 64 rows of 32 adapters 4096 -> 4096 9.5; 8192 rows 14336 -> 4096 of
 // rank 64: plan 6.5, shrink 54-67 (3.5-4.3 TB/s), join 5, expand 32 (4.4 TB/s of base, out and v).
 #include <algorithm>
@@ -395,13 +397,31 @@ __device__ __forceinline__ f32x16_t mfma_planes(const bf16x8_t (&w)[PB], const b
     return acc;
 }
 
+// sum[0 .. 7] = the sums over i in [i0, i1) of factor(i) times the first n of eight values at p + i ld.
+template <class T, class F>
+__device__ __forceinline__ void resum(float (&sum)[8], int i0, int i1, F factor, const T* p, int64_t ld, int n)
+{
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        sum[e] = 0.0f;
+#pragma unroll 1
+    for (int i = i0; i < i1; ++i) {
+        const float f = factor(i);
+        float w[8];
+        load8(w, p + i * ld, n);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            sum[e] = fmaf(f, w[e], sum[e]);
+    }
+}
+
 // Eight values of v as the planes that enter the second product.
 template <class T>
 __device__ __forceinline__ void store_v(uint16_t* p, int64_t plane, const float (&w)[8])
 {
     constexpr int PV = kPlanesOf<T> == 1 ? 2 : 3;
     u32x4_t pl[PV];
-    split8<PV>(w, pl);
+    split8<PV, true>(w, pl);
 #pragma unroll
     for (int q = 0; q < PV; ++q)
         *reinterpret_cast<u32x4_t*>(p + q * plane) = pl[q];
@@ -552,11 +572,17 @@ __global__ __launch_bounds__(kThreads) void shrink_kernel(Args g, TileArgs p)
                 float w[8], u[8];
                 run8(acc[j], h, w);
                 load8(u, join + 32 * j + 16 * h, 8);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = c + i < rank ? (w[i] + u[i]) * f : 0.0f;
                 if (32 * wr + (lane & 31) >= n)
                     continue;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = c + i < rank ? w[i] + u[i] : 0.0f;
+                if constexpr (P > 1)
+                    if (any_nan(w))                       // of columns below the rank
+                        resum(w, step0 * kStep, min(step1 * kStep, g.K), [&](int k) { return x[k]; }, A + a0 + c, g.R, rank - c);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = c + i < rank ? w[i] * f : 0.0f;
                 if (p.splits == 1)
                     store_v<T>(p.v + at + c, static_cast<int64_t>(g.T) * kCols, w);
                 else
@@ -718,16 +744,42 @@ __global__ __launch_bounds__(kThreads) void expand_kernel(Args g, TileArgs p)
                                                 4 * (32 * wave + 8 * q + 4 * (lane >> 5))) =
                         f32x4_t{acc[b][4 * q], acc[b][4 * q + 1], acc[b][4 * q + 2], acc[b][4 * q + 3]};
             __syncthreads();
+            // rows whose sums are looked at together: a branch at each would part their loads, four of float32 take registers
+            // of a third workgroup
+            constexpr int kTogether = PB == 1 ? 4 : 2;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float sum[8], u[8];
-                load8(sum, reinterpret_cast<const float*>(smem + (row0 + 16 * i) * M::kOutRow) + col, 8);
-                base[i].values(u);
+            for (int i0 = 0; i0 < 4; i0 += kTogether) {
+                float sum[kTogether][8];
+                bool nan = false;
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum[e] += u[e];
-                if (row0 + 16 * i < n && c0 + col < g.N)
-                    store_from(static_cast<T*>(g.out) + at[i], min(c0 + col, g.N - 8), c0 + col, sum);
+                for (int i = 0; i < kTogether; ++i) {
+                    load8(sum[i], reinterpret_cast<const float*>(smem + (row0 + 16 * (i0 + i)) * M::kOutRow) + col, 8);
+                    nan |= any_nan(sum[i]);
+                }
+                if (nan)
+#pragma unroll
+                    for (int i = 0; i < kTogether; ++i) {
+                        const unsigned char* const v = smem + M::kV + (row0 + 16 * (i0 + i)) * M::kVRow;
+                        const auto value = [&](int r) {
+                            float f = 0.0f;
+#pragma unroll
+                            for (int q = PV - 1; q >= 0; --q)
+                                f += bf16_to_f32(*reinterpret_cast<const uint16_t*>(v + q * M::kVPlane + 2 * r));
+                            return f;
+                        };
+                        if (any_nan(sum[i]))
+                            resum(sum[i], 0, rank, value, B + min(c0 + col, g.N - 8), g.N, 8);
+                    }
+#pragma unroll
+                for (int i = 0; i < kTogether; ++i) {
+                    float u[8];
+                    base[i0 + i].values(u);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        u[e] += sum[i][e];
+                    if (row0 + 16 * (i0 + i) < n && c0 + col < g.N)
+                        store_from(static_cast<T*>(g.out) + at[i0 + i], min(c0 + col, g.N - 8), c0 + col, u);
+                }
             }
             // the next run's values are loaded when their registers are free: copying them would wait for the loads
             __builtin_amdgcn_sched_barrier(0);

@@ -15,8 +15,8 @@ constexpr int kPlanePairs[6][2] = {{2, 0}, {0, 2}, {1, 1}, {1, 0}, {0, 1}, {0, 0
 
 // x as the sum of its first P planes (x0 rounds towards zero where the nearest would be infinite).  P = 2 keeps 16 bits
 // (what is left out is at most 2^-16 |x|).  An infinity becomes infinity and (three planes) NaN, so that sums it takes
-// part in are NaN.
-template <int P>
+// part in are NaN; kSum: infinity and zeros, whose sum it is.
+template <int P, bool kSum = P == 2>
 __device__ __forceinline__ void split(float x, uint16_t (&p)[P])
 {
 #pragma unroll
@@ -26,18 +26,18 @@ __device__ __forceinline__ void split(float x, uint16_t (&p)[P])
         if ((b & 0x7FFFu) == 0x7F80u && finite)
             b = static_cast<uint16_t>(__float_as_uint(x) >> 16);
         p[i] = b;
-        x = P == 2 && !finite ? 0.0f : x - bf16_to_f32(b);
+        x = kSum && !finite ? 0.0f : x - bf16_to_f32(b);
     }
 }
 
 // Eight values as P planes of eight.
-template <int P>
+template <int P, bool kSum = P == 2>
 __device__ __forceinline__ void split8(const float (&v)[8], u32x4_t (&out)[P])
 {
     uint16_t s[8][P];
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        split<P>(v[i], s[i]);
+        split<P, kSum>(v[i], s[i]);
 #pragma unroll
     for (int q = 0; q < P; ++q)
         out[q] = u32x4_t{s[0][q] | static_cast<uint32_t>(s[1][q]) << 16, s[2][q] | static_cast<uint32_t>(s[3][q]) << 16,

@@ -76,6 +76,12 @@ __device__ __forceinline__ Raw8<float> load_raw(const float* p, int n)
     return r;
 }
 
+__device__ __forceinline__ bool any_nan(const float (&v)[8])
+{
+    return __builtin_isunordered(v[0], v[1]) || __builtin_isunordered(v[2], v[3]) || __builtin_isunordered(v[4], v[5]) ||
+           __builtin_isunordered(v[6], v[7]);
+}
+
 template <class T>
 __device__ __forceinline__ void load8(float (&v)[8], const T* p, int n)
 {

@@ -130,3 +130,48 @@ def test_activations_to_float32(act, T):
     # s + g s (1 - s) z' and its like, which cancel near the slope's zero; the second term has a few roundings more
     terms = slope.abs() + 2 * (slope - value / g.double()).abs()
     assert bool(((dwg.double() - slope).abs() <= 2.0 ** -19 * terms + 1e-37).all())
+
+
+def _product(x, a):
+    """x @ a in float64, term by term (no library product: zero times infinity is NaN where it stands)."""
+    return (x.double()[:, :, None] * a.double()[None]).sum(1)
+
+
+@TYPES
+@pytest.mark.parametrize("T", [40, 1200])
+@pytest.mark.parametrize("where", ["x", "a", "b", "all"])
+def test_adapters_of_infinite_values(dtype, T, where):
+    """Infinities give what the formula gives, by single rows and by tiles alike; finite results stay what they are."""
+    K, N, L, R = 300, 40, 3, 12
+    base, x, a, b, ids = adapter_ops(T, K, N, L, R, dtype)
+    ranks = torch.tensor([R, 9, 1], dtype=torch.int32, device="cuda")
+    scale = torch.tensor([0.5, 2.0, -1.0], device="cuda")
+    if where in ("x", "all"):
+        x[5, 7], x[6, 299], x[7, 100], x[11, 0] = INF, -INF, INF, -INF
+        x[10, 1], x[10, 2] = INF, -INF
+    if where in ("a", "all"):
+        a[1, 250, 3], a[2, 20, 0] = INF, INF
+    if where in ("b", "all"):
+        b[0, 2, 5], b[0, 3, 6], b[0, 4, 6] = INF, INF, -INF
+        b[1, 10, 7] = INF                                  # past the rank: counts for nothing
+        b[2, :, 39] = -INF
+    # one value of v that is zero, one that its first plane holds whole: zero times infinity is NaN, others are infinite
+    x[13], x[17] = 0.0, 0.0
+    x[17, 0] = 1.0
+    a[0, 0] = 2.0                                          # row 17 has adapter 0
+    want = base.double().clone()
+    for i in range(L):
+        rows, r = torch.nonzero(ids == i)[:, 0], int(ranks[i])
+        v = scale[i].double() * _product(x[rows], a[i, :, :r])
+        want[rows] += _product(v, b[i, :r])
+    got = add_adapters(base, x, a, b, ids, scale=scale, ranks=ranks).double()
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isfinite(got), ~odd), (torch.isfinite(got) == odd).nonzero()[:8]
+    assert torch.equal(coded(got[odd]), coded(want[odd]))
+    # where no infinity takes part the bound is that of finite operands
+    zeroed = [torch.nan_to_num(t, posinf=0.0, neginf=0.0) for t in (x, a, b)]
+    bound = ref.adapter(base, *zeroed, ids, scale, ranks)[1]
+    ref.close(got[~odd].to(dtype), want[~odd], bound[~odd], "finite")
+    inplace = base.clone()
+    mel.adapter_add(inplace, x, a, b, ids, scale=scale, ranks=ranks, out=inplace)
+    assert torch.equal(coded(inplace), coded(got))
