@@ -47,6 +47,11 @@ def add_adapters(base, x, a, b, ids, **kw):
     return mel.adapter_add(base, x, a, b, ids, workspace=ws, **kw)
 
 
+def coded(t):
+    """Numbers that compare in place of infinities and NaN."""
+    return torch.nan_to_num(t.double(), nan=7e40, posinf=1e40, neginf=-1e40)
+
+
 # ------------------------------------------------------------------------------------------- adapters
 
 @TYPES
@@ -58,12 +63,52 @@ def test_adapters_of_fewer_than_eight_values(dtype, T, K, R, L):
     ref.close(add_adapters(*ops), *ref.adapter(*ops, None, None), "adapter")
 
 
+def _product(x, a):
+    """x @ a in float64, term by term (no library product: zero times infinity is NaN where it stands)."""
+    return (x.double()[:, :, None] * a.double()[None]).sum(1)
+
+
+@TYPES
+@pytest.mark.parametrize("T", [40, 1200])
+@pytest.mark.parametrize("where", ["x", "a", "b", "all"])
+def test_adapters_of_infinite_values(dtype, T, where):
+    """Infinities give what the formula gives, by single rows and by tiles alike; finite results stay what they are."""
+    K, N, L, R = 300, 40, 3, 12
+    base, x, a, b, ids = adapter_ops(T, K, N, L, R, dtype)
+    ranks = torch.tensor([R, 9, 1], dtype=torch.int32, device="cuda")
+    scale = torch.tensor([0.5, 2.0, -1.0], device="cuda")
+    if where in ("x", "all"):
+        x[5, 7], x[6, 299], x[7, 100], x[11, 0] = INF, -INF, INF, -INF
+        x[10, 1], x[10, 2] = INF, -INF
+    if where in ("a", "all"):
+        a[1, 250, 3], a[2, 20, 0] = INF, INF
+    if where in ("b", "all"):
+        b[0, 2, 5], b[0, 3, 6], b[0, 4, 6] = INF, INF, -INF
+        b[1, 10, 7] = INF                                  # past the rank: counts for nothing
+        b[2, :, 39] = -INF
+    # one value of v that is zero, one that its first plane holds whole: zero times infinity is NaN, others are infinite
+    x[13], x[17] = 0.0, 0.0
+    x[17, 0] = 1.0
+    a[0, 0] = 2.0                                          # row 17 has adapter 0
+    want = base.double().clone()
+    for i in range(L):
+        rows, r = torch.nonzero(ids == i)[:, 0], int(ranks[i])
+        v = scale[i].double() * _product(x[rows], a[i, :, :r])
+        want[rows] += _product(v, b[i, :r])
+    got = add_adapters(base, x, a, b, ids, scale=scale, ranks=ranks).double()
+    odd = ~torch.isfinite(want)
+    assert torch.equal(torch.isfinite(got), ~odd), (torch.isfinite(got) == odd).nonzero()[:8]
+    assert torch.equal(coded(got[odd]), coded(want[odd]))
+    # where no infinity takes part the bound is that of finite operands
+    zeroed = [torch.nan_to_num(t, posinf=0.0, neginf=0.0) for t in (x, a, b)]
+    bound = ref.adapter(base, *zeroed, ids, scale, ranks)[1]
+    ref.close(got[~odd].to(dtype), want[~odd], bound[~odd], "finite")
+    inplace = base.clone()
+    mel.adapter_add(inplace, x, a, b, ids, scale=scale, ranks=ranks, out=inplace)
+    assert torch.equal(coded(inplace), coded(got))
+
+
 # ------------------------------------------------------------------------------------------- gated block: values
-
-def coded(t):
-    """Numbers that compare in place of infinities and NaN."""
-    return torch.nan_to_num(t.double(), nan=7e40, posinf=1e40, neginf=-1e40)
-
 
 @TYPES
 @ACTS
@@ -132,46 +177,83 @@ def test_activations_to_float32(act, T):
     assert bool(((dwg.double() - slope).abs() <= 2.0 ** -19 * terms + 1e-37).all())
 
 
-def _product(x, a):
-    """x @ a in float64, term by term (no library product: zero times infinity is NaN where it stands)."""
-    return (x.double()[:, :, None] * a.double()[None]).sum(1)
+# ------------------------------------------------------------------------------------------- float32 products in planes
 
 
-@TYPES
-@pytest.mark.parametrize("T", [40, 1200])
-@pytest.mark.parametrize("where", ["x", "a", "b", "all"])
-def test_adapters_of_infinite_values(dtype, T, where):
-    """Infinities give what the formula gives, by single rows and by tiles alike; finite results stay what they are."""
-    K, N, L, R = 300, 40, 3, 12
-    base, x, a, b, ids = adapter_ops(T, K, N, L, R, dtype)
-    ranks = torch.tensor([R, 9, 1], dtype=torch.int32, device="cuda")
-    scale = torch.tensor([0.5, 2.0, -1.0], device="cuda")
-    if where in ("x", "all"):
-        x[5, 7], x[6, 299], x[7, 100], x[11, 0] = INF, -INF, INF, -INF
-        x[10, 1], x[10, 2] = INF, -INF
-    if where in ("a", "all"):
-        a[1, 250, 3], a[2, 20, 0] = INF, INF
-    if where in ("b", "all"):
-        b[0, 2, 5], b[0, 3, 6], b[0, 4, 6] = INF, INF, -INF
-        b[1, 10, 7] = INF                                  # past the rank: counts for nothing
-        b[2, :, 39] = -INF
-    # one value of v that is zero, one that its first plane holds whole: zero times infinity is NaN, others are infinite
-    x[13], x[17] = 0.0, 0.0
-    x[17, 0] = 1.0
-    a[0, 0] = 2.0                                          # row 17 has adapter 0
-    want = base.double().clone()
+def hard(seed, *shape):
+    """Values in [1, 1.25) whose second and third bfloat16 planes are as large as they come (2^-8.4 and 2^-17.4 at least): the
+    loss of one product of planes changes a product of two of them by 2^-17.7 = 4.6e-6 or more."""
+    g = torch.Generator().manual_seed(seed)
+    j, m, n = (torch.randint(lo, hi, shape, generator=g).double() for lo, hi in ((0, 32), (64, 128), (16, 32)))
+    return (1 + j / 128 + 2.0 ** -9 * (1 + m / 128) + 2.0 ** -18 * (1 + n / 32)).float().cuda()
+
+
+def sparse(seed, rows, cols):
+    """Rows of eight hard values at random places, zeros between them."""
+    g = torch.Generator().manual_seed(seed)
+    at = torch.stack([torch.randperm(cols, generator=g)[:8] for _ in range(rows)]).cuda()
+    return torch.zeros((rows, cols), device="cuda").scatter_(1, at, hard(seed, rows, 8))
+
+
+# sums of eight positive products: each addition 2^-23 of the sum, the products left out 2^-23, the roundings 2^-24
+EIGHT = 10 * 2.0 ** -23
+
+
+def relative(got, want):
+    return float(((got.double() - want).abs() / want.abs()).max())
+
+
+@pytest.mark.parametrize("T,H,F", [(65, 513, 130), (200, 1024, 328), (1000, 250, 1500)])
+def test_float32_tiles_keep_every_plane(T, H, F):
+    """Each product of planes at each place of K, in the tiles of the forward and of both gradients (in one launch and in
+    parts): eight terms a sum, so that a lost product is larger than what the sum may be off by."""
+    x, w = sparse(1, T, H), hard(2, H, F)
+    kept = torch.empty((2, T, F), device="cuda")
+    mel.gated_projection(x, w, w.flip(1).contiguous(), saved_gu=kept)
+    assert relative(kept[0], x.double() @ w.double()) <= EIGHT
+    assert relative(kept[1], x.double() @ w.flip(1).double()) <= EIGHT
+    # silu at g = 0: value 0, slope 1/2, so with u = 2: dg = dh, du = 0
+    kept[0], kept[1] = 0.0, 2.0
+    dh = sparse(3, T, F)
+    dx = mel.gated_projection_backward(x, w, w, dh, saved_gu=kept)[0]
+    assert relative(dx, dh.double() @ w.double().t()) <= EIGHT
+    dh, x = sparse(4, F, T).t().contiguous(), hard(5, T, H)
+    dwg, dwu = mel.gated_projection_backward(x, w, w, dh, saved_gu=kept)[1:]
+    assert relative(dwg, x.double().t() @ dh.double()) <= EIGHT
+    assert bool((dwu == 0).all())
+
+
+def test_float32_tiles_keep_24_bits():
+    """Single products of operands that need all their bits, in every row and column of several tiles: what is left out is
+    below 2^-23, one rounding."""
+    T, F = 200, 300
+    g = torch.Generator().manual_seed(9)
+    x, w = ((1 + torch.randint(0, 2 ** 23, s, generator=g) / 2.0 ** 23).float().cuda() for s in ((T, 1), (1, F)))
+    x[:6, 0] = torch.tensor([1 + 2.0 ** -23, 1 - 2.0 ** -24, 3.0000002, 1 / 3, 3.3e38, -3.4e38])
+    w[0, :5] = torch.tensor([1 - 2.0 ** -24, 1 + 2.0 ** -23, 0.1, 1.0, 1e-3])
+    w[0, 5:] *= 0.25                                       # no product of the largest value is past the range
+    w[0, 1] = 1 - 2.0 ** -23
+    kept = torch.empty((2, T, F), device="cuda")
+    mel.gated_projection(x, w, w, saved_gu=kept)
+    assert relative(kept[0], x.double() @ w.double()) <= 2.0 ** -22
+    # dx and dWg as products of one term: at g = 0 with u = 1, dg = dh / 2 and du = 0
+    kept[0], kept[1] = 0.0, 1.0
+    want = 0.5 * (x.double() @ w.double())
+    dx = mel.gated_projection_backward(x.new_zeros((T, F)), w.t().contiguous(), w.t().contiguous(), x,
+                                       saved_gu=kept[:, :, :1].contiguous())[0]
+    assert relative(dx, want) <= 2.0 ** -22
+    dwg = mel.gated_projection_backward(x.t().contiguous(), w.new_ones((T, F)), w.new_ones((T, F)), w,
+                                        saved_gu=kept[:, :1].contiguous())[1]
+    assert relative(dwg, want) <= 2.0 ** -22
+
+
+def test_float32_adapter_tiles_keep_every_plane():
+    """v from eight terms, out from one: two sums' roundings."""
+    T, K, N, L, R = 1000, 700, 264, 3, 40
+    ids = (torch.arange(T) % L).to(torch.int32).cuda()
+    x, a = sparse(6, T, K), hard(7, L, K, R)
+    b = hard(8, L, R, N) * (torch.arange(N, device="cuda") % R == torch.arange(R, device="cuda")[:, None])
+    out = mel.adapter_add(torch.zeros((T, N), device="cuda"), x, a, b, ids)
     for i in range(L):
-        rows, r = torch.nonzero(ids == i)[:, 0], int(ranks[i])
-        v = scale[i].double() * _product(x[rows], a[i, :, :r])
-        want[rows] += _product(v, b[i, :r])
-    got = add_adapters(base, x, a, b, ids, scale=scale, ranks=ranks).double()
-    odd = ~torch.isfinite(want)
-    assert torch.equal(torch.isfinite(got), ~odd), (torch.isfinite(got) == odd).nonzero()[:8]
-    assert torch.equal(coded(got[odd]), coded(want[odd]))
-    # where no infinity takes part the bound is that of finite operands
-    zeroed = [torch.nan_to_num(t, posinf=0.0, neginf=0.0) for t in (x, a, b)]
-    bound = ref.adapter(base, *zeroed, ids, scale, ranks)[1]
-    ref.close(got[~odd].to(dtype), want[~odd], bound[~odd], "finite")
-    inplace = base.clone()
-    mel.adapter_add(inplace, x, a, b, ids, scale=scale, ranks=ranks, out=inplace)
-    assert torch.equal(coded(inplace), coded(got))
+        rows = ids == i
+        assert relative(out[rows], (x[rows].double() @ a[i].double()) @ b[i].double()) <= EIGHT + 3 * 2.0 ** -23
