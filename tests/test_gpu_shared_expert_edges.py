@@ -108,6 +108,19 @@ def test_adapters_of_infinite_values(dtype, T, where):
     assert torch.equal(coded(inplace), coded(got))
 
 
+@TYPES
+@pytest.mark.parametrize("T,K,N,L,R", [(896, 40, 24, 3, 4), (897, 40, 24, 3, 4), (300, 64, 9001, 3, 4), (260, 24, 20000, 2, 3)])
+def test_adapter_limits_of_single_rows(dtype, T, K, N, L, R):
+    """The most single rows and one more; rows of more columns than one pass of a workgroup takes."""
+    ops = adapter_ops(T, K, N, L, R, dtype)
+    out = add_adapters(*ops)
+    ref.close(out, *ref.adapter(*ops, None, None), "adapter")
+    assert torch.equal(out[ops[4] < 0], ops[0][ops[4] < 0])
+    inplace = ops[0].clone()
+    add_adapters(inplace, *ops[1:], out=inplace)
+    assert torch.equal(inplace, out)
+
+
 # ------------------------------------------------------------------------------------------- gated block: values
 
 @TYPES
