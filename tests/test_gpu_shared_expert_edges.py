@@ -190,6 +190,29 @@ def test_activations_to_float32(act, T):
     assert bool(((dwg.double() - slope).abs() <= 2.0 ** -19 * terms + 1e-37).all())
 
 
+@ACTS
+@pytest.mark.parametrize("T,H,F", [(2100, 520, 2056), (4100, 200, 1000)])
+def test_dropout_in_the_largest_tiles(act, T, H, F):
+    """bfloat16 products of 256 x 256 tiles with dropout, forward and both gradients.  The mask is that of dropout() with the
+    same rng, whose own test compares it with the generator."""
+    p = 0.3
+    x = randn(1, T, H, dtype=BF)
+    wg, wu = (randn(2 + i, H, F, dtype=BF, scale=H ** -0.5) for i in range(2))
+    dh = randn(4, T, F, dtype=BF)
+    rng = torch.tensor([2 ** 40 + 3, -9], dtype=torch.int64, device="cuda")
+    keep = mel.dropout(torch.ones((T, F), dtype=BF, device="cuda"), p, rng) != 0
+    mask = (keep, 65536 / (65536 - ref.threshold(p)))
+    h, eh, *_ = ref.gated(x, wg, wu, act, mask)
+    got = mel.gated_projection(x, wg, wu, activation=act, dropout=p, rng=rng)
+    ref.close(got, h, eh, "h")
+    assert bool((got[~keep] == 0).all())
+    ws = poisoned(mel.gated_workspace_size(T, H, F, mel.BF16, backward=True))
+    grads = mel.gated_projection_backward(x, wg, wu, dh, activation=act, dropout=p, rng=rng, workspace=ws)
+    want, bounds = ref.gated_backward(x, wg, wu, dh, act, mask)
+    for name, a, b, e in zip(("dx", "dw_gate", "dw_up"), grads, want, bounds):
+        ref.close(a, b, e, name)
+
+
 # ------------------------------------------------------------------------------------------- float32 products in planes
 
 
