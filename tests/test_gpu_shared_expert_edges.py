@@ -293,3 +293,59 @@ def test_float32_adapter_tiles_keep_every_plane():
     for i in range(L):
         rows = ids == i
         assert relative(out[rows], (x[rows].double() @ a[i].double()) @ b[i].double()) <= EIGHT + 3 * 2.0 ** -23
+
+
+# ------------------------------------------------------------------------------------------- replays, far offsets
+
+@TYPES
+def test_captured_adapters_by_tiles_follow_their_ids(dtype):
+    """A captured call by tiles, replayed with other ids, ranks and factors: the plan is made anew each time."""
+    T, L = 1100, 5
+    base, x, a, b, ids = adapter_ops(T, 520, 264, L, 24, dtype)
+    ranks, scale = torch.full((L,), 24, dtype=torch.int32, device="cuda"), torch.ones(L, device="cuda")
+    mel.adapter_add(base, x, a, b, ids, scale=scale, ranks=ranks)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = mel.adapter_add(base, x, a, b, ids, scale=scale, ranks=ranks)
+    for i in range(4):
+        ids.copy_((torch.arange(T) * (2 * i + 1) // 7 % (L + 1) - 1).to(torch.int32) if i < 3 else torch.full((T,), L))
+        ranks.copy_((torch.arange(L) * 7 + i) % 25)
+        scale.copy_(torch.arange(L) - 1.5 * i)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, mel.adapter_add(base, x, a, b, ids, scale=scale, ranks=ranks))
+        ref.close(got, *ref.adapter(base, x, a, b, ids, scale, ranks), i)
+
+
+def test_offsets_past_32_bits():
+    """Tensors of more than 2^31 values: the last rows are what they are alone."""
+    T, N = 70000, 32768
+    base = torch.zeros((T, N), dtype=BF, device="cuda")
+    tail = randn(1, 100, N, dtype=BF)
+    base[-100:] = tail
+    rng = torch.tensor([77, 5], dtype=torch.int64, device="cuda")
+    out = mel.dropout(base, 0.5, rng)
+    bits = [ref.philox((g, T - 1, 5, 0), (77, 0)) for g in range(N // 8)]
+    keep = torch.tensor([(w[i // 2] >> (16 * (i % 2)) & 0xFFFF) >= ref.threshold(0.5) for w in bits for i in range(8)]).cuda()
+    assert torch.equal(out[-1], torch.where(keep, tail[-1] * 2, torch.zeros_like(tail[-1])))
+    assert bool((out[:-100] == 0).all())
+    del out
+    K, L, R = 40, 2, 8
+    x, a, b = randn(2, T, K, dtype=BF), randn(3, L, K, R, dtype=BF), randn(4, L, R, N, dtype=BF)
+    ids = (torch.arange(T) % (L + 1) - 1).to(torch.int32).cuda()
+    mel.adapter_add(base, x, a, b, ids, out=base)
+    ref.close(base[-100:], *ref.adapter(tail, x[-100:], a, b, ids[-100:], None, None), "adapter")
+    wg, wu = randn(5, K, N, dtype=BF, scale=0.1), randn(6, K, N, dtype=BF, scale=0.1)
+    mel.gated_projection(x, wg, wu, out=base)
+    want, bound, *_ = ref.gated(x[-100:], wg, wu, "silu")
+    ref.close(base[-100:], want, bound, "h")
+    dh = base
+    dh[:-100] = 0                                          # gradients of the last rows alone
+    dx, dwg, dwu = mel.gated_projection_backward(x, wg, wu, dh)
+    grads, bounds = ref.gated_backward(x[-100:], wg, wu, dh[-100:], "silu")
+    ref.close(dx[-100:], grads[0], bounds[0], "dx")
+    assert bool((dx[:-100] == 0).all())
+    ref.close(dwg, grads[1], bounds[1], "dw_gate")
+    ref.close(dwu, grads[2], bounds[2], "dw_up")
