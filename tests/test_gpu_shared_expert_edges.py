@@ -295,6 +295,18 @@ def test_float32_adapter_tiles_keep_every_plane():
         assert relative(out[rows], (x[rows].double() @ a[i].double()) @ b[i].double()) <= EIGHT + 3 * 2.0 ** -23
 
 
+@pytest.mark.parametrize("T", [6, 200])
+@pytest.mark.parametrize("e", [-110, -118, -125, -130])
+def test_float32_small_factors(T, e):
+    """24 bits down to 2^-110, below that the nearest multiple of 2^-133 (and one rounding of the product)."""
+    x, w = hard(11, T, 1) * 2.0 ** -100 * 2.0 ** (e + 100), hard(12, 1, 70) * 2.0 ** 60
+    kept = torch.empty((2, T, 70), device="cuda")
+    mel.gated_projection(x, w, w, saved_gu=kept)
+    want = x.double() @ w.double()
+    lost = 2.0 ** -134 * w.double() if e < -110 else 0.0
+    assert bool(((kept[0].double() - want).abs() <= 2.0 ** -22 * want + lost).all())
+
+
 # ------------------------------------------------------------------------------------------- replays, far offsets
 
 @TYPES
