@@ -13,8 +13,9 @@
 // out places nor other rows change it.  Planes of infinite values can make a product NaN that is infinite by the formula:
 // a sum that comes out NaN is taken again from the values themselves (resum), as single rows have it
 // (1% of float32 calls, less of bfloat16 ones: 4000 x 4096 x 4096 of rank 128 187 -> 190 us).
-// Measured: one row 4096 -> 14336 of rank 16 7.6 us, 64 rows of 32 adapters 4096 -> 4096 9.5; 8192 rows 14336 -> 4096 of
-// rank 64: plan 6.5, shrink 54-67 (3.5-4.3 TB/s), join 5, expand 32 (4.4 TB/s of base, out and v).
+// Measured: one row 4096 -> 14336 of rank 16 7.5 us, 64 rows of 32 adapters 4096 -> 4096 10.5; 8192 rows 14336 -> 4096 of
+// rank 64: plan 7, shrink 54-71 (median 71; it fetches 317 MB, x once and A once for each XCD, 4.5 TB/s), join 5, expand 32 (4.4
+// TB/s of base, out and v).
 #include <algorithm>
 
 #include "dropout.h"
@@ -242,7 +243,8 @@ __global__ __launch_bounds__(kRowThreads) void row_kernel(Args g, int cols)
     }
 }
 
-// Rows of fewer than 8 columns, or fewer than 8 values of A in all: nothing that is read 8 values at a time exists.
+// Rows of fewer than 8 columns, or fewer than 8 values of A in all: nothing that is read 8 values at a time exists.  A column of
+// A after the other, for the sizes that nothing else takes: 4096 -> 7 of rank 16, 64 rows 50 us, 4096 rows 468.
 template <class T>
 __global__ __launch_bounds__(kThreads) void narrow_kernel(Args g)
 {

@@ -568,7 +568,8 @@ hipError_t prepare(int dtype, const Source (&in)[kCount], Planes* (&out)[kCount]
 
 // bfloat16: large tiles of 256 x 256, 8 waves of 64 x 128, one workgroup per CU.  4096 tokens, H = 4096, F = 14336: the
 // gated product 810-860 us, dx 740-770, dWg and dWu 790-835 (1.1-1.3 PF).  The matrix cores are busy 60-66% of the cycles
-// at the 1.7 GHz that the chip's power leaves (2.5 GHz in short products): stages of 32 k, four or five of them, took 4-8%
+// at the 1.75-1.9 GHz that the chip's power leaves (2.5 GHz in short products), which is not all that holds dx back: the
+// library's product of its operands takes 630-700.  Stages of 32 k, four or five of them, took 4-8%
 // longer, other groupings of tiles, orders of the copies and wave priorities nothing off.
 // Small ones of 128 x 128, 4 waves of 64 x 64, two workgroups per CU, for products that leave CUs without a large tile: LDS
 // bounds them (16 KiB of fragments per 16 MFMAs); 4 stages of 32 k: the same times.

@@ -155,7 +155,9 @@ __device__ __forceinline__ void finish_gated(const EpiArgs& e, const DropKey& ke
     store8(static_cast<T*>(e.o0) + at, h, n);
 }
 
-// dg and du of eight columns; columns from N on are written as zero, they pad the products' K.
+// dg and du of eight columns.  bfloat16: rounded once, so that a plane each enters the products, as the operands do; the
+// gradients' error is 0.0023 of their norm, 0.0017 (the rounding of the results) with dg and du in float32, whose two planes
+// would double the products' work (4096 x 4096 x 14336: 1560 us of 1670).  Columns from N on are written as zero, they pad the products' K.
 template <bool kF32>
 __device__ __forceinline__ void finish_gated_bwd(const EpiArgs& e, const DropKey& key, float (&g)[8], float (&u)[8],
                                                  int64_t row, int col)

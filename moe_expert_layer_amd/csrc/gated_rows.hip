@@ -11,7 +11,8 @@
 // A workgroup takes 64 or 32 columns of both matrices; its waves take K in turn, 32 rows at a time with more of them in
 // flight, and join their sums through LDS in a fixed order.  One CU moves 70 GB/s with 128-byte rows, 35 with 64-byte ones:
 // where the columns give few workgroups, K is cut over workgroups too, which costs a second launch (plan).
-// 1 x 4096 x 14336: 50 us, 4.7 TB/s (through LDS tiles 73); 33 x 2048 x 768 7.4 and 4.9 to join six parts.
+// 1 x 4096 x 14336: 50 us, 4.7 TB/s (through LDS tiles 73); 33 x 2048 x 768, 24 x 8 workgroups of 32 columns, 7.4 and 4.2-5.2
+// to join the eight parts.
 #include <algorithm>
 
 #include "gated_epilogue.h"

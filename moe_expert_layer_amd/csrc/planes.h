@@ -2,7 +2,8 @@
 //
 // Three planes hold a float32 value exactly (x = x0 + x1 + x2, each the nearest to what is left, so |x1| <= 2^-8 |x| and
 // |x2| <= 2^-16 |x|).  Six of the nine products of two values' planes make their product; the three left out are together
-// at most 2^-23 of |a| |b|, the size of one float32 rounding.  Six bfloat16 MFMAs have about 2.6 times the rate of one
+// at most 2^-23 of |a| |b|, the size of one float32 rounding.  (Below 2^-110 a value's last bits lie under bfloat16's smallest
+// number, 2^-133, which the matrix cores do not flush: they are rounded there.)  Six bfloat16 MFMAs have about 2.6 times the rate of one
 // float32 MFMA.
 #pragma once
 
